@@ -337,7 +337,8 @@ int32_t lossk_distill_from_logits(int64_t n_tok, int64_t vocab, int32_t dtype, c
                                   int64_t workspace_bytes, lossk_stream_t stream);
 
 /* Synchronises `stream`, then reports and clears the workspace's device
- * error word: 580 (none), 590 (a bounded device wait timed out) or 589. */
+ * error words: 580 (none), 590 (a bounded device wait timed out), 589, or what
+ * a decoding call found on the device (586, 585 or 584, see there). */
 int32_t lossk_device_status(void *workspace, int64_t workspace_bytes, lossk_stream_t stream);
 
 /* ---- vocabulary-parallel cross-entropy ---------------------------------------
@@ -455,6 +456,102 @@ int32_t lossk_ce_from_logits_static(int64_t n_tok, int64_t vocab, int32_t dtype,
                                     float *lse_out, float *ce_out, double *scalars_out,
                                     void *grad_logits, int64_t grad_len, lossk_stream_t stream);
 
+/* ---- beam-search decoding ------------------------------------------------------
+ * What a user of the loss needs to generate with the head it trains: the
+ * sequences of a sequence-level distillation, or those an evaluation reads.
+ * The pages have no counterpart to these calls.  One decoding step runs
+ *   lossk_cache_fork      the sequences take their parents' cache pages
+ *   lossk_cache_reserve   each gets a place of its own for the next token
+ *   per layer: lossk_cache_write (the token's key and value rows), then
+ *              lossk_paged_attn over the cache
+ *   the head (any product of hidden rows with the weight), then
+ *   lossk_beam_select     the next beams from the logits.
+ *
+ * The cache.  A pool holds n_pages pages of page_size tokens each.  A
+ * sequence is a row of `table` (int32[n_seq][max_pages], page ids in order)
+ * and its length in tokens `lens` (int32[n_seq]); entries from
+ * ceil(len / page_size) on are not read.  ref (int32[n_pages]) counts the
+ * rows that hold each page; a page is free while its count is 0, so there is
+ * no other list of free pages to keep.  A page that several rows hold is
+ * shared and is never written to (lossk_cache_reserve sees to that).
+ *
+ * Rules of these calls, where they differ from the ones above:
+ *  - They do not synchronise: a call returns once its kernels are queued, and
+ *    can be recorded into a CUDA graph.
+ *  - Ids and lengths live on the device and are checked there.  An id or
+ *    length out of range is not followed (nothing is read or written through
+ *    it) and leaves 586 in the workspace's header; a beam whose logits hold a
+ *    NaN or +infinity leaves 585, a pool without enough free pages 584.
+ *    lossk_device_status reads and clears it; the largest code stays when
+ *    there are several.
+ *  - The workspace's first 256 bytes must be zero before its first use (they
+ *    hold that header).  lossk_decode_workspace_bytes gives its size.
+ *  - Results do not depend on how the work is split over the GPU, except for
+ *    the rounding of lossk_paged_attn, whose order of sums is a function of
+ *    the shape, the lengths and the device alone. */
+
+/* Workspace kinds of the decoding calls, with the sizes a..d that
+ * lossk_decode_workspace_bytes takes:
+ *   LOSSK_KIND_BEAM_SELECT: batch, beams, vocab, n_out
+ *   LOSSK_KIND_CACHE:       n_seq, n_pages, 0, 0 (every lossk_cache_ call and
+ *                           lossk_beam_gather; n_seq counts the larger side
+ *                           of a fork)
+ *   LOSSK_KIND_PAGED_ATTN:  n_seq, n_q_heads, n_kv_heads, head_dim */
+enum lossk_decode_kind { LOSSK_KIND_BEAM_SELECT = 0, LOSSK_KIND_CACHE = 1, LOSSK_KIND_PAGED_ATTN = 2 };
+
+/* Bytes of workspace (a multiple of 256); -1 for sizes the call refuses. */
+int64_t lossk_decode_workspace_bytes(int32_t kind, int64_t a, int64_t b, int64_t c, int64_t d);
+
+#define LOSSK_BEAM_MAX_BEAMS 64
+#define LOSSK_BEAM_MAX_OUT 128
+
+/* Beam search's selection over beams and vocabulary.  Row r = b beams + k of
+ * logits[batch beams][vocab] (dtype; row_stride elements apart) belongs to
+ * beam k of batch entry b, whose hypothesis has the log-probability
+ * scores[b][k].  With x = logits / temperature over the allowed entries,
+ *   lse_r = log sum exp x,  score(k, v) = scores[b][k] + x_v - lse_r
+ * and a candidate's rank is score / max(1, len)^length_alpha, len being
+ * lengths[b][k] + 1 (lengths NULL: rank = score).  A finished beam has one
+ * candidate: itself, with token end_token, its own score and len =
+ * lengths[b][k]; its logits are not read.  Per batch entry the n_out best
+ * candidates are written in order of falling rank; equal ranks go by the
+ * lower beam, then the lower token.  Ranks are compared in double.
+ *   allow        uint32 words or NULL: bit v % 32 of word v / 32 of the row's
+ *                mask is 1 where token v may follow.  allow_stride words lie
+ *                between rows' masks; 0: one mask for all rows.  What the
+ *                logits hold at other tokens does not matter.
+ *   finished     uint8[batch][beams] or NULL (none)
+ *   end_token    in [0, vocab), or -1: no token ends a hypothesis (586)
+ *   lengths      int32[batch][beams] or NULL
+ * A logit of -infinity is no candidate.  A beam whose score is -infinity, or
+ * whose allowed logits are all -infinity (or whose mask allows nothing), has
+ * no candidates; nor has one with a NaN or +infinity among its allowed
+ * logits, or as its score (585 in the header).  Where fewer than n_out
+ * candidates exist, the places left get parent -1, token -1, score -infinity,
+ * finished 0, length 0.
+ * Outputs per batch entry [n_out]: parent_out int32 (the beam), token_out
+ * int64, score_out float; and unless NULL finished_out uint8 (the beam was
+ * finished or the token is end_token) and length_out int32 (len; with lengths
+ * NULL it counts from 0).  lse_out float[batch beams] or NULL: lse_r, or
+ * -infinity for a row without candidates of its own.
+ * 1 <= beams <= 64 and n_out <= 128 (583).  temperature finite and > 0,
+ * length_alpha finite (585). */
+int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out, int32_t dtype,
+                          const void *logits, int64_t logits_len, int64_t row_stride, const float *scores,
+                          int64_t scores_len, double temperature, const uint32_t *allow, int64_t allow_len,
+                          int64_t allow_stride, const uint8_t *finished, int64_t end_token, const int32_t *lengths,
+                          double length_alpha, int32_t *parent_out, int64_t *token_out, float *score_out,
+                          uint8_t *finished_out, int32_t *length_out, float *lse_out, void *workspace,
+                          int64_t workspace_bytes, lossk_stream_t stream);
+
+/* Reorders states by parent: row j of group g of dst takes row parent[g][j]
+ * of group g of src, row_bytes bytes each (src [n_group][n_src][row_bytes],
+ * dst [n_group][n_dst][row_bytes], which must not overlap src).  Parent -1
+ * gives zeros; another id outside [0, n_src) gives zeros and 586. */
+int32_t lossk_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t row_bytes, const int32_t *parent,
+                          int64_t parent_len, const void *src, int64_t src_bytes, void *dst, int64_t dst_bytes,
+                          void *workspace, int64_t workspace_bytes, lossk_stream_t stream);
+
 /* ---- tracing ----------------------------------------------------------------
  * Every kernel the library launches belongs to one of LOSSK_N_KERNELS kinds
  * (lossk_kernel_name gives its name).  lossk_launch_count() is the number of
@@ -464,7 +561,7 @@ int32_t lossk_ce_from_logits_static(int64_t n_tok, int64_t vocab, int32_t dtype,
  * events, adds their durations per kind into total_ms[kind] and
  * launches[kind] (host arrays of `cap` entries), and clears them if `reset`.
  * Returns the number of kinds written, or -1 on a CUDA error. */
-#define LOSSK_N_KERNELS 23
+#define LOSSK_N_KERNELS 35
 const char *lossk_kernel_name(int32_t kind);
 int64_t lossk_launch_count(void);
 int32_t lossk_profile_enable(int32_t on);

@@ -1216,13 +1216,14 @@ int32_t lossk_device_status(void *workspace, int64_t workspace_bytes, lossk_stre
     if (!workspace || workspace_bytes < 256) return LOSSK_LENGTH_MISMATCH;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
-    int err = 0;
-    if (cudaMemcpy(&err, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
-        return LOSSK_DEVICE_ERROR;
-    if (err == 0) return LOSSK_OK;
-    const int zero = 0;
-    if (cudaMemcpy(workspace, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
-        return LOSSK_DEVICE_ERROR;
+    WsHeader h;
+    if (cudaMemcpy(&h, workspace, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    const int fault = h.pad[HDR_FAULT];
+    if (h.err == 0 && fault == 0) return LOSSK_OK;
+    const int err = h.err;
+    h.err = h.pad[HDR_FAULT] = 0;
+    if (cudaMemcpy(workspace, &h, sizeof(h), cudaMemcpyHostToDevice) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    if (err == 0) return fault;
     return LOSSK_DEVICE_TIMEOUT;
 }
 
@@ -1399,7 +1400,9 @@ const char *lossk_kernel_name(int32_t kind)
                                       "merge_distill", "reduce",        "tokp_ce",     "sum_splits",
                                       "from_logits",  "tc_fused",      "tgt_logit",   "merge_fused",
                                       "combine_dh",   "teacher_stats", "distill_logits", "readback",
-                                      "wait_selftest", "shard_tgt",    "shard_combine"};
+                                      "wait_selftest", "shard_tgt",    "shard_combine", "beam_rows",    "beam_merge",
+                                      "beam_gather",  "cache_fork",    "cache_plan",    "cache_copy",   "cache_free",
+                                      "cache_rank",   "cache_write",   "attn_plan",     "attn",         "attn_join"};
     return (kind >= 0 && kind < KK_N) ? names[kind] : "unknown_kernel";
 }
 

@@ -26,8 +26,9 @@ struct WsHeader {
     int bad_targets;  // count of targets outside [0, vocab)
     int n_valid;      // counted tokens
     int redo;         // fused pass: a row left the range its reference shift covers
-    int pad[60];
+    int pad[60];      // pad[HDR_FAULT]: what a decoding call found wrong on the device (a lossk_status)
 };
+constexpr int HDR_FAULT = 1;
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
 // Per-(token, logit tile) partial statistics written by the forward pass
@@ -183,6 +184,18 @@ enum KernelKind : int {
     KK_SELFTEST,
     KK_SHARD_TGT,
     KK_SHARD_COMBINE,
+    KK_BEAM_ROWS,
+    KK_BEAM_MERGE,
+    KK_BEAM_GATHER,
+    KK_CACHE_FORK,
+    KK_CACHE_PLAN,
+    KK_CACHE_COPY,
+    KK_CACHE_FREE,
+    KK_CACHE_RANK,
+    KK_CACHE_WRITE,
+    KK_ATTN_PLAN,
+    KK_ATTN,
+    KK_ATTN_JOIN,
     KK_N
 };
 

@@ -77,6 +77,10 @@ def _load():
         "lossk_ce_shard_bwd": (_i32, [_i64, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64,
                                       _vp, _dbl, _dbl, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
         "lossk_selftest_wait": (_i32, [_i32, _i32, _i64, ctypes.POINTER(_i32), _vp, _i64, _vp]),
+        "lossk_decode_workspace_bytes": (_i64, [_i32, _i64, _i64, _i64, _i64]),
+        "lossk_beam_select": (_i32, [_i64, _i64, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _dbl, _vp, _i64,
+                                     _i64, _vp, _i64, _vp, _dbl, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+        "lossk_beam_gather": (_i32, [_i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
         "lossk_kernel_name": (ctypes.c_char_p, [_i32]),
         "lossk_launch_count": (_i64, []),
         "lossk_profile_enable": (_i32, [_i32]),
@@ -97,8 +101,9 @@ EXPORTED = ("lossk_status_name", "lossk_dims_check", "lossk_chunk_check", "lossk
             "lossk_ce_fwd_bwd_ex", "lossk_distill_fwd_bwd_ex", "lossk_ce_chunk_invariance",
             "lossk_distill_from_logits",
             "lossk_ce_from_logits_static", "lossk_selftest_wait", "lossk_ce_shard_fwd",
-            "lossk_ce_shard_combine", "lossk_ce_shard_bwd", "lossk_kernel_name", "lossk_launch_count", "lossk_profile_enable", "lossk_profile_read")
-N_KERNELS = 23
+            "lossk_ce_shard_combine", "lossk_ce_shard_bwd", "lossk_decode_workspace_bytes", "lossk_beam_select",
+            "lossk_beam_gather", "lossk_kernel_name", "lossk_launch_count", "lossk_profile_enable", "lossk_profile_read")
+N_KERNELS = 35
 
 
 class LosskError(RuntimeError):
