@@ -552,6 +552,91 @@ int32_t lossk_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t
                           int64_t parent_len, const void *src, int64_t src_bytes, void *dst, int64_t dst_bytes,
                           void *workspace, int64_t workspace_bytes, lossk_stream_t stream);
 
+/* ---- the cache's pages -----------------------------------------------------------
+ * Sizes shared by these calls: n_seq rows of table (table_stride >= max_pages
+ * entries apart), page_size tokens per page, n_pages pages (581, 583). */
+
+/* Forks: row j of group g of table_out takes the pages and the length of row
+ * parent[g][j] of the same group of table (n_group groups of n_src rows become
+ * n_group groups of n_dst).  Parent -1 makes an empty sequence.  Every source
+ * row is given up and every new one holds its pages: ref[p] += children - 1
+ * for each page p of a row with `children` children.  Pages left without a
+ * holder are free from then on.  Entries past a row's last page become -1.
+ * table_out and lens_out must not overlap table and lens (582 where they are
+ * the same).  An id or length out of range: the row's length counts as 0, the
+ * entry becomes -1, 586 in the header. */
+int32_t lossk_cache_fork(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t max_pages, int64_t page_size,
+                         int64_t n_pages, const int32_t *parent, int64_t parent_len, const int32_t *table,
+                         int64_t table_len, int64_t table_stride, const int32_t *lens, int64_t lens_len, int32_t *ref,
+                         int64_t ref_len, int32_t *table_out, int64_t table_out_len, int64_t table_out_stride,
+                         int32_t *lens_out, int64_t lens_out_len, void *workspace, int64_t workspace_bytes,
+                         lossk_stream_t stream);
+
+/* Gives each sequence places of its own for its next n_new tokens (int32[n_seq],
+ * or NULL: n_new_all for every one; 0 leaves a sequence alone).  A last page
+ * that is partly filled and shared is replaced by a copy, in every plane of
+ * the pool; of a page's sharers in this call the last one keeps the page
+ * itself if no other row holds it.  Pages that the tokens open are added.
+ * Pages are handed out in sequence order, the free page of lowest id first,
+ * and their count becomes 1; lens stays as it is (the caller adds the tokens
+ * once they are written).  Either every sequence is served or nothing changes:
+ * too few free pages or table entries leave 584 in the header, an id or length
+ * out of range 586.
+ * The pool: n_planes planes (say 2 per layer, keys and values) plane_stride
+ * bytes apart, each of n_pages pages page_stride bytes apart, page_bytes long;
+ * address and sizes multiples of 16 bytes (591). */
+int32_t lossk_cache_reserve(int64_t n_seq, int64_t max_pages, int64_t page_size, int64_t n_pages, int64_t n_new_all,
+                            const int32_t *n_new, int64_t n_new_len, int32_t *table, int64_t table_len,
+                            int64_t table_stride, const int32_t *lens, int64_t lens_len, int32_t *ref,
+                            int64_t ref_len, void *pool, int64_t pool_bytes, int64_t n_planes, int64_t plane_stride,
+                            int64_t page_stride, int64_t page_bytes, void *workspace, int64_t workspace_bytes,
+                            lossk_stream_t stream);
+
+/* Drops sequences: those with a nonzero byte in drop (uint8[n_seq]; NULL: all)
+ * give up their pages; their entries become -1, their length 0. */
+int32_t lossk_cache_free(int64_t n_seq, int64_t max_pages, int64_t page_size, int64_t n_pages, const uint8_t *drop,
+                         int64_t drop_len, int32_t *table, int64_t table_len, int64_t table_stride, int32_t *lens,
+                         int64_t lens_len, int32_t *ref, int64_t ref_len, void *workspace, int64_t workspace_bytes,
+                         lossk_stream_t stream);
+
+/* Moves the live pages to the front of the pool, so that its tail can be given
+ * back: with n_live pages of positive count, the k-th such page of id >= n_live
+ * moves to the k-th free page below n_live, in every plane.  table must list
+ * every row that holds pages.  table_out (may be table itself) gets the new
+ * ids, ref_out (not ref) the new counts, *n_live_out (device) n_live.  What a
+ * page held stays in its old place as well.  An entry that is out of range or
+ * whose page is free becomes -1 and leaves 586 in the header. */
+int32_t lossk_cache_compact(int64_t n_seq, int64_t max_pages, int64_t page_size, int64_t n_pages, const int32_t *table,
+                            int64_t table_len, int64_t table_stride, const int32_t *lens, int64_t lens_len,
+                            const int32_t *ref, int64_t ref_len, int32_t *table_out, int64_t table_out_len,
+                            int64_t table_out_stride, int32_t *ref_out, int64_t ref_out_len, int32_t *n_live_out,
+                            void *pool, int64_t pool_bytes, int64_t n_planes, int64_t plane_stride,
+                            int64_t page_stride, int64_t page_bytes, void *workspace, int64_t workspace_bytes,
+                            lossk_stream_t stream);
+
+/* Copies page src[i] to page dst[i] in every plane, for i < n_copy; -1 in both
+ * is skipped.  No page may be written twice, or both written and read. */
+int32_t lossk_cache_copy(int64_t n_copy, int64_t n_pages, const int32_t *src, int64_t src_len, const int32_t *dst,
+                         int64_t dst_len, void *pool, int64_t pool_bytes, int64_t n_planes, int64_t plane_stride,
+                         int64_t page_stride, int64_t page_bytes, void *workspace, int64_t workspace_bytes,
+                         lossk_stream_t stream);
+
+/* Writes new tokens' key and value rows of one layer into their pages.
+ * k_new, v_new [n_tok][n_kv_heads][head_dim] (tokens new_stride elements
+ * apart) go to positions lens[i], lens[i] + 1, ... of their sequence: sequence
+ * i has rows first[i] .. first[i + 1] - 1 (int32[n_seq + 1]; NULL: n_tok ==
+ * n_seq and row i is sequence i's one token).  Element (page, token, head, e)
+ * of the layer's pages lies at page page_stride + token tok_stride + head
+ * head_stride + e from k_pages and v_pages (pages_len elements each).  A
+ * position without a page leaves 586 in the header and is not written. */
+int32_t lossk_cache_write(int64_t n_tok, int64_t n_seq, int64_t n_kv_heads, int64_t head_dim, int64_t max_pages,
+                          int64_t page_size, int64_t n_pages, int32_t dtype, const void *k_new, const void *v_new,
+                          int64_t new_len, int64_t new_stride, void *k_pages, void *v_pages, int64_t pages_len,
+                          int64_t page_stride, int64_t tok_stride, int64_t head_stride, const int32_t *table,
+                          int64_t table_len, int64_t table_stride, const int32_t *lens, int64_t lens_len,
+                          const int32_t *first, int64_t first_len, void *workspace, int64_t workspace_bytes,
+                          lossk_stream_t stream);
+
 /* ---- tracing ----------------------------------------------------------------
  * Every kernel the library launches belongs to one of LOSSK_N_KERNELS kinds
  * (lossk_kernel_name gives its name).  lossk_launch_count() is the number of

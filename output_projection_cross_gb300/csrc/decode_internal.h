@@ -56,4 +56,82 @@ cudaError_t launch_beam_merge(const BeamArgs &a, cudaStream_t st);
 cudaError_t launch_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t row_bytes,
                                const int32_t *parent, const void *src, void *dst, int *fault, cudaStream_t st);
 
+// ---- cache pages -----------------------------------------------------------------
+struct ForkArgs {
+    int n_group, n_src, n_dst, max_pages, page, n_pages;
+    const int32_t *parent, *table, *lens;
+    int64_t table_stride, table_out_stride;
+    int32_t *ref, *table_out, *lens_out;
+    int *fault;
+};
+
+struct SharerSlot {
+    int page, count, top;
+};
+struct ReserveArgs {
+    int n_seq, max_pages, page, n_pages, n_new_all;
+    const int32_t *n_new, *lens;
+    int32_t *table, *ref;
+    int64_t table_stride;
+    SharerSlot *hash;       // a power of two of slots, at least 2 n_seq
+    int hash_mask;
+    int4 *need;             // [n_seq]
+    int32_t *free_list;     // [n_pages]
+    int2 *moves;            // pages to copy (from, to) and their number
+    int *n_copy;
+    int *fault;
+};
+
+struct CopyArgs {
+    char *pool;
+    int64_t plane_stride, page_stride, page_bytes;   // bytes
+    int n_planes, n_pages;
+    const int2 *moves;      // or src and dst
+    const int32_t *src, *dst;
+    int64_t n;
+    const int *n_dev;       // the number of moves where it is the device's (else n)
+    int *fault;
+};
+
+struct FreeArgs {
+    int n_seq, max_pages, page, n_pages;
+    const uint8_t *drop;
+    int32_t *table, *lens, *ref;
+    int64_t table_stride;
+    int *fault;
+};
+
+struct CompactArgs {
+    int n_seq, max_pages, page, n_pages;
+    const int32_t *table, *lens, *ref;
+    int64_t table_stride, table_out_stride;
+    int32_t *table_out, *ref_out, *n_live_out;
+    int32_t *new_id;        // [n_pages]: a mover's new id
+    int2 *moves;
+    int *n_copy;
+    int *fault;
+};
+
+struct WriteArgs {
+    int64_t n_tok;
+    int n_seq, n_kv, row_bytes, page, n_pages, max_pages;
+    const char *k_new, *v_new;
+    int64_t k_row, v_row;                                   // bytes from token to token
+    char *k, *v;
+    int64_t k_page, k_tok, k_head, v_page, v_tok, v_head;   // bytes
+    const int32_t *table, *lens, *first;
+    int64_t table_stride;
+    int *fault;
+};
+
+cudaError_t launch_cache_fork(const ForkArgs &a, cudaStream_t st);
+cudaError_t launch_cache_plan(const ReserveArgs &a, cudaStream_t st);
+// most: the largest number of moves there can be
+cudaError_t launch_cache_copy(const CopyArgs &a, int64_t most, cudaStream_t st);
+cudaError_t launch_cache_free(const FreeArgs &a, cudaStream_t st);
+cudaError_t launch_cache_rank(const CompactArgs &a, cudaStream_t st);
+cudaError_t launch_cache_move(const CompactArgs &a, const CopyArgs &c, cudaStream_t st);
+// word: bytes of the widest access every row allows (16, 4 or 2)
+cudaError_t launch_cache_write(const WriteArgs &a, int word, cudaStream_t st);
+
 } // namespace lossk

@@ -18,12 +18,6 @@ bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_
 bool dtype_ok(int32_t d) { return d == LOSSK_F32 || d == LOSSK_BF16 || d == LOSSK_F16; }
 int64_t esize(int32_t d) { return d == LOSSK_F32 ? 4 : 2; }
 
-// 581 or 583 for the first size outside [1, most].
-int32_t size_check(int64_t v, int64_t most)
-{
-    return v < 1 ? LOSSK_EMPTY_DIMENSION : v > most ? LOSSK_DIMENSION_TOO_LARGE : LOSSK_OK;
-}
-
 struct BeamLayout {
     int n_split;
     size_t off_stat, off_cand, total;
@@ -41,6 +35,86 @@ int32_t beam_layout(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out, 
     L->off_cand = align256(L->off_stat + sizeof(BeamStat) * rows * L->n_split);
     L->total = align256(L->off_cand + sizeof(BeamCand) * rows * L->n_split * n_out);
     return LOSSK_OK;
+}
+
+// The scratch of the cache calls.
+struct CacheLayout {
+    int64_t slots;
+    size_t off_hash, off_need, off_free, off_moves, off_id, total;
+};
+
+int32_t cache_layout(int64_t n_seq, int64_t n_pages, CacheLayout *L)
+{
+    if (n_seq < 1 || n_pages < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_seq > MAX_DIM || n_pages > MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    L->slots = 2;
+    while (L->slots < 2 * n_seq) L->slots *= 2;
+    const int64_t moves = n_seq > n_pages / 2 + 1 ? n_seq : n_pages / 2 + 1;
+    L->off_hash = 512;                                     // the header, then counters
+    L->off_need = align256(L->off_hash + sizeof(SharerSlot) * L->slots);
+    L->off_free = align256(L->off_need + sizeof(int4) * n_seq);
+    L->off_moves = align256(L->off_free + sizeof(int32_t) * n_pages);
+    L->off_id = align256(L->off_moves + sizeof(int2) * moves);
+    L->total = align256(L->off_id + sizeof(int32_t) * n_pages);
+    return LOSSK_OK;
+}
+
+// The sizes every cache call shares.
+int32_t cache_sizes(int64_t n_seq, int64_t max_pages, int64_t page, int64_t n_pages)
+{
+    if (n_seq < 1 || max_pages < 1 || page < 1 || n_pages < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_seq > MAX_DIM || max_pages > MAX_DIM || page > MAX_DIM || n_pages > MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    return LOSSK_OK;
+}
+
+bool table_short(int64_t n_seq, int64_t max_pages, const void *table, int64_t len, int64_t stride)
+{
+    return !table || stride < max_pages || stride > (int64_t(1) << 40) || len < (n_seq - 1) * stride + max_pages;
+}
+
+// A pool of n_planes planes of n_pages pages: 581, 582 or 591.
+int32_t pool_check(int64_t n_pages, const void *pool, int64_t pool_bytes, int64_t n_planes, int64_t plane_stride,
+                   int64_t page_stride, int64_t page_bytes)
+{
+    const int64_t most = int64_t(1) << 45;
+    if (n_planes < 1 || page_bytes < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_planes > MAX_DIM || page_bytes > most) return LOSSK_DIMENSION_TOO_LARGE;
+    if (!pool || page_stride < page_bytes || page_stride > most / n_pages || plane_stride < 0 ||
+        plane_stride > most / n_planes ||
+        (n_planes > 1 && plane_stride < page_bytes) ||
+        pool_bytes < (n_planes - 1) * plane_stride + (n_pages - 1) * page_stride + page_bytes)
+        return LOSSK_LENGTH_MISMATCH;
+    return LOSSK_OK;
+}
+
+bool pool_unaligned(const void *pool, int64_t plane_stride, int64_t page_stride, int64_t page_bytes)
+{
+    return misaligned(pool, 16) || ((plane_stride | page_stride | page_bytes) & 15) != 0;
+}
+
+// Key or value pages of one layer: element (page, token, head, i) at page
+// page_stride + token tok_stride + head head_stride + i.
+bool pages_short(int64_t n_pages, int64_t page, int64_t n_kv, int64_t hd, const void *p, int64_t len,
+                 int64_t page_stride, int64_t tok_stride, int64_t head_stride)
+{
+    const int64_t most = int64_t(1) << 44;
+    return !p || page_stride < 0 || tok_stride < 0 || head_stride < 0 || page_stride > most / n_pages ||
+           tok_stride > most / page || head_stride > most / n_kv ||
+           len < (n_pages - 1) * page_stride + (page - 1) * tok_stride + (n_kv - 1) * head_stride + hd;
+}
+
+CopyArgs copy_args(void *pool, int64_t n_planes, int64_t plane_stride, int64_t page_stride, int64_t page_bytes,
+                   int64_t n_pages, int *fault)
+{
+    CopyArgs c{};
+    c.pool = static_cast<char *>(pool);
+    c.plane_stride = plane_stride;
+    c.page_stride = page_stride;
+    c.page_bytes = page_bytes;
+    c.n_planes = static_cast<int>(n_planes);
+    c.n_pages = static_cast<int>(n_pages);
+    c.fault = fault;
+    return c;
 }
 
 int32_t ws_check(const void *ws, int64_t bytes, size_t need)
@@ -64,8 +138,8 @@ int64_t lossk_decode_workspace_bytes(int32_t kind, int64_t a, int64_t b, int64_t
         return beam_layout(a, b, c, d, &L) == LOSSK_OK ? static_cast<int64_t>(L.total) : -1;
     }
     if (kind == LOSSK_KIND_CACHE) {
-        if (size_check(a, MAX_DIM) != LOSSK_OK || size_check(b, MAX_DIM) != LOSSK_OK) return -1;
-        return 256;
+        CacheLayout L;
+        return cache_layout(a, b, &L) == LOSSK_OK ? static_cast<int64_t>(L.total) : -1;
     }
     return -1;
 }
@@ -152,6 +226,261 @@ int32_t lossk_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Launch k(KK_BEAM_GATHER, st);
     return status_of(launch_beam_gather(n_group, n_src, n_dst, row_bytes, parent, src, dst, fault_of(workspace), st));
+}
+
+int32_t lossk_cache_fork(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t max_pages, int64_t page_size,
+                         int64_t n_pages, const int32_t *parent, int64_t parent_len, const int32_t *table,
+                         int64_t table_len, int64_t table_stride, const int32_t *lens, int64_t lens_len, int32_t *ref,
+                         int64_t ref_len, int32_t *table_out, int64_t table_out_len, int64_t table_out_stride,
+                         int32_t *lens_out, int64_t lens_out_len, void *workspace, int64_t workspace_bytes,
+                         lossk_stream_t stream)
+{
+    if (n_group < 1 || n_src < 1 || n_dst < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_group > MAX_DIM || n_src > MAX_DIM || n_dst > MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    const int64_t rs = n_group * n_src, rd = n_group * n_dst;
+    int32_t s = cache_sizes(rs > rd ? rs : rd, max_pages, page_size, n_pages);
+    if (s != LOSSK_OK) return s;
+    if (!parent || parent_len < rd || table_short(rs, max_pages, table, table_len, table_stride) || !lens ||
+        lens_len < rs || !ref || ref_len < n_pages ||
+        table_short(rd, max_pages, table_out, table_out_len, table_out_stride) || !lens_out || lens_out_len < rd ||
+        table_out == table || lens_out == lens)
+        return LOSSK_LENGTH_MISMATCH;
+    if ((s = ws_check(workspace, workspace_bytes, 256)) != LOSSK_OK) return s;
+    if (misaligned(workspace, 256) || misaligned(parent, 4) || misaligned(table, 4) || misaligned(lens, 4) ||
+        misaligned(ref, 4) || misaligned(table_out, 4) || misaligned(lens_out, 4))
+        return LOSSK_UNALIGNED;
+    ForkArgs a{};
+    a.n_group = static_cast<int>(n_group);
+    a.n_src = static_cast<int>(n_src);
+    a.n_dst = static_cast<int>(n_dst);
+    a.max_pages = static_cast<int>(max_pages);
+    a.page = static_cast<int>(page_size);
+    a.n_pages = static_cast<int>(n_pages);
+    a.parent = parent;
+    a.table = table;
+    a.lens = lens;
+    a.table_stride = table_stride;
+    a.table_out_stride = table_out_stride;
+    a.ref = ref;
+    a.table_out = table_out;
+    a.lens_out = lens_out;
+    a.fault = fault_of(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Launch k(KK_CACHE_FORK, st);
+    return status_of(launch_cache_fork(a, st));
+}
+
+int32_t lossk_cache_reserve(int64_t n_seq, int64_t max_pages, int64_t page_size, int64_t n_pages, int64_t n_new_all,
+                            const int32_t *n_new, int64_t n_new_len, int32_t *table, int64_t table_len,
+                            int64_t table_stride, const int32_t *lens, int64_t lens_len, int32_t *ref,
+                            int64_t ref_len, void *pool, int64_t pool_bytes, int64_t n_planes, int64_t plane_stride,
+                            int64_t page_stride, int64_t page_bytes, void *workspace, int64_t workspace_bytes,
+                            lossk_stream_t stream)
+{
+    int32_t s = cache_sizes(n_seq, max_pages, page_size, n_pages);
+    if (s != LOSSK_OK) return s;
+    CacheLayout L;
+    if ((s = cache_layout(n_seq, n_pages, &L)) != LOSSK_OK) return s;
+    if ((s = pool_check(n_pages, pool, pool_bytes, n_planes, plane_stride, page_stride, page_bytes)) != LOSSK_OK)
+        return s;
+    if (n_new_all < 0 || n_new_all > MAX_DIM || (n_new && n_new_len < n_seq) ||
+        table_short(n_seq, max_pages, table, table_len, table_stride) || !lens || lens_len < n_seq || !ref ||
+        ref_len < n_pages)
+        return LOSSK_LENGTH_MISMATCH;
+    if ((s = ws_check(workspace, workspace_bytes, L.total)) != LOSSK_OK) return s;
+    if (pool_unaligned(pool, plane_stride, page_stride, page_bytes) || misaligned(workspace, 256) ||
+        misaligned(n_new, 4) || misaligned(table, 4) || misaligned(lens, 4) || misaligned(ref, 4))
+        return LOSSK_UNALIGNED;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    ReserveArgs a{};
+    a.n_seq = static_cast<int>(n_seq);
+    a.max_pages = static_cast<int>(max_pages);
+    a.page = static_cast<int>(page_size);
+    a.n_pages = static_cast<int>(n_pages);
+    a.n_new_all = static_cast<int>(n_new_all);
+    a.n_new = n_new;
+    a.lens = lens;
+    a.table = table;
+    a.ref = ref;
+    a.table_stride = table_stride;
+    a.hash = reinterpret_cast<SharerSlot *>(ws + L.off_hash);
+    a.hash_mask = static_cast<int>(L.slots - 1);
+    a.need = reinterpret_cast<int4 *>(ws + L.off_need);
+    a.free_list = reinterpret_cast<int32_t *>(ws + L.off_free);
+    a.moves = reinterpret_cast<int2 *>(ws + L.off_moves);
+    a.n_copy = reinterpret_cast<int *>(ws + 256);
+    a.fault = fault_of(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    {
+        Launch k(KK_CACHE_PLAN, st);
+        if (launch_cache_plan(a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    }
+    CopyArgs c = copy_args(pool, n_planes, plane_stride, page_stride, page_bytes, n_pages, a.fault);
+    c.moves = a.moves;
+    c.n_dev = a.n_copy;
+    Launch k(KK_CACHE_COPY, st);
+    return status_of(launch_cache_copy(c, n_seq, st));
+}
+
+int32_t lossk_cache_free(int64_t n_seq, int64_t max_pages, int64_t page_size, int64_t n_pages, const uint8_t *drop,
+                         int64_t drop_len, int32_t *table, int64_t table_len, int64_t table_stride, int32_t *lens,
+                         int64_t lens_len, int32_t *ref, int64_t ref_len, void *workspace, int64_t workspace_bytes,
+                         lossk_stream_t stream)
+{
+    int32_t s = cache_sizes(n_seq, max_pages, page_size, n_pages);
+    if (s != LOSSK_OK) return s;
+    if ((drop && drop_len < n_seq) || table_short(n_seq, max_pages, table, table_len, table_stride) || !lens ||
+        lens_len < n_seq || !ref || ref_len < n_pages)
+        return LOSSK_LENGTH_MISMATCH;
+    if ((s = ws_check(workspace, workspace_bytes, 256)) != LOSSK_OK) return s;
+    if (misaligned(workspace, 256) || misaligned(table, 4) || misaligned(lens, 4) || misaligned(ref, 4))
+        return LOSSK_UNALIGNED;
+    FreeArgs a{};
+    a.n_seq = static_cast<int>(n_seq);
+    a.max_pages = static_cast<int>(max_pages);
+    a.page = static_cast<int>(page_size);
+    a.n_pages = static_cast<int>(n_pages);
+    a.drop = drop;
+    a.table = table;
+    a.lens = lens;
+    a.ref = ref;
+    a.table_stride = table_stride;
+    a.fault = fault_of(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Launch k(KK_CACHE_FREE, st);
+    return status_of(launch_cache_free(a, st));
+}
+
+int32_t lossk_cache_compact(int64_t n_seq, int64_t max_pages, int64_t page_size, int64_t n_pages, const int32_t *table,
+                            int64_t table_len, int64_t table_stride, const int32_t *lens, int64_t lens_len,
+                            const int32_t *ref, int64_t ref_len, int32_t *table_out, int64_t table_out_len,
+                            int64_t table_out_stride, int32_t *ref_out, int64_t ref_out_len, int32_t *n_live_out,
+                            void *pool, int64_t pool_bytes, int64_t n_planes, int64_t plane_stride,
+                            int64_t page_stride, int64_t page_bytes, void *workspace, int64_t workspace_bytes,
+                            lossk_stream_t stream)
+{
+    int32_t s = cache_sizes(n_seq, max_pages, page_size, n_pages);
+    if (s != LOSSK_OK) return s;
+    CacheLayout L;
+    if ((s = cache_layout(n_seq, n_pages, &L)) != LOSSK_OK) return s;
+    if ((s = pool_check(n_pages, pool, pool_bytes, n_planes, plane_stride, page_stride, page_bytes)) != LOSSK_OK)
+        return s;
+    if (table_short(n_seq, max_pages, table, table_len, table_stride) || !lens || lens_len < n_seq || !ref ||
+        ref_len < n_pages || table_short(n_seq, max_pages, table_out, table_out_len, table_out_stride) || !ref_out ||
+        ref_out_len < n_pages || ref_out == ref || !n_live_out || (table_out == table && table_out_stride != table_stride))
+        return LOSSK_LENGTH_MISMATCH;
+    if ((s = ws_check(workspace, workspace_bytes, L.total)) != LOSSK_OK) return s;
+    if (pool_unaligned(pool, plane_stride, page_stride, page_bytes) || misaligned(workspace, 256) ||
+        misaligned(table, 4) || misaligned(lens, 4) || misaligned(ref, 4) || misaligned(table_out, 4) ||
+        misaligned(ref_out, 4) || misaligned(n_live_out, 4))
+        return LOSSK_UNALIGNED;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    CompactArgs a{};
+    a.n_seq = static_cast<int>(n_seq);
+    a.max_pages = static_cast<int>(max_pages);
+    a.page = static_cast<int>(page_size);
+    a.n_pages = static_cast<int>(n_pages);
+    a.table = table;
+    a.lens = lens;
+    a.ref = ref;
+    a.table_stride = table_stride;
+    a.table_out_stride = table_out_stride;
+    a.table_out = table_out;
+    a.ref_out = ref_out;
+    a.n_live_out = n_live_out;
+    a.new_id = reinterpret_cast<int32_t *>(ws + L.off_id);
+    a.moves = reinterpret_cast<int2 *>(ws + L.off_moves);
+    a.n_copy = reinterpret_cast<int *>(ws + 256);
+    a.fault = fault_of(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    {
+        Launch k(KK_CACHE_RANK, st);
+        if (launch_cache_rank(a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    }
+    CopyArgs c = copy_args(pool, n_planes, plane_stride, page_stride, page_bytes, n_pages, a.fault);
+    c.moves = a.moves;
+    Launch k(KK_CACHE_COPY, st);
+    return status_of(launch_cache_move(a, c, st));
+}
+
+int32_t lossk_cache_copy(int64_t n_copy, int64_t n_pages, const int32_t *src, int64_t src_len, const int32_t *dst,
+                         int64_t dst_len, void *pool, int64_t pool_bytes, int64_t n_planes, int64_t plane_stride,
+                         int64_t page_stride, int64_t page_bytes, void *workspace, int64_t workspace_bytes,
+                         lossk_stream_t stream)
+{
+    if (n_copy < 1 || n_pages < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_copy > MAX_DIM || n_pages > MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    int32_t s = pool_check(n_pages, pool, pool_bytes, n_planes, plane_stride, page_stride, page_bytes);
+    if (s != LOSSK_OK) return s;
+    if (!src || !dst || src_len < n_copy || dst_len < n_copy) return LOSSK_LENGTH_MISMATCH;
+    if ((s = ws_check(workspace, workspace_bytes, 256)) != LOSSK_OK) return s;
+    if (pool_unaligned(pool, plane_stride, page_stride, page_bytes) || misaligned(workspace, 256) ||
+        misaligned(src, 4) || misaligned(dst, 4))
+        return LOSSK_UNALIGNED;
+    CopyArgs c = copy_args(pool, n_planes, plane_stride, page_stride, page_bytes, n_pages, fault_of(workspace));
+    c.src = src;
+    c.dst = dst;
+    c.n = n_copy;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Launch k(KK_CACHE_COPY, st);
+    return status_of(launch_cache_copy(c, n_copy, st));
+}
+
+int32_t lossk_cache_write(int64_t n_tok, int64_t n_seq, int64_t n_kv_heads, int64_t head_dim, int64_t max_pages,
+                          int64_t page_size, int64_t n_pages, int32_t dtype, const void *k_new, const void *v_new,
+                          int64_t new_len, int64_t new_stride, void *k_pages, void *v_pages, int64_t pages_len,
+                          int64_t page_stride, int64_t tok_stride, int64_t head_stride, const int32_t *table,
+                          int64_t table_len, int64_t table_stride, const int32_t *lens, int64_t lens_len,
+                          const int32_t *first, int64_t first_len, void *workspace, int64_t workspace_bytes,
+                          lossk_stream_t stream)
+{
+    if (n_tok < 1 || n_kv_heads < 1 || head_dim < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_tok > MAX_DIM || n_kv_heads > MAX_DIM || head_dim > MAX_DIM || n_kv_heads * head_dim > MAX_DIM)
+        return LOSSK_DIMENSION_TOO_LARGE;
+    int32_t s = cache_sizes(n_seq, max_pages, page_size, n_pages);
+    if (s != LOSSK_OK) return s;
+    const int64_t row = n_kv_heads * head_dim;
+    if (!dtype_ok(dtype) || !k_new || !v_new || new_stride < row || new_stride > (int64_t(1) << 40) ||
+        new_len < (n_tok - 1) * new_stride + row ||
+        pages_short(n_pages, page_size, n_kv_heads, head_dim, k_pages, pages_len, page_stride, tok_stride,
+                    head_stride) ||
+        !v_pages || table_short(n_seq, max_pages, table, table_len, table_stride) || !lens || lens_len < n_seq ||
+        (first ? first_len < n_seq + 1 : n_tok != n_seq))
+        return LOSSK_LENGTH_MISMATCH;
+    if ((s = ws_check(workspace, workspace_bytes, 256)) != LOSSK_OK) return s;
+    const uintptr_t es = static_cast<uintptr_t>(esize(dtype));
+    if (misaligned(workspace, 256) || misaligned(k_new, es) || misaligned(v_new, es) || misaligned(k_pages, es) ||
+        misaligned(v_pages, es) || misaligned(table, 4) || misaligned(lens, 4) || misaligned(first, 4))
+        return LOSSK_UNALIGNED;
+    const int64_t e = esize(dtype);
+    WriteArgs a{};
+    a.n_tok = n_tok;
+    a.n_seq = static_cast<int>(n_seq);
+    a.n_kv = static_cast<int>(n_kv_heads);
+    a.row_bytes = static_cast<int>(head_dim * e);
+    a.page = static_cast<int>(page_size);
+    a.n_pages = static_cast<int>(n_pages);
+    a.max_pages = static_cast<int>(max_pages);
+    a.k_new = static_cast<const char *>(k_new);
+    a.v_new = static_cast<const char *>(v_new);
+    a.k_row = a.v_row = new_stride * e;
+    a.k = static_cast<char *>(k_pages);
+    a.v = static_cast<char *>(v_pages);
+    a.k_page = a.v_page = page_stride * e;
+    a.k_tok = a.v_tok = tok_stride * e;
+    a.k_head = a.v_head = head_stride * e;
+    a.table = table;
+    a.lens = lens;
+    a.first = first;
+    a.table_stride = table_stride;
+    a.fault = fault_of(workspace);
+    const uint64_t all = reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
+                         reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages) |
+                         static_cast<uint64_t>(a.row_bytes | a.k_row | a.k_page | a.k_tok | a.k_head);
+    const int word = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Launch k(KK_CACHE_WRITE, st);
+    return status_of(launch_cache_write(a, word, st));
 }
 
 } // extern "C"

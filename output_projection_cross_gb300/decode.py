@@ -17,7 +17,8 @@ from .lossk import LosskError, _check, _dtype_code, _len, _ptr, _stream, lib
 KIND_BEAM_SELECT, KIND_CACHE, KIND_PAGED_ATTN = 0, 1, 2
 
 __all__ = ["KIND_BEAM_SELECT", "KIND_CACHE", "KIND_PAGED_ATTN", "decode_workspace", "beam_buffers",
-           "lossk_decode_workspace_bytes", "lossk_beam_select", "lossk_beam_gather"]
+           "lossk_decode_workspace_bytes", "lossk_beam_select", "lossk_beam_gather", "lossk_cache_fork",
+           "lossk_cache_reserve", "lossk_cache_free", "lossk_cache_compact", "lossk_cache_copy", "lossk_cache_write"]
 
 
 def lossk_decode_workspace_bytes(kind: int, a: int, b: int, c: int = 0, d: int = 0) -> int:
@@ -125,3 +126,155 @@ def lossk_beam_gather(src, parent, dst=None, ws=None, stream=None):
                                ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, "lossk_beam_gather")
     return dst
+
+
+# ---- the cache's pages ------------------------------------------------------------------
+
+def _ints(**named):
+    for nm, t in named.items():
+        _on_gpu(t, nm, torch.int32)
+
+
+def _table(table, name="table"):
+    """(rows, entries per row, row stride) of a table, whose rows may be strided."""
+    _on_gpu(table, name, torch.int32, contiguous=False)
+    if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"{name} must be [n_seq, max_pages] with contiguous rows")
+    n, m = table.shape
+    return n, m, table.stride(0) if n > 1 else max(m, 1)
+
+
+def _pool(pool):
+    """(address, bytes, planes, plane stride, page stride, page bytes) of a pool [planes, pages, ...]."""
+    _on_gpu(pool, "pool", contiguous=False)
+    if pool.dim() < 3 or not pool[0, 0].is_contiguous():
+        raise ValueError("pool must be [planes, pages, ...] with contiguous pages")
+    es = pool.element_size()
+    page = pool[0, 0].numel() * es
+    planes, pages = pool.shape[:2]
+    return (pool.data_ptr(), _span(pool) * es, planes, pool.stride(0) * es if planes > 1 else 0,
+            pool.stride(1) * es if pages > 1 else page, page)
+
+
+def _cache_ws(ws, n_seq, n_pages, device):
+    return ws if ws is not None else decode_workspace(KIND_CACHE, n_seq, n_pages, device=device)
+
+
+def lossk_cache_fork(parent, table, lens, ref, page_size, table_out=None, lens_out=None, ws=None, stream=None):
+    """parent int32 [groups, n_dst]; table holds groups * n_src rows.  Returns (table_out, lens_out)."""
+    _ints(parent=parent, lens=lens, ref=ref, lens_out=lens_out)
+    n, m, stride = _table(table)
+    G, n_dst = parent.shape
+    if n % G or lens.numel() != n:
+        raise ValueError(f"{n} rows and {lens.numel()} lengths in {G} groups")
+    if table_out is None:
+        table_out = torch.empty((G * n_dst, m), dtype=torch.int32, device=table.device)
+    if lens_out is None:
+        lens_out = torch.empty(G * n_dst, dtype=torch.int32, device=table.device)
+    no, mo, stride_out = _table(table_out, "table_out")
+    if no != G * n_dst or mo != m:
+        raise ValueError("table_out must be [groups * n_dst, max_pages]")
+    ws = _cache_ws(ws, max(n, no), ref.numel(), table.device)
+    st = lib.lossk_cache_fork(G, n // G, n_dst, m, page_size, ref.numel(), parent.data_ptr(), parent.numel(),
+                              table.data_ptr(), _span(table), stride, lens.data_ptr(), n, ref.data_ptr(), ref.numel(),
+                              table_out.data_ptr(), _span(table_out), stride_out, lens_out.data_ptr(),
+                              lens_out.numel(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "lossk_cache_fork")
+    return table_out, lens_out
+
+
+def lossk_cache_reserve(table, lens, ref, pool, page_size, n_new=1, ws=None, stream=None) -> None:
+    """n_new: tokens to come for every sequence, or an int32 tensor with one count each."""
+    _ints(lens=lens, ref=ref)
+    n, m, stride = _table(table)
+    each = n_new if isinstance(n_new, torch.Tensor) else None
+    _ints(n_new=each)
+    P = _pool(pool)
+    if pool.shape[1] != ref.numel():
+        raise ValueError(f"a pool of {pool.shape[1]} pages with {ref.numel()} counts")
+    ws = _cache_ws(ws, n, ref.numel(), table.device)
+    st = lib.lossk_cache_reserve(n, m, page_size, ref.numel(), 0 if each is not None else n_new, _ptr(each),
+                                 _len(each), table.data_ptr(), _span(table), stride, lens.data_ptr(), lens.numel(),
+                                 ref.data_ptr(), ref.numel(), *P, ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "lossk_cache_reserve")
+
+
+def lossk_cache_free(table, lens, ref, page_size, drop=None, ws=None, stream=None) -> None:
+    """drop: uint8 [n_seq], nonzero where the sequence goes (None: all)."""
+    _ints(lens=lens, ref=ref)
+    _on_gpu(drop, "drop", torch.uint8)
+    n, m, stride = _table(table)
+    ws = _cache_ws(ws, n, ref.numel(), table.device)
+    st = lib.lossk_cache_free(n, m, page_size, ref.numel(), _ptr(drop), _len(drop), table.data_ptr(), _span(table),
+                              stride, lens.data_ptr(), lens.numel(), ref.data_ptr(), ref.numel(), ws.data_ptr(),
+                              ws.numel(), _stream(stream))
+    _check(st, "lossk_cache_free")
+
+
+def lossk_cache_compact(table, lens, ref, pool, page_size, table_out=None, ref_out=None, n_live_out=None, ws=None,
+                        stream=None):
+    """Returns (table_out, ref_out, n_live_out); the pool's live pages are in front then."""
+    _ints(lens=lens, ref=ref, ref_out=ref_out, n_live_out=n_live_out)
+    n, m, stride = _table(table)
+    P = _pool(pool)
+    if pool.shape[1] != ref.numel():
+        raise ValueError(f"a pool of {pool.shape[1]} pages with {ref.numel()} counts")
+    dev = table.device
+    table_out = table_out if table_out is not None else torch.empty((n, m), dtype=torch.int32, device=dev)
+    ref_out = ref_out if ref_out is not None else torch.empty_like(ref)
+    n_live_out = n_live_out if n_live_out is not None else torch.empty(1, dtype=torch.int32, device=dev)
+    no, mo, stride_out = _table(table_out, "table_out")
+    if (no, mo) != (n, m) or n_live_out.numel() < 1:
+        raise ValueError("table_out must be shaped like table, n_live_out hold one value")
+    ws = _cache_ws(ws, n, ref.numel(), dev)
+    st = lib.lossk_cache_compact(n, m, page_size, ref.numel(), table.data_ptr(), _span(table), stride,
+                                 lens.data_ptr(), lens.numel(), ref.data_ptr(), ref.numel(), table_out.data_ptr(),
+                                 _span(table_out), stride_out, ref_out.data_ptr(), ref_out.numel(),
+                                 n_live_out.data_ptr(), *P, ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "lossk_cache_compact")
+    return table_out, ref_out, n_live_out
+
+
+def lossk_cache_copy(src, dst, pool, ws=None, stream=None) -> None:
+    """Page src[i] of the pool to page dst[i], in every plane."""
+    _ints(src=src, dst=dst)
+    P = _pool(pool)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must list as many pages")
+    ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=pool.device)
+    st = lib.lossk_cache_copy(src.numel(), pool.shape[1], src.data_ptr(), src.numel(), dst.data_ptr(), dst.numel(),
+                              *P, ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "lossk_cache_copy")
+
+
+def _pages(k, v):
+    """(pages, page size, heads, head dim, strides) of one layer's key and value pages
+    [pages, page, heads, head_dim], whose elements of a head are contiguous."""
+    _on_gpu(k, "k_pages", contiguous=False)
+    _on_gpu(v, "v_pages", k.dtype, contiguous=False)
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or (k.shape[3] > 1 and k.stride(3) != 1):
+        raise ValueError("k_pages and v_pages must be [pages, page, heads, head_dim], laid out alike, heads contiguous")
+    return k.shape, k.stride()
+
+
+def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, ws=None, stream=None) -> None:
+    """k_new, v_new [n_tok, heads, head_dim] (tokens may be strided) into one layer's pages
+    [pages, page, heads, head_dim] (any strides).  first: int32 [n_seq + 1], where each sequence's
+    rows begin (None: one row per sequence)."""
+    (n_pages, page, kv, hd), (sp, stok, sh, _) = _pages(k_pages, v_pages)
+    _ints(lens=lens, first=first)
+    n, m, stride = _table(table)
+    for t, nm in ((k_new, "k_new"), (v_new, "v_new")):
+        _on_gpu(t, nm, k_pages.dtype, contiguous=False)
+        if t.dim() != 3 or t.shape[1:] != (kv, hd) or (t.shape[0] and not t[0].is_contiguous()):
+            raise ValueError(f"{nm} must be [n_tok, heads, head_dim] with contiguous tokens")
+    if k_new.shape != v_new.shape or k_new.stride() != v_new.stride():
+        raise ValueError("k_new and v_new must be laid out alike")
+    n_tok = k_new.shape[0]
+    ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=table.device)
+    st = lib.lossk_cache_write(n_tok, n, kv, hd, m, page, n_pages, _dtype_code(k_pages), k_new.data_ptr(),
+                               v_new.data_ptr(), _span(k_new), k_new.stride(0) if n_tok > 1 else kv * hd,
+                               k_pages.data_ptr(), v_pages.data_ptr(), _span(k_pages), sp, stok, sh,
+                               table.data_ptr(), _span(table), stride, lens.data_ptr(), lens.numel(), _ptr(first),
+                               _len(first), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "lossk_cache_write")

@@ -48,3 +48,77 @@ def beam_select(logits, scores, n_out, temperature=1.0, allow=None, finished=Non
             out["parent"][b, j], out["token"][b, j], out["score"][b, j] = c[1], c[2], c[3]
             out["finished"][b, j], out["length"][b, j] = c[4], c[5]
     return out
+
+
+class Cache:
+    """A paged cache kept by hand: tables as lists of pages, the pool as an array [planes][pages][page][row]."""
+
+    def __init__(self, pool, page, rows):
+        self.pool, self.page = pool.copy(), page
+        self.rows, self.lens = [list(r) for r in rows], [0] * len(rows)
+
+    def ref(self):
+        n = np.zeros(self.pool.shape[1], np.int64)
+        for r in self.rows:
+            for p in r:
+                n[p] += 1
+        return n
+
+    def table(self, max_pages):
+        t = np.full((len(self.rows), max_pages), -1, np.int32)
+        for i, r in enumerate(self.rows):
+            t[i, :len(r)] = r
+        return t
+
+    def used(self, i):
+        return -(-self.lens[i] // self.page)
+
+    def fork(self, parent, n_src):
+        take = [None if p < 0 else g * n_src + p for g, ps in enumerate(parent) for p in ps]
+        self.rows = [[] if s is None else list(self.rows[s][:self.used(s)]) for s in take]
+        self.lens = [0 if s is None else self.lens[s] for s in take]
+
+    def reserve(self, n_new):
+        """False, with nothing changed, where there are too few free pages."""
+        ref = self.ref()
+        free = [p for p in range(len(ref)) if ref[p] == 0]
+        copies = []
+        for i, r in enumerate(self.rows):
+            if n_new[i] and self.lens[i] % self.page:
+                p = r[self.lens[i] // self.page]
+                who = [j for j, q in enumerate(self.rows) if n_new[j] and self.lens[j] % self.page
+                       and q[self.lens[j] // self.page] == p]
+                if not (ref[p] == len(who) and i == who[-1]):
+                    copies.append(i)
+        add = [-(-(self.lens[i] + n_new[i]) // self.page) - self.used(i) for i in range(len(self.rows))]
+        if len(copies) + sum(add) > len(free):
+            return False
+        for i, r in enumerate(self.rows):
+            if i in copies:
+                c = self.lens[i] // self.page
+                self.pool[:, free[0]] = self.pool[:, r[c]]
+                r[c] = free.pop(0)
+            for _ in range(add[i]):
+                r.append(free.pop(0))
+        return True
+
+    def write(self, k_new, v_new, first):
+        for i, r in enumerate(self.rows):
+            for j in range(first[i], first[i + 1]):
+                pos = self.lens[i] + j - first[i]
+                self.pool[0, r[pos // self.page], pos % self.page] = k_new[j]
+                self.pool[1, r[pos // self.page], pos % self.page] = v_new[j]
+
+    def free(self, drop):
+        for i, d in enumerate(drop):
+            if d:
+                self.rows[i], self.lens[i] = [], 0
+
+    def compact(self):
+        ref = self.ref()
+        n = int((ref > 0).sum())
+        to = dict(zip([p for p in range(n, len(ref)) if ref[p]], [p for p in range(n) if not ref[p]]))
+        for a, b in to.items():
+            self.pool[:, b] = self.pool[:, a]
+        self.rows = [[to.get(p, p) for p in r] for r in self.rows]
+        return n

@@ -102,3 +102,120 @@ def test_reference_orders_candidates():
     assert r["parent"].tolist() == [[0, 1, 0, 0]] and r["token"].tolist() == [[0, 2, 1, 2]]
     np.testing.assert_allclose(np.exp(r["score"]), [[0.5, 0.5, 0.25, 0.25]], rtol=1e-12)
     np.testing.assert_allclose(r["lse"], 0.0, atol=1e-12)
+
+
+# ---- the cache's pages ---------------------------------------------------------------
+
+def call(fn, a, over):
+    assert not set(over) - set(a), set(over) - set(a)
+    a.update(over)
+    return fn(*a.values())
+
+
+def fork_call(L, **over):
+    return call(L.lib.lossk_cache_fork, dict(
+        n_group=2, n_src=3, n_dst=4, max_pages=5, page=16, n_pages=40, parent=P, parent_len=8, table=P, table_len=30,
+        table_stride=5, lens=P, lens_len=6, ref=P, ref_len=40, table_out=2 * P, out_len=40, out_stride=5,
+        lens_out=2 * P, lens_out_len=8, ws=P, ws_bytes=256, stream=None), over)
+
+
+def reserve_call(L, **over):
+    return call(L.lib.lossk_cache_reserve, dict(
+        n_seq=6, max_pages=5, page=16, n_pages=40, n_new_all=1, n_new=None, n_new_len=0, table=P, table_len=30,
+        table_stride=5, lens=P, lens_len=6, ref=P, ref_len=40, pool=P, pool_bytes=2 * 40 * 512, n_planes=2,
+        plane_stride=40 * 512, page_stride=512, page_bytes=512, ws=P, ws_bytes=1 << 20, stream=None), over)
+
+
+def free_call(L, **over):
+    return call(L.lib.lossk_cache_free, dict(
+        n_seq=6, max_pages=5, page=16, n_pages=40, drop=P, drop_len=6, table=P, table_len=30, table_stride=5, lens=P,
+        lens_len=6, ref=P, ref_len=40, ws=P, ws_bytes=256, stream=None), over)
+
+
+def compact_call(L, **over):
+    return call(L.lib.lossk_cache_compact, dict(
+        n_seq=6, max_pages=5, page=16, n_pages=40, table=P, table_len=30, table_stride=5, lens=P, lens_len=6, ref=P,
+        ref_len=40, table_out=2 * P, out_len=30, out_stride=5, ref_out=2 * P, ref_out_len=40, n_live=P, pool=P,
+        pool_bytes=2 * 40 * 512, n_planes=2, plane_stride=40 * 512, page_stride=512, page_bytes=512, ws=P,
+        ws_bytes=1 << 20, stream=None), over)
+
+
+def copy_call(L, **over):
+    return call(L.lib.lossk_cache_copy, dict(
+        n_copy=3, n_pages=40, src=P, src_len=3, dst=P, dst_len=3, pool=P, pool_bytes=2 * 40 * 512, n_planes=2,
+        plane_stride=40 * 512, page_stride=512, page_bytes=512, ws=P, ws_bytes=256, stream=None), over)
+
+
+def write_call(L, **over):
+    return call(L.lib.lossk_cache_write, dict(
+        n_tok=6, n_seq=6, n_kv=2, hd=8, max_pages=5, page=16, n_pages=40, dtype=1, k_new=P, v_new=P, new_len=96,
+        new_stride=16, k=P, v=P, pages_len=40 * 256, page_stride=256, tok_stride=16, head_stride=8, table=P,
+        table_len=30, table_stride=5, lens=P, lens_len=6, first=None, first_len=0, ws=P, ws_bytes=256, stream=None),
+        over)
+
+
+@pytest.mark.parametrize("fn,sizes", [
+    (fork_call, ("n_group", "n_src", "n_dst", "max_pages", "page", "n_pages")),
+    (reserve_call, ("n_seq", "max_pages", "page", "n_pages", "n_planes", "page_bytes")),
+    (free_call, ("n_seq", "max_pages", "page", "n_pages")),
+    (compact_call, ("n_seq", "max_pages", "page", "n_pages", "n_planes", "page_bytes")),
+    (copy_call, ("n_copy", "n_pages", "n_planes", "page_bytes")),
+    (write_call, ("n_tok", "n_seq", "n_kv", "hd", "max_pages", "page", "n_pages"))])
+def test_cache_sizes_refused(L, fn, sizes):
+    for s in sizes:
+        assert fn(L, **{s: 0}) == 581, s
+        if s != "page_bytes":
+            assert fn(L, **{s: (1 << 24) + 1}) == 583, s
+
+
+@pytest.mark.parametrize("fn,pointers,shorts", [
+    (fork_call, ("parent", "table", "lens", "ref", "table_out", "lens_out", "ws"),
+     dict(parent_len=7, table_len=29, table_stride=4, lens_len=5, ref_len=39, out_len=39, out_stride=4,
+          lens_out_len=7, ws_bytes=255, table_out=P, lens_out=P)),
+    (reserve_call, ("table", "lens", "ref", "pool", "ws"),
+     dict(table_len=29, table_stride=4, lens_len=5, ref_len=39, pool_bytes=2 * 40 * 512 - 1, page_stride=496,
+          plane_stride=-16, n_new_all=-1, ws_bytes=512)),
+    (free_call, ("table", "lens", "ref", "ws"),
+     dict(drop_len=5, table_len=29, table_stride=4, lens_len=5, ref_len=39, ws_bytes=255)),
+    (compact_call, ("table", "lens", "ref", "table_out", "ref_out", "n_live", "pool", "ws"),
+     dict(table_len=29, lens_len=5, ref_len=39, out_len=29, out_stride=4, ref_out_len=39, ref_out=P,
+          pool_bytes=2 * 40 * 512 - 1, page_stride=496, ws_bytes=512)),
+    (copy_call, ("src", "dst", "pool", "ws"),
+     dict(src_len=2, dst_len=2, pool_bytes=2 * 40 * 512 - 1, page_stride=496, ws_bytes=255)),
+    (write_call, ("k_new", "v_new", "k", "v", "table", "lens", "ws"),
+     dict(dtype=9, new_len=95, new_stride=15, pages_len=40 * 256 - 1, page_stride=-1, tok_stride=17, head_stride=9,
+          table_len=29, lens_len=5, n_tok=5, ws_bytes=255))])
+def test_cache_arguments_refused(L, fn, pointers, shorts):
+    for p in pointers:
+        assert fn(L, **{p: None}) == 582, p
+    for k, v in shorts.items():
+        assert fn(L, **{k: v}) == 582, k
+    assert fn(L, ws=P + 128) == 591
+
+
+def test_cache_alignment_refused(L):
+    for fn in (reserve_call, compact_call, copy_call):
+        assert fn(L, pool=P + 8, pool_bytes=1 << 20) == 591
+        assert fn(L, page_bytes=504) == 591
+        assert fn(L, page_stride=520, pool_bytes=1 << 20) == 591
+    assert write_call(L, k=P + 1) == 591
+    assert write_call(L, dtype=0, k_new=P + 2) == 591
+    assert write_call(L, first=P, first_len=6) == 582
+    assert fork_call(L, ref=P + 2) == 591
+
+
+def test_reference_cache_by_hand():
+    """Two beams fork from one sequence of three tokens in pages of two: the shared half-full page is
+    copied for the first and kept by the second."""
+    import decode_ref as ref
+    c = ref.Cache(np.arange(12.0).reshape(2, 6, 1, 1).repeat(2, 2), 2, [[4, 1]])
+    c.lens = [3]
+    c.fork([[0, 0]], 1)
+    assert c.ref().tolist() == [0, 2, 0, 0, 2, 0]
+    assert c.reserve([1, 1])
+    assert c.rows == [[4, 0], [4, 1]] and c.ref().tolist() == [1, 1, 0, 0, 2, 0]
+    assert (c.pool[:, 0] == c.pool[:, 1]).all()
+    c.lens = [4, 4]
+    assert not c.reserve([1, 5]) and c.reserve([1, 0]) and c.rows[0] == [4, 0, 2]
+    c.free([1, 0])
+    assert c.compact() == 2 and c.rows == [[], [0, 1]]
