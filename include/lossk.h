@@ -488,7 +488,7 @@ int32_t lossk_ce_from_logits_static(int64_t n_tok, int64_t vocab, int32_t dtype,
  *    hold that header).  lossk_decode_workspace_bytes gives its size.
  *  - Results do not depend on how the work is split over the GPU, except for
  *    the rounding of lossk_paged_attn, whose order of sums is a function of
- *    the shape, the lengths and the device alone. */
+ *    the sizes, the lengths and what is shared alone: every call's bits repeat. */
 
 /* Workspace kinds of the decoding calls, with the sizes a..d that
  * lossk_decode_workspace_bytes takes:
@@ -636,6 +636,39 @@ int32_t lossk_cache_write(int64_t n_tok, int64_t n_seq, int64_t n_kv_heads, int6
                           int64_t table_len, int64_t table_stride, const int32_t *lens, int64_t lens_len,
                           const int32_t *first, int64_t first_len, void *workspace, int64_t workspace_bytes,
                           lossk_stream_t stream);
+
+/* ---- attention of one new token ----------------------------------------------------
+ * For each sequence s and query head h, with KV head h / (n_q_heads /
+ * n_kv_heads) and tokens j in [max(0, lens[s] - window), lens[s]) (window 0:
+ * all of them):
+ *   x_j = scale q.k_j,  out = sum_j softmax(x)_j v_j,  lse = log sum_j exp x_j
+ * The new token's own key and value are among the cache's (written before,
+ * and counted in lens).  A sequence of length 0 gives zeros and lse -infinity.
+ *   q        [n_seq][n_q_heads][head_dim] (dtype; sequences q_stride elements apart)
+ *   k_pages, v_pages  one layer's pages, as in lossk_cache_write
+ *   share    sequences [g share, (g + 1) share) form group g: the beams of one
+ *            prompt.  Leading full pages that all of a group's rows hold in common
+ *            (the same ids) are read once for the whole group.  1: no groups.  The
+ *            result is the same but for rounding.  n_seq a multiple of share (582)
+ *   max_len  an upper bound of lens that the caller knows, or 0: spares idle
+ *            warps; longer sequences are right as well
+ *   out      [n_seq][n_q_heads][head_dim] (dtype, contiguous)
+ *   lse_out  float[n_seq][n_q_heads] or NULL
+ * What lies in the pages past a sequence's end does not matter.  Sums, the
+ * softmax's maximum and weights are fp32; the tensor cores take each weight as
+ * the sum of two 16-bit values, so that only the output is rounded.
+ * head_dim <= 256, max_pages * page_size <= 2^30 (583); q, pages, out and every
+ * stride multiples of 16 bytes (591), so head_dim % 8 == 0 (16-bit types) or
+ * % 4 (fp32).  n_q_heads a multiple of n_kv_heads (582).  A length out of range
+ * counts as 0, a token of a page out of range is left out of the softmax: 586
+ * in the header. */
+int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim, int64_t max_pages,
+                         int64_t page_size, int64_t n_pages, int64_t share, int32_t dtype, const void *q,
+                         int64_t q_len, int64_t q_stride, const void *k_pages, const void *v_pages,
+                         int64_t pages_len, int64_t page_stride, int64_t tok_stride, int64_t head_stride,
+                         const int32_t *table, int64_t table_len, int64_t table_stride, const int32_t *lens,
+                         int64_t lens_len, int64_t max_len, int64_t window, double scale, void *out, int64_t out_len,
+                         float *lse_out, void *workspace, int64_t workspace_bytes, lossk_stream_t stream);
 
 /* ---- tracing ----------------------------------------------------------------
  * Every kernel the library launches belongs to one of LOSSK_N_KERNELS kinds

@@ -134,4 +134,38 @@ cudaError_t launch_cache_move(const CompactArgs &a, const CopyArgs &c, cudaStrea
 // word: bytes of the widest access every row allows (16, 4 or 2)
 cudaError_t launch_cache_write(const WriteArgs &a, int word, cudaStream_t st);
 
+// ---- paged attention ---------------------------------------------------------------
+struct AttnArgs {
+    int n_group, share, n_q, n_kv, group, hd;      // group: query heads per KV head
+    int max_pages, page, n_pages;
+    int window;                                    // 0: none
+    float scale_log2;                              // scale * log2(e)
+    const void *q, *k, *v;
+    int64_t q_stride;                              // elements between sequences
+    int64_t page_stride, tok_stride, head_stride;  // elements
+    const int32_t *table, *lens;
+    int64_t table_stride;
+    void *out;
+    float *lse;
+    int kt, mr;                                    // tokens per unit, query rows per item
+    int cs, cp;                                    // items per KV head: of a group's shared part, of a sequence
+    int ra, rb;                                    // rows a partial result holds, shared and private
+    int nw;                                        // warps at most
+    int32_t *shared;                               // [n_group] shared tokens
+    long long *base;                               // [n_group + 1] units before each group
+    float *part_a, *part_b;                        // partial results: o[hd], m (log2 units), l per row
+    int *fault;
+};
+
+// Query rows per item and tokens per unit of the kernel that takes this type and head size.
+struct AttnShape {
+    int mr, kt;
+};
+constexpr int ATTN_MAX_MR = 32;
+constexpr int ATTN_MAX_WARPS = 152 * 8;
+AttnShape attn_shape(int dtype, int hd);
+cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st);
+cudaError_t launch_attn_join(int dtype, const AttnArgs &a, cudaStream_t st);
+
 } // namespace lossk

@@ -1,0 +1,439 @@
+// k_attn.cu -- attention of one new token per sequence over a paged key-value
+// cache, split over the cache's length and joined.
+//
+//   attn_plan   per group of sequences: how many leading pages they share, and
+//               the work in units
+//   attn        the split pass
+//   attn_join   the partial results of each output row joined
+//
+// For query row q of a sequence with tokens j in [lo, len):
+//   x_j = scale q.k_j,   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m)
+// computed online: a running maximum m, the sum l and the unnormalised output
+// o are rescaled when m rises, so one pass over the keys and values is enough
+// and any cut of the tokens into pieces (m, l, o) can be joined afterwards.
+//
+// The split.  A unit is a tile of KT tokens of one item; an item is a KV head
+// of a sequence with up to MR of the query rows that read it, or, where the
+// sequences of a group share their leading pages, of the group's shared tokens
+// with the rows of all its sequences (read once for all of them).  The units
+// are numbered in a row and every warp takes an equal run of them, whatever the
+// lengths: a long sequence is cut over many warps, short ones share a warp.
+#include "../../include/lossk.h"
+#include "decode_internal.h"
+#include "ptx.cuh"
+
+namespace lossk {
+
+namespace {
+
+constexpr int PLAN_T = 256;
+constexpr int ATTN_WARPS = 4;
+constexpr int JOIN_THREADS = 128;
+
+__device__ __forceinline__ float attn_f(float x) { return x; }
+__device__ __forceinline__ float attn_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__device__ __forceinline__ float attn_f(h16_t x) { return f16_to_f(x.bits); }
+__device__ __forceinline__ void attn_put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void attn_put(uint16_t *p, float v)
+{
+    *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+}
+__device__ __forceinline__ void attn_put(h16_t *p, float v)
+{
+    p->bits = static_cast<uint16_t>(pack_f16x2(v, 0.f) & 0xFFFFu);
+}
+
+// A sequence's length as the kernels use it: 0 where it is out of range.
+__device__ __forceinline__ int attn_len(const AttnArgs &a, int s)
+{
+    const int n = a.lens[s];
+    return n >= 0 && n <= static_cast<int64_t>(a.max_pages) * a.page ? n : 0;
+}
+
+// What of a sequence is read: tokens [lo, hi) with its group (the leading
+// `shared` tokens, lo on), then [mid, hi) by itself.
+struct Span {
+    int lo, mid, hi;
+};
+__device__ __forceinline__ Span attn_span(const AttnArgs &a, int s, int g)
+{
+    Span r;
+    r.hi = attn_len(a, s);
+    r.lo = a.window > 0 && r.hi > a.window ? r.hi - a.window : 0;
+    const int shared = a.share > 1 ? a.shared[g] : 0;
+    r.mid = shared > r.lo ? shared : r.lo;
+    return r;
+}
+__device__ __forceinline__ int tiles_of(int n, int kt) { return (n + kt - 1) / kt; }
+
+// Units of a group's shared part, per item.
+__device__ __forceinline__ int shared_tiles(const AttnArgs &a, int g)
+{
+    if (a.share <= 1) return 0;
+    const Span r = attn_span(a, g * a.share, g);
+    return tiles_of(r.mid - r.lo, a.kt);
+}
+__device__ __forceinline__ long long group_units(const AttnArgs &a, int g)
+{
+    long long u = static_cast<long long>(shared_tiles(a, g)) * a.n_kv * a.cs;
+    for (int i = 0; i < a.share; ++i) {
+        const Span r = attn_span(a, g * a.share + i, g);
+        u += static_cast<long long>(tiles_of(r.hi - r.mid, a.kt)) * a.n_kv * a.cp;
+    }
+    return u;
+}
+
+// Shared tokens of each group: the leading pages whose ids agree in all its
+// rows, full in all of them.  With a window the rows have to be equally long,
+// for the first token read depends on the length.
+__global__ void __launch_bounds__(PLAN_T) attn_share_kernel(AttnArgs a)
+{
+    __shared__ int s_first, s_min, s_max;
+    const int g = blockIdx.x, t = threadIdx.x;
+    if (t == 0) {
+        int mn = 1 << 30, mx = 0;
+        for (int i = 0; i < a.share; ++i) {
+            const int n = attn_len(a, g * a.share + i);
+            mn = n < mn ? n : mn;
+            mx = n > mx ? n : mx;
+        }
+        s_min = mn;
+        s_max = mx;
+        s_first = mn / a.page;
+    }
+    __syncthreads();
+    const int full = s_min / a.page;
+    if (a.window > 0 && s_min != s_max) {
+        if (t == 0) a.shared[g] = 0;
+        return;
+    }
+    const int32_t *row0 = a.table + static_cast<int64_t>(g) * a.share * a.table_stride;
+    for (int base = 0; base < full; base += PLAN_T) {
+        const int c = base + t;
+        bool differ = false;
+        if (c < full)
+            for (int i = 1; i < a.share; ++i) differ |= row0[i * a.table_stride + c] != row0[c];
+        if (differ) atomicMin(&s_first, c);
+        __syncthreads();
+        if (s_first < base + PLAN_T) break;
+        __syncthreads();
+    }
+    __syncthreads();
+    if (t == 0) a.shared[g] = (s_first < full ? s_first : full) * a.page;
+}
+
+// One block: the units before each group (a prefix sum), base[n_group] their number.
+__global__ void __launch_bounds__(PLAN_T) attn_plan_kernel(AttnArgs a)
+{
+    __shared__ long long s_warp[PLAN_T / 32];
+    const int t = threadIdx.x, lane = t & 31;
+    long long done = 0;
+    for (int base = 0; base < a.n_group; base += PLAN_T) {
+        const int g = base + t;
+        const long long x = g < a.n_group ? group_units(a, g) : 0;
+        if (g < a.n_group)
+            for (int i = 0; i < a.share; ++i) {
+                const int n = a.lens[g * a.share + i];
+                if (n < 0 || n > static_cast<int64_t>(a.max_pages) * a.page)
+                    raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
+            }
+        long long inc = x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[t >> 5] = inc;
+        __syncthreads();
+        long long before = 0, all = 0;
+        for (int w = 0; w < PLAN_T / 32; ++w) {
+            if (w < (t >> 5)) before += s_warp[w];
+            all += s_warp[w];
+        }
+        if (g < a.n_group) a.base[g] = done + before + inc - x;
+        done += all;
+    }
+    if (t == 0) a.base[a.n_group] = done;
+}
+
+// The run of units of warp w of nw, and the warp that has unit u.
+__device__ __forceinline__ long long run_start(long long units, int nw, int w) { return units * w / nw; }
+__device__ __forceinline__ int warp_of(long long units, int nw, long long u)
+{
+    return static_cast<int>(((u + 1) * nw - 1) / units);
+}
+__device__ __forceinline__ int warps_used(long long units, int nw) { return units < nw ? static_cast<int>(units) : nw; }
+
+// One item's piece as a warp computes it.
+struct Piece {
+    int first_row;      // its rows are rows first_row.. of sequences from seq on, counted group rows of heads
+    int rows;
+    int seq;            // the sequence (private) or the group's first one (shared)
+    int head;           // KV head
+    int t0, t1;         // tokens [t0, t1)
+    int64_t slot;       // where a partial result goes; -1: the whole row is here
+    float *part;
+};
+
+// Query row i of a piece: sequence and query head.
+__device__ __forceinline__ int row_seq(const AttnArgs &a, const Piece &p, int i)
+{
+    return p.seq + (p.first_row + i) / a.group;
+}
+__device__ __forceinline__ int row_head(const AttnArgs &a, const Piece &p, int i)
+{
+    return p.head * a.group + (p.first_row + i) % a.group;
+}
+
+// Walks warp w's run; body(piece) computes each piece.
+template <typename F> __device__ __forceinline__ void walk_run(const AttnArgs &a, int w, F &&body)
+{
+    const long long units = a.base[a.n_group];
+    const int nw = warps_used(units, a.nw);
+    if (w >= nw) return;
+    long long u = run_start(units, nw, w);
+    const long long u1 = run_start(units, nw, w + 1);
+    int g = 0;
+    for (int lo = 0, hi = a.n_group; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (a.base[mid] <= u) lo = mid;
+        else hi = mid;
+        g = lo;
+    }
+    while (u < u1) {
+        while (a.base[g + 1] <= u) ++g;
+        long long in = u - a.base[g];
+        const int ts = shared_tiles(a, g);
+        const long long su = static_cast<long long>(ts) * a.n_kv * a.cs;
+        Piece p;
+        int tile, tiles, lo, hi;
+        if (in < su) {
+            const int item = static_cast<int>(in / ts), c = item % a.cs;
+            tile = static_cast<int>(in % ts);
+            tiles = ts;
+            p.head = item / a.cs;
+            p.seq = g * a.share;
+            p.first_row = c * a.mr;
+            p.rows = min(a.mr, a.share * a.group - p.first_row);
+            const Span r = attn_span(a, p.seq, g);
+            lo = r.lo;
+            hi = r.mid;
+            p.slot = (static_cast<int64_t>(g) * a.n_kv + p.head) * a.cs + c + w;
+            p.part = a.part_a + p.slot * a.ra * (a.hd + 2);
+        } else {
+            in -= su;
+            int s = g * a.share;
+            Span r = attn_span(a, s, g);
+            tiles = tiles_of(r.hi - r.mid, a.kt);
+            while (in >= static_cast<long long>(tiles) * a.n_kv * a.cp) {
+                in -= static_cast<long long>(tiles) * a.n_kv * a.cp;
+                r = attn_span(a, ++s, g);
+                tiles = tiles_of(r.hi - r.mid, a.kt);
+            }
+            const int item = static_cast<int>(in / tiles), c = item % a.cp;
+            tile = static_cast<int>(in % tiles);
+            p.head = item / a.cp;
+            p.seq = s;
+            p.first_row = c * a.mr;
+            p.rows = min(a.mr, a.group - p.first_row);
+            lo = r.mid;
+            hi = r.hi;
+            p.slot = (static_cast<int64_t>(s) * a.n_kv + p.head) * a.cp + c + w;
+            p.part = a.part_b + p.slot * a.rb * (a.hd + 2);
+            if (ts == 0 && tile == 0 && u + tiles <= u1) p.slot = -1;
+        }
+        const int n = static_cast<int>(min(static_cast<long long>(tiles - tile), u1 - u));
+        p.t0 = lo + tile * a.kt;
+        p.t1 = min(hi, p.t0 + n * a.kt);
+        body(p);
+        u += n;
+    }
+}
+
+// Where token j of a sequence lies, in elements from the pages' start; -1 for
+// an entry out of range.
+__device__ __forceinline__ int64_t token_at(const AttnArgs &a, int seq, int j)
+{
+    const int p = a.table[seq * a.table_stride + j / a.page];
+    if (p < 0 || p >= a.n_pages) {
+        raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
+        return -1;
+    }
+    return p * a.page_stride + (j % a.page) * a.tok_stride;
+}
+
+// ---- CUDA cores ---------------------------------------------------------------------
+// One key at a time per warp, a lane holding elements lane, lane + 32, ... of
+// the head.
+constexpr int SIMT_MR = 4;
+
+template <typename T> __global__ void __launch_bounds__(ATTN_WARPS * 32) attn_simt_kernel(AttnArgs a)
+{
+    const int lane = threadIdx.x & 31, w = blockIdx.x * ATTN_WARPS + (threadIdx.x >> 5);
+    walk_run(a, w, [&](const Piece &p) {
+        float q[SIMT_MR][8], o[SIMT_MR][8], m[SIMT_MR], l[SIMT_MR];
+        for (int i = 0; i < SIMT_MR; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            const T *row = static_cast<const T *>(a.q) +
+                           (i < p.rows ? row_seq(a, p, i) * a.q_stride + static_cast<int64_t>(row_head(a, p, i)) * a.hd : 0);
+            for (int e = 0; e < 8; ++e) {
+                q[i][e] = i < p.rows && lane + 32 * e < a.hd ? attn_f(row[lane + 32 * e]) : 0.f;
+                o[i][e] = 0.f;
+            }
+        }
+        for (int j = p.t0; j < p.t1; ++j) {
+            const int64_t at = token_at(a, p.seq, j);
+            if (at < 0) continue;
+            const T *k = static_cast<const T *>(a.k) + at + p.head * a.head_stride;
+            const T *v = static_cast<const T *>(a.v) + at + p.head * a.head_stride;
+            float kv[8], vv[8];
+            for (int e = 0; e < 8; ++e) {
+                kv[e] = lane + 32 * e < a.hd ? attn_f(k[lane + 32 * e]) : 0.f;
+                vv[e] = lane + 32 * e < a.hd ? attn_f(v[lane + 32 * e]) : 0.f;
+            }
+            for (int i = 0; i < SIMT_MR; ++i) {
+                float x = 0.f;
+                for (int e = 0; e < 8; ++e) x = fmaf(q[i][e], kv[e], x);
+                for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
+                x *= a.scale_log2;
+                const float mn = fmaxf(m[i], x), mz = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[i] - mz), pr = exp2f(x - mz);
+                l[i] = l[i] * f + pr;
+                for (int e = 0; e < 8; ++e) o[i][e] = o[i][e] * f + pr * vv[e];
+                m[i] = mn;
+            }
+        }
+        for (int i = 0; i < p.rows; ++i) {
+            if (p.slot < 0) {
+                const float inv = l[i] > 0.f ? 1.f / l[i] : 1.f;
+                const int64_t row = static_cast<int64_t>(row_seq(a, p, i)) * a.n_q + row_head(a, p, i);
+                T *out = static_cast<T *>(a.out) + row * a.hd;
+                for (int e = 0; e < 8; ++e)
+                    if (lane + 32 * e < a.hd) attn_put(out + lane + 32 * e, o[i][e] * inv);
+                if (a.lse && lane == 0) a.lse[row] = (m[i] == -INFINITY ? 0.f : m[i]) * float(LN2) + logf(l[i]);
+            } else {
+                float *d = p.part + static_cast<int64_t>(i) * (a.hd + 2);
+                for (int e = 0; e < 8; ++e)
+                    if (lane + 32 * e < a.hd) d[lane + 32 * e] = o[i][e];
+                if (lane == 0) {
+                    d[a.hd] = m[i];
+                    d[a.hd + 1] = l[i];
+                }
+            }
+        }
+    });
+}
+
+// ---- joining -----------------------------------------------------------------------
+// One block per output row: the row's pieces, from the group's shared tokens
+// and from its own, weighted by e^(m - M).  A row that one piece covers was
+// written by it.
+template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(AttnArgs a)
+{
+    __shared__ float s_o[JOIN_THREADS / 32][256];
+    __shared__ float s_m[JOIN_THREADS / 32], s_l[JOIN_THREADS / 32];
+    const int s = blockIdx.x / a.n_q, hq = blockIdx.x % a.n_q, g = s / a.share;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int head = hq / a.group, r = hq % a.group;
+    const long long units = a.base[a.n_group];
+    const int nw = warps_used(units, a.nw);
+    const int ts = shared_tiles(a, g);
+    const Span own = attn_span(a, s, g);
+    const int tp = tiles_of(own.hi - own.mid, a.kt);
+    // the pieces: n_a of the shared item (from slot a0 on), then n_b of its own
+    const int ri = (s % a.share) * a.group + r, ca = ri / a.mr, cb = r / a.mr;
+    int n_a = 0, n_b = 0;
+    int64_t a0 = 0, b0 = 0;
+    if (ts > 0) {
+        const long long u = a.base[g] + (static_cast<long long>(head) * a.cs + ca) * ts;
+        const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + ts - 1);
+        n_a = w1 - w0 + 1;
+        a0 = (static_cast<int64_t>(g) * a.n_kv + head) * a.cs + ca + w0;
+    }
+    if (tp > 0) {
+        long long u = a.base[g] + static_cast<long long>(ts) * a.n_kv * a.cs;
+        for (int i = g * a.share; i < s; ++i) {
+            const Span x = attn_span(a, i, g);
+            u += static_cast<long long>(tiles_of(x.hi - x.mid, a.kt)) * a.n_kv * a.cp;
+        }
+        u += (static_cast<long long>(head) * a.cp + cb) * tp;
+        const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + tp - 1);
+        n_b = w1 - w0 + 1;
+        b0 = (static_cast<int64_t>(s) * a.n_kv + head) * a.cp + cb + w0;
+    }
+    if (n_a == 0 && n_b == 1) return;
+    const int64_t stride = a.hd + 2;
+    float m = -INFINITY, l = 0.f, o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    for (int i = warp; i < n_a + n_b; i += JOIN_THREADS / 32) {
+        const float *d = i < n_a ? a.part_a + ((a0 + i) * a.ra + ri % a.mr) * stride
+                                 : a.part_b + ((b0 + i - n_a) * a.rb + r % a.mr) * stride;
+        const float mi = d[a.hd], li = d[a.hd + 1];
+        const float mn = fmaxf(m, mi), mz = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m - mz), fi = exp2f(mi - mz);
+        l = l * f + li * fi;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (lane + 32 * e < a.hd) o[e] = o[e] * f + d[lane + 32 * e] * fi;
+        m = mn;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_o[warp][lane + 32 * e] = o[e];
+    if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = l;
+    }
+    __syncthreads();
+    float M = -INFINITY, L = 0.f;
+    for (int i = 0; i < JOIN_THREADS / 32; ++i) M = fmaxf(M, s_m[i]);
+    const float mz = M == -INFINITY ? 0.f : M;
+    float f[JOIN_THREADS / 32];
+    for (int i = 0; i < JOIN_THREADS / 32; ++i) {
+        f[i] = exp2f(s_m[i] - mz);
+        L += s_l[i] * f[i];
+    }
+    const float inv = L > 0.f ? 1.f / L : 1.f;
+    const int64_t row = static_cast<int64_t>(s) * a.n_q + hq;
+    for (int e = t; e < a.hd; e += JOIN_THREADS) {
+        float x = 0.f;
+        for (int i = 0; i < JOIN_THREADS / 32; ++i) x += s_o[i][e] * f[i];
+        attn_put(static_cast<T *>(a.out) + row * a.hd + e, x * inv);
+    }
+    if (a.lse && t == 0) a.lse[row] = mz * float(LN2) + logf(L);
+}
+
+} // namespace
+
+AttnShape attn_shape(int dtype, int hd)
+{
+    (void)dtype;
+    (void)hd;
+    return AttnShape{SIMT_MR, 32};
+}
+
+cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st)
+{
+    if (a.share > 1) attn_share_kernel<<<static_cast<unsigned>(a.n_group), PLAN_T, 0, st>>>(a);
+    attn_plan_kernel<<<1, PLAN_T, 0, st>>>(a);
+    return cudaGetLastError();
+}
+cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st)
+{
+    const unsigned grid = static_cast<unsigned>((a.nw + ATTN_WARPS - 1) / ATTN_WARPS);
+    if (dtype == LOSSK_F32) attn_simt_kernel<float><<<grid, ATTN_WARPS * 32, 0, st>>>(a);
+    else if (dtype == LOSSK_BF16) attn_simt_kernel<uint16_t><<<grid, ATTN_WARPS * 32, 0, st>>>(a);
+    else attn_simt_kernel<h16_t><<<grid, ATTN_WARPS * 32, 0, st>>>(a);
+    return cudaGetLastError();
+}
+cudaError_t launch_attn_join(int dtype, const AttnArgs &a, cudaStream_t st)
+{
+    const unsigned grid = static_cast<unsigned>(a.n_group) * a.share * a.n_q;
+    if (dtype == LOSSK_F32) attn_join_kernel<float><<<grid, JOIN_THREADS, 0, st>>>(a);
+    else if (dtype == LOSSK_BF16) attn_join_kernel<uint16_t><<<grid, JOIN_THREADS, 0, st>>>(a);
+    else attn_join_kernel<h16_t><<<grid, JOIN_THREADS, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+} // namespace lossk

@@ -117,6 +117,26 @@ CopyArgs copy_args(void *pool, int64_t n_planes, int64_t plane_stride, int64_t p
     return c;
 }
 
+// The scratch of lossk_paged_attn.  Partial results take at most twice the query
+// rows on either side (a group's shared rows are cut into items of mr rows,
+// the last one less than full), and one item's rows more for each warp.
+struct AttnLayout {
+    size_t off_shared, off_base, off_part, total;
+};
+
+int32_t attn_layout(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t hd, AttnLayout *L)
+{
+    if (n_seq < 1 || n_q < 1 || n_kv < 1 || hd < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_seq > MAX_DIM || n_q > MAX_DIM || n_kv > MAX_DIM || n_seq * n_q > MAX_DIM || hd > 256)
+        return LOSSK_DIMENSION_TOO_LARGE;
+    L->off_shared = 256;
+    L->off_base = align256(L->off_shared + sizeof(int32_t) * n_seq);
+    L->off_part = align256(L->off_base + sizeof(long long) * (n_seq + 1));
+    const size_t rows = 4 * static_cast<size_t>(n_seq) * n_q + 2 * ATTN_MAX_MR * ATTN_MAX_WARPS;
+    L->total = align256(L->off_part + sizeof(float) * rows * (hd + 2));
+    return LOSSK_OK;
+}
+
 int32_t ws_check(const void *ws, int64_t bytes, size_t need)
 {
     if (!ws || bytes < static_cast<int64_t>(need)) return LOSSK_LENGTH_MISMATCH;
@@ -140,6 +160,10 @@ int64_t lossk_decode_workspace_bytes(int32_t kind, int64_t a, int64_t b, int64_t
     if (kind == LOSSK_KIND_CACHE) {
         CacheLayout L;
         return cache_layout(a, b, &L) == LOSSK_OK ? static_cast<int64_t>(L.total) : -1;
+    }
+    if (kind == LOSSK_KIND_PAGED_ATTN) {
+        AttnLayout L;
+        return attn_layout(a, b, c, d, &L) == LOSSK_OK ? static_cast<int64_t>(L.total) : -1;
     }
     return -1;
 }
@@ -481,6 +505,92 @@ int32_t lossk_cache_write(int64_t n_tok, int64_t n_seq, int64_t n_kv_heads, int6
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Launch k(KK_CACHE_WRITE, st);
     return status_of(launch_cache_write(a, word, st));
+}
+
+int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim, int64_t max_pages,
+                         int64_t page_size, int64_t n_pages, int64_t share, int32_t dtype, const void *q,
+                         int64_t q_len, int64_t q_stride, const void *k_pages, const void *v_pages,
+                         int64_t pages_len, int64_t page_stride, int64_t tok_stride, int64_t head_stride,
+                         const int32_t *table, int64_t table_len, int64_t table_stride, const int32_t *lens,
+                         int64_t lens_len, int64_t max_len, int64_t window, double scale, void *out, int64_t out_len,
+                         float *lse_out, void *workspace, int64_t workspace_bytes, lossk_stream_t stream)
+{
+    AttnLayout L;
+    int32_t s = attn_layout(n_seq, n_q_heads, n_kv_heads, head_dim, &L);
+    if (s != LOSSK_OK) return s;
+    if ((s = cache_sizes(n_seq, max_pages, page_size, n_pages)) != LOSSK_OK) return s;
+    if (share < 1) return LOSSK_EMPTY_DIMENSION;
+    if (max_pages * page_size > (int64_t(1) << 30)) return LOSSK_DIMENSION_TOO_LARGE;
+    const int64_t row = n_q_heads * head_dim;
+    if (!dtype_ok(dtype) || n_q_heads % n_kv_heads || n_seq % share || max_len < 0 || window < 0 || !q ||
+        q_stride < row || q_stride > (int64_t(1) << 40) || q_len < (n_seq - 1) * q_stride + row || !out ||
+        out_len < n_seq * row || !v_pages ||
+        pages_short(n_pages, page_size, n_kv_heads, head_dim, k_pages, pages_len, page_stride, tok_stride,
+                    head_stride) ||
+        table_short(n_seq, max_pages, table, table_len, table_stride) || !lens || lens_len < n_seq)
+        return LOSSK_LENGTH_MISMATCH;
+    if ((s = ws_check(workspace, workspace_bytes, L.total)) != LOSSK_OK) return s;
+    // rows are read 16 bytes at a time
+    const int64_t e = esize(dtype);
+    if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(out, 16) ||
+        misaligned(workspace, 256) || misaligned(table, 4) || misaligned(lens, 4) || misaligned(lse_out, 4) ||
+        ((head_dim | q_stride | page_stride | tok_stride | head_stride) * e & 15) != 0)
+        return LOSSK_UNALIGNED;
+    if (!std::isfinite(scale) || !std::isfinite(static_cast<float>(scale * LOG2E))) return LOSSK_NON_FINITE_SCALAR;
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const AttnShape shape = attn_shape(dtype, static_cast<int>(head_dim));
+    AttnArgs a{};
+    a.n_group = static_cast<int>(n_seq / share);
+    a.share = static_cast<int>(share);
+    a.n_q = static_cast<int>(n_q_heads);
+    a.n_kv = static_cast<int>(n_kv_heads);
+    a.group = a.n_q / a.n_kv;
+    a.hd = static_cast<int>(head_dim);
+    a.max_pages = static_cast<int>(max_pages);
+    a.page = static_cast<int>(page_size);
+    a.n_pages = static_cast<int>(n_pages);
+    a.window = static_cast<int>(window < (int64_t(1) << 30) ? window : 0);   // wider than any sequence: none
+    a.scale_log2 = static_cast<float>(scale * LOG2E);
+    a.q = q;
+    a.k = k_pages;
+    a.v = v_pages;
+    a.q_stride = q_stride;
+    a.page_stride = page_stride;
+    a.tok_stride = tok_stride;
+    a.head_stride = head_stride;
+    a.table = table;
+    a.lens = lens;
+    a.table_stride = table_stride;
+    a.out = out;
+    a.lse = lse_out;
+    a.kt = shape.kt;
+    a.mr = shape.mr;
+    const int rows_s = a.share * a.group;
+    a.cs = (rows_s + a.mr - 1) / a.mr;
+    a.cp = (a.group + a.mr - 1) / a.mr;
+    a.ra = rows_s < a.mr ? rows_s : a.mr;
+    a.rb = a.group < a.mr ? a.group : a.mr;
+    // no more warps than units there can be
+    const int64_t cap = max_len > 0 && max_len < max_pages * page_size ? max_len : max_pages * page_size;
+    const int64_t units = n_seq * n_kv_heads * a.cp * ((cap + a.kt - 1) / a.kt + 1);
+    a.nw = static_cast<int>(units < ATTN_MAX_WARPS ? units : ATTN_MAX_WARPS);
+    a.shared = reinterpret_cast<int32_t *>(ws + L.off_shared);
+    a.base = reinterpret_cast<long long *>(ws + L.off_base);
+    a.part_a = reinterpret_cast<float *>(ws + L.off_part);
+    a.part_b = a.part_a + (static_cast<int64_t>(a.n_group) * a.n_kv * a.cs + a.nw) * a.ra * (a.hd + 2);
+    a.fault = fault_of(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    {
+        Launch k(KK_ATTN_PLAN, st);
+        if (launch_attn_plan(a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    }
+    {
+        Launch k(KK_ATTN, st);
+        if (launch_attn(dtype, a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    }
+    Launch k(KK_ATTN_JOIN, st);
+    return status_of(launch_attn_join(dtype, a, st));
 }
 
 } // extern "C"

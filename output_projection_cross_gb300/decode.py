@@ -18,7 +18,8 @@ KIND_BEAM_SELECT, KIND_CACHE, KIND_PAGED_ATTN = 0, 1, 2
 
 __all__ = ["KIND_BEAM_SELECT", "KIND_CACHE", "KIND_PAGED_ATTN", "decode_workspace", "beam_buffers",
            "lossk_decode_workspace_bytes", "lossk_beam_select", "lossk_beam_gather", "lossk_cache_fork",
-           "lossk_cache_reserve", "lossk_cache_free", "lossk_cache_compact", "lossk_cache_copy", "lossk_cache_write"]
+           "lossk_cache_reserve", "lossk_cache_free", "lossk_cache_compact", "lossk_cache_copy", "lossk_cache_write",
+           "lossk_paged_attn"]
 
 
 def lossk_decode_workspace_bytes(kind: int, a: int, b: int, c: int = 0, d: int = 0) -> int:
@@ -278,3 +279,34 @@ def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, w
                                table.data_ptr(), _span(table), stride, lens.data_ptr(), lens.numel(), _ptr(first),
                                _len(first), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, "lossk_cache_write")
+
+
+# ---- attention of one new token ------------------------------------------------------------
+
+def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, share=1, max_len=0, out=None,
+                     lse_out=None, ws=None, stream=None):
+    """q [n_seq, n_q_heads, head_dim] (sequences may be strided) over one layer's pages
+    [pages, page, heads, head_dim] (any strides).  scale defaults to head_dim ** -0.5; share: how
+    many consecutive sequences may share leading pages.  Returns out."""
+    (n_pages, page, kv, hd), (sp, stok, sh, _) = _pages(k_pages, v_pages)
+    _ints(lens=lens)
+    _on_gpu(q, "q", k_pages.dtype, contiguous=False)
+    n, m, stride = _table(table)
+    if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd or (n and not q[0].is_contiguous()):
+        raise ValueError("q must be [n_seq, n_q_heads, head_dim] with contiguous sequences")
+    hq = q.shape[1]
+    if out is None:
+        out = torch.empty((n, hq, hd), dtype=q.dtype, device=q.device)
+    _on_gpu(out, "out", q.dtype)
+    _on_gpu(lse_out, "lse_out", torch.float32)
+    if lse_out is not None and lse_out.numel() != n * hq:
+        raise ValueError("lse_out must be [n_seq, n_q_heads]")
+    if ws is None:
+        ws = decode_workspace(KIND_PAGED_ATTN, n, hq, kv, hd, q.device)
+    st = lib.lossk_paged_attn(n, hq, kv, hd, m, page, n_pages, share, _dtype_code(q), q.data_ptr(), _span(q),
+                              q.stride(0) if n > 1 else hq * hd, k_pages.data_ptr(), v_pages.data_ptr(),
+                              _span(k_pages), sp, stok, sh, table.data_ptr(), _span(table), stride, lens.data_ptr(),
+                              lens.numel(), max_len, window, hd ** -0.5 if scale is None else scale, out.data_ptr(),
+                              out.numel(), _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "lossk_paged_attn")
+    return out

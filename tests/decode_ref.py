@@ -122,3 +122,22 @@ class Cache:
             self.pool[:, b] = self.pool[:, a]
         self.rows = [[to.get(p, p) for p in r] for r in self.rows]
         return n
+
+
+def attend(q, k, v, table, lens, page, scale, window=0):
+    """q [S][Hq][hd], k and v [pages][page][Hkv][hd], all float64.  Returns (out, lse)."""
+    S, Hq, hd = q.shape
+    group = Hq // k.shape[2]
+    out, lse = np.zeros((S, Hq, hd)), np.full((S, Hq), -np.inf)
+    for s in range(S):
+        n = int(lens[s])
+        j = np.arange(max(0, n - window) if window else 0, n)
+        if not len(j):
+            continue
+        kk, vv = k[table[s, j // page], j % page], v[table[s, j // page], j % page]
+        for h in range(Hq):
+            x = kk[:, h // group] @ q[s, h] * scale
+            m = x.max()
+            p = np.exp(x - m)
+            out[s, h], lse[s, h] = p @ vv[:, h // group] / p.sum(), m + math.log(p.sum())
+    return out, lse

@@ -219,3 +219,51 @@ def test_reference_cache_by_hand():
     assert not c.reserve([1, 5]) and c.reserve([1, 0]) and c.rows[0] == [4, 0, 2]
     c.free([1, 0])
     assert c.compact() == 2 and c.rows == [[], [0, 1]]
+
+
+# ---- attention of one new token ---------------------------------------------------------
+
+def attn_call(L, **over):
+    return call(L.lib.lossk_paged_attn, dict(
+        n_seq=6, n_q=8, n_kv=2, hd=64, max_pages=5, page=16, n_pages=40, share=1, dtype=1, q=P, q_len=6 * 512,
+        q_stride=512, k=P, v=P, pages_len=40 * 2048, page_stride=2048, tok_stride=128, head_stride=64, table=P,
+        table_len=30, table_stride=5, lens=P, lens_len=6, max_len=0, window=0, scale=0.125, out=P, out_len=6 * 512,
+        lse=P, ws=P, ws_bytes=1 << 28, stream=None), over)
+
+
+def test_attention_refusals(L):
+    for size in ("n_seq", "n_q", "n_kv", "hd", "max_pages", "page", "n_pages", "share"):
+        assert attn_call(L, **{size: 0}) == 581, size
+    for size in ("n_seq", "n_q", "max_pages", "page", "n_pages"):
+        assert attn_call(L, **{size: (1 << 24) + 1}) == 583, size
+    assert attn_call(L, hd=264) == 583
+    assert attn_call(L, max_pages=1 << 20, page=1 << 11) == 583
+    for p in ("q", "k", "v", "table", "lens", "out", "ws"):
+        assert attn_call(L, **{p: None}) == 582, p
+    for k, v in dict(n_q=7, share=4, q_len=6 * 512 - 1, q_stride=511, pages_len=40 * 2048 - 1, table_len=29,
+                     table_stride=4, lens_len=5, out_len=6 * 512 - 1, max_len=-1, window=-1, dtype=5,
+                     page_stride=-8, tok_stride=136,
+                     ws_bytes=L.lossk_decode_workspace_bytes(L.KIND_PAGED_ATTN, 6, 8, 2, 64) - 1).items():
+        assert attn_call(L, **{k: v}) == 582, k
+    for p in ("q", "k", "v", "out"):
+        assert attn_call(L, **{p: P + 8}) == 591, p
+    assert attn_call(L, ws=P + 128) == 591
+    assert attn_call(L, hd=60, q_len=1 << 20) == 591
+    assert attn_call(L, tok_stride=132, pages_len=1 << 20) == 591
+    assert attn_call(L, q_stride=516, q_len=1 << 20) == 591
+    for x in (float("nan"), float("inf"), 1e300):
+        assert attn_call(L, scale=x) == 585
+    assert attn_call(L, scale=float("nan"), ws=P + 1) == 591
+    assert L.lossk_decode_workspace_bytes(L.KIND_PAGED_ATTN, 1, 1, 1, 257) == -1
+
+
+def test_reference_attention_by_hand():
+    import decode_ref as ref
+    k = np.zeros((2, 2, 1, 1))
+    k[1, :, 0, 0] = [0.0, math_log3 := float(np.log(3.0))]
+    v = np.zeros((2, 2, 1, 1))
+    v[1, :, 0, 0] = [4.0, 8.0]
+    o, lse = ref.attend(np.ones((1, 1, 1)), k, v, np.array([[1]]), [2], 2, 1.0)
+    np.testing.assert_allclose([o.item(), lse.item()], [7.0, np.log(4.0)], rtol=1e-12)
+    o, lse = ref.attend(np.ones((1, 1, 1)), k, v, np.array([[1]]), [2], 2, 1.0, window=1)
+    np.testing.assert_allclose([o.item(), lse.item()], [8.0, math_log3], rtol=1e-12)
