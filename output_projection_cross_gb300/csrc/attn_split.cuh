@@ -1,0 +1,169 @@
+// attn_split.cuh -- how attention over a paged cache is split into units, items
+// and runs (see k_attn.cu), shared by its kernels.
+#pragma once
+#include "../../include/lossk.h"
+#include "decode_internal.h"
+#include "ptx.cuh"
+
+namespace lossk {
+
+__device__ __forceinline__ float attn_f(float x) { return x; }
+__device__ __forceinline__ float attn_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__device__ __forceinline__ float attn_f(h16_t x) { return f16_to_f(x.bits); }
+__device__ __forceinline__ void attn_put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void attn_put(uint16_t *p, float v)
+{
+    *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+}
+__device__ __forceinline__ void attn_put(h16_t *p, float v)
+{
+    p->bits = static_cast<uint16_t>(pack_f16x2(v, 0.f) & 0xFFFFu);
+}
+
+// A sequence's length as the kernels use it: 0 where it is out of range.
+__device__ __forceinline__ int attn_len(const AttnArgs &a, int s)
+{
+    const int n = a.lens[s];
+    return n >= 0 && n <= static_cast<int64_t>(a.max_pages) * a.page ? n : 0;
+}
+
+// What of a sequence is read: tokens [lo, hi) with its group (the leading
+// `shared` tokens, lo on), then [mid, hi) by itself.
+struct Span {
+    int lo, mid, hi;
+};
+__device__ __forceinline__ Span attn_span(const AttnArgs &a, int s, int g)
+{
+    Span r;
+    r.hi = attn_len(a, s);
+    r.lo = a.window > 0 && r.hi > a.window ? r.hi - a.window : 0;
+    const int shared = a.share > 1 ? a.shared[g] : 0;
+    r.mid = shared > r.lo ? shared : r.lo;
+    return r;
+}
+__device__ __forceinline__ int tiles_of(int n, int kt) { return (n + kt - 1) / kt; }
+
+// Units of a group's shared part, per item.
+__device__ __forceinline__ int shared_tiles(const AttnArgs &a, int g)
+{
+    if (a.share <= 1) return 0;
+    const Span r = attn_span(a, g * a.share, g);
+    return tiles_of(r.mid - r.lo, a.kt);
+}
+__device__ __forceinline__ long long group_units(const AttnArgs &a, int g)
+{
+    long long u = static_cast<long long>(shared_tiles(a, g)) * a.n_kv * a.cs;
+    for (int i = 0; i < a.share; ++i) {
+        const Span r = attn_span(a, g * a.share + i, g);
+        u += static_cast<long long>(tiles_of(r.hi - r.mid, a.kt)) * a.n_kv * a.cp;
+    }
+    return u;
+}
+
+// The run of units of warp w of nw, and the warp that has unit u.
+__device__ __forceinline__ long long run_start(long long units, int nw, int w) { return units * w / nw; }
+__device__ __forceinline__ int warp_of(long long units, int nw, long long u)
+{
+    return static_cast<int>(((u + 1) * nw - 1) / units);
+}
+__device__ __forceinline__ int warps_used(long long units, int nw) { return units < nw ? static_cast<int>(units) : nw; }
+
+// One item's piece as a warp computes it.
+struct Piece {
+    int first_row;      // its rows are rows first_row.. of sequences from seq on, counted group rows of heads
+    int rows;
+    int seq;            // the sequence (private) or the group's first one (shared)
+    int head;           // KV head
+    int t0, t1;         // tokens [t0, t1)
+    int64_t slot;       // where a partial result goes; -1: the whole row is here
+    float *part;
+};
+
+// Query row i of a piece: sequence and query head.
+__device__ __forceinline__ int row_seq(const AttnArgs &a, const Piece &p, int i)
+{
+    return p.seq + (p.first_row + i) / a.group;
+}
+__device__ __forceinline__ int row_head(const AttnArgs &a, const Piece &p, int i)
+{
+    return p.head * a.group + (p.first_row + i) % a.group;
+}
+
+// Walks warp w's run; body(piece) computes each piece.
+template <typename F> __device__ __forceinline__ void walk_run(const AttnArgs &a, int w, F &&body)
+{
+    const long long units = a.base[a.n_group];
+    const int nw = warps_used(units, a.nw);
+    if (w >= nw) return;
+    long long u = run_start(units, nw, w);
+    const long long u1 = run_start(units, nw, w + 1);
+    int g = 0;
+    for (int lo = 0, hi = a.n_group; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (a.base[mid] <= u) lo = mid;
+        else hi = mid;
+        g = lo;
+    }
+    while (u < u1) {
+        while (a.base[g + 1] <= u) ++g;
+        long long in = u - a.base[g];
+        const int ts = shared_tiles(a, g);
+        const long long su = static_cast<long long>(ts) * a.n_kv * a.cs;
+        Piece p;
+        int tile, tiles, lo, hi;
+        if (in < su) {
+            const int item = static_cast<int>(in / ts), c = item % a.cs;
+            tile = static_cast<int>(in % ts);
+            tiles = ts;
+            p.head = item / a.cs;
+            p.seq = g * a.share;
+            p.first_row = c * a.mr;
+            p.rows = min(a.mr, a.share * a.group - p.first_row);
+            const Span r = attn_span(a, p.seq, g);
+            lo = r.lo;
+            hi = r.mid;
+            p.slot = (static_cast<int64_t>(g) * a.n_kv + p.head) * a.cs + c + w;
+            p.part = a.part_a + p.slot * a.ra * (a.hd + ATTN_ROW);
+        } else {
+            in -= su;
+            int s = g * a.share;
+            Span r = attn_span(a, s, g);
+            tiles = tiles_of(r.hi - r.mid, a.kt);
+            while (in >= static_cast<long long>(tiles) * a.n_kv * a.cp) {
+                in -= static_cast<long long>(tiles) * a.n_kv * a.cp;
+                r = attn_span(a, ++s, g);
+                tiles = tiles_of(r.hi - r.mid, a.kt);
+            }
+            const int item = static_cast<int>(in / tiles), c = item % a.cp;
+            tile = static_cast<int>(in % tiles);
+            p.head = item / a.cp;
+            p.seq = s;
+            p.first_row = c * a.mr;
+            p.rows = min(a.mr, a.group - p.first_row);
+            lo = r.mid;
+            hi = r.hi;
+            p.slot = (static_cast<int64_t>(s) * a.n_kv + p.head) * a.cp + c + w;
+            p.part = a.part_b + p.slot * a.rb * (a.hd + ATTN_ROW);
+            if (ts == 0 && tile == 0 && u + tiles <= u1) p.slot = -1;
+        }
+        const int n = static_cast<int>(min(static_cast<long long>(tiles - tile), u1 - u));
+        p.t0 = lo + tile * a.kt;
+        p.t1 = min(hi, p.t0 + n * a.kt);
+        body(p);
+        u += n;
+    }
+}
+
+// Where token j of a sequence lies, in elements from the pages' start; -1 for
+// an entry out of range.
+__device__ __forceinline__ int64_t token_at(const AttnArgs &a, int seq, int j)
+{
+    const int p = a.table[seq * a.table_stride + j / a.page];
+    if (p < 0 || p >= a.n_pages) {
+        raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
+        return -1;
+    }
+    return p * a.page_stride + (j % a.page) * a.tok_stride;
+}
+
+} // namespace lossk

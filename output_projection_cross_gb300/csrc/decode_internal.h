@@ -153,19 +153,24 @@ struct AttnArgs {
     int nw;                                        // warps at most
     int32_t *shared;                               // [n_group] shared tokens
     long long *base;                               // [n_group + 1] units before each group
-    float *part_a, *part_b;                        // partial results: o[hd], m (log2 units), l per row
+    float *part_a, *part_b;                        // partial results per row: o[hd], m (log2 units), l, and 2 unused
     int *fault;
 };
 
-// Query rows per item and tokens per unit of the kernel that takes this type and head size.
+// The kernel that takes this type, head size and number of query rows per KV
+// head: rows per item, tokens per unit, warps a block (one block per SM).
 struct AttnShape {
-    int mr, kt;
+    int mr, kt, warps;
 };
 constexpr int ATTN_MAX_MR = 32;
 constexpr int ATTN_MAX_WARPS = 152 * 8;
-AttnShape attn_shape(int dtype, int hd);
+constexpr int ATTN_ROW = 4;            // floats a partial row holds beside o
+AttnShape attn_shape(int dtype, int hd, int rows);
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st);
+// The tensor-core kernel (16-bit types).
+AttnShape attn_mma_shape(int hd, int rows);
+cudaError_t launch_attn_mma(bool f16, const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_join(int dtype, const AttnArgs &a, cudaStream_t st);
 
 } // namespace lossk

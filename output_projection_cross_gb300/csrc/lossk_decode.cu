@@ -133,7 +133,7 @@ int32_t attn_layout(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t hd, AttnLa
     L->off_base = align256(L->off_shared + sizeof(int32_t) * n_seq);
     L->off_part = align256(L->off_base + sizeof(long long) * (n_seq + 1));
     const size_t rows = 4 * static_cast<size_t>(n_seq) * n_q + 2 * ATTN_MAX_MR * ATTN_MAX_WARPS;
-    L->total = align256(L->off_part + sizeof(float) * rows * (hd + 2));
+    L->total = align256(L->off_part + sizeof(float) * rows * (hd + ATTN_ROW));
     return LOSSK_OK;
 }
 
@@ -539,7 +539,6 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
     if (!std::isfinite(scale) || !std::isfinite(static_cast<float>(scale * LOG2E))) return LOSSK_NON_FINITE_SCALAR;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const AttnShape shape = attn_shape(dtype, static_cast<int>(head_dim));
     AttnArgs a{};
     a.n_group = static_cast<int>(n_seq / share);
     a.share = static_cast<int>(share);
@@ -564,9 +563,10 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
     a.table_stride = table_stride;
     a.out = out;
     a.lse = lse_out;
+    const int rows_s = a.share * a.group;
+    const AttnShape shape = attn_shape(dtype, a.hd, rows_s);
     a.kt = shape.kt;
     a.mr = shape.mr;
-    const int rows_s = a.share * a.group;
     a.cs = (rows_s + a.mr - 1) / a.mr;
     a.cp = (a.group + a.mr - 1) / a.mr;
     a.ra = rows_s < a.mr ? rows_s : a.mr;
@@ -574,11 +574,11 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
     // no more warps than units there can be
     const int64_t cap = max_len > 0 && max_len < max_pages * page_size ? max_len : max_pages * page_size;
     const int64_t units = n_seq * n_kv_heads * a.cp * ((cap + a.kt - 1) / a.kt + 1);
-    a.nw = static_cast<int>(units < ATTN_MAX_WARPS ? units : ATTN_MAX_WARPS);
+    a.nw = static_cast<int>(units < 152 * shape.warps ? units : 152 * shape.warps);
     a.shared = reinterpret_cast<int32_t *>(ws + L.off_shared);
     a.base = reinterpret_cast<long long *>(ws + L.off_base);
     a.part_a = reinterpret_cast<float *>(ws + L.off_part);
-    a.part_b = a.part_a + (static_cast<int64_t>(a.n_group) * a.n_kv * a.cs + a.nw) * a.ra * (a.hd + 2);
+    a.part_b = a.part_a + (static_cast<int64_t>(a.n_group) * a.n_kv * a.cs + a.nw) * a.ra * (a.hd + ATTN_ROW);
     a.fault = fault_of(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     {
