@@ -43,6 +43,13 @@ __device__ __forceinline__ Span attn_span(const AttnArgs &a, int s, int g)
 }
 __device__ __forceinline__ int tiles_of(int n, int kt) { return (n + kt - 1) / kt; }
 
+// Starting an item (its query rows, its first tile's latency, its result) takes
+// a warp about as long as ITEM_COST tiles; counting it so keeps runs of many
+// short items from lagging behind.  An item's units are ITEM_COST for its
+// start, then one per tile.
+constexpr int ITEM_COST = 4;
+__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + ITEM_COST : 0; }
+
 // Units of a group's shared part, per item.
 __device__ __forceinline__ int shared_tiles(const AttnArgs &a, int g)
 {
@@ -52,10 +59,10 @@ __device__ __forceinline__ int shared_tiles(const AttnArgs &a, int g)
 }
 __device__ __forceinline__ long long group_units(const AttnArgs &a, int g)
 {
-    long long u = static_cast<long long>(shared_tiles(a, g)) * a.n_kv * a.cs;
+    long long u = static_cast<long long>(units_of(shared_tiles(a, g))) * a.n_kv * a.cs;
     for (int i = 0; i < a.share; ++i) {
         const Span r = attn_span(a, g * a.share + i, g);
-        u += static_cast<long long>(tiles_of(r.hi - r.mid, a.kt)) * a.n_kv * a.cp;
+        u += static_cast<long long>(units_of(tiles_of(r.hi - r.mid, a.kt))) * a.n_kv * a.cp;
     }
     return u;
 }
@@ -67,6 +74,13 @@ __device__ __forceinline__ int warp_of(long long units, int nw, long long u)
     return static_cast<int>(((u + 1) * nw - 1) / units);
 }
 __device__ __forceinline__ int warps_used(long long units, int nw) { return units < nw ? static_cast<int>(units) : nw; }
+
+// a / b, mostly in 32 bits (a 64-bit division is a long routine).
+__device__ __forceinline__ int quotient(long long a, int b)
+{
+    return a <= 0xFFFFFFFFll ? static_cast<int>(static_cast<unsigned>(a) / static_cast<unsigned>(b))
+                             : static_cast<int>(a / b);
+}
 
 // One item's piece as a warp computes it.
 struct Piece {
@@ -107,13 +121,13 @@ template <typename F> __device__ __forceinline__ void walk_run(const AttnArgs &a
     while (u < u1) {
         while (a.base[g + 1] <= u) ++g;
         long long in = u - a.base[g];
-        const int ts = shared_tiles(a, g);
-        const long long su = static_cast<long long>(ts) * a.n_kv * a.cs;
+        const int ts = shared_tiles(a, g), us = units_of(ts);
+        const long long su = static_cast<long long>(us) * a.n_kv * a.cs;
         Piece p;
-        int tile, tiles, lo, hi;
+        int at, tiles, lo, hi;                      // the run goes on `at` units into the item
         if (in < su) {
-            const int item = static_cast<int>(in / ts), c = item % a.cs;
-            tile = static_cast<int>(in % ts);
+            const int item = quotient(in, us), c = item % a.cs;
+            at = static_cast<int>(in - static_cast<long long>(item) * us);
             tiles = ts;
             p.head = item / a.cs;
             p.seq = g * a.share;
@@ -129,13 +143,13 @@ template <typename F> __device__ __forceinline__ void walk_run(const AttnArgs &a
             int s = g * a.share;
             Span r = attn_span(a, s, g);
             tiles = tiles_of(r.hi - r.mid, a.kt);
-            while (in >= static_cast<long long>(tiles) * a.n_kv * a.cp) {
-                in -= static_cast<long long>(tiles) * a.n_kv * a.cp;
+            for (long long all; in >= (all = static_cast<long long>(units_of(tiles)) * a.n_kv * a.cp);) {
+                in -= all;
                 r = attn_span(a, ++s, g);
                 tiles = tiles_of(r.hi - r.mid, a.kt);
             }
-            const int item = static_cast<int>(in / tiles), c = item % a.cp;
-            tile = static_cast<int>(in % tiles);
+            const int up = units_of(tiles), item = quotient(in, up), c = item % a.cp;
+            at = static_cast<int>(in - static_cast<long long>(item) * up);
             p.head = item / a.cp;
             p.seq = s;
             p.first_row = c * a.mr;
@@ -144,13 +158,15 @@ template <typename F> __device__ __forceinline__ void walk_run(const AttnArgs &a
             hi = r.hi;
             p.slot = (static_cast<int64_t>(s) * a.n_kv + p.head) * a.cp + c + w;
             p.part = a.part_b + p.slot * a.rb * (a.hd + ATTN_ROW);
-            if (ts == 0 && tile == 0 && u + tiles <= u1) p.slot = -1;
         }
-        const int n = static_cast<int>(min(static_cast<long long>(tiles - tile), u1 - u));
-        p.t0 = lo + tile * a.kt;
-        p.t1 = min(hi, p.t0 + n * a.kt);
-        body(p);
+        const int n = static_cast<int>(min(static_cast<long long>(units_of(tiles) - at), u1 - u));
+        const int tile0 = max(at - ITEM_COST, 0), tile1 = at + n - ITEM_COST;
         u += n;
+        if (tile1 <= 0) continue;                   // the run ends within the item's start
+        if (ts == 0 && tile0 == 0 && tile1 == tiles) p.slot = -1;
+        p.t0 = lo + tile0 * a.kt;
+        p.t1 = min(hi, lo + tile1 * a.kt);
+        body(p);
     }
 }
 

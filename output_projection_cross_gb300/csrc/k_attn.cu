@@ -26,7 +26,9 @@ namespace {
 
 constexpr int PLAN_T = 256;
 constexpr int ATTN_WARPS = 4;
-constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_THREADS = JOIN_WARPS * 32;
+constexpr int JOIN_W = 1024;
 
 // Shared tokens of each group: the leading pages whose ids agree in all its
 // rows, full in all of them.  With a window the rows have to be equally long,
@@ -170,8 +172,8 @@ template <typename T> __global__ void __launch_bounds__(ATTN_WARPS * 32) attn_si
 // written by it.
 template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(AttnArgs a)
 {
-    __shared__ float s_o[JOIN_THREADS / 32][256];
-    __shared__ float s_m[JOIN_THREADS / 32], s_l[JOIN_THREADS / 32];
+    __shared__ __align__(16) float s_o[JOIN_WARPS][256];
+    __shared__ float s_w[JOIN_W], s_x[JOIN_WARPS], s_l[JOIN_WARPS];
     const int s = blockIdx.x / a.n_q, hq = blockIdx.x % a.n_q, g = s / a.share;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int head = hq / a.group, r = hq % a.group;
@@ -185,59 +187,71 @@ template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_
     int n_a = 0, n_b = 0;
     int64_t a0 = 0, b0 = 0;
     if (ts > 0) {
-        const long long u = a.base[g] + (static_cast<long long>(head) * a.cs + ca) * ts;
+        const long long u = a.base[g] + (static_cast<long long>(head) * a.cs + ca) * units_of(ts) + ITEM_COST;
         const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + ts - 1);
         n_a = w1 - w0 + 1;
         a0 = (static_cast<int64_t>(g) * a.n_kv + head) * a.cs + ca + w0;
     }
     if (tp > 0) {
-        long long u = a.base[g] + static_cast<long long>(ts) * a.n_kv * a.cs;
+        long long u = a.base[g] + static_cast<long long>(units_of(ts)) * a.n_kv * a.cs;
         for (int i = g * a.share; i < s; ++i) {
             const Span x = attn_span(a, i, g);
-            u += static_cast<long long>(tiles_of(x.hi - x.mid, a.kt)) * a.n_kv * a.cp;
+            u += static_cast<long long>(units_of(tiles_of(x.hi - x.mid, a.kt))) * a.n_kv * a.cp;
         }
-        u += (static_cast<long long>(head) * a.cp + cb) * tp;
+        u += (static_cast<long long>(head) * a.cp + cb) * units_of(tp) + ITEM_COST;
         const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + tp - 1);
         n_b = w1 - w0 + 1;
         b0 = (static_cast<int64_t>(s) * a.n_kv + head) * a.cp + cb + w0;
     }
     if (n_a == 0 && n_b == 1) return;
+    const int n = n_a + n_b;
     const int64_t stride = a.hd + ATTN_ROW;
-    float m = -INFINITY, l = 0.f, o[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = 0.f;
-    for (int i = warp; i < n_a + n_b; i += JOIN_THREADS / 32) {
-        const float *d = i < n_a ? a.part_a + ((a0 + i) * a.ra + ri % a.mr) * stride
-                                 : a.part_b + ((b0 + i - n_a) * a.rb + r % a.mr) * stride;
-        const float mi = d[a.hd], li = d[a.hd + 1];
-        const float mn = fmaxf(m, mi), mz = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - mz), fi = exp2f(mi - mz);
-        l = l * f + li * fi;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (lane + 32 * e < a.hd) o[e] = o[e] * f + d[lane + 32 * e] * fi;
-        m = mn;
+    const float *pa = a.part_a + (a0 * a.ra + ri % a.mr) * stride, *pb = a.part_b + (b0 * a.rb + r % a.mr) * stride;
+    const int64_t sa = a.ra * stride, sb = a.rb * stride;
+    auto piece = [&](int i) { return i < n_a ? pa + i * sa : pb + (i - n_a) * sb; };
+    // the largest m, then each piece's weight e^(m - M), kept for the first JOIN_W pieces
+    float M = -INFINITY;
+    for (int i = t; i < n; i += JOIN_THREADS) {
+        const float m = piece(i)[a.hd];
+        if (i < JOIN_W) s_w[i] = m;
+        M = fmaxf(M, m);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s_o[warp][lane + 32 * e] = o[e];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    if (lane == 0) s_x[warp] = M;
     __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < JOIN_THREADS / 32; ++i) M = fmaxf(M, s_m[i]);
+    for (int i = 0; i < JOIN_WARPS; ++i) M = fmaxf(M, s_x[i]);
     const float mz = M == -INFINITY ? 0.f : M;
-    float f[JOIN_THREADS / 32];
-    for (int i = 0; i < JOIN_THREADS / 32; ++i) {
-        f[i] = exp2f(s_m[i] - mz);
-        L += s_l[i] * f[i];
+    // each warp adds up its share of the pieces, a lane holding elements 4 lane.. and 128 + 4 lane..
+    float4 acc[2] = {};
+    float L = 0.f;
+    const int words = a.hd >> 2;
+#pragma unroll 4
+    for (int i = warp; i < n; i += JOIN_WARPS) {
+        const float *d = piece(i);
+        const float f = exp2f((i < JOIN_W ? s_w[i] : d[a.hd]) - mz);
+        L += f * d[a.hd + 1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (lane + 32 * h < words) {
+                const float4 x = *reinterpret_cast<const float4 *>(d + 4 * (lane + 32 * h));
+                acc[h].x += f * x.x;
+                acc[h].y += f * x.y;
+                acc[h].z += f * x.z;
+                acc[h].w += f * x.w;
+            }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < words) *reinterpret_cast<float4 *>(&s_o[warp][4 * (lane + 32 * h)]) = acc[h];
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    L = 0.f;
+    for (int i = 0; i < JOIN_WARPS; ++i) L += s_l[i];
     const float inv = L > 0.f ? 1.f / L : 1.f;
     const int64_t row = static_cast<int64_t>(s) * a.n_q + hq;
     for (int e = t; e < a.hd; e += JOIN_THREADS) {
         float x = 0.f;
-        for (int i = 0; i < JOIN_THREADS / 32; ++i) x += s_o[i][e] * f[i];
+        for (int i = 0; i < JOIN_WARPS; ++i) x += s_o[i][e];
         attn_put(static_cast<T *>(a.out) + row * a.hd + e, x * inv);
     }
     if (a.lse && t == 0) a.lse[row] = mz * float(LN2) + logf(L);

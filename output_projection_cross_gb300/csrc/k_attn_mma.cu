@@ -24,12 +24,18 @@
 #include "attn_split.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace lossk {
 
 namespace {
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// bytes 0: zeros, src is not read
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, int bytes)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -69,7 +75,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // rows, KT tokens a unit, STAGES tiles in a warp's ring, WARPS warps a block.
 template <int HDP_, int MT_> struct Variant {
     static constexpr int HDP = HDP_, MT = MT_;
-    static constexpr int KT = HDP <= 128 ? 32 : 16;
+    static constexpr int KT = 16;
     static constexpr int STAGES = 3;
     // rows an odd number of 16-byte words apart: the 8 rows of a matrix load lie in different banks
     static constexpr int RS = HDP * 2 + 16;
@@ -86,6 +92,7 @@ __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_mma_kernel(AttnArgs a)
 {
     constexpr int HDP = V::HDP, MT = V::MT, KT = V::KT, STAGES = V::STAGES, RS = V::RS;
     constexpr int KS = HDP / 16, NT = KT / 8, DT = HDP / 8;
+    constexpr uint32_t FULL = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned char *mine = smem + warp * V::WARP_BYTES;
@@ -112,39 +119,64 @@ __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_mma_kernel(AttnArgs a)
         const int n_tiles = (p.t1 - p.t0 + KT - 1) / KT;
         const int64_t head = p.head * a.head_stride;
         const int32_t *row = a.table + p.seq * a.table_stride;
-        // the page of this lane's token of tile i, loaded a tile before it is needed
-        auto page_of = [&](int i) {
-            const int t = p.t0 + i * KT + lane;
-            return lane < KT && t < p.t1 ? row[t / a.page] : -1;
-        };
-        auto fetch = [&](int i, int pg) {
-            const int st = i % STAGES;
-            const int t = p.t0 + i * KT + lane;
+        // lane < KT: this lane's token of the tile to be looked up next, its page's column and its
+        // place in the page; the page itself is loaded a tile before it is needed
+        int t = p.t0 + lane, col = t / a.page, off = t % a.page;
+        auto look_up = [&](int &pg, int &place) {
             const bool in = lane < KT && t < p.t1;
-            const bool ok = in && pg >= 0 && pg < a.n_pages;
-            if (in && !ok) raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
-            const int64_t at = ok ? pg * a.page_stride + (t % a.page) * a.tok_stride + head : -1;
+            pg = in ? row[col] : -2;
+            place = off;
+            t += KT;
+            off += KT;
+            while (off >= a.page) {
+                off -= a.page;
+                ++col;
+            }
+        };
+        auto fetch = [&](int i, int pg, int place) {
+            const int st = i % STAGES;
+            const bool ok = pg >= 0 && pg < a.n_pages;
+            if (!ok && pg != -2) raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
+            const int64_t at = ok ? pg * a.page_stride + place * a.tok_stride + head : -1;
             const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
             if (lane == 0) valid[st] = mask;
             const uint32_t kd = ring + st * 2 * V::TILE + r0 * RS + c * 16, vd = kd + V::TILE;
+            constexpr int STEP = 32 / V::LPR;
+            // a whole tile inside one page: its rows are tok_stride apart
+            if (mask == FULL && __shfl_sync(0xFFFFFFFFu, place, 0) + KT <= a.page) {
+                const int64_t o = __shfl_sync(0xFFFFFFFFu, at, 0) + r0 * a.tok_stride;
+                if (copies) {
+                    const uint16_t *ks = kb + o, *vs = vb + o;
 #pragma unroll
-            for (int j = 0; j < KT * V::LPR / 32; ++j) {
-                const int r = j * (32 / V::LPR) + r0;
-                const int64_t o = __shfl_sync(0xFFFFFFFFu, at, r);
+                    for (int j = 0; j < KT / STEP; ++j) {
+                        cp16(kd + j * STEP * RS, ks);
+                        cp16(vd + j * STEP * RS, vs);
+                        ks += STEP * a.tok_stride;
+                        vs += STEP * a.tok_stride;
+                    }
+                }
+                return;
+            }
+#pragma unroll
+            for (int j = 0; j < KT / STEP; ++j) {
+                const int64_t o = __shfl_sync(0xFFFFFFFFu, at, j * STEP + r0);
                 if (copies) {
                     const int bytes = o >= 0 ? 16 : 0;
-                    cp16(kd + j * (32 / V::LPR) * RS, kb + (o >= 0 ? o : 0), bytes);
-                    cp16(vd + j * (32 / V::LPR) * RS, vb + (o >= 0 ? o : 0), bytes);
+                    cp16_or_zero(kd + j * STEP * RS, kb + (o >= 0 ? o : 0), bytes);
+                    cp16_or_zero(vd + j * STEP * RS, vb + (o >= 0 ? o : 0), bytes);
                 }
             }
         };
-        int pg = page_of(0);
+        int pg, place;
+        look_up(pg, place);
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) {
-            const int nx = page_of(i + 1);
-            if (i < n_tiles) fetch(i, pg);
+            int pg2, place2;
+            look_up(pg2, place2);
+            if (i < n_tiles) fetch(i, pg, place);
             cp_commit();
-            pg = nx;
+            pg = pg2;
+            place = place2;
         }
         // the query rows, zeros past the last one
         uint32_t qf[V::QREG ? MT : 1][V::QREG ? KS : 1][4];
@@ -177,85 +209,118 @@ __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_mma_kernel(AttnArgs a)
             m[mt][0] = m[mt][1] = -INFINITY;
             l[mt][0] = l[mt][1] = 0.f;
         }
-        const int used = MT == 1 || p.rows <= 16 ? 1 : MT;
-
-        for (int i = 0; i < n_tiles; ++i) {
-            cp_wait<STAGES - 2>();
-            __syncwarp();
-            const int st = i % STAGES;
+        // one tile's scores, weights and products for the first U tiles of query rows
+        auto tile = [&](auto u_, int st) {
+            constexpr int U = decltype(u_)::value;
             const uint32_t kt = ring + st * 2 * V::TILE, vt = kt + V::TILE;
             const uint32_t mask = valid[st];
-            uint32_t ph[MT][NT][2], pl[MT][NT][2];
-            // scores and weights
+            // with one tile of rows the even and odd steps add up apart: four sums in flight, not two
+            constexpr int C = U == 1 ? 2 : 1;
+            float s[U][C][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (mt >= used) break;
-                float s[NT][4];
+            for (int mt = 0; mt < U; ++mt)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int x = 0; x < C; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+                    for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t q4[4];
+                        for (int e = 0; e < 4; ++e) s[mt][x][j][e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t q4[U][4];
+#pragma unroll
+                for (int mt = 0; mt < U; ++mt) {
                     if constexpr (V::QREG) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) q4[e] = qf[mt][ks][e];
+                        for (int e = 0; e < 4; ++e) q4[mt][e] = qf[mt][ks][e];
                     } else {
-                        ldsm4(q4, qs + mt * 16 * RS + v_off + ks * 32);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; j += 2) {
-                        uint32_t b[4];
-                        ldsm4(b, kt + j * 8 * RS + k_off + ks * 32);
-                        mma16816<F16>(s[j], q4, b[0], b[1]);
-                        mma16816<F16>(s[j + 1], q4, b[2], b[3]);
+                        ldsm4(q4[mt], qs + mt * 16 * RS + v_off + ks * 32);
                     }
                 }
-                float mx[2] = {-INFINITY, -INFINITY};
-                const bool all = mask == (KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u);
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t b[4];
+                    ldsm4(b, kt + j * 8 * RS + k_off + ks * 32);
+#pragma unroll
+                    for (int mt = 0; mt < U; ++mt) {
+                        mma16816<F16>(s[mt][ks % C][j], q4[mt], b[0], b[1]);
+                        mma16816<F16>(s[mt][ks % C][j + 1], q4[mt], b[2], b[3]);
+                    }
+                }
+            }
+            uint32_t ph[U][NT][2], pl[U][NT][2];
+            float mx[U][2];
+#pragma unroll
+            for (int mt = 0; mt < U; ++mt) {
+                mx[mt][0] = mx[mt][1] = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[j][e] *= a.scale_log2;
-                        if (!all && !((mask >> (j * 8 + (lane & 3) * 2 + (e & 1))) & 1u)) s[j][e] = -INFINITY;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], s[j][e]);
+                        if constexpr (C == 2) s[mt][0][j][e] += s[mt][1][j][e];
+                        s[mt][0][j][e] *= a.scale_log2;
                     }
-                float f[2];
+            }
+            if (mask != FULL) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((mask >> (j * 8 + (lane & 3) * 2 + (e & 1))) & 1u))
+#pragma unroll
+                            for (int mt = 0; mt < U; ++mt) s[mt][0][j][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int mt = 0; mt < U; ++mt) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[mt][e >> 1] = fmaxf(mx[mt][e >> 1], s[mt][0][j][e]);
+            }
+            float f[U][2];
+            bool rose = false;
+#pragma unroll
+            for (int mt = 0; mt < U; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
-                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
-                    mx[h] = fmaxf(mx[h], m[mt][h]);
-                    const float z = mx[h] == -INFINITY ? 0.f : mx[h];
-                    f[h] = ex2_approx(m[mt][h] - z);
-                    m[mt][h] = mx[h];
-                    mx[h] = z;
+                    float x = mx[mt][h];
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                    x = fmaxf(x, m[mt][h]);
+                    const float z = x == -INFINITY ? 0.f : x;
+                    f[mt][h] = ex2_approx(m[mt][h] - z);
+                    rose |= f[mt][h] != 1.f;
+                    m[mt][h] = x;
+                    mx[mt][h] = z;
                 }
-                // the outputs are rescaled only where some row's maximum rose
-                if (__any_sync(0xFFFFFFFFu, f[0] != 1.f || f[1] != 1.f)) {
-                    l[mt][0] *= f[0];
-                    l[mt][1] *= f[1];
+            // the outputs are rescaled only where some row's maximum rose
+            if (__any_sync(0xFFFFFFFFu, rose)) {
+#pragma unroll
+                for (int mt = 0; mt < U; ++mt) {
+                    l[mt][0] *= f[mt][0];
+                    l[mt][1] *= f[mt][1];
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
-                        o[mt][d][0] *= f[0];
-                        o[mt][d][1] *= f[0];
-                        o[mt][d][2] *= f[1];
-                        o[mt][d][3] *= f[1];
+                        o[mt][d][0] *= f[mt][0];
+                        o[mt][d][1] *= f[mt][0];
+                        o[mt][d][2] *= f[mt][1];
+                        o[mt][d][3] *= f[mt][1];
                     }
                 }
+            }
+#pragma unroll
+            for (int mt = 0; mt < U; ++mt)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float x = ex2_approx(s[j][2 * h] - mx[h]), y = ex2_approx(s[j][2 * h + 1] - mx[h]);
+                        const float x = ex2_approx(s[mt][0][j][2 * h] - mx[mt][h]);
+                        const float y = ex2_approx(s[mt][0][j][2 * h + 1] - mx[mt][h]);
                         l[mt][h] += x + y;
                         const uint32_t hi = pack_16x2<F16>(x, y);
                         ph[mt][j][h] = hi;
                         pl[mt][j][h] = pack_16x2<F16>(x - h16_lo<F16>(hi), y - h16_hi<F16>(hi));
                     }
-            }
             // weights times values
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
@@ -264,8 +329,7 @@ __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_mma_kernel(AttnArgs a)
                     uint32_t b[4];
                     ldsm4_t(b, vt + kk * 16 * RS + v_off + d * 16);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if (mt >= used) break;
+                    for (int mt = 0; mt < U; ++mt) {
                         const uint32_t hi[4] = {ph[mt][2 * kk][0], ph[mt][2 * kk][1], ph[mt][2 * kk + 1][0],
                                                 ph[mt][2 * kk + 1][1]};
                         const uint32_t lo[4] = {pl[mt][2 * kk][0], pl[mt][2 * kk][1], pl[mt][2 * kk + 1][0],
@@ -276,11 +340,20 @@ __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_mma_kernel(AttnArgs a)
                         mma16816<F16>(o[mt][d + 1], lo, b[2], b[3]);
                     }
                 }
+        };
+        const int used = MT == 1 || p.rows <= 16 ? 1 : MT;
+        for (int i = 0; i < n_tiles; ++i) {
+            cp_wait<STAGES - 2>();
             __syncwarp();
-            const int nx = page_of(i + STAGES);
-            if (i + STAGES - 1 < n_tiles) fetch(i + STAGES - 1, pg);
+            if (MT == 1 || used == 1) tile(std::integral_constant<int, 1>(), i % STAGES);
+            else tile(std::integral_constant<int, MT>(), i % STAGES);
+            __syncwarp();
+            int pg2, place2;
+            look_up(pg2, place2);
+            if (i + STAGES - 1 < n_tiles) fetch(i + STAGES - 1, pg, place);
             cp_commit();
-            pg = nx;
+            pg = pg2;
+            place = place2;
         }
         cp_wait<0>();
 #pragma unroll
