@@ -47,7 +47,7 @@ __device__ __forceinline__ int tiles_of(int n, int kt) { return (n + kt - 1) / k
 // a warp about as long as ITEM_COST tiles; counting it so keeps runs of many
 // short items from lagging behind.  An item's units are ITEM_COST for its
 // start, then one per tile.
-constexpr int ITEM_COST = 4;
+constexpr int ITEM_COST = 6;
 __device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + ITEM_COST : 0; }
 
 // Units of a group's shared part, per item.
@@ -67,13 +67,62 @@ __device__ __forceinline__ long long group_units(const AttnArgs &a, int g)
     return u;
 }
 
-// The run of units of warp w of nw, and the warp that has unit u.
-__device__ __forceinline__ long long run_start(long long units, int nw, int w) { return units * w / nw; }
-__device__ __forceinline__ int warp_of(long long units, int nw, long long u)
+// Groups whose prefix sum a block keeps in shared memory; more take attn_plan.
+constexpr int BASE_GROUPS = 1024;
+constexpr int BASE_BYTES = 10 * 1024;              // that array and some to spare
+
+// Exclusive prefix sum of the groups' units into out[0 .. n_group], by the whole
+// block; s_warp holds one value per warp.
+__device__ __forceinline__ void sum_units(const AttnArgs &a, long long *out, long long *s_warp)
 {
-    return static_cast<int>(((u + 1) * nw - 1) / units);
+    const int t = threadIdx.x, lane = t & 31, nt = blockDim.x;
+    long long done = 0;
+    for (int base = 0; base < a.n_group; base += nt) {
+        const int g = base + t;
+        const long long x = g < a.n_group ? group_units(a, g) : 0;
+        long long inc = x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[t >> 5] = inc;
+        __syncthreads();
+        long long before = 0, all = 0;
+        for (int w = 0; w < nt / 32; ++w) {
+            if (w < (t >> 5)) before += s_warp[w];
+            all += s_warp[w];
+        }
+        if (g < a.n_group) out[g] = done + before + inc - x;
+        done += all;
+    }
+    if (t == 0) out[a.n_group] = done;
+    __syncthreads();
 }
-__device__ __forceinline__ int warps_used(long long units, int nw) { return units < nw ? static_cast<int>(units) : nw; }
+// Lengths out of range leave their fault (they count as 0 everywhere).
+__device__ __forceinline__ void check_lens(const AttnArgs &a)
+{
+    for (int s = threadIdx.x; s < a.n_group * a.share; s += blockDim.x)
+        if (a.lens[s] < 0 || a.lens[s] > static_cast<int64_t>(a.max_pages) * a.page)
+            raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
+}
+
+// The units before each group, for the split pass: summed by every block for
+// itself (block 0 also leaves them to the join) unless attn_plan already did.
+__device__ __forceinline__ const long long *unit_bases(const AttnArgs &a, long long *s_base)
+{
+    __shared__ long long s_warp[32];
+    // what share or plan left is complete after the wait (the join is not let in early: its blocks,
+    // resident and waiting, cost the pass 2.5 us)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.n_group > BASE_GROUPS) return a.base;
+    sum_units(a, s_base, s_warp);
+    if (blockIdx.x == 0) {
+        check_lens(a);
+        for (int g = threadIdx.x; g <= a.n_group; g += blockDim.x) a.base[g] = s_base[g];
+    }
+    return s_base;
+}
 
 // a / b, mostly in 32 bits (a 64-bit division is a long routine).
 __device__ __forceinline__ int quotient(long long a, int b)
@@ -81,6 +130,15 @@ __device__ __forceinline__ int quotient(long long a, int b)
     return a <= 0xFFFFFFFFll ? static_cast<int>(static_cast<unsigned>(a) / static_cast<unsigned>(b))
                              : static_cast<int>(a / b);
 }
+
+// The run of units of warp w of nw, and the warp that has unit u.
+__device__ __forceinline__ long long run_start(long long units, int nw, int w) { return units * w / nw; }
+__device__ __forceinline__ int warp_of(long long units, int nw, long long u)
+{
+    const long long x = (u + 1) * nw - 1;
+    return units <= 0x7FFFFFFF ? quotient(x, static_cast<int>(units)) : static_cast<int>(x / units);
+}
+__device__ __forceinline__ int warps_used(long long units, int nw) { return units < nw ? static_cast<int>(units) : nw; }
 
 // One item's piece as a warp computes it.
 struct Piece {
@@ -103,10 +161,11 @@ __device__ __forceinline__ int row_head(const AttnArgs &a, const Piece &p, int i
     return p.head * a.group + (p.first_row + i) % a.group;
 }
 
-// Walks warp w's run; body(piece) computes each piece.
-template <typename F> __device__ __forceinline__ void walk_run(const AttnArgs &a, int w, F &&body)
+// Walks run w; body(piece) computes each piece.
+template <typename F>
+__device__ __forceinline__ void walk_run(const AttnArgs &a, const long long *base, int w, F &&body)
 {
-    const long long units = a.base[a.n_group];
+    const long long units = base[a.n_group];
     const int nw = warps_used(units, a.nw);
     if (w >= nw) return;
     long long u = run_start(units, nw, w);
@@ -114,13 +173,13 @@ template <typename F> __device__ __forceinline__ void walk_run(const AttnArgs &a
     int g = 0;
     for (int lo = 0, hi = a.n_group; hi - lo > 1;) {
         const int mid = (lo + hi) >> 1;
-        if (a.base[mid] <= u) lo = mid;
+        if (base[mid] <= u) lo = mid;
         else hi = mid;
         g = lo;
     }
     while (u < u1) {
-        while (a.base[g + 1] <= u) ++g;
-        long long in = u - a.base[g];
+        while (base[g + 1] <= u) ++g;
+        long long in = u - base[g];
         const int ts = shared_tiles(a, g), us = units_of(ts);
         const long long su = static_cast<long long>(us) * a.n_kv * a.cs;
         Piece p;
@@ -180,6 +239,25 @@ __device__ __forceinline__ int64_t token_at(const AttnArgs &a, int seq, int j)
         return -1;
     }
     return p * a.page_stride + (j % a.page) * a.tok_stride;
+}
+
+// A launch that may begin before the kernel ahead of it in the stream has
+// ended (`after`: that kernel is one of the same call); the kernel waits with
+// griddepcontrol.wait before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(bool after, void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 } // namespace lossk

@@ -150,7 +150,7 @@ struct AttnArgs {
     int kt, mr;                                    // tokens per unit, query rows per item
     int cs, cp;                                    // items per KV head: of a group's shared part, of a sequence
     int ra, rb;                                    // rows a partial result holds, shared and private
-    int nw;                                        // warps at most
+    int nw;                                        // runs at most
     int32_t *shared;                               // [n_group] shared tokens
     long long *base;                               // [n_group + 1] units before each group
     float *part_a, *part_b;                        // partial results per row: o[hd], m (log2 units), l, and 2 unused
@@ -158,14 +158,15 @@ struct AttnArgs {
 };
 
 // The kernel that takes this type, head size and number of query rows per KV
-// head: rows per item, tokens per unit, warps a block (one block per SM).
+// head: rows per item, tokens per unit, runs a block walks (one block per SM).
 struct AttnShape {
-    int mr, kt, warps;
+    int mr, kt, runs;
 };
-constexpr int ATTN_MAX_MR = 32;
-constexpr int ATTN_MAX_WARPS = 152 * 8;
+constexpr int ATTN_MAX_ROWS = 152 * 12 * 16;       // runs x rows per item: a block has at most 12 warps of 16 rows
 constexpr int ATTN_ROW = 4;            // floats a partial row holds beside o
 AttnShape attn_shape(int dtype, int hd, int rows);
+// Whether the split pass needs attn_share or attn_plan ahead of it.
+bool attn_plans(const AttnArgs &a);
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st);
 // The tensor-core kernel (16-bit types).

@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(PLAN_T) attn_share_kernel(AttnArgs a)
 {
     __shared__ int s_first, s_min, s_max;
     const int g = blockIdx.x, t = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (t == 0) {
         int mn = 1 << 30, mx = 0;
         for (int i = 0; i < a.share; ++i) {
@@ -69,38 +70,15 @@ __global__ void __launch_bounds__(PLAN_T) attn_share_kernel(AttnArgs a)
     if (t == 0) a.shared[g] = (s_first < full ? s_first : full) * a.page;
 }
 
-// One block: the units before each group (a prefix sum), base[n_group] their number.
+// One block: the units before each group, where they are too many for every
+// block of the split pass to sum up for itself.
 __global__ void __launch_bounds__(PLAN_T) attn_plan_kernel(AttnArgs a)
 {
     __shared__ long long s_warp[PLAN_T / 32];
-    const int t = threadIdx.x, lane = t & 31;
-    long long done = 0;
-    for (int base = 0; base < a.n_group; base += PLAN_T) {
-        const int g = base + t;
-        const long long x = g < a.n_group ? group_units(a, g) : 0;
-        if (g < a.n_group)
-            for (int i = 0; i < a.share; ++i) {
-                const int n = a.lens[g * a.share + i];
-                if (n < 0 || n > static_cast<int64_t>(a.max_pages) * a.page)
-                    raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
-            }
-        long long inc = x;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        __syncthreads();
-        if (lane == 31) s_warp[t >> 5] = inc;
-        __syncthreads();
-        long long before = 0, all = 0;
-        for (int w = 0; w < PLAN_T / 32; ++w) {
-            if (w < (t >> 5)) before += s_warp[w];
-            all += s_warp[w];
-        }
-        if (g < a.n_group) a.base[g] = done + before + inc - x;
-        done += all;
-    }
-    if (t == 0) a.base[a.n_group] = done;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    check_lens(a);
+    sum_units(a, a.base, s_warp);
 }
 
 // ---- CUDA cores ---------------------------------------------------------------------
@@ -110,8 +88,10 @@ constexpr int SIMT_MR = 4;
 
 template <typename T> __global__ void __launch_bounds__(ATTN_WARPS * 32) attn_simt_kernel(AttnArgs a)
 {
+    __shared__ long long s_base[BASE_GROUPS + 1];
+    const long long *base = unit_bases(a, s_base);
     const int lane = threadIdx.x & 31, w = blockIdx.x * ATTN_WARPS + (threadIdx.x >> 5);
-    walk_run(a, w, [&](const Piece &p) {
+    walk_run(a, base, w, [&](const Piece &p) {
         float q[SIMT_MR][8], o[SIMT_MR][8], m[SIMT_MR], l[SIMT_MR];
         for (int i = 0; i < SIMT_MR; ++i) {
             m[i] = -INFINITY;
@@ -167,31 +147,32 @@ template <typename T> __global__ void __launch_bounds__(ATTN_WARPS * 32) attn_si
 }
 
 // ---- joining -----------------------------------------------------------------------
-// One block per output row: the row's pieces, from the group's shared tokens
-// and from its own, weighted by e^(m - M).  A row that one piece covers was
-// written by it.
-template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(AttnArgs a)
+// An output row's pieces, from its group's shared tokens and from its own,
+// weighted by e^(m - M).  A row that one piece covers was written by it.
+struct RowPieces {
+    const float *pa, *pb;       // this row of the first shared and the first own piece
+    int64_t sa, sb;             // floats from piece to piece
+    int n_a, n;
+    __device__ __forceinline__ const float *at(int i) const { return i < n_a ? pa + i * sa : pb + (i - n_a) * sb; }
+};
+__device__ __forceinline__ RowPieces row_pieces(const AttnArgs &a, int s, int hq)
 {
-    __shared__ __align__(16) float s_o[JOIN_WARPS][256];
-    __shared__ float s_w[JOIN_W], s_x[JOIN_WARPS], s_l[JOIN_WARPS];
-    const int s = blockIdx.x / a.n_q, hq = blockIdx.x % a.n_q, g = s / a.share;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int head = hq / a.group, r = hq % a.group;
+    const int g = s / a.share, head = hq / a.group, r = hq % a.group;
     const long long units = a.base[a.n_group];
     const int nw = warps_used(units, a.nw);
     const int ts = shared_tiles(a, g);
     const Span own = attn_span(a, s, g);
     const int tp = tiles_of(own.hi - own.mid, a.kt);
-    // the pieces: n_a of the shared item (from slot a0 on), then n_b of its own
     const int ri = (s % a.share) * a.group + r, ca = ri / a.mr, cb = r / a.mr;
-    int n_a = 0, n_b = 0;
-    int64_t a0 = 0, b0 = 0;
+    const int64_t stride = a.hd + ATTN_ROW;
+    RowPieces p{nullptr, nullptr, a.ra * stride, a.rb * stride, 0, 0};
     if (ts > 0) {
         const long long u = a.base[g] + (static_cast<long long>(head) * a.cs + ca) * units_of(ts) + ITEM_COST;
         const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + ts - 1);
-        n_a = w1 - w0 + 1;
-        a0 = (static_cast<int64_t>(g) * a.n_kv + head) * a.cs + ca + w0;
+        p.n_a = w1 - w0 + 1;
+        p.pa = a.part_a + (((static_cast<int64_t>(g) * a.n_kv + head) * a.cs + ca + w0) * a.ra + ri % a.mr) * stride;
     }
+    p.n = p.n_a;
     if (tp > 0) {
         long long u = a.base[g] + static_cast<long long>(units_of(ts)) * a.n_kv * a.cs;
         for (int i = g * a.share; i < s; ++i) {
@@ -200,19 +181,90 @@ template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_
         }
         u += (static_cast<long long>(head) * a.cp + cb) * units_of(tp) + ITEM_COST;
         const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + tp - 1);
-        n_b = w1 - w0 + 1;
-        b0 = (static_cast<int64_t>(s) * a.n_kv + head) * a.cp + cb + w0;
+        p.n += w1 - w0 + 1;
+        p.pb = a.part_b + (((static_cast<int64_t>(s) * a.n_kv + head) * a.cp + cb + w0) * a.rb + r % a.mr) * stride;
     }
-    if (n_a == 0 && n_b == 1) return;
-    const int n = n_a + n_b;
-    const int64_t stride = a.hd + ATTN_ROW;
-    const float *pa = a.part_a + (a0 * a.ra + ri % a.mr) * stride, *pb = a.part_b + (b0 * a.rb + r % a.mr) * stride;
-    const int64_t sa = a.ra * stride, sb = a.rb * stride;
-    auto piece = [&](int i) { return i < n_a ? pa + i * sa : pb + (i - n_a) * sb; };
-    // the largest m, then each piece's weight e^(m - M), kept for the first JOIN_W pieces
+    if (p.n_a == 0 && p.n == 1) p.n = -1;
+    return p;
+}
+
+// The weighted sum of pieces i0, i0 + step, ...: a lane holds elements 4 lane..
+// and 128 + 4 lane..
+struct RowSum {
+    float4 o[2];
+    float l;
+};
+template <typename W>
+__device__ __forceinline__ RowSum sum_pieces(const RowPieces &p, int hd, int i0, int step, int lane, W &&weight)
+{
+    RowSum r = {};
+    const int words = hd >> 2;
+#pragma unroll 4
+    for (int i = i0; i < p.n; i += step) {
+        const float *d = p.at(i);
+        const float f = weight(i, d);
+        r.l += f * d[hd + 1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (lane + 32 * h < words) {
+                const float4 x = *reinterpret_cast<const float4 *>(d + 4 * (lane + 32 * h));
+                r.o[h].x += f * x.x;
+                r.o[h].y += f * x.y;
+                r.o[h].z += f * x.z;
+                r.o[h].w += f * x.w;
+            }
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void put_row(const AttnArgs &a, int64_t row, int lane, const RowSum &r, float mz)
+{
+    const float inv = r.l > 0.f ? 1.f / r.l : 1.f;
+    T *out = static_cast<T *>(a.out) + row * a.hd;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = 4 * (lane + 32 * h);
+        if (e < a.hd) {
+            attn_put(out + e, r.o[h].x * inv);
+            attn_put(out + e + 1, r.o[h].y * inv);
+            attn_put(out + e + 2, r.o[h].z * inv);
+            attn_put(out + e + 3, r.o[h].w * inv);
+        }
+    }
+    if (a.lse && lane == 0) a.lse[row] = mz * float(LN2) + logf(r.l);
+}
+
+// A warp per output row: many rows, of few pieces each.
+template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_rows_kernel(AttnArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * JOIN_WARPS + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (row >= static_cast<int64_t>(a.n_group) * a.share * a.n_q) return;
+    const RowPieces p = row_pieces(a, static_cast<int>(row / a.n_q), static_cast<int>(row % a.n_q));
+    if (p.n < 0) return;
     float M = -INFINITY;
-    for (int i = t; i < n; i += JOIN_THREADS) {
-        const float m = piece(i)[a.hd];
+    for (int i = lane; i < p.n; i += 32) M = fmaxf(M, p.at(i)[a.hd]);
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    const float mz = M == -INFINITY ? 0.f : M;
+    const RowSum r = sum_pieces(p, a.hd, 0, 1, lane, [&](int, const float *d) { return exp2f(d[a.hd] - mz); });
+    put_row<T>(a, row, lane, r, mz);
+}
+
+// A block per output row: few rows, cut into many pieces.
+template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(AttnArgs a)
+{
+    __shared__ float4 s_o[JOIN_WARPS][64];
+    __shared__ float s_w[JOIN_W], s_x[JOIN_WARPS], s_l[JOIN_WARPS];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const RowPieces p = row_pieces(a, blockIdx.x / a.n_q, blockIdx.x % a.n_q);
+    if (p.n < 0) return;
+    // the largest m; the pieces' m are kept for the weights
+    float M = -INFINITY;
+    for (int i = t; i < p.n; i += JOIN_THREADS) {
+        const float m = p.at(i)[a.hd];
         if (i < JOIN_W) s_w[i] = m;
         M = fmaxf(M, m);
     }
@@ -221,40 +273,35 @@ template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_
     __syncthreads();
     for (int i = 0; i < JOIN_WARPS; ++i) M = fmaxf(M, s_x[i]);
     const float mz = M == -INFINITY ? 0.f : M;
-    // each warp adds up its share of the pieces, a lane holding elements 4 lane.. and 128 + 4 lane..
-    float4 acc[2] = {};
-    float L = 0.f;
-    const int words = a.hd >> 2;
-#pragma unroll 4
-    for (int i = warp; i < n; i += JOIN_WARPS) {
-        const float *d = piece(i);
-        const float f = exp2f((i < JOIN_W ? s_w[i] : d[a.hd]) - mz);
-        L += f * d[a.hd + 1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (lane + 32 * h < words) {
-                const float4 x = *reinterpret_cast<const float4 *>(d + 4 * (lane + 32 * h));
-                acc[h].x += f * x.x;
-                acc[h].y += f * x.y;
-                acc[h].z += f * x.z;
-                acc[h].w += f * x.w;
-            }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (lane + 32 * h < words) *reinterpret_cast<float4 *>(&s_o[warp][4 * (lane + 32 * h)]) = acc[h];
-    if (lane == 0) s_l[warp] = L;
+    RowSum r = sum_pieces(p, a.hd, warp, JOIN_WARPS, lane,
+                          [&](int i, const float *d) { return exp2f((i < JOIN_W ? s_w[i] : d[a.hd]) - mz); });
+    s_o[warp][lane] = r.o[0];
+    s_o[warp][lane + 32] = r.o[1];
+    if (lane == 0) s_l[warp] = r.l;
     __syncthreads();
-    L = 0.f;
-    for (int i = 0; i < JOIN_WARPS; ++i) L += s_l[i];
-    const float inv = L > 0.f ? 1.f / L : 1.f;
-    const int64_t row = static_cast<int64_t>(s) * a.n_q + hq;
-    for (int e = t; e < a.hd; e += JOIN_THREADS) {
-        float x = 0.f;
-        for (int i = 0; i < JOIN_WARPS; ++i) x += s_o[i][e];
-        attn_put(static_cast<T *>(a.out) + row * a.hd + e, x * inv);
+    if (warp) return;
+    for (int i = 1; i < JOIN_WARPS; ++i) {
+        r.l += s_l[i];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 x = s_o[i][lane + 32 * h];
+            r.o[h].x += x.x;
+            r.o[h].y += x.y;
+            r.o[h].z += x.z;
+            r.o[h].w += x.w;
+        }
     }
-    if (a.lse && t == 0) a.lse[row] = mz * float(LN2) + logf(L);
+    put_row<T>(a, blockIdx.x, lane, r, mz);
+}
+
+template <typename T> cudaError_t launch_join(const AttnArgs &a, cudaStream_t st)
+{
+    const int64_t rows = static_cast<int64_t>(a.n_group) * a.share * a.n_q;
+    // a block per row while all blocks fit at once (8 per SM): 1056 rows of up to 28 pieces took
+    // 7 us less than a warp per row, 2048 rows of 2 to 14 pieces 10 us more
+    if (rows <= 8 * 152) return launch_after(true, attn_join_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(JOIN_THREADS), 0, st, a);
+    return launch_after(true, attn_join_rows_kernel<T>, dim3(static_cast<unsigned>((rows + JOIN_WARPS - 1) / JOIN_WARPS)),
+                        dim3(JOIN_THREADS), 0, st, a);
 }
 
 } // namespace
@@ -265,26 +312,27 @@ AttnShape attn_shape(int dtype, int hd, int rows)
     return AttnShape{SIMT_MR, 32, 8};
 }
 
+bool attn_plans(const AttnArgs &a) { return a.share > 1 || a.n_group > BASE_GROUPS; }
+
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st)
 {
-    if (a.share > 1) attn_share_kernel<<<static_cast<unsigned>(a.n_group), PLAN_T, 0, st>>>(a);
-    attn_plan_kernel<<<1, PLAN_T, 0, st>>>(a);
-    return cudaGetLastError();
+    if (a.share > 1) {
+        attn_share_kernel<<<static_cast<unsigned>(a.n_group), PLAN_T, 0, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess || a.n_group <= BASE_GROUPS) return e;
+    }
+    return launch_after(a.share > 1, attn_plan_kernel, dim3(1), dim3(PLAN_T), 0, st, a);
 }
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st)
 {
-    const unsigned grid = static_cast<unsigned>((a.nw + ATTN_WARPS - 1) / ATTN_WARPS);
     if (dtype != LOSSK_F32) return launch_attn_mma(dtype == LOSSK_F16, a, st);
-    attn_simt_kernel<float><<<grid, ATTN_WARPS * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    const unsigned grid = static_cast<unsigned>((a.nw + ATTN_WARPS - 1) / ATTN_WARPS);
+    return launch_after(attn_plans(a), attn_simt_kernel<float>, dim3(grid), dim3(ATTN_WARPS * 32), 0, st, a);
 }
 cudaError_t launch_attn_join(int dtype, const AttnArgs &a, cudaStream_t st)
 {
-    const unsigned grid = static_cast<unsigned>(a.n_group) * a.share * a.n_q;
-    if (dtype == LOSSK_F32) attn_join_kernel<float><<<grid, JOIN_THREADS, 0, st>>>(a);
-    else if (dtype == LOSSK_BF16) attn_join_kernel<uint16_t><<<grid, JOIN_THREADS, 0, st>>>(a);
-    else attn_join_kernel<h16_t><<<grid, JOIN_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    return dtype == LOSSK_F32 ? launch_join<float>(a, st)
+         : dtype == LOSSK_BF16 ? launch_join<uint16_t>(a, st) : launch_join<h16_t>(a, st);
 }
 
 } // namespace lossk

@@ -119,7 +119,7 @@ CopyArgs copy_args(void *pool, int64_t n_planes, int64_t plane_stride, int64_t p
 
 // The scratch of lossk_paged_attn.  Partial results take at most twice the query
 // rows on either side (a group's shared rows are cut into items of mr rows,
-// the last one less than full), and one item's rows more for each warp.
+// the last one less than full), and one item's rows more for each run.
 struct AttnLayout {
     size_t off_shared, off_base, off_part, total;
 };
@@ -132,7 +132,7 @@ int32_t attn_layout(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t hd, AttnLa
     L->off_shared = 256;
     L->off_base = align256(L->off_shared + sizeof(int32_t) * n_seq);
     L->off_part = align256(L->off_base + sizeof(long long) * (n_seq + 1));
-    const size_t rows = 4 * static_cast<size_t>(n_seq) * n_q + 2 * ATTN_MAX_MR * ATTN_MAX_WARPS;
+    const size_t rows = 4 * static_cast<size_t>(n_seq) * n_q + 2 * ATTN_MAX_ROWS;
     L->total = align256(L->off_part + sizeof(float) * rows * (hd + ATTN_ROW));
     return LOSSK_OK;
 }
@@ -571,17 +571,17 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
     a.cp = (a.group + a.mr - 1) / a.mr;
     a.ra = rows_s < a.mr ? rows_s : a.mr;
     a.rb = a.group < a.mr ? a.group : a.mr;
-    // no more warps than units there can be
+    // no more runs than units there can be
     const int64_t cap = max_len > 0 && max_len < max_pages * page_size ? max_len : max_pages * page_size;
     const int64_t units = n_seq * n_kv_heads * a.cp * ((cap + a.kt - 1) / a.kt + 1);
-    a.nw = static_cast<int>(units < 152 * shape.warps ? units : 152 * shape.warps);
+    a.nw = static_cast<int>(units < 152 * shape.runs ? units : 152 * shape.runs);
     a.shared = reinterpret_cast<int32_t *>(ws + L.off_shared);
     a.base = reinterpret_cast<long long *>(ws + L.off_base);
     a.part_a = reinterpret_cast<float *>(ws + L.off_part);
     a.part_b = a.part_a + (static_cast<int64_t>(a.n_group) * a.n_kv * a.cs + a.nw) * a.ra * (a.hd + ATTN_ROW);
     a.fault = fault_of(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    {
+    if (attn_plans(a)) {
         Launch k(KK_ATTN_PLAN, st);
         if (launch_attn_plan(a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
     }
