@@ -534,7 +534,7 @@ int64_t lossk_decode_workspace_bytes(int32_t kind, int64_t a, int64_t b, int64_t
  * finished or the token is end_token) and length_out int32 (len; with lengths
  * NULL it counts from 0).  lse_out float[batch beams] or NULL: lse_r, or
  * -infinity for a row without candidates of its own.
- * 1 <= beams <= 64 and n_out <= 128 (583).  temperature finite and > 0,
+ * 1 <= beams <= 64 and n_out <= 128 (583).  temperature in [1e-30, 1e30],
  * length_alpha finite (585). */
 int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out, int32_t dtype,
                           const void *logits, int64_t logits_len, int64_t row_stride, const float *scores,

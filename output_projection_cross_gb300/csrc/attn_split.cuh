@@ -3,6 +3,7 @@
 #pragma once
 #include "../../include/lossk.h"
 #include "decode_internal.h"
+#include "decode_launch.h"
 #include "ptx.cuh"
 
 namespace lossk {
@@ -239,25 +240,6 @@ __device__ __forceinline__ int64_t token_at(const AttnArgs &a, int seq, int j)
         return -1;
     }
     return p * a.page_stride + (j % a.page) * a.tok_stride;
-}
-
-// A launch that may begin before the kernel ahead of it in the stream has
-// ended (`after`: that kernel is one of the same call); the kernel waits with
-// griddepcontrol.wait before it touches memory.
-template <typename... P, typename... A>
-cudaError_t launch_after(bool after, void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 } // namespace lossk

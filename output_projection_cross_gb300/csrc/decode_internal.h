@@ -13,8 +13,8 @@ __device__ __forceinline__ void raise_fault(int *fault, int status) { atomicMax(
 // ---- beam selection ------------------------------------------------------------
 // What the rows kernel leaves per (row, split): the largest kept logit m, the
 // sum z of exp((x - m) / T) over the kept logits (NaN where one of them is a NaN
-// or +infinity), and the split's n_out best (logit, token) pairs in any order,
-// token -1 filling the places left.
+// or +infinity), and the split's n_out best (logit, token) pairs in falling
+// order, token -1 filling the places left.
 struct BeamStat {
     double z;
     float m;
@@ -28,7 +28,9 @@ struct BeamCand {
 struct BeamArgs {
     const void *logits;
     int64_t row_stride;
-    int batch, beams, vocab, n_out, n_split;
+    int dtype, batch, beams, vocab, n_out;
+    int n_split, split_len; // tokens a split has (the last one less)
+    int cap, merge_cap;     // keys the kernels' buffers hold
     float c_hi, c_lo;       // log2(e) / T as the sum of two floats
     double temperature;
     const uint32_t *allow;
@@ -49,9 +51,9 @@ struct BeamArgs {
     int *fault;
 };
 
-// Splits of a row: enough blocks for every SM, no split below 4096 tokens.
 int beam_splits(int64_t rows, int64_t vocab);
-cudaError_t launch_beam_rows(int dtype, const BeamArgs &a, cudaStream_t st);
+int beam_cap(int dtype, int n_out);
+cudaError_t launch_beam_rows(const BeamArgs &a, cudaStream_t st);
 cudaError_t launch_beam_merge(const BeamArgs &a, cudaStream_t st);
 cudaError_t launch_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t row_bytes,
                                const int32_t *parent, const void *src, void *dst, int *fault, cudaStream_t st);

@@ -23,8 +23,6 @@
 //    one, which the stream hides, for an output that is rounded once.
 #include "attn_split.cuh"
 
-#include <atomic>
-
 namespace lossk {
 
 namespace {
@@ -366,17 +364,9 @@ template <int HDP, int W> cudaError_t launch_variant(bool f16, const AttnArgs &a
 {
     using V = Variant<HDP, W>;
     constexpr int bytes = V::RINGS * V::RING_BYTES;
-    auto kern = f16 ? attn_mma_kernel<V, true> : attn_mma_kernel<V, false>;
-    // the shared-memory attribute is set once per device
-    static std::atomic<int> ready[2][64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = f16 ? raise_smem<attn_mma_kernel<V, true>>(bytes) : raise_smem<attn_mma_kernel<V, false>>(bytes);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !ready[f16][dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) ready[f16][dev].store(1, std::memory_order_release);
-    }
+    auto kern = f16 ? attn_mma_kernel<V, true> : attn_mma_kernel<V, false>;
     return launch_after(a.share > 1 || a.n_group > BASE_GROUPS, kern, dim3(a.nw < 152 ? a.nw : 152),
                         dim3(V::THREADS), bytes, st, a);
 }

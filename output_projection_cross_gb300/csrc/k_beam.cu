@@ -12,20 +12,29 @@
 // different beams may lie closer together than floats resolve.
 #include "../../include/lossk.h"
 #include "decode_internal.h"
+#include "decode_launch.h"
 #include "ptx.cuh"
+
+#include <type_traits>
 
 namespace lossk {
 
 namespace {
 
-constexpr int ROW_THREADS = 256;
-constexpr int MERGE_THREADS = 256;
+constexpr int NT = 256;                    // threads of a block, here throughout
+constexpr int WARPS = NT / 32;
 
-__device__ __forceinline__ float beam_f(float x) { return x + 0.f; }   // -0 to +0: they tie
-__device__ __forceinline__ float beam_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16) + 0.f; }
-__device__ __forceinline__ float beam_f(h16_t x) { return f16_to_f(x.bits) + 0.f; }
+// ---- the n best of many -----------------------------------------------------------
+// A block streams keys past a threshold into a buffer in shared memory.  The
+// threshold comes from the first chunk: cut the block into groups of threads;
+// the n-th largest of the groups' largest keys has n keys at or above it, so
+// nothing below it can be among the n best.  Keys are unique, so at most n
+// groups hold keys that pass.  When the buffer fills up, it is cut back to its
+// n best and the threshold raised to the last of them.
+//
+// A key orders by logit, then by falling token.  0 stands for none.
+using Key = uint64_t;
 
-// A float's order as an unsigned integer's (no NaN).
 __device__ __forceinline__ uint32_t order_of(float x)
 {
     const uint32_t b = __float_as_uint(x);
@@ -35,12 +44,192 @@ __device__ __forceinline__ float value_of(uint32_t o)
 {
     return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
-
-// (logit, token) as one key: the larger logit first, then the lower token.
-// 0 is below every key of a logit above -infinity.
-__device__ __forceinline__ uint64_t key_of(float x, int tok)
+__device__ __forceinline__ Key key_of(float x, int tok)
 {
     return (static_cast<uint64_t>(order_of(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(tok));
+}
+
+// The order of a rank (a double) and, among equals, of the lower flat index.
+struct RankKey {
+    uint64_t rank;          // order of the rank, 0: none
+    uint64_t flat;          // ~(beam * vocab + token)
+};
+__device__ __forceinline__ bool operator>(const RankKey &x, const RankKey &y)
+{
+    return x.rank > y.rank || (x.rank == y.rank && x.flat > y.flat);
+}
+__device__ __forceinline__ uint64_t order_of(double x)
+{
+    const uint64_t b = __double_as_longlong(x + 0.0);
+    return b >> 63 ? ~b : b | (1ull << 63);
+}
+__device__ __forceinline__ bool is_none(const Key &k) { return k == 0; }
+__device__ __forceinline__ bool is_none(const RankKey &k) { return k.rank == 0; }
+__device__ __forceinline__ Key shfl_xor(const Key &k, int o) { return __shfl_xor_sync(0xFFFFFFFFu, k, o); }
+__device__ __forceinline__ RankKey shfl_xor(const RankKey &k, int o)
+{
+    return RankKey{__shfl_xor_sync(0xFFFFFFFFu, k.rank, o), __shfl_xor_sync(0xFFFFFFFFu, k.flat, o)};
+}
+
+// Groups of threads a threshold is taken over: at least 4 n of them where
+// there are that many threads (fewer keys to rank; with 4 n groups about n / 7
+// keys more than n pass).
+__host__ __device__ constexpr int groups_for(int n) { return n <= 16 ? 64 : n <= 32 ? 128 : 256; }
+
+// The n-th largest of the groups' largest keys (none where fewer groups have
+// any).  All threads call it with their largest key; s_keys holds NT keys.
+template <typename K> __device__ __forceinline__ K nth_of_groups(K mine, int n, K *s_keys, K *s_nth)
+{
+    const int t = threadIdx.x, groups = groups_for(n), per = NT / groups;
+    for (int o = 1; o < per; o <<= 1) {
+        const K other = shfl_xor(mine, o);
+        if (other > mine) mine = other;
+    }
+    __syncthreads();
+    if (t == 0) *s_nth = K{};
+    if (t % per == 0) s_keys[t / per] = mine;
+    __syncthreads();
+    if (t < groups) {
+        mine = s_keys[t];
+        int above = 0;
+#pragma unroll 8
+        for (int i = 0; i < groups; ++i) above += s_keys[i] > mine;
+        if (above == n - 1 && !is_none(mine)) *s_nth = mine;
+    }
+    __syncthreads();
+    return *s_nth;
+}
+
+// The n best of buf[0 .. cnt), in falling order, into buf[0 ..); returns how
+// many there are.  tmp holds as many keys as buf.
+template <typename K>
+__device__ __forceinline__ int keep_best(K *buf, K *tmp, int cnt, int n, K *s_keys, K *s_nth, int *s_cnt)
+{
+    const int t = threadIdx.x;
+    K mine{};
+    for (int i = t; i < cnt; i += NT)
+        if (buf[i] > mine) mine = buf[i];
+    const K nth = nth_of_groups(mine, n, s_keys, s_nth);
+    if (t == 0) *s_cnt = 0;
+    __syncthreads();
+    for (int i = t; i < cnt; i += NT)
+        if (!(nth > buf[i])) tmp[atomicAdd(s_cnt, 1)] = buf[i];
+    __syncthreads();
+    const int left = *s_cnt;
+    for (int i = t; i < left; i += NT) {
+        const K k = tmp[i];
+        int above = 0;
+        for (int j = 0; j < left; ++j) above += tmp[j] > k;
+        if (above < n) buf[above] = k;
+    }
+    __syncthreads();
+    return left < n ? left : n;
+}
+
+// ---- rows --------------------------------------------------------------------------
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+    static constexpr int NV = 4;
+};
+template <> struct Elem<uint16_t> {
+    static constexpr int NV = 8;
+};
+template <> struct Elem<h16_t> {
+    static constexpr int NV = 8;
+};
+constexpr int U = 4;                       // 16-byte vectors a thread holds of a chunk
+
+__device__ __forceinline__ float beam_f(float x) { return x + 0.f; }   // -0 to +0: they tie
+__device__ __forceinline__ float beam_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16) + 0.f; }
+__device__ __forceinline__ float beam_f(h16_t x) { return f16_to_f(x.bits) + 0.f; }
+
+template <typename T> __device__ __forceinline__ void unpack(const uint4 &v, float *f)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = h16_lo<std::is_same<T, h16_t>::value>(w[i]);
+            f[2 * i + 1] = h16_hi<std::is_same<T, h16_t>::value>(w[i]);
+        }
+    }
+}
+
+// max that a NaN goes through
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+template <typename T> __device__ __forceinline__ uint32_t max_nan2(uint32_t x, uint32_t y)
+{
+    uint32_t r;
+    if constexpr (std::is_same<T, h16_t>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+// The largest of a vector (of 16-bit types two at a time, before they are unpacked).
+template <typename T> __device__ __forceinline__ float vec_max(const uint4 &v)
+{
+    if constexpr (sizeof(T) == 4) {
+        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                       max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+        constexpr bool F16 = std::is_same<T, h16_t>::value;
+        const uint32_t x = max_nan2<T>(max_nan2<T>(v.x, v.y), max_nan2<T>(v.z, v.w));
+        return max_nan(h16_lo<F16>(x), h16_hi<F16>(x));
+    }
+}
+
+// A running sum of exp((x - ref) / T): ref follows the largest logit only
+// once that is FAR above it (in log2 units), so a warp seldom rescales; z is
+// kept in two floats, sum and what its roundings lost.
+struct RowStat {
+    float m, ref, z, lost;
+};
+constexpr float FAR = 24.f;
+
+__device__ __forceinline__ float pow2_of(float d, const BeamArgs &a)
+{
+    return ex2_approx(fmaf(d, a.c_hi, d * a.c_lo));
+}
+__device__ __forceinline__ void add_z(RowStat &r, float x)
+{
+    const float s = r.z + x, b = s - r.z;
+    r.lost += (r.z - (s - b)) + (x - b);
+    r.z = s;
+}
+// One vector f of largest value lm.
+template <int NV> __device__ __forceinline__ void add_vec(RowStat &r, const float (&f)[NV], float lm, const BeamArgs &a)
+{
+    if (lm == -INFINITY) return;
+    r.m = max_nan(r.m, lm);
+    if (!((lm - r.ref) * a.c_hi < FAR)) {
+        const float g = r.ref == -INFINITY ? 0.f : pow2_of(r.ref - lm, a);
+        r.z *= g;
+        r.lost *= g;
+        r.ref = lm;
+    }
+    float e[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) e[i] = pow2_of(f[i] - r.ref, a);
+#pragma unroll
+    for (int s = NV / 2; s; s >>= 1)
+#pragma unroll
+        for (int i = 0; i < s; ++i) e[i] += e[i + s];
+    add_z(r, e[0]);
+}
+
+// 32 bits of a row's mask from token v on.
+__device__ __forceinline__ uint32_t allow_bits(const uint32_t *allow, int words, int v)
+{
+    const int w = v >> 5;
+    const uint32_t lo = __ldg(allow + w), hi = w + 1 < words ? __ldg(allow + w + 1) : 0u;
+    return __funnelshift_r(lo, hi, v & 31);
 }
 
 // Whether beam k of entry b has logits to read: not finished, a finite score.
@@ -49,193 +238,344 @@ __device__ __forceinline__ bool beam_reads(const BeamArgs &a, int r)
     return !(a.finished && a.finished[r]) && isfinite(a.scores[r]);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(ROW_THREADS) beam_rows_kernel(BeamArgs a)
+// Bytes [skew, skew + 16) of two vectors.
+__device__ __forceinline__ uint4 joined(uint4 x, uint4 y, int skew)
 {
-    __shared__ uint64_t s_key[ROW_THREADS / 32];
-    __shared__ double s_z[ROW_THREADS / 32];
-    __shared__ float s_m[ROW_THREADS / 32];
+    if (skew & 8) {
+        x = make_uint4(x.z, x.w, y.x, y.y);
+        y.x = y.z;
+        y.y = y.w;
+    }
+    if (skew & 4) {
+        x = make_uint4(x.y, x.z, x.w, y.x);
+        y.x = y.y;
+    }
+    const int bits = (skew & 3) * 8;
+    return make_uint4(__funnelshift_r(x.x, x.y, bits), __funnelshift_r(x.y, x.z, bits),
+                      __funnelshift_r(x.z, x.w, bits), __funnelshift_r(x.w, y.x, bits));
+}
+
+// A block streams a split of a row: NT x U vectors of 16 bytes a chunk, the
+// next chunk's loads in flight while one is worked on.  The tokens after the
+// last vector are one more value of a thread's first chunk.
+template <typename T, bool MASK> __global__ void __launch_bounds__(NT, 3) beam_rows_kernel(BeamArgs a)
+{
+    constexpr int NV = Elem<T>::NV, CHUNK = NT * U;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Key *buf = reinterpret_cast<Key *>(smem), *tmp = buf + a.cap;
+    __shared__ Key s_keys[NT], s_nth;
+    __shared__ double s_z[WARPS];
+    __shared__ float s_m[WARPS];
+    __shared__ int s_cnt, s_kept;
     const int r = blockIdx.x, split = blockIdx.y, t = threadIdx.x;
     if (!beam_reads(a, r)) return;
     const T *row = static_cast<const T *>(a.logits) + r * a.row_stride;
-    const uint32_t *allow = a.allow ? a.allow + r * a.allow_stride : nullptr;
-    const int v0 = static_cast<int>(static_cast<int64_t>(a.vocab) * split / a.n_split);
-    const int v1 = static_cast<int>(static_cast<int64_t>(a.vocab) * (split + 1) / a.n_split);
-    auto kept = [&](int v) { return !allow || ((allow[v >> 5] >> (v & 31)) & 1u); };
+    const uint32_t *allow = MASK ? a.allow + r * a.allow_stride : nullptr;
+    const int words = (a.vocab + 31) >> 5;
+    const int v0 = min(split * a.split_len, a.vocab), v1 = min(v0 + a.split_len, a.vocab);
+    // Vectors are cut from the split's start on whatever the row's alignment, so that equal rows
+    // have equal sums and tie; the last NV to 2 NV - 1 tokens go one by one (a vector of a row
+    // that is off by `skew` bytes is put together from two aligned ones, the second of which then
+    // still ends inside the row).
+    const int n_vec = max((v1 - v0) / NV - 1, 0), tail = v0 + n_vec * NV;
+    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row + v0) & 15);
+    const uint4 *vec = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + v0) - skew);
+    auto load = [&](int i) { return skew ? __ldg(vec + i) : __ldcs(vec + i); };
 
-    float m = -INFINITY;
-    bool bad = false;
-    for (int v = v0 + t; v < v1; v += ROW_THREADS)
-        if (kept(v)) {
-            const float x = beam_f(row[v]);
-            bad |= !(x < INFINITY);
-            m = fmaxf(m, x);
+    if (t == 0) s_cnt = 0;
+    RowStat st{-INFINITY, -INFINITY, 0.f, 0.f};
+    float one = -INFINITY;
+    int one_v = -1;
+    if (t < v1 - tail) one_v = tail + t;
+    if (one_v >= 0 && (!MASK || (allow[one_v >> 5] >> (one_v & 31)) & 1u)) {
+        one = beam_f(row[one_v]);
+        st.m = max_nan(st.m, one);
+        if (one > -INFINITY) {
+            st.ref = one;
+            st.z = one < INFINITY ? 1.f : NAN;
         }
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if ((t & 31) == 0) s_m[t >> 5] = m;
-    bad = __syncthreads_or(bad);
-    m = s_m[0];
-    for (int i = 1; i < ROW_THREADS / 32; ++i) m = fmaxf(m, s_m[i]);
-
-    BeamStat *stat = a.stat + static_cast<int64_t>(r) * a.n_split + split;
-    BeamCand *cand = a.cand + (static_cast<int64_t>(r) * a.n_split + split) * a.n_out;
-    if (bad) {
-        if (t == 0) *stat = BeamStat{NAN, 0.f, 0};
-        return;
     }
-    double z = 0.0;
-    for (int v = v0 + t; v < v1; v += ROW_THREADS)
-        if (kept(v)) {
-            const float d = beam_f(row[v]) - m;
-            if (m > -INFINITY) z += exp2f(fmaf(d, a.c_hi, d * a.c_lo));
+
+    Key limit = 0;                                     // keys below it are not among the best
+    float limit_x = -INFINITY;
+    uint4 next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (u * NT + t < n_vec) next[u] = load(u * NT + t);
+    for (int base = 0; base == 0 || base < n_vec; base += CHUNK) {
+        uint4 cur[U];
+        float lm[U];
+        uint32_t bits[U];
+        float top = base == 0 ? one : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            cur[u] = next[u];
+            const int i = base + u * NT + t;
+            if (skew && i < n_vec) cur[u] = joined(cur[u], __ldg(vec + i + 1), skew);
+            if (i + CHUNK < n_vec) next[u] = load(i + CHUNK);
+            lm[u] = -INFINITY;
+            bits[u] = 0;
+            if (i < n_vec) {
+                float f[NV];
+                unpack<T>(cur[u], f);
+                if constexpr (MASK) {
+                    bits[u] = allow_bits(allow, words, v0 + i * NV);
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) {
+                        if (!((bits[u] >> e) & 1u)) f[e] = -INFINITY;
+                        lm[u] = max_nan(lm[u], f[e]);
+                    }
+                } else {
+                    lm[u] = vec_max<T>(cur[u]);
+                }
+                add_vec(st, f, lm[u], a);
+            }
+            top = fmaxf(top, lm[u]);
         }
+        // puts this chunk's keys from `from` on into the buffer; true where it ran over
+        auto push = [&](Key from, float from_x) {
+            bool over = false;
+            auto put = [&](float x, int v) {
+                const Key k = key_of(x + 0.f, v);
+                if (k < from) return;
+                const int at = atomicAdd(&s_cnt, 1);
+                if (at < a.cap) buf[at] = k;
+                over |= at >= a.cap;
+            };
+            if (base == 0 && one > -INFINITY && one >= from_x) put(one, one_v);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (lm[u] > -INFINITY && lm[u] >= from_x) {
+                    float f[NV];
+                    unpack<T>(cur[u], f);
+#pragma unroll
+                    for (int e = 0; e < NV; ++e)
+                        if (f[e] > -INFINITY && f[e] >= from_x && (!MASK || ((bits[u] >> e) & 1u)))
+                            put(f[e], v0 + (base + u * NT + t) * NV + e);
+                }
+            return over;
+        };
+        // a threshold from this chunk alone
+        auto raise = [&] {
+            Key best = 0;
+            if (base == 0 && one > -INFINITY) best = key_of(one, one_v);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (lm[u] > -INFINITY) {
+                    float f[NV];
+                    unpack<T>(cur[u], f);
+#pragma unroll
+                    for (int e = NV - 1; e >= 0; --e)
+                        if (f[e] == lm[u] && (!MASK || ((bits[u] >> e) & 1u))) {
+                            const Key k = key_of(f[e] + 0.f, v0 + (base + u * NT + t) * NV + e);
+                            best = k > best ? k : best;
+                        }
+                }
+            const Key nth = nth_of_groups(best, a.n_out, s_keys, &s_nth);
+            if (nth > limit) {
+                limit = nth;
+                limit_x = value_of(static_cast<uint32_t>(nth >> 32));
+            }
+        };
+        if (base == 0) raise();
+        const int before = s_cnt;                      // (the last chunk's pushes ended at a barrier)
+        __syncthreads();
+        if (__syncthreads_or(top >= limit_x ? push(limit, limit_x) : false)) {
+            // over: take the chunk back, cut the buffer to its best, raise the threshold, put the
+            // chunk in again (what passes now fits: n groups' keys beside n)
+            const int kept = keep_best(buf, tmp, before, a.n_out, s_keys, &s_nth, &s_kept);
+            if (kept == a.n_out && buf[kept - 1] > limit) {
+                limit = buf[kept - 1];
+                limit_x = value_of(static_cast<uint32_t>(limit >> 32));
+            }
+            raise();
+            if (t == 0) s_cnt = kept;
+            __syncthreads();
+            push(limit, limit_x);
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+    const int kept = keep_best(buf, tmp, min(s_cnt, a.cap), a.n_out, s_keys, &s_nth, &s_kept);
+    const int64_t at = static_cast<int64_t>(r) * a.n_split + split;
+    for (int j = t; j < a.n_out; j += NT)
+        a.cand[at * a.n_out + j] = j < kept ? BeamCand{value_of(static_cast<uint32_t>(buf[j] >> 32)),
+                                                       static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[j]))}
+                                            : BeamCand{0.f, -1};
+    // the split's sum, against its largest logit
+    float m = st.m;
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if ((t & 31) == 0) s_m[t >> 5] = m;
+    __syncthreads();
+    m = s_m[0];
+    for (int i = 1; i < WARPS; ++i) m = max_nan(m, s_m[i]);
+    double z = 0.0;
+    if (st.ref > -INFINITY) z = (static_cast<double>(st.z) + st.lost) * pow2_of(st.ref - m, a);
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
     if ((t & 31) == 0) s_z[t >> 5] = z;
     __syncthreads();
     if (t == 0) {
-        for (int i = 1; i < ROW_THREADS / 32; ++i) z += s_z[i];
-        *stat = BeamStat{z, m, 0};
-    }
-    // n_out rounds, each the largest key below the last one's
-    uint64_t last = ~0ull;
-    for (int j = 0; j < a.n_out; ++j) {
-        uint64_t best = 0;
-        if (last)
-            for (int v = v0 + t; v < v1; v += ROW_THREADS)
-                if (kept(v)) {
-                    const float x = beam_f(row[v]);
-                    const uint64_t k = key_of(x, v);
-                    if (x > -INFINITY && k < last && k > best) best = k;
-                }
-        for (int o = 16; o; o >>= 1) {
-            const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-            best = other > best ? other : best;
-        }
-        __syncthreads();
-        if ((t & 31) == 0) s_key[t >> 5] = best;
-        __syncthreads();
-        for (int i = 0; i < ROW_THREADS / 32; ++i) best = s_key[i] > best ? s_key[i] : best;
-        if (t == 0)
-            cand[j] = best ? BeamCand{value_of(static_cast<uint32_t>(best >> 32)),
-                                      static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best))}
-                           : BeamCand{0.f, -1};
-        last = best;
+        for (int i = 1; i < WARPS; ++i) z += s_z[i];
+        a.stat[at] = BeamStat{m < INFINITY ? z : NAN, m, 0};
     }
 }
 
-struct Ranked {
-    double rank;
-    int64_t flat;   // beam * vocab + token; -1: none
-};
-__device__ __forceinline__ bool better(const Ranked &x, const Ranked &y)
+// A row's logit as the rows kernel reads it.
+template <typename T> __device__ __forceinline__ float logit(const BeamArgs &a, int r, int tok)
 {
-    if (x.flat < 0 || y.flat < 0) return x.flat >= 0 && y.flat < 0;
-    return x.rank > y.rank || (x.rank == y.rank && x.flat < y.flat);
+    return beam_f(static_cast<const T *>(a.logits)[r * a.row_stride + tok]);
 }
+constexpr int MERGE_U = 4;                 // candidates a thread ranks at once
 
-__global__ void __launch_bounds__(MERGE_THREADS) beam_merge_kernel(BeamArgs a)
+// ---- merge -------------------------------------------------------------------------
+// One block per batch entry: a warp per beam for its log-sum-exp and for the
+// join of its splits' lists; then every beam's candidates ranked.
+__global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
 {
+    extern __shared__ __align__(16) unsigned char smem[];
+    RankKey *buf = reinterpret_cast<RankKey *>(smem), *tmp = buf + a.merge_cap;
+    Key *lists = reinterpret_cast<Key *>(tmp + a.merge_cap);           // [beams][n_out] where rows are split
+    __shared__ RankKey s_keys[NT], s_nth;
     __shared__ double s_lse[LOSSK_BEAM_MAX_BEAMS], s_div[LOSSK_BEAM_MAX_BEAMS];
+    __shared__ float s_start[LOSSK_BEAM_MAX_BEAMS];
     __shared__ int s_kind[LOSSK_BEAM_MAX_BEAMS];       // 0: no candidates, 1: its own (finished), 2: the row's
-    __shared__ Ranked s_best[MERGE_THREADS / 32];
-    __shared__ double s_score[MERGE_THREADS / 32];
-    const int b = blockIdx.x, t = threadIdx.x;
-    for (int k = t; k < a.beams; k += MERGE_THREADS) {
+    __shared__ int s_cnt, s_kept;
+    const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int k = warp; k < a.beams; k += WARPS) {
         const int r = b * a.beams + k;
         const float start = a.scores[r];
         const bool done = a.finished && a.finished[r];
         int kind = done ? 1 : 2;
         double lse = -INFINITY;
         if (!isfinite(start)) {
-            if (start != -INFINITY) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
+            if (start != -INFINITY && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
             kind = 0;
         }
         if (kind == 2) {
             const BeamStat *st = a.stat + static_cast<int64_t>(r) * a.n_split;
             float m = -INFINITY;
-            for (int i = 0; i < a.n_split; ++i) m = fmaxf(m, st[i].m);
+            for (int i = lane; i < a.n_split; i += 32) m = fmaxf(m, st[i].m);
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             double z = 0.0;
-            for (int i = 0; i < a.n_split; ++i)
-                if (st[i].z != 0.0)
-                    z += st[i].z * exp((static_cast<double>(st[i].m) - static_cast<double>(m)) / a.temperature);
-            if (isnan(z)) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
+            for (int i = lane; i < a.n_split; i += 32)
+                if (st[i].z != 0.0) {
+                    const double d = static_cast<double>(st[i].m) - static_cast<double>(m);
+                    z += d == 0.0 ? st[i].z : st[i].z * exp(d / a.temperature);
+                }
+            for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+            if (isnan(z) && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
             if (z > 0.0) lse = static_cast<double>(m) / a.temperature + log(z);
             else kind = 0;
         }
-        if (a.lse_out) a.lse_out[r] = static_cast<float>(lse);
-        const int len = (a.lengths ? a.lengths[r] : 0) + (done ? 0 : 1);
-        s_lse[k] = lse;
-        s_div[k] = a.length_alpha == 0.0 ? 1.0 : pow(static_cast<double>(len > 1 ? len : 1), a.length_alpha);
-        s_kind[k] = kind;
+        if (lane == 0) {
+            const int len = (a.lengths ? a.lengths[r] : 0) + (done ? 0 : 1);
+            if (a.lse_out) a.lse_out[r] = static_cast<float>(lse);
+            s_lse[k] = lse;
+            s_div[k] = a.length_alpha == 0.0 ? 1.0 : pow(static_cast<double>(len > 1 ? len : 1), a.length_alpha);
+            s_start[k] = start;
+            s_kind[k] = kind;
+        }
+        if (kind == 2 && a.n_split > 1) {
+            // the splits' lists, each in falling order: a lane keeps the heads of two
+            const BeamCand *c = a.cand + static_cast<int64_t>(r) * a.n_split * a.n_out;
+            int at[2] = {0, 0};
+            Key head[2];
+            auto load = [&](int h) {
+                const int i = lane + 32 * h;
+                head[h] = 0;
+                if (i < a.n_split && at[h] < a.n_out) {
+                    const BeamCand q = c[i * a.n_out + at[h]];
+                    if (q.tok >= 0) head[h] = key_of(q.x, q.tok);
+                }
+            };
+            load(0);
+            load(1);
+            for (int j = 0; j < a.n_out; ++j) {
+                const Key mine = head[0] > head[1] ? head[0] : head[1];
+                const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32));
+                const uint32_t lo = __reduce_max_sync(
+                    0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
+                const Key best = (static_cast<uint64_t>(hi) << 32) | lo;
+                if (lane == 0) lists[k * a.n_out + j] = best;
+                if (best && mine == best) {
+                    const int h = head[0] == best ? 0 : 1;
+                    ++at[h];
+                    load(h);
+                }
+            }
+        }
     }
+    if (t == 0) s_cnt = 0;
     __syncthreads();
-    const int per_row = a.n_split * a.n_out;
-    Ranked last{INFINITY, -1};
-    for (int j = 0; j < a.n_out; ++j) {
-        Ranked best{0.0, -1};
-        double score = 0.0;
-        for (int i = t; i < a.beams * per_row; i += MERGE_THREADS) {
-            const int k = i / per_row, r = b * a.beams + k;
-            Ranked c{0.0, -1};
-            double s = a.scores[r];
-            if (s_kind[k] == 1 && i % per_row == 0) {
-                c.flat = static_cast<int64_t>(k) * a.vocab + (a.end_token < 0 ? 0 : a.end_token);
-            } else if (s_kind[k] == 2) {
-                const BeamCand q = a.cand[static_cast<int64_t>(r) * per_row + i % per_row];
-                if (q.tok >= 0) c.flat = static_cast<int64_t>(k) * a.vocab + q.tok;
-                s += static_cast<double>(q.x) / a.temperature - s_lse[k];
-            }
-            c.rank = s / s_div[k];
-            if (c.flat >= 0 && (j == 0 || better(last, c)) && better(c, best)) {
-                best = c;
-                score = s;
+    const int all = a.beams * a.n_out;
+    RankKey limit{};
+    for (int base = 0; base < all; base += NT * MERGE_U) {
+        RankKey mine[MERGE_U], best{};
+#pragma unroll
+        for (int u = 0; u < MERGE_U; ++u) {
+            const int i = base + u * NT + t, k = i / a.n_out, j = i % a.n_out;
+            mine[u] = RankKey{};
+            if (i < all && s_kind[k]) {
+                double s = s_start[k];
+                int tok = -1;
+                if (s_kind[k] == 1) {
+                    if (j == 0) tok = a.end_token < 0 ? 0 : a.end_token;
+                } else {
+                    float x;
+                    if (a.n_split > 1) {
+                        const Key q = lists[i];
+                        x = value_of(static_cast<uint32_t>(q >> 32));
+                        if (q) tok = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(q));
+                    } else {
+                        const BeamCand q = a.cand[static_cast<int64_t>(b) * all + i];
+                        x = q.x;
+                        tok = q.tok;
+                    }
+                    s += static_cast<double>(x) / a.temperature - s_lse[k];
+                }
+                if (tok >= 0) {
+                    const double rank = a.length_alpha == 0.0 ? s : s / s_div[k];
+                    mine[u] = RankKey{order_of(rank), ~static_cast<uint64_t>(static_cast<int64_t>(k) * a.vocab + tok)};
+                    if (mine[u] > best) best = mine[u];
+                }
             }
         }
-        for (int o = 16; o; o >>= 1) {
-            Ranked c{__shfl_xor_sync(0xFFFFFFFFu, best.rank, o), __shfl_xor_sync(0xFFFFFFFFu, best.flat, o)};
-            const double s = __shfl_xor_sync(0xFFFFFFFFu, score, o);
-            if (better(c, best)) {
-                best = c;
-                score = s;
-            }
+        const RankKey nth = nth_of_groups(best, a.n_out, s_keys, &s_nth);
+        if (nth > limit) limit = nth;
+        if (base) {
+            // what is kept so far, with the limit it gives
+            const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
+            if (kept == a.n_out && buf[kept - 1] > limit) limit = buf[kept - 1];
+            __syncthreads();
+            if (t == 0) s_cnt = kept;
+            __syncthreads();
         }
+#pragma unroll
+        for (int u = 0; u < MERGE_U; ++u)
+            if (!is_none(mine[u]) && !(limit > mine[u])) buf[atomicAdd(&s_cnt, 1)] = mine[u];
         __syncthreads();
-        if ((t & 31) == 0) {
-            s_best[t >> 5] = best;
-            s_score[t >> 5] = score;
+    }
+    const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
+    for (int j = t; j < a.n_out; j += NT) {
+        const int64_t o = static_cast<int64_t>(b) * a.n_out + j;
+        const bool any = j < kept;
+        const int64_t flat = any ? static_cast<int64_t>(~buf[j].flat) : 0;
+        const int k = static_cast<int>(flat / a.vocab), r = b * a.beams + k;
+        const bool was = any && s_kind[k] == 1;
+        const int tok = was ? a.end_token : static_cast<int>(flat - static_cast<int64_t>(k) * a.vocab);
+        double s = s_start[k];
+        if (any && !was) {
+            // the logit again, for the score
+            const float x = a.dtype == LOSSK_F32 ? logit<float>(a, r, tok)
+                          : a.dtype == LOSSK_BF16 ? logit<uint16_t>(a, r, tok) : logit<h16_t>(a, r, tok);
+            s += static_cast<double>(x) / a.temperature - s_lse[k];
         }
-        __syncthreads();
-        for (int i = 0; i < MERGE_THREADS / 32; ++i)
-            if (better(s_best[i], best)) {
-                best = s_best[i];
-                score = s_score[i];
-            }
-        if (t == 0) {
-            const int64_t o = static_cast<int64_t>(b) * a.n_out + j;
-            const bool any = best.flat >= 0;
-            const int k = any ? static_cast<int>(best.flat / a.vocab) : 0;
-            const int r = b * a.beams + k;
-            const bool was = any && s_kind[k] == 1;
-            const int64_t tok = was ? a.end_token : best.flat - static_cast<int64_t>(k) * a.vocab;
-            a.parent_out[o] = any ? k : -1;
-            a.token_out[o] = any ? tok : -1;
-            a.score_out[o] = any ? static_cast<float>(score) : -INFINITY;
-            if (a.finished_out) a.finished_out[o] = any && (was || tok == a.end_token);
-            if (a.length_out) a.length_out[o] = any ? (a.lengths ? a.lengths[r] : 0) + (was ? 0 : 1) : 0;
-        }
-        if (best.flat < 0) {
-            // the places left
-            for (int i = j + 1 + t; i < a.n_out; i += MERGE_THREADS) {
-                const int64_t o = static_cast<int64_t>(b) * a.n_out + i;
-                a.parent_out[o] = -1;
-                a.token_out[o] = -1;
-                a.score_out[o] = -INFINITY;
-                if (a.finished_out) a.finished_out[o] = 0;
-                if (a.length_out) a.length_out[o] = 0;
-            }
-            return;
-        }
-        last = best;
+        a.parent_out[o] = any ? k : -1;
+        a.token_out[o] = any ? tok : -1;
+        a.score_out[o] = any ? static_cast<float>(s) : -INFINITY;
+        if (a.finished_out) a.finished_out[o] = any && (was || tok == a.end_token);
+        if (a.length_out) a.length_out[o] = any ? (a.lengths ? a.lengths[r] : 0) + (was ? 0 : 1) : 0;
     }
 }
 
@@ -256,26 +596,63 @@ __global__ void beam_gather_kernel(int64_t n_src, int64_t n_dst, int64_t words, 
 
 } // namespace
 
+// Three blocks of the rows kernel fit an SM.  Few rows are cut so that one
+// wave of blocks covers the GPU, no split below 4096 tokens (a block's fixed
+// work, its two thresholds, is about that of 4096 tokens); many rows are cut
+// where that fills the last wave better.
 int beam_splits(int64_t rows, int64_t vocab)
 {
-    const int64_t want = (2 * 152 + rows - 1) / rows, most = (vocab + 4095) / 4096;
-    const int64_t n = want < most ? want : most;
-    return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+    const int64_t wave = 3 * 152;
+    int64_t most = vocab / 4096;
+    most = most < 1 ? 1 : most > 64 ? 64 : most;
+    int64_t best = 1;
+    double cost = 0.0;
+    for (int64_t n = 1; n <= most; ++n) {
+        const double c = static_cast<double>((rows * n + wave - 1) / wave) * (static_cast<double>(vocab) / n + 4096.0);
+        if (n == 1 || c < cost * 0.97) {
+            cost = c;
+            best = n;
+        }
+    }
+    return static_cast<int>(best);
 }
 
-cudaError_t launch_beam_rows(int dtype, const BeamArgs &a, cudaStream_t st)
+// Keys the rows kernel's buffer holds: the n best, and what passes a chunk's
+// threshold at most (a group's every key, for n groups).
+int beam_cap(int dtype, int n_out)
 {
+    const int per = (dtype == LOSSK_F32 ? 4 : 8) * U + 1;
+    const int keys = n_out * (NT / groups_for(n_out)) * per;
+    return n_out + (keys < NT * per ? keys : NT * per);
+}
+
+template <typename T, bool MASK> cudaError_t launch_rows(const BeamArgs &a, cudaStream_t st)
+{
+    const size_t bytes = 2 * sizeof(Key) * static_cast<size_t>(a.cap);
+    const cudaError_t e = raise_smem<beam_rows_kernel<T, MASK>>(bytes);
+    if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(a.batch) * a.beams, a.n_split);
-    if (dtype == LOSSK_F32) beam_rows_kernel<float><<<grid, ROW_THREADS, 0, st>>>(a);
-    else if (dtype == LOSSK_BF16) beam_rows_kernel<uint16_t><<<grid, ROW_THREADS, 0, st>>>(a);
-    else beam_rows_kernel<h16_t><<<grid, ROW_THREADS, 0, st>>>(a);
+    beam_rows_kernel<T, MASK><<<grid, NT, bytes, st>>>(a);
     return cudaGetLastError();
 }
 
-cudaError_t launch_beam_merge(const BeamArgs &a, cudaStream_t st)
+cudaError_t launch_beam_rows(const BeamArgs &a, cudaStream_t st)
 {
-    beam_merge_kernel<<<static_cast<unsigned>(a.batch), MERGE_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    if (a.dtype == LOSSK_F32) return a.allow ? launch_rows<float, true>(a, st) : launch_rows<float, false>(a, st);
+    if (a.dtype == LOSSK_BF16) return a.allow ? launch_rows<uint16_t, true>(a, st) : launch_rows<uint16_t, false>(a, st);
+    return a.allow ? launch_rows<h16_t, true>(a, st) : launch_rows<h16_t, false>(a, st);
+}
+
+cudaError_t launch_beam_merge(const BeamArgs &a0, cudaStream_t st)
+{
+    BeamArgs a = a0;
+    const int keys = a.n_out * (NT / groups_for(a.n_out)) * MERGE_U, all = a.beams * a.n_out;
+    a.merge_cap = a.n_out + (keys < all ? keys : all);
+    const size_t bytes = 2 * sizeof(RankKey) * static_cast<size_t>(a.merge_cap) +
+                         (a.n_split > 1 ? sizeof(Key) * static_cast<size_t>(all) : 0);
+    const cudaError_t e = raise_smem<beam_merge_kernel>(bytes);
+    if (e != cudaSuccess) return e;
+    return launch_after(true, beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(NT), bytes, st, a);
 }
 
 cudaError_t launch_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t row_bytes,

@@ -192,7 +192,8 @@ int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n
         misaligned(lengths, 4) || misaligned(parent_out, 4) || misaligned(token_out, 8) || misaligned(score_out, 4) ||
         misaligned(length_out, 4) || misaligned(lse_out, 4))
         return LOSSK_UNALIGNED;
-    if (!std::isfinite(temperature) || temperature <= 0.0 || !std::isfinite(length_alpha)) return LOSSK_NON_FINITE_SCALAR;
+    // (1 / temperature has to be a float with room for a logit's size)
+    if (!(temperature >= 1e-30 && temperature <= 1e30) || !std::isfinite(length_alpha)) return LOSSK_NON_FINITE_SCALAR;
     if (end_token < -1 || end_token >= vocab) return LOSSK_TARGET_OUT_OF_RANGE;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -204,9 +205,13 @@ int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n
     a.beams = static_cast<int>(beams);
     a.vocab = static_cast<int>(vocab);
     a.n_out = static_cast<int>(n_out);
-    a.n_split = L.n_split;
+    a.dtype = dtype;
+    // splits begin on 16-byte boundaries of an aligned row
+    a.split_len = static_cast<int>(((vocab + L.n_split - 1) / L.n_split + 63) & ~int64_t(63));
+    a.n_split = static_cast<int>((vocab + a.split_len - 1) / a.split_len);
+    a.cap = beam_cap(dtype, a.n_out);
     a.c_hi = static_cast<float>(c);
-    a.c_lo = static_cast<float>(c - static_cast<double>(a.c_hi));
+    a.c_lo = c > 1e6 ? 0.f : static_cast<float>(c - static_cast<double>(a.c_hi));   // (no overflow times a logit)
     a.temperature = temperature;
     a.allow = allow;
     a.allow_stride = allow_stride;
@@ -227,7 +232,7 @@ int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     {
         Launch k(KK_BEAM_ROWS, st);
-        if (launch_beam_rows(dtype, a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+        if (launch_beam_rows(a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
     }
     Launch k(KK_BEAM_MERGE, st);
     return status_of(launch_beam_merge(a, st));
