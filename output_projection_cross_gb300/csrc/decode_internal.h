@@ -12,7 +12,7 @@ __device__ __forceinline__ void raise_fault(int *fault, int status) { atomicMax(
 
 // ---- beam selection ------------------------------------------------------------
 // What the rows kernel leaves per (row, split): the largest kept logit m, the
-// sum z of exp((x - m) / T) over the kept logits (NaN where one of them is a NaN
+// sum z of 2^(c (x - m)) over the kept logits (NaN where one of them is a NaN
 // or +infinity), and the split's n_out best (logit, token) pairs in falling
 // order, token -1 filling the places left.
 struct BeamStat {
@@ -31,8 +31,8 @@ struct BeamArgs {
     int dtype, batch, beams, vocab, n_out;
     int n_split, split_len; // tokens a split has (the last one less)
     int cap, merge_cap;     // keys the kernels' buffers hold
-    float c_hi, c_lo;       // log2(e) / T as the sum of two floats
-    double temperature;
+    float c;                // log2(e) / T
+    double inv_t;           // 1 / T
     const uint32_t *allow;
     int64_t allow_stride;
     const float *scores;

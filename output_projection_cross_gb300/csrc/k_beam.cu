@@ -113,7 +113,7 @@ __device__ __forceinline__ int keep_best(K *buf, K *tmp, int cnt, int n, K *s_ke
     if (t == 0) *s_cnt = 0;
     __syncthreads();
     for (int i = t; i < cnt; i += NT)
-        if (!(nth > buf[i])) tmp[atomicAdd(s_cnt, 1)] = buf[i];
+        if (!is_none(buf[i]) && !(nth > buf[i])) tmp[atomicAdd(s_cnt, 1)] = buf[i];
     __syncthreads();
     const int left = *s_cnt;
     for (int i = t; i < left; i += NT) {
@@ -185,17 +185,33 @@ template <typename T> __device__ __forceinline__ float vec_max(const uint4 &v)
     }
 }
 
-// A running sum of exp((x - ref) / T): ref follows the largest logit only
-// once that is FAR above it (in log2 units), so a warp seldom rescales; z is
-// kept in two floats, sum and what its roundings lost.
+// A thread's running sum of 2^(c x + b), c = log2(e) / T.  b follows the
+// largest logit only once that is FAR above it (in log2 units), so a warp
+// seldom rescales.  The sum's true base is what b says, rounded or not: it is
+// taken off again in double.  Where c ref is near the end of the floats' range
+// b could overflow; a float next to ref is then so far off that only logits
+// equal to ref count.  z is two floats, sum and what its roundings lost.
 struct RowStat {
-    float m, ref, z, lost;
+    float m, ref, b, z, lost;
 };
-constexpr float FAR = 24.f;
+constexpr float FAR = 24.f, NEAR_END = 1e37f;
 
-__device__ __forceinline__ float pow2_of(float d, const BeamArgs &a)
+// log2 of what the sum has to be multiplied by.
+__device__ __forceinline__ double base_of(const RowStat &r, float c)
 {
-    return ex2_approx(fmaf(d, a.c_hi, d * a.c_lo));
+    return fabsf(r.b) < NEAR_END ? -static_cast<double>(r.b) : static_cast<double>(r.ref) * c;
+}
+__device__ __forceinline__ void rebase(RowStat &r, float lm, float c)
+{
+    RowStat n = r;
+    n.ref = lm;
+    n.b = -lm * c;
+    if (r.ref > -INFINITY) {
+        const float g = ex2_approx(static_cast<float>(base_of(r, c) - base_of(n, c)));
+        n.z *= g;
+        n.lost *= g;
+    }
+    r = n;
 }
 __device__ __forceinline__ void add_z(RowStat &r, float x)
 {
@@ -203,25 +219,16 @@ __device__ __forceinline__ void add_z(RowStat &r, float x)
     r.lost += (r.z - (s - b)) + (x - b);
     r.z = s;
 }
-// One vector f of largest value lm.
-template <int NV> __device__ __forceinline__ void add_vec(RowStat &r, const float (&f)[NV], float lm, const BeamArgs &a)
+__device__ __forceinline__ bool far_above(const RowStat &r, float lm, float c)
 {
-    if (lm == -INFINITY) return;
-    r.m = max_nan(r.m, lm);
-    if (!((lm - r.ref) * a.c_hi < FAR)) {
-        const float g = r.ref == -INFINITY ? 0.f : pow2_of(r.ref - lm, a);
-        r.z *= g;
-        r.lost *= g;
-        r.ref = lm;
-    }
-    float e[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) e[i] = pow2_of(f[i] - r.ref, a);
-#pragma unroll
-    for (int s = NV / 2; s; s >>= 1)
-#pragma unroll
-        for (int i = 0; i < s; ++i) e[i] += e[i + s];
-    add_z(r, e[0]);
+    return !((lm - r.ref) * c < FAR);          // (a NaN is, too)
+}
+
+// A vector of -infinity.
+template <typename T> __device__ __forceinline__ uint4 all_low()
+{
+    const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, h16_t>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    return make_uint4(w, w, w, w);
 }
 
 // 32 bits of a row's mask from token v on.
@@ -258,7 +265,7 @@ __device__ __forceinline__ uint4 joined(uint4 x, uint4 y, int skew)
 // A block streams a split of a row: NT x U vectors of 16 bytes a chunk, the
 // next chunk's loads in flight while one is worked on.  The tokens after the
 // last vector are one more value of a thread's first chunk.
-template <typename T, bool MASK> __global__ void __launch_bounds__(NT, 3) beam_rows_kernel(BeamArgs a)
+template <typename T, bool MASK> __global__ void __launch_bounds__(NT, MASK ? 2 : 3) beam_rows_kernel(BeamArgs a)
 {
     constexpr int NV = Elem<T>::NV, CHUNK = NT * U;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -283,16 +290,17 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT, 3) beam_r
     auto load = [&](int i) { return skew ? __ldg(vec + i) : __ldcs(vec + i); };
 
     if (t == 0) s_cnt = 0;
-    RowStat st{-INFINITY, -INFINITY, 0.f, 0.f};
+    const float c = a.c;
+    RowStat st{-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
     float one = -INFINITY;
     int one_v = -1;
     if (t < v1 - tail) one_v = tail + t;
     if (one_v >= 0 && (!MASK || (allow[one_v >> 5] >> (one_v & 31)) & 1u)) {
         one = beam_f(row[one_v]);
-        st.m = max_nan(st.m, one);
-        if (one > -INFINITY) {
-            st.ref = one;
-            st.z = one < INFINITY ? 1.f : NAN;
+        st.m = one;
+        if (!(one == -INFINITY)) {
+            rebase(st, one, c);
+            st.z = 1.f;
         }
     }
 
@@ -300,77 +308,121 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT, 3) beam_r
     float limit_x = -INFINITY;
     uint4 next[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+        next[u] = all_low<T>();
         if (u * NT + t < n_vec) next[u] = load(u * NT + t);
+    }
     for (int base = 0; base == 0 || base < n_vec; base += CHUNK) {
         uint4 cur[U];
-        float lm[U];
-        uint32_t bits[U];
-        float top = base == 0 ? one : -INFINITY;
+        float lm[U];                                   // each vector's largest, then the chunk's
+        uint32_t bits = ~0u;                           // MASK: which of the thread's tokens are allowed
+        float top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             cur[u] = next[u];
             const int i = base + u * NT + t;
             if (skew && i < n_vec) cur[u] = joined(cur[u], __ldg(vec + i + 1), skew);
+            next[u] = all_low<T>();
             if (i + CHUNK < n_vec) next[u] = load(i + CHUNK);
-            lm[u] = -INFINITY;
-            bits[u] = 0;
-            if (i < n_vec) {
+            if constexpr (MASK) {
+                const uint32_t w = i < n_vec ? allow_bits(allow, words, v0 + i * NV) : 0u;
+                constexpr uint32_t ONES = (1u << NV) - 1u;
+                bits = (bits & ~(ONES << (u * NV))) | ((w & ONES) << (u * NV));
                 float f[NV];
                 unpack<T>(cur[u], f);
-                if constexpr (MASK) {
-                    bits[u] = allow_bits(allow, words, v0 + i * NV);
+                lm[u] = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < NV; ++e) {
-                        if (!((bits[u] >> e) & 1u)) f[e] = -INFINITY;
-                        lm[u] = max_nan(lm[u], f[e]);
-                    }
-                } else {
-                    lm[u] = vec_max<T>(cur[u]);
-                }
-                add_vec(st, f, lm[u], a);
+                for (int e = 0; e < NV; ++e)
+                    if ((w >> e) & 1u) lm[u] = max_nan(lm[u], f[e]);
+            } else {
+                lm[u] = vec_max<T>(cur[u]);
             }
-            top = fmaxf(top, lm[u]);
+            top = max_nan(top, lm[u]);
         }
-        // puts this chunk's keys from `from` on into the buffer; true where it ran over
-        auto push = [&](Key from, float from_x) {
-            bool over = false;
-            auto put = [&](float x, int v) {
-                const Key k = key_of(x + 0.f, v);
-                if (k < from) return;
-                const int at = atomicAdd(&s_cnt, 1);
-                if (at < a.cap) buf[at] = k;
-                over |= at >= a.cap;
-            };
-            if (base == 0 && one > -INFINITY && one >= from_x) put(one, one_v);
+        if (!(top == -INFINITY)) {
+            st.m = max_nan(st.m, top);
+            if (far_above(st, top, c)) rebase(st, top, c);
+            float sum = 0.f;
+            const bool plain = fabsf(st.b) < NEAR_END;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[NV];
+                unpack<T>(cur[u], f);
+                if (plain) {
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) f[e] = ex2_approx(fmaf(f[e], c, st.b));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) f[e] = f[e] == st.ref ? 1.f : 0.f;
+                }
+                if constexpr (MASK) {
+#pragma unroll
+                    for (int e = 0; e < NV; ++e)
+                        if (!((bits >> (u * NV + e)) & 1u)) f[e] = 0.f;
+                }
+#pragma unroll
+                for (int h = NV / 2; h; h >>= 1)
+#pragma unroll
+                    for (int e = 0; e < h; ++e) f[e] += f[e + h];
+                sum += f[0];
+            }
+            add_z(st, sum);
+        }
+        const auto token = [&](int x) { return v0 + (base + (x / NV) * NT + t) * NV + x % NV; };   // of value x
+        // puts this chunk's keys from `limit` on into the buffer; true where it ran over
+        auto push = [&] {
+            uint32_t hits = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (lm[u] > -INFINITY && lm[u] >= from_x) {
+                if (lm[u] >= limit_x && lm[u] > -INFINITY) {
                     float f[NV];
                     unpack<T>(cur[u], f);
 #pragma unroll
                     for (int e = 0; e < NV; ++e)
-                        if (f[e] > -INFINITY && f[e] >= from_x && (!MASK || ((bits[u] >> e) & 1u)))
-                            put(f[e], v0 + (base + u * NT + t) * NV + e);
+                        if (f[e] >= limit_x && f[e] > -INFINITY) hits |= 1u << (u * NV + e);
                 }
+            hits &= bits;
+            bool over = false;
+            bool last = base == 0 && one >= limit_x && one > -INFINITY;
+            while (hits || last) {
+                int v = one_v;
+                if (hits) {
+                    v = token(__ffs(hits) - 1);
+                    hits &= hits - 1;
+                } else {
+                    last = false;
+                }
+                const Key k = key_of(beam_f(row[v]), v);         // (read again: a hit is rare)
+                if (k < limit) continue;
+                const int at = atomicAdd(&s_cnt, 1);
+                if (at < a.cap) buf[at] = k;
+                over |= at >= a.cap;
+            }
             return over;
         };
         // a threshold from this chunk alone
         auto raise = [&] {
-            Key best = 0;
-            if (base == 0 && one > -INFINITY) best = key_of(one, one_v);
+            Key best = base == 0 && one > -INFINITY ? key_of(one, one_v) : 0;
+            int u_best = 0;
+            uint4 vb = cur[0];
+            float x = lm[0];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (lm[u] > -INFINITY) {
-                    float f[NV];
-                    unpack<T>(cur[u], f);
-#pragma unroll
-                    for (int e = NV - 1; e >= 0; --e)
-                        if (f[e] == lm[u] && (!MASK || ((bits[u] >> e) & 1u))) {
-                            const Key k = key_of(f[e] + 0.f, v0 + (base + u * NT + t) * NV + e);
-                            best = k > best ? k : best;
-                        }
+            for (int u = 1; u < U; ++u)
+                if (lm[u] > x) {
+                    x = lm[u];
+                    vb = cur[u];
+                    u_best = u;
                 }
+            if (x > -INFINITY) {
+                float f[NV];
+                unpack<T>(vb, f);
+                int e_best = 0;
+#pragma unroll
+                for (int e = NV - 1; e >= 0; --e)
+                    if (f[e] == x && ((bits >> (u_best * NV + e)) & 1u)) e_best = e;
+                const Key k = key_of(x + 0.f, token(u_best * NV + e_best));
+                best = k > best ? k : best;
+            }
             const Key nth = nth_of_groups(best, a.n_out, s_keys, &s_nth);
             if (nth > limit) {
                 limit = nth;
@@ -378,12 +430,17 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT, 3) beam_r
             }
         };
         if (base == 0) raise();
-        const int before = s_cnt;                      // (the last chunk's pushes ended at a barrier)
-        __syncthreads();
-        if (__syncthreads_or(top >= limit_x ? push(limit, limit_x) : false)) {
+        if (__syncthreads_or(fmaxf(top, base == 0 ? one : top) >= limit_x ? push() : false)) {
             // over: take the chunk back, cut the buffer to its best, raise the threshold, put the
             // chunk in again (what passes now fits: n groups' keys beside n)
-            const int kept = keep_best(buf, tmp, before, a.n_out, s_keys, &s_nth, &s_kept);
+            const int cnt = min(s_cnt, a.cap);
+            const int first = v0 + base * NV, past = first + CHUNK * NV;
+            for (int i = t; i < cnt; i += NT) {
+                const int v = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[i]));
+                if ((v >= first && v < past) || (base == 0 && v >= tail)) buf[i] = 0;
+            }
+            __syncthreads();
+            const int kept = keep_best(buf, tmp, cnt, a.n_out, s_keys, &s_nth, &s_kept);
             if (kept == a.n_out && buf[kept - 1] > limit) {
                 limit = buf[kept - 1];
                 limit_x = value_of(static_cast<uint32_t>(limit >> 32));
@@ -391,7 +448,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT, 3) beam_r
             raise();
             if (t == 0) s_cnt = kept;
             __syncthreads();
-            push(limit, limit_x);
+            push();
             __syncthreads();
         }
     }
@@ -402,15 +459,16 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT, 3) beam_r
         a.cand[at * a.n_out + j] = j < kept ? BeamCand{value_of(static_cast<uint32_t>(buf[j] >> 32)),
                                                        static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[j]))}
                                             : BeamCand{0.f, -1};
-    // the split's sum, against its largest logit
+    // the split's sum, against the base of its largest logit
     float m = st.m;
     for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     if ((t & 31) == 0) s_m[t >> 5] = m;
     __syncthreads();
     m = s_m[0];
     for (int i = 1; i < WARPS; ++i) m = max_nan(m, s_m[i]);
+    const double top = static_cast<double>(m) * c;
     double z = 0.0;
-    if (st.ref > -INFINITY) z = (static_cast<double>(st.z) + st.lost) * pow2_of(st.ref - m, a);
+    if (st.ref > -INFINITY) z = (static_cast<double>(st.z) + st.lost) * ex2_approx(static_cast<float>(base_of(st, c) - top));
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
     if ((t & 31) == 0) s_z[t >> 5] = z;
     __syncthreads();
@@ -425,7 +483,7 @@ template <typename T> __device__ __forceinline__ float logit(const BeamArgs &a, 
 {
     return beam_f(static_cast<const T *>(a.logits)[r * a.row_stride + tok]);
 }
-constexpr int MERGE_U = 4;                 // candidates a thread ranks at once
+constexpr int MERGE_U = 4;                 // candidates a thread ranks at once (one, where that is enough)
 
 // ---- merge -------------------------------------------------------------------------
 // One block per batch entry: a warp per beam for its log-sum-exp and for the
@@ -458,50 +516,56 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
             for (int i = lane; i < a.n_split; i += 32) m = fmaxf(m, st[i].m);
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             double z = 0.0;
+            const double top = static_cast<double>(m) * a.c;
             for (int i = lane; i < a.n_split; i += 32)
-                if (st[i].z != 0.0) {
-                    const double d = static_cast<double>(st[i].m) - static_cast<double>(m);
-                    z += d == 0.0 ? st[i].z : st[i].z * exp(d / a.temperature);
-                }
+                if (st[i].z != 0.0) z += st[i].z * ex2_approx(static_cast<float>(static_cast<double>(st[i].m) * a.c - top));
             for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
             if (isnan(z) && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
-            if (z > 0.0) lse = static_cast<double>(m) / a.temperature + log(z);
+            if (z > 0.0) lse = static_cast<double>(m) * a.inv_t + log(z);
             else kind = 0;
         }
         if (lane == 0) {
             const int len = (a.lengths ? a.lengths[r] : 0) + (done ? 0 : 1);
             if (a.lse_out) a.lse_out[r] = static_cast<float>(lse);
             s_lse[k] = lse;
-            s_div[k] = a.length_alpha == 0.0 ? 1.0 : pow(static_cast<double>(len > 1 ? len : 1), a.length_alpha);
+            const double n = len > 1 ? len : 1;
+            s_div[k] = a.length_alpha == 0.0 ? 1.0 : a.length_alpha == 1.0 ? n : pow(n, a.length_alpha);
             s_start[k] = start;
             s_kind[k] = kind;
         }
         if (kind == 2 && a.n_split > 1) {
             // the splits' lists, each in falling order: a lane keeps the heads of two
             const BeamCand *c = a.cand + static_cast<int64_t>(r) * a.n_split * a.n_out;
+            // (the next three are loaded with the head: a pop then rarely waits for memory)
             int at[2] = {0, 0};
-            Key head[2];
-            auto load = [&](int h) {
+            Key q[2][4];
+            auto entry = [&](int h, int j) {
                 const int i = lane + 32 * h;
-                head[h] = 0;
-                if (i < a.n_split && at[h] < a.n_out) {
-                    const BeamCand q = c[i * a.n_out + at[h]];
-                    if (q.tok >= 0) head[h] = key_of(q.x, q.tok);
-                }
+                if (i >= a.n_split || j >= a.n_out) return Key(0);
+                const BeamCand x = c[i * a.n_out + j];
+                return x.tok >= 0 ? key_of(x.x, x.tok) : Key(0);
             };
-            load(0);
-            load(1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[h][j] = entry(h, j);
             for (int j = 0; j < a.n_out; ++j) {
-                const Key mine = head[0] > head[1] ? head[0] : head[1];
+                const bool second = q[1][0] > q[0][0];
+                const Key mine = second ? q[1][0] : q[0][0];
                 const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32));
                 const uint32_t lo = __reduce_max_sync(
                     0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
                 const Key best = (static_cast<uint64_t>(hi) << 32) | lo;
                 if (lane == 0) lists[k * a.n_out + j] = best;
                 if (best && mine == best) {
-                    const int h = head[0] == best ? 0 : 1;
-                    ++at[h];
-                    load(h);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (second == (h == 1)) {
+                            q[h][0] = q[h][1];
+                            q[h][1] = q[h][2];
+                            q[h][2] = q[h][3];
+                            q[h][3] = entry(h, 4 + at[h]++);
+                        }
                 }
             }
         }
@@ -532,7 +596,7 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
                         x = q.x;
                         tok = q.tok;
                     }
-                    s += static_cast<double>(x) / a.temperature - s_lse[k];
+                    s += static_cast<double>(x) * a.inv_t - s_lse[k];
                 }
                 if (tok >= 0) {
                     const double rank = a.length_alpha == 0.0 ? s : s / s_div[k];
@@ -569,7 +633,7 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
             // the logit again, for the score
             const float x = a.dtype == LOSSK_F32 ? logit<float>(a, r, tok)
                           : a.dtype == LOSSK_BF16 ? logit<uint16_t>(a, r, tok) : logit<h16_t>(a, r, tok);
-            s += static_cast<double>(x) / a.temperature - s_lse[k];
+            s += static_cast<double>(x) * a.inv_t - s_lse[k];
         }
         a.parent_out[o] = any ? k : -1;
         a.token_out[o] = any ? tok : -1;

@@ -197,7 +197,6 @@ int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n
     if (end_token < -1 || end_token >= vocab) return LOSSK_TARGET_OUT_OF_RANGE;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const double c = LOG2E / temperature;
     BeamArgs a{};
     a.logits = logits;
     a.row_stride = row_stride;
@@ -210,9 +209,8 @@ int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n
     a.split_len = static_cast<int>(((vocab + L.n_split - 1) / L.n_split + 63) & ~int64_t(63));
     a.n_split = static_cast<int>((vocab + a.split_len - 1) / a.split_len);
     a.cap = beam_cap(dtype, a.n_out);
-    a.c_hi = static_cast<float>(c);
-    a.c_lo = c > 1e6 ? 0.f : static_cast<float>(c - static_cast<double>(a.c_hi));   // (no overflow times a logit)
-    a.temperature = temperature;
+    a.c = static_cast<float>(LOG2E / temperature);
+    a.inv_t = 1.0 / temperature;
     a.allow = allow;
     a.allow_stride = allow_stride;
     a.scores = scores;
