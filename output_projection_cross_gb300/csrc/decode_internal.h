@@ -48,6 +48,8 @@ struct BeamArgs {
     float *lse_out;
     BeamStat *stat;         // [rows][n_split]
     BeamCand *cand;         // [rows][n_split][n_out]
+    int *next;              // the rows kernel's next item: 0 between calls
+    int *err;               // the header's error word (expired waits)
     int *fault;
 };
 

@@ -24,6 +24,9 @@ namespace {
 constexpr int NT = 256;                    // threads of a block, here throughout
 constexpr int WARPS = NT / 32;
 
+// A barrier of those threads (the rows kernel has a loading warp beside them).
+__device__ __forceinline__ void block_sync() { named_bar_sync(1, NT); }
+
 // ---- the n best of many -----------------------------------------------------------
 // A block streams keys past a threshold into a buffer in shared memory.  The
 // threshold comes from the first chunk: cut the block into groups of threads;
@@ -85,10 +88,10 @@ template <typename K> __device__ __forceinline__ K nth_of_groups(K mine, int n, 
         const K other = shfl_xor(mine, o);
         if (other > mine) mine = other;
     }
-    __syncthreads();
+    block_sync();
     if (t == 0) *s_nth = K{};
     if (t % per == 0) s_keys[t / per] = mine;
-    __syncthreads();
+    block_sync();
     if (t < groups) {
         mine = s_keys[t];
         int above = 0;
@@ -96,7 +99,7 @@ template <typename K> __device__ __forceinline__ K nth_of_groups(K mine, int n, 
         for (int i = 0; i < groups; ++i) above += s_keys[i] > mine;
         if (above == n - 1 && !is_none(mine)) *s_nth = mine;
     }
-    __syncthreads();
+    block_sync();
     return *s_nth;
 }
 
@@ -111,10 +114,10 @@ __device__ __forceinline__ int keep_best(K *buf, K *tmp, int cnt, int n, K *s_ke
         if (buf[i] > mine) mine = buf[i];
     const K nth = nth_of_groups(mine, n, s_keys, s_nth);
     if (t == 0) *s_cnt = 0;
-    __syncthreads();
+    block_sync();
     for (int i = t; i < cnt; i += NT)
         if (!is_none(buf[i]) && !(nth > buf[i])) tmp[atomicAdd(s_cnt, 1)] = buf[i];
-    __syncthreads();
+    block_sync();
     const int left = *s_cnt;
     for (int i = t; i < left; i += NT) {
         const K k = tmp[i];
@@ -122,7 +125,7 @@ __device__ __forceinline__ int keep_best(K *buf, K *tmp, int cnt, int n, K *s_ke
         for (int j = 0; j < left; ++j) above += tmp[j] > k;
         if (above < n) buf[above] = k;
     }
-    __syncthreads();
+    block_sync();
     return left < n ? left : n;
 }
 
@@ -138,6 +141,8 @@ template <> struct Elem<h16_t> {
     static constexpr int NV = 8;
 };
 constexpr int U = 4;                       // 16-byte vectors a thread holds of a chunk
+constexpr int CHUNK = NT * U;
+constexpr int STAGES = 3, STAGE_BYTES = (CHUNK + 1) * 16;
 
 __device__ __forceinline__ float beam_f(float x) { return x + 0.f; }   // -0 to +0: they tie
 __device__ __forceinline__ float beam_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16) + 0.f; }
@@ -262,219 +267,359 @@ __device__ __forceinline__ uint4 joined(uint4 x, uint4 y, int skew)
                       __funnelshift_r(x.z, x.w, bits), __funnelshift_r(x.w, y.x, bits));
 }
 
-// A block streams a split of a row: NT x U vectors of 16 bytes a chunk, the
-// next chunk's loads in flight while one is worked on.  The tokens after the
-// last vector are one more value of a thread's first chunk.
-template <typename T, bool MASK> __global__ void __launch_bounds__(NT, MASK ? 2 : 3) beam_rows_kernel(BeamArgs a)
+// ---- a row's items ------------------------------------------------------------------
+// An item is a split of a row.  Vectors are cut from the split's start on
+// whatever the row's alignment, so that equal rows have equal sums and tie; a
+// vector of a row that is off by `skew` bytes is put together from two aligned
+// ones.  The last NV to 2 NV - 1 tokens go one by one, so that the second of
+// those always ends inside the row.
+template <typename T> struct Item {
+    static constexpr int NV = Elem<T>::NV;
+    int r, v0, v1, n_vec, tail, skew;
+    const T *row;
+    const char *from;                      // the first aligned vector
+    __device__ __forceinline__ Item(const BeamArgs &a, int item)
+    {
+        r = item / a.n_split;
+        const int split = item % a.n_split;
+        row = static_cast<const T *>(a.logits) + r * a.row_stride;
+        v0 = min(split * a.split_len, a.vocab);
+        v1 = min(v0 + a.split_len, a.vocab);
+        n_vec = max((v1 - v0) / NV - 1, 0);
+        tail = v0 + n_vec * NV;
+        skew = static_cast<int>(reinterpret_cast<uintptr_t>(row + v0) & 15);
+        from = reinterpret_cast<const char *>(row + v0) - skew;
+    }
+    __device__ __forceinline__ int chunks() const { return n_vec > CHUNK ? (n_vec + CHUNK - 1) / CHUNK : 1; }
+};
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
-    constexpr int NV = Elem<T>::NV, CHUNK = NT * U;
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The n best of a split once more, step by step with a barrier each, for data
+// that ran over the buffer (logits that keep rising): where a step's keys do
+// not fit, the buffer is cut to its best and the threshold raised first.
+template <typename T, bool MASK>
+__device__ __noinline__ int best_by_steps(const BeamArgs &a, const Item<T> &it, Key *buf, Key *tmp, Key *s_keys,
+                                          Key *s_nth, int *s_cnt, int *s_kept)
+{
+    constexpr int NV = Elem<T>::NV;
+    const int t = threadIdx.x, words = (a.vocab + 31) >> 5;
+    const uint32_t *allow = MASK ? a.allow + it.r * a.allow_stride : nullptr;
+    const uint4 *vec = reinterpret_cast<const uint4 *>(it.from);
+    block_sync();
+    if (t == 0) *s_cnt = 0;
+    Key limit = 0;
+    // step -1: the tokens after the last vector
+    for (int base = -NT; base < it.n_vec; base += NT) {
+        float f[NV];
+        const int i = base + t;
+        int v = it.tail + t;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) f[e] = -INFINITY;
+        if (base < 0) {
+            if (v < it.v1) f[0] = beam_f(it.row[v]);
+        } else if (i < it.n_vec) {
+            v = it.v0 + i * NV;
+            uint4 x = vec[i];
+            if (it.skew) x = joined(x, vec[i + 1], it.skew);
+            unpack<T>(x, f);
+        }
+        if constexpr (MASK) {
+            const uint32_t bits = v < it.v1 ? allow_bits(allow, words, v) : 0u;
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+                if (!((bits >> e) & 1u)) f[e] = -INFINITY;
+        }
+        Key k[NV], best = 0;
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            k[e] = f[e] > -INFINITY ? key_of(f[e] + 0.f, v + e) : 0;
+            best = k[e] > best ? k[e] : best;
+            mine += k[e] && k[e] >= limit;
+        }
+        block_sync();
+        const int before = *s_cnt;
+        block_sync();
+        int at = mine ? atomicAdd(s_cnt, mine) : 0;
+        block_sync();
+        if (*s_cnt > a.cap) {
+            const int kept = keep_best(buf, tmp, before, a.n_out, s_keys, s_nth, s_kept);
+            if (kept == a.n_out && buf[kept - 1] > limit) limit = buf[kept - 1];
+            const Key nth = nth_of_groups(best, a.n_out, s_keys, s_nth);
+            if (nth > limit) limit = nth;
+            mine = 0;
+#pragma unroll
+            for (int e = 0; e < NV; ++e) mine += k[e] && k[e] >= limit;
+            if (t == 0) *s_cnt = kept;
+            block_sync();
+            at = mine ? atomicAdd(s_cnt, mine) : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < NV; ++e)
+            if (k[e] && k[e] >= limit) buf[at++] = k[e];
+    }
+    block_sync();
+    return *s_cnt;
+}
+
+// Persistent blocks of eight warps that work and one that loads.  The loading
+// warp takes items from a common counter and keeps a ring of STAGES chunks
+// full with bulk copies, across items, so that the ends of one item (its
+// threshold, its lists) cost no memory time.  In a chunk a thread has U
+// vectors; the working warps meet at a barrier only for thresholds: after the
+// first chunk, and after the 2nd, 4th, 8th ..., where the buffer is cut to its n
+// best (of random logits a chunk then brings n / (chunks so far) keys).  Keys
+// that do not fit the buffer are dropped, and the item's best are found by
+// best_by_steps instead.
+template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK ? 2 : 3) beam_rows_kernel(BeamArgs a)
+{
+    constexpr int NV = Elem<T>::NV;
     extern __shared__ __align__(16) unsigned char smem[];
-    Key *buf = reinterpret_cast<Key *>(smem), *tmp = buf + a.cap;
+    Key *buf = reinterpret_cast<Key *>(smem + STAGES * STAGE_BYTES), *tmp = buf + a.cap;
+    __shared__ __align__(8) uint64_t s_full[STAGES], s_empty[STAGES];
     __shared__ Key s_keys[NT], s_nth;
     __shared__ double s_z[WARPS];
     __shared__ float s_m[WARPS];
-    __shared__ int s_cnt, s_kept;
-    const int r = blockIdx.x, split = blockIdx.y, t = threadIdx.x;
-    if (!beam_reads(a, r)) return;
-    const T *row = static_cast<const T *>(a.logits) + r * a.row_stride;
-    const uint32_t *allow = MASK ? a.allow + r * a.allow_stride : nullptr;
-    const int words = (a.vocab + 31) >> 5;
-    const int v0 = min(split * a.split_len, a.vocab), v1 = min(v0 + a.split_len, a.vocab);
-    // Vectors are cut from the split's start on whatever the row's alignment, so that equal rows
-    // have equal sums and tie; the last NV to 2 NV - 1 tokens go one by one (a vector of a row
-    // that is off by `skew` bytes is put together from two aligned ones, the second of which then
-    // still ends inside the row).
-    const int n_vec = max((v1 - v0) / NV - 1, 0), tail = v0 + n_vec * NV;
-    const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row + v0) & 15);
-    const uint4 *vec = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + v0) - skew);
-    auto load = [&](int i) { return skew ? __ldg(vec + i) : __ldcs(vec + i); };
-
-    if (t == 0) s_cnt = 0;
-    const float c = a.c;
-    RowStat st{-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
-    float one = -INFINITY;
-    int one_v = -1;
-    if (t < v1 - tail) one_v = tail + t;
-    if (one_v >= 0 && (!MASK || (allow[one_v >> 5] >> (one_v & 31)) & 1u)) {
-        one = beam_f(row[one_v]);
-        st.m = one;
-        if (!(one == -INFINITY)) {
-            rebase(st, one, c);
-            st.z = 1.f;
+    __shared__ int s_item[STAGES], s_cnt, s_kept, s_over;
+    const int t = threadIdx.x, lane = t & 31;
+    if (t == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], WARPS);
         }
+        fence_mbarrier_init();
     }
+    __syncthreads();
 
-    Key limit = 0;                                     // keys below it are not among the best
-    float limit_x = -INFINITY;
-    uint4 next[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        next[u] = all_low<T>();
-        if (u * NT + t < n_vec) next[u] = load(u * NT + t);
-    }
-    for (int base = 0; base == 0 || base < n_vec; base += CHUNK) {
-        uint4 cur[U];
-        float lm[U];                                   // each vector's largest, then the chunk's
-        uint32_t bits = ~0u;                           // MASK: which of the thread's tokens are allowed
-        float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            cur[u] = next[u];
-            const int i = base + u * NT + t;
-            if (skew && i < n_vec) cur[u] = joined(cur[u], __ldg(vec + i + 1), skew);
-            next[u] = all_low<T>();
-            if (i + CHUNK < n_vec) next[u] = load(i + CHUNK);
-            if constexpr (MASK) {
-                const uint32_t w = i < n_vec ? allow_bits(allow, words, v0 + i * NV) : 0u;
-                constexpr uint32_t ONES = (1u << NV) - 1u;
-                bits = (bits & ~(ONES << (u * NV))) | ((w & ONES) << (u * NV));
-                float f[NV];
-                unpack<T>(cur[u], f);
-                lm[u] = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < NV; ++e)
-                    if ((w >> e) & 1u) lm[u] = max_nan(lm[u], f[e]);
-            } else {
-                lm[u] = vec_max<T>(cur[u]);
+    if (t >= NT) {
+        if (lane) return;
+        int k = 0;                                     // stages filled so far
+        // an expired wait leaves its error and the loop runs on without waiting
+        auto stage = [&] {
+            const int st = k % STAGES;
+            if (k >= STAGES) mbar_wait(&s_empty[st], (k / STAGES - 1) & 1, a.err);
+            ++k;
+            return st;
+        };
+        const int items = a.batch * a.beams * a.n_split;
+        for (int i; (i = atomicAdd(a.next, 1)) < items;) {
+            const Item<T> it(a, i);
+            if (!beam_reads(a, it.r)) continue;
+            for (int c = 0; c < it.chunks(); ++c) {
+                const int st = stage();
+                s_item[st] = i;
+                const int n = min(it.n_vec - c * CHUNK, CHUNK);
+                if (n > 0) {
+                    const uint32_t bytes = static_cast<uint32_t>(n + (it.skew ? 1 : 0)) * 16;
+                    mbar_arrive_expect_tx(&s_full[st], bytes);
+                    bulk_load(smem + st * STAGE_BYTES, it.from + static_cast<int64_t>(c) * CHUNK * 16, bytes, &s_full[st]);
+                } else {
+                    mbar_arrive(&s_full[st]);
+                }
             }
-            top = max_nan(top, lm[u]);
         }
-        if (!(top == -INFINITY)) {
-            st.m = max_nan(st.m, top);
-            if (far_above(st, top, c)) rebase(st, top, c);
-            float sum = 0.f;
-            const bool plain = fabsf(st.b) < NEAR_END;
+        const int st = stage();
+        s_item[st] = -1;
+        mbar_arrive(&s_full[st]);
+        // no copy of this block is in flight when it ends
+        for (int i = max(k - STAGES, 0); i < k; ++i) mbar_wait(&s_full[i % STAGES], (i / STAGES) & 1, a.err);
+        return;
+    }
+
+    const float c = a.c;
+    const int words = (a.vocab + 31) >> 5;
+    int k = 0;                                         // stages used so far
+    while (true) {
+        mbar_wait(&s_full[k % STAGES], (k / STAGES) & 1, a.err);
+        const int item = s_item[k % STAGES];
+        if (item < 0) return;
+        const Item<T> it(a, item);
+        const uint32_t *allow = MASK ? a.allow + it.r * a.allow_stride : nullptr;
+        if (t == 0) s_cnt = s_over = 0;
+        RowStat st{-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
+        float one = -INFINITY;
+        const int one_v = it.tail + t;
+        if (one_v < it.v1 && (!MASK || (allow[one_v >> 5] >> (one_v & 31)) & 1u)) {
+            one = beam_f(it.row[one_v]);
+            st.m = one;
+            if (!(one == -INFINITY)) {
+                rebase(st, one, c);
+                st.z = 1.f;
+            }
+        }
+        Key limit = 0;                                 // keys below it are not among the best
+        float limit_x = -INFINITY;
+        const int chunks = it.chunks();
+        for (int j = 0; j < chunks; ++j, ++k) {
+            const int sg = k % STAGES, base = j * CHUNK;
+            uint32_t bits = ~0u;                       // MASK: which of the thread's tokens are allowed
+            if constexpr (MASK) {
+                bits = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = base + u * NT + t;
+                    const uint32_t w = i < it.n_vec ? allow_bits(allow, words, it.v0 + i * NV) : 0u;
+                    bits |= (w & ((1u << NV) - 1u)) << (u * NV);
+                }
+            }
+            if (j) mbar_wait(&s_full[sg], (k / STAGES) & 1, a.err);
+            const uint4 *tile = reinterpret_cast<const uint4 *>(smem + sg * STAGE_BYTES);
+            uint4 cur[U];
+            float lm[U], top = -INFINITY;              // each vector's largest, the chunk's
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float f[NV];
-                unpack<T>(cur[u], f);
-                if (plain) {
-#pragma unroll
-                    for (int e = 0; e < NV; ++e) f[e] = ex2_approx(fmaf(f[e], c, st.b));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < NV; ++e) f[e] = f[e] == st.ref ? 1.f : 0.f;
+                const int i = u * NT + t;
+                cur[u] = all_low<T>();
+                if (base + i < it.n_vec) {
+                    cur[u] = tile[i];
+                    if (it.skew) cur[u] = joined(cur[u], tile[i + 1], it.skew);
                 }
                 if constexpr (MASK) {
-#pragma unroll
-                    for (int e = 0; e < NV; ++e)
-                        if (!((bits >> (u * NV + e)) & 1u)) f[e] = 0.f;
-                }
-#pragma unroll
-                for (int h = NV / 2; h; h >>= 1)
-#pragma unroll
-                    for (int e = 0; e < h; ++e) f[e] += f[e + h];
-                sum += f[0];
-            }
-            add_z(st, sum);
-        }
-        const auto token = [&](int x) { return v0 + (base + (x / NV) * NT + t) * NV + x % NV; };   // of value x
-        // puts this chunk's keys from `limit` on into the buffer; true where it ran over
-        auto push = [&] {
-            uint32_t hits = 0;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (lm[u] >= limit_x && lm[u] > -INFINITY) {
                     float f[NV];
                     unpack<T>(cur[u], f);
+                    lm[u] = -INFINITY;
 #pragma unroll
                     for (int e = 0; e < NV; ++e)
-                        if (f[e] >= limit_x && f[e] > -INFINITY) hits |= 1u << (u * NV + e);
-                }
-            hits &= bits;
-            bool over = false;
-            bool last = base == 0 && one >= limit_x && one > -INFINITY;
-            while (hits || last) {
-                int v = one_v;
-                if (hits) {
-                    v = token(__ffs(hits) - 1);
-                    hits &= hits - 1;
+                        if ((bits >> (u * NV + e)) & 1u) lm[u] = max_nan(lm[u], f[e]);
                 } else {
-                    last = false;
+                    lm[u] = vec_max<T>(cur[u]);
                 }
-                const Key k = key_of(beam_f(row[v]), v);         // (read again: a hit is rare)
-                if (k < limit) continue;
-                const int at = atomicAdd(&s_cnt, 1);
-                if (at < a.cap) buf[at] = k;
-                over |= at >= a.cap;
+                top = max_nan(top, lm[u]);
             }
-            return over;
-        };
-        // a threshold from this chunk alone
-        auto raise = [&] {
-            Key best = base == 0 && one > -INFINITY ? key_of(one, one_v) : 0;
-            int u_best = 0;
-            uint4 vb = cur[0];
-            float x = lm[0];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[sg]);  // the chunk is in registers
+            if (!(top == -INFINITY)) {
+                st.m = max_nan(st.m, top);
+                if (far_above(st, top, c)) rebase(st, top, c);
+                float sum = 0.f;
+                const bool plain = fabsf(st.b) < NEAR_END;
 #pragma unroll
-            for (int u = 1; u < U; ++u)
-                if (lm[u] > x) {
-                    x = lm[u];
-                    vb = cur[u];
-                    u_best = u;
+                for (int u = 0; u < U; ++u) {
+                    float f[NV];
+                    unpack<T>(cur[u], f);
+                    if (plain) {
+#pragma unroll
+                        for (int e = 0; e < NV; ++e) f[e] = ex2_approx(fmaf(f[e], c, st.b));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < NV; ++e) f[e] = f[e] == st.ref ? 1.f : 0.f;
+                    }
+                    if constexpr (MASK) {
+#pragma unroll
+                        for (int e = 0; e < NV; ++e)
+                            if (!((bits >> (u * NV + e)) & 1u)) f[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int h = NV / 2; h; h >>= 1)
+#pragma unroll
+                        for (int e = 0; e < h; ++e) f[e] += f[e + h];
+                    sum += f[0];
                 }
-            if (x > -INFINITY) {
-                float f[NV];
-                unpack<T>(vb, f);
-                int e_best = 0;
+                add_z(st, sum);
+            }
+            const auto token = [&](int x) { return it.v0 + (base + (x / NV) * NT + t) * NV + x % NV; };   // of value x
+            if (j == 0) {
+                // the first threshold, from each thread's best
+                Key best = one > -INFINITY ? key_of(one, one_v) : 0;
+                int u_best = 0;
+                uint4 vb = cur[0];
+                float x = lm[0];
 #pragma unroll
-                for (int e = NV - 1; e >= 0; --e)
-                    if (f[e] == x && ((bits >> (u_best * NV + e)) & 1u)) e_best = e;
-                const Key k = key_of(x + 0.f, token(u_best * NV + e_best));
-                best = k > best ? k : best;
+                for (int u = 1; u < U; ++u)
+                    if (lm[u] > x) {
+                        x = lm[u];
+                        vb = cur[u];
+                        u_best = u;
+                    }
+                if (x > -INFINITY) {
+                    float f[NV];
+                    unpack<T>(vb, f);
+                    int e_best = 0;
+#pragma unroll
+                    for (int e = NV - 1; e >= 0; --e)
+                        if (f[e] == x && ((bits >> (u_best * NV + e)) & 1u)) e_best = e;
+                    const Key q = key_of(x + 0.f, token(u_best * NV + e_best));
+                    best = q > best ? q : best;
+                }
+                limit = nth_of_groups(best, a.n_out, s_keys, &s_nth);
+                if (limit) limit_x = value_of(static_cast<uint32_t>(limit >> 32));
             }
-            const Key nth = nth_of_groups(best, a.n_out, s_keys, &s_nth);
-            if (nth > limit) {
-                limit = nth;
-                limit_x = value_of(static_cast<uint32_t>(nth >> 32));
+            // keys from the limit on go to the buffer
+            if (fmaxf(top, j == 0 ? one : top) >= limit_x) {
+                uint32_t hits = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (lm[u] >= limit_x && lm[u] > -INFINITY) {
+                        float f[NV];
+                        unpack<T>(cur[u], f);
+#pragma unroll
+                        for (int e = 0; e < NV; ++e)
+                            if (f[e] >= limit_x && f[e] > -INFINITY) hits |= 1u << (u * NV + e);
+                    }
+                hits &= bits;
+                bool last = j == 0 && one >= limit_x && one > -INFINITY;
+                while (hits || last) {
+                    int v = one_v;
+                    if (hits) {
+                        v = token(__ffs(hits) - 1);
+                        hits &= hits - 1;
+                    } else {
+                        last = false;
+                    }
+                    const Key q = key_of(beam_f(it.row[v]), v);      // (read again: a hit is rare)
+                    if (q < limit) continue;
+                    const int at = atomicAdd(&s_cnt, 1);
+                    if (at < a.cap) buf[at] = q;
+                    else s_over = 1;
+                }
             }
-        };
-        if (base == 0) raise();
-        if (__syncthreads_or(fmaxf(top, base == 0 ? one : top) >= limit_x ? push() : false)) {
-            // over: take the chunk back, cut the buffer to its best, raise the threshold, put the
-            // chunk in again (what passes now fits: n groups' keys beside n)
-            const int cnt = min(s_cnt, a.cap);
-            const int first = v0 + base * NV, past = first + CHUNK * NV;
-            for (int i = t; i < cnt; i += NT) {
-                const int v = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[i]));
-                if ((v >= first && v < past) || (base == 0 && v >= tail)) buf[i] = 0;
+            if (j && (j & (j + 1)) == 0 && j + 1 < chunks) {
+                block_sync();
+                if (!s_over) {
+                    const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
+                    if (kept == a.n_out && buf[kept - 1] > limit) {
+                        limit = buf[kept - 1];
+                        limit_x = value_of(static_cast<uint32_t>(limit >> 32));
+                    }
+                    if (t == 0) s_cnt = kept;
+                    block_sync();
+                }
             }
-            __syncthreads();
-            const int kept = keep_best(buf, tmp, cnt, a.n_out, s_keys, &s_nth, &s_kept);
-            if (kept == a.n_out && buf[kept - 1] > limit) {
-                limit = buf[kept - 1];
-                limit_x = value_of(static_cast<uint32_t>(limit >> 32));
-            }
-            raise();
-            if (t == 0) s_cnt = kept;
-            __syncthreads();
-            push();
-            __syncthreads();
         }
-    }
-    __syncthreads();
-    const int kept = keep_best(buf, tmp, min(s_cnt, a.cap), a.n_out, s_keys, &s_nth, &s_kept);
-    const int64_t at = static_cast<int64_t>(r) * a.n_split + split;
-    for (int j = t; j < a.n_out; j += NT)
-        a.cand[at * a.n_out + j] = j < kept ? BeamCand{value_of(static_cast<uint32_t>(buf[j] >> 32)),
-                                                       static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[j]))}
-                                            : BeamCand{0.f, -1};
-    // the split's sum, against the base of its largest logit
-    float m = st.m;
-    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if ((t & 31) == 0) s_m[t >> 5] = m;
-    __syncthreads();
-    m = s_m[0];
-    for (int i = 1; i < WARPS; ++i) m = max_nan(m, s_m[i]);
-    const double top = static_cast<double>(m) * c;
-    double z = 0.0;
-    if (st.ref > -INFINITY) z = (static_cast<double>(st.z) + st.lost) * ex2_approx(static_cast<float>(base_of(st, c) - top));
-    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-    if ((t & 31) == 0) s_z[t >> 5] = z;
-    __syncthreads();
-    if (t == 0) {
-        for (int i = 1; i < WARPS; ++i) z += s_z[i];
-        a.stat[at] = BeamStat{m < INFINITY ? z : NAN, m, 0};
+        block_sync();
+        int cnt = s_cnt;
+        if (s_over) cnt = best_by_steps<T, MASK>(a, it, buf, tmp, s_keys, &s_nth, &s_cnt, &s_kept);
+        const int kept = keep_best(buf, tmp, cnt, a.n_out, s_keys, &s_nth, &s_kept);
+        for (int i = t; i < a.n_out; i += NT)
+            a.cand[static_cast<int64_t>(item) * a.n_out + i] =
+                i < kept ? BeamCand{value_of(static_cast<uint32_t>(buf[i] >> 32)),
+                                    static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[i]))}
+                         : BeamCand{0.f, -1};
+        // the split's sum, against the base of its largest logit
+        float m = st.m;
+        for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (lane == 0) s_m[t >> 5] = m;
+        block_sync();
+        m = s_m[0];
+        for (int i = 1; i < WARPS; ++i) m = max_nan(m, s_m[i]);
+        const double top = static_cast<double>(m) * c;
+        double z = 0.0;
+        if (st.ref > -INFINITY)
+            z = (static_cast<double>(st.z) + st.lost) * ex2_approx(static_cast<float>(base_of(st, c) - top));
+        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+        if (lane == 0) s_z[t >> 5] = z;
+        block_sync();
+        if (t == 0) {
+            for (int i = 1; i < WARPS; ++i) z += s_z[i];
+            a.stat[item] = BeamStat{m < INFINITY ? z : NAN, m, 0};
+        }
     }
 }
 
@@ -500,6 +645,7 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
     __shared__ int s_cnt, s_kept;
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (b == 0 && t == 0) *a.next = 0;                 // for the workspace's next call
     for (int k = warp; k < a.beams; k += WARPS) {
         const int r = b * a.beams + k;
         const float start = a.scores[r];
@@ -660,19 +806,19 @@ __global__ void beam_gather_kernel(int64_t n_src, int64_t n_dst, int64_t words, 
 
 } // namespace
 
-// Three blocks of the rows kernel fit an SM.  Few rows are cut so that one
-// wave of blocks covers the GPU, no split below 4096 tokens (a block's fixed
-// work, its two thresholds, is about that of 4096 tokens); many rows are cut
-// where that fills the last wave better.
+// Blocks take items as they get free.  A row is cut where that makes the last
+// round of items fuller; an item's fixed work (its thresholds and lists) is
+// about that of 6000 tokens, and none is below 4096.
+constexpr int ROW_BLOCKS = 3 * 152;
 int beam_splits(int64_t rows, int64_t vocab)
 {
-    const int64_t wave = 3 * 152;
     int64_t most = vocab / 4096;
     most = most < 1 ? 1 : most > 64 ? 64 : most;
     int64_t best = 1;
     double cost = 0.0;
     for (int64_t n = 1; n <= most; ++n) {
-        const double c = static_cast<double>((rows * n + wave - 1) / wave) * (static_cast<double>(vocab) / n + 4096.0);
+        const double c = static_cast<double>((rows * n + ROW_BLOCKS - 1) / ROW_BLOCKS) *
+                         (static_cast<double>(vocab) / n + 6000.0);
         if (n == 1 || c < cost * 0.97) {
             cost = c;
             best = n;
@@ -681,22 +827,22 @@ int beam_splits(int64_t rows, int64_t vocab)
     return static_cast<int>(best);
 }
 
-// Keys the rows kernel's buffer holds: the n best, and what passes a chunk's
-// threshold at most (a group's every key, for n groups).
+// Keys the rows kernel's buffer holds: what passes one step's threshold of
+// best_by_steps at most (n groups' every key) beside the n best, and room for
+// a first chunk of random logits.
 int beam_cap(int dtype, int n_out)
 {
-    const int per = (dtype == LOSSK_F32 ? 4 : 8) * U + 1;
-    const int keys = n_out * (NT / groups_for(n_out)) * per;
-    return n_out + (keys < NT * per ? keys : NT * per);
+    const int keys = n_out + n_out * (NT / groups_for(n_out)) * (dtype == LOSSK_F32 ? 4 : 8);
+    return keys > 1024 ? keys : 1024;
 }
 
 template <typename T, bool MASK> cudaError_t launch_rows(const BeamArgs &a, cudaStream_t st)
 {
-    const size_t bytes = 2 * sizeof(Key) * static_cast<size_t>(a.cap);
+    const size_t bytes = STAGES * STAGE_BYTES + 2 * sizeof(Key) * static_cast<size_t>(a.cap);
     const cudaError_t e = raise_smem<beam_rows_kernel<T, MASK>>(bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(a.batch) * a.beams, a.n_split);
-    beam_rows_kernel<T, MASK><<<grid, NT, bytes, st>>>(a);
+    const int64_t items = static_cast<int64_t>(a.batch) * a.beams * a.n_split;
+    beam_rows_kernel<T, MASK><<<static_cast<unsigned>(items < ROW_BLOCKS ? items : ROW_BLOCKS), NT + 32, bytes, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -226,6 +226,8 @@ int32_t lossk_beam_select(int64_t batch, int64_t beams, int64_t vocab, int64_t n
     a.lse_out = lse_out;
     a.stat = reinterpret_cast<BeamStat *>(ws + L.off_stat);
     a.cand = reinterpret_cast<BeamCand *>(ws + L.off_cand);
+    a.next = &static_cast<WsHeader *>(workspace)->pad[HDR_NEXT];
+    a.err = &static_cast<WsHeader *>(workspace)->err;
     a.fault = fault_of(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     {

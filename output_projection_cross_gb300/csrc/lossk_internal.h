@@ -26,9 +26,10 @@ struct WsHeader {
     int bad_targets;  // count of targets outside [0, vocab)
     int n_valid;      // counted tokens
     int redo;         // fused pass: a row left the range its reference shift covers
-    int pad[60];      // pad[HDR_FAULT]: what a decoding call found wrong on the device (a lossk_status)
+    int pad[60];      // decoding calls: pad[HDR_FAULT] what was found wrong on the device (a
+                      // lossk_status), pad[HDR_NEXT] a work counter, 0 between calls
 };
-constexpr int HDR_FAULT = 1;
+constexpr int HDR_FAULT = 1, HDR_NEXT = 2;
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
 // Per-(token, logit tile) partial statistics written by the forward pass
