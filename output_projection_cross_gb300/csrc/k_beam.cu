@@ -92,13 +92,14 @@ template <typename K> __device__ __forceinline__ K nth_of_groups(K mine, int n, 
     if (t == 0) *s_nth = K{};
     if (t % per == 0) s_keys[t / per] = mine;
     block_sync();
-    if (t < groups) {
-        mine = s_keys[t];
-        int above = 0;
+    // `per` threads count the keys above each group's, a part each
+    mine = s_keys[t / per];
+    int above = 0;
+    const int part = groups / per, first = (t % per) * part;
 #pragma unroll 8
-        for (int i = 0; i < groups; ++i) above += s_keys[i] > mine;
-        if (above == n - 1 && !is_none(mine)) *s_nth = mine;
-    }
+    for (int i = 0; i < part; ++i) above += s_keys[first + i] > mine;
+    for (int o = 1; o < per; o <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+    if (t % per == 0 && above == n - 1 && !is_none(mine)) *s_nth = mine;
     block_sync();
     return *s_nth;
 }
@@ -143,6 +144,7 @@ template <> struct Elem<h16_t> {
 constexpr int U = 4;                       // 16-byte vectors a thread holds of a chunk
 constexpr int CHUNK = NT * U;
 constexpr int STAGES = 3, STAGE_BYTES = (CHUNK + 1) * 16;
+constexpr int STEADY = 32;
 
 __device__ __forceinline__ float beam_f(float x) { return x + 0.f; }   // -0 to +0: they tie
 __device__ __forceinline__ float beam_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16) + 0.f; }
@@ -373,11 +375,12 @@ __device__ __noinline__ int best_by_steps(const BeamArgs &a, const Item<T> &it, 
 // warp takes items from a common counter and keeps a ring of STAGES chunks
 // full with bulk copies, across items, so that the ends of one item (its
 // threshold, its lists) cost no memory time.  In a chunk a thread has U
-// vectors; the working warps meet at a barrier only for thresholds: after the
-// first chunk, and after the 2nd, 4th, 8th ..., where the buffer is cut to its n
-// best (of random logits a chunk then brings n / (chunks so far) keys).  Keys
-// that do not fit the buffer are dropped, and the item's best are found by
-// best_by_steps instead.
+// vectors; the working warps meet at a barrier only for thresholds.  The first
+// chunk's threshold stays for the item while n <= STEADY (of random logits
+// every chunk then brings n keys, at most 19 chunks; cutting the buffer cost
+// 17 us of 127 at 896 rows of 151936 with n = 16); for larger n the buffer is
+// cut to its n best after the 2nd, 4th, 8th ... chunk.  Keys that do not fit
+// the buffer are dropped, and the item's best are found by best_by_steps.
 template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK ? 2 : 3) beam_rows_kernel(BeamArgs a)
 {
     constexpr int NV = Elem<T>::NV;
@@ -477,10 +480,17 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
             for (int u = 0; u < U; ++u) {
                 const int i = u * NT + t;
                 cur[u] = all_low<T>();
-                if (base + i < it.n_vec) {
-                    cur[u] = tile[i];
-                    if (it.skew) cur[u] = joined(cur[u], tile[i + 1], it.skew);
+                if (base + i < it.n_vec) cur[u] = tile[i];
+            }
+            if (it.skew) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = u * NT + t;
+                    if (base + i < it.n_vec) cur[u] = joined(cur[u], tile[i + 1], it.skew);
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
                 if constexpr (MASK) {
                     float f[NV];
                     unpack<T>(cur[u], f);
@@ -493,35 +503,29 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                 }
                 top = max_nan(top, lm[u]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[sg]);  // the chunk is in registers
             if (!(top == -INFINITY)) {
                 st.m = max_nan(st.m, top);
                 if (far_above(st, top, c)) rebase(st, top, c);
                 float sum = 0.f;
-                const bool plain = fabsf(st.b) < NEAR_END;
+                const auto add = [&](auto term) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float f[NV];
-                    unpack<T>(cur[u], f);
-                    if (plain) {
+                    for (int u = 0; u < U; ++u) {
+                        float f[NV];
+                        unpack<T>(cur[u], f);
 #pragma unroll
-                        for (int e = 0; e < NV; ++e) f[e] = ex2_approx(fmaf(f[e], c, st.b));
-                    } else {
+                        for (int e = 0; e < NV; ++e) {
+                            f[e] = term(f[e]);
+                            if (MASK && !((bits >> (u * NV + e)) & 1u)) f[e] = 0.f;
+                        }
 #pragma unroll
-                        for (int e = 0; e < NV; ++e) f[e] = f[e] == st.ref ? 1.f : 0.f;
+                        for (int h = NV / 2; h; h >>= 1)
+#pragma unroll
+                            for (int e = 0; e < h; ++e) f[e] += f[e + h];
+                        sum += f[0];
                     }
-                    if constexpr (MASK) {
-#pragma unroll
-                        for (int e = 0; e < NV; ++e)
-                            if (!((bits >> (u * NV + e)) & 1u)) f[e] = 0.f;
-                    }
-#pragma unroll
-                    for (int h = NV / 2; h; h >>= 1)
-#pragma unroll
-                        for (int e = 0; e < h; ++e) f[e] += f[e + h];
-                    sum += f[0];
-                }
+                };
+                if (fabsf(st.b) < NEAR_END) add([&](float x) { return ex2_approx(fmaf(x, c, st.b)); });
+                else add([&](float x) { return x == st.ref ? 1.f : 0.f; });
                 add_z(st, sum);
             }
             const auto token = [&](int x) { return it.v0 + (base + (x / NV) * NT + t) * NV + x % NV; };   // of value x
@@ -566,21 +570,27 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                 hits &= bits;
                 bool last = j == 0 && one >= limit_x && one > -INFINITY;
                 while (hits || last) {
+                    float x = one;
                     int v = one_v;
                     if (hits) {
-                        v = token(__ffs(hits) - 1);
+                        // (read again, by its place: a hit is rare)
+                        const int b = __ffs(hits) - 1;
                         hits &= hits - 1;
+                        v = token(b);
+                        x = beam_f(reinterpret_cast<const T *>(smem + sg * STAGE_BYTES + it.skew)[v - it.v0 - base * NV]);
                     } else {
                         last = false;
                     }
-                    const Key q = key_of(beam_f(it.row[v]), v);      // (read again: a hit is rare)
+                    const Key q = key_of(x, v);
                     if (q < limit) continue;
                     const int at = atomicAdd(&s_cnt, 1);
                     if (at < a.cap) buf[at] = q;
                     else s_over = 1;
                 }
             }
-            if (j && (j & (j + 1)) == 0 && j + 1 < chunks) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[sg]);  // this warp is done with the chunk
+            if (a.n_out > STEADY && j && (j & (j + 1)) == 0 && j + 1 < chunks) {
                 block_sync();
                 if (!s_over) {
                     const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
