@@ -11,12 +11,12 @@ namespace lossk {
 __device__ __forceinline__ void raise_fault(int *fault, int status) { atomicMax(fault, status); }
 
 // ---- beam selection ------------------------------------------------------------
-// What the rows kernel leaves per (row, split): the largest kept logit m, the
-// sum z of 2^(c (x - m)) over the kept logits (NaN where one of them is a NaN
-// or +infinity), and the split's n_out best (logit, token) pairs in falling
-// order, token -1 filling the places left.
+// What the rows kernel leaves per (row, split): the largest kept logit m; the
+// sum z of 2^(c x - base) over the kept logits, c = log2(e) / T (NaN where one
+// of them is a NaN or +infinity); and the split's n_out best (logit, token)
+// pairs in falling order, token -1 filling the places left.
 struct BeamStat {
-    double z;
+    double z, base;
     float m;
     int pad;
 };

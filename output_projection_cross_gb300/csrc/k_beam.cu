@@ -203,28 +203,29 @@ struct RowStat {
 };
 constexpr float FAR = 24.f, NEAR_END = 1e37f;
 
-// log2 of what the sum has to be multiplied by.
-__device__ __forceinline__ double base_of(const RowStat &r, float c)
+__device__ __forceinline__ bool plain(float b) { return fabsf(b) < NEAR_END; }
+// 2^(the base of a sum (ref, b) - the base `top` of one at least as high)
+__device__ __forceinline__ float to_base(float ref, float b, float top_ref, float top_b)
 {
-    return fabsf(r.b) < NEAR_END ? -static_cast<double>(r.b) : static_cast<double>(r.ref) * c;
+    return plain(top_b) ? (plain(b) ? ex2_approx(top_b - b) : 0.f) : ref == top_ref ? 1.f : 0.f;
 }
 __device__ __forceinline__ void rebase(RowStat &r, float lm, float c)
 {
-    RowStat n = r;
-    n.ref = lm;
-    n.b = -lm * c;
+    const float b = -lm * c;
     if (r.ref > -INFINITY) {
-        const float g = ex2_approx(static_cast<float>(base_of(r, c) - base_of(n, c)));
-        n.z *= g;
-        n.lost *= g;
+        const float g = to_base(r.ref, r.b, lm, b);
+        r.z *= g;
+        r.lost *= g;
     }
-    r = n;
+    r.ref = lm;
+    r.b = b;
 }
-__device__ __forceinline__ void add_z(RowStat &r, float x)
+// (z, lost) += (x, rest)
+__device__ __forceinline__ void add_z(float &z, float &lost, float x, float rest)
 {
-    const float s = r.z + x, b = s - r.z;
-    r.lost += (r.z - (s - b)) + (x - b);
-    r.z = s;
+    const float s = z + x, y = s - z;
+    lost += (z - (s - y)) + (x - y) + rest;
+    z = s;
 }
 __device__ __forceinline__ bool far_above(const RowStat &r, float lm, float c)
 {
@@ -294,6 +295,20 @@ template <typename T> struct Item {
     }
     __device__ __forceinline__ int chunks() const { return n_vec > CHUNK ? (n_vec + CHUNK - 1) / CHUNK : 1; }
 };
+
+// mbar_wait, asleep for up to 20 us at a try: the block's warps wait for memory
+// most of the time, and a warp that polls takes issue slots from those that work.
+__device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, int *err)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+                 : "memory");
+    if (!ok) mbar_wait(bar, parity, err);
+}
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
@@ -388,8 +403,8 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
     Key *buf = reinterpret_cast<Key *>(smem + STAGES * STAGE_BYTES), *tmp = buf + a.cap;
     __shared__ __align__(8) uint64_t s_full[STAGES], s_empty[STAGES];
     __shared__ Key s_keys[NT], s_nth;
-    __shared__ double s_z[WARPS];
-    __shared__ float s_m[WARPS];
+    __shared__ float4 s_part[WARPS];
+    __shared__ float2 s_z[WARPS];
     __shared__ int s_item[STAGES], s_cnt, s_kept, s_over;
     const int t = threadIdx.x, lane = t & 31;
     if (t == 0) {
@@ -407,7 +422,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
         // an expired wait leaves its error and the loop runs on without waiting
         auto stage = [&] {
             const int st = k % STAGES;
-            if (k >= STAGES) mbar_wait(&s_empty[st], (k / STAGES - 1) & 1, a.err);
+            if (k >= STAGES) wait_for(&s_empty[st], (k / STAGES - 1) & 1, a.err);
             ++k;
             return st;
         };
@@ -432,7 +447,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
         s_item[st] = -1;
         mbar_arrive(&s_full[st]);
         // no copy of this block is in flight when it ends
-        for (int i = max(k - STAGES, 0); i < k; ++i) mbar_wait(&s_full[i % STAGES], (i / STAGES) & 1, a.err);
+        for (int i = max(k - STAGES, 0); i < k; ++i) wait_for(&s_full[i % STAGES], (i / STAGES) & 1, a.err);
         return;
     }
 
@@ -440,23 +455,16 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
     const int words = (a.vocab + 31) >> 5;
     int k = 0;                                         // stages used so far
     while (true) {
-        mbar_wait(&s_full[k % STAGES], (k / STAGES) & 1, a.err);
+        wait_for(&s_full[k % STAGES], (k / STAGES) & 1, a.err);
         const int item = s_item[k % STAGES];
         if (item < 0) return;
         const Item<T> it(a, item);
         const uint32_t *allow = MASK ? a.allow + it.r * a.allow_stride : nullptr;
         if (t == 0) s_cnt = s_over = 0;
         RowStat st{-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
-        float one = -INFINITY;
+        float one = -INFINITY;                         // used after the first chunk's sum
         const int one_v = it.tail + t;
-        if (one_v < it.v1 && (!MASK || (allow[one_v >> 5] >> (one_v & 31)) & 1u)) {
-            one = beam_f(it.row[one_v]);
-            st.m = one;
-            if (!(one == -INFINITY)) {
-                rebase(st, one, c);
-                st.z = 1.f;
-            }
-        }
+        if (one_v < it.v1 && (!MASK || (allow[one_v >> 5] >> (one_v & 31)) & 1u)) one = beam_f(it.row[one_v]);
         Key limit = 0;                                 // keys below it are not among the best
         float limit_x = -INFINITY;
         const int chunks = it.chunks();
@@ -472,36 +480,46 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                     bits |= (w & ((1u << NV) - 1u)) << (u * NV);
                 }
             }
-            if (j) mbar_wait(&s_full[sg], (k / STAGES) & 1, a.err);
+            if (j) wait_for(&s_full[sg], (k / STAGES) & 1, a.err);
             const uint4 *tile = reinterpret_cast<const uint4 *>(smem + sg * STAGE_BYTES);
             uint4 cur[U];
-            float lm[U], top = -INFINITY;              // each vector's largest, the chunk's
+            if (base + CHUNK <= it.n_vec) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = u * NT + t;
-                cur[u] = all_low<T>();
-                if (base + i < it.n_vec) cur[u] = tile[i];
+                for (int u = 0; u < U; ++u) cur[u] = tile[u * NT + t];
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) cur[u] = base + u * NT + t < it.n_vec ? tile[u * NT + t] : all_low<T>();
             }
             if (it.skew) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = u * NT + t;
-                    if (base + i < it.n_vec) cur[u] = joined(cur[u], tile[i + 1], it.skew);
-                }
+                for (int u = 0; u < U; ++u)
+                    if (base + u * NT + t < it.n_vec) cur[u] = joined(cur[u], tile[u * NT + t + 1], it.skew);
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+            // the largest of vector u, and of the chunk
+            const auto largest = [&](int u) {
                 if constexpr (MASK) {
-                    float f[NV];
+                    float f[NV], x = -INFINITY;
                     unpack<T>(cur[u], f);
-                    lm[u] = -INFINITY;
 #pragma unroll
                     for (int e = 0; e < NV; ++e)
-                        if ((bits >> (u * NV + e)) & 1u) lm[u] = max_nan(lm[u], f[e]);
+                        if ((bits >> (u * NV + e)) & 1u) x = max_nan(x, f[e]);
+                    return x;
                 } else {
-                    lm[u] = vec_max<T>(cur[u]);
+                    return vec_max<T>(cur[u]);
                 }
-                top = max_nan(top, lm[u]);
+            };
+            float top;
+            if constexpr (MASK || sizeof(T) == 4) {
+                top = largest(0);
+#pragma unroll
+                for (int u = 1; u < U; ++u) top = max_nan(top, largest(u));
+            } else {
+                static_assert(U == 4, "the chunk's largest in pairs");
+                const auto both = [](const uint4 &x, const uint4 &y) {
+                    return make_uint4(max_nan2<T>(x.x, y.x), max_nan2<T>(x.y, y.y), max_nan2<T>(x.z, y.z),
+                                      max_nan2<T>(x.w, y.w));
+                };
+                top = vec_max<T>(both(both(cur[0], cur[1]), both(cur[2], cur[3])));
             }
             if (!(top == -INFINITY)) {
                 st.m = max_nan(st.m, top);
@@ -524,32 +542,30 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                         sum += f[0];
                     }
                 };
-                if (fabsf(st.b) < NEAR_END) add([&](float x) { return ex2_approx(fmaf(x, c, st.b)); });
+                if (plain(st.b)) add([&](float x) { return ex2_approx(fmaf(x, c, st.b)); });
                 else add([&](float x) { return x == st.ref ? 1.f : 0.f; });
-                add_z(st, sum);
+                add_z(st.z, st.lost, sum, 0.f);
             }
             const auto token = [&](int x) { return it.v0 + (base + (x / NV) * NT + t) * NV + x % NV; };   // of value x
             if (j == 0) {
+                if (!(one == -INFINITY)) {
+                    st.m = max_nan(st.m, one);
+                    if (far_above(st, one, c)) rebase(st, one, c);
+                    add_z(st.z, st.lost, plain(st.b) ? ex2_approx(fmaf(one, c, st.b)) : one == st.ref ? 1.f : 0.f, 0.f);
+                }
                 // the first threshold, from each thread's best
                 Key best = one > -INFINITY ? key_of(one, one_v) : 0;
-                int u_best = 0;
-                uint4 vb = cur[0];
-                float x = lm[0];
+                if (top > -INFINITY) {
+                    int at = -1;
 #pragma unroll
-                for (int u = 1; u < U; ++u)
-                    if (lm[u] > x) {
-                        x = lm[u];
-                        vb = cur[u];
-                        u_best = u;
+                    for (int u = U - 1; u >= 0; --u) {
+                        float f[NV];
+                        unpack<T>(cur[u], f);
+#pragma unroll
+                        for (int e = NV - 1; e >= 0; --e)
+                            if (f[e] == top && ((bits >> (u * NV + e)) & 1u)) at = u * NV + e;
                     }
-                if (x > -INFINITY) {
-                    float f[NV];
-                    unpack<T>(vb, f);
-                    int e_best = 0;
-#pragma unroll
-                    for (int e = NV - 1; e >= 0; --e)
-                        if (f[e] == x && ((bits >> (u_best * NV + e)) & 1u)) e_best = e;
-                    const Key q = key_of(x + 0.f, token(u_best * NV + e_best));
+                    const Key q = at >= 0 ? key_of(top + 0.f, token(at)) : 0;    // (none: a NaN was the largest)
                     best = q > best ? q : best;
                 }
                 limit = nth_of_groups(best, a.n_out, s_keys, &s_nth);
@@ -560,7 +576,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                 uint32_t hits = 0;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (lm[u] >= limit_x && lm[u] > -INFINITY) {
+                    if (!(largest(u) < limit_x)) {
                         float f[NV];
                         unpack<T>(cur[u], f);
 #pragma unroll
@@ -612,23 +628,42 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                 i < kept ? BeamCand{value_of(static_cast<uint32_t>(buf[i] >> 32)),
                                     static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[i]))}
                          : BeamCand{0.f, -1};
-        // the split's sum, against the base of its largest logit
-        float m = st.m;
-        for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (lane == 0) s_m[t >> 5] = m;
+        // the split's sum: every thread's brought to the highest base, then added up in two floats
+        // (a double addition runs at a sixty-fourth of a float's rate)
+        float m = st.m, ref = st.ref, bb = st.b;
+        auto higher = [&](float x, float y) {
+            if (x > ref) {
+                ref = x;
+                bb = y;
+            }
+        };
+        for (int o = 16; o; o >>= 1) {
+            m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            higher(__shfl_xor_sync(0xFFFFFFFFu, ref, o), __shfl_xor_sync(0xFFFFFFFFu, bb, o));
+        }
+        if (lane == 0) s_part[t >> 5] = make_float4(m, ref, bb, 0.f);
         block_sync();
-        m = s_m[0];
-        for (int i = 1; i < WARPS; ++i) m = max_nan(m, s_m[i]);
-        const double top = static_cast<double>(m) * c;
-        double z = 0.0;
-        if (st.ref > -INFINITY)
-            z = (static_cast<double>(st.z) + st.lost) * ex2_approx(static_cast<float>(base_of(st, c) - top));
-        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-        if (lane == 0) s_z[t >> 5] = z;
+        for (int i = 0; i < WARPS; ++i) {
+            const float4 x = s_part[i];
+            m = max_nan(m, x.x);
+            higher(x.y, x.z);
+        }
+        float z = 0.f, lost = 0.f;
+        if (st.ref > -INFINITY) {
+            const float g = to_base(st.ref, st.b, ref, bb);
+            z = st.z * g;
+            lost = st.lost * g;
+        }
+        for (int o = 16; o; o >>= 1) {
+            const float x = __shfl_xor_sync(0xFFFFFFFFu, z, o), y = __shfl_xor_sync(0xFFFFFFFFu, lost, o);
+            add_z(z, lost, x, y);
+        }
+        if (lane == 0) s_z[t >> 5] = make_float2(z, lost);
         block_sync();
         if (t == 0) {
-            for (int i = 1; i < WARPS; ++i) z += s_z[i];
-            a.stat[item] = BeamStat{m < INFINITY ? z : NAN, m, 0};
+            for (int i = 1; i < WARPS; ++i) add_z(z, lost, s_z[i].x, s_z[i].y);
+            a.stat[item] = BeamStat{m < INFINITY ? static_cast<double>(z) + lost : NAN,
+                                    plain(bb) ? -static_cast<double>(bb) : static_cast<double>(ref) * c, m, 0};
         }
     }
 }
@@ -669,15 +704,23 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
         if (kind == 2) {
             const BeamStat *st = a.stat + static_cast<int64_t>(r) * a.n_split;
             float m = -INFINITY;
-            for (int i = lane; i < a.n_split; i += 32) m = fmaxf(m, st[i].m);
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            double top = -INFINITY;                    // the highest base
+            for (int i = lane; i < a.n_split; i += 32) {
+                m = fmaxf(m, st[i].m);
+                if (st[i].z != 0.0) top = fmax(top, st[i].base);
+            }
+            for (int o = 16; o; o >>= 1) {
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                const double x = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+                top = x > top ? x : top;
+            }
             double z = 0.0;
-            const double top = static_cast<double>(m) * a.c;
             for (int i = lane; i < a.n_split; i += 32)
-                if (st[i].z != 0.0) z += st[i].z * ex2_approx(static_cast<float>(static_cast<double>(st[i].m) * a.c - top));
+                if (st[i].z != 0.0) z += st[i].z * ex2_approx(static_cast<float>(st[i].base - top));
             for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
             if (isnan(z) && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
-            if (z > 0.0) lse = static_cast<double>(m) * a.inv_t + log(z);
+            // (the logits' own scale 1 / T about their largest; c about that)
+            if (z > 0.0) lse = static_cast<double>(m) * a.inv_t + (log(z) + LN2 * (top - static_cast<double>(m) * a.c));
             else kind = 0;
         }
         if (lane == 0) {
@@ -817,9 +860,10 @@ __global__ void beam_gather_kernel(int64_t n_src, int64_t n_dst, int64_t words, 
 } // namespace
 
 // Blocks take items as they get free.  A row is cut where that makes the last
-// round of items fuller; an item's fixed work (its thresholds and lists) is
-// about that of 6000 tokens, and none is below 4096.
+// round of items fuller; an item's fixed work (its thresholds, lists and
+// sums) is about that of ITEM_TOKENS tokens, and none is below 4096.
 constexpr int ROW_BLOCKS = 3 * 152;
+constexpr double ITEM_TOKENS = 32000.0;
 int beam_splits(int64_t rows, int64_t vocab)
 {
     int64_t most = vocab / 4096;
@@ -828,7 +872,7 @@ int beam_splits(int64_t rows, int64_t vocab)
     double cost = 0.0;
     for (int64_t n = 1; n <= most; ++n) {
         const double c = static_cast<double>((rows * n + ROW_BLOCKS - 1) / ROW_BLOCKS) *
-                         (static_cast<double>(vocab) / n + 6000.0);
+                         (static_cast<double>(vocab) / n + ITEM_TOKENS);
         if (n == 1 || c < cost * 0.97) {
             cost = c;
             best = n;
