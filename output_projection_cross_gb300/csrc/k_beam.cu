@@ -386,8 +386,8 @@ __device__ __noinline__ int best_by_steps(const BeamArgs &a, const Item<T> &it, 
     return *s_cnt;
 }
 
-// Persistent blocks of eight warps that work and one that loads.  The loading
-// warp takes items from a common counter and keeps a ring of STAGES chunks
+// Persistent blocks of eight warps that work and one that loads.  After a
+// block's first item the loading warp takes items from a common counter; it keeps a ring of STAGES chunks
 // full with bulk copies, across items, so that the ends of one item (its
 // threshold, its lists) cost no memory time.  In a chunk a thread has U
 // vectors; the working warps meet at a barrier only for thresholds.  The first
@@ -427,7 +427,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
             return st;
         };
         const int items = a.batch * a.beams * a.n_split;
-        for (int i; (i = atomicAdd(a.next, 1)) < items;) {
+        for (int i = blockIdx.x; i < items; i = gridDim.x + atomicAdd(a.next, 1)) {
             const Item<T> it(a, i);
             if (!beam_reads(a, it.r)) continue;
             for (int c = 0; c < it.chunks(); ++c) {
@@ -662,92 +662,110 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
         block_sync();
         if (t == 0) {
             for (int i = 1; i < WARPS; ++i) add_z(z, lost, s_z[i].x, s_z[i].y);
-            a.stat[item] = BeamStat{m < INFINITY ? static_cast<double>(z) + lost : NAN,
-                                    plain(bb) ? -static_cast<double>(bb) : static_cast<double>(ref) * c, m, 0};
+            a.stat[item] = BeamStat{m < INFINITY ? z : NAN, lost, m, ref, bb};
         }
     }
 }
 
-// A row's logit as the rows kernel reads it.
-template <typename T> __device__ __forceinline__ float logit(const BeamArgs &a, int r, int tok)
-{
-    return beam_f(static_cast<const T *>(a.logits)[r * a.row_stride + tok]);
-}
-constexpr int MERGE_U = 4;                 // candidates a thread ranks at once (one, where that is enough)
-
 // ---- merge -------------------------------------------------------------------------
-// One block per batch entry: a warp per beam for its log-sum-exp and for the
-// join of its splits' lists; then every beam's candidates ranked.
+// One block per batch entry.  A warp per beam joins the sums and lists of its
+// splits; lane k of the first warps then forms beam k's log-sum-exp and
+// divisor in double; then every beam's candidates are ranked.  Doubles run at a
+// sixty-fourth of a float's rate here, so only what orders the beams is one:
+// a logarithm and a power per beam, a product and two sums per candidate.
+constexpr int MERGE_U = 4;                 // candidates a thread ranks at once, where one is not enough
+
+struct BeamRow {
+    float z, lost, m, ref, b, start;
+    int kind, len;                         // kind 0: no candidates, 1: its own (finished), 2: the row's
+};
+
+__device__ __forceinline__ void put_out(const BeamArgs &a, int b, int j, int k, int64_t tok, double score, bool was, int len)
+{
+    const int64_t o = static_cast<int64_t>(b) * a.n_out + j;
+    a.parent_out[o] = k;
+    a.token_out[o] = tok;
+    a.score_out[o] = static_cast<float>(score);
+    if (a.finished_out) a.finished_out[o] = k >= 0 && (was || tok == a.end_token);
+    if (a.length_out) a.length_out[o] = len;
+}
+
 __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     RankKey *buf = reinterpret_cast<RankKey *>(smem), *tmp = buf + a.merge_cap;
-    Key *lists = reinterpret_cast<Key *>(tmp + a.merge_cap);           // [beams][n_out] where rows are split
+    Key *lists = reinterpret_cast<Key *>(tmp + a.merge_cap);           // [beams][n_out]
     __shared__ RankKey s_keys[NT], s_nth;
-    __shared__ double s_lse[LOSSK_BEAM_MAX_BEAMS], s_div[LOSSK_BEAM_MAX_BEAMS];
-    __shared__ float s_start[LOSSK_BEAM_MAX_BEAMS];
-    __shared__ int s_kind[LOSSK_BEAM_MAX_BEAMS];       // 0: no candidates, 1: its own (finished), 2: the row's
+    __shared__ BeamRow s_row[LOSSK_BEAM_MAX_BEAMS];
+    __shared__ double s_lse[LOSSK_BEAM_MAX_BEAMS], s_inv[LOSSK_BEAM_MAX_BEAMS];
     __shared__ int s_cnt, s_kept;
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b == 0 && t == 0) *a.next = 0;                 // for the workspace's next call
+    const int all = a.beams * a.n_out;
     for (int k = warp; k < a.beams; k += WARPS) {
         const int r = b * a.beams + k;
         const float start = a.scores[r];
         const bool done = a.finished && a.finished[r];
-        int kind = done ? 1 : 2;
-        double lse = -INFINITY;
-        if (!isfinite(start)) {
-            if (start != -INFINITY && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
-            kind = 0;
-        }
-        if (kind == 2) {
-            const BeamStat *st = a.stat + static_cast<int64_t>(r) * a.n_split;
-            float m = -INFINITY;
-            double top = -INFINITY;                    // the highest base
-            for (int i = lane; i < a.n_split; i += 32) {
-                m = fmaxf(m, st[i].m);
-                if (st[i].z != 0.0) top = fmax(top, st[i].base);
+        const int len = (a.lengths ? a.lengths[r] : 0) + (done ? 0 : 1);
+        BeamRow row{0.f, 0.f, -INFINITY, -INFINITY, 0.f, start, isfinite(start) ? (done ? 1 : 2) : 0, len};
+        if (!isfinite(start) && start != -INFINITY && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
+        if (row.kind == 2) {
+            // lane i has splits i and i + 32
+            BeamStat st[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                st[h] = BeamStat{0.f, 0.f, -INFINITY, -INFINITY, 0.f};
+                if (lane + 32 * h < a.n_split) st[h] = a.stat[static_cast<int64_t>(r) * a.n_split + lane + 32 * h];
+                row.m = fmaxf(row.m, st[h].m);
+                if (st[h].ref > row.ref) {
+                    row.ref = st[h].ref;
+                    row.b = st[h].b;
+                }
             }
             for (int o = 16; o; o >>= 1) {
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                const double x = __shfl_xor_sync(0xFFFFFFFFu, top, o);
-                top = x > top ? x : top;
+                row.m = fmaxf(row.m, __shfl_xor_sync(0xFFFFFFFFu, row.m, o));
+                const float x = __shfl_xor_sync(0xFFFFFFFFu, row.ref, o), y = __shfl_xor_sync(0xFFFFFFFFu, row.b, o);
+                if (x > row.ref) {
+                    row.ref = x;
+                    row.b = y;
+                }
             }
-            double z = 0.0;
-            for (int i = lane; i < a.n_split; i += 32)
-                if (st[i].z != 0.0) z += st[i].z * ex2_approx(static_cast<float>(st[i].base - top));
-            for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-            if (isnan(z) && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
-            // (the logits' own scale 1 / T about their largest; c about that)
-            if (z > 0.0) lse = static_cast<double>(m) * a.inv_t + (log(z) + LN2 * (top - static_cast<double>(m) * a.c));
-            else kind = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (st[h].ref > -INFINITY || isnan(st[h].z)) {
+                    const float g = isnan(st[h].z) ? NAN : to_base(st[h].ref, st[h].b, row.ref, row.b);
+                    add_z(row.z, row.lost, st[h].z * g, st[h].lost * g);
+                }
+            for (int o = 16; o; o >>= 1) {
+                const float x = __shfl_xor_sync(0xFFFFFFFFu, row.z, o), y = __shfl_xor_sync(0xFFFFFFFFu, row.lost, o);
+                add_z(row.z, row.lost, x, y);
+            }
+            if (!(row.z == row.z) && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
+            if (!(row.z > 0.f)) row.kind = 0;
         }
-        if (lane == 0) {
-            const int len = (a.lengths ? a.lengths[r] : 0) + (done ? 0 : 1);
-            if (a.lse_out) a.lse_out[r] = static_cast<float>(lse);
-            s_lse[k] = lse;
-            const double n = len > 1 ? len : 1;
-            s_div[k] = a.length_alpha == 0.0 ? 1.0 : a.length_alpha == 1.0 ? n : pow(n, a.length_alpha);
-            s_start[k] = start;
-            s_kind[k] = kind;
-        }
-        if (kind == 2 && a.n_split > 1) {
-            // the splits' lists, each in falling order: a lane keeps the heads of two
-            const BeamCand *c = a.cand + static_cast<int64_t>(r) * a.n_split * a.n_out;
-            // (the next three are loaded with the head: a pop then rarely waits for memory)
-            int at[2] = {0, 0};
+        if (lane == 0) s_row[k] = row;
+        const BeamCand *c = a.cand + static_cast<int64_t>(r) * a.n_split * a.n_out;
+        auto entry = [&](int i, int j) {
+            if (i >= a.n_split || j >= a.n_out) return Key(0);
+            const BeamCand x = c[i * a.n_out + j];
+            return x.tok >= 0 ? key_of(x.x, x.tok) : Key(0);
+        };
+        if (row.kind != 2) {
+            // a finished beam's candidate is itself (its logit is not used)
+            const int tok = a.end_token < 0 ? 0 : a.end_token;
+            for (int j = lane; j < a.n_out; j += 32) lists[k * a.n_out + j] = row.kind == 1 && j == 0 ? key_of(0.f, tok) : 0;
+        } else if (a.n_split == 1) {
+            for (int j = lane; j < a.n_out; j += 32) lists[k * a.n_out + j] = entry(0, j);
+        } else {
+            // the splits' lists, each in falling order: a lane keeps the heads of two, and the next
+            // three of each (a pop then rarely waits for memory)
+            int at[2] = {4, 4};
             Key q[2][4];
-            auto entry = [&](int h, int j) {
-                const int i = lane + 32 * h;
-                if (i >= a.n_split || j >= a.n_out) return Key(0);
-                const BeamCand x = c[i * a.n_out + j];
-                return x.tok >= 0 ? key_of(x.x, x.tok) : Key(0);
-            };
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q[h][j] = entry(h, j);
+                for (int j = 0; j < 4; ++j) q[h][j] = entry(lane + 32 * h, j);
             for (int j = 0; j < a.n_out; ++j) {
                 const bool second = q[1][0] > q[0][0];
                 const Key mine = second ? q[1][0] : q[0][0];
@@ -763,46 +781,81 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
                             q[h][0] = q[h][1];
                             q[h][1] = q[h][2];
                             q[h][2] = q[h][3];
-                            q[h][3] = entry(h, 4 + at[h]++);
+                            q[h][3] = entry(lane + 32 * h, at[h]++);
                         }
                 }
             }
         }
     }
     if (t == 0) s_cnt = 0;
-    __syncthreads();
-    const int all = a.beams * a.n_out;
+    block_sync();
+    if (t < a.beams) {
+        const BeamRow row = s_row[t];
+        double lse = -INFINITY;
+        if (row.kind == 2) {
+            // the sum's base in log2 units; the logits' own scale 1 / T about their largest, c about that
+            const double base = plain(row.b) ? -static_cast<double>(row.b) : static_cast<double>(row.ref) * a.c;
+            const double m = row.m;
+            lse = m * a.inv_t + (log(static_cast<double>(row.z) + row.lost) + LN2 * (base - m * a.c));
+        }
+        s_lse[t] = lse;
+        const double n = row.len > 1 ? row.len : 1;
+        s_inv[t] = a.length_alpha == 0.0 ? 1.0 : 1.0 / (a.length_alpha == 1.0 ? n : pow(n, a.length_alpha));
+        if (a.lse_out) a.lse_out[b * a.beams + t] = static_cast<float>(lse);
+    }
+    block_sync();
+    // candidate i: its key (none where there is none) and its score
+    auto ranked = [&](int i, double &score) {
+        const int k = i / a.n_out;
+        const Key q = lists[i];
+        score = s_row[k].start;
+        if (!q) return RankKey{};
+        if (s_row[k].kind == 2) score += static_cast<double>(value_of(static_cast<uint32_t>(q >> 32))) * a.inv_t - s_lse[k];
+        const uint32_t tok = 0xFFFFFFFFu - static_cast<uint32_t>(q);
+        return RankKey{order_of(a.length_alpha == 0.0 ? score : score * s_inv[k]),
+                       ~static_cast<uint64_t>(static_cast<int64_t>(k) * a.vocab + tok)};
+    };
+    auto write = [&](int j, int i, double score) {
+        const int k = i / a.n_out;
+        const bool was = s_row[k].kind == 1;
+        put_out(a, b, j, k, was ? a.end_token : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(lists[i])), score,
+                was, s_row[k].len);
+    };
+    auto rest = [&](int from) {
+        for (int j = from + t; j < a.n_out; j += NT) put_out(a, b, j, -1, -1, -INFINITY, false, 0);
+    };
+    if (all <= NT) {
+        // each key's place by counting the better ones, several threads a key
+        double score = 0.0;
+        RankKey mine{};
+        if (t < all) mine = ranked(t, score);
+        s_keys[t] = mine;
+        const int valid = __syncthreads_count(!is_none(mine));
+        int per = 1;
+        while (per * 2 * all <= NT && per < 32) per *= 2;
+        const int key = t / per;
+        int above = 0;
+        if (key < all) {
+            const RankKey x = s_keys[key];
+            for (int i = t % per; i < all; i += per) above += s_keys[i] > x;
+        }
+        for (int o = 1; o < per; o <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+        int *place = reinterpret_cast<int *>(tmp);
+        if (key < all && t % per == 0) place[key] = above;
+        block_sync();
+        if (t < all && !is_none(mine) && place[t] < a.n_out) write(place[t], t, score);
+        rest(valid);
+        return;
+    }
     RankKey limit{};
     for (int base = 0; base < all; base += NT * MERGE_U) {
         RankKey mine[MERGE_U], best{};
 #pragma unroll
         for (int u = 0; u < MERGE_U; ++u) {
-            const int i = base + u * NT + t, k = i / a.n_out, j = i % a.n_out;
-            mine[u] = RankKey{};
-            if (i < all && s_kind[k]) {
-                double s = s_start[k];
-                int tok = -1;
-                if (s_kind[k] == 1) {
-                    if (j == 0) tok = a.end_token < 0 ? 0 : a.end_token;
-                } else {
-                    float x;
-                    if (a.n_split > 1) {
-                        const Key q = lists[i];
-                        x = value_of(static_cast<uint32_t>(q >> 32));
-                        if (q) tok = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(q));
-                    } else {
-                        const BeamCand q = a.cand[static_cast<int64_t>(b) * all + i];
-                        x = q.x;
-                        tok = q.tok;
-                    }
-                    s += static_cast<double>(x) * a.inv_t - s_lse[k];
-                }
-                if (tok >= 0) {
-                    const double rank = a.length_alpha == 0.0 ? s : s / s_div[k];
-                    mine[u] = RankKey{order_of(rank), ~static_cast<uint64_t>(static_cast<int64_t>(k) * a.vocab + tok)};
-                    if (mine[u] > best) best = mine[u];
-                }
-            }
+            const int i = base + u * NT + t;
+            double score;
+            mine[u] = i < all ? ranked(i, score) : RankKey{};
+            if (mine[u] > best) best = mine[u];
         }
         const RankKey nth = nth_of_groups(best, a.n_out, s_keys, &s_nth);
         if (nth > limit) limit = nth;
@@ -810,36 +863,28 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
             // what is kept so far, with the limit it gives
             const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
             if (kept == a.n_out && buf[kept - 1] > limit) limit = buf[kept - 1];
-            __syncthreads();
+            block_sync();
             if (t == 0) s_cnt = kept;
-            __syncthreads();
+            block_sync();
         }
 #pragma unroll
         for (int u = 0; u < MERGE_U; ++u)
             if (!is_none(mine[u]) && !(limit > mine[u])) buf[atomicAdd(&s_cnt, 1)] = mine[u];
-        __syncthreads();
+        block_sync();
     }
     const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
-    for (int j = t; j < a.n_out; j += NT) {
-        const int64_t o = static_cast<int64_t>(b) * a.n_out + j;
-        const bool any = j < kept;
-        const int64_t flat = any ? static_cast<int64_t>(~buf[j].flat) : 0;
-        const int k = static_cast<int>(flat / a.vocab), r = b * a.beams + k;
-        const bool was = any && s_kind[k] == 1;
-        const int tok = was ? a.end_token : static_cast<int>(flat - static_cast<int64_t>(k) * a.vocab);
-        double s = s_start[k];
-        if (any && !was) {
-            // the logit again, for the score
-            const float x = a.dtype == LOSSK_F32 ? logit<float>(a, r, tok)
-                          : a.dtype == LOSSK_BF16 ? logit<uint16_t>(a, r, tok) : logit<h16_t>(a, r, tok);
-            s += static_cast<double>(x) * a.inv_t - s_lse[k];
-        }
-        a.parent_out[o] = any ? k : -1;
-        a.token_out[o] = any ? tok : -1;
-        a.score_out[o] = any ? static_cast<float>(s) : -INFINITY;
-        if (a.finished_out) a.finished_out[o] = any && (was || tok == a.end_token);
-        if (a.length_out) a.length_out[o] = any ? (a.lengths ? a.lengths[r] : 0) + (was ? 0 : 1) : 0;
+    // the candidate again, by its place in its beam's list
+    for (int j = t; j < kept; j += NT) {
+        const int64_t flat = static_cast<int64_t>(~buf[j].flat);
+        const int k = static_cast<int>(flat / a.vocab);
+        const uint32_t tok = static_cast<uint32_t>(flat - static_cast<int64_t>(k) * a.vocab);
+        int i = k * a.n_out;
+        while (0xFFFFFFFFu - static_cast<uint32_t>(lists[i]) != tok) ++i;
+        double score;
+        ranked(i, score);
+        write(j, i, score);
     }
+    rest(kept);
 }
 
 template <typename V>
@@ -911,9 +956,8 @@ cudaError_t launch_beam_merge(const BeamArgs &a0, cudaStream_t st)
 {
     BeamArgs a = a0;
     const int keys = a.n_out * (NT / groups_for(a.n_out)) * MERGE_U, all = a.beams * a.n_out;
-    a.merge_cap = a.n_out + (keys < all ? keys : all);
-    const size_t bytes = 2 * sizeof(RankKey) * static_cast<size_t>(a.merge_cap) +
-                         (a.n_split > 1 ? sizeof(Key) * static_cast<size_t>(all) : 0);
+    a.merge_cap = all <= NT ? NT : a.n_out + (keys < all ? keys : all);
+    const size_t bytes = 2 * sizeof(RankKey) * static_cast<size_t>(a.merge_cap) + sizeof(Key) * static_cast<size_t>(all);
     const cudaError_t e = raise_smem<beam_merge_kernel>(bytes);
     if (e != cudaSuccess) return e;
     return launch_after(true, beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(NT), bytes, st, a);

@@ -35,6 +35,18 @@ def decode_workspace(kind: int, a: int, b: int, c: int = 0, d: int = 0, device=N
     return torch.zeros(nb, dtype=torch.uint8, device=device or "cuda")
 
 
+# These calls take microseconds, so the checks below are kept to attribute reads: a decoding step
+# makes several calls per layer, and building a stream object alone takes 3 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t, stream):
+    """The CUDA stream handle: the given stream's, or the current one of t's device."""
+    if stream is not None or _raw_stream is None:
+        return _stream(stream)
+    return _raw_stream(t.get_device())
+
+
 def _on_gpu(t, name, dtype=None, contiguous=True):
     if t is None:
         return
@@ -46,7 +58,23 @@ def _on_gpu(t, name, dtype=None, contiguous=True):
 
 def _span(t) -> int:
     """Elements from a strided tensor's first to its last."""
-    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else 0
+    n = t.numel()
+    if n == 0 or t.is_contiguous():
+        return n
+    span = 1
+    for size, stride in zip(t.shape, t.stride()):
+        span += (size - 1) * stride
+    return span
+
+
+def _packed(shape, strides, first) -> bool:
+    """Whether dimensions first.. lie in memory one after another."""
+    want = 1
+    for i in range(len(shape) - 1, first - 1, -1):
+        if shape[i] != 1 and strides[i] != want:
+            return False
+        want *= shape[i]
+    return True
 
 
 # ---- beams --------------------------------------------------------------------------
@@ -87,12 +115,15 @@ def lossk_beam_select(logits, scores, n_out, temperature=1.0, allow=None, finish
             allow_stride = allow.shape[1]
     if out is None:
         out = beam_buffers(batch, n_out, logits.device)
-    for key, dtype in (("parent", torch.int32), ("token", torch.int64), ("score", torch.float32),
-                       ("finished", torch.uint8), ("length", torch.int32)):
-        t = out[key]
-        _on_gpu(t, key, dtype)
-        if t.numel() != batch * n_out:
-            raise ValueError(f"out[{key!r}] must be [batch, n_out]")
+    parent, token, score, done, length = out["parent"], out["token"], out["score"], out["finished"], out["length"]
+    _on_gpu(parent, "parent", torch.int32)
+    _on_gpu(token, "token", torch.int64)
+    _on_gpu(score, "score", torch.float32)
+    _on_gpu(done, "finished", torch.uint8)
+    _on_gpu(length, "length", torch.int32)
+    n = batch * n_out
+    if not (parent.numel() == token.numel() == score.numel() == done.numel() == length.numel() == n):
+        raise ValueError("out must hold tensors of [batch, n_out]")
     _on_gpu(lse_out, "lse_out", torch.float32)
     if lse_out is not None and lse_out.numel() != rows:
         raise ValueError("lse_out must hold one value per row of logits")
@@ -101,9 +132,8 @@ def lossk_beam_select(logits, scores, n_out, temperature=1.0, allow=None, finish
     st = lib.lossk_beam_select(batch, beams, V, n_out, _dtype_code(logits), logits.data_ptr(), _span(logits),
                                logits.stride(0) if rows > 1 else max(V, 1), scores.data_ptr(), rows, temperature,
                                _ptr(allow), _len(allow), allow_stride, _ptr(finished), end_token, _ptr(lengths),
-                               length_alpha, out["parent"].data_ptr(), out["token"].data_ptr(),
-                               out["score"].data_ptr(), out["finished"].data_ptr(), out["length"].data_ptr(),
-                               _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream(stream))
+                               length_alpha, parent.data_ptr(), token.data_ptr(), score.data_ptr(), done.data_ptr(),
+                               length.data_ptr(), _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream_of(logits, stream))
     _check(st, "lossk_beam_select")
     return out
 
@@ -119,165 +149,177 @@ def lossk_beam_gather(src, parent, dst=None, ws=None, stream=None):
     if dst is None:
         dst = torch.empty((G, n_dst) + tuple(src.shape[2:]), dtype=src.dtype, device=src.device)
     _on_gpu(dst, "dst", src.dtype)
-    row = src[0, 0].numel() * src.element_size() if src.numel() else 0
+    row = src.numel() * src.element_size() // max(G * n_src, 1)
     if ws is None:
         ws = torch.zeros(256, dtype=torch.uint8, device=src.device)
     st = lib.lossk_beam_gather(G, n_src, n_dst, row, parent.data_ptr(), parent.numel(), src.data_ptr(),
                                src.numel() * src.element_size(), dst.data_ptr(), dst.numel() * dst.element_size(),
-                               ws.data_ptr(), ws.numel(), _stream(stream))
+                               ws.data_ptr(), ws.numel(), _stream_of(src, stream))
     _check(st, "lossk_beam_gather")
     return dst
 
 
 # ---- the cache's pages ------------------------------------------------------------------
 
-def _ints(**named):
-    for nm, t in named.items():
-        _on_gpu(t, nm, torch.int32)
-
-
 def _table(table, name="table"):
-    """(rows, entries per row, row stride) of a table, whose rows may be strided."""
+    """(rows, entries per row, row stride, elements) of a table, whose rows may be strided."""
     _on_gpu(table, name, torch.int32, contiguous=False)
-    if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"{name} must be [n_seq, max_pages] with contiguous rows")
-    n, m = table.shape
-    return n, m, table.stride(0) if n > 1 else max(m, 1)
+    shape = table.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [n_seq, max_pages]")
+    n, m = shape
+    if table.is_contiguous():
+        return n, m, max(m, 1), n * m
+    stride, one = table.stride()
+    if m > 1 and one != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return n, m, stride if n > 1 else max(m, 1), _span(table)
 
 
-def _pool(pool):
+def _pool(pool, pages):
     """(address, bytes, planes, plane stride, page stride, page bytes) of a pool [planes, pages, ...]."""
     _on_gpu(pool, "pool", contiguous=False)
-    if pool.dim() < 3 or not pool[0, 0].is_contiguous():
+    shape, strides, es = pool.shape, pool.stride(), pool.element_size()
+    if len(shape) < 3 or not (pool.is_contiguous() or _packed(shape, strides, 2)):
         raise ValueError("pool must be [planes, pages, ...] with contiguous pages")
-    es = pool.element_size()
-    page = pool[0, 0].numel() * es
-    planes, pages = pool.shape[:2]
-    return (pool.data_ptr(), _span(pool) * es, planes, pool.stride(0) * es if planes > 1 else 0,
-            pool.stride(1) * es if pages > 1 else page, page)
-
-
-def _cache_ws(ws, n_seq, n_pages, device):
-    return ws if ws is not None else decode_workspace(KIND_CACHE, n_seq, n_pages, device=device)
+    if shape[1] != pages:
+        raise ValueError(f"a pool of {shape[1]} pages with {pages} counts")
+    page = pool.numel() * es // max(shape[0] * shape[1], 1)
+    return (pool.data_ptr(), _span(pool) * es, shape[0], strides[0] * es if shape[0] > 1 else 0,
+            strides[1] * es if pages > 1 else page, page)
 
 
 def lossk_cache_fork(parent, table, lens, ref, page_size, table_out=None, lens_out=None, ws=None, stream=None):
     """parent int32 [groups, n_dst]; table holds groups * n_src rows.  Returns (table_out, lens_out)."""
-    _ints(parent=parent, lens=lens, ref=ref, lens_out=lens_out)
-    n, m, stride = _table(table)
+    _on_gpu(parent, "parent", torch.int32)
+    _on_gpu(lens, "lens", torch.int32)
+    _on_gpu(ref, "ref", torch.int32)
+    _on_gpu(lens_out, "lens_out", torch.int32)
+    n, m, stride, table_len = _table(table)
     G, n_dst = parent.shape
+    pages = ref.numel()
     if n % G or lens.numel() != n:
         raise ValueError(f"{n} rows and {lens.numel()} lengths in {G} groups")
     if table_out is None:
         table_out = torch.empty((G * n_dst, m), dtype=torch.int32, device=table.device)
     if lens_out is None:
         lens_out = torch.empty(G * n_dst, dtype=torch.int32, device=table.device)
-    no, mo, stride_out = _table(table_out, "table_out")
+    no, mo, stride_out, out_len = _table(table_out, "table_out")
     if no != G * n_dst or mo != m:
         raise ValueError("table_out must be [groups * n_dst, max_pages]")
-    ws = _cache_ws(ws, max(n, no), ref.numel(), table.device)
-    st = lib.lossk_cache_fork(G, n // G, n_dst, m, page_size, ref.numel(), parent.data_ptr(), parent.numel(),
-                              table.data_ptr(), _span(table), stride, lens.data_ptr(), n, ref.data_ptr(), ref.numel(),
-                              table_out.data_ptr(), _span(table_out), stride_out, lens_out.data_ptr(),
-                              lens_out.numel(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if ws is None:
+        ws = decode_workspace(KIND_CACHE, max(n, no), pages, device=table.device)
+    st = lib.lossk_cache_fork(G, n // G, n_dst, m, page_size, pages, parent.data_ptr(), parent.numel(),
+                              table.data_ptr(), table_len, stride, lens.data_ptr(), n, ref.data_ptr(), pages,
+                              table_out.data_ptr(), out_len, stride_out, lens_out.data_ptr(), lens_out.numel(),
+                              ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_fork")
     return table_out, lens_out
 
 
 def lossk_cache_reserve(table, lens, ref, pool, page_size, n_new=1, ws=None, stream=None) -> None:
     """n_new: tokens to come for every sequence, or an int32 tensor with one count each."""
-    _ints(lens=lens, ref=ref)
-    n, m, stride = _table(table)
+    _on_gpu(lens, "lens", torch.int32)
+    _on_gpu(ref, "ref", torch.int32)
+    n, m, stride, table_len = _table(table)
     each = n_new if isinstance(n_new, torch.Tensor) else None
-    _ints(n_new=each)
-    P = _pool(pool)
-    if pool.shape[1] != ref.numel():
-        raise ValueError(f"a pool of {pool.shape[1]} pages with {ref.numel()} counts")
-    ws = _cache_ws(ws, n, ref.numel(), table.device)
-    st = lib.lossk_cache_reserve(n, m, page_size, ref.numel(), 0 if each is not None else n_new, _ptr(each),
-                                 _len(each), table.data_ptr(), _span(table), stride, lens.data_ptr(), lens.numel(),
-                                 ref.data_ptr(), ref.numel(), *P, ws.data_ptr(), ws.numel(), _stream(stream))
+    _on_gpu(each, "n_new", torch.int32)
+    pages = ref.numel()
+    P = _pool(pool, pages)
+    if ws is None:
+        ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+    st = lib.lossk_cache_reserve(n, m, page_size, pages, 0 if each is not None else n_new, _ptr(each),
+                                 _len(each), table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(),
+                                 ref.data_ptr(), pages, *P, ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_reserve")
 
 
 def lossk_cache_free(table, lens, ref, page_size, drop=None, ws=None, stream=None) -> None:
     """drop: uint8 [n_seq], nonzero where the sequence goes (None: all)."""
-    _ints(lens=lens, ref=ref)
+    _on_gpu(lens, "lens", torch.int32)
+    _on_gpu(ref, "ref", torch.int32)
     _on_gpu(drop, "drop", torch.uint8)
-    n, m, stride = _table(table)
-    ws = _cache_ws(ws, n, ref.numel(), table.device)
-    st = lib.lossk_cache_free(n, m, page_size, ref.numel(), _ptr(drop), _len(drop), table.data_ptr(), _span(table),
+    n, m, stride, table_len = _table(table)
+    if ws is None:
+        ws = decode_workspace(KIND_CACHE, n, ref.numel(), device=table.device)
+    st = lib.lossk_cache_free(n, m, page_size, ref.numel(), _ptr(drop), _len(drop), table.data_ptr(), table_len,
                               stride, lens.data_ptr(), lens.numel(), ref.data_ptr(), ref.numel(), ws.data_ptr(),
-                              ws.numel(), _stream(stream))
+                              ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_free")
 
 
 def lossk_cache_compact(table, lens, ref, pool, page_size, table_out=None, ref_out=None, n_live_out=None, ws=None,
                         stream=None):
     """Returns (table_out, ref_out, n_live_out); the pool's live pages are in front then."""
-    _ints(lens=lens, ref=ref, ref_out=ref_out, n_live_out=n_live_out)
-    n, m, stride = _table(table)
-    P = _pool(pool)
-    if pool.shape[1] != ref.numel():
-        raise ValueError(f"a pool of {pool.shape[1]} pages with {ref.numel()} counts")
-    dev = table.device
-    table_out = table_out if table_out is not None else torch.empty((n, m), dtype=torch.int32, device=dev)
+    _on_gpu(lens, "lens", torch.int32)
+    _on_gpu(ref, "ref", torch.int32)
+    _on_gpu(ref_out, "ref_out", torch.int32)
+    _on_gpu(n_live_out, "n_live_out", torch.int32)
+    n, m, stride, table_len = _table(table)
+    pages = ref.numel()
+    P = _pool(pool, pages)
+    table_out = table_out if table_out is not None else table.new_empty((n, m))
     ref_out = ref_out if ref_out is not None else torch.empty_like(ref)
-    n_live_out = n_live_out if n_live_out is not None else torch.empty(1, dtype=torch.int32, device=dev)
-    no, mo, stride_out = _table(table_out, "table_out")
-    if (no, mo) != (n, m) or n_live_out.numel() < 1:
+    n_live_out = n_live_out if n_live_out is not None else ref.new_empty(1)
+    no, mo, stride_out, out_len = _table(table_out, "table_out")
+    if no != n or mo != m or n_live_out.numel() < 1:
         raise ValueError("table_out must be shaped like table, n_live_out hold one value")
-    ws = _cache_ws(ws, n, ref.numel(), dev)
-    st = lib.lossk_cache_compact(n, m, page_size, ref.numel(), table.data_ptr(), _span(table), stride,
-                                 lens.data_ptr(), lens.numel(), ref.data_ptr(), ref.numel(), table_out.data_ptr(),
-                                 _span(table_out), stride_out, ref_out.data_ptr(), ref_out.numel(),
-                                 n_live_out.data_ptr(), *P, ws.data_ptr(), ws.numel(), _stream(stream))
+    if ws is None:
+        ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+    st = lib.lossk_cache_compact(n, m, page_size, pages, table.data_ptr(), table_len, stride, lens.data_ptr(),
+                                 lens.numel(), ref.data_ptr(), pages, table_out.data_ptr(), out_len, stride_out,
+                                 ref_out.data_ptr(), ref_out.numel(), n_live_out.data_ptr(), *P, ws.data_ptr(),
+                                 ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_compact")
     return table_out, ref_out, n_live_out
 
 
 def lossk_cache_copy(src, dst, pool, ws=None, stream=None) -> None:
     """Page src[i] of the pool to page dst[i], in every plane."""
-    _ints(src=src, dst=dst)
-    P = _pool(pool)
+    _on_gpu(src, "src", torch.int32)
+    _on_gpu(dst, "dst", torch.int32)
+    P = _pool(pool, pool.shape[1])
     if src.numel() != dst.numel():
         raise ValueError("src and dst must list as many pages")
     ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=pool.device)
     st = lib.lossk_cache_copy(src.numel(), pool.shape[1], src.data_ptr(), src.numel(), dst.data_ptr(), dst.numel(),
-                              *P, ws.data_ptr(), ws.numel(), _stream(stream))
+                              *P, ws.data_ptr(), ws.numel(), _stream_of(pool, stream))
     _check(st, "lossk_cache_copy")
 
 
 def _pages(k, v):
-    """(pages, page size, heads, head dim, strides) of one layer's key and value pages
-    [pages, page, heads, head_dim], whose elements of a head are contiguous."""
+    """(shape, strides, elements) of one layer's key and value pages [pages, page, heads, head_dim],
+    whose elements of a head are contiguous."""
     _on_gpu(k, "k_pages", contiguous=False)
     _on_gpu(v, "v_pages", k.dtype, contiguous=False)
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or (k.shape[3] > 1 and k.stride(3) != 1):
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 4 or shape != v.shape or strides != v.stride() or (shape[3] > 1 and strides[3] != 1):
         raise ValueError("k_pages and v_pages must be [pages, page, heads, head_dim], laid out alike, heads contiguous")
-    return k.shape, k.stride()
+    return shape, strides, _span(k)
 
 
 def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, ws=None, stream=None) -> None:
     """k_new, v_new [n_tok, heads, head_dim] (tokens may be strided) into one layer's pages
     [pages, page, heads, head_dim] (any strides).  first: int32 [n_seq + 1], where each sequence's
     rows begin (None: one row per sequence)."""
-    (n_pages, page, kv, hd), (sp, stok, sh, _) = _pages(k_pages, v_pages)
-    _ints(lens=lens, first=first)
-    n, m, stride = _table(table)
-    for t, nm in ((k_new, "k_new"), (v_new, "v_new")):
-        _on_gpu(t, nm, k_pages.dtype, contiguous=False)
-        if t.dim() != 3 or t.shape[1:] != (kv, hd) or (t.shape[0] and not t[0].is_contiguous()):
-            raise ValueError(f"{nm} must be [n_tok, heads, head_dim] with contiguous tokens")
-    if k_new.shape != v_new.shape or k_new.stride() != v_new.stride():
+    (n_pages, page, kv, hd), (sp, stok, sh, _), pages_len = _pages(k_pages, v_pages)
+    _on_gpu(lens, "lens", torch.int32)
+    _on_gpu(first, "first", torch.int32)
+    n, m, stride, table_len = _table(table)
+    _on_gpu(k_new, "k_new", k_pages.dtype, contiguous=False)
+    _on_gpu(v_new, "v_new", k_pages.dtype, contiguous=False)
+    shape, strides = k_new.shape, k_new.stride()
+    if len(shape) != 3 or shape[1] != kv or shape[2] != hd or not (k_new.is_contiguous() or _packed(shape, strides, 1)):
+        raise ValueError("k_new must be [n_tok, heads, head_dim] with contiguous tokens")
+    if shape != v_new.shape or strides != v_new.stride():
         raise ValueError("k_new and v_new must be laid out alike")
-    n_tok = k_new.shape[0]
+    n_tok = shape[0]
     ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=table.device)
     st = lib.lossk_cache_write(n_tok, n, kv, hd, m, page, n_pages, _dtype_code(k_pages), k_new.data_ptr(),
-                               v_new.data_ptr(), _span(k_new), k_new.stride(0) if n_tok > 1 else kv * hd,
-                               k_pages.data_ptr(), v_pages.data_ptr(), _span(k_pages), sp, stok, sh,
-                               table.data_ptr(), _span(table), stride, lens.data_ptr(), lens.numel(), _ptr(first),
-                               _len(first), ws.data_ptr(), ws.numel(), _stream(stream))
+                               v_new.data_ptr(), _span(k_new), strides[0] if n_tok > 1 else kv * hd,
+                               k_pages.data_ptr(), v_pages.data_ptr(), pages_len, sp, stok, sh,
+                               table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(), _ptr(first),
+                               _len(first), ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_write")
 
 
@@ -288,13 +330,14 @@ def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, sha
     """q [n_seq, n_q_heads, head_dim] (sequences may be strided) over one layer's pages
     [pages, page, heads, head_dim] (any strides).  scale defaults to head_dim ** -0.5; share: how
     many consecutive sequences may share leading pages.  Returns out."""
-    (n_pages, page, kv, hd), (sp, stok, sh, _) = _pages(k_pages, v_pages)
-    _ints(lens=lens)
+    (n_pages, page, kv, hd), (sp, stok, sh, _), pages_len = _pages(k_pages, v_pages)
+    _on_gpu(lens, "lens", torch.int32)
     _on_gpu(q, "q", k_pages.dtype, contiguous=False)
-    n, m, stride = _table(table)
-    if q.dim() != 3 or q.shape[0] != n or q.shape[2] != hd or (n and not q[0].is_contiguous()):
+    n, m, stride, table_len = _table(table)
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or shape[0] != n or shape[2] != hd or not (q.is_contiguous() or _packed(shape, strides, 1)):
         raise ValueError("q must be [n_seq, n_q_heads, head_dim] with contiguous sequences")
-    hq = q.shape[1]
+    hq = shape[1]
     if out is None:
         out = torch.empty((n, hq, hd), dtype=q.dtype, device=q.device)
     _on_gpu(out, "out", q.dtype)
@@ -304,9 +347,9 @@ def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, sha
     if ws is None:
         ws = decode_workspace(KIND_PAGED_ATTN, n, hq, kv, hd, q.device)
     st = lib.lossk_paged_attn(n, hq, kv, hd, m, page, n_pages, share, _dtype_code(q), q.data_ptr(), _span(q),
-                              q.stride(0) if n > 1 else hq * hd, k_pages.data_ptr(), v_pages.data_ptr(),
-                              _span(k_pages), sp, stok, sh, table.data_ptr(), _span(table), stride, lens.data_ptr(),
-                              lens.numel(), max_len, window, hd ** -0.5 if scale is None else scale, out.data_ptr(),
-                              out.numel(), _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream(stream))
+                              strides[0] if n > 1 else hq * hd, k_pages.data_ptr(), v_pages.data_ptr(), pages_len,
+                              sp, stok, sh, table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(),
+                              max_len, window, hd ** -0.5 if scale is None else scale, out.data_ptr(), out.numel(),
+                              _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream_of(q, stream))
     _check(st, "lossk_paged_attn")
     return out
