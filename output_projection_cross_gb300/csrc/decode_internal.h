@@ -29,7 +29,7 @@ struct BeamArgs {
     int64_t row_stride;
     int dtype, batch, beams, vocab, n_out;
     int n_split, split_len; // tokens a split has (the last one less)
-    int cap, merge_cap;     // keys the kernels' buffers hold
+    int cap, depth;         // keys the rows kernel's buffer holds, the merge's of each split's list
     float c;                // log2(e) / T
     double inv_t;           // 1 / T
     const uint32_t *allow;

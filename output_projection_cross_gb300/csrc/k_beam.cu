@@ -52,26 +52,10 @@ __device__ __forceinline__ Key key_of(float x, int tok)
     return (static_cast<uint64_t>(order_of(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(tok));
 }
 
-// The order of a rank (a double) and, among equals, of the lower flat index.
-struct RankKey {
-    uint64_t rank;          // order of the rank, 0: none
-    uint64_t flat;          // ~(beam * vocab + token)
-};
-__device__ __forceinline__ bool operator>(const RankKey &x, const RankKey &y)
-{
-    return x.rank > y.rank || (x.rank == y.rank && x.flat > y.flat);
-}
 __device__ __forceinline__ uint64_t order_of(double x)
 {
     const uint64_t b = __double_as_longlong(x + 0.0);
     return b >> 63 ? ~b : b | (1ull << 63);
-}
-__device__ __forceinline__ bool is_none(const Key &k) { return k == 0; }
-__device__ __forceinline__ bool is_none(const RankKey &k) { return k.rank == 0; }
-__device__ __forceinline__ Key shfl_xor(const Key &k, int o) { return __shfl_xor_sync(0xFFFFFFFFu, k, o); }
-__device__ __forceinline__ RankKey shfl_xor(const RankKey &k, int o)
-{
-    return RankKey{__shfl_xor_sync(0xFFFFFFFFu, k.rank, o), __shfl_xor_sync(0xFFFFFFFFu, k.flat, o)};
 }
 
 // Groups of threads a threshold is taken over: at least 4 n of them where
@@ -81,15 +65,15 @@ __host__ __device__ constexpr int groups_for(int n) { return n <= 16 ? 64 : n <=
 
 // The n-th largest of the groups' largest keys (none where fewer groups have
 // any).  All threads call it with their largest key; s_keys holds NT keys.
-template <typename K> __device__ __forceinline__ K nth_of_groups(K mine, int n, K *s_keys, K *s_nth)
+__device__ __forceinline__ Key nth_of_groups(Key mine, int n, Key *s_keys, Key *s_nth)
 {
     const int t = threadIdx.x, groups = groups_for(n), per = NT / groups;
     for (int o = 1; o < per; o <<= 1) {
-        const K other = shfl_xor(mine, o);
+        const Key other = __shfl_xor_sync(0xFFFFFFFFu, mine, o);
         if (other > mine) mine = other;
     }
     block_sync();
-    if (t == 0) *s_nth = K{};
+    if (t == 0) *s_nth = 0;
     if (t % per == 0) s_keys[t / per] = mine;
     block_sync();
     // `per` threads count the keys above each group's, a part each
@@ -99,29 +83,28 @@ template <typename K> __device__ __forceinline__ K nth_of_groups(K mine, int n, 
 #pragma unroll 8
     for (int i = 0; i < part; ++i) above += s_keys[first + i] > mine;
     for (int o = 1; o < per; o <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
-    if (t % per == 0 && above == n - 1 && !is_none(mine)) *s_nth = mine;
+    if (t % per == 0 && above == n - 1 && mine) *s_nth = mine;
     block_sync();
     return *s_nth;
 }
 
 // The n best of buf[0 .. cnt), in falling order, into buf[0 ..); returns how
 // many there are.  tmp holds as many keys as buf.
-template <typename K>
-__device__ __forceinline__ int keep_best(K *buf, K *tmp, int cnt, int n, K *s_keys, K *s_nth, int *s_cnt)
+__device__ __forceinline__ int keep_best(Key *buf, Key *tmp, int cnt, int n, Key *s_keys, Key *s_nth, int *s_cnt)
 {
     const int t = threadIdx.x;
-    K mine{};
+    Key mine = 0;
     for (int i = t; i < cnt; i += NT)
         if (buf[i] > mine) mine = buf[i];
-    const K nth = nth_of_groups(mine, n, s_keys, s_nth);
+    const Key nth = nth_of_groups(mine, n, s_keys, s_nth);
     if (t == 0) *s_cnt = 0;
     block_sync();
     for (int i = t; i < cnt; i += NT)
-        if (!is_none(buf[i]) && !(nth > buf[i])) tmp[atomicAdd(s_cnt, 1)] = buf[i];
+        if (buf[i] && buf[i] >= nth) tmp[atomicAdd(s_cnt, 1)] = buf[i];
     block_sync();
     const int left = *s_cnt;
     for (int i = t; i < left; i += NT) {
-        const K k = tmp[i];
+        const Key k = tmp[i];
         int above = 0;
         for (int j = 0; j < left; ++j) above += tmp[j] > k;
         if (above < n) buf[above] = k;
@@ -237,6 +220,23 @@ template <typename T> __device__ __forceinline__ uint4 all_low()
 {
     const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, h16_t>::value ? 0xFC00FC00u : 0xFF80FF80u;
     return make_uint4(w, w, w, w);
+}
+
+// A vector with -infinity where its token's bit is 0.
+template <typename T> __device__ __forceinline__ uint4 masked(const uint4 &v, uint32_t bits)
+{
+    const uint4 low = all_low<T>();
+    auto word = [&](uint32_t w, int i) {
+        uint32_t keep;
+        if constexpr (sizeof(T) == 4) {
+            keep = (bits >> i) & 1u ? 0xFFFFFFFFu : 0u;
+        } else {
+            const uint32_t x = (bits >> (2 * i)) & 3u;
+            keep = ((x | (x << 15)) & 0x10001u) * 0xFFFFu;
+        }
+        return (w & keep) | (low.x & ~keep);
+    };
+    return make_uint4(word(v.x, 0), word(v.y, 1), word(v.z, 2), word(v.w, 3));
 }
 
 // 32 bits of a row's mask from token v on.
@@ -396,7 +396,7 @@ __device__ __noinline__ int best_by_steps(const BeamArgs &a, const Item<T> &it, 
 // 17 us of 127 at 896 rows of 151936 with n = 16); for larger n the buffer is
 // cut to its n best after the 2nd, 4th, 8th ... chunk.  Keys that do not fit
 // the buffer are dropped, and the item's best are found by best_by_steps.
-template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK ? 2 : 3) beam_rows_kernel(BeamArgs a)
+template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) beam_rows_kernel(BeamArgs a)
 {
     constexpr int NV = Elem<T>::NV;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -470,14 +470,12 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
         const int chunks = it.chunks();
         for (int j = 0; j < chunks; ++j, ++k) {
             const int sg = k % STAGES, base = j * CHUNK;
-            uint32_t bits = ~0u;                       // MASK: which of the thread's tokens are allowed
+            uint32_t bits[U];                          // MASK: which of a vector's tokens are allowed
             if constexpr (MASK) {
-                bits = 0;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int i = base + u * NT + t;
-                    const uint32_t w = i < it.n_vec ? allow_bits(allow, words, it.v0 + i * NV) : 0u;
-                    bits |= (w & ((1u << NV) - 1u)) << (u * NV);
+                    bits[u] = i < it.n_vec ? allow_bits(allow, words, it.v0 + i * NV) : 0u;
                 }
             }
             if (j) wait_for(&s_full[sg], (k / STAGES) & 1, a.err);
@@ -495,26 +493,15 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                 for (int u = 0; u < U; ++u)
                     if (base + u * NT + t < it.n_vec) cur[u] = joined(cur[u], tile[u * NT + t + 1], it.skew);
             }
-            // the largest of vector u, and of the chunk
-            const auto largest = [&](int u) {
-                if constexpr (MASK) {
-                    float f[NV], x = -INFINITY;
-                    unpack<T>(cur[u], f);
+            if constexpr (MASK) {
 #pragma unroll
-                    for (int e = 0; e < NV; ++e)
-                        if ((bits >> (u * NV + e)) & 1u) x = max_nan(x, f[e]);
-                    return x;
-                } else {
-                    return vec_max<T>(cur[u]);
-                }
-            };
+                for (int u = 0; u < U; ++u) cur[u] = masked<T>(cur[u], bits[u]);
+            }
+            static_assert(U == 4, "the chunk's largest in pairs");
             float top;
-            if constexpr (MASK || sizeof(T) == 4) {
-                top = largest(0);
-#pragma unroll
-                for (int u = 1; u < U; ++u) top = max_nan(top, largest(u));
+            if constexpr (sizeof(T) == 4) {
+                top = max_nan(max_nan(vec_max<T>(cur[0]), vec_max<T>(cur[1])), max_nan(vec_max<T>(cur[2]), vec_max<T>(cur[3])));
             } else {
-                static_assert(U == 4, "the chunk's largest in pairs");
                 const auto both = [](const uint4 &x, const uint4 &y) {
                     return make_uint4(max_nan2<T>(x.x, y.x), max_nan2<T>(x.y, y.y), max_nan2<T>(x.z, y.z),
                                       max_nan2<T>(x.w, y.w));
@@ -531,10 +518,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                         float f[NV];
                         unpack<T>(cur[u], f);
 #pragma unroll
-                        for (int e = 0; e < NV; ++e) {
-                            f[e] = term(f[e]);
-                            if (MASK && !((bits >> (u * NV + e)) & 1u)) f[e] = 0.f;
-                        }
+                        for (int e = 0; e < NV; ++e) f[e] = term(f[e]);
 #pragma unroll
                         for (int h = NV / 2; h; h >>= 1)
 #pragma unroll
@@ -563,7 +547,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                         unpack<T>(cur[u], f);
 #pragma unroll
                         for (int e = NV - 1; e >= 0; --e)
-                            if (f[e] == top && ((bits >> (u * NV + e)) & 1u)) at = u * NV + e;
+                            if (f[e] == top) at = u * NV + e;
                     }
                     const Key q = at >= 0 ? key_of(top + 0.f, token(at)) : 0;    // (none: a NaN was the largest)
                     best = q > best ? q : best;
@@ -576,14 +560,13 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
                 uint32_t hits = 0;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (!(largest(u) < limit_x)) {
+                    if (!(vec_max<T>(cur[u]) < limit_x)) {
                         float f[NV];
                         unpack<T>(cur[u], f);
 #pragma unroll
                         for (int e = 0; e < NV; ++e)
                             if (f[e] >= limit_x && f[e] > -INFINITY) hits |= 1u << (u * NV + e);
                     }
-                hits &= bits;
                 bool last = j == 0 && one >= limit_x && one > -INFINITY;
                 while (hits || last) {
                     float x = one;
@@ -667,14 +650,74 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, MASK
     }
 }
 
+// ---- rows of few tokens ----------------------------------------------------------------
+// A warp per row, SMALL / 32 tokens a lane: the rows kernel's blocks, each with
+// its thresholds and barriers per item, took 42 us for 1560 rows of 20 tokens.
+constexpr int SMALL = 512;
+template <typename T> __global__ void __launch_bounds__(128) beam_small_kernel(BeamArgs a)
+{
+    constexpr int N = SMALL / 32;
+    const int r = static_cast<int>((static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    if (r >= a.batch * a.beams || !beam_reads(a, r)) return;
+    const T *row = static_cast<const T *>(a.logits) + r * a.row_stride;
+    const uint32_t *allow = a.allow ? a.allow + r * a.allow_stride : nullptr;
+    float x[N], m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = lane + 32 * i;
+        x[i] = -INFINITY;
+        if (v < a.vocab && (!allow || (allow[i] >> lane) & 1u)) x[i] = beam_f(row[v]);
+        m = max_nan(m, x[i]);
+    }
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float b = -m * a.c;
+    float z = 0.f, lost = 0.f;
+    if (m > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            add_z(z, lost, plain(b) ? ex2_approx(fmaf(x[i], a.c, b)) : x[i] == m ? 1.f : 0.f, 0.f);
+        for (int o = 16; o; o >>= 1) {
+            const float p = __shfl_xor_sync(0xFFFFFFFFu, z, o), q = __shfl_xor_sync(0xFFFFFFFFu, lost, o);
+            add_z(z, lost, p, q);
+        }
+    }
+    if (lane == 0) a.stat[r] = BeamStat{m < INFINITY ? z : NAN, lost, m, m, b};
+    // the best one by one: the largest logit, the lowest of its tokens
+    BeamCand *cand = a.cand + static_cast<int64_t>(r) * a.n_out;
+    for (int j = 0; j < a.n_out; ++j) {
+        float best = -INFINITY;
+        int at = 0;
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i)
+            if (x[i] >= best) {
+                best = x[i];
+                at = i;
+            }
+        const uint32_t mine = best > -INFINITY ? order_of(best) : 0u;
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, mine);
+        const uint32_t tok = __reduce_min_sync(0xFFFFFFFFu, top && mine == top ? lane + 32u * at : 0xFFFFFFFFu);
+        if (lane == 0) cand[j] = top ? BeamCand{value_of(top), static_cast<int>(tok)} : BeamCand{0.f, -1};
+        if (!top) {
+            for (int i = j + 1 + lane; i < a.n_out; i += 32) cand[i] = BeamCand{0.f, -1};
+            break;
+        }
+        if (tok == lane + 32u * at) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i == at) x[i] = -INFINITY;
+        }
+    }
+}
+
 // ---- merge -------------------------------------------------------------------------
 // One block per batch entry.  A warp per beam joins the sums and lists of its
 // splits; lane k of the first warps then forms beam k's log-sum-exp and
-// divisor in double; then every beam's candidates are ranked.  Doubles run at a
+// divisor in double; then every beam's candidates are ranked.  A list is in
+// falling order, so a candidate's place among all is its place in its list
+// and what a binary search counts in each other list.  Doubles run at a
 // sixty-fourth of a float's rate here, so only what orders the beams is one:
-// a logarithm and a power per beam, a product and two sums per candidate.
-constexpr int MERGE_U = 4;                 // candidates a thread ranks at once, where one is not enough
-
+// two logarithms and an exponential per beam, a product and two sums per
+// candidate.
 struct BeamRow {
     float z, lost, m, ref, b, start;
     int kind, len;                         // kind 0: no candidates, 1: its own (finished), 2: the row's
@@ -693,16 +736,16 @@ __device__ __forceinline__ void put_out(const BeamArgs &a, int b, int j, int k, 
 __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    RankKey *buf = reinterpret_cast<RankKey *>(smem), *tmp = buf + a.merge_cap;
-    Key *lists = reinterpret_cast<Key *>(tmp + a.merge_cap);           // [beams][n_out]
-    __shared__ RankKey s_keys[NT], s_nth;
+    const int all = a.beams * a.n_out;
+    Key *lists = reinterpret_cast<Key *>(smem);        // [beams][n_out]
+    uint64_t *ranks = lists + all;                     // the same places: order of the rank, 0: no candidate
+    Key *heads = ranks + all;                          // a warp's splits' lists, `depth` of each
     __shared__ BeamRow s_row[LOSSK_BEAM_MAX_BEAMS];
     __shared__ double s_lse[LOSSK_BEAM_MAX_BEAMS], s_inv[LOSSK_BEAM_MAX_BEAMS];
-    __shared__ int s_cnt, s_kept;
+    __shared__ int s_valid[WARPS];
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b == 0 && t == 0) *a.next = 0;                 // for the workspace's next call
-    const int all = a.beams * a.n_out;
     for (int k = warp; k < a.beams; k += WARPS) {
         const int r = b * a.beams + k;
         const float start = a.scores[r];
@@ -758,36 +801,28 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
         } else if (a.n_split == 1) {
             for (int j = lane; j < a.n_out; j += 32) lists[k * a.n_out + j] = entry(0, j);
         } else {
-            // the splits' lists, each in falling order: a lane keeps the heads of two, and the next
-            // three of each (a pop then rarely waits for memory)
-            int at[2] = {4, 4};
-            Key q[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q[h][j] = entry(lane + 32 * h, j);
+            // the splits' lists, each in falling order, from shared memory (what lies deeper than
+            // `depth` from where it is): lane i keeps the heads of lists i and i + 32
+            const int depth = a.depth;
+            Key *mine = heads + warp * a.n_split * depth;
+            for (int i = lane; i < a.n_split * depth; i += 32) mine[i] = entry(i / depth, i % depth);
+            __syncwarp();
+            auto at = [&](int i, int j) { return i < a.n_split && j < depth ? mine[i * depth + j] : entry(i, j); };
+            int j0 = 0, j1 = 0;
+            Key q0 = at(lane, 0), q1 = at(lane + 32, 0);
             for (int j = 0; j < a.n_out; ++j) {
-                const bool second = q[1][0] > q[0][0];
-                const Key mine = second ? q[1][0] : q[0][0];
-                const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32));
+                const Key q = q1 > q0 ? q1 : q0;
+                const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(q >> 32));
                 const uint32_t lo = __reduce_max_sync(
-                    0xFFFFFFFFu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
+                    0xFFFFFFFFu, static_cast<uint32_t>(q >> 32) == hi ? static_cast<uint32_t>(q) : 0u);
                 const Key best = (static_cast<uint64_t>(hi) << 32) | lo;
                 if (lane == 0) lists[k * a.n_out + j] = best;
-                if (best && mine == best) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (second == (h == 1)) {
-                            q[h][0] = q[h][1];
-                            q[h][1] = q[h][2];
-                            q[h][2] = q[h][3];
-                            q[h][3] = entry(lane + 32 * h, at[h]++);
-                        }
-                }
+                if (best && q0 == best) q0 = at(lane, ++j0);
+                else if (best && q1 == best) q1 = at(lane + 32, ++j1);
             }
+            __syncwarp();
         }
     }
-    if (t == 0) s_cnt = 0;
     block_sync();
     if (t < a.beams) {
         const BeamRow row = s_row[t];
@@ -800,91 +835,51 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
         }
         s_lse[t] = lse;
         const double n = row.len > 1 ? row.len : 1;
-        s_inv[t] = a.length_alpha == 0.0 ? 1.0 : 1.0 / (a.length_alpha == 1.0 ? n : pow(n, a.length_alpha));
+        s_inv[t] = a.length_alpha == 0.0 ? 1.0 : a.length_alpha == 1.0 ? 1.0 / n : exp(-a.length_alpha * log(n));
         if (a.lse_out) a.lse_out[b * a.beams + t] = static_cast<float>(lse);
     }
     block_sync();
-    // candidate i: its key (none where there is none) and its score
-    auto ranked = [&](int i, double &score) {
-        const int k = i / a.n_out;
-        const Key q = lists[i];
-        score = s_row[k].start;
-        if (!q) return RankKey{};
-        if (s_row[k].kind == 2) score += static_cast<double>(value_of(static_cast<uint32_t>(q >> 32))) * a.inv_t - s_lse[k];
-        const uint32_t tok = 0xFFFFFFFFu - static_cast<uint32_t>(q);
-        return RankKey{order_of(a.length_alpha == 0.0 ? score : score * s_inv[k]),
-                       ~static_cast<uint64_t>(static_cast<int64_t>(k) * a.vocab + tok)};
+    auto score_of = [&](int i, int k) {
+        const double s = s_row[k].start;
+        return s_row[k].kind == 2 ? s + (static_cast<double>(value_of(static_cast<uint32_t>(lists[i] >> 32))) * a.inv_t - s_lse[k])
+                                  : s;
     };
-    auto write = [&](int j, int i, double score) {
+    int valid = 0;
+    for (int i = t; i < all; i += NT) {
         const int k = i / a.n_out;
+        const double s = lists[i] ? score_of(i, k) : 0.0;
+        ranks[i] = lists[i] ? order_of(a.length_alpha == 0.0 ? s : s * s_inv[k]) : 0;
+        valid += lists[i] != 0;
+    }
+    for (int o = 16; o; o >>= 1) valid += __shfl_xor_sync(0xFFFFFFFFu, valid, o);
+    if (lane == 0) s_valid[warp] = valid;
+    block_sync();
+    // A candidate's place: equal ranks go by the lower beam, then by the order of its list (the
+    // larger logit, the lower token).
+    for (int i = t; i < all; i += NT) {
+        const uint64_t mine = ranks[i];
+        if (!mine) continue;
+        const int k = i / a.n_out;
+        int place = i - k * a.n_out;
+        for (int o = 0; o < a.beams && place < a.n_out; ++o) {
+            if (o == k) continue;
+            const uint64_t *list = ranks + o * a.n_out;
+            int lo = 0, hi = a.n_out;                  // the first entry that does not come before mine
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (list[mid] > mine || (list[mid] == mine && o < k)) lo = mid + 1;
+                else hi = mid;
+            }
+            place += lo;
+        }
+        if (place >= a.n_out) continue;
         const bool was = s_row[k].kind == 1;
-        put_out(a, b, j, k, was ? a.end_token : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(lists[i])), score,
-                was, s_row[k].len);
-    };
-    auto rest = [&](int from) {
-        for (int j = from + t; j < a.n_out; j += NT) put_out(a, b, j, -1, -1, -INFINITY, false, 0);
-    };
-    if (all <= NT) {
-        // each key's place by counting the better ones, several threads a key
-        double score = 0.0;
-        RankKey mine{};
-        if (t < all) mine = ranked(t, score);
-        s_keys[t] = mine;
-        const int valid = __syncthreads_count(!is_none(mine));
-        int per = 1;
-        while (per * 2 * all <= NT && per < 32) per *= 2;
-        const int key = t / per;
-        int above = 0;
-        if (key < all) {
-            const RankKey x = s_keys[key];
-            for (int i = t % per; i < all; i += per) above += s_keys[i] > x;
-        }
-        for (int o = 1; o < per; o <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
-        int *place = reinterpret_cast<int *>(tmp);
-        if (key < all && t % per == 0) place[key] = above;
-        block_sync();
-        if (t < all && !is_none(mine) && place[t] < a.n_out) write(place[t], t, score);
-        rest(valid);
-        return;
+        put_out(a, b, place, k, was ? a.end_token : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(lists[i])),
+                score_of(i, k), was, s_row[k].len);
     }
-    RankKey limit{};
-    for (int base = 0; base < all; base += NT * MERGE_U) {
-        RankKey mine[MERGE_U], best{};
-#pragma unroll
-        for (int u = 0; u < MERGE_U; ++u) {
-            const int i = base + u * NT + t;
-            double score;
-            mine[u] = i < all ? ranked(i, score) : RankKey{};
-            if (mine[u] > best) best = mine[u];
-        }
-        const RankKey nth = nth_of_groups(best, a.n_out, s_keys, &s_nth);
-        if (nth > limit) limit = nth;
-        if (base) {
-            // what is kept so far, with the limit it gives
-            const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
-            if (kept == a.n_out && buf[kept - 1] > limit) limit = buf[kept - 1];
-            block_sync();
-            if (t == 0) s_cnt = kept;
-            block_sync();
-        }
-#pragma unroll
-        for (int u = 0; u < MERGE_U; ++u)
-            if (!is_none(mine[u]) && !(limit > mine[u])) buf[atomicAdd(&s_cnt, 1)] = mine[u];
-        block_sync();
-    }
-    const int kept = keep_best(buf, tmp, s_cnt, a.n_out, s_keys, &s_nth, &s_kept);
-    // the candidate again, by its place in its beam's list
-    for (int j = t; j < kept; j += NT) {
-        const int64_t flat = static_cast<int64_t>(~buf[j].flat);
-        const int k = static_cast<int>(flat / a.vocab);
-        const uint32_t tok = static_cast<uint32_t>(flat - static_cast<int64_t>(k) * a.vocab);
-        int i = k * a.n_out;
-        while (0xFFFFFFFFu - static_cast<uint32_t>(lists[i]) != tok) ++i;
-        double score;
-        ranked(i, score);
-        write(j, i, score);
-    }
-    rest(kept);
+    valid = 0;
+    for (int i = 0; i < WARPS; ++i) valid += s_valid[i];
+    for (int j = valid + t; j < a.n_out; j += NT) put_out(a, b, j, -1, -1, -INFINITY, false, 0);
 }
 
 template <typename V>
@@ -945,8 +940,17 @@ template <typename T, bool MASK> cudaError_t launch_rows(const BeamArgs &a, cuda
     return cudaGetLastError();
 }
 
+template <typename T> cudaError_t launch_small(const BeamArgs &a, cudaStream_t st)
+{
+    beam_small_kernel<T><<<static_cast<unsigned>((static_cast<int64_t>(a.batch) * a.beams + 3) / 4), 128, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_beam_rows(const BeamArgs &a, cudaStream_t st)
 {
+    if (a.vocab <= SMALL)
+        return a.dtype == LOSSK_F32 ? launch_small<float>(a, st)
+             : a.dtype == LOSSK_BF16 ? launch_small<uint16_t>(a, st) : launch_small<h16_t>(a, st);
     if (a.dtype == LOSSK_F32) return a.allow ? launch_rows<float, true>(a, st) : launch_rows<float, false>(a, st);
     if (a.dtype == LOSSK_BF16) return a.allow ? launch_rows<uint16_t, true>(a, st) : launch_rows<uint16_t, false>(a, st);
     return a.allow ? launch_rows<h16_t, true>(a, st) : launch_rows<h16_t, false>(a, st);
@@ -955,9 +959,10 @@ cudaError_t launch_beam_rows(const BeamArgs &a, cudaStream_t st)
 cudaError_t launch_beam_merge(const BeamArgs &a0, cudaStream_t st)
 {
     BeamArgs a = a0;
-    const int keys = a.n_out * (NT / groups_for(a.n_out)) * MERGE_U, all = a.beams * a.n_out;
-    a.merge_cap = all <= NT ? NT : a.n_out + (keys < all ? keys : all);
-    const size_t bytes = 2 * sizeof(RankKey) * static_cast<size_t>(a.merge_cap) + sizeof(Key) * static_cast<size_t>(all);
+    const int all = a.beams * a.n_out;
+    // at most 1024 entries of a beam's splits in shared memory
+    a.depth = a.n_split == 1 ? 0 : a.n_out < 1024 / a.n_split ? a.n_out : 1024 / a.n_split;
+    const size_t bytes = sizeof(Key) * (2 * static_cast<size_t>(all) + WARPS * static_cast<size_t>(a.n_split) * a.depth);
     const cudaError_t e = raise_smem<beam_merge_kernel>(bytes);
     if (e != cudaSuccess) return e;
     return launch_after(true, beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(NT), bytes, st, a);
