@@ -718,6 +718,8 @@ template <typename T> __global__ void __launch_bounds__(128) beam_small_kernel(B
 // sixty-fourth of a float's rate here, so only what orders the beams is one:
 // two logarithms and an exponential per beam, a product and two sums per
 // candidate.
+constexpr int MERGE_NT = 512, MERGE_WARPS = MERGE_NT / 32;     // a warp for each of up to 16 beams
+
 struct BeamRow {
     float z, lost, m, ref, b, start;
     int kind, len;                         // kind 0: no candidates, 1: its own (finished), 2: the row's
@@ -733,7 +735,7 @@ __device__ __forceinline__ void put_out(const BeamArgs &a, int b, int j, int k, 
     if (a.length_out) a.length_out[o] = len;
 }
 
-__global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
+__global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     const int all = a.beams * a.n_out;
@@ -742,11 +744,11 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
     Key *heads = ranks + all;                          // a warp's splits' lists, `depth` of each
     __shared__ BeamRow s_row[LOSSK_BEAM_MAX_BEAMS];
     __shared__ double s_lse[LOSSK_BEAM_MAX_BEAMS], s_inv[LOSSK_BEAM_MAX_BEAMS];
-    __shared__ int s_valid[WARPS];
+    __shared__ int s_valid[MERGE_WARPS];
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b == 0 && t == 0) *a.next = 0;                 // for the workspace's next call
-    for (int k = warp; k < a.beams; k += WARPS) {
+    for (int k = warp; k < a.beams; k += MERGE_WARPS) {
         const int r = b * a.beams + k;
         const float start = a.scores[r];
         const bool done = a.finished && a.finished[r];
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
             __syncwarp();
         }
     }
-    block_sync();
+    __syncthreads();
     if (t < a.beams) {
         const BeamRow row = s_row[t];
         double lse = -INFINITY;
@@ -838,14 +840,14 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
         s_inv[t] = a.length_alpha == 0.0 ? 1.0 : a.length_alpha == 1.0 ? 1.0 / n : exp(-a.length_alpha * log(n));
         if (a.lse_out) a.lse_out[b * a.beams + t] = static_cast<float>(lse);
     }
-    block_sync();
+    __syncthreads();
     auto score_of = [&](int i, int k) {
         const double s = s_row[k].start;
         return s_row[k].kind == 2 ? s + (static_cast<double>(value_of(static_cast<uint32_t>(lists[i] >> 32))) * a.inv_t - s_lse[k])
                                   : s;
     };
     int valid = 0;
-    for (int i = t; i < all; i += NT) {
+    for (int i = t; i < all; i += MERGE_NT) {
         const int k = i / a.n_out;
         const double s = lists[i] ? score_of(i, k) : 0.0;
         ranks[i] = lists[i] ? order_of(a.length_alpha == 0.0 ? s : s * s_inv[k]) : 0;
@@ -853,10 +855,10 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
     }
     for (int o = 16; o; o >>= 1) valid += __shfl_xor_sync(0xFFFFFFFFu, valid, o);
     if (lane == 0) s_valid[warp] = valid;
-    block_sync();
+    __syncthreads();
     // A candidate's place: equal ranks go by the lower beam, then by the order of its list (the
     // larger logit, the lower token).
-    for (int i = t; i < all; i += NT) {
+    for (int i = t; i < all; i += MERGE_NT) {
         const uint64_t mine = ranks[i];
         if (!mine) continue;
         const int k = i / a.n_out;
@@ -878,8 +880,8 @@ __global__ void __launch_bounds__(NT) beam_merge_kernel(BeamArgs a)
                 score_of(i, k), was, s_row[k].len);
     }
     valid = 0;
-    for (int i = 0; i < WARPS; ++i) valid += s_valid[i];
-    for (int j = valid + t; j < a.n_out; j += NT) put_out(a, b, j, -1, -1, -INFINITY, false, 0);
+    for (int i = 0; i < MERGE_WARPS; ++i) valid += s_valid[i];
+    for (int j = valid + t; j < a.n_out; j += MERGE_NT) put_out(a, b, j, -1, -1, -INFINITY, false, 0);
 }
 
 template <typename V>
@@ -901,13 +903,14 @@ __global__ void beam_gather_kernel(int64_t n_src, int64_t n_dst, int64_t words, 
 
 // Blocks take items as they get free.  A row is cut where that makes the last
 // round of items fuller; an item's fixed work (its thresholds, lists and
-// sums) is about that of ITEM_TOKENS tokens, and none is below 4096.
+// sums) is about that of ITEM_TOKENS tokens, and a split has a chunk of 16-bit
+// logits at least (smaller ones make the merge's lists more, not the rows' time less).
 constexpr int ROW_BLOCKS = 3 * 152;
 constexpr double ITEM_TOKENS = 32000.0;
 int beam_splits(int64_t rows, int64_t vocab)
 {
-    int64_t most = vocab / 4096;
-    most = most < 1 ? 1 : most > 64 ? 64 : most;
+    int64_t most = (vocab + CHUNK * 8 - 1) / (CHUNK * 8);
+    if (most > 64) most = 64;
     int64_t best = 1;
     double cost = 0.0;
     for (int64_t n = 1; n <= most; ++n) {
@@ -960,12 +963,12 @@ cudaError_t launch_beam_merge(const BeamArgs &a0, cudaStream_t st)
 {
     BeamArgs a = a0;
     const int all = a.beams * a.n_out;
-    // at most 1024 entries of a beam's splits in shared memory
-    a.depth = a.n_split == 1 ? 0 : a.n_out < 1024 / a.n_split ? a.n_out : 1024 / a.n_split;
-    const size_t bytes = sizeof(Key) * (2 * static_cast<size_t>(all) + WARPS * static_cast<size_t>(a.n_split) * a.depth);
+    // at most 512 entries of a beam's splits in shared memory
+    a.depth = a.n_split == 1 ? 0 : a.n_out < 512 / a.n_split ? a.n_out : 512 / a.n_split;
+    const size_t bytes = sizeof(Key) * (2 * static_cast<size_t>(all) + MERGE_WARPS * static_cast<size_t>(a.n_split) * a.depth);
     const cudaError_t e = raise_smem<beam_merge_kernel>(bytes);
     if (e != cudaSuccess) return e;
-    return launch_after(true, beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(NT), bytes, st, a);
+    return launch_after(true, beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(MERGE_NT), bytes, st, a);
 }
 
 cudaError_t launch_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t row_bytes,
