@@ -230,16 +230,117 @@ __device__ __forceinline__ void walk_run(const AttnArgs &a, const long long *bas
     }
 }
 
-// Where token j of a sequence lies, in elements from the pages' start; -1 for
-// an entry out of range.
-__device__ __forceinline__ int64_t token_at(const AttnArgs &a, int seq, int j)
+// ---- tiles of keys and values --------------------------------------------------------
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
 {
-    const int p = a.table[seq * a.table_stride + j / a.page];
-    if (p < 0 || p >= a.n_pages) {
-        raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
-        return -1;
-    }
-    return p * a.page_stride + (j % a.page) * a.tok_stride;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// bytes 0: zeros, src is not read
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+
+// The tiles of a piece, copied into a ring of V::STAGES of them in shared memory
+// (each V::KT tokens' keys, then their values, rows V::RS bytes apart): start()
+// sends for the first tiles, next(i) for tile i + STAGES - 1, once every warp of
+// the ring is past tile i - 1.  Each of the ring's V::W warps copies its share
+// of the rows and leaves the tile's valid tokens as a mask in valid[stage].
+template <typename V> struct TileStream {
+    static constexpr int KT = V::KT, STEP = 32 / V::LPR, MINE = KT / STEP / V::W;
+    static constexpr uint32_t FULL = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
+    const AttnArgs &a;
+    const Piece &p;
+    const int lane, c, first, words;
+    const uint32_t ring;
+    uint32_t *valid;
+    const int32_t *row;
+    const char *kb, *vb;
+    // lane < KT: this lane's token of the tile to be looked up next, its page's column and its
+    // place in the page; the page itself is loaded a tile before it is needed
+    int t, col, off, pg, place;
+
+    __device__ __forceinline__ TileStream(const AttnArgs &a_, const Piece &p_, int sub, int lane_, uint32_t ring_,
+                                          uint32_t *valid_)
+        : a(a_), p(p_), lane(lane_), c(lane_ % V::LPR), first(sub * MINE * STEP + lane_ / V::LPR),
+          words(a_.hd * V::ESIZE / 16), ring(ring_), valid(valid_)
+    {
+        row = a.table + p.seq * a.table_stride;
+        kb = static_cast<const char *>(a.k) + p.head * a.head_stride * V::ESIZE + c * 16;
+        vb = static_cast<const char *>(a.v) + p.head * a.head_stride * V::ESIZE + c * 16;
+        t = p.t0 + lane;
+        col = t / a.page;
+        off = t % a.page;
+        look_up();
+    }
+    __device__ __forceinline__ void look_up()
+    {
+        const bool in = lane < KT && t < p.t1;
+        pg = in ? row[col] : -2;
+        place = off;
+        t += KT;
+        off += KT;
+        while (off >= a.page) {
+            off -= a.page;
+            ++col;
+        }
+    }
+    // Tile i, whose pages are pg_ and places place_.
+    __device__ __forceinline__ void fetch(int i, int pg_, int place_)
+    {
+        const int st = i % V::STAGES;
+        const bool ok = pg_ >= 0 && pg_ < a.n_pages;
+        if (!ok && pg_ != -2) raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
+        const int64_t at = ok ? (pg_ * a.page_stride + place_ * a.tok_stride) * V::ESIZE : -1;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
+        if (lane == 0) valid[st] = mask;
+        const uint32_t kd = ring + st * 2 * V::TILE + first * V::RS + c * 16, vd = kd + V::TILE;
+        // a whole tile inside one page: its rows are tok_stride apart
+        if (mask == FULL && __shfl_sync(0xFFFFFFFFu, place_, 0) + KT <= a.page) {
+            const int64_t step = a.tok_stride * V::ESIZE;
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, at, 0) + first * step;
+#pragma unroll
+            for (int x = 0; x < V::CPL; ++x)
+                if (c + x * V::LPR < words) {
+                    const char *ks = kb + o + x * V::LPR * 16, *vs = vb + o + x * V::LPR * 16;
+#pragma unroll
+                    for (int j = 0; j < MINE; ++j) {
+                        cp16(kd + j * STEP * V::RS + x * V::LPR * 16, ks);
+                        cp16(vd + j * STEP * V::RS + x * V::LPR * 16, vs);
+                        ks += STEP * step;
+                        vs += STEP * step;
+                    }
+                }
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < MINE; ++j) {
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, at, j * STEP + first);
+            const int bytes = o >= 0 ? 16 : 0;
+#pragma unroll
+            for (int x = 0; x < V::CPL; ++x)
+                if (c + x * V::LPR < words) {
+                    cp16_or_zero(kd + j * STEP * V::RS + x * V::LPR * 16, kb + (o >= 0 ? o : 0) + x * V::LPR * 16, bytes);
+                    cp16_or_zero(vd + j * STEP * V::RS + x * V::LPR * 16, vb + (o >= 0 ? o : 0) + x * V::LPR * 16, bytes);
+                }
+        }
+    }
+    __device__ __forceinline__ void send(int i, int n_tiles)
+    {
+        const int pg_ = pg, place_ = place;
+        look_up();
+        if (i < n_tiles) fetch(i, pg_, place_);
+        cp_commit();
+    }
+    __device__ __forceinline__ void start(int n_tiles)
+    {
+#pragma unroll
+        for (int i = 0; i < V::STAGES - 1; ++i) send(i, n_tiles);
+    }
+    __device__ __forceinline__ void next(int i, int n_tiles) { send(i + V::STAGES - 1, n_tiles); }
+};
 
 } // namespace lossk

@@ -172,7 +172,9 @@ AttnShape attn_shape(int dtype, int hd, int rows);
 bool attn_plans(const AttnArgs &a);
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st);
-// The tensor-core kernel (16-bit types).
+// The tensor-core kernel (16-bit types) and the CUDA-core one (fp32).
+AttnShape attn_ffma_shape(int hd, int rows);
+cudaError_t launch_attn_ffma(const AttnArgs &a, cudaStream_t st);
 AttnShape attn_mma_shape(int hd, int rows);
 cudaError_t launch_attn_mma(bool f16, const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_join(int dtype, const AttnArgs &a, cudaStream_t st);

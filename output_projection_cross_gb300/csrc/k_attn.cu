@@ -3,7 +3,7 @@
 //
 //   attn_plan   per group of sequences: how many leading pages they share, and
 //               the work in units
-//   attn        the split pass
+//   attn        the split pass (k_attn_mma.cu, k_attn_ffma.cu)
 //   attn_join   the partial results of each output row joined
 //
 // For query row q of a sequence with tokens j in [lo, len):
@@ -25,7 +25,6 @@ namespace lossk {
 namespace {
 
 constexpr int PLAN_T = 256;
-constexpr int ATTN_WARPS = 4;
 constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_THREADS = JOIN_WARPS * 32;
 constexpr int JOIN_W = 1024;
@@ -79,71 +78,6 @@ __global__ void __launch_bounds__(PLAN_T) attn_plan_kernel(AttnArgs a)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     check_lens(a);
     sum_units(a, a.base, s_warp);
-}
-
-// ---- CUDA cores ---------------------------------------------------------------------
-// One key at a time per warp, a lane holding elements lane, lane + 32, ... of
-// the head.
-constexpr int SIMT_MR = 4;
-
-template <typename T> __global__ void __launch_bounds__(ATTN_WARPS * 32) attn_simt_kernel(AttnArgs a)
-{
-    __shared__ long long s_base[BASE_GROUPS + 1];
-    const long long *base = unit_bases(a, s_base);
-    const int lane = threadIdx.x & 31, w = blockIdx.x * ATTN_WARPS + (threadIdx.x >> 5);
-    walk_run(a, base, w, [&](const Piece &p) {
-        float q[SIMT_MR][8], o[SIMT_MR][8], m[SIMT_MR], l[SIMT_MR];
-        for (int i = 0; i < SIMT_MR; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-            const T *row = static_cast<const T *>(a.q) +
-                           (i < p.rows ? row_seq(a, p, i) * a.q_stride + static_cast<int64_t>(row_head(a, p, i)) * a.hd : 0);
-            for (int e = 0; e < 8; ++e) {
-                q[i][e] = i < p.rows && lane + 32 * e < a.hd ? attn_f(row[lane + 32 * e]) : 0.f;
-                o[i][e] = 0.f;
-            }
-        }
-        for (int j = p.t0; j < p.t1; ++j) {
-            const int64_t at = token_at(a, p.seq, j);
-            if (at < 0) continue;
-            const T *k = static_cast<const T *>(a.k) + at + p.head * a.head_stride;
-            const T *v = static_cast<const T *>(a.v) + at + p.head * a.head_stride;
-            float kv[8], vv[8];
-            for (int e = 0; e < 8; ++e) {
-                kv[e] = lane + 32 * e < a.hd ? attn_f(k[lane + 32 * e]) : 0.f;
-                vv[e] = lane + 32 * e < a.hd ? attn_f(v[lane + 32 * e]) : 0.f;
-            }
-            for (int i = 0; i < SIMT_MR; ++i) {
-                float x = 0.f;
-                for (int e = 0; e < 8; ++e) x = fmaf(q[i][e], kv[e], x);
-                for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
-                x *= a.scale_log2;
-                const float mn = fmaxf(m[i], x), mz = mn == -INFINITY ? 0.f : mn;
-                const float f = exp2f(m[i] - mz), pr = exp2f(x - mz);
-                l[i] = l[i] * f + pr;
-                for (int e = 0; e < 8; ++e) o[i][e] = o[i][e] * f + pr * vv[e];
-                m[i] = mn;
-            }
-        }
-        for (int i = 0; i < p.rows; ++i) {
-            if (p.slot < 0) {
-                const float inv = l[i] > 0.f ? 1.f / l[i] : 1.f;
-                const int64_t row = static_cast<int64_t>(row_seq(a, p, i)) * a.n_q + row_head(a, p, i);
-                T *out = static_cast<T *>(a.out) + row * a.hd;
-                for (int e = 0; e < 8; ++e)
-                    if (lane + 32 * e < a.hd) attn_put(out + lane + 32 * e, o[i][e] * inv);
-                if (a.lse && lane == 0) a.lse[row] = (m[i] == -INFINITY ? 0.f : m[i]) * float(LN2) + logf(l[i]);
-            } else {
-                float *d = p.part + static_cast<int64_t>(i) * (a.hd + ATTN_ROW);
-                for (int e = 0; e < 8; ++e)
-                    if (lane + 32 * e < a.hd) d[lane + 32 * e] = o[i][e];
-                if (lane == 0) {
-                    d[a.hd] = m[i];
-                    d[a.hd + 1] = l[i];
-                }
-            }
-        }
-    });
 }
 
 // ---- joining -----------------------------------------------------------------------
@@ -308,8 +242,7 @@ template <typename T> cudaError_t launch_join(const AttnArgs &a, cudaStream_t st
 
 AttnShape attn_shape(int dtype, int hd, int rows)
 {
-    if (dtype != LOSSK_F32) return attn_mma_shape(hd, rows);
-    return AttnShape{SIMT_MR, 32, 8};
+    return dtype == LOSSK_F32 ? attn_ffma_shape(hd, rows) : attn_mma_shape(hd, rows);
 }
 
 bool attn_plans(const AttnArgs &a) { return a.share > 1 || a.n_group > BASE_GROUPS; }
@@ -325,9 +258,7 @@ cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st)
 }
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st)
 {
-    if (dtype != LOSSK_F32) return launch_attn_mma(dtype == LOSSK_F16, a, st);
-    const unsigned grid = static_cast<unsigned>((a.nw + ATTN_WARPS - 1) / ATTN_WARPS);
-    return launch_after(attn_plans(a), attn_simt_kernel<float>, dim3(grid), dim3(ATTN_WARPS * 32), 0, st, a);
+    return dtype == LOSSK_F32 ? launch_attn_ffma(a, st) : launch_attn_mma(dtype == LOSSK_F16, a, st);
 }
 cudaError_t launch_attn_join(int dtype, const AttnArgs &a, cudaStream_t st)
 {

@@ -27,18 +27,6 @@ namespace lossk {
 
 namespace {
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// bytes 0: zeros, src is not read
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -83,6 +71,7 @@ template <int HDP_, int W_> struct Variant {
     static constexpr int RS = HDP * 2 + 16;
     static constexpr int TILE = KT * RS;
     static constexpr int LPR = HDP <= 64 ? 8 : HDP <= 128 ? 16 : 32;   // lanes that copy a row
+    static constexpr int CPL = 1, ESIZE = 2;                           // 16-byte words each, bytes an element
     static constexpr bool QREG = W == 1 && HDP <= 128;                // query rows in registers
     static constexpr int QBYTES = W * 16 * RS;
     static constexpr int RING_BYTES = STAGES * 2 * TILE + QBYTES + 16 * W;
@@ -117,10 +106,6 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
     }
     const long long *base = unit_bases(a, s_base);
     const int ch = a.hd >> 3;                              // 16-byte words of a row
-    const int c = lane % V::LPR, r0 = lane / V::LPR;
-    const bool copies = c < ch;
-    const uint16_t *kb = static_cast<const uint16_t *>(a.k) + c * 8;
-    const uint16_t *vb = static_cast<const uint16_t *>(a.v) + c * 8;
     // matrix loads: K rows (tokens) lane % 8 + 8 (lane / 16), word (lane / 8) % 2; V and Q rows lane % 16, word lane / 16
     const uint32_t k_off = ((lane & 7) + ((lane >> 4) << 3)) * RS + ((lane >> 3) & 1) * 16;
     const uint32_t v_off = (lane & 15) * RS + (lane >> 4) * 16;
@@ -131,69 +116,8 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
         const int mine0 = sub * 16;                        // this warp's first row of the item
         const bool active = mine0 < p.rows;
         const int n_tiles = (p.t1 - p.t0 + KT - 1) / KT;
-        const int64_t head = p.head * a.head_stride;
-        const int32_t *row = a.table + p.seq * a.table_stride;
-        // lane < KT: this lane's token of the tile to be looked up next, its page's column and its
-        // place in the page; the page itself is loaded a tile before it is needed
-        int t = p.t0 + lane, col = t / a.page, off = t % a.page;
-        auto look_up = [&](int &pg, int &place) {
-            const bool in = lane < KT && t < p.t1;
-            pg = in ? row[col] : -2;
-            place = off;
-            t += KT;
-            off += KT;
-            while (off >= a.page) {
-                off -= a.page;
-                ++col;
-            }
-        };
-        auto fetch = [&](int i, int pg, int place) {
-            const int st = i % STAGES;
-            const bool ok = pg >= 0 && pg < a.n_pages;
-            if (!ok && pg != -2) raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
-            const int64_t at = ok ? pg * a.page_stride + place * a.tok_stride + head : -1;
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
-            if (lane == 0) valid[st] = mask;
-            // the ring's warps copy MINE steps of STEP rows each
-            constexpr int STEP = 32 / V::LPR, MINE = KT / STEP / W;
-            const int first = sub * MINE * STEP + r0;
-            const uint32_t kd = ring + st * 2 * V::TILE + first * RS + c * 16, vd = kd + V::TILE;
-            // a whole tile inside one page: its rows are tok_stride apart
-            if (mask == FULL && __shfl_sync(0xFFFFFFFFu, place, 0) + KT <= a.page) {
-                const int64_t o = __shfl_sync(0xFFFFFFFFu, at, 0) + first * a.tok_stride;
-                if (copies) {
-                    const uint16_t *ks = kb + o, *vs = vb + o;
-#pragma unroll
-                    for (int j = 0; j < MINE; ++j) {
-                        cp16(kd + j * STEP * RS, ks);
-                        cp16(vd + j * STEP * RS, vs);
-                        ks += STEP * a.tok_stride;
-                        vs += STEP * a.tok_stride;
-                    }
-                }
-                return;
-            }
-#pragma unroll
-            for (int j = 0; j < MINE; ++j) {
-                const int64_t o = __shfl_sync(0xFFFFFFFFu, at, j * STEP + first);
-                if (copies) {
-                    const int bytes = o >= 0 ? 16 : 0;
-                    cp16_or_zero(kd + j * STEP * RS, kb + (o >= 0 ? o : 0), bytes);
-                    cp16_or_zero(vd + j * STEP * RS, vb + (o >= 0 ? o : 0), bytes);
-                }
-            }
-        };
-        int pg, place;
-        look_up(pg, place);
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) {
-            int pg2, place2;
-            look_up(pg2, place2);
-            if (i < n_tiles) fetch(i, pg, place);
-            cp_commit();
-            pg = pg2;
-            place = place2;
-        }
+        TileStream<V> in(a, p, sub, lane, ring, valid);
+        in.start(n_tiles);
         // the query rows, zeros past the last one
         uint32_t qf[V::QREG ? KS : 1][4];
         for (int i = lane; i < 16 * (HDP / 8); i += 32) {
@@ -222,12 +146,7 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
             // once every warp of the ring is here, tile i has landed and tile i - 1's stage is free
             cp_wait<STAGES - 2>();
             ring_sync();
-            int pg2, place2;
-            look_up(pg2, place2);
-            if (i + STAGES - 1 < n_tiles) fetch(i + STAGES - 1, pg, place);
-            cp_commit();
-            pg = pg2;
-            place = place2;
+            in.next(i, n_tiles);
             const int st = i % STAGES;
             if (active) {
                 const uint32_t kt = ring + st * 2 * V::TILE, vt = kt + V::TILE;
