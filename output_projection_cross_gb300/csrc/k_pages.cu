@@ -16,6 +16,7 @@
 // function of the inputs alone.
 #include "../../include/lossk.h"
 #include "decode_internal.h"
+#include "decode_launch.h"
 #include "ptx.cuh"
 
 namespace lossk {
@@ -110,6 +111,20 @@ template <typename I> __device__ __forceinline__ I block_scan(I x, I *s_warp, I 
     return inc - x + (w ? s_warp[w - 1] : 0);
 }
 
+// Eight counts from ref[p0] on (of pages past the last one: `past`).
+constexpr int PER = 8;
+__device__ __forceinline__ void load_counts(const int32_t *ref, int p0, int n_pages, int past, int (&r)[PER])
+{
+    if (p0 + PER <= n_pages && (reinterpret_cast<uintptr_t>(ref + p0) & 15) == 0) {
+        const int4 x = *reinterpret_cast<const int4 *>(ref + p0), y = *reinterpret_cast<const int4 *>(ref + p0 + 4);
+        r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
+        r[4] = y.x; r[5] = y.y; r[6] = y.z; r[7] = y.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) r[i] = p0 + i < n_pages ? ref[p0 + i] : past;
+    }
+}
+
 // One slot of the sharers' table: how many sequences of the call have this
 // page as their partial last one, and the highest of them.
 __device__ __forceinline__ int sharer_slot(SharerSlot *h, int mask, int page)
@@ -197,12 +212,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) cache_plan_kernel(ReserveArgs a)
     __syncthreads();
     // the lowest `given` free pages
     int found = 0;
-    for (int base = 0; base < a.n_pages && found < given; base += PLAN_THREADS) {
-        const int p = base + t;
-        const int free = p < a.n_pages && a.ref[p] == 0;
-        int sum;
-        const int at = found + block_scan(free, s_warp, &sum);
-        if (free && at < given) a.free_list[at] = p;
+    for (int base = 0; base < a.n_pages && found < given; base += PLAN_THREADS * PER) {
+        int r[PER], free = 0, sum;
+        const int p0 = base + t * PER;
+        load_counts(a.ref, p0, a.n_pages, 1, r);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) free += r[i] == 0;
+        int at = found + block_scan(free, s_warp, &sum);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (r[i] == 0 && at < given) a.free_list[at++] = p0 + i;
         found += sum;
     }
     if (found < given) {
@@ -288,6 +307,7 @@ __device__ __forceinline__ void copy_moves(const CopyArgs &a, int64_t n, int blo
 
 __global__ void __launch_bounds__(COPY_THREADS) cache_copy_kernel(CopyArgs a)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     copy_moves(a, a.n_dev ? *a.n_dev : a.n, blockIdx.x, gridDim.x);
 }
 
@@ -319,28 +339,39 @@ __global__ void __launch_bounds__(128) cache_free_kernel(FreeArgs a)
 __global__ void __launch_bounds__(PLAN_THREADS) cache_rank_kernel(CompactArgs a)
 {
     __shared__ int s_warp[32];
+    __shared__ long long s_long[32];
     const int t = threadIdx.x;
-    int live = 0;
-    for (int p = t; p < a.n_pages; p += PLAN_THREADS) live += a.ref[p] > 0;
-    int n_live;
-    block_scan(live, s_warp, &n_live);
-    __syncthreads();
-    int holes = 0, movers = 0;
-    for (int base = 0; base < a.n_pages; base += PLAN_THREADS) {
-        const int p = base + t;
-        const bool in = p < a.n_pages, isl = in && a.ref[p] > 0;
-        int sum;
-        const int hole = in && !isl && p < n_live;
-        const int h = holes + block_scan(hole, s_warp, &sum);
-        holes += sum;
-        __syncthreads();
-        const int mover = isl && p >= n_live;
-        const int m = movers + block_scan(mover, s_warp, &sum);
-        movers += sum;
-        __syncthreads();
-        if (hole) a.moves[h].y = p;
-        if (mover) a.moves[m].x = p;
+    int live = 0, n_live;
+    for (int base = 0; base < a.n_pages; base += PLAN_THREADS * PER) {
+        int r[PER];
+        load_counts(a.ref, base + t * PER, a.n_pages, 0, r);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) live += r[i] > 0;
     }
+    block_scan(live, s_warp, &n_live);
+    // (both sums at once: holes in the low half, movers in the high one)
+    long long done = 0;
+    for (int base = 0; base < a.n_pages; base += PLAN_THREADS * PER) {
+        int r[PER];
+        const int p0 = base + t * PER;
+        load_counts(a.ref, p0, a.n_pages, 0, r);
+        long long mine = 0, sum;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            mine += r[i] > 0 ? (p0 + i >= n_live ? 1ll << 32 : 0) : p0 + i < n_live ? 1 : 0;
+        const long long at = done + block_scan(mine, s_long, &sum);
+        int h = static_cast<int>(at & 0xFFFFFFFF), m = static_cast<int>(at >> 32);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (r[i] > 0) {
+                if (p0 + i >= n_live) a.moves[m++].x = p0 + i;
+            } else if (p0 + i < n_live) {
+                a.moves[h++].y = p0 + i;
+            }
+        }
+        done += sum;
+    }
+    const int movers = static_cast<int>(done >> 32);
     __syncthreads();
     for (int k = t; k < movers; k += PLAN_THREADS) a.new_id[a.moves[k].x] = a.moves[k].y;
     if (t == 0) {
@@ -351,6 +382,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) cache_rank_kernel(CompactArgs a)
 
 __global__ void __launch_bounds__(COPY_THREADS) cache_move_kernel(CompactArgs a, CopyArgs c)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n_live = *a.n_live_out, n = *a.n_copy;
     const int64_t gt = static_cast<int64_t>(blockIdx.x) * COPY_THREADS + threadIdx.x;
     const int64_t all = static_cast<int64_t>(gridDim.x) * COPY_THREADS;
@@ -446,8 +478,8 @@ cudaError_t launch_cache_plan(const ReserveArgs &a, cudaStream_t st)
 }
 cudaError_t launch_cache_copy(const CopyArgs &a, int64_t most, cudaStream_t st)
 {
-    cache_copy_kernel<<<copy_blocks(most * pieces_of(a)), COPY_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    // (moves that the plan of the same call listed)
+    return launch_after(a.n_dev != nullptr, cache_copy_kernel, dim3(copy_blocks(most * pieces_of(a))), dim3(COPY_THREADS), 0, st, a);
 }
 cudaError_t launch_cache_free(const FreeArgs &a, cudaStream_t st)
 {
@@ -461,8 +493,7 @@ cudaError_t launch_cache_rank(const CompactArgs &a, cudaStream_t st)
 }
 cudaError_t launch_cache_move(const CompactArgs &a, const CopyArgs &c, cudaStream_t st)
 {
-    cache_move_kernel<<<copy_blocks((a.n_pages / 2 + 1) * pieces_of(c)), COPY_THREADS, 0, st>>>(a, c);
-    return cudaGetLastError();
+    return launch_after(true, cache_move_kernel, dim3(copy_blocks((a.n_pages / 2 + 1) * pieces_of(c))), dim3(COPY_THREADS), 0, st, a, c);
 }
 cudaError_t launch_cache_write(const WriteArgs &a, int word, cudaStream_t st)
 {
