@@ -132,14 +132,32 @@ __device__ __forceinline__ int quotient(long long a, int b)
                              : static_cast<int>(a / b);
 }
 
-// The run of units of warp w of nw, and the warp that has unit u.
-__device__ __forceinline__ long long run_start(long long units, int nw, int w) { return units * w / nw; }
-__device__ __forceinline__ int warp_of(long long units, int nw, long long u)
-{
-    const long long x = (u + 1) * nw - 1;
-    return units <= 0x7FFFFFFF ? quotient(x, static_cast<int>(units)) : static_cast<int>(x / units);
-}
-__device__ __forceinline__ int warps_used(long long units, int nw) { return units < nw ? static_cast<int>(units) : nw; }
+// How the units fall into runs: n runs (no more than there are units), the
+// first `more` of q + 1 units, the others of q.
+struct Runs {
+    int n;
+    long long q;
+    int more;
+    __device__ __forceinline__ Runs(long long units, int most)
+    {
+        n = units < most ? static_cast<int>(units) : most;
+        if (n < 1) n = 1;
+        q = units <= 0xFFFFFFFFll ? static_cast<unsigned>(units) / static_cast<unsigned>(n) : units / n;
+        more = static_cast<int>(units - q * n);
+    }
+    __device__ __forceinline__ long long start(int w) const { return q * w + (w < more ? w : more); }
+    // the run that has unit u
+    __device__ __forceinline__ int of(long long u) const
+    {
+        const long long big = (q + 1) * more;
+        return u < big ? over(u, q + 1) : more + over(u - big, q);
+    }
+    static __device__ __forceinline__ int over(long long a, long long b)
+    {
+        return a <= 0xFFFFFFFFll && b <= 0xFFFFFFFFll ? static_cast<int>(static_cast<unsigned>(a) / static_cast<unsigned>(b))
+                                                      : static_cast<int>(a / b);
+    }
+};
 
 // One item's piece as a warp computes it.
 struct Piece {
@@ -167,10 +185,10 @@ template <typename F>
 __device__ __forceinline__ void walk_run(const AttnArgs &a, const long long *base, int w, F &&body)
 {
     const long long units = base[a.n_group];
-    const int nw = warps_used(units, a.nw);
-    if (w >= nw) return;
-    long long u = run_start(units, nw, w);
-    const long long u1 = run_start(units, nw, w + 1);
+    const Runs runs(units, a.nw);
+    if (w >= runs.n || units == 0) return;
+    long long u = runs.start(w);
+    const long long u1 = runs.start(w + 1);
     int g = 0;
     for (int lo = 0, hi = a.n_group; hi - lo > 1;) {
         const int mid = (lo + hi) >> 1;

@@ -93,7 +93,7 @@ __device__ __forceinline__ RowPieces row_pieces(const AttnArgs &a, int s, int hq
 {
     const int g = s / a.share, head = hq / a.group, r = hq % a.group;
     const long long units = a.base[a.n_group];
-    const int nw = warps_used(units, a.nw);
+    const Runs runs(units, a.nw);
     const int ts = shared_tiles(a, g);
     const Span own = attn_span(a, s, g);
     const int tp = tiles_of(own.hi - own.mid, a.kt);
@@ -102,7 +102,7 @@ __device__ __forceinline__ RowPieces row_pieces(const AttnArgs &a, int s, int hq
     RowPieces p{nullptr, nullptr, a.ra * stride, a.rb * stride, 0, 0};
     if (ts > 0) {
         const long long u = a.base[g] + (static_cast<long long>(head) * a.cs + ca) * units_of(ts) + ITEM_COST;
-        const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + ts - 1);
+        const int w0 = runs.of(u), w1 = runs.of(u + ts - 1);
         p.n_a = w1 - w0 + 1;
         p.pa = a.part_a + (((static_cast<int64_t>(g) * a.n_kv + head) * a.cs + ca + w0) * a.ra + ri % a.mr) * stride;
     }
@@ -114,7 +114,7 @@ __device__ __forceinline__ RowPieces row_pieces(const AttnArgs &a, int s, int hq
             u += static_cast<long long>(units_of(tiles_of(x.hi - x.mid, a.kt))) * a.n_kv * a.cp;
         }
         u += (static_cast<long long>(head) * a.cp + cb) * units_of(tp) + ITEM_COST;
-        const int w0 = warp_of(units, nw, u), w1 = warp_of(units, nw, u + tp - 1);
+        const int w0 = runs.of(u), w1 = runs.of(u + tp - 1);
         p.n += w1 - w0 + 1;
         p.pb = a.part_b + (((static_cast<int64_t>(s) * a.n_kv + head) * a.cp + cb + w0) * a.rb + r % a.mr) * stride;
     }
