@@ -4,10 +4,22 @@
 // As in k_attn_mma.cu every warp walks its own run of units with its own ring
 // of tiles.  A tile's KT tokens lie across the lanes for the scores, 32 / KT
 // lanes to a token, each with its part of the head; the head's columns lie
-// across the lanes for the output.  Each element of a tile is read from
-// shared memory once and meets R query rows (scores: broadcast reads of q;
-// output: of the weights): with R = 4 that takes in 64 bytes a clock and SM,
-// with 16 rows 25, against the 24 that HBM delivers.
+// across the lanes for the output (of heads up to 64 wide across half the
+// lanes, the other half with the next token; the halves are added at the end).
+// Each element of a tile is read from shared memory once and meets R query rows
+// (scores: broadcast reads of q; output: of the weights).
+//
+// A warp's chain from a tile's scores to its output is longer than its loads, so
+// warps are worth more than deep rings: two stages of small tiles, and as many
+// warps as fit (12 where R rows leave them registers, 8 for R = 16).  Against
+// three stages of 16 tokens (4 warps for heads of 128): 34 -> 28 us for 64
+// sequences of 20 to 500 tokens with 8 KV heads of 128 and 32 query heads,
+// 301 -> 238 us for 4 of 20000 with 128 query heads.
+//
+// Measured at 4 sequences of 20000 tokens, 8 KV heads of 128 (655 MB): 117 us =
+// 5.6 TB/s for 8 query heads, 121 for 32, 146 for 64.  Up to 4 rows to a KV head
+// the stream bounds it, beyond that the multiply-adds and their reads of q and
+// of the weights.
 #include "attn_split.cuh"
 
 namespace lossk {
@@ -18,20 +30,23 @@ constexpr float RISE = 8.f;                // as in k_attn_mma.cu
 
 template <int HDP_, int R_> struct FVariant {
     static constexpr int HDP = HDP_, R = R_, W = 1;
-    static constexpr int KT = HDP <= 128 ? 16 : 8;
-    static constexpr int STAGES = 3;
+    // (a tile of 8 tokens of 256 columns for 8 rows: 172 us, of 4: 159; for 4 rows 121 and 123)
+    static constexpr int KT = HDP <= 64 ? 16 : HDP <= 128 || R < 8 ? 8 : 4;
+    static constexpr int STAGES = 2;
     static constexpr int RS = HDP * 4 + 16;            // an odd number of 16-byte words
     static constexpr int TILE = KT * RS;
     static constexpr int LPR = HDP <= 64 ? 16 : 32, CPL = HDP <= 128 ? 1 : 2, ESIZE = 4;
     static constexpr int QBYTES = R * HDP * 4, PBYTES = KT * R * 4;
     static constexpr int WARP_BYTES = STAGES * 2 * TILE + QBYTES + PBYTES + 16;
     static constexpr int SPACE = 227 * 1024 - BASE_BYTES;
-    static constexpr int WARPS = SPACE / WARP_BYTES < 8 ? SPACE / WARP_BYTES : 8;
+    static constexpr int MOST = R == 16 ? 8 : 12;
+    static constexpr int WARPS = SPACE / WARP_BYTES < MOST ? SPACE / WARP_BYTES : MOST;
 };
 
 template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_ffma_kernel(AttnArgs a)
 {
     constexpr int HDP = V::HDP, R = V::R, KT = V::KT, STAGES = V::STAGES, PARTS = 32 / KT, C = HDP <= 128 ? 1 : 2;
+    constexpr int SETS = HDP <= 64 ? 128 / HDP : 1, COLS = 32 / SETS;   // a set of lanes has every SETS-th token's columns
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ long long s_base[BASE_GROUPS + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -44,7 +59,7 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
         __syncwarp();
     }
     const long long *base = unit_bases(a, s_base);
-    const int tok = lane % KT, part = lane / KT;
+    const int tok = lane % KT, part = lane / KT, set = lane / COLS, col = lane % COLS;
     const int steps = (a.hd + 4 * PARTS - 1) / (4 * PARTS);      // of four elements a lane
     const int w = warp * gridDim.x + blockIdx.x;
 
@@ -134,15 +149,16 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
             }
             __syncwarp();
 #pragma unroll 4
-            for (int j = 0; j < KT; ++j) {
+            for (int jj = 0; jj < KT; jj += SETS) {
+                const int j = jj + set;
                 float pr[R];
 #pragma unroll
                 for (int r = 0; r < R; r += 4)
                     *reinterpret_cast<float4 *>(pr + r) = *reinterpret_cast<const float4 *>(ps + j * R + r);
 #pragma unroll
                 for (int x = 0; x < C; ++x)
-                    if (lane * 4 + 128 * x < HDP) {
-                        const float4 v = *reinterpret_cast<const float4 *>(vt + j * V::RS + lane * 16 + 512 * x);
+                    if (SETS > 1 || lane * 4 + 128 * x < HDP) {
+                        const float4 v = *reinterpret_cast<const float4 *>(vt + j * V::RS + col * 16 + 512 * x);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             o[r][x].x = fmaf(pr[r], v.x, o[r][x].x);
@@ -157,6 +173,13 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (r >= p.rows) break;
+#pragma unroll
+            for (int x = COLS; x < 32; x <<= 1) {
+                o[r][0].x += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].x, x);
+                o[r][0].y += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].y, x);
+                o[r][0].z += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].z, x);
+                o[r][0].w += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].w, x);
+            }
             float sum = l[r];
             for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
             const int64_t row = static_cast<int64_t>(row_seq(a, p, r)) * a.n_q + row_head(a, p, r);
@@ -165,8 +188,8 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
             const float f = p.slot < 0 ? inv : 1.f;
 #pragma unroll
             for (int x = 0; x < C; ++x) {
-                const int e = lane * 4 + 128 * x;
-                if (e < a.hd)
+                const int e = col * 4 + 128 * x;
+                if (set == 0 && e < a.hd)
                     *reinterpret_cast<float4 *>(d + e) = make_float4(o[r][x].x * f, o[r][x].y * f, o[r][x].z * f, o[r][x].w * f);
             }
             if (lane == 0) {

@@ -3,11 +3,10 @@
 //
 // One new token per sequence makes the pass a stream: every key and value is
 // read once from HBM and meets only the query rows of its KV head (and, for
-// shared pages, of its group), 2 to 32 multiply-adds a byte.  That is far below
-// what tcgen05 needs to be worth its 128-row tiles, so the products run as
-// mma.sync m16n8k16 with 16 query rows (1.5 of 16 tensor instructions per
-// issue slot would be needed to keep HBM waiting), and the kernel is built
-// around the loads:
+// shared pages, of its group), 2 to 32 multiply-adds a byte.  tcgen05 would
+// spend tiles of 128 rows on them, so the products run as mma.sync m16n8k16 with
+// 16 query rows (the tensor pipe is 23 to 28 % active while HBM is read at 86 %
+// of the copy rate), and the kernel is built around the loads:
 //
 //  - every warp walks its own run of units with its own ring of STAGES tiles
 //    of KT tokens in shared memory, filled by 16-byte asynchronous copies two
@@ -21,6 +20,14 @@
 //  - a weight goes to the tensor cores as the sum of two 16-bit values, so
 //    that it keeps 16 (bf16) or 22 (fp16) bits: two instructions instead of
 //    one, which the stream hides, for an output that is rounded once.
+//
+// Measured, split pass and join: one sequence of 131072 tokens (8 KV heads of
+// 128, bf16, 537 MB) 99 to 103 us, the pass alone 94 us = 5.7 TB/s; 33 sequences
+// of 1 to 9000 tokens (160 MB) 40 us; 8 x 8 beams on 4096 shared tokens (170 MB)
+// 56 us.  What bounds it: the stream at 6.2 TB/s at the margin, and about 9 us
+// before the first tile and after the last.  With the loads alone the three
+// take 92, 36 and 43 us, with the products alone 35, 20 and 38.  Two or four
+// stages are within 2 % of three.
 #include "attn_split.cuh"
 
 namespace lossk {
