@@ -11,14 +11,17 @@ namespace lossk {
 __device__ __forceinline__ float attn_f(float x) { return x; }
 __device__ __forceinline__ float attn_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 __device__ __forceinline__ float attn_f(h16_t x) { return f16_to_f(x.bits); }
-__device__ __forceinline__ void attn_put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void attn_put(uint16_t *p, float v)
+__device__ __forceinline__ void attn_put4(float *p, float4 v, float f)
 {
-    *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+    *reinterpret_cast<float4 *>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
 }
-__device__ __forceinline__ void attn_put(h16_t *p, float v)
+__device__ __forceinline__ void attn_put4(uint16_t *p, float4 v, float f)
 {
-    p->bits = static_cast<uint16_t>(pack_f16x2(v, 0.f) & 0xFFFFu);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+}
+__device__ __forceinline__ void attn_put4(h16_t *p, float4 v, float f)
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_f16x2(v.x * f, v.y * f), pack_f16x2(v.z * f, v.w * f));
 }
 
 // A sequence's length as the kernels use it: 0 where it is out of range.
@@ -109,7 +112,7 @@ __device__ __forceinline__ void check_lens(const AttnArgs &a)
 }
 
 // The units before each group, for the split pass: summed by every block for
-// itself (block 0 also leaves them to the join) unless attn_plan already did.
+// itself unless attn_plan already did.
 __device__ __forceinline__ const long long *unit_bases(const AttnArgs &a, long long *s_base)
 {
     __shared__ long long s_warp[32];
@@ -118,10 +121,7 @@ __device__ __forceinline__ const long long *unit_bases(const AttnArgs &a, long l
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (a.n_group > BASE_GROUPS) return a.base;
     sum_units(a, s_base, s_warp);
-    if (blockIdx.x == 0) {
-        check_lens(a);
-        for (int g = threadIdx.x; g <= a.n_group; g += blockDim.x) a.base[g] = s_base[g];
-    }
+    if (blockIdx.x == 0) check_lens(a);
     return s_base;
 }
 
@@ -170,6 +170,16 @@ struct Piece {
     float *part;
 };
 
+// Items numbered: of a group's shared part, of a sequence.
+__device__ __forceinline__ int64_t shared_item(const AttnArgs &a, int g, int head, int c)
+{
+    return (static_cast<int64_t>(g) * a.n_kv + head) * a.cs + c;
+}
+__device__ __forceinline__ int64_t own_item(const AttnArgs &a, int s, int head, int c)
+{
+    return (static_cast<int64_t>(s) * a.n_kv + head) * a.cp + c;
+}
+
 // Query row i of a piece: sequence and query head.
 __device__ __forceinline__ int row_seq(const AttnArgs &a, const Piece &p, int i)
 {
@@ -180,7 +190,8 @@ __device__ __forceinline__ int row_head(const AttnArgs &a, const Piece &p, int i
     return p.head * a.group + (p.first_row + i) % a.group;
 }
 
-// Walks run w; body(piece) computes each piece.
+// Walks run w; body(piece) computes each piece.  The run that has an item's first
+// tile also notes for the join which runs have the others.
 template <typename F>
 __device__ __forceinline__ void walk_run(const AttnArgs &a, const long long *base, int w, F &&body)
 {
@@ -203,6 +214,7 @@ __device__ __forceinline__ void walk_run(const AttnArgs &a, const long long *bas
         const long long su = static_cast<long long>(us) * a.n_kv * a.cs;
         Piece p;
         int at, tiles, lo, hi;                      // the run goes on `at` units into the item
+        int2 *runs_of;
         if (in < su) {
             const int item = quotient(in, us), c = item % a.cs;
             at = static_cast<int>(in - static_cast<long long>(item) * us);
@@ -214,7 +226,9 @@ __device__ __forceinline__ void walk_run(const AttnArgs &a, const long long *bas
             const Span r = attn_span(a, p.seq, g);
             lo = r.lo;
             hi = r.mid;
-            p.slot = (static_cast<int64_t>(g) * a.n_kv + p.head) * a.cs + c + w;
+            p.slot = shared_item(a, g, p.head, c);
+            runs_of = a.runs_a + p.slot;
+            p.slot += w;
             p.part = a.part_a + p.slot * a.ra * (a.hd + ATTN_ROW);
         } else {
             in -= su;
@@ -234,13 +248,18 @@ __device__ __forceinline__ void walk_run(const AttnArgs &a, const long long *bas
             p.rows = min(a.mr, a.group - p.first_row);
             lo = r.mid;
             hi = r.hi;
-            p.slot = (static_cast<int64_t>(s) * a.n_kv + p.head) * a.cp + c + w;
+            p.slot = own_item(a, s, p.head, c);
+            runs_of = a.runs_b + p.slot;
+            p.slot += w;
             p.part = a.part_b + p.slot * a.rb * (a.hd + ATTN_ROW);
         }
         const int n = static_cast<int>(min(static_cast<long long>(units_of(tiles) - at), u1 - u));
         const int tile0 = max(at - ITEM_COST, 0), tile1 = at + n - ITEM_COST;
         u += n;
         if (tile1 <= 0) continue;                   // the run ends within the item's start
+        // (every warp of a ring notes the same)
+        if (tile0 == 0 && (threadIdx.x & 31) == 0)
+            *runs_of = make_int2(w, tile1 == tiles ? 1 : runs.of(u + (tiles - tile1) - 1) - w + 1);
         if (ts == 0 && tile0 == 0 && tile1 == tiles) p.slot = -1;
         p.t0 = lo + tile0 * a.kt;
         p.t1 = min(hi, lo + tile1 * a.kt);

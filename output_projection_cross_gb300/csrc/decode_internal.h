@@ -155,7 +155,8 @@ struct AttnArgs {
     int ra, rb;                                    // rows a partial result holds, shared and private
     int nw;                                        // runs at most
     int32_t *shared;                               // [n_group] shared tokens
-    long long *base;                               // [n_group + 1] units before each group
+    long long *base;                               // [n_group + 1] units before each group, where attn_plan leaves them
+    int2 *runs_a, *runs_b;                         // per item of a group's shared part, of a sequence: first run, runs
     float *part_a, *part_b;                        // partial results per row: o[hd], m (log2 units), l, and 2 unused
     int *fault;
 };

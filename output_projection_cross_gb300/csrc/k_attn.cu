@@ -21,10 +21,12 @@
 // The split pass then ends everywhere at much the same time, and its results
 // are few: a run has a partial one only where it begins or ends inside an item.
 //
-// Measured: a single sequence of 512 tokens takes 10 us (two launches and a
-// chain of dependent loads each: lengths, table, tokens), of 131072 tokens 99 to
-// 103 us (k_attn_mma.cu); the join takes 4 us of the first and 9 us for 2048 rows
-// in 2 to 14 pieces.
+// Measured: a single sequence of 512 tokens takes 9 us (two launches and a
+// chain of dependent loads each: lengths, table, tokens), of 131072 tokens 96 us
+// (k_attn_mma.cu).  The join's own share is 3 us of the first, 4 us of the second
+// (32 rows in 152 pieces) and 6 us for 2048 rows in 2 to 14 pieces: its loads'
+// latency, twice (which runs have pieces, then the pieces).  Where it worked out
+// the runs itself from the lengths it took 4, 9 and 10 us.
 #include "attn_split.cuh"
 
 namespace lossk {
@@ -32,9 +34,7 @@ namespace lossk {
 namespace {
 
 constexpr int PLAN_T = 256;
-constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_THREADS = JOIN_WARPS * 32;
-constexpr int JOIN_W = 1024;
+constexpr int JOIN_FEW = 3, JOIN_MANY = 16;
 
 // Shared tokens of each group: the leading pages whose ids agree in all its
 // rows, full in all of them.  With a window the rows have to be equally long,
@@ -99,150 +99,132 @@ struct RowPieces {
 __device__ __forceinline__ RowPieces row_pieces(const AttnArgs &a, int s, int hq)
 {
     const int g = s / a.share, head = hq / a.group, r = hq % a.group;
-    const long long units = a.base[a.n_group];
-    const Runs runs(units, a.nw);
-    const int ts = shared_tiles(a, g);
-    const Span own = attn_span(a, s, g);
-    const int tp = tiles_of(own.hi - own.mid, a.kt);
     const int ri = (s % a.share) * a.group + r, ca = ri / a.mr, cb = r / a.mr;
-    const int64_t stride = a.hd + ATTN_ROW;
-    RowPieces p{nullptr, nullptr, a.ra * stride, a.rb * stride, 0, 0};
-    if (ts > 0) {
-        const long long u = a.base[g] + (static_cast<long long>(head) * a.cs + ca) * units_of(ts) + ITEM_COST;
-        const int w0 = runs.of(u), w1 = runs.of(u + ts - 1);
-        p.n_a = w1 - w0 + 1;
-        p.pa = a.part_a + (((static_cast<int64_t>(g) * a.n_kv + head) * a.cs + ca + w0) * a.ra + ri % a.mr) * stride;
-    }
-    p.n = p.n_a;
-    if (tp > 0) {
-        long long u = a.base[g] + static_cast<long long>(units_of(ts)) * a.n_kv * a.cs;
-        for (int i = g * a.share; i < s; ++i) {
-            const Span x = attn_span(a, i, g);
-            u += static_cast<long long>(units_of(tiles_of(x.hi - x.mid, a.kt))) * a.n_kv * a.cp;
-        }
-        u += (static_cast<long long>(head) * a.cp + cb) * units_of(tp) + ITEM_COST;
-        const int w0 = runs.of(u), w1 = runs.of(u + tp - 1);
-        p.n += w1 - w0 + 1;
-        p.pb = a.part_b + (((static_cast<int64_t>(s) * a.n_kv + head) * a.cp + cb + w0) * a.rb + r % a.mr) * stride;
-    }
+    const int64_t ia = shared_item(a, g, head, ca), ib = own_item(a, s, head, cb), stride = a.hd + ATTN_ROW;
+    // (read before it is known whether there are such items: one wait for all of it)
+    const int2 wa = a.share > 1 ? a.runs_a[ia] : make_int2(0, 0), wb = a.runs_b[ib];
+    const Span own = attn_span(a, s, g);
+    RowPieces p;
+    p.sa = a.ra * stride;
+    p.sb = a.rb * stride;
+    p.pa = a.part_a + ((ia + wa.x) * a.ra + ri % a.mr) * stride;
+    p.pb = a.part_b + ((ib + wb.x) * a.rb + r % a.mr) * stride;
+    p.n_a = shared_tiles(a, g) > 0 ? wa.y : 0;
+    p.n = p.n_a + (own.hi > own.mid ? wb.y : 0);
     if (p.n_a == 0 && p.n == 1) p.n = -1;
     return p;
 }
 
-// The weighted sum of pieces i0, i0 + step, ...: a lane holds elements 4 lane..
-// and 128 + 4 lane..
-struct RowSum {
-    float4 o[2];
-    float l;
-};
-template <typename W>
-__device__ __forceinline__ RowSum sum_pieces(const RowPieces &p, int hd, int i0, int step, int lane, W &&weight)
+// A row by WPR warps (a block of WPR warps, or of eight rows where it is 1); H
+// vectors of four columns a lane.  A warp takes every WPR-th piece, B at a time,
+// all their loads in flight together; its maximum runs on as in the split pass.
+template <typename T, int H, int WPR>
+__global__ void __launch_bounds__(WPR == 1 ? 256 : WPR * 32) attn_join_kernel(AttnArgs a)
 {
-    RowSum r = {};
-    const int words = hd >> 2;
-#pragma unroll 4
-    for (int i = i0; i < p.n; i += step) {
-        const float *d = p.at(i);
-        const float f = weight(i, d);
-        r.l += f * d[hd + 1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (lane + 32 * h < words) {
-                const float4 x = *reinterpret_cast<const float4 *>(d + 4 * (lane + 32 * h));
-                r.o[h].x += f * x.x;
-                r.o[h].y += f * x.y;
-                r.o[h].z += f * x.z;
-                r.o[h].w += f * x.w;
-            }
-    }
-    return r;
-}
-
-template <typename T>
-__device__ __forceinline__ void put_row(const AttnArgs &a, int64_t row, int lane, const RowSum &r, float mz)
-{
-    const float inv = r.l > 0.f ? 1.f / r.l : 1.f;
-    T *out = static_cast<T *>(a.out) + row * a.hd;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int e = 4 * (lane + 32 * h);
-        if (e < a.hd) {
-            attn_put(out + e, r.o[h].x * inv);
-            attn_put(out + e + 1, r.o[h].y * inv);
-            attn_put(out + e + 2, r.o[h].z * inv);
-            attn_put(out + e + 3, r.o[h].w * inv);
-        }
-    }
-    if (a.lse && lane == 0) a.lse[row] = mz * float(LN2) + logf(r.l);
-}
-
-// A warp per output row: many rows, of few pieces each.
-template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_rows_kernel(AttnArgs a)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * JOIN_WARPS + (threadIdx.x >> 5);
+    constexpr int B = 8 / H;
+    __shared__ float4 s_o[WPR > 1 ? WPR : 1][32 * H];
+    __shared__ float2 s_ml[WPR > 1 ? WPR : 1];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, k0 = WPR == 1 ? 0 : warp;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t row = WPR == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : blockIdx.x;
     if (row >= static_cast<int64_t>(a.n_group) * a.share * a.n_q) return;
     const RowPieces p = row_pieces(a, static_cast<int>(row / a.n_q), static_cast<int>(row % a.n_q));
     if (p.n < 0) return;
-    float M = -INFINITY;
-    for (int i = lane; i < p.n; i += 32) M = fmaxf(M, p.at(i)[a.hd]);
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    const float mz = M == -INFINITY ? 0.f : M;
-    const RowSum r = sum_pieces(p, a.hd, 0, 1, lane, [&](int, const float *d) { return exp2f(d[a.hd] - mz); });
-    put_row<T>(a, row, lane, r, mz);
-}
-
-// A block per output row: few rows, cut into many pieces.
-template <typename T> __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(AttnArgs a)
-{
-    __shared__ float4 s_o[JOIN_WARPS][64];
-    __shared__ float s_w[JOIN_W], s_x[JOIN_WARPS], s_l[JOIN_WARPS];
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const RowPieces p = row_pieces(a, blockIdx.x / a.n_q, blockIdx.x % a.n_q);
-    if (p.n < 0) return;
-    // the largest m; the pieces' m are kept for the weights
-    float M = -INFINITY;
-    for (int i = t; i < p.n; i += JOIN_THREADS) {
-        const float m = p.at(i)[a.hd];
-        if (i < JOIN_W) s_w[i] = m;
-        M = fmaxf(M, m);
-    }
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    if (lane == 0) s_x[warp] = M;
-    __syncthreads();
-    for (int i = 0; i < JOIN_WARPS; ++i) M = fmaxf(M, s_x[i]);
-    const float mz = M == -INFINITY ? 0.f : M;
-    RowSum r = sum_pieces(p, a.hd, warp, JOIN_WARPS, lane,
-                          [&](int i, const float *d) { return exp2f((i < JOIN_W ? s_w[i] : d[a.hd]) - mz); });
-    s_o[warp][lane] = r.o[0];
-    s_o[warp][lane + 32] = r.o[1];
-    if (lane == 0) s_l[warp] = r.l;
-    __syncthreads();
-    if (warp) return;
-    for (int i = 1; i < JOIN_WARPS; ++i) {
-        r.l += s_l[i];
+    const int words = a.hd >> 2;
+    float M = -INFINITY, mz = 0.f, l = 0.f;
+    float4 o[H] = {};
+    for (int i0 = k0; i0 < p.n; i0 += WPR * B) {
+        float2 ml[B];
+        float4 x[B][H];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 x = s_o[i][lane + 32 * h];
-            r.o[h].x += x.x;
-            r.o[h].y += x.y;
-            r.o[h].z += x.z;
-            r.o[h].w += x.w;
+        for (int b = 0; b < B; ++b) {
+            const int i = i0 + b * WPR;
+            ml[b] = make_float2(-INFINITY, 0.f);
+            if (i < p.n) {
+                const float *d = p.at(i);
+                ml[b] = *reinterpret_cast<const float2 *>(d + a.hd);
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    if (lane + 32 * h < words) x[b][h] = *reinterpret_cast<const float4 *>(d + 4 * (lane + 32 * h));
+            }
         }
+        float top = M;
+#pragma unroll
+        for (int b = 0; b < B; ++b) top = fmaxf(top, ml[b].x);
+        mz = top == -INFINITY ? 0.f : top;
+        const float old = exp2f(M - mz);
+        M = top;
+        l *= old;
+#pragma unroll
+        for (int h = 0; h < H; ++h) o[h] = make_float4(o[h].x * old, o[h].y * old, o[h].z * old, o[h].w * old);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (i0 + b * WPR < p.n) {
+                const float f = exp2f(ml[b].x - mz);
+                l += f * ml[b].y;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    if (lane + 32 * h < words) {
+                        o[h].x += f * x[b][h].x;
+                        o[h].y += f * x[b][h].y;
+                        o[h].z += f * x[b][h].z;
+                        o[h].w += f * x[b][h].w;
+                    }
+            }
     }
-    put_row<T>(a, blockIdx.x, lane, r, mz);
+    T *out = static_cast<T *>(a.out) + row * a.hd;
+    if constexpr (WPR == 1) {
+        const float inv = l > 0.f ? 1.f / l : 1.f;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            if (lane + 32 * h < words) attn_put4(out + 4 * (lane + 32 * h), o[h], inv);
+        if (a.lse && lane == 0) a.lse[row] = mz * float(LN2) + logf(l);
+    } else {
+#pragma unroll
+        for (int h = 0; h < H; ++h) s_o[warp][lane + 32 * h] = o[h];
+        if (lane == 0) s_ml[warp] = make_float2(M, l);
+        __syncthreads();
+        // warp h joins the sums of vector h of every lane
+        if (warp >= H) return;
+        const float2 mine = lane < WPR ? s_ml[lane] : make_float2(-INFINITY, 0.f);
+        float top = mine.x;
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        mz = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(mine.x - mz);
+        l = f * mine.y;
+        for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < WPR; ++k) {
+            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+            const float4 x = s_o[k][t];
+            sum.x += fk * x.x;
+            sum.y += fk * x.y;
+            sum.z += fk * x.z;
+            sum.w += fk * x.w;
+        }
+        const float inv = l > 0.f ? 1.f / l : 1.f;
+        if (t < words) attn_put4(out + 4 * t, sum, inv);
+        if (a.lse && t == 0) a.lse[row] = mz * float(LN2) + logf(l);
+    }
 }
 
-template <typename T> cudaError_t launch_join(const AttnArgs &a, cudaStream_t st)
+template <typename T, int H> cudaError_t launch_join_h(const AttnArgs &a, cudaStream_t st)
 {
     const int64_t rows = static_cast<int64_t>(a.n_group) * a.share * a.n_q;
-    // a block per row while all blocks fit at once (8 per SM): 1056 rows of up to 28 pieces took
-    // 7 us less than a warp per row, 2048 rows of 2 to 14 pieces 10 us more
-    if (rows <= 8 * 152) return launch_after(true, attn_join_kernel<T>, dim3(static_cast<unsigned>(rows)), dim3(JOIN_THREADS), 0, st, a);
-    return launch_after(true, attn_join_rows_kernel<T>, dim3(static_cast<unsigned>((rows + JOIN_WARPS - 1) / JOIN_WARPS)),
-                        dim3(JOIN_THREADS), 0, st, a);
+    const int64_t pieces = a.nw / (static_cast<int64_t>(a.n_group) * a.share * a.n_kv * a.cp) + 1;
+    // pieces a row has where lengths are equal.  One, 4 and 16 warps a row take, split pass and join:
+    // 52, 54 and 82 us (64 sequences in groups of 8, 2048 rows, pieces 3); 41, 37 and 46 us (33 sequences of
+    // up to 9000 tokens, 1056 rows, pieces 5); 100, 100 and 96 us (one of 131072, 32 rows, pieces 153)
+    if (pieces > JOIN_MANY)
+        return launch_after(true, attn_join_kernel<T, H, 16>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, a);
+    if (pieces > JOIN_FEW)
+        return launch_after(true, attn_join_kernel<T, H, 4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, a);
+    return launch_after(true, attn_join_kernel<T, H, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, a);
+}
+template <typename T> cudaError_t launch_join(const AttnArgs &a, cudaStream_t st)
+{
+    return a.hd <= 128 ? launch_join_h<T, 1>(a, st) : launch_join_h<T, 2>(a, st);
 }
 
 } // namespace

@@ -22,9 +22,8 @@
 //    one, which the stream hides, for an output that is rounded once.
 //
 // Measured, split pass and join: one sequence of 131072 tokens (8 KV heads of
-// 128, bf16, 537 MB) 99 to 103 us, the pass alone 94 us = 5.7 TB/s; 33 sequences
-// of 1 to 9000 tokens (160 MB) 40 us; 8 x 8 beams on 4096 shared tokens (170 MB)
-// 56 us.  What bounds it: the stream at 6.2 TB/s at the margin, and about 9 us
+// 128, bf16, 537 MB) 96 us, the pass alone 92 us = 5.8 TB/s; 33 sequences of 1 to
+// 9000 tokens (160 MB) 37 us; 8 x 8 beams on 4096 shared tokens (170 MB) 52 us.  What bounds it: the stream at 6.2 TB/s at the margin, and about 9 us
 // before the first tile and after the last.  With the loads alone the three
 // take 92, 36 and 43 us, with the products alone 35, 20 and 38.  Two or four
 // stages are within 2 % of three.

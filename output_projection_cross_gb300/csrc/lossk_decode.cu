@@ -121,7 +121,7 @@ CopyArgs copy_args(void *pool, int64_t n_planes, int64_t plane_stride, int64_t p
 // rows on either side (a group's shared rows are cut into items of mr rows,
 // the last one less than full), and one item's rows more for each run.
 struct AttnLayout {
-    size_t off_shared, off_base, off_part, total;
+    size_t off_shared, off_base, off_runs, off_part, total;
 };
 
 int32_t attn_layout(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t hd, AttnLayout *L)
@@ -131,7 +131,9 @@ int32_t attn_layout(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t hd, AttnLa
         return LOSSK_DIMENSION_TOO_LARGE;
     L->off_shared = 256;
     L->off_base = align256(L->off_shared + sizeof(int32_t) * n_seq);
-    L->off_part = align256(L->off_base + sizeof(long long) * (n_seq + 1));
+    L->off_runs = align256(L->off_base + sizeof(long long) * (n_seq + 1));
+    // (an item has at least one query row)
+    L->off_part = align256(L->off_runs + sizeof(int2) * 2 * n_seq * n_q);
     const size_t rows = 4 * static_cast<size_t>(n_seq) * n_q + 2 * ATTN_MAX_ROWS;
     L->total = align256(L->off_part + sizeof(float) * rows * (hd + ATTN_ROW));
     return LOSSK_OK;
@@ -582,6 +584,8 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
     a.nw = static_cast<int>(units < 152 * shape.runs ? units : 152 * shape.runs);
     a.shared = reinterpret_cast<int32_t *>(ws + L.off_shared);
     a.base = reinterpret_cast<long long *>(ws + L.off_base);
+    a.runs_a = reinterpret_cast<int2 *>(ws + L.off_runs);
+    a.runs_b = a.runs_a + n_seq * n_q_heads;
     a.part_a = reinterpret_cast<float *>(ws + L.off_part);
     a.part_b = a.part_a + (static_cast<int64_t>(a.n_group) * a.n_kv * a.cs + a.nw) * a.ra * (a.hd + ATTN_ROW);
     a.fault = fault_of(workspace);
