@@ -555,37 +555,32 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) b
                 limit = nth_of_groups(best, a.n_out, s_keys, &s_nth);
                 if (limit) limit_x = value_of(static_cast<uint32_t>(limit >> 32));
             }
-            // keys from the limit on go to the buffer
-            if (fmaxf(top, j == 0 ? one : top) >= limit_x) {
-                uint32_t hits = 0;
+            // keys from the limit on go to the buffer.  Few threads have any, so a warp looks through one such
+            // thread's values together, a value a lane
+            const auto put = [&](float x, int v) {
+                const Key q = key_of(x, v);
+                if (q < limit) return;
+                const int at = atomicAdd(&s_cnt, 1);
+                if (at < a.cap) buf[at] = q;
+                else s_over = 1;
+            };
+            if (j == 0 && one >= limit_x && one > -INFINITY) put(one, one_v);
+            const T *mine = reinterpret_cast<const T *>(smem + sg * STAGE_BYTES + it.skew) +
+                            ((lane / NV) * NT + (t - lane)) * NV + lane % NV;
+            for (uint32_t who = __ballot_sync(0xFFFFFFFFu, top >= limit_x && top > -INFINITY); who; who &= who - 1) {
+                const int from = __ffs(who) - 1, i = base + (lane / NV) * NT + t - lane + from;
+                float x = -INFINITY;
+                if (lane < U * NV && i < it.n_vec) x = beam_f(mine[from * NV]);
+                if constexpr (MASK) {
+                    uint32_t w = 0;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (!(vec_max<T>(cur[u]) < limit_x)) {
-                        float f[NV];
-                        unpack<T>(cur[u], f);
-#pragma unroll
-                        for (int e = 0; e < NV; ++e)
-                            if (f[e] >= limit_x && f[e] > -INFINITY) hits |= 1u << (u * NV + e);
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t y = __shfl_sync(0xFFFFFFFFu, bits[u], from);
+                        if (lane / NV == u) w = y;
                     }
-                bool last = j == 0 && one >= limit_x && one > -INFINITY;
-                while (hits || last) {
-                    float x = one;
-                    int v = one_v;
-                    if (hits) {
-                        // (read again, by its place: a hit is rare)
-                        const int b = __ffs(hits) - 1;
-                        hits &= hits - 1;
-                        v = token(b);
-                        x = beam_f(reinterpret_cast<const T *>(smem + sg * STAGE_BYTES + it.skew)[v - it.v0 - base * NV]);
-                    } else {
-                        last = false;
-                    }
-                    const Key q = key_of(x, v);
-                    if (q < limit) continue;
-                    const int at = atomicAdd(&s_cnt, 1);
-                    if (at < a.cap) buf[at] = q;
-                    else s_over = 1;
+                    if (!((w >> (lane % NV)) & 1u)) x = -INFINITY;
                 }
+                if (x >= limit_x && x > -INFINITY) put(x, it.v0 + i * NV + lane % NV);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[sg]);  // this warp is done with the chunk
