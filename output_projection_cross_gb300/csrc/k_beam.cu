@@ -705,27 +705,29 @@ template <typename T> __global__ void __launch_bounds__(128) beam_small_kernel(B
 }
 
 // ---- merge -------------------------------------------------------------------------
-// One block per batch entry.  A warp per beam joins the sums and lists of its
-// splits; lane k of the first warps then forms beam k's log-sum-exp and
-// divisor in double; then every beam's candidates are ranked.  A list is in
-// falling order, so a candidate's place among all is its place in its list
-// and what a binary search counts in each other list.  Doubles run at a
+// One block per batch entry.  A warp per beam joins the sums of its splits; the
+// lists are joined while lane k of another warp forms beam k's log-sum-exp in
+// double; then every beam's candidates are ranked.  A list is in falling order,
+// so a candidate's place among all is its place in its list and what a binary
+// search counts in each other list, a thread for each (candidate, list).  Doubles run at a
 // sixty-fourth of a float's rate here, so only what orders the beams is one:
 // two logarithms and an exponential per beam, a product and two sums per
 // candidate.
-constexpr int MERGE_NT = 512, MERGE_WARPS = MERGE_NT / 32;     // a warp for each of up to 16 beams
+// The lists are joined by a warp per beam (up to 16 at a time) while one more
+// warp does the logarithms, a lane per beam, and another the divisors.
+constexpr int LIST_WARPS = 16, MERGE_WARPS = LIST_WARPS + 2, MERGE_NT = MERGE_WARPS * 32;
 
 struct BeamRow {
     float z, lost, m, ref, b, start;
     int kind, len;                         // kind 0: no candidates, 1: its own (finished), 2: the row's
 };
 
-__device__ __forceinline__ void put_out(const BeamArgs &a, int b, int j, int k, int64_t tok, double score, bool was, int len)
+__device__ __forceinline__ void put_out(const BeamArgs &a, int b, int j, int k, int64_t tok, float score, bool was, int len)
 {
     const int64_t o = static_cast<int64_t>(b) * a.n_out + j;
     a.parent_out[o] = k;
     a.token_out[o] = tok;
-    a.score_out[o] = static_cast<float>(score);
+    a.score_out[o] = score;
     if (a.finished_out) a.finished_out[o] = k >= 0 && (was || tok == a.end_token);
     if (a.length_out) a.length_out[o] = len;
 }
@@ -736,27 +738,48 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
     const int all = a.beams * a.n_out;
     Key *lists = reinterpret_cast<Key *>(smem);        // [beams][n_out]
     uint64_t *ranks = lists + all;                     // the same places: order of the rank, 0: no candidate
-    Key *heads = ranks + all;                          // a warp's splits' lists, `depth` of each
+    Key *heads = ranks + all;                          // a warp's splits' lists, `depth` of each, and then:
+    float *score = reinterpret_cast<float *>(heads);
+    int *place = reinterpret_cast<int *>(score + all);
     __shared__ BeamRow s_row[LOSSK_BEAM_MAX_BEAMS];
     __shared__ double s_lse[LOSSK_BEAM_MAX_BEAMS], s_inv[LOSSK_BEAM_MAX_BEAMS];
     __shared__ int s_valid[MERGE_WARPS];
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b == 0 && t == 0) *a.next = 0;                 // for the workspace's next call
+    // the splits' lists, each in falling order, from shared memory (what lies deeper than `depth` from
+    // where it is); asked for before it is known whether the beam has any
+    const int depth = a.n_split > 1 ? a.depth : a.n_out;
+    Key *mine = heads + warp * a.n_split * depth;
+    auto entry = [&](int k, int i, int j) {
+        if (i >= a.n_split || j >= a.n_out) return Key(0);
+        const BeamCand x = a.cand[(static_cast<int64_t>(b) * a.beams + k) * a.n_split * a.n_out + i * a.n_out + j];
+        return x.tok >= 0 ? key_of(x.x, x.tok) : Key(0);
+    };
+    auto fetch = [&](int k) {
+        if (a.n_split == 1)
+            for (int j = lane; j < a.n_out; j += 32) lists[k * a.n_out + j] = entry(k, 0, j);
+        else
+            for (int i = lane; i < a.n_split * depth; i += 32) mine[i] = entry(k, i / depth, i % depth);
+    };
+    if (warp < LIST_WARPS && warp < a.beams) fetch(warp);
     for (int k = warp; k < a.beams; k += MERGE_WARPS) {
         const int r = b * a.beams + k;
         const float start = a.scores[r];
         const bool done = a.finished && a.finished[r];
         const int len = (a.lengths ? a.lengths[r] : 0) + (done ? 0 : 1);
+        // lane i has splits i and i + 32
+        BeamStat st[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            st[h] = BeamStat{0.f, 0.f, -INFINITY, -INFINITY, 0.f};
+            if (lane + 32 * h < a.n_split) st[h] = a.stat[static_cast<int64_t>(r) * a.n_split + lane + 32 * h];
+        }
         BeamRow row{0.f, 0.f, -INFINITY, -INFINITY, 0.f, start, isfinite(start) ? (done ? 1 : 2) : 0, len};
         if (!isfinite(start) && start != -INFINITY && lane == 0) raise_fault(a.fault, LOSSK_NON_FINITE_SCALAR);
         if (row.kind == 2) {
-            // lane i has splits i and i + 32
-            BeamStat st[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                st[h] = BeamStat{0.f, 0.f, -INFINITY, -INFINITY, 0.f};
-                if (lane + 32 * h < a.n_split) st[h] = a.stat[static_cast<int64_t>(r) * a.n_split + lane + 32 * h];
                 row.m = fmaxf(row.m, st[h].m);
                 if (st[h].ref > row.ref) {
                     row.ref = st[h].ref;
@@ -785,55 +808,55 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
             if (!(row.z > 0.f)) row.kind = 0;
         }
         if (lane == 0) s_row[k] = row;
-        const BeamCand *c = a.cand + static_cast<int64_t>(r) * a.n_split * a.n_out;
-        auto entry = [&](int i, int j) {
-            if (i >= a.n_split || j >= a.n_out) return Key(0);
-            const BeamCand x = c[i * a.n_out + j];
-            return x.tok >= 0 ? key_of(x.x, x.tok) : Key(0);
-        };
-        if (row.kind != 2) {
-            // a finished beam's candidate is itself (its logit is not used)
-            const int tok = a.end_token < 0 ? 0 : a.end_token;
-            for (int j = lane; j < a.n_out; j += 32) lists[k * a.n_out + j] = row.kind == 1 && j == 0 ? key_of(0.f, tok) : 0;
-        } else if (a.n_split == 1) {
-            for (int j = lane; j < a.n_out; j += 32) lists[k * a.n_out + j] = entry(0, j);
-        } else {
-            // the splits' lists, each in falling order, from shared memory (what lies deeper than
-            // `depth` from where it is): lane i keeps the heads of lists i and i + 32
-            const int depth = a.depth;
-            Key *mine = heads + warp * a.n_split * depth;
-            for (int i = lane; i < a.n_split * depth; i += 32) mine[i] = entry(i / depth, i % depth);
-            __syncwarp();
-            auto at = [&](int i, int j) { return i < a.n_split && j < depth ? mine[i * depth + j] : entry(i, j); };
-            int j0 = 0, j1 = 0;
-            Key q0 = at(lane, 0), q1 = at(lane + 32, 0);
-            for (int j = 0; j < a.n_out; ++j) {
-                const Key q = q1 > q0 ? q1 : q0;
-                const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(q >> 32));
-                const uint32_t lo = __reduce_max_sync(
-                    0xFFFFFFFFu, static_cast<uint32_t>(q >> 32) == hi ? static_cast<uint32_t>(q) : 0u);
-                const Key best = (static_cast<uint64_t>(hi) << 32) | lo;
-                if (lane == 0) lists[k * a.n_out + j] = best;
-                if (best && q0 == best) q0 = at(lane, ++j0);
-                else if (best && q1 == best) q1 = at(lane + 32, ++j1);
-            }
-            __syncwarp();
-        }
     }
     __syncthreads();
-    if (t < a.beams) {
-        const BeamRow row = s_row[t];
-        double lse = -INFINITY;
-        if (row.kind == 2) {
-            // the sum's base in log2 units; the logits' own scale 1 / T about their largest, c about that
-            const double base = plain(row.b) ? -static_cast<double>(row.b) : static_cast<double>(row.ref) * a.c;
-            const double m = row.m;
-            lse = m * a.inv_t + (log(static_cast<double>(row.z) + row.lost) + LN2 * (base - m * a.c));
+    if (warp == LIST_WARPS) {
+        for (int k = lane; k < a.beams; k += 32) {
+            const BeamRow row = s_row[k];
+            double lse = -INFINITY;
+            if (row.kind == 2) {
+                // the sum's base in log2 units; the logits' own scale 1 / T about their largest, c about that
+                const double base = plain(row.b) ? -static_cast<double>(row.b) : static_cast<double>(row.ref) * a.c;
+                const double m = row.m;
+                lse = m * a.inv_t + (log(static_cast<double>(row.z) + row.lost) + LN2 * (base - m * a.c));
+            }
+            s_lse[k] = lse;
+            if (a.lse_out) a.lse_out[b * a.beams + k] = static_cast<float>(lse);
         }
-        s_lse[t] = lse;
-        const double n = row.len > 1 ? row.len : 1;
-        s_inv[t] = a.length_alpha == 0.0 ? 1.0 : a.length_alpha == 1.0 ? 1.0 / n : exp(-a.length_alpha * log(n));
-        if (a.lse_out) a.lse_out[b * a.beams + t] = static_cast<float>(lse);
+    } else if (warp > LIST_WARPS) {
+        for (int k = lane; k < a.beams; k += 32) {
+            const double n = s_row[k].len > 1 ? s_row[k].len : 1;
+            s_inv[k] = a.length_alpha == 0.0 ? 1.0 : a.length_alpha == 1.0 ? 1.0 / n : exp(-a.length_alpha * log(n));
+        }
+    } else {
+        for (int k = warp; k < a.beams; k += LIST_WARPS) {
+            if (k != warp) {
+                __syncwarp();
+                fetch(k);
+            }
+            const int kind = s_row[k].kind;
+            __syncwarp();
+            if (kind != 2) {
+                // a finished beam's candidate is itself (its logit is not used)
+                const int tok = a.end_token < 0 ? 0 : a.end_token;
+                for (int j = lane; j < a.n_out; j += 32) lists[k * a.n_out + j] = kind == 1 && j == 0 ? key_of(0.f, tok) : 0;
+            } else if (a.n_split > 1) {
+                // lane i keeps the heads of lists i and i + 32
+                auto at = [&](int i, int j) { return i < a.n_split && j < depth ? mine[i * depth + j] : entry(k, i, j); };
+                int j0 = 0, j1 = 0;
+                Key q0 = at(lane, 0), q1 = at(lane + 32, 0);
+                for (int j = 0; j < a.n_out; ++j) {
+                    const Key q = q1 > q0 ? q1 : q0;
+                    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(q >> 32));
+                    const uint32_t lo = __reduce_max_sync(
+                        0xFFFFFFFFu, static_cast<uint32_t>(q >> 32) == hi ? static_cast<uint32_t>(q) : 0u);
+                    const Key best = (static_cast<uint64_t>(hi) << 32) | lo;
+                    if (lane == 0) lists[k * a.n_out + j] = best;
+                    if (best && q0 == best) q0 = at(lane, ++j0);
+                    else if (best && q1 == best) q1 = at(lane + 32, ++j1);
+                }
+            }
+        }
     }
     __syncthreads();
     auto score_of = [&](int i, int k) {
@@ -846,6 +869,8 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
         const int k = i / a.n_out;
         const double s = lists[i] ? score_of(i, k) : 0.0;
         ranks[i] = lists[i] ? order_of(a.length_alpha == 0.0 ? s : s * s_inv[k]) : 0;
+        score[i] = static_cast<float>(s);
+        place[i] = i - k * a.n_out;
         valid += lists[i] != 0;
     }
     for (int o = 16; o; o >>= 1) valid += __shfl_xor_sync(0xFFFFFFFFu, valid, o);
@@ -853,26 +878,26 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
     __syncthreads();
     // A candidate's place: equal ranks go by the lower beam, then by the order of its list (the
     // larger logit, the lower token).
-    for (int i = t; i < all; i += MERGE_NT) {
-        const uint64_t mine = ranks[i];
-        if (!mine) continue;
-        const int k = i / a.n_out;
-        int place = i - k * a.n_out;
-        for (int o = 0; o < a.beams && place < a.n_out; ++o) {
-            if (o == k) continue;
-            const uint64_t *list = ranks + o * a.n_out;
-            int lo = 0, hi = a.n_out;                  // the first entry that does not come before mine
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (list[mid] > mine || (list[mid] == mine && o < k)) lo = mid + 1;
-                else hi = mid;
-            }
-            place += lo;
+    for (int x = t; x < all * a.beams; x += MERGE_NT) {
+        const int o = x / all, i = x - o * all, k = i / a.n_out;
+        const uint64_t rank = ranks[i];
+        if (o == k || !rank || place[i] >= a.n_out) continue;   // (another thread may just be adding to it)
+        const uint64_t *list = ranks + o * a.n_out;
+        int lo = 0, hi = a.n_out;                      // the first entry that does not come before mine
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (list[mid] > rank || (list[mid] == rank && o < k)) lo = mid + 1;
+            else hi = mid;
         }
-        if (place >= a.n_out) continue;
+        if (lo) atomicAdd(&place[i], lo);
+    }
+    __syncthreads();
+    for (int i = t; i < all; i += MERGE_NT) {
+        if (!ranks[i] || place[i] >= a.n_out) continue;
+        const int k = i / a.n_out;
         const bool was = s_row[k].kind == 1;
-        put_out(a, b, place, k, was ? a.end_token : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(lists[i])),
-                score_of(i, k), was, s_row[k].len);
+        put_out(a, b, place[i], k, was ? a.end_token : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(lists[i])),
+                score[i], was, s_row[k].len);
     }
     valid = 0;
     for (int i = 0; i < MERGE_WARPS; ++i) valid += s_valid[i];
@@ -957,10 +982,11 @@ cudaError_t launch_beam_rows(const BeamArgs &a, cudaStream_t st)
 cudaError_t launch_beam_merge(const BeamArgs &a0, cudaStream_t st)
 {
     BeamArgs a = a0;
-    const int all = a.beams * a.n_out;
+    const size_t all = static_cast<size_t>(a.beams) * a.n_out;
     // at most 512 entries of a beam's splits in shared memory
     a.depth = a.n_split == 1 ? 0 : a.n_out < 512 / a.n_split ? a.n_out : 512 / a.n_split;
-    const size_t bytes = sizeof(Key) * (2 * static_cast<size_t>(all) + MERGE_WARPS * static_cast<size_t>(a.n_split) * a.depth);
+    const size_t heads = LIST_WARPS * static_cast<size_t>(a.n_split) * a.depth;
+    const size_t bytes = sizeof(Key) * (2 * all + (heads > all ? heads : all));
     const cudaError_t e = raise_smem<beam_merge_kernel>(bytes);
     if (e != cudaSuccess) return e;
     return launch_after(true, beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(MERGE_NT), bytes, st, a);
