@@ -106,6 +106,7 @@ __device__ __forceinline__ int keep_best(Key *buf, Key *tmp, int cnt, int n, Key
     for (int i = t; i < left; i += NT) {
         const Key k = tmp[i];
         int above = 0;
+#pragma unroll 4
         for (int j = 0; j < left; ++j) above += tmp[j] > k;
         if (above < n) buf[above] = k;
     }
@@ -213,6 +214,30 @@ __device__ __forceinline__ void add_z(float &z, float &lost, float x, float rest
 __device__ __forceinline__ bool far_above(const RowStat &r, float lm, float c)
 {
     return !((lm - r.ref) * c < FAR);          // (a NaN is, too)
+}
+
+// Two floats in one register pair.
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t p, float &x, float &y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
 }
 
 // A vector of -infinity.
@@ -392,10 +417,18 @@ __device__ __noinline__ int best_by_steps(const BeamArgs &a, const Item<T> &it, 
 // threshold, its lists) cost no memory time.  In a chunk a thread has U
 // vectors; the working warps meet at a barrier only for thresholds.  The first
 // chunk's threshold stays for the item while n <= STEADY (of random logits
-// every chunk then brings n keys, at most 19 chunks; cutting the buffer cost
-// 17 us of 127 at 896 rows of 151936 with n = 16); for larger n the buffer is
-// cut to its n best after the 2nd, 4th, 8th ... chunk.  Keys that do not fit
-// the buffer are dropped, and the item's best are found by best_by_steps.
+// every chunk then brings n keys, at most 19 chunks; raising it as keys come in
+// cost 17 us of 127 at 896 rows of 151936 with n = 16 where the block cut its
+// buffer, and 3 of 65 where one warp did while the others went on); for larger
+// n the buffer is cut to its n best after the 2nd, 4th, 8th ... chunk.  Keys that
+// do not fit the buffer are dropped, and the item's best are found by
+// best_by_steps.
+//
+// Measured at 1024 rows of 151936 bf16, 896 of them alive (272 MB), n = 16: 59 us
+// = 4.6 TB/s, where the loads alone take 45.  The rest is what ring and blocks do
+// not hide: the first chunk's threshold 2 us, keys past it 4, exponentials 4 (two
+// floats an instruction; 5 with one), an item's end 5 (each of 456 blocks has two
+// items, all end at much the same time).
 template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) beam_rows_kernel(BeamArgs a)
 {
     constexpr int NV = Elem<T>::NV;
@@ -512,22 +545,33 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) b
                 st.m = max_nan(st.m, top);
                 if (far_above(st, top, c)) rebase(st, top, c);
                 float sum = 0.f;
+                // (two floats an instruction)
                 const auto add = [&](auto term) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         float f[NV];
                         unpack<T>(cur[u], f);
+                        uint64_t p[NV / 2];
 #pragma unroll
-                        for (int e = 0; e < NV; ++e) f[e] = term(f[e]);
+                        for (int e = 0; e < NV / 2; ++e) p[e] = term(f[2 * e], f[2 * e + 1]);
 #pragma unroll
-                        for (int h = NV / 2; h; h >>= 1)
+                        for (int h = NV / 4; h; h >>= 1)
 #pragma unroll
-                            for (int e = 0; e < h; ++e) f[e] += f[e + h];
-                        sum += f[0];
+                            for (int e = 0; e < h; ++e) p[e] = add2(p[e], p[e + h]);
+                        float x, y;
+                        unpack2(p[0], x, y);
+                        sum += x + y;
                     }
                 };
-                if (plain(st.b)) add([&](float x) { return ex2_approx(fmaf(x, c, st.b)); });
-                else add([&](float x) { return x == st.ref ? 1.f : 0.f; });
+                if (plain(st.b)) {
+                    const uint64_t c2 = pack2(c, c), b2 = pack2(st.b, st.b);
+                    add([&](float x, float y) {
+                        unpack2(fma2(pack2(x, y), c2, b2), x, y);
+                        return pack2(ex2_approx(x), ex2_approx(y));
+                    });
+                } else {
+                    add([&](float x, float y) { return pack2(x == st.ref ? 1.f : 0.f, y == st.ref ? 1.f : 0.f); });
+                }
                 add_z(st.z, st.lost, sum, 0.f);
             }
             const auto token = [&](int x) { return it.v0 + (base + (x / NV) * NT + t) * NV + x % NV; };   // of value x
@@ -597,17 +641,8 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) b
                 }
             }
         }
-        block_sync();
-        int cnt = s_cnt;
-        if (s_over) cnt = best_by_steps<T, MASK>(a, it, buf, tmp, s_keys, &s_nth, &s_cnt, &s_kept);
-        const int kept = keep_best(buf, tmp, cnt, a.n_out, s_keys, &s_nth, &s_kept);
-        for (int i = t; i < a.n_out; i += NT)
-            a.cand[static_cast<int64_t>(item) * a.n_out + i] =
-                i < kept ? BeamCand{value_of(static_cast<uint32_t>(buf[i] >> 32)),
-                                    static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[i]))}
-                         : BeamCand{0.f, -1};
-        // the split's sum: every thread's brought to the highest base, then added up in two floats
-        // (a double addition runs at a sixty-fourth of a float's rate)
+        // the split's highest base, its keys cut to the best, its sum: every thread's sum is brought to that
+        // base and added up in two floats (a double addition runs at a sixty-fourth of a float's rate)
         float m = st.m, ref = st.ref, bb = st.b;
         auto higher = [&](float x, float y) {
             if (x > ref) {
@@ -621,6 +656,9 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) b
         }
         if (lane == 0) s_part[t >> 5] = make_float4(m, ref, bb, 0.f);
         block_sync();
+        int cnt = s_cnt;
+        if (s_over) cnt = best_by_steps<T, MASK>(a, it, buf, tmp, s_keys, &s_nth, &s_cnt, &s_kept);
+#pragma unroll
         for (int i = 0; i < WARPS; ++i) {
             const float4 x = s_part[i];
             m = max_nan(m, x.x);
@@ -637,9 +675,15 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) b
             add_z(z, lost, x, y);
         }
         if (lane == 0) s_z[t >> 5] = make_float2(z, lost);
-        block_sync();
-        if (t == 0) {
-            for (int i = 1; i < WARPS; ++i) add_z(z, lost, s_z[i].x, s_z[i].y);
+        const int kept = keep_best(buf, tmp, cnt, a.n_out, s_keys, &s_nth, &s_kept);
+        for (int i = t; i < a.n_out; i += NT)
+            a.cand[static_cast<int64_t>(item) * a.n_out + i] =
+                i < kept ? BeamCand{value_of(static_cast<uint32_t>(buf[i] >> 32)),
+                                    static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(buf[i]))}
+                         : BeamCand{0.f, -1};
+        if (t == NT - 32) {
+            z = lost = 0.f;
+            for (int i = 0; i < WARPS; ++i) add_z(z, lost, s_z[i].x, s_z[i].y);
             a.stat[item] = BeamStat{m < INFINITY ? z : NAN, lost, m, ref, bb};
         }
     }
