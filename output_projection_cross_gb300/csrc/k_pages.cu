@@ -14,6 +14,15 @@
 // found by scanning the counts (4 bytes a page, read once), which keeps no
 // list that could disagree with the counts and makes every allocation a
 // function of the inputs alone.
+//
+// Copies and moves are bound by HBM (compaction of 8192 pages, 515 MB read and
+// written: 87 us in all; cache_move alone 77 us = 6.7 TB/s), everything else by
+// the latency of its few dependent loads and scans: a fork or a write 2 to 5 us,
+// the plan of a reservation 6 us for 4 sequences and 160 pages, 10 us for 512
+// sequences and 13312 pages.  Plan and copies are two launches: one launch whose
+// blocks wait for the first one's plan made that decoding step (fork,
+// reservation and writes for 512 sequences) 38 us instead of 30, a compaction of
+// 331 pages 15 instead of 8.
 #include "../../include/lossk.h"
 #include "decode_internal.h"
 #include "decode_launch.h"
@@ -264,7 +273,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) cache_plan_kernel(ReserveArgs a)
 
 // ---- copying pages ----------------------------------------------------------------
 // moves[i] = (from, to), n of them (*n_dev where the count is the device's).  A
-// block takes pieces of a page; a piece is 256 threads x 4 loads of 16 bytes.
+// block takes pieces of a page; a piece is 256 threads x 4 loads of 16 bytes
+// (four blocks of it in flight on an SM are the 64 KB that HBM's latency asks for).
 constexpr int COPY_THREADS = 256;
 constexpr int COPY_U = 4;
 
