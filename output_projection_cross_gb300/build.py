@@ -3,6 +3,8 @@
 Each CUDA translation unit is compiled by its own nvcc process (in parallel),
 then linked into ``output_projection_cross_gb300/_build/liblossk.so``.  The
 CUDA runtime is linked statically, so the library needs only the driver.
+Beside it stands ``_lossk_calls.so``, the CPython module through which the
+decoding calls are made.
 """
 from __future__ import annotations
 
@@ -11,15 +13,18 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "liblossk.so")
+CALLS = os.path.join(BUILD, "_lossk_calls.so")
 SOURCES = ["lossk_abi.cu", "k_fwd2.cu", "k_bwp.cu", "k_simt.cu", "lossk_static.cu", "lossk_decode.cu", "k_beam.cu", "k_pages.cu",
            "k_attn.cu", "k_attn_mma.cu", "k_attn_ffma.cu"]
 HEADERS = ["ptx.cuh", "lossk_internal.h", "decode_internal.h", "decode_launch.h", "attn_split.cuh"]
+CALLS_SOURCE = "lossk_calls.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -31,10 +36,10 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [CALLS_SOURCE]]
     deps.append(os.path.join(ROOT, "include", "lossk.h"))
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(p) > t for p in deps)
@@ -61,7 +66,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    def compile_calls():
+        cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+        tmp = CALLS + f".tmp{os.getpid()}"
+        cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"),
+               "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, CALLS_SOURCE), "-o", tmp, "-ldl"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cxx} failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+        return tmp
+
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs
@@ -69,6 +85,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(calls.result(), CALLS)
     return LIB
 
 

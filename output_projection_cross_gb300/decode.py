@@ -10,10 +10,29 @@ in; both are created here when left out.
 """
 from __future__ import annotations
 
+import importlib.util
+import os
+
 import torch
 
+from . import build as _build
 from .lossk import LosskError, _check, _dtype_code, _len, _ptr, _stream, lib
 
+
+def _load_calls():
+    """The module through which the calls are made (ctypes takes 2 us for the arguments of one)."""
+    path = _build.CALLS
+    if not os.path.exists(path):
+        raise ImportError(f"{os.path.basename(path)} is not built ({path}); run `python "
+                          f"output_projection_cross_gb300/build.py`")
+    spec = importlib.util.spec_from_file_location("_lossk_calls", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.load(_build.LIB)
+    return m
+
+
+_calls = _load_calls()
 KIND_BEAM_SELECT, KIND_CACHE, KIND_PAGED_ATTN = 0, 1, 2
 
 __all__ = ["KIND_BEAM_SELECT", "KIND_CACHE", "KIND_PAGED_ATTN", "decode_workspace", "beam_buffers",
@@ -129,7 +148,7 @@ def lossk_beam_select(logits, scores, n_out, temperature=1.0, allow=None, finish
         raise ValueError("lse_out must hold one value per row of logits")
     if ws is None:
         ws = decode_workspace(KIND_BEAM_SELECT, batch, beams, V, n_out, logits.device)
-    st = lib.lossk_beam_select(batch, beams, V, n_out, _dtype_code(logits), logits.data_ptr(), _span(logits),
+    st = _calls.lossk_beam_select(batch, beams, V, n_out, _dtype_code(logits), logits.data_ptr(), _span(logits),
                                logits.stride(0) if rows > 1 else max(V, 1), scores.data_ptr(), rows, temperature,
                                _ptr(allow), _len(allow), allow_stride, _ptr(finished), end_token, _ptr(lengths),
                                length_alpha, parent.data_ptr(), token.data_ptr(), score.data_ptr(), done.data_ptr(),
@@ -152,7 +171,7 @@ def lossk_beam_gather(src, parent, dst=None, ws=None, stream=None):
     row = src.numel() * src.element_size() // max(G * n_src, 1)
     if ws is None:
         ws = torch.zeros(256, dtype=torch.uint8, device=src.device)
-    st = lib.lossk_beam_gather(G, n_src, n_dst, row, parent.data_ptr(), parent.numel(), src.data_ptr(),
+    st = _calls.lossk_beam_gather(G, n_src, n_dst, row, parent.data_ptr(), parent.numel(), src.data_ptr(),
                                src.numel() * src.element_size(), dst.data_ptr(), dst.numel() * dst.element_size(),
                                ws.data_ptr(), ws.numel(), _stream_of(src, stream))
     _check(st, "lossk_beam_gather")
@@ -209,7 +228,7 @@ def lossk_cache_fork(parent, table, lens, ref, page_size, table_out=None, lens_o
         raise ValueError("table_out must be [groups * n_dst, max_pages]")
     if ws is None:
         ws = decode_workspace(KIND_CACHE, max(n, no), pages, device=table.device)
-    st = lib.lossk_cache_fork(G, n // G, n_dst, m, page_size, pages, parent.data_ptr(), parent.numel(),
+    st = _calls.lossk_cache_fork(G, n // G, n_dst, m, page_size, pages, parent.data_ptr(), parent.numel(),
                               table.data_ptr(), table_len, stride, lens.data_ptr(), n, ref.data_ptr(), pages,
                               table_out.data_ptr(), out_len, stride_out, lens_out.data_ptr(), lens_out.numel(),
                               ws.data_ptr(), ws.numel(), _stream_of(table, stream))
@@ -228,7 +247,7 @@ def lossk_cache_reserve(table, lens, ref, pool, page_size, n_new=1, ws=None, str
     P = _pool(pool, pages)
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
-    st = lib.lossk_cache_reserve(n, m, page_size, pages, 0 if each is not None else n_new, _ptr(each),
+    st = _calls.lossk_cache_reserve(n, m, page_size, pages, 0 if each is not None else n_new, _ptr(each),
                                  _len(each), table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(),
                                  ref.data_ptr(), pages, *P, ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_reserve")
@@ -242,7 +261,7 @@ def lossk_cache_free(table, lens, ref, page_size, drop=None, ws=None, stream=Non
     n, m, stride, table_len = _table(table)
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, ref.numel(), device=table.device)
-    st = lib.lossk_cache_free(n, m, page_size, ref.numel(), _ptr(drop), _len(drop), table.data_ptr(), table_len,
+    st = _calls.lossk_cache_free(n, m, page_size, ref.numel(), _ptr(drop), _len(drop), table.data_ptr(), table_len,
                               stride, lens.data_ptr(), lens.numel(), ref.data_ptr(), ref.numel(), ws.data_ptr(),
                               ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_free")
@@ -266,7 +285,7 @@ def lossk_cache_compact(table, lens, ref, pool, page_size, table_out=None, ref_o
         raise ValueError("table_out must be shaped like table, n_live_out hold one value")
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
-    st = lib.lossk_cache_compact(n, m, page_size, pages, table.data_ptr(), table_len, stride, lens.data_ptr(),
+    st = _calls.lossk_cache_compact(n, m, page_size, pages, table.data_ptr(), table_len, stride, lens.data_ptr(),
                                  lens.numel(), ref.data_ptr(), pages, table_out.data_ptr(), out_len, stride_out,
                                  ref_out.data_ptr(), ref_out.numel(), n_live_out.data_ptr(), *P, ws.data_ptr(),
                                  ws.numel(), _stream_of(table, stream))
@@ -282,7 +301,7 @@ def lossk_cache_copy(src, dst, pool, ws=None, stream=None) -> None:
     if src.numel() != dst.numel():
         raise ValueError("src and dst must list as many pages")
     ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=pool.device)
-    st = lib.lossk_cache_copy(src.numel(), pool.shape[1], src.data_ptr(), src.numel(), dst.data_ptr(), dst.numel(),
+    st = _calls.lossk_cache_copy(src.numel(), pool.shape[1], src.data_ptr(), src.numel(), dst.data_ptr(), dst.numel(),
                               *P, ws.data_ptr(), ws.numel(), _stream_of(pool, stream))
     _check(st, "lossk_cache_copy")
 
@@ -315,7 +334,7 @@ def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, w
         raise ValueError("k_new and v_new must be laid out alike")
     n_tok = shape[0]
     ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=table.device)
-    st = lib.lossk_cache_write(n_tok, n, kv, hd, m, page, n_pages, _dtype_code(k_pages), k_new.data_ptr(),
+    st = _calls.lossk_cache_write(n_tok, n, kv, hd, m, page, n_pages, _dtype_code(k_pages), k_new.data_ptr(),
                                v_new.data_ptr(), _span(k_new), strides[0] if n_tok > 1 else kv * hd,
                                k_pages.data_ptr(), v_pages.data_ptr(), pages_len, sp, stok, sh,
                                table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(), _ptr(first),
@@ -346,7 +365,7 @@ def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, sha
         raise ValueError("lse_out must be [n_seq, n_q_heads]")
     if ws is None:
         ws = decode_workspace(KIND_PAGED_ATTN, n, hq, kv, hd, q.device)
-    st = lib.lossk_paged_attn(n, hq, kv, hd, m, page, n_pages, share, _dtype_code(q), q.data_ptr(), _span(q),
+    st = _calls.lossk_paged_attn(n, hq, kv, hd, m, page, n_pages, share, _dtype_code(q), q.data_ptr(), _span(q),
                               strides[0] if n > 1 else hq * hd, k_pages.data_ptr(), v_pages.data_ptr(), pages_len,
                               sp, stok, sh, table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(),
                               max_len, window, hd ** -0.5 if scale is None else scale, out.data_ptr(), out.numel(),
