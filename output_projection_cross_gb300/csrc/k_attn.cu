@@ -34,12 +34,15 @@ namespace lossk {
 namespace {
 
 constexpr int PLAN_T = 256;
+constexpr int SHARE_T = 512, SHARE_U = 4;
 constexpr int JOIN_FEW = 3, JOIN_MANY = 16;
 
 // Shared tokens of each group: the leading pages whose ids agree in all its
 // rows, full in all of them.  With a window the rows have to be equally long,
 // for the first token read depends on the length.
-__global__ void __launch_bounds__(PLAN_T) attn_share_kernel(AttnArgs a)
+// A thread looks at SHARE_U columns at a time (one: 16 us instead of SHAREUS for
+// one group of 4 beams of 3750 pages).
+__global__ void __launch_bounds__(SHARE_T) attn_share_kernel(AttnArgs a)
 {
     __shared__ int s_first, s_min, s_max;
     const int g = blockIdx.x, t = threadIdx.x;
@@ -62,15 +65,28 @@ __global__ void __launch_bounds__(PLAN_T) attn_share_kernel(AttnArgs a)
         return;
     }
     const int32_t *row0 = a.table + static_cast<int64_t>(g) * a.share * a.table_stride;
-    for (int base = 0; base < full; base += PLAN_T) {
-        const int c = base + t;
-        bool differ = false;
-        if (c < full)
-            for (int i = 1; i < a.share; ++i) differ |= row0[i * a.table_stride + c] != row0[c];
-        if (differ) atomicMin(&s_first, c);
+    for (int base = 0; base < full; base += SHARE_T * SHARE_U) {
+        int32_t v[SHARE_U];
+        bool differ[SHARE_U];
+#pragma unroll
+        for (int u = 0; u < SHARE_U; ++u) {
+            const int c = base + u * SHARE_T + t;
+            v[u] = c < full ? row0[c] : 0;
+            differ[u] = false;
+        }
+#pragma unroll 4
+        for (int i = 1; i < a.share; ++i)
+#pragma unroll
+            for (int u = 0; u < SHARE_U; ++u) {
+                const int c = base + u * SHARE_T + t;
+                if (c < full) differ[u] |= row0[i * a.table_stride + c] != v[u];
+            }
+#pragma unroll
+        for (int u = 0; u < SHARE_U; ++u)
+            if (differ[u]) atomicMin(&s_first, base + u * SHARE_T + t);
         __syncthreads();
-        if (s_first < base + PLAN_T) break;
-        __syncthreads();
+        // (what others find meanwhile lies beyond these columns)
+        if (s_first < base + SHARE_T * SHARE_U) break;
     }
     __syncthreads();
     if (t == 0) a.shared[g] = (s_first < full ? s_first : full) * a.page;
@@ -121,14 +137,15 @@ __device__ __forceinline__ RowPieces row_pieces(const AttnArgs &a, int s, int hq
 template <typename T, int H, int WPR>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : WPR * 32) attn_join_kernel(AttnArgs a)
 {
-    constexpr int B = 8 / H;
+    constexpr int B = (WPR == 1 ? 4 : 8) / H;              // (a row of one warp has few pieces)
     __shared__ float4 s_o[WPR > 1 ? WPR : 1][32 * H];
     __shared__ float2 s_ml[WPR > 1 ? WPR : 1];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, k0 = WPR == 1 ? 0 : warp;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = WPR == 1 ? static_cast<int64_t>(blockIdx.x) * 8 + warp : blockIdx.x;
-    if (row >= static_cast<int64_t>(a.n_group) * a.share * a.n_q) return;
-    const RowPieces p = row_pieces(a, static_cast<int>(row / a.n_q), static_cast<int>(row % a.n_q));
+    // (there are fewer than 2^31 rows)
+    const unsigned row = WPR == 1 ? blockIdx.x * 8 + warp : blockIdx.x, n_q = a.n_q;
+    if (row >= static_cast<unsigned>(a.n_group) * a.share * n_q) return;
+    const RowPieces p = row_pieces(a, static_cast<int>(row / n_q), static_cast<int>(row % n_q));
     if (p.n < 0) return;
     const int words = a.hd >> 2;
     float M = -INFINITY, mz = 0.f, l = 0.f;
@@ -172,7 +189,7 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : WPR * 32) attn_join_kernel(At
                     }
             }
     }
-    T *out = static_cast<T *>(a.out) + row * a.hd;
+    T *out = static_cast<T *>(a.out) + static_cast<int64_t>(row) * a.hd;
     if constexpr (WPR == 1) {
         const float inv = l > 0.f ? 1.f / l : 1.f;
 #pragma unroll
@@ -239,7 +256,7 @@ bool attn_plans(const AttnArgs &a) { return a.share > 1 || a.n_group > BASE_GROU
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st)
 {
     if (a.share > 1) {
-        attn_share_kernel<<<static_cast<unsigned>(a.n_group), PLAN_T, 0, st>>>(a);
+        attn_share_kernel<<<static_cast<unsigned>(a.n_group), SHARE_T, 0, st>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || a.n_group <= BASE_GROUPS) return e;
     }

@@ -66,15 +66,16 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
     walk_run(a, base, w, [&](const Piece &p) {
         const int n_tiles = (p.t1 - p.t0 + KT - 1) / KT;
         TileStream<V> in(a, p, 0, lane, smem_u32(mine), valid);
-        in.start(n_tiles);
+        // the query rows, zeros past the last one, come with the first tile
+#pragma unroll 4
         for (int i = lane; i < R * (HDP / 4); i += 32) {
             const int r = i / (HDP / 4), e = i % (HDP / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < p.rows && e < a.hd)
-                x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + row_seq(a, p, r) * a.q_stride +
-                                                           static_cast<int64_t>(row_head(a, p, r)) * a.hd + e));
-            *reinterpret_cast<float4 *>(qs + r * HDP + e) = x;
+            const bool in_row = r < p.rows && e < a.hd;
+            const float *from = static_cast<const float *>(a.q);
+            if (in_row) from += row_seq(a, p, r) * a.q_stride + static_cast<int64_t>(row_head(a, p, r)) * a.hd + e;
+            cp16_or_zero(smem_u32(qs + r * HDP + e), from, in_row ? 16 : 0);
         }
+        in.start(n_tiles);
         float4 o[R][C];
         float m[R], l[R];
 #pragma unroll

@@ -123,21 +123,20 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
         const bool active = mine0 < p.rows;
         const int n_tiles = (p.t1 - p.t0 + KT - 1) / KT;
         TileStream<V> in(a, p, sub, lane, ring, valid);
-        in.start(n_tiles);
-        // the query rows, zeros past the last one
-        uint32_t qf[V::QREG ? KS : 1][4];
+        // the query rows, zeros past the last one, come with the first tile
+#pragma unroll 4
         for (int i = lane; i < 16 * (HDP / 8); i += 32) {
             const int rr = i / (HDP / 8), cc = i % (HDP / 8);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (mine0 + rr < p.rows && cc < ch)
-                x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
-                                                          row_seq(a, p, mine0 + rr) * a.q_stride +
-                                                          static_cast<int64_t>(row_head(a, p, mine0 + rr)) * a.hd) + cc);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qs + rr * RS + cc * 16), "r"(x.x), "r"(x.y),
-                         "r"(x.z), "r"(x.w)
-                         : "memory");
+            const bool in_row = mine0 + rr < p.rows && cc < ch;
+            const uint16_t *from = static_cast<const uint16_t *>(a.q);
+            if (in_row)
+                from += row_seq(a, p, mine0 + rr) * a.q_stride + static_cast<int64_t>(row_head(a, p, mine0 + rr)) * a.hd + cc * 8;
+            cp16_or_zero(qs + rr * RS + cc * 16, from, in_row ? 16 : 0);
         }
+        in.start(n_tiles);
+        cp_wait<STAGES - 2>();
         __syncwarp();
+        uint32_t qf[V::QREG ? KS : 1][4];
         if constexpr (V::QREG) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) ldsm4(qf[ks], qs + v_off + ks * 32);
