@@ -50,8 +50,9 @@ __device__ __forceinline__ int tiles_of(int n, int kt) { return (n + kt - 1) / k
 // Starting an item (its query rows, its first tile's latency, its result) takes
 // a warp about as long as ITEM_COST tiles; counting it so keeps runs of many
 // short items from lagging behind.  An item's units are ITEM_COST for its
-// start, then one per tile.
-constexpr int ITEM_COST = 6;
+// start, then one per tile.  (Counted as 2, 3, 4 and 6: 55, 50, 51 and 51 us for
+// 8 x 8 beams on 4096 shared tokens, 137, 133, 134 and 140 for 64 x 8 of 1501.)
+constexpr int ITEM_COST = 3;
 __device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + ITEM_COST : 0; }
 
 // Units of a group's shared part, per item.

@@ -34,15 +34,15 @@ namespace lossk {
 namespace {
 
 constexpr int PLAN_T = 256;
-constexpr int SHARE_T = 512, SHARE_U = 4;
+constexpr int SHARE_U = 4;
 constexpr int JOIN_FEW = 3, JOIN_MANY = 16;
 
 // Shared tokens of each group: the leading pages whose ids agree in all its
 // rows, full in all of them.  With a window the rows have to be equally long,
 // for the first token read depends on the length.
-// A thread looks at SHARE_U columns at a time (one: 16 us instead of SHAREUS for
-// one group of 4 beams of 3750 pages).
-__global__ void __launch_bounds__(SHARE_T) attn_share_kernel(AttnArgs a)
+// A thread looks at SHARE_U columns at a time (one, in blocks of 256: 16 us
+// instead of 5 for one group of 4 beams of 3750 pages).
+template <int T> __global__ void __launch_bounds__(T) attn_share_kernel(AttnArgs a)
 {
     __shared__ int s_first, s_min, s_max;
     const int g = blockIdx.x, t = threadIdx.x;
@@ -65,12 +65,12 @@ __global__ void __launch_bounds__(SHARE_T) attn_share_kernel(AttnArgs a)
         return;
     }
     const int32_t *row0 = a.table + static_cast<int64_t>(g) * a.share * a.table_stride;
-    for (int base = 0; base < full; base += SHARE_T * SHARE_U) {
+    for (int base = 0; base < full; base += T * SHARE_U) {
         int32_t v[SHARE_U];
         bool differ[SHARE_U];
 #pragma unroll
         for (int u = 0; u < SHARE_U; ++u) {
-            const int c = base + u * SHARE_T + t;
+            const int c = base + u * T + t;
             v[u] = c < full ? row0[c] : 0;
             differ[u] = false;
         }
@@ -78,15 +78,15 @@ __global__ void __launch_bounds__(SHARE_T) attn_share_kernel(AttnArgs a)
         for (int i = 1; i < a.share; ++i)
 #pragma unroll
             for (int u = 0; u < SHARE_U; ++u) {
-                const int c = base + u * SHARE_T + t;
+                const int c = base + u * T + t;
                 if (c < full) differ[u] |= row0[i * a.table_stride + c] != v[u];
             }
 #pragma unroll
         for (int u = 0; u < SHARE_U; ++u)
-            if (differ[u]) atomicMin(&s_first, base + u * SHARE_T + t);
+            if (differ[u]) atomicMin(&s_first, base + u * T + t);
         __syncthreads();
         // (what others find meanwhile lies beyond these columns)
-        if (s_first < base + SHARE_T * SHARE_U) break;
+        if (s_first < base + T * SHARE_U) break;
     }
     __syncthreads();
     if (t == 0) a.shared[g] = (s_first < full ? s_first : full) * a.page;
@@ -256,7 +256,11 @@ bool attn_plans(const AttnArgs &a) { return a.share > 1 || a.n_group > BASE_GROU
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st)
 {
     if (a.share > 1) {
-        attn_share_kernel<<<static_cast<unsigned>(a.n_group), SHARE_T, 0, st>>>(a);
+        // the more threads the fewer rounds over a long table, and the later a short one is done: 4 beams of
+        // 3750 pages took 8 us with 256 threads and 4 with 1024, 8 x 8 of 136 pages 4 and 5
+        const unsigned groups = static_cast<unsigned>(a.n_group);
+        if (a.max_pages <= 256 * SHARE_U) attn_share_kernel<256><<<groups, 256, 0, st>>>(a);
+        else attn_share_kernel<1024><<<groups, 1024, 0, st>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || a.n_group <= BASE_GROUPS) return e;
     }

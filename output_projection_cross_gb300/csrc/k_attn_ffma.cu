@@ -16,8 +16,8 @@
 // sequences of 20 to 500 tokens with 8 KV heads of 128 and 32 query heads,
 // 301 -> 238 us for 4 of 20000 with 128 query heads.
 //
-// Measured at 4 sequences of 20000 tokens, 8 KV heads of 128 (655 MB): 117 us =
-// 5.6 TB/s for 8 query heads, 121 for 32, 146 for 64.  Up to 4 rows to a KV head
+// Measured at 4 sequences of 20000 tokens, 8 KV heads of 128 (655 MB): 111 us =
+// 5.9 TB/s for 8 query heads, 114 for 32, 139 for 64.  Up to 4 rows to a KV head
 // the stream bounds it, beyond that the multiply-adds and their reads of q and
 // of the weights.
 #include "attn_split.cuh"

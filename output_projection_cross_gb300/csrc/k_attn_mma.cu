@@ -23,10 +23,11 @@
 //
 // Measured, split pass and join: one sequence of 131072 tokens (8 KV heads of
 // 128, bf16, 537 MB) 96 us, the pass alone 92 us = 5.8 TB/s; 33 sequences of 1 to
-// 9000 tokens (160 MB) 37 us; 8 x 8 beams on 4096 shared tokens (170 MB) 52 us.  What bounds it: the stream at 6.2 TB/s at the margin, and about 9 us
-// before the first tile and after the last.  With the loads alone the three
-// take 92, 36 and 43 us, with the products alone 35, 20 and 38.  Two or four
-// stages are within 2 % of three.
+// 9000 tokens (160 MB) 37 us; 8 x 8 beams on 4096 shared tokens (170 MB) 50 us.
+// What bounds it: the stream at 6.2 TB/s at the margin, and about 9 us before
+// the first tile and after the last; with many short items also their products
+// (8 x 8 beams: 37 us without the products, 32 without the loads, 42 with both).
+// Two or four stages are within 2 % of three.
 #include "attn_split.cuh"
 
 namespace lossk {
@@ -123,7 +124,8 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
         const bool active = mine0 < p.rows;
         const int n_tiles = (p.t1 - p.t0 + KT - 1) / KT;
         TileStream<V> in(a, p, sub, lane, ring, valid);
-        // the query rows, zeros past the last one, come with the first tile
+        // the query rows, zeros past the last one, come with the first tile (loaded and stored one after the
+        // other: 132 instead of 105 us for 200 groups of 4 sequences of 120 to 320 tokens)
 #pragma unroll 4
         for (int i = lane; i < 16 * (HDP / 8); i += 32) {
             const int rr = i / (HDP / 8), cc = i % (HDP / 8);
