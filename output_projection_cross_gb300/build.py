@@ -23,7 +23,7 @@ LIB = os.path.join(BUILD, "liblossk.so")
 CALLS = os.path.join(BUILD, "_lossk_calls.so")
 SOURCES = ["lossk_abi.cu", "k_fwd2.cu", "k_bwp.cu", "k_simt.cu", "lossk_static.cu", "lossk_decode.cu", "k_beam.cu", "k_pages.cu",
            "k_attn.cu", "k_attn_mma.cu", "k_attn_ffma.cu"]
-HEADERS = ["ptx.cuh", "lossk_internal.h", "decode_internal.h", "decode_launch.h", "attn_split.cuh"]
+HEADERS = ["ptx.cuh", "lossk_internal.h", "decode_internal.h", "decode_launch.h", "attn_split.cuh", "float2.cuh"]
 CALLS_SOURCE = "lossk_calls.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

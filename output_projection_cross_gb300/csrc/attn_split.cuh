@@ -300,11 +300,12 @@ template <typename V> struct TileStream {
     // lane < KT: this lane's token of the tile to be looked up next, its page's column and its
     // place in the page; the page itself is loaded a tile before it is needed
     int t, col, off, pg, place;
+    const int step_col, step_off;       // a tile is that many pages and tokens long
 
     __device__ __forceinline__ TileStream(const AttnArgs &a_, const Piece &p_, int sub, int lane_, uint32_t ring_,
                                           uint32_t *valid_)
         : a(a_), p(p_), lane(lane_), c(lane_ % V::LPR), first(sub * MINE * STEP + lane_ / V::LPR),
-          words(a_.hd * V::ESIZE / 16), ring(ring_), valid(valid_)
+          words(a_.hd * V::ESIZE / 16), ring(ring_), valid(valid_), step_col(KT / a_.page), step_off(KT % a_.page)
     {
         row = a.table + p.seq * a.table_stride;
         kb = static_cast<const char *>(a.k) + p.head * a.head_stride * V::ESIZE + c * 16;
@@ -320,8 +321,9 @@ template <typename V> struct TileStream {
         pg = in ? row[col] : -2;
         place = off;
         t += KT;
-        off += KT;
-        while (off >= a.page) {
+        off += step_off;
+        col += step_col;
+        if (off >= a.page) {
             off -= a.page;
             ++col;
         }

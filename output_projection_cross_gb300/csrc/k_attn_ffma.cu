@@ -14,13 +14,15 @@
 // warps as fit (12 where R rows leave them registers, 8 for R = 16).  Against
 // three stages of 16 tokens (4 warps for heads of 128): 34 -> 28 us for 64
 // sequences of 20 to 500 tokens with 8 KV heads of 128 and 32 query heads,
-// 301 -> 238 us for 4 of 20000 with 128 query heads.
+// 301 -> 238 us for 4 of 20000 with 128 query heads.  Products and sums go two
+// floats an instruction (219 instead of 237 us at 128 query heads).
 //
 // Measured at 4 sequences of 20000 tokens, 8 KV heads of 128 (655 MB): 111 us =
-// 5.9 TB/s for 8 query heads, 114 for 32, 139 for 64.  Up to 4 rows to a KV head
+// 5.9 TB/s for 8 query heads, 114 for 32, 135 for 64.  Up to 4 rows to a KV head
 // the stream bounds it, beyond that the multiply-adds and their reads of q and
 // of the weights.
 #include "attn_split.cuh"
+#include "float2.cuh"
 
 namespace lossk {
 
@@ -76,14 +78,14 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
             cp16_or_zero(smem_u32(qs + r * HDP + e), from, in_row ? 16 : 0);
         }
         in.start(n_tiles);
-        float4 o[R][C];
+        ulonglong2 o[R][C];                                // four columns, in pairs
         float m[R], l[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
 #pragma unroll
-            for (int x = 0; x < C; ++x) o[r][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int x = 0; x < C; ++x) o[r][x] = make_ulonglong2(0, 0);
         }
         for (int i = 0; i < n_tiles; ++i) {
             cp_wait<STAGES - 2>();
@@ -91,22 +93,28 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
             in.next(i, n_tiles);
             const int st = i % STAGES;
             const unsigned char *kt = mine + st * 2 * V::TILE, *vt = kt + V::TILE;
-            float s[R];
+            // (two products an instruction)
+            uint64_t s2[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) s[r] = 0.f;
+            for (int r = 0; r < R; ++r) s2[r] = 0;
             const float *kr = reinterpret_cast<const float *>(kt + tok * V::RS);
 #pragma unroll 2
             for (int e = 0; e < steps; ++e) {
                 const int at = (e * PARTS + part) * 4;
-                const float4 x = *reinterpret_cast<const float4 *>(kr + at);
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(kr + at);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float4 q = *reinterpret_cast<const float4 *>(qs + r * HDP + at);
-                    s[r] = fmaf(q.x, x.x, s[r]);
-                    s[r] = fmaf(q.y, x.y, s[r]);
-                    s[r] = fmaf(q.z, x.z, s[r]);
-                    s[r] = fmaf(q.w, x.w, s[r]);
+                    const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(qs + r * HDP + at);
+                    s2[r] = fma2(q.x, x.x, s2[r]);
+                    s2[r] = fma2(q.y, x.y, s2[r]);
                 }
+            }
+            float s[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float y;
+                unpack2(s2[r], s[r], y);
+                s[r] += y;
             }
             const bool ok = (valid[st] >> tok) & 1u;
             bool rose = false;
@@ -130,10 +138,8 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
                     l[r] *= f;
 #pragma unroll
                     for (int x = 0; x < C; ++x) {
-                        o[r][x].x *= f;
-                        o[r][x].y *= f;
-                        o[r][x].z *= f;
-                        o[r][x].w *= f;
+                        o[r][x].x = mul2(o[r][x].x, pack2(f, f));
+                        o[r][x].y = mul2(o[r][x].y, pack2(f, f));
                     }
                 }
             }
@@ -159,13 +165,12 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
 #pragma unroll
                 for (int x = 0; x < C; ++x)
                     if (SETS > 1 || lane * 4 + 128 * x < HDP) {
-                        const float4 v = *reinterpret_cast<const float4 *>(vt + j * V::RS + col * 16 + 512 * x);
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(vt + j * V::RS + col * 16 + 512 * x);
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
-                            o[r][x].x = fmaf(pr[r], v.x, o[r][x].x);
-                            o[r][x].y = fmaf(pr[r], v.y, o[r][x].y);
-                            o[r][x].z = fmaf(pr[r], v.z, o[r][x].z);
-                            o[r][x].w = fmaf(pr[r], v.w, o[r][x].w);
+                            const uint64_t w2 = pack2(pr[r], pr[r]);
+                            o[r][x].x = fma2(w2, v.x, o[r][x].x);
+                            o[r][x].y = fma2(w2, v.y, o[r][x].y);
                         }
                     }
             }
@@ -176,10 +181,8 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
             if (r >= p.rows) break;
 #pragma unroll
             for (int x = COLS; x < 32; x <<= 1) {
-                o[r][0].x += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].x, x);
-                o[r][0].y += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].y, x);
-                o[r][0].z += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].z, x);
-                o[r][0].w += __shfl_xor_sync(0xFFFFFFFFu, o[r][0].w, x);
+                o[r][0].x = add2(o[r][0].x, __shfl_xor_sync(0xFFFFFFFFu, o[r][0].x, x));
+                o[r][0].y = add2(o[r][0].y, __shfl_xor_sync(0xFFFFFFFFu, o[r][0].y, x));
             }
             float sum = l[r];
             for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
@@ -191,7 +194,8 @@ template <typename V> __global__ void __launch_bounds__(V::WARPS * 32, 1) attn_f
             for (int x = 0; x < C; ++x) {
                 const int e = col * 4 + 128 * x;
                 if (set == 0 && e < a.hd)
-                    *reinterpret_cast<float4 *>(d + e) = make_float4(o[r][x].x * f, o[r][x].y * f, o[r][x].z * f, o[r][x].w * f);
+                    *reinterpret_cast<ulonglong2 *>(d + e) =
+                        make_ulonglong2(mul2(o[r][x].x, pack2(f, f)), mul2(o[r][x].y, pack2(f, f)));
             }
             if (lane == 0) {
                 if (p.slot >= 0) *reinterpret_cast<float2 *>(d + a.hd) = make_float2(m[r], sum);

@@ -18,6 +18,7 @@
 #include "../../include/lossk.h"
 #include "decode_internal.h"
 #include "decode_launch.h"
+#include "float2.cuh"
 #include "ptx.cuh"
 
 #include <type_traits>
@@ -219,30 +220,6 @@ __device__ __forceinline__ void add_z(float &z, float &lost, float x, float rest
 __device__ __forceinline__ bool far_above(const RowStat &r, float lm, float c)
 {
     return !((lm - r.ref) * c < FAR);          // (a NaN is, too)
-}
-
-// Two floats in one register pair.
-__device__ __forceinline__ uint64_t pack2(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t p, float &x, float &y)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
 }
 
 // A vector of -infinity.
