@@ -1,5 +1,6 @@
 // lossk_calls.cpp -- the decoding calls as a CPython module: arguments by
-// position, in the order of lossk.h, None for NULL, the status returned.
+// position, in the order of lossk.h, None for NULL, the status returned.  And
+// spans(), the checks and addresses of the tensors that such a call takes.
 //
 // A decoding step makes several of these calls per layer, of 13 to 30
 // arguments each; through ctypes such a call took 2 us for its arguments
@@ -78,6 +79,51 @@ template <typename R, typename... A> struct Caller<R(A...)> {
 LOSSK_CALLS(X)
 #undef X
 
+// Attributes and methods of a tensor.
+PyObject *s_is_cuda, *s_dtype, *s_is_contiguous, *s_data_ptr, *s_numel;
+
+// Whether an attribute (or what a method returns) is the object `want`.
+bool is(PyObject *got, PyObject *want)
+{
+    Py_XDECREF(got);
+    return got == want;
+}
+
+// spans(dtype, t0, t1, ...): (address, elements) of each, flat, where all are
+// contiguous CUDA tensors of that type; None, and no error, where one is not.  A
+// t that is None counts as no elements at address 0.
+PyObject *spans(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n < 1) {
+        PyErr_SetString(PyExc_TypeError, "spans needs a type");
+        return nullptr;
+    }
+    PyObject *r = PyTuple_New(2 * (n - 1));
+    if (!r) return nullptr;
+    for (Py_ssize_t i = 1; i < n; ++i) {
+        PyObject *t = a[i], *p, *k;
+        if (t == Py_None) {
+            p = PyLong_FromLong(0);
+            k = PyLong_FromLong(0);
+        } else if (is(PyObject_GetAttr(t, s_is_cuda), Py_True) && is(PyObject_GetAttr(t, s_dtype), a[0]) &&
+                   is(PyObject_CallMethodNoArgs(t, s_is_contiguous), Py_True)) {
+            p = PyObject_CallMethodNoArgs(t, s_data_ptr);
+            k = PyObject_CallMethodNoArgs(t, s_numel);
+        } else {
+            Py_DECREF(r);
+            PyErr_Clear();
+            Py_RETURN_NONE;
+        }
+        if (p) PyTuple_SET_ITEM(r, 2 * (i - 1), p);
+        if (k) PyTuple_SET_ITEM(r, 2 * (i - 1) + 1, k);
+        if (!p || !k) {
+            Py_DECREF(r);
+            return nullptr;
+        }
+    }
+    return r;
+}
+
 // load(path): the library's functions.
 PyObject *load(PyObject *, PyObject *path)
 {
@@ -103,6 +149,7 @@ PyObject *load(PyObject *, PyObject *path)
 
 PyMethodDef methods[] = {
     {"load", load, METH_O, nullptr},
+    {"spans", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(spans)), METH_FASTCALL, nullptr},
 #define X(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr},
     LOSSK_CALLS(X)
 #undef X
@@ -112,4 +159,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lossk_calls", nullptr, -1, method
 
 } // namespace
 
-PyMODINIT_FUNC PyInit__lossk_calls(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__lossk_calls(void)
+{
+    const std::pair<PyObject **, const char *> names[] = {{&s_is_cuda, "is_cuda"},
+                                                          {&s_dtype, "dtype"},
+                                                          {&s_is_contiguous, "is_contiguous"},
+                                                          {&s_data_ptr, "data_ptr"},
+                                                          {&s_numel, "numel"}};
+    for (const auto &x : names)
+        if (!(*x.first = PyUnicode_InternFromString(x.second))) return nullptr;
+    return PyModule_Create(&module);
+}

@@ -33,6 +33,7 @@ def _load_calls():
 
 
 _calls = _load_calls()
+_int32 = torch.int32
 KIND_BEAM_SELECT, KIND_CACHE, KIND_PAGED_ATTN = 0, 1, 2
 
 __all__ = ["KIND_BEAM_SELECT", "KIND_CACHE", "KIND_PAGED_ATTN", "decode_workspace", "beam_buffers",
@@ -73,6 +74,15 @@ def _on_gpu(t, name, dtype=None, contiguous=True):
         raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _ints(names, *tensors):
+    """(address, elements) of each int32 tensor, flat; None is no elements at address 0."""
+    r = _calls.spans(_int32, *tensors)
+    if r is None:
+        for t, name in zip(tensors, names):
+            _on_gpu(t, name, _int32)
+    return r
 
 
 def _span(t) -> int:
@@ -210,85 +220,73 @@ def _pool(pool, pages):
 
 def lossk_cache_fork(parent, table, lens, ref, page_size, table_out=None, lens_out=None, ws=None, stream=None):
     """parent int32 [groups, n_dst]; table holds groups * n_src rows.  Returns (table_out, lens_out)."""
-    _on_gpu(parent, "parent", torch.int32)
-    _on_gpu(lens, "lens", torch.int32)
-    _on_gpu(ref, "ref", torch.int32)
-    _on_gpu(lens_out, "lens_out", torch.int32)
-    n, m, stride, table_len = _table(table)
     G, n_dst = parent.shape
-    pages = ref.numel()
-    if n % G or lens.numel() != n:
-        raise ValueError(f"{n} rows and {lens.numel()} lengths in {G} groups")
-    if table_out is None:
-        table_out = torch.empty((G * n_dst, m), dtype=torch.int32, device=table.device)
     if lens_out is None:
         lens_out = torch.empty(G * n_dst, dtype=torch.int32, device=table.device)
+    parents, parents_len, lengths, lengths_len, refs, pages, outs, outs_len = _ints(
+        ("parent", "lens", "ref", "lens_out"), parent, lens, ref, lens_out)
+    n, m, stride, table_len = _table(table)
+    if n % G or lengths_len != n:
+        raise ValueError(f"{n} rows and {lengths_len} lengths in {G} groups")
+    if table_out is None:
+        table_out = torch.empty((G * n_dst, m), dtype=torch.int32, device=table.device)
     no, mo, stride_out, out_len = _table(table_out, "table_out")
     if no != G * n_dst or mo != m:
         raise ValueError("table_out must be [groups * n_dst, max_pages]")
     if ws is None:
         ws = decode_workspace(KIND_CACHE, max(n, no), pages, device=table.device)
-    st = _calls.lossk_cache_fork(G, n // G, n_dst, m, page_size, pages, parent.data_ptr(), parent.numel(),
-                              table.data_ptr(), table_len, stride, lens.data_ptr(), n, ref.data_ptr(), pages,
-                              table_out.data_ptr(), out_len, stride_out, lens_out.data_ptr(), lens_out.numel(),
-                              ws.data_ptr(), ws.numel(), _stream_of(table, stream))
+    st = _calls.lossk_cache_fork(G, n // G, n_dst, m, page_size, pages, parents, parents_len, table.data_ptr(),
+                                 table_len, stride, lengths, n, refs, pages, table_out.data_ptr(), out_len,
+                                 stride_out, outs, outs_len, ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_fork")
     return table_out, lens_out
 
 
 def lossk_cache_reserve(table, lens, ref, pool, page_size, n_new=1, ws=None, stream=None) -> None:
     """n_new: tokens to come for every sequence, or an int32 tensor with one count each."""
-    _on_gpu(lens, "lens", torch.int32)
-    _on_gpu(ref, "ref", torch.int32)
-    n, m, stride, table_len = _table(table)
     each = n_new if isinstance(n_new, torch.Tensor) else None
-    _on_gpu(each, "n_new", torch.int32)
-    pages = ref.numel()
+    lengths, lengths_len, refs, pages, new, new_len = _ints(("lens", "ref", "n_new"), lens, ref, each)
+    n, m, stride, table_len = _table(table)
     P = _pool(pool, pages)
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
-    st = _calls.lossk_cache_reserve(n, m, page_size, pages, 0 if each is not None else n_new, _ptr(each),
-                                 _len(each), table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(),
-                                 ref.data_ptr(), pages, *P, ws.data_ptr(), ws.numel(), _stream_of(table, stream))
+    st = _calls.lossk_cache_reserve(n, m, page_size, pages, 0 if each is not None else n_new, new, new_len,
+                                    table.data_ptr(), table_len, stride, lengths, lengths_len, refs, pages, *P,
+                                    ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_reserve")
 
 
 def lossk_cache_free(table, lens, ref, page_size, drop=None, ws=None, stream=None) -> None:
     """drop: uint8 [n_seq], nonzero where the sequence goes (None: all)."""
-    _on_gpu(lens, "lens", torch.int32)
-    _on_gpu(ref, "ref", torch.int32)
+    lengths, lengths_len, refs, pages = _ints(("lens", "ref"), lens, ref)
     _on_gpu(drop, "drop", torch.uint8)
     n, m, stride, table_len = _table(table)
     if ws is None:
-        ws = decode_workspace(KIND_CACHE, n, ref.numel(), device=table.device)
-    st = _calls.lossk_cache_free(n, m, page_size, ref.numel(), _ptr(drop), _len(drop), table.data_ptr(), table_len,
-                              stride, lens.data_ptr(), lens.numel(), ref.data_ptr(), ref.numel(), ws.data_ptr(),
-                              ws.numel(), _stream_of(table, stream))
+        ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+    st = _calls.lossk_cache_free(n, m, page_size, pages, _ptr(drop), _len(drop), table.data_ptr(), table_len, stride,
+                                 lengths, lengths_len, refs, pages, ws.data_ptr(), ws.numel(),
+                                 _stream_of(table, stream))
     _check(st, "lossk_cache_free")
 
 
 def lossk_cache_compact(table, lens, ref, pool, page_size, table_out=None, ref_out=None, n_live_out=None, ws=None,
                         stream=None):
     """Returns (table_out, ref_out, n_live_out); the pool's live pages are in front then."""
-    _on_gpu(lens, "lens", torch.int32)
-    _on_gpu(ref, "ref", torch.int32)
-    _on_gpu(ref_out, "ref_out", torch.int32)
-    _on_gpu(n_live_out, "n_live_out", torch.int32)
-    n, m, stride, table_len = _table(table)
-    pages = ref.numel()
-    P = _pool(pool, pages)
-    table_out = table_out if table_out is not None else table.new_empty((n, m))
     ref_out = ref_out if ref_out is not None else torch.empty_like(ref)
     n_live_out = n_live_out if n_live_out is not None else ref.new_empty(1)
+    lengths, lengths_len, refs, pages, refs_out, refs_out_len, live, live_len = _ints(
+        ("lens", "ref", "ref_out", "n_live_out"), lens, ref, ref_out, n_live_out)
+    n, m, stride, table_len = _table(table)
+    P = _pool(pool, pages)
+    table_out = table_out if table_out is not None else table.new_empty((n, m))
     no, mo, stride_out, out_len = _table(table_out, "table_out")
-    if no != n or mo != m or n_live_out.numel() < 1:
+    if no != n or mo != m or live_len < 1:
         raise ValueError("table_out must be shaped like table, n_live_out hold one value")
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
-    st = _calls.lossk_cache_compact(n, m, page_size, pages, table.data_ptr(), table_len, stride, lens.data_ptr(),
-                                 lens.numel(), ref.data_ptr(), pages, table_out.data_ptr(), out_len, stride_out,
-                                 ref_out.data_ptr(), ref_out.numel(), n_live_out.data_ptr(), *P, ws.data_ptr(),
-                                 ws.numel(), _stream_of(table, stream))
+    st = _calls.lossk_cache_compact(n, m, page_size, pages, table.data_ptr(), table_len, stride, lengths,
+                                    lengths_len, refs, pages, table_out.data_ptr(), out_len, stride_out, refs_out,
+                                    refs_out_len, live, *P, ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_compact")
     return table_out, ref_out, n_live_out
 
@@ -322,8 +320,7 @@ def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, w
     [pages, page, heads, head_dim] (any strides).  first: int32 [n_seq + 1], where each sequence's
     rows begin (None: one row per sequence)."""
     (n_pages, page, kv, hd), (sp, stok, sh, _), pages_len = _pages(k_pages, v_pages)
-    _on_gpu(lens, "lens", torch.int32)
-    _on_gpu(first, "first", torch.int32)
+    lengths, lengths_len, firsts, firsts_len = _ints(("lens", "first"), lens, first)
     n, m, stride, table_len = _table(table)
     _on_gpu(k_new, "k_new", k_pages.dtype, contiguous=False)
     _on_gpu(v_new, "v_new", k_pages.dtype, contiguous=False)
@@ -337,8 +334,8 @@ def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, w
     st = _calls.lossk_cache_write(n_tok, n, kv, hd, m, page, n_pages, _dtype_code(k_pages), k_new.data_ptr(),
                                v_new.data_ptr(), _span(k_new), strides[0] if n_tok > 1 else kv * hd,
                                k_pages.data_ptr(), v_pages.data_ptr(), pages_len, sp, stok, sh,
-                               table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(), _ptr(first),
-                               _len(first), ws.data_ptr(), ws.numel(), _stream_of(table, stream))
+                               table.data_ptr(), table_len, stride, lengths, lengths_len, firsts, firsts_len,
+                               ws.data_ptr(), ws.numel(), _stream_of(table, stream))
     _check(st, "lossk_cache_write")
 
 
@@ -350,7 +347,7 @@ def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, sha
     [pages, page, heads, head_dim] (any strides).  scale defaults to head_dim ** -0.5; share: how
     many consecutive sequences may share leading pages.  Returns out."""
     (n_pages, page, kv, hd), (sp, stok, sh, _), pages_len = _pages(k_pages, v_pages)
-    _on_gpu(lens, "lens", torch.int32)
+    lengths, lengths_len = _ints(("lens",), lens)
     _on_gpu(q, "q", k_pages.dtype, contiguous=False)
     n, m, stride, table_len = _table(table)
     shape, strides = q.shape, q.stride()
@@ -367,7 +364,7 @@ def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, sha
         ws = decode_workspace(KIND_PAGED_ATTN, n, hq, kv, hd, q.device)
     st = _calls.lossk_paged_attn(n, hq, kv, hd, m, page, n_pages, share, _dtype_code(q), q.data_ptr(), _span(q),
                               strides[0] if n > 1 else hq * hd, k_pages.data_ptr(), v_pages.data_ptr(), pages_len,
-                              sp, stok, sh, table.data_ptr(), table_len, stride, lens.data_ptr(), lens.numel(),
+                              sp, stok, sh, table.data_ptr(), table_len, stride, lengths, lengths_len,
                               max_len, window, hd ** -0.5 if scale is None else scale, out.data_ptr(), out.numel(),
                               _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream_of(q, stream))
     _check(st, "lossk_paged_attn")

@@ -47,3 +47,14 @@ def test_a_code_out_of_range_is_no_other_code():
     args[4] = (1 << 32) + 1                    # the type code is an int32
     with pytest.raises(OverflowError):
         decode._calls.lossk_beam_select(*args)
+
+
+def test_spans_of_no_gpu_tensor():
+    import torch
+    spans = decode._calls.spans
+    assert spans(torch.int32) == ()
+    assert spans(torch.int32, None) == (0, 0)
+    assert spans(torch.int32, None, torch.zeros(3, dtype=torch.int32)) is None     # not on a GPU
+    assert spans(torch.int32, [1]) is None                                          # no tensor
+    with pytest.raises(TypeError):
+        spans()
