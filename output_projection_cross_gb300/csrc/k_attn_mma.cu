@@ -5,7 +5,7 @@
 // read once from HBM and meets only the query rows of its KV head (and, for
 // shared pages, of its group), 2 to 32 multiply-adds a byte.  tcgen05 would
 // spend tiles of 128 rows on them, so the products run as mma.sync m16n8k16 with
-// 16 query rows (the tensor pipe is 23 to 28 % active while HBM is read at 86 %
+// 16 query rows (the tensor pipe is 24 to 29 % active while HBM is read at 86 %
 // of the copy rate), and the kernel is built around the loads:
 //
 //  - every warp walks its own run of units with its own ring of STAGES tiles
