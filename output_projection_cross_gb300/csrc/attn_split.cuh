@@ -119,7 +119,7 @@ __device__ __forceinline__ const long long *unit_bases(const AttnArgs &a, long l
     __shared__ long long s_warp[32];
     // what share or plan left is complete after the wait (the join is not let in early: its blocks,
     // resident and waiting, cost the pass 2.5 us)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     if (a.n_group > BASE_GROUPS) return a.base;
     sum_units(a, s_base, s_warp);
     if (blockIdx.x == 0) check_lens(a);

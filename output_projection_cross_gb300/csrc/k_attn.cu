@@ -46,6 +46,7 @@ template <int T> __global__ void __launch_bounds__(T) attn_share_kernel(AttnArgs
 {
     __shared__ int s_first, s_min, s_max;
     const int g = blockIdx.x, t = threadIdx.x;
+    wait_for_stream();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (t == 0) {
         int mn = 1 << 30, mx = 0;
@@ -97,8 +98,8 @@ template <int T> __global__ void __launch_bounds__(T) attn_share_kernel(AttnArgs
 __global__ void __launch_bounds__(PLAN_T) attn_plan_kernel(AttnArgs a)
 {
     __shared__ long long s_warp[PLAN_T / 32];
+    wait_for_stream();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     check_lens(a);
     sum_units(a, a.base, s_warp);
 }
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : WPR * 32) attn_join_kernel(At
     __shared__ float4 s_o[WPR > 1 ? WPR : 1][32 * H];
     __shared__ float2 s_ml[WPR > 1 ? WPR : 1];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, k0 = WPR == 1 ? 0 : warp;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     // (there are fewer than 2^31 rows)
     const unsigned row = WPR == 1 ? blockIdx.x * 8 + warp : blockIdx.x, n_q = a.n_q;
     if (row >= static_cast<unsigned>(a.n_group) * a.share * n_q) return;
@@ -234,10 +235,10 @@ template <typename T, int H> cudaError_t launch_join_h(const AttnArgs &a, cudaSt
     // 52, 54 and 82 us (64 sequences in groups of 8, 2048 rows, pieces 3); 41, 37 and 46 us (33 sequences of
     // up to 9000 tokens, 1056 rows, pieces 5); 100, 100 and 96 us (one of 131072, 32 rows, pieces 153)
     if (pieces > JOIN_MANY)
-        return launch_after(true, attn_join_kernel<T, H, 16>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, a);
+        return launch(attn_join_kernel<T, H, 16>, dim3(static_cast<unsigned>(rows)), dim3(512), 0, st, a);
     if (pieces > JOIN_FEW)
-        return launch_after(true, attn_join_kernel<T, H, 4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, a);
-    return launch_after(true, attn_join_kernel<T, H, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, a);
+        return launch(attn_join_kernel<T, H, 4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, a);
+    return launch(attn_join_kernel<T, H, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, a);
 }
 template <typename T> cudaError_t launch_join(const AttnArgs &a, cudaStream_t st)
 {
@@ -259,12 +260,11 @@ cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st)
         // the more threads the fewer rounds over a long table, and the later a short one is done: 4 beams of
         // 3750 pages took 8 us with 256 threads and 4 with 1024, 8 x 8 of 136 pages 4 and 5
         const unsigned groups = static_cast<unsigned>(a.n_group);
-        if (a.max_pages <= 256 * SHARE_U) attn_share_kernel<256><<<groups, 256, 0, st>>>(a);
-        else attn_share_kernel<1024><<<groups, 1024, 0, st>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = a.max_pages <= 256 * SHARE_U ? launch(attn_share_kernel<256>, dim3(groups), dim3(256), 0, st, a)
+                                                           : launch(attn_share_kernel<1024>, dim3(groups), dim3(1024), 0, st, a);
         if (e != cudaSuccess || a.n_group <= BASE_GROUPS) return e;
     }
-    return launch_after(a.share > 1, attn_plan_kernel, dim3(1), dim3(PLAN_T), 0, st, a);
+    return launch(attn_plan_kernel, dim3(1), dim3(PLAN_T), 0, st, a);
 }
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st)
 {

@@ -212,7 +212,7 @@ template <int HDP, int R> cudaError_t launch_fvariant(const AttnArgs &a, cudaStr
     constexpr int bytes = V::WARPS * V::WARP_BYTES;
     const cudaError_t e = raise_smem<attn_ffma_kernel<V>>(bytes);
     if (e != cudaSuccess) return e;
-    return launch_after(attn_plans(a), attn_ffma_kernel<V>, dim3(a.nw < 152 ? a.nw : 152), dim3(V::WARPS * 32), bytes, st, a);
+    return launch(attn_ffma_kernel<V>, dim3(a.nw < 152 ? a.nw : 152), dim3(V::WARPS * 32), bytes, st, a);
 }
 
 template <int HDP> cudaError_t launch_fhdp(const AttnArgs &a, cudaStream_t st)

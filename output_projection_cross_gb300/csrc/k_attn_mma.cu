@@ -293,7 +293,7 @@ template <int HDP, int W> cudaError_t launch_variant(bool f16, const AttnArgs &a
     const cudaError_t e = f16 ? raise_smem<attn_mma_kernel<V, true>>(bytes) : raise_smem<attn_mma_kernel<V, false>>(bytes);
     if (e != cudaSuccess) return e;
     auto kern = f16 ? attn_mma_kernel<V, true> : attn_mma_kernel<V, false>;
-    return launch_after(a.share > 1 || a.n_group > BASE_GROUPS, kern, dim3(a.nw < 152 ? a.nw : 152),
+    return launch(kern, dim3(a.nw < 152 ? a.nw : 152),
                         dim3(V::THREADS), bytes, st, a);
 }
 

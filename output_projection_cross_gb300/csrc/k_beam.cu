@@ -429,6 +429,7 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) b
         }
         fence_mbarrier_init();
     }
+    wait_for_stream();
     __syncthreads();
 
     if (t >= NT) {
@@ -679,6 +680,7 @@ template <typename T> __global__ void __launch_bounds__(128) beam_small_kernel(B
 {
     constexpr int N = SMALL / 32;
     const int r = static_cast<int>((static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    wait_for_stream();
     if (r >= a.batch * a.beams || !beam_reads(a, r)) return;
     const T *row = static_cast<const T *>(a.logits) + r * a.row_stride;
     const uint32_t *allow = a.allow ? a.allow + r * a.allow_stride : nullptr;
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
     __shared__ double s_lse[LOSSK_BEAM_MAX_BEAMS], s_inv[LOSSK_BEAM_MAX_BEAMS];
     __shared__ int s_valid[MERGE_WARPS];
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     if (b == 0 && t == 0) *a.next = 0;                 // for the workspace's next call
     // the splits' lists, each in falling order, from shared memory (what lies deeper than `depth` from
     // where it is); asked for before it is known whether the beam has any
@@ -935,6 +937,7 @@ __global__ void beam_gather_kernel(int64_t n_src, int64_t n_dst, int64_t words, 
                                    const V *__restrict__ src, V *__restrict__ dst, int *fault)
 {
     const int64_t j = blockIdx.x, g = j / n_dst;
+    wait_for_stream();
     const int p = parent[j];
     const bool ok = p >= 0 && p < n_src;
     if (!ok && p != -1 && threadIdx.x == 0 && blockIdx.y == 0) raise_fault(fault, LOSSK_TARGET_OUT_OF_RANGE);
@@ -985,14 +988,14 @@ template <typename T, bool MASK> cudaError_t launch_rows(const BeamArgs &a, cuda
     const cudaError_t e = raise_smem<beam_rows_kernel<T, MASK>>(bytes);
     if (e != cudaSuccess) return e;
     const int64_t items = static_cast<int64_t>(a.batch) * a.beams * a.n_split;
-    beam_rows_kernel<T, MASK><<<static_cast<unsigned>(items < ROW_BLOCKS ? items : ROW_BLOCKS), NT + 32, bytes, st>>>(a);
-    return cudaGetLastError();
+    return launch(beam_rows_kernel<T, MASK>, dim3(static_cast<unsigned>(items < ROW_BLOCKS ? items : ROW_BLOCKS)),
+                  dim3(NT + 32), bytes, st, a);
 }
 
 template <typename T> cudaError_t launch_small(const BeamArgs &a, cudaStream_t st)
 {
-    beam_small_kernel<T><<<static_cast<unsigned>((static_cast<int64_t>(a.batch) * a.beams + 3) / 4), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch(beam_small_kernel<T>, dim3(static_cast<unsigned>((static_cast<int64_t>(a.batch) * a.beams + 3) / 4)),
+                  dim3(128), 0, st, a);
 }
 
 cudaError_t launch_beam_rows(const BeamArgs &a, cudaStream_t st)
@@ -1015,7 +1018,7 @@ cudaError_t launch_beam_merge(const BeamArgs &a0, cudaStream_t st)
     const size_t bytes = sizeof(Key) * (2 * all + (heads > all ? heads : all));
     const cudaError_t e = raise_smem<beam_merge_kernel>(bytes);
     if (e != cudaSuccess) return e;
-    return launch_after(true, beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(MERGE_NT), bytes, st, a);
+    return launch(beam_merge_kernel, dim3(static_cast<unsigned>(a.batch)), dim3(MERGE_NT), bytes, st, a);
 }
 
 cudaError_t launch_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t row_bytes,
@@ -1028,17 +1031,13 @@ cudaError_t launch_beam_gather(int64_t n_group, int64_t n_src, int64_t n_dst, in
     const int64_t cut = (words + 256 * 16 - 1) / (256 * 16);
     const dim3 grid(static_cast<unsigned>(n_group * n_dst), static_cast<unsigned>(cut > 64 ? 64 : cut));
     if (unit == 16)
-        beam_gather_kernel<uint4><<<grid, 256, 0, st>>>(n_src, n_dst, words, parent, static_cast<const uint4 *>(src),
-                                                        static_cast<uint4 *>(dst), fault);
-    else if (unit == 4)
-        beam_gather_kernel<uint32_t><<<grid, 256, 0, st>>>(n_src, n_dst, words, parent,
-                                                           static_cast<const uint32_t *>(src),
-                                                           static_cast<uint32_t *>(dst), fault);
-    else
-        beam_gather_kernel<uint8_t><<<grid, 256, 0, st>>>(n_src, n_dst, words, parent,
-                                                          static_cast<const uint8_t *>(src),
-                                                          static_cast<uint8_t *>(dst), fault);
-    return cudaGetLastError();
+        return launch(beam_gather_kernel<uint4>, grid, dim3(256), 0, st, n_src, n_dst, words, parent,
+                      static_cast<const uint4 *>(src), static_cast<uint4 *>(dst), fault);
+    if (unit == 4)
+        return launch(beam_gather_kernel<uint32_t>, grid, dim3(256), 0, st, n_src, n_dst, words, parent,
+                      static_cast<const uint32_t *>(src), static_cast<uint32_t *>(dst), fault);
+    return launch(beam_gather_kernel<uint8_t>, grid, dim3(256), 0, st, n_src, n_dst, words, parent,
+                  static_cast<const uint8_t *>(src), static_cast<uint8_t *>(dst), fault);
 }
 
 } // namespace lossk

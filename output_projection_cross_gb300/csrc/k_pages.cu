@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(128) cache_fork_kernel(ForkArgs a)
     __shared__ int s_n;
     const int t = threadIdx.x, b = blockIdx.x;
     const int rows_dst = a.n_group * a.n_dst;
+    wait_for_stream();
     if (b < rows_dst) {
         const int g = b / a.n_dst, p = a.parent[b];
         const bool ok = p >= 0 && p < a.n_src;
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) cache_plan_kernel(ReserveArgs a)
     __shared__ long long s_long[32];
     __shared__ int s_status;
     const int t = threadIdx.x;
+    wait_for_stream();
     if (t == 0) {
         s_status = 0;
         *a.n_copy = 0;
@@ -317,7 +319,7 @@ __device__ __forceinline__ void copy_moves(const CopyArgs &a, int64_t n, int blo
 
 __global__ void __launch_bounds__(COPY_THREADS) cache_copy_kernel(CopyArgs a)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     copy_moves(a, a.n_dev ? *a.n_dev : a.n, blockIdx.x, gridDim.x);
 }
 
@@ -325,6 +327,7 @@ __global__ void __launch_bounds__(COPY_THREADS) cache_copy_kernel(CopyArgs a)
 __global__ void __launch_bounds__(128) cache_free_kernel(FreeArgs a)
 {
     const int i = blockIdx.x, t = threadIdx.x;
+    wait_for_stream();
     if (a.drop && !a.drop[i]) return;
     int32_t *row = a.table + i * a.table_stride;
     const int used = pages_of(len_checked(a.lens[i], a.max_pages, a.page, a.fault), a.page);
@@ -351,6 +354,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) cache_rank_kernel(CompactArgs a)
     __shared__ int s_warp[32];
     __shared__ long long s_long[32];
     const int t = threadIdx.x;
+    wait_for_stream();
     int live = 0, n_live;
     for (int base = 0; base < a.n_pages; base += PLAN_THREADS * PER) {
         int r[PER];
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) cache_rank_kernel(CompactArgs a)
 
 __global__ void __launch_bounds__(COPY_THREADS) cache_move_kernel(CompactArgs a, CopyArgs c)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     const int n_live = *a.n_live_out, n = *a.n_copy;
     const int64_t gt = static_cast<int64_t>(blockIdx.x) * COPY_THREADS + threadIdx.x;
     const int64_t all = static_cast<int64_t>(gridDim.x) * COPY_THREADS;
@@ -430,6 +434,7 @@ __global__ void __launch_bounds__(128) cache_write_kernel(WriteArgs a)
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     const int64_t tok = w >> 1;
+    wait_for_stream();
     if (tok >= a.n_tok) return;
     int seq = static_cast<int>(tok), off = 0;
     if (a.first) {
@@ -478,40 +483,33 @@ int64_t pieces_of(const CopyArgs &c)
 
 cudaError_t launch_cache_fork(const ForkArgs &a, cudaStream_t st)
 {
-    cache_fork_kernel<<<static_cast<unsigned>(a.n_group) * (a.n_dst + a.n_src), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch(cache_fork_kernel, dim3(static_cast<unsigned>(a.n_group) * (a.n_dst + a.n_src)), dim3(128), 0, st, a);
 }
 cudaError_t launch_cache_plan(const ReserveArgs &a, cudaStream_t st)
 {
-    cache_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch(cache_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, a);
 }
 cudaError_t launch_cache_copy(const CopyArgs &a, int64_t most, cudaStream_t st)
 {
-    // (moves that the plan of the same call listed)
-    return launch_after(a.n_dev != nullptr, cache_copy_kernel, dim3(copy_blocks(most * pieces_of(a))), dim3(COPY_THREADS), 0, st, a);
+    return launch(cache_copy_kernel, dim3(copy_blocks(most * pieces_of(a))), dim3(COPY_THREADS), 0, st, a);
 }
 cudaError_t launch_cache_free(const FreeArgs &a, cudaStream_t st)
 {
-    cache_free_kernel<<<static_cast<unsigned>(a.n_seq), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch(cache_free_kernel, dim3(static_cast<unsigned>(a.n_seq)), dim3(128), 0, st, a);
 }
 cudaError_t launch_cache_rank(const CompactArgs &a, cudaStream_t st)
 {
-    cache_rank_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch(cache_rank_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, a);
 }
 cudaError_t launch_cache_move(const CompactArgs &a, const CopyArgs &c, cudaStream_t st)
 {
-    return launch_after(true, cache_move_kernel, dim3(copy_blocks((a.n_pages / 2 + 1) * pieces_of(c))), dim3(COPY_THREADS), 0, st, a, c);
+    return launch(cache_move_kernel, dim3(copy_blocks((a.n_pages / 2 + 1) * pieces_of(c))), dim3(COPY_THREADS), 0, st, a, c);
 }
 cudaError_t launch_cache_write(const WriteArgs &a, int word, cudaStream_t st)
 {
     const unsigned grid = static_cast<unsigned>((a.n_tok * 2 + 3) / 4);
-    if (word == 16) cache_write_kernel<uint4><<<grid, 128, 0, st>>>(a);
-    else if (word == 4) cache_write_kernel<uint32_t><<<grid, 128, 0, st>>>(a);
-    else cache_write_kernel<uint16_t><<<grid, 128, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch(word == 16 ? cache_write_kernel<uint4> : word == 4 ? cache_write_kernel<uint32_t> : cache_write_kernel<uint16_t>,
+                  dim3(grid), dim3(128), 0, st, a);
 }
 
 } // namespace lossk
