@@ -443,7 +443,14 @@ template <typename T, bool MASK> __global__ void __launch_bounds__(NT + 32, 3) b
             return st;
         };
         const int items = a.batch * a.beams * a.n_split;
-        for (int i = blockIdx.x; i < items; i = gridDim.x + atomicAdd(a.next, 1)) {
+        // an item is followed by one look at the counter: the items-th look is the last of the launch and
+        // puts it back, so that the next call finds 0 whatever becomes of the kernels after this one
+        auto following = [&] {
+            const int n = atomicAdd(a.next, 1);
+            if (n == items - 1) *a.next = 0;
+            return static_cast<int>(gridDim.x) + n;
+        };
+        for (int i = blockIdx.x; i < items; i = following()) {
             const Item<T> it(a, i);
             if (!beam_reads(a, it.r)) continue;
             for (int c = 0; c < it.chunks(); ++c) {
@@ -774,7 +781,6 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
     __shared__ int s_valid[MERGE_WARPS];
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     wait_for_stream();
-    if (b == 0 && t == 0) *a.next = 0;                 // for the workspace's next call
     // the splits' lists, each in falling order, from shared memory (what lies deeper than `depth` from
     // where it is); asked for before it is known whether the beam has any
     const int depth = a.n_split > 1 ? a.depth : a.n_out;

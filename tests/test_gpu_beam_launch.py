@@ -1,0 +1,51 @@
+"""Selections whose launches a process makes first: sizes on either side of the shared memory a kernel has
+without asking, and what a call finds on a workspace that another call left.
+
+Each script runs in a process of its own, for a larger selection before it would raise the limits.
+"""
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+START = """
+import torch
+import output_projection_cross_gb300 as L
+g = torch.Generator(device="cuda").manual_seed(1)
+
+def inputs(B, K, V):
+    return (torch.randn(B * K, V, device="cuda", generator=g).bfloat16(),
+            -torch.rand(B, K, device="cuda", generator=g))
+"""
+
+
+def run(script):
+    from conftest import build_lib
+    build_lib()
+    r = subprocess.run([sys.executable, "-c", START + script], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_a_call_after_one_that_was_refused():
+    """512 rows are more than the rows kernel has blocks: which rows it takes hangs on its counter."""
+    run("""
+B, K, V = 16, 32, 32000
+ws = L.decode_workspace(L.KIND_BEAM_SELECT, B, K, V, 64)
+x, s = inputs(B, K, V)
+try:
+    L.lossk_beam_select(x, s, 64, ws=ws)
+except L.LosskError:
+    pass
+for n in (8, 3):
+    x, s = inputs(B, K, V)
+    got = L.lossk_beam_select(x, s, n, ws=ws)
+    want = L.lossk_beam_select(x, s, n)
+    assert all(torch.equal(got[k], want[k]) for k in got)
+    rank = (s.double()[:, :, None] + torch.log_softmax(x.double(), -1).view(B, K, V)).view(B, -1)
+    assert torch.equal(rank.topk(n).indices, got["parent"].long() * V + got["token"])
+assert L.lossk_device_status(ws) == 580
+""")
