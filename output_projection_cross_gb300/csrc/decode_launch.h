@@ -30,11 +30,11 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaS
 }
 
 // Lets kernel K take `bytes` of dynamic shared memory: set on the current device
-// when first needed, or when more is.
+// when first needed.  (Without it a block has 48 KB in all, its static arrays
+// among them: a kernel of 3 KB of those is refused 46 KB beside them.)
 template <auto K> cudaError_t raise_smem(size_t bytes)
 {
     static std::atomic<size_t> have[64];
-    if (bytes <= 48 * 1024) return cudaSuccess;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -49,3 +49,26 @@ for n in (8, 3):
     assert torch.equal(rank.topk(n).indices, got["parent"].long() * V + got["token"])
 assert L.lossk_device_status(ws) == 580
 """)
+
+
+@pytest.mark.parametrize("B,K,V,n", [
+    # the merge takes 24 bytes a candidate, or 128 an entry of a beam's split lists: on both sides of 48 KB
+    # less its own arrays (45 to 46 KB), and of 48 KB
+    (64, 32, 151936, 64), (16, 32, 32000, 64), (1, 12, 128256, 24), (1, 9, 151936, 18), (2000, 30, 513, 64),
+    (2000, 30, 513, 63), (2000, 31, 513, 62), (700, 15, 600, 128), (700, 17, 600, 128)])
+def test_sizes_about_the_limit_as_a_process_first_call(B, K, V, n):
+    run(f"B, K, V, n = {B}, {K}, {V}, {n}" + """
+x, s = inputs(B, K, V)
+ws = L.decode_workspace(L.KIND_BEAM_SELECT, B, K, V, n)
+got = L.lossk_beam_select(x, s, n, ws=ws)
+assert L.lossk_device_status(ws) == 580
+for b in (0, B // 2, B - 1):
+    rows = x[b * K:(b + 1) * K].double()
+    rank = (s[b].double()[:, None] + torch.log_softmax(rows, -1)).view(-1)
+    best = rank.topk(n + 1).values
+    at = got["parent"][b].long() * V + got["token"][b]
+    # (bf16 logits tie: candidates of equal rank may stand in another order here; a score's rounding is
+    # 2^-24 of 20 and its log-sum-exp's error 3e-6)
+    assert torch.allclose(rank[at], best[:n], rtol=0, atol=1e-5) and len(set(at.tolist())) == n
+    assert torch.allclose(got["score"][b].double(), best[:n], rtol=0, atol=1e-5)
+""")
