@@ -28,7 +28,7 @@ namespace lossk {
 
 namespace {
 
-constexpr float RISE = 8.f;                // as in k_attn_mma.cu
+constexpr float RISE = 8.f;                // a row's reference moves once its maximum is that far above it
 
 template <int HDP_, int R_> struct FVariant {
     static constexpr int HDP = HDP_, R = R_, W = 1;

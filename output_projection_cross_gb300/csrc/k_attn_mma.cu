@@ -17,9 +17,12 @@
 //    filled with zeros and masked, whatever the page holds there.
 //  - scores stay in the accumulators' registers, where they already have the
 //    layout of the second product's left operand.
-//  - a weight goes to the tensor cores as the sum of two 16-bit values, so
-//    that it keeps 16 (bf16) or 22 (fp16) bits: two instructions instead of
-//    one, which the stream hides, for an output that is rounded once.
+//  - a weight goes to the tensor cores as the sum of two 16-bit values: two
+//    instructions instead of one, which the stream hides.  Of bf16 that keeps
+//    16 bits of every weight.  Of fp16 it keeps 22 of those above 2^-14, and
+//    below that what lies above 2^-25, so the exponents' reference follows the
+//    tiles' maxima both up and down (see Reference): every weight is within 2^-22 of
+//    the largest in its tile, and the output's sums stay those of fp32.
 //
 // Measured, split pass and join: one sequence of 131072 tokens (8 KV heads of
 // 128, bf16, 537 MB) 96 us, the pass alone 92 us = 5.8 TB/s; 33 sequences of 1 to
@@ -63,13 +66,41 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// m, the reference that a row's exponents are taken against, is not the running
+// maximum: any m gives the same result, and rescaling the outputs for every new
+// maximum would cost most tiles one (with 16 rows some maximum rises).  It moves
+// where a tile's maximum x lies outside [m - LOW, m + TOP], to x - LIFT.
+//   bf16: up alone (LOW infinite), TOP 8 and LIFT 0: weights of 2^8 at most.
+//   fp16: LIFT 7 and TOP 15, so weights are up to 2^15 and a tile's largest is
+//   2^7 when m moves.  m moves down as well: behind a token that outweighs the
+//   rest by 2^26 their weights would be 0 to the tensor cores, while the sum of
+//   weights in fp32 counts them (an output of 6 % off at 2^23, of 0 at 2^26, where
+//   the heavy token's value is 0).  At most DEEP below its highest place: sums of
+//   2^30 weights of 2^75 times 2^16 are still floats, and what is that far below
+//   the heaviest token is less than any fp16 output's step.
+template <bool F16> struct Reference {
+    static constexpr float LIFT = F16 ? 7.f : 0.f, TOP = F16 ? 15.f : 8.f, LOW = 3.f, DEEP = 60.f;
+    float m = -INFINITY, peak = -INFINITY;
+    // where m goes for a tile of maximum x; peak is the highest place m has had
+    __device__ __forceinline__ float place(float x) const
+    {
+        if (x > m + TOP) return x - LIFT;
+        if constexpr (F16)
+            if (x < m - LOW && x > -INFINITY) return fmaxf(x - LIFT, peak - DEEP);
+        return m;
+    }
+    __device__ __forceinline__ void move(float to)
+    {
+        m = to;
+        if constexpr (F16) peak = fmaxf(peak, to);
+    }
+};
+
 // A variant: head sizes up to HDP (a multiple of 32) and W warps on a ring.
 // The warps of a ring share its tiles and its run of units, each with 16 query
 // rows of its own: where more than 16 rows meet a key (a wide group of heads,
 // beams over shared pages) it is still read once, and no warp carries more than
 // 16 rows' outputs in registers.
-constexpr float RISE = 8.f;
-
 template <int HDP_, int W_> struct Variant {
     static constexpr int HDP = HDP_, W = W_;
     static constexpr int KT = 16;
@@ -143,7 +174,8 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) ldsm4(qf[ks], qs + v_off + ks * 32);
         }
-        float o[DT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[DT][4], l[2] = {0.f, 0.f};
+        Reference<F16> ref[2];
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -194,26 +226,22 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
                         for (int e = 0; e < 4; ++e)
                             if (!((mask >> (j * 8 + (lane & 3) * 2 + (e & 1))) & 1u)) s[0][j][e] = -INFINITY;
                 }
-                // m is the reference the exponents are taken against.  It follows the maximum only
-                // once that is RISE above it (a weight is at most 2^RISE until then), so that the
-                // outputs are seldom rescaled: with 16 rows some maximum rises in most tiles.
                 float z[2];
-                bool rose = false;
+                bool moves = false;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x = fmaxf(fmaxf(s[0][0][2 * h], s[0][0][2 * h + 1]), fmaxf(s[0][1][2 * h], s[0][1][2 * h + 1]));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                    rose |= x > m[h] + RISE;
-                    z[h] = x;
+                    z[h] = ref[h].place(x);
+                    moves |= z[h] != ref[h].m;
                 }
-                if (__any_sync(0xFFFFFFFFu, rose)) {
+                if (__any_sync(0xFFFFFFFFu, moves)) {
                     float f[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float x = z[h] > m[h] + RISE ? z[h] : m[h];
-                        f[h] = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - x);
-                        m[h] = x;
+                        f[h] = ref[h].m == -INFINITY ? 0.f : ex2_approx(ref[h].m - z[h]);
+                        ref[h].move(z[h]);
                         l[h] *= f[h];
                     }
 #pragma unroll
@@ -224,8 +252,8 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
                         o[d][3] *= f[1];
                     }
                 }
-                z[0] = m[0] == -INFINITY ? 0.f : m[0];
-                z[1] = m[1] == -INFINITY ? 0.f : m[1];
+                z[0] = ref[0].m == -INFINITY ? 0.f : ref[0].m;
+                z[1] = ref[1].m == -INFINITY ? 0.f : ref[1].m;
                 uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -271,14 +299,14 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
                         if (d * 8 < a.hd)
                             *reinterpret_cast<uint32_t *>(out + d * 8 + col0) =
                                 pack_16x2<F16>(o[d][2 * h] * inv, o[d][2 * h + 1] * inv);
-                    if (a.lse && col0 == 0) a.lse[r] = (m[h] == -INFINITY ? 0.f : m[h]) * float(LN2) + logf(sum);
+                    if (a.lse && col0 == 0) a.lse[r] = (ref[h].m == -INFINITY ? 0.f : ref[h].m) * float(LN2) + logf(sum);
                 } else {
                     float *d0 = p.part + static_cast<int64_t>(i) * (a.hd + ATTN_ROW);
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
                         if (d * 8 < a.hd)
                             *reinterpret_cast<float2 *>(d0 + d * 8 + col0) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
-                    if (col0 == 0) *reinterpret_cast<float2 *>(d0 + a.hd) = make_float2(m[h], sum);
+                    if (col0 == 0) *reinterpret_cast<float2 *>(d0 + a.hd) = make_float2(ref[h].m, sum);
                 }
             }
         }
