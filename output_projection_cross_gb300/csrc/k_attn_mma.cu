@@ -69,30 +69,30 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // m, the reference that a row's exponents are taken against, is not the running
 // maximum: any m gives the same result, and rescaling the outputs for every new
 // maximum would cost most tiles one (with 16 rows some maximum rises).  It moves
-// where a tile's maximum x lies outside [m - LOW, m + TOP], to x - LIFT.
-//   bf16: up alone (LOW infinite), TOP 8 and LIFT 0: weights of 2^8 at most.
+// to x - LIFT where a tile's maximum x is more than TOP above it, or LOW below.
+//   bf16: up alone, TOP 8 and LIFT 0: weights of 2^8 at most.
 //   fp16: LIFT 7 and TOP 15, so weights are up to 2^15 and a tile's largest is
 //   2^7 when m moves.  m moves down as well: behind a token that outweighs the
 //   rest by 2^26 their weights would be 0 to the tensor cores, while the sum of
 //   weights in fp32 counts them (an output of 6 % off at 2^23, of 0 at 2^26, where
-//   the heavy token's value is 0).  At most DEEP below its highest place: sums of
-//   2^30 weights of 2^75 times 2^16 are still floats, and what is that far below
-//   the heaviest token is less than any fp16 output's step.
+//   the heavy token's value is 0).  It stops where the weights so far add up to
+//   2^MOST, which leaves the outputs' sums floats (values are below 2^16); what
+//   weighs that much less is under any fp16 output's step.
 template <bool F16> struct Reference {
-    static constexpr float LIFT = F16 ? 7.f : 0.f, TOP = F16 ? 15.f : 8.f, LOW = 3.f, DEEP = 60.f;
-    float m = -INFINITY, peak = -INFINITY;
-    // where m goes for a tile of maximum x; peak is the highest place m has had
-    __device__ __forceinline__ float place(float x) const
+    static constexpr float LIFT = F16 ? 7.f : 0.f, TOP = F16 ? 15.f : 8.f, LOW = 3.f, MOST = 70.f;
+    // whether a tile of maximum x moves m (a row without tokens so far has m -infinity: it does)
+    static __device__ __forceinline__ bool moves(float m, float x)
+    {
+        if constexpr (F16) return fabsf(x - m - (TOP - LOW) / 2) > (TOP + LOW) / 2;
+        else return x > m + TOP;
+    }
+    // where to; l: the row's weights so far, against m
+    static __device__ __forceinline__ float place(float m, float x, float l)
     {
         if (x > m + TOP) return x - LIFT;
         if constexpr (F16)
-            if (x < m - LOW && x > -INFINITY) return fmaxf(x - LIFT, peak - DEEP);
+            if (x < m - LOW && x > -INFINITY) return fminf(m, fmaxf(x - LIFT, m - MOST + log2f(l)));
         return m;
-    }
-    __device__ __forceinline__ void move(float to)
-    {
-        m = to;
-        if constexpr (F16) peak = fmaxf(peak, to);
     }
 };
 
@@ -174,8 +174,7 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) ldsm4(qf[ks], qs + v_off + ks * 32);
         }
-        float o[DT][4], l[2] = {0.f, 0.f};
-        Reference<F16> ref[2];
+        float o[DT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -233,15 +232,19 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
                     float x = fmaxf(fmaxf(s[0][0][2 * h], s[0][0][2 * h + 1]), fmaxf(s[0][1][2 * h], s[0][1][2 * h + 1]));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                    z[h] = ref[h].place(x);
-                    moves |= z[h] != ref[h].m;
+                    moves |= Reference<F16>::moves(m[h], x);
+                    z[h] = x;
                 }
                 if (__any_sync(0xFFFFFFFFu, moves)) {
                     float f[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        f[h] = ref[h].m == -INFINITY ? 0.f : ex2_approx(ref[h].m - z[h]);
-                        ref[h].move(z[h]);
+                        float sum = l[h];                  // of this lane's keys, then of the row's
+                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                        const float to = Reference<F16>::place(m[h], z[h], sum);
+                        f[h] = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - to);
+                        m[h] = to;
                         l[h] *= f[h];
                     }
 #pragma unroll
@@ -252,8 +255,8 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
                         o[d][3] *= f[1];
                     }
                 }
-                z[0] = ref[0].m == -INFINITY ? 0.f : ref[0].m;
-                z[1] = ref[1].m == -INFINITY ? 0.f : ref[1].m;
+                z[0] = m[0] == -INFINITY ? 0.f : m[0];
+                z[1] = m[1] == -INFINITY ? 0.f : m[1];
                 uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -299,14 +302,14 @@ __global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
                         if (d * 8 < a.hd)
                             *reinterpret_cast<uint32_t *>(out + d * 8 + col0) =
                                 pack_16x2<F16>(o[d][2 * h] * inv, o[d][2 * h + 1] * inv);
-                    if (a.lse && col0 == 0) a.lse[r] = (ref[h].m == -INFINITY ? 0.f : ref[h].m) * float(LN2) + logf(sum);
+                    if (a.lse && col0 == 0) a.lse[r] = (m[h] == -INFINITY ? 0.f : m[h]) * float(LN2) + logf(sum);
                 } else {
                     float *d0 = p.part + static_cast<int64_t>(i) * (a.hd + ATTN_ROW);
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
                         if (d * 8 < a.hd)
                             *reinterpret_cast<float2 *>(d0 + d * 8 + col0) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
-                    if (col0 == 0) *reinterpret_cast<float2 *>(d0 + a.hd) = make_float2(ref[h].m, sum);
+                    if (col0 == 0) *reinterpret_cast<float2 *>(d0 + a.hd) = make_float2(m[h], sum);
                 }
             }
         }
