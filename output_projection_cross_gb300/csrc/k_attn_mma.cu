@@ -114,207 +114,275 @@ template <int HDP_, int W_> struct Variant {
     static constexpr int QBYTES = W * 16 * RS;
     static constexpr int RING_BYTES = STAGES * 2 * TILE + QBYTES + 16 * W;
     static constexpr int SPACE = 227 * 1024 - BASE_BYTES;
-    static constexpr int MOST = HDP <= 64 ? 12 : HDP <= 128 ? 12 : 8;  // warps whose registers fit
+    // warps whose registers fit (9 of heads of 96 have 168 each, as 12 have, and spill: 33 ragged sequences 32 us, 8 25)
+    static constexpr int MOST = HDP <= 64 ? 12 : HDP <= 96 && W == 1 ? 8 : HDP <= 128 ? 12 : 8;
     static constexpr int RINGS = SPACE / RING_BYTES < MOST / W ? SPACE / RING_BYTES : MOST / W;
     static constexpr int THREADS = RINGS * W * 32;
 };
 
-template <typename V, bool F16>
-__global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(AttnArgs a)
+// Where a warp works: its ring's place in shared memory, its own masks of valid
+// tokens there, its number in the ring, and the ring's barrier.
+struct Seat {
+    uint32_t ring;
+    uint32_t *valid;
+    int sub, bar;
+};
+template <typename V> __device__ __forceinline__ void ring_sync(const Seat &at)
 {
-    constexpr int HDP = V::HDP, W = V::W, KT = V::KT, STAGES = V::STAGES, RS = V::RS;
+    if constexpr (V::W == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(at.bar), "n"(V::W * 32) : "memory");
+}
+// Whether x holds in any thread of the ring; a barrier, too.
+template <typename V> __device__ __forceinline__ bool ring_any(const Seat &at, bool x)
+{
+    if constexpr (V::W == 1) {
+        return __any_sync(0xFFFFFFFFu, x) != 0;
+    } else {
+        uint32_t r;
+        asm volatile("{\n\t.reg .pred p, q;\n\t"
+                     "setp.ne.u32 p, %1, 0;\n\t"
+                     "bar.red.or.pred q, %2, %3, p;\n\t"
+                     "selp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(r)
+                     : "r"(static_cast<uint32_t>(x)), "r"(at.bar), "n"(V::W * 32)
+                     : "memory");
+        return r != 0;
+    }
+}
+__device__ __forceinline__ float unless_nan(float x, float other) { return x == x ? x : other; }
+
+// One piece; returns whether one of this lane's outputs is NaN.
+// An infinite value times a weight's low part, which may be negative or 0, takes
+// from what its high part gave: NaN instead of infinity.  So a run that leaves a
+// NaN is walked once more with AGAIN, where every weight above 0 is 1, twice, and
+// what that gives is stored where a NaN was.
+template <typename V, bool F16, bool AGAIN>
+__device__ __forceinline__ bool attn_piece(const AttnArgs &a, const Piece &p, const Seat &at)
+{
+    constexpr int HDP = V::HDP, KT = V::KT, STAGES = V::STAGES, RS = V::RS;
     constexpr int KS = HDP / 16, NT = KT / 8, DT = HDP / 8;
     static_assert(KT == 16 && DT % 4 == 0, "one step of keys, column tiles in fours");
     constexpr uint32_t FULL = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ long long s_base[BASE_GROUPS + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ring_i = warp / W, sub = warp % W;
-    unsigned char *mine = smem + ring_i * V::RING_BYTES;
-    const uint32_t ring = smem_u32(mine), qs = ring + STAGES * 2 * V::TILE + sub * 16 * RS;
-    uint32_t *valid = reinterpret_cast<uint32_t *>(mine + STAGES * 2 * V::TILE + V::QBYTES) + 4 * sub;
-    auto ring_sync = [&] {
-        if constexpr (W == 1) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(1 + ring_i), "n"(W * 32) : "memory");
-    };
-    // the columns between the head's size and HDP are zero in every tile and stay so
-    if (a.hd != HDP) {
-        for (int i = sub * 32 + lane; i < V::RING_BYTES / 16; i += W * 32)
-            reinterpret_cast<uint4 *>(mine)[i] = make_uint4(0, 0, 0, 0);
-        ring_sync();
-    }
-    const long long *base = unit_bases(a, s_base);
+    const int lane = threadIdx.x & 31, sub = at.sub;
+    const uint32_t ring = at.ring, qs = ring + STAGES * 2 * V::TILE + sub * 16 * RS;
+    uint32_t *valid = at.valid;
     const int ch = a.hd >> 3;                              // 16-byte words of a row
     // matrix loads: K rows (tokens) lane % 8 + 8 (lane / 16), word (lane / 8) % 2; V and Q rows lane % 16, word lane / 16
     const uint32_t k_off = ((lane & 7) + ((lane >> 4) << 3)) * RS + ((lane >> 3) & 1) * 16;
     const uint32_t v_off = (lane & 15) * RS + (lane >> 4) * 16;
-    // rings are numbered across the blocks first, so that few units still use every SM
-    const int w = ring_i * gridDim.x + blockIdx.x;
-
-    walk_run(a, base, w, [&](const Piece &p) {
-        const int mine0 = sub * 16;                        // this warp's first row of the item
-        const bool active = mine0 < p.rows;
-        const int n_tiles = (p.t1 - p.t0 + KT - 1) / KT;
-        TileStream<V> in(a, p, sub, lane, ring, valid);
-        // the query rows, zeros past the last one, come with the first tile (loaded and stored one after the
-        // other: 132 instead of 105 us for 200 groups of 4 sequences of 120 to 320 tokens)
+    const int mine0 = sub * 16;                        // this warp's first row of the item
+    const bool active = mine0 < p.rows;
+    const int n_tiles = (p.t1 - p.t0 + KT - 1) / KT;
+    TileStream<V> in(a, p, sub, lane, ring, valid);
+    // the query rows, zeros past the last one, come with the first tile (loaded and stored one after the
+    // other: 132 instead of 105 us for 200 groups of 4 sequences of 120 to 320 tokens)
 #pragma unroll 4
-        for (int i = lane; i < 16 * (HDP / 8); i += 32) {
-            const int rr = i / (HDP / 8), cc = i % (HDP / 8);
-            const bool in_row = mine0 + rr < p.rows && cc < ch;
-            const uint16_t *from = static_cast<const uint16_t *>(a.q);
-            if (in_row)
-                from += row_seq(a, p, mine0 + rr) * a.q_stride + static_cast<int64_t>(row_head(a, p, mine0 + rr)) * a.hd + cc * 8;
-            cp16_or_zero(qs + rr * RS + cc * 16, from, in_row ? 16 : 0);
-        }
-        in.start(n_tiles);
-        cp_wait<STAGES - 2>();
-        __syncwarp();
-        uint32_t qf[V::QREG ? KS : 1][4];
-        if constexpr (V::QREG) {
+    for (int i = lane; i < 16 * (HDP / 8); i += 32) {
+        const int rr = i / (HDP / 8), cc = i % (HDP / 8);
+        const bool in_row = mine0 + rr < p.rows && cc < ch;
+        const uint16_t *from = static_cast<const uint16_t *>(a.q);
+        if (in_row)
+            from += row_seq(a, p, mine0 + rr) * a.q_stride + static_cast<int64_t>(row_head(a, p, mine0 + rr)) * a.hd + cc * 8;
+        cp16_or_zero(qs + rr * RS + cc * 16, from, in_row ? 16 : 0);
+    }
+    in.start(n_tiles);
+    cp_wait<STAGES - 2>();
+    __syncwarp();
+    uint32_t qf[V::QREG ? KS : 1][4];
+    if constexpr (V::QREG) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) ldsm4(qf[ks], qs + v_off + ks * 32);
-        }
-        float o[DT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int ks = 0; ks < KS; ++ks) ldsm4(qf[ks], qs + v_off + ks * 32);
+    }
+    float o[DT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
 
-        for (int i = 0; i < n_tiles; ++i) {
-            // once every warp of the ring is here, tile i has landed and tile i - 1's stage is free
-            cp_wait<STAGES - 2>();
-            ring_sync();
-            in.next(i, n_tiles);
-            const int st = i % STAGES;
-            if (active) {
-                const uint32_t kt = ring + st * 2 * V::TILE, vt = kt + V::TILE;
-                const uint32_t mask = valid[st];
-                // scores; even and odd steps add up apart: four sums in flight, not two
-                float s[2][NT][4];
+    for (int i = 0; i < n_tiles; ++i) {
+        // once every warp of the ring is here, tile i has landed and tile i - 1's stage is free
+        cp_wait<STAGES - 2>();
+        ring_sync<V>(at);
+        in.next(i, n_tiles);
+        const int st = i % STAGES;
+        if (active) {
+            const uint32_t kt = ring + st * 2 * V::TILE, vt = kt + V::TILE;
+            const uint32_t mask = valid[st];
+            // scores; even and odd steps add up apart: four sums in flight, not two
+            float s[2][NT][4];
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[x][j][e] = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t q4[4];
-                    if constexpr (V::QREG) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) q4[e] = qf[ks][e];
-                    } else {
-                        ldsm4(q4, qs + v_off + ks * 32);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; j += 2) {
-                        uint32_t b[4];
-                        ldsm4(b, kt + j * 8 * RS + k_off + ks * 32);
-                        mma16816<F16>(s[ks & 1][j], q4, b[0], b[1]);
-                        mma16816<F16>(s[ks & 1][j + 1], q4, b[2], b[3]);
-                    }
-                }
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[0][j][e] = (s[0][j][e] + s[1][j][e]) * a.scale_log2;
-                if (mask != FULL) {
+                    for (int e = 0; e < 4; ++e) s[x][j][e] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t q4[4];
+                if constexpr (V::QREG) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!((mask >> (j * 8 + (lane & 3) * 2 + (e & 1))) & 1u)) s[0][j][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) q4[e] = qf[ks][e];
+                } else {
+                    ldsm4(q4, qs + v_off + ks * 32);
                 }
-                float z[2];
-                bool moves = false;
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t b[4];
+                    ldsm4(b, kt + j * 8 * RS + k_off + ks * 32);
+                    mma16816<F16>(s[ks & 1][j], q4, b[0], b[1]);
+                    mma16816<F16>(s[ks & 1][j + 1], q4, b[2], b[3]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[0][j][e] = (s[0][j][e] + s[1][j][e]) * a.scale_log2;
+            if (mask != FULL) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((mask >> (j * 8 + (lane & 3) * 2 + (e & 1))) & 1u)) s[0][j][e] = -INFINITY;
+            }
+            float z[2];
+            bool moves = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x = fmaxf(fmaxf(s[0][0][2 * h], s[0][0][2 * h + 1]), fmaxf(s[0][1][2 * h], s[0][1][2 * h + 1]));
+                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                moves |= Reference<F16>::moves(m[h], x);
+                z[h] = x;
+            }
+            if (__any_sync(0xFFFFFFFFu, moves)) {
+                float f[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float x = fmaxf(fmaxf(s[0][0][2 * h], s[0][0][2 * h + 1]), fmaxf(s[0][1][2 * h], s[0][1][2 * h + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                    moves |= Reference<F16>::moves(m[h], x);
-                    z[h] = x;
+                    float sum = l[h];                  // of this lane's keys, then of the row's
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                    const float to = Reference<F16>::place(m[h], z[h], sum);
+                    f[h] = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - to);
+                    m[h] = to;
+                    l[h] *= f[h];
                 }
-                if (__any_sync(0xFFFFFFFFu, moves)) {
-                    float f[2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float sum = l[h];                  // of this lane's keys, then of the row's
-                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                        const float to = Reference<F16>::place(m[h], z[h], sum);
-                        f[h] = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - to);
-                        m[h] = to;
-                        l[h] *= f[h];
-                    }
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        o[d][0] *= f[0];
-                        o[d][1] *= f[0];
-                        o[d][2] *= f[1];
-                        o[d][3] *= f[1];
-                    }
+                for (int d = 0; d < DT; ++d) {
+                    o[d][0] *= f[0];
+                    o[d][1] *= f[0];
+                    o[d][2] *= f[1];
+                    o[d][3] *= f[1];
                 }
-                z[0] = m[0] == -INFINITY ? 0.f : m[0];
-                z[1] = m[1] == -INFINITY ? 0.f : m[1];
-                uint32_t ph[NT][2], pl[NT][2];
+            }
+            z[0] = m[0] == -INFINITY ? 0.f : m[0];
+            z[1] = m[1] == -INFINITY ? 0.f : m[1];
+            uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float x = ex2_approx(s[0][j][2 * h] - z[h]), y = ex2_approx(s[0][j][2 * h + 1] - z[h]);
-                        l[h] += x + y;
+                for (int h = 0; h < 2; ++h) {
+                    const float x = ex2_approx(s[0][j][2 * h] - z[h]), y = ex2_approx(s[0][j][2 * h + 1] - z[h]);
+                    l[h] += x + y;
+                    if constexpr (AGAIN) {
+                        ph[j][h] = pl[j][h] = pack_16x2<F16>(x > 0.f ? 1.f : x, y > 0.f ? 1.f : y);
+                    } else {
                         const uint32_t hi = pack_16x2<F16>(x, y);
                         ph[j][h] = hi;
                         pl[j][h] = pack_16x2<F16>(x - h16_lo<F16>(hi), y - h16_hi<F16>(hi));
                     }
-                // weights times values, two pairs of column tiles at a time: four sums in flight
-#pragma unroll
-                for (int d = 0; d < DT; d += 4) {
-                    uint32_t b[2][4];
-                    ldsm4_t(b[0], vt + v_off + d * 16);
-                    ldsm4_t(b[1], vt + v_off + (d + 2) * 16);
-                    const uint32_t hi[4] = {ph[0][0], ph[0][1], ph[1][0], ph[1][1]};
-                    const uint32_t lo[4] = {pl[0][0], pl[0][1], pl[1][0], pl[1][1]};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) mma16816<F16>(o[d + x], hi, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) mma16816<F16>(o[d + x], lo, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
                 }
+            // weights times values, two pairs of column tiles at a time: four sums in flight
+#pragma unroll
+            for (int d = 0; d < DT; d += 4) {
+                uint32_t b[2][4];
+                ldsm4_t(b[0], vt + v_off + d * 16);
+                ldsm4_t(b[1], vt + v_off + (d + 2) * 16);
+                const uint32_t hi[4] = {ph[0][0], ph[0][1], ph[1][0], ph[1][1]};
+                const uint32_t lo[4] = {pl[0][0], pl[0][1], pl[1][0], pl[1][1]};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma16816<F16>(o[d + x], hi, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma16816<F16>(o[d + x], lo, b[x >> 1][2 * (x & 1)], b[x >> 1][2 * (x & 1) + 1]);
             }
         }
-        cp_wait<0>();
-        if (active) {
+    }
+    cp_wait<0>();
+    bool none = false;                                     // whether one of this warp's outputs is NaN
+    if (active) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float sum = l[h];
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                const int i = mine0 + h * 8 + (lane >> 2);
-                if (i >= p.rows) continue;
-                const int col0 = (lane & 3) * 2;
-                if (p.slot < 0) {
-                    const float inv = sum > 0.f ? 1.f / sum : 1.f;
-                    const int64_t r = static_cast<int64_t>(row_seq(a, p, i)) * a.n_q + row_head(a, p, i);
-                    uint16_t *out = static_cast<uint16_t *>(a.out) + r * a.hd;
+        for (int h = 0; h < 2; ++h) {
+            float sum = l[h];
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+            const int i = mine0 + h * 8 + (lane >> 2);
+            if (i >= p.rows) continue;
+            const int col0 = (lane & 3) * 2;
 #pragma unroll
-                    for (int d = 0; d < DT; ++d)
-                        if (d * 8 < a.hd)
-                            *reinterpret_cast<uint32_t *>(out + d * 8 + col0) =
-                                pack_16x2<F16>(o[d][2 * h] * inv, o[d][2 * h + 1] * inv);
-                    if (a.lse && col0 == 0) a.lse[r] = (m[h] == -INFINITY ? 0.f : m[h]) * float(LN2) + logf(sum);
-                } else {
-                    float *d0 = p.part + static_cast<int64_t>(i) * (a.hd + ATTN_ROW);
+            for (int d = 0; d < DT; ++d) none |= o[d][2 * h] != o[d][2 * h] || o[d][2 * h + 1] != o[d][2 * h + 1];
+            if (p.slot < 0) {
+                const float inv = sum > 0.f ? 1.f / sum : 1.f;
+                const int64_t r = static_cast<int64_t>(row_seq(a, p, i)) * a.n_q + row_head(a, p, i);
+                uint16_t *out = static_cast<uint16_t *>(a.out) + r * a.hd;
 #pragma unroll
-                    for (int d = 0; d < DT; ++d)
-                        if (d * 8 < a.hd)
-                            *reinterpret_cast<float2 *>(d0 + d * 8 + col0) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
-                    if (col0 == 0) *reinterpret_cast<float2 *>(d0 + a.hd) = make_float2(m[h], sum);
-                }
+                for (int d = 0; d < DT; ++d)
+                    if (d * 8 < a.hd) {
+                        uint32_t *to = reinterpret_cast<uint32_t *>(out + d * 8 + col0);
+                        float x = o[d][2 * h] * inv, y = o[d][2 * h + 1] * inv;
+                        if constexpr (AGAIN) {
+                            x = unless_nan(h16_lo<F16>(*to), x);
+                            y = unless_nan(h16_hi<F16>(*to), y);
+                        }
+                        *to = pack_16x2<F16>(x, y);
+                    }
+                if (a.lse && col0 == 0) a.lse[r] = (m[h] == -INFINITY ? 0.f : m[h]) * float(LN2) + logf(sum);
+            } else {
+                float *d0 = p.part + static_cast<int64_t>(i) * (a.hd + ATTN_ROW);
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    if (d * 8 < a.hd) {
+                        float2 *to = reinterpret_cast<float2 *>(d0 + d * 8 + col0);
+                        float2 x = make_float2(o[d][2 * h], o[d][2 * h + 1]);
+                        if constexpr (AGAIN) x = make_float2(unless_nan(to->x, x.x), unless_nan(to->y, x.y));
+                        *to = x;
+                    }
+                if (col0 == 0) *reinterpret_cast<float2 *>(d0 + a.hd) = make_float2(m[h], sum);
             }
         }
-        ring_sync();
-    });
+    }
+    ring_sync<V>(at);
+    return none;
+}
+
+// (a function of its own, so that its registers are not the first walk's; with a piece at a time walked
+// again, what it needs stayed in registers throughout the first walk)
+template <typename V, bool F16>
+__device__ __noinline__ void attn_run_again(const AttnArgs &a, const long long *base, int w, Seat at)
+{
+    walk_run(a, base, w, [&](const Piece &p) { attn_piece<V, F16, true>(a, p, at); });
+}
+
+template <typename V, bool F16>
+__global__ void __launch_bounds__(V::THREADS, 1) attn_mma_kernel(const __grid_constant__ AttnArgs a)
+{
+    constexpr int W = V::W;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ long long s_base[BASE_GROUPS + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ring_i = warp / W, sub = warp % W;
+    unsigned char *mine = smem + ring_i * V::RING_BYTES;
+    const Seat at{smem_u32(mine), reinterpret_cast<uint32_t *>(mine + V::STAGES * 2 * V::TILE + V::QBYTES) + 4 * sub, sub,
+                  1 + ring_i};
+    // the columns between the head's size and HDP are zero in every tile and stay so
+    if (a.hd != V::HDP) {
+        for (int i = sub * 32 + lane; i < V::RING_BYTES / 16; i += W * 32)
+            reinterpret_cast<uint4 *>(mine)[i] = make_uint4(0, 0, 0, 0);
+        ring_sync<V>(at);
+    }
+    const long long *base = unit_bases(a, s_base);
+    // rings are numbered across the blocks first, so that few units still use every SM
+    const int w = ring_i * gridDim.x + blockIdx.x;
+    bool none = false;
+    walk_run(a, base, w, [&](const Piece &p) { none |= attn_piece<V, F16, false>(a, p, at); });
+    if (ring_any<V>(at, none)) attn_run_again<V, F16>(a, base, w, at);
 }
 
 template <int HDP, int W> cudaError_t launch_variant(bool f16, const AttnArgs &a, cudaStream_t st)

@@ -104,3 +104,67 @@ def test_large_values_under_a_small_weight(L, d):
     v *= 40000.0
     s[0], v[:16] = d, 0.0
     check(L, s, np.floor(v), "f16", 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hq,kv,hd,share,lens", [
+    (4, 2, 64, 1, [1, 37, 300, 16]), (40, 2, 128, 1, [200, 5, 90]), (80, 1, 72, 1, [130, 33]),
+    (8, 2, 96, 4, [150, 150, 170, 149]), (3, 3, 200, 1, [64, 9000]), (8, 1, 256, 2, [70, 75])])
+def test_infinite_values(L, dtype, hq, kv, hd, share, lens):
+    """A value of infinity under a positive weight is infinity, under both signs of it no number; what the
+    other columns hold is what it was."""
+    rng = np.random.default_rng([hq, hd])
+    S, dt = len(lens), DTYPES[dtype]
+    used = [-(-n // PAGE) for n in lens]
+    table = np.full((S, max(used)), -1, np.int32)
+    table[:] = np.arange(max(used))
+    if share == 1:
+        for s in range(S):
+            table[s] += sum(used[:s])
+    n_pages = int(table.max()) + 1
+    k = torch.from_numpy(rng.standard_normal((n_pages, PAGE, kv, hd))).cuda().to(dt)
+    v = torch.from_numpy(rng.standard_normal((n_pages, PAGE, kv, hd))).cuda().to(dt)
+    q = torch.from_numpy(rng.standard_normal((S, hq, hd))).cuda().to(dt)
+    t, n = torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    inf = float("inf")
+    for page in range(0, n_pages, 3):
+        v[page, 0, :, 0:4] = inf
+        v[page, 3, :, 4:6] = -inf
+        v[page, 0, :, 6], v[page, 9, :, 6] = inf, -inf
+        v[page, 2, 0, 7] = float("nan")
+        v[page, 15, :, hd - 1] = inf
+    for window in (0, 20):
+        ws = L.decode_workspace(L.KIND_PAGED_ATTN, S, hq, kv, hd)
+        lse = torch.empty((S, hq), device="cuda")
+        out = L.lossk_paged_attn(q, k, v, t, n, share=share, window=window, lse_out=lse, ws=ws)
+        assert L.lossk_device_status(ws) == 580
+        with np.errstate(invalid="ignore"):
+            args = table, lens, PAGE, hd ** -0.5, window
+            r, rl = ref.attend(*(x.double().cpu().numpy() for x in (q, k, v)), *args)
+            mean, _ = ref.attend(*(x.double().cpu().numpy() for x in (q, k, v.abs())), *args)
+        assert np.isposinf(r).any() and np.isfinite(r).any() and (window or np.isneginf(r).any() and np.isnan(r).any())
+        got = out.double().cpu().numpy()
+        fin = np.isfinite(r)
+        np.testing.assert_array_equal(got[~fin], r[~fin])
+        x_err = 2.0 ** -24 * (40 * (hd / 8 + 8) + 64)
+        bound = torch.finfo(dt).eps / 2 * np.abs(r[fin]) + x_err * mean[fin] + (2.0 ** -24 if dtype == "f16" else 0)
+        assert (np.abs(got[fin] - r[fin]) <= bound).all()
+        assert (np.abs(lse.double().cpu().numpy() - rl) <= 2.0 ** -24 * np.abs(rl) + x_err).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_infinite_keys(L, dtype):
+    """A key that makes a score -infinity takes its token out."""
+    rng = np.random.default_rng(5)
+    dt = DTYPES[dtype]
+    k, v = (torch.from_numpy(rng.standard_normal((5, PAGE, 2, 64))).cuda().to(dt) for _ in range(2))
+    q = torch.from_numpy(rng.uniform(0.5, 1.5, (1, 4, 64))).cuda().to(dt)
+    table = torch.arange(5, dtype=torch.int32, device="cuda")[None]
+    k[1, 4, :, 3] = -float("inf")
+    k[3, :, :, 9] = -float("inf")
+    out = L.lossk_paged_attn(q, k, v, table, torch.tensor([75], dtype=torch.int32, device="cuda"))
+    r, _ = ref.attend(*(x.double().cpu().numpy() for x in (q, k, v)), table.cpu().numpy(), [75], PAGE, 0.125)
+    mean, _ = ref.attend(*(x.double().cpu().numpy() for x in (q, k, v.abs())), table.cpu().numpy(), [75], PAGE, 0.125)
+    x_err = 2.0 ** -24 * (40 * (64 / 8 + 8) + 64)
+    bound = torch.finfo(dt).eps / 2 * np.abs(r) + x_err * mean + (2.0 ** -24 if dtype == "f16" else 0)
+    assert (np.abs(out.double().cpu().numpy() - r) <= bound).all()
