@@ -1,6 +1,7 @@
 // lossk_calls.cpp -- the decoding calls as a CPython module: arguments by
 // position, in the order of lossk.h, None for NULL, the status returned.  And
-// spans(), the checks and addresses of the tensors that such a call takes.
+// spans() and device(), the checks and addresses of the tensors that such a call
+// takes.
 //
 // A decoding step makes several of these calls per layer, of 13 to 30
 // arguments each; through ctypes such a call took 2 us for its arguments
@@ -80,7 +81,7 @@ LOSSK_CALLS(X)
 #undef X
 
 // Attributes and methods of a tensor.
-PyObject *s_is_cuda, *s_dtype, *s_is_contiguous, *s_data_ptr, *s_numel;
+PyObject *s_is_cuda, *s_dtype, *s_is_contiguous, *s_data_ptr, *s_numel, *s_get_device;
 
 // Whether an attribute (or what a method returns) is the object `want`.
 bool is(PyObject *got, PyObject *want)
@@ -124,6 +125,24 @@ PyObject *spans(PyObject *, PyObject *const *a, Py_ssize_t n)
     return r;
 }
 
+// device(t0, t1, ...): the index of the GPU that the tensors (None left out) are
+// on; -1 where one is on none or on another than those before it.
+PyObject *device(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    long all = -1;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (a[i] == Py_None) continue;
+        PyObject *got = PyObject_CallMethodNoArgs(a[i], s_get_device);
+        if (!got) return nullptr;
+        const long index = PyLong_AsLong(got);
+        Py_DECREF(got);
+        if (index == -1 && PyErr_Occurred()) return nullptr;
+        if (index < 0 || (all >= 0 && index != all)) return PyLong_FromLong(-1);
+        all = index;
+    }
+    return PyLong_FromLong(all);
+}
+
 // load(path): the library's functions.
 PyObject *load(PyObject *, PyObject *path)
 {
@@ -150,6 +169,7 @@ PyObject *load(PyObject *, PyObject *path)
 PyMethodDef methods[] = {
     {"load", load, METH_O, nullptr},
     {"spans", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(spans)), METH_FASTCALL, nullptr},
+    {"device", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(device)), METH_FASTCALL, nullptr},
 #define X(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr},
     LOSSK_CALLS(X)
 #undef X
@@ -165,7 +185,8 @@ PyMODINIT_FUNC PyInit__lossk_calls(void)
                                                           {&s_dtype, "dtype"},
                                                           {&s_is_contiguous, "is_contiguous"},
                                                           {&s_data_ptr, "data_ptr"},
-                                                          {&s_numel, "numel"}};
+                                                          {&s_numel, "numel"},
+                                                          {&s_get_device, "get_device"}};
     for (const auto &x : names)
         if (!(*x.first = PyUnicode_InternFromString(x.second))) return nullptr;
     return PyModule_Create(&module);

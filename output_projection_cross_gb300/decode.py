@@ -6,7 +6,8 @@ and raises :class:`LosskError` for any status other than 580.  These calls do
 not synchronise: ids and lengths are checked on the device, and what was found
 wrong there is read with ``lossk_device_status(ws)``.  So a decoding loop keeps
 a workspace (:func:`decode_workspace`) and its output tensors and passes them
-in; both are created here when left out.
+in; both are created here when left out.  All of a call's tensors have to be on
+the current device (``ValueError`` otherwise).
 """
 from __future__ import annotations
 
@@ -58,20 +59,28 @@ def decode_workspace(kind: int, a: int, b: int, c: int = 0, d: int = 0, device=N
 # These calls take microseconds, so the checks below are kept to attribute reads: a decoding step
 # makes several calls per layer, and building a stream object alone takes 3 us.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream_of(t, stream):
-    """The CUDA stream handle: the given stream's, or the current one of t's device."""
+def _stream_of(stream, *tensors):
+    """The CUDA stream handle, the given stream's or the current one, of a call on these tensors (None
+    left out).  Launches go to the current device, so tensors and stream have to be on it."""
+    index = _calls.device(*tensors)
+    if index < 0 or index != _current_device() or (stream is not None and stream.device_index != index):
+        on = sorted({str(t.device) for t in tensors if t is not None})
+        raise ValueError(f"the tensors (on {', '.join(on)}), workspace among them, and the stream must be on the "
+                         f"current CUDA device")
     if stream is not None or _raw_stream is None:
         return _stream(stream)
-    return _raw_stream(t.get_device())
+    return _raw_stream(index)
 
 
 def _on_gpu(t, name, dtype=None, contiguous=True):
+    # (that it is on the GPU is seen to for all tensors of a call together, in _stream_of)
     if t is None:
         return
-    if not t.is_cuda or (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}CUDA tensor")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
 
@@ -82,6 +91,7 @@ def _ints(names, *tensors):
     if r is None:
         for t, name in zip(tensors, names):
             _on_gpu(t, name, _int32)
+        raise ValueError(f"{', '.join(names)} must be CUDA tensors")
     return r
 
 
@@ -158,11 +168,13 @@ def lossk_beam_select(logits, scores, n_out, temperature=1.0, allow=None, finish
         raise ValueError("lse_out must hold one value per row of logits")
     if ws is None:
         ws = decode_workspace(KIND_BEAM_SELECT, batch, beams, V, n_out, logits.device)
+    stream = _stream_of(stream, logits, scores, allow, finished, lengths, parent, token, score, done, length,
+                        lse_out, ws)
     st = _calls.lossk_beam_select(batch, beams, V, n_out, _dtype_code(logits), logits.data_ptr(), _span(logits),
                                logits.stride(0) if rows > 1 else max(V, 1), scores.data_ptr(), rows, temperature,
                                _ptr(allow), _len(allow), allow_stride, _ptr(finished), end_token, _ptr(lengths),
                                length_alpha, parent.data_ptr(), token.data_ptr(), score.data_ptr(), done.data_ptr(),
-                               length.data_ptr(), _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream_of(logits, stream))
+                               length.data_ptr(), _ptr(lse_out), ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_beam_select")
     return out
 
@@ -181,9 +193,10 @@ def lossk_beam_gather(src, parent, dst=None, ws=None, stream=None):
     row = src.numel() * src.element_size() // max(G * n_src, 1)
     if ws is None:
         ws = torch.zeros(256, dtype=torch.uint8, device=src.device)
+    stream = _stream_of(stream, parent, src, dst, ws)
     st = _calls.lossk_beam_gather(G, n_src, n_dst, row, parent.data_ptr(), parent.numel(), src.data_ptr(),
                                src.numel() * src.element_size(), dst.data_ptr(), dst.numel() * dst.element_size(),
-                               ws.data_ptr(), ws.numel(), _stream_of(src, stream))
+                               ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_beam_gather")
     return dst
 
@@ -235,9 +248,10 @@ def lossk_cache_fork(parent, table, lens, ref, page_size, table_out=None, lens_o
         raise ValueError("table_out must be [groups * n_dst, max_pages]")
     if ws is None:
         ws = decode_workspace(KIND_CACHE, max(n, no), pages, device=table.device)
+    stream = _stream_of(stream, parent, table, lens, ref, table_out, lens_out, ws)
     st = _calls.lossk_cache_fork(G, n // G, n_dst, m, page_size, pages, parents, parents_len, table.data_ptr(),
                                  table_len, stride, lengths, n, refs, pages, table_out.data_ptr(), out_len,
-                                 stride_out, outs, outs_len, ws.data_ptr(), ws.numel(), _stream_of(table, stream))
+                                 stride_out, outs, outs_len, ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_cache_fork")
     return table_out, lens_out
 
@@ -250,9 +264,10 @@ def lossk_cache_reserve(table, lens, ref, pool, page_size, n_new=1, ws=None, str
     P = _pool(pool, pages)
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+    stream = _stream_of(stream, each, table, lens, ref, pool, ws)
     st = _calls.lossk_cache_reserve(n, m, page_size, pages, 0 if each is not None else n_new, new, new_len,
                                     table.data_ptr(), table_len, stride, lengths, lengths_len, refs, pages, *P,
-                                    ws.data_ptr(), ws.numel(), _stream_of(table, stream))
+                                    ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_cache_reserve")
 
 
@@ -263,9 +278,10 @@ def lossk_cache_free(table, lens, ref, page_size, drop=None, ws=None, stream=Non
     n, m, stride, table_len = _table(table)
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+    stream = _stream_of(stream, drop, table, lens, ref, ws)
     st = _calls.lossk_cache_free(n, m, page_size, pages, _ptr(drop), _len(drop), table.data_ptr(), table_len, stride,
                                  lengths, lengths_len, refs, pages, ws.data_ptr(), ws.numel(),
-                                 _stream_of(table, stream))
+                                 stream)
     _check(st, "lossk_cache_free")
 
 
@@ -284,9 +300,10 @@ def lossk_cache_compact(table, lens, ref, pool, page_size, table_out=None, ref_o
         raise ValueError("table_out must be shaped like table, n_live_out hold one value")
     if ws is None:
         ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+    stream = _stream_of(stream, table, lens, ref, table_out, ref_out, n_live_out, pool, ws)
     st = _calls.lossk_cache_compact(n, m, page_size, pages, table.data_ptr(), table_len, stride, lengths,
                                     lengths_len, refs, pages, table_out.data_ptr(), out_len, stride_out, refs_out,
-                                    refs_out_len, live, *P, ws.data_ptr(), ws.numel(), _stream_of(table, stream))
+                                    refs_out_len, live, *P, ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_cache_compact")
     return table_out, ref_out, n_live_out
 
@@ -299,8 +316,9 @@ def lossk_cache_copy(src, dst, pool, ws=None, stream=None) -> None:
     if src.numel() != dst.numel():
         raise ValueError("src and dst must list as many pages")
     ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=pool.device)
+    stream = _stream_of(stream, src, dst, pool, ws)
     st = _calls.lossk_cache_copy(src.numel(), pool.shape[1], src.data_ptr(), src.numel(), dst.data_ptr(), dst.numel(),
-                              *P, ws.data_ptr(), ws.numel(), _stream_of(pool, stream))
+                              *P, ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_cache_copy")
 
 
@@ -331,11 +349,12 @@ def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, w
         raise ValueError("k_new and v_new must be laid out alike")
     n_tok = shape[0]
     ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=table.device)
+    stream = _stream_of(stream, k_new, v_new, k_pages, v_pages, table, lens, first, ws)
     st = _calls.lossk_cache_write(n_tok, n, kv, hd, m, page, n_pages, _dtype_code(k_pages), k_new.data_ptr(),
                                v_new.data_ptr(), _span(k_new), strides[0] if n_tok > 1 else kv * hd,
                                k_pages.data_ptr(), v_pages.data_ptr(), pages_len, sp, stok, sh,
                                table.data_ptr(), table_len, stride, lengths, lengths_len, firsts, firsts_len,
-                               ws.data_ptr(), ws.numel(), _stream_of(table, stream))
+                               ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_cache_write")
 
 
@@ -362,10 +381,11 @@ def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, sha
         raise ValueError("lse_out must be [n_seq, n_q_heads]")
     if ws is None:
         ws = decode_workspace(KIND_PAGED_ATTN, n, hq, kv, hd, q.device)
+    stream = _stream_of(stream, q, k_pages, v_pages, table, lens, out, lse_out, ws)
     st = _calls.lossk_paged_attn(n, hq, kv, hd, m, page, n_pages, share, _dtype_code(q), q.data_ptr(), _span(q),
                               strides[0] if n > 1 else hq * hd, k_pages.data_ptr(), v_pages.data_ptr(), pages_len,
                               sp, stok, sh, table.data_ptr(), table_len, stride, lengths, lengths_len,
                               max_len, window, hd ** -0.5 if scale is None else scale, out.data_ptr(), out.numel(),
-                              _ptr(lse_out), ws.data_ptr(), ws.numel(), _stream_of(q, stream))
+                              _ptr(lse_out), ws.data_ptr(), ws.numel(), stream)
     _check(st, "lossk_paged_attn")
     return out
