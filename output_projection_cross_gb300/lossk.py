@@ -158,6 +158,9 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _contig(t, name):
     if t is not None and (not t.is_cuda or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t is not None and t.get_device() != torch.cuda.current_device():
+        # (launches go to the current device, where another's addresses mean nothing)
+        raise ValueError(f"{name} must be on the current CUDA device")
     return t
 
 
@@ -211,7 +214,7 @@ def lossk_targets_check(targets, vocab, ws=None, stream=None) -> int:
 
 
 def _ws(ws, kind, n, d, V, dtype, dev):
-    return ws if ws is not None else workspace(kind, n, d, V, dtype, dev)
+    return _contig(ws, "ws") if ws is not None else workspace(kind, n, d, V, dtype, dev)
 
 
 def lossk_ce_fwd(hidden, weight, targets, loss_mask=None, chunk=None, z_weight=0.0, lse_out=None,
