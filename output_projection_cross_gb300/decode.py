@@ -75,6 +75,18 @@ def _stream_of(stream, *tensors):
     return _raw_stream(index)
 
 
+# What a call makes for itself it makes on its stream: zeroed there before the call's kernels, and, once
+# it is dropped, its memory handed on to that stream's work alone, which comes after them.
+def _new(stream, shape, dtype, device, zeros=False):
+    with torch.cuda.stream(stream):
+        return (torch.zeros if zeros else torch.empty)(shape, dtype=dtype, device=device)
+
+
+def _new_workspace(stream, device, kind, *sizes):
+    with torch.cuda.stream(stream):
+        return decode_workspace(kind, *sizes, device=device)
+
+
 def _on_gpu(t, name, dtype=None, contiguous=True):
     # (that it is on the GPU is seen to for all tensors of a call together, in _stream_of)
     if t is None:
@@ -153,7 +165,8 @@ def lossk_beam_select(logits, scores, n_out, temperature=1.0, allow=None, finish
                 raise ValueError("allow must hold one mask, or one per row of logits")
             allow_stride = allow.shape[1]
     if out is None:
-        out = beam_buffers(batch, n_out, logits.device)
+        with torch.cuda.stream(stream):
+            out = beam_buffers(batch, n_out, logits.device)
     parent, token, score, done, length = out["parent"], out["token"], out["score"], out["finished"], out["length"]
     _on_gpu(parent, "parent", torch.int32)
     _on_gpu(token, "token", torch.int64)
@@ -167,7 +180,7 @@ def lossk_beam_select(logits, scores, n_out, temperature=1.0, allow=None, finish
     if lse_out is not None and lse_out.numel() != rows:
         raise ValueError("lse_out must hold one value per row of logits")
     if ws is None:
-        ws = decode_workspace(KIND_BEAM_SELECT, batch, beams, V, n_out, logits.device)
+        ws = _new_workspace(stream, logits.device, KIND_BEAM_SELECT, batch, beams, V, n_out)
     stream = _stream_of(stream, logits, scores, allow, finished, lengths, parent, token, score, done, length,
                         lse_out, ws)
     st = _calls.lossk_beam_select(batch, beams, V, n_out, _dtype_code(logits), logits.data_ptr(), _span(logits),
@@ -188,11 +201,11 @@ def lossk_beam_gather(src, parent, dst=None, ws=None, stream=None):
     G, n_src = src.shape[:2]
     n_dst = parent.shape[1]
     if dst is None:
-        dst = torch.empty((G, n_dst) + tuple(src.shape[2:]), dtype=src.dtype, device=src.device)
+        dst = _new(stream, (G, n_dst) + tuple(src.shape[2:]), src.dtype, src.device)
     _on_gpu(dst, "dst", src.dtype)
     row = src.numel() * src.element_size() // max(G * n_src, 1)
     if ws is None:
-        ws = torch.zeros(256, dtype=torch.uint8, device=src.device)
+        ws = _new(stream, 256, torch.uint8, src.device, zeros=True)
     stream = _stream_of(stream, parent, src, dst, ws)
     st = _calls.lossk_beam_gather(G, n_src, n_dst, row, parent.data_ptr(), parent.numel(), src.data_ptr(),
                                src.numel() * src.element_size(), dst.data_ptr(), dst.numel() * dst.element_size(),
@@ -235,19 +248,19 @@ def lossk_cache_fork(parent, table, lens, ref, page_size, table_out=None, lens_o
     """parent int32 [groups, n_dst]; table holds groups * n_src rows.  Returns (table_out, lens_out)."""
     G, n_dst = parent.shape
     if lens_out is None:
-        lens_out = torch.empty(G * n_dst, dtype=torch.int32, device=table.device)
+        lens_out = _new(stream, G * n_dst, torch.int32, table.device)
     parents, parents_len, lengths, lengths_len, refs, pages, outs, outs_len = _ints(
         ("parent", "lens", "ref", "lens_out"), parent, lens, ref, lens_out)
     n, m, stride, table_len = _table(table)
     if n % G or lengths_len != n:
         raise ValueError(f"{n} rows and {lengths_len} lengths in {G} groups")
     if table_out is None:
-        table_out = torch.empty((G * n_dst, m), dtype=torch.int32, device=table.device)
+        table_out = _new(stream, (G * n_dst, m), torch.int32, table.device)
     no, mo, stride_out, out_len = _table(table_out, "table_out")
     if no != G * n_dst or mo != m:
         raise ValueError("table_out must be [groups * n_dst, max_pages]")
     if ws is None:
-        ws = decode_workspace(KIND_CACHE, max(n, no), pages, device=table.device)
+        ws = _new_workspace(stream, table.device, KIND_CACHE, max(n, no), pages)
     stream = _stream_of(stream, parent, table, lens, ref, table_out, lens_out, ws)
     st = _calls.lossk_cache_fork(G, n // G, n_dst, m, page_size, pages, parents, parents_len, table.data_ptr(),
                                  table_len, stride, lengths, n, refs, pages, table_out.data_ptr(), out_len,
@@ -263,7 +276,7 @@ def lossk_cache_reserve(table, lens, ref, pool, page_size, n_new=1, ws=None, str
     n, m, stride, table_len = _table(table)
     P = _pool(pool, pages)
     if ws is None:
-        ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+        ws = _new_workspace(stream, table.device, KIND_CACHE, n, pages)
     stream = _stream_of(stream, each, table, lens, ref, pool, ws)
     st = _calls.lossk_cache_reserve(n, m, page_size, pages, 0 if each is not None else n_new, new, new_len,
                                     table.data_ptr(), table_len, stride, lengths, lengths_len, refs, pages, *P,
@@ -277,7 +290,7 @@ def lossk_cache_free(table, lens, ref, page_size, drop=None, ws=None, stream=Non
     _on_gpu(drop, "drop", torch.uint8)
     n, m, stride, table_len = _table(table)
     if ws is None:
-        ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+        ws = _new_workspace(stream, table.device, KIND_CACHE, n, pages)
     stream = _stream_of(stream, drop, table, lens, ref, ws)
     st = _calls.lossk_cache_free(n, m, page_size, pages, _ptr(drop), _len(drop), table.data_ptr(), table_len, stride,
                                  lengths, lengths_len, refs, pages, ws.data_ptr(), ws.numel(),
@@ -288,18 +301,18 @@ def lossk_cache_free(table, lens, ref, page_size, drop=None, ws=None, stream=Non
 def lossk_cache_compact(table, lens, ref, pool, page_size, table_out=None, ref_out=None, n_live_out=None, ws=None,
                         stream=None):
     """Returns (table_out, ref_out, n_live_out); the pool's live pages are in front then."""
-    ref_out = ref_out if ref_out is not None else torch.empty_like(ref)
-    n_live_out = n_live_out if n_live_out is not None else ref.new_empty(1)
+    ref_out = ref_out if ref_out is not None else _new(stream, ref.shape, torch.int32, ref.device)
+    n_live_out = n_live_out if n_live_out is not None else _new(stream, 1, torch.int32, ref.device)
     lengths, lengths_len, refs, pages, refs_out, refs_out_len, live, live_len = _ints(
         ("lens", "ref", "ref_out", "n_live_out"), lens, ref, ref_out, n_live_out)
     n, m, stride, table_len = _table(table)
     P = _pool(pool, pages)
-    table_out = table_out if table_out is not None else table.new_empty((n, m))
+    table_out = table_out if table_out is not None else _new(stream, (n, m), torch.int32, table.device)
     no, mo, stride_out, out_len = _table(table_out, "table_out")
     if no != n or mo != m or live_len < 1:
         raise ValueError("table_out must be shaped like table, n_live_out hold one value")
     if ws is None:
-        ws = decode_workspace(KIND_CACHE, n, pages, device=table.device)
+        ws = _new_workspace(stream, table.device, KIND_CACHE, n, pages)
     stream = _stream_of(stream, table, lens, ref, table_out, ref_out, n_live_out, pool, ws)
     st = _calls.lossk_cache_compact(n, m, page_size, pages, table.data_ptr(), table_len, stride, lengths,
                                     lengths_len, refs, pages, table_out.data_ptr(), out_len, stride_out, refs_out,
@@ -315,7 +328,7 @@ def lossk_cache_copy(src, dst, pool, ws=None, stream=None) -> None:
     P = _pool(pool, pool.shape[1])
     if src.numel() != dst.numel():
         raise ValueError("src and dst must list as many pages")
-    ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=pool.device)
+    ws = ws if ws is not None else _new(stream, 256, torch.uint8, pool.device, zeros=True)
     stream = _stream_of(stream, src, dst, pool, ws)
     st = _calls.lossk_cache_copy(src.numel(), pool.shape[1], src.data_ptr(), src.numel(), dst.data_ptr(), dst.numel(),
                               *P, ws.data_ptr(), ws.numel(), stream)
@@ -348,7 +361,7 @@ def lossk_cache_write(k_new, v_new, k_pages, v_pages, table, lens, first=None, w
     if shape != v_new.shape or strides != v_new.stride():
         raise ValueError("k_new and v_new must be laid out alike")
     n_tok = shape[0]
-    ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=table.device)
+    ws = ws if ws is not None else _new(stream, 256, torch.uint8, table.device, zeros=True)
     stream = _stream_of(stream, k_new, v_new, k_pages, v_pages, table, lens, first, ws)
     st = _calls.lossk_cache_write(n_tok, n, kv, hd, m, page, n_pages, _dtype_code(k_pages), k_new.data_ptr(),
                                v_new.data_ptr(), _span(k_new), strides[0] if n_tok > 1 else kv * hd,
@@ -374,13 +387,13 @@ def lossk_paged_attn(q, k_pages, v_pages, table, lens, scale=None, window=0, sha
         raise ValueError("q must be [n_seq, n_q_heads, head_dim] with contiguous sequences")
     hq = shape[1]
     if out is None:
-        out = torch.empty((n, hq, hd), dtype=q.dtype, device=q.device)
+        out = _new(stream, (n, hq, hd), q.dtype, q.device)
     _on_gpu(out, "out", q.dtype)
     _on_gpu(lse_out, "lse_out", torch.float32)
     if lse_out is not None and lse_out.numel() != n * hq:
         raise ValueError("lse_out must be [n_seq, n_q_heads]")
     if ws is None:
-        ws = decode_workspace(KIND_PAGED_ATTN, n, hq, kv, hd, q.device)
+        ws = _new_workspace(stream, q.device, KIND_PAGED_ATTN, n, hq, kv, hd)
     stream = _stream_of(stream, q, k_pages, v_pages, table, lens, out, lse_out, ws)
     st = _calls.lossk_paged_attn(n, hq, kv, hd, m, page, n_pages, share, _dtype_code(q), q.data_ptr(), _span(q),
                               strides[0] if n > 1 else hq * hd, k_pages.data_ptr(), v_pages.data_ptr(), pages_len,

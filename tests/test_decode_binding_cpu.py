@@ -115,3 +115,48 @@ def test_a_stream_of_another_gpu(name):
         call(name, stub, dict(rest, stream=types.SimpleNamespace(cuda_stream=0, device_index=0)))
     with pytest.raises(ValueError):
         call(name, stub, dict(rest, stream=types.SimpleNamespace(cuda_stream=0, device_index=1)))
+
+
+# what each call makes where it is left out
+MADE = {"lossk_beam_select": ["ws", "out_"], "lossk_beam_gather": ["ws", "dst"],
+        "lossk_cache_fork": ["ws", "table_out", "lens_out"], "lossk_cache_reserve": ["ws"], "lossk_cache_free": ["ws"],
+        "lossk_cache_compact": ["ws", "table_out", "ref_out", "n_live_out"], "lossk_cache_copy": ["ws"],
+        "lossk_cache_write": ["ws"], "lossk_paged_attn": ["ws", "out"]}
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_what_a_call_makes_is_made_on_its_stream(name, monkeypatch):
+    """Made on the current stream, a workspace would be zeroed there while the call runs on its own, and its
+    memory given to the current stream's next allocation while the call still uses it."""
+    side = types.SimpleNamespace(cuda_stream=0, device_index=0)
+    current, made = [None], []
+
+    class Stream:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    def maker(make):
+        def f(*args, device=None, **kw):
+            made.append(current[-1])
+            return OnGpu(make(*args, **kw))
+        return f
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    for n in ("empty", "zeros", "empty_like"):
+        monkeypatch.setattr(torch, n, maker(getattr(torch, n)))
+    tensors, rest = arguments(name)
+    stub = {k: OnGpu(t) if not isinstance(t, OnGpu) else t for k, t in tensors.items()
+            if not any(k == m or m.endswith("_") and k.startswith(m) for m in MADE[name])}
+    made.clear()
+    with pytest.raises(Reached):
+        call(name, stub, dict(rest, stream=side))
+    assert len(made) >= len(MADE[name]) and all(s is side for s in made)
+    made.clear()
+    with pytest.raises(Reached):
+        call(name, stub, rest)
+    assert all(s is None for s in made)
