@@ -289,6 +289,7 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 // of the rows and leaves the tile's valid tokens as a mask in valid[stage].
 template <typename V> struct TileStream {
     static constexpr int KT = V::KT, STEP = 32 / V::LPR, MINE = KT / STEP / V::W;
+    static constexpr int NO_TOKEN = -2;                // beside pages, of which -1 stands for every negative id
     static constexpr uint32_t FULL = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
     const AttnArgs &a;
     const Piece &p;
@@ -318,7 +319,7 @@ template <typename V> struct TileStream {
     __device__ __forceinline__ void look_up()
     {
         const bool in = lane < KT && t < p.t1;
-        pg = in ? row[col] : -2;
+        pg = in ? max(row[col], -1) : NO_TOKEN;
         place = off;
         t += KT;
         off += step_off;
@@ -333,7 +334,7 @@ template <typename V> struct TileStream {
     {
         const int st = i % V::STAGES;
         const bool ok = pg_ >= 0 && pg_ < a.n_pages;
-        if (!ok && pg_ != -2) raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
+        if (!ok && pg_ != NO_TOKEN) raise_fault(a.fault, LOSSK_TARGET_OUT_OF_RANGE);
         const int64_t at = ok ? (pg_ * a.page_stride + place_ * a.tok_stride) * V::ESIZE : -1;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
         if (lane == 0) valid[st] = mask;
