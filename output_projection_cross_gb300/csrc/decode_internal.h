@@ -13,7 +13,7 @@ __device__ __forceinline__ void raise_fault(int *fault, int status) { atomicMax(
 // ---- beam selection ------------------------------------------------------------
 // What the rows kernel leaves per (row, split): the largest kept logit m; the
 // sum z + lost of 2^(c x + b) over the kept logits, c = log2(e) / T and b what
-// -c ref rounds to (of 2^(c (x - ref)) where b would overflow; z NaN where a kept
+// -c ref rounds to (of 2^(c (x - ref)) where b is large; z NaN where a kept
 // logit is a NaN or +infinity); and the split's n_out best (logit, token) pairs in
 // falling order, token -1 filling the places left.
 struct BeamStat {

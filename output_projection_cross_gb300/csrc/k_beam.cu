@@ -185,15 +185,17 @@ template <typename T> __device__ __forceinline__ float vec_max(const uint4 &v)
 // A thread's running sum of 2^(c x + b), c = log2(e) / T.  b follows the
 // largest logit only once that is FAR above it (in log2 units), so a warp
 // seldom rescales.  The sum's true base is what b says, rounded or not: it is
-// taken off again in double.  Where c ref is near the end of the floats' range
-// b could overflow; a float next to ref is then so far off that only logits
-// equal to ref count.  z is two floats, sum and what its roundings lost.
+// taken off again in double.  Below 2^30 the rounding moves the exponents by 32
+// at most, which the sum's range has room for (2^(32 + FAR) a logit).  From
+// LARGE on it could take the sum to infinity or 0; there a float next to ref is
+// 64 or more off in the exponent, so only logits equal to ref count.  z is two
+// floats, sum and what its roundings lost.
 struct RowStat {
     float m, ref, b, z, lost;
 };
-constexpr float FAR = 24.f, NEAR_END = 1e37f;
+constexpr float FAR = 24.f, LARGE = 0x1p30f;
 
-__device__ __forceinline__ bool plain(float b) { return fabsf(b) < NEAR_END; }
+__device__ __forceinline__ bool plain(float b) { return fabsf(b) < LARGE; }
 // 2^(the base of a sum (ref, b) - the base `top` of one at least as high)
 __device__ __forceinline__ float to_base(float ref, float b, float top_ref, float top_b)
 {
