@@ -514,8 +514,11 @@ int64_t lossk_decode_workspace_bytes(int32_t kind, int64_t a, int64_t b, int64_t
  * lengths[b][k] + 1 (lengths NULL: rank = score).  A finished beam has one
  * candidate: itself, with token end_token, its own score and len =
  * lengths[b][k]; its logits are not read.  Per batch entry the n_out best
- * candidates are written in order of falling rank; equal ranks go by the
- * lower beam, then the lower token.  Ranks are compared in double.
+ * candidates are written in order of falling rank.  A beam's own candidates
+ * are in the order of their logits, of equal logits the lower token first:
+ * that is the rank's order before any rounding, also where different logits
+ * meet in one double (a temperature of 1e20).  Candidates of different beams
+ * are compared by rank, in double; equal ranks go to the lower beam.
  *   allow        uint32 words or NULL: bit v % 32 of word v / 32 of the row's
  *                mask is 1 where token v may follow.  allow_stride words lie
  *                between rows' masks; 0: one mask for all rows.  What the
