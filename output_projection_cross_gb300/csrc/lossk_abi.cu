@@ -6,6 +6,7 @@
 #include "lossk_internal.h"
 
 #include <atomic>
+#include <cstddef>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -1216,15 +1217,18 @@ int32_t lossk_device_status(void *workspace, int64_t workspace_bytes, lossk_stre
     if (!workspace || workspace_bytes < 256) return LOSSK_LENGTH_MISMATCH;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (cudaStreamSynchronize(st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
-    WsHeader h;
-    if (cudaMemcpy(&h, workspace, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return LOSSK_DEVICE_ERROR;
-    const int fault = h.pad[HDR_FAULT];
-    if (h.err == 0 && fault == 0) return LOSSK_OK;
-    const int err = h.err;
-    h.err = h.pad[HDR_FAULT] = 0;
-    if (cudaMemcpy(workspace, &h, sizeof(h), cudaMemcpyHostToDevice) != cudaSuccess) return LOSSK_DEVICE_ERROR;
-    if (err == 0) return fault;
-    return LOSSK_DEVICE_TIMEOUT;
+    WsHeader *hdr = static_cast<WsHeader *>(workspace);
+    int words[4 + HDR_FAULT + 1];
+    static_assert(offsetof(WsHeader, pad) == 4 * sizeof(int), "the words up to the fault word");
+    if (cudaMemcpy(words, hdr, sizeof(words), cudaMemcpyDeviceToHost) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    // the losses' calls neither use nor clear the fault word: what is no code of the decoding calls is not theirs
+    const int err = words[0], left = words[4 + HDR_FAULT];
+    const bool fault = left == LOSSK_TARGET_OUT_OF_RANGE || left == LOSSK_NON_FINITE_SCALAR || left == LOSSK_WORK_BUDGET_EXCEEDED;
+    const int zero = 0;
+    if ((err && cudaMemcpy(&hdr->err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) ||
+        (fault && cudaMemcpy(&hdr->pad[HDR_FAULT], &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess))
+        return LOSSK_DEVICE_ERROR;
+    return err ? LOSSK_DEVICE_TIMEOUT : fault ? left : LOSSK_OK;
 }
 
 // ---- vocabulary-parallel cross-entropy ---------------------------------------
