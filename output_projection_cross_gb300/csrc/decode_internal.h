@@ -169,8 +169,10 @@ struct AttnShape {
 constexpr int ATTN_MAX_ROWS = 152 * 12 * 16;       // runs x rows per item: a block has at most 12 warps of 16 rows
 constexpr int ATTN_ROW = 4;            // floats a partial row holds beside o
 AttnShape attn_shape(int dtype, int hd, int rows);
-// Whether the split pass needs attn_share or attn_plan ahead of it.
+// Whether the split pass needs attn_share, and attn_plan, ahead of it.
+bool attn_shares(const AttnArgs &a);
 bool attn_plans(const AttnArgs &a);
+cudaError_t launch_attn_share(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st);
 // The tensor-core kernel (16-bit types) and the CUDA-core one (fp32).

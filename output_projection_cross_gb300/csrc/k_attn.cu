@@ -1,8 +1,8 @@
 // k_attn.cu -- attention of one new token per sequence over a paged key-value
 // cache, split over the cache's length and joined.
 //
-//   attn_plan   per group of sequences: how many leading pages they share, and
-//               the work in units
+//   attn_share  per group of sequences: how many leading pages they share
+//   attn_plan   the work in units, where there are many groups
 //   attn        the split pass (k_attn_mma.cu, k_attn_ffma.cu)
 //   attn_join   the partial results of each output row joined
 //
@@ -252,18 +252,19 @@ AttnShape attn_shape(int dtype, int hd, int rows)
     return dtype == LOSSK_F32 ? attn_ffma_shape(hd, rows) : attn_mma_shape(hd, rows);
 }
 
-bool attn_plans(const AttnArgs &a) { return a.share > 1 || a.n_group > BASE_GROUPS; }
+bool attn_shares(const AttnArgs &a) { return a.share > 1; }
+bool attn_plans(const AttnArgs &a) { return a.n_group > BASE_GROUPS; }
 
+cudaError_t launch_attn_share(const AttnArgs &a, cudaStream_t st)
+{
+    // the more threads the fewer rounds over a long table, and the later a short one is done: 4 beams of
+    // 3750 pages took 8 us with 256 threads and 4 with 1024, 8 x 8 of 136 pages 4 and 5
+    const dim3 groups(static_cast<unsigned>(a.n_group));
+    return a.max_pages <= 256 * SHARE_U ? launch(attn_share_kernel<256>, groups, dim3(256), 0, st, a)
+                                        : launch(attn_share_kernel<1024>, groups, dim3(1024), 0, st, a);
+}
 cudaError_t launch_attn_plan(const AttnArgs &a, cudaStream_t st)
 {
-    if (a.share > 1) {
-        // the more threads the fewer rounds over a long table, and the later a short one is done: 4 beams of
-        // 3750 pages took 8 us with 256 threads and 4 with 1024, 8 x 8 of 136 pages 4 and 5
-        const unsigned groups = static_cast<unsigned>(a.n_group);
-        const cudaError_t e = a.max_pages <= 256 * SHARE_U ? launch(attn_share_kernel<256>, dim3(groups), dim3(256), 0, st, a)
-                                                           : launch(attn_share_kernel<1024>, dim3(groups), dim3(1024), 0, st, a);
-        if (e != cudaSuccess || a.n_group <= BASE_GROUPS) return e;
-    }
     return launch(attn_plan_kernel, dim3(1), dim3(PLAN_T), 0, st, a);
 }
 cudaError_t launch_attn(int dtype, const AttnArgs &a, cudaStream_t st)

@@ -590,6 +590,10 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
     a.part_b = a.part_a + (static_cast<int64_t>(a.n_group) * a.n_kv * a.cs + a.nw) * a.ra * (a.hd + ATTN_ROW);
     a.fault = fault_of(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (attn_shares(a)) {
+        Launch k(KK_ATTN_PLAN, st);
+        if (launch_attn_share(a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
+    }
     if (attn_plans(a)) {
         Launch k(KK_ATTN_PLAN, st);
         if (launch_attn_plan(a, st) != cudaSuccess) return LOSSK_DEVICE_ERROR;
