@@ -8,9 +8,6 @@
 
 namespace lossk {
 
-__device__ __forceinline__ float attn_f(float x) { return x; }
-__device__ __forceinline__ float attn_f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-__device__ __forceinline__ float attn_f(h16_t x) { return f16_to_f(x.bits); }
 __device__ __forceinline__ void attn_put4(float *p, float4 v, float f)
 {
     *reinterpret_cast<float4 *>(p) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
