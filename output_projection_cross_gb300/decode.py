@@ -20,12 +20,19 @@ from . import build as _build
 from .lossk import LosskError, _check, _dtype_code, _len, _ptr, _stream, lib
 
 
+class _NotBuilt:
+    """Stands for the module where it is not built: importing the package, for the losses, does not need it."""
+
+    def __getattr__(self, name):
+        raise ImportError(f"the decoding calls' module is not built ({_build.CALLS}); run `python "
+                          f"output_projection_cross_gb300/build.py` with a Python that has its headers")
+
+
 def _load_calls():
     """The module through which the calls are made (ctypes takes 2 us for the arguments of one)."""
     path = _build.CALLS
     if not os.path.exists(path):
-        raise ImportError(f"{os.path.basename(path)} is not built ({path}); run `python "
-                          f"output_projection_cross_gb300/build.py`")
+        return _NotBuilt()
     spec = importlib.util.spec_from_file_location("_lossk_calls", path)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
