@@ -770,6 +770,10 @@ __device__ __forceinline__ void put_out(const BeamArgs &a, int b, int j, int k, 
     if (a.length_out) a.length_out[o] = len;
 }
 
+// x / T, rounded: joined with a sum to one instruction it would be exact on one side of x / T - lse and rounded
+// on the other, 1e22 apart where logits lie at -3e38 (a row of which everything is masked).
+__device__ __forceinline__ double scaled(float x, double inv_t) { return __dmul_rn(x, inv_t); }
+
 // n^alpha; of multiples of a half (1 among them) exact wherever that is a double, so that ranks that are
 // equal come out so.  Of others by a logarithm and an exponential, some steps of a double off: lengths that
 // differ give no equal ranks there.  (By pow: 1.7 us more a selection.)
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
                 // the sum's base in log2 units; the logits' own scale 1 / T about their largest, c about that
                 const double base = plain(row.b) ? -static_cast<double>(row.b) : static_cast<double>(row.ref) * a.c;
                 const double m = row.m;
-                lse = m * a.inv_t + (log(static_cast<double>(row.z) + row.lost) + LN2 * (base - m * a.c));
+                lse = scaled(row.m, a.inv_t) + (log(static_cast<double>(row.z) + row.lost) + LN2 * (base - m * a.c));
             }
             s_lse[k] = lse;
             if (a.lse_out) a.lse_out[b * a.beams + k] = static_cast<float>(lse);
@@ -911,8 +915,7 @@ __global__ void __launch_bounds__(MERGE_NT) beam_merge_kernel(BeamArgs a)
     __syncthreads();
     auto score_of = [&](int i, int k) {
         const double s = s_row[k].start;
-        return s_row[k].kind == 2 ? s + (static_cast<double>(value_of(static_cast<uint32_t>(lists[i] >> 32))) * a.inv_t - s_lse[k])
-                                  : s;
+        return s_row[k].kind == 2 ? s + (scaled(value_of(static_cast<uint32_t>(lists[i] >> 32)), a.inv_t) - s_lse[k]) : s;
     };
     int valid = 0;
     for (int i = t; i < all; i += MERGE_NT) {

@@ -78,3 +78,35 @@ def test_a_row_masked_by_adding(L, mask):
     check(L, torch.from_numpy(m).cuda(), 6, 1.0)
     m[0, [5, 900, 4002]] = x[0, [5, 900, 4002]]
     check(L, torch.from_numpy(m).cuda(), 6, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("temperature", [0.7, 1.0, 3.0, 1000.0, 1e-4])
+@pytest.mark.parametrize("V", [1, 3, 700, 20011])
+def test_beams_of_which_everything_is_masked(L, dtype, temperature, V):
+    """A row whose every logit is the type's lowest value (or -1e30): its log-sum-exp is that value, in a double, and
+    its scores are the beam's, beside those of ordinary rows."""
+    rng = np.random.default_rng(V)
+    K = 6
+    x = (rng.standard_normal((K, V)) * 3).astype(np.float32)
+    low = torch.finfo(DTYPES[dtype]).min
+    x[1] = low
+    x[3] = low if dtype == "f16" else -1e30
+    x[4, V // 2:] = low
+    x = torch.from_numpy(x).cuda().to(DTYPES[dtype])
+    s = -np.linspace(0.5, 3.0, K).astype(np.float32)[None]
+    n = min(2 * K, K * V)
+    ws = L.decode_workspace(L.KIND_BEAM_SELECT, 1, K, V, n)
+    o = L.lossk_beam_select(x, torch.from_numpy(s).cuda(), n, temperature=temperature, ws=ws)
+    assert L.lossk_device_status(ws) == 580
+    r = ref.beam_select(x.double().cpu().numpy(), s.astype(np.float64), n, temperature=temperature)
+    got, want = o["score"].cpu().numpy(), r["score"]
+    with np.errstate(over="ignore"):
+        want = np.where(np.isinf(want.astype(np.float32)), -np.inf, want)
+    fin = np.isfinite(want)
+    assert (got[~fin] == -np.inf).all()
+    # (2^-51: of 65504 / T the doubles' own steps; of the lowest fp32 and bf16 values no step may be seen)
+    bound = 2.0 ** -24 * np.abs(want[fin]) + 3e-6 + 2.0 ** -51 * 65504 / temperature
+    assert (np.abs(got[fin] - want[fin]) <= bound).all()
+    for k in ("parent", "token"):
+        np.testing.assert_array_equal(o[k].cpu().numpy(), r[k], err_msg=k)
