@@ -486,6 +486,8 @@ int32_t lossk_ce_from_logits_static(int64_t n_tok, int64_t vocab, int32_t dtype,
  *    there are several.
  *  - The workspace's first 256 bytes must be zero before its first use (they
  *    hold that header).  lossk_decode_workspace_bytes gives its size.
+ *  - Kernels are launched on the current device; every address has to be one
+ *    of its.
  *  - Results do not depend on how the work is split over the GPU, except for
  *    the rounding of lossk_paged_attn, whose order of sums is a function of
  *    the sizes, the lengths and what is shared alone: every call's bits repeat. */
@@ -582,9 +584,10 @@ int32_t lossk_cache_fork(int64_t n_group, int64_t n_src, int64_t n_dst, int64_t 
  * itself if no other row holds it.  Pages that the tokens open are added.
  * Pages are handed out in sequence order, the free page of lowest id first,
  * and their count becomes 1; lens stays as it is (the caller adds the tokens
- * once they are written).  Either every sequence is served or nothing changes:
- * too few free pages or table entries leave 584 in the header, an id or length
- * out of range 586.
+ * once they are written: all of them, before the next reservation or fork,
+ * which know a sequence's pages by lens alone).  Either every sequence is
+ * served or nothing changes: too few free pages or table entries leave 584 in
+ * the header, an id or length out of range 586.
  * The pool: n_planes planes (say 2 per layer, keys and values) plane_stride
  * bytes apart, each of n_pages pages page_stride bytes apart, page_bytes long;
  * address and sizes multiples of 16 bytes (591). */
@@ -657,9 +660,12 @@ int32_t lossk_cache_write(int64_t n_tok, int64_t n_seq, int64_t n_kv_heads, int6
  *            warps; longer sequences are right as well
  *   out      [n_seq][n_q_heads][head_dim] (dtype, contiguous)
  *   lse_out  float[n_seq][n_q_heads] or NULL
- * What lies in the pages past a sequence's end does not matter.  Sums, the
- * softmax's maximum and weights are fp32; the tensor cores take each weight as
- * the sum of two 16-bit values, so that only the output is rounded.
+ * What lies in the pages past a sequence's end does not matter.  An infinite
+ * value under a positive weight gives infinity.  Sums, the softmax's maximum
+ * and weights are fp32; the tensor cores take each weight as the sum of two
+ * 16-bit values, to 16 bits of it (bf16) or to 2^-22 of the largest weight
+ * among its 16 tokens (fp16), beside which the output's rounding is what
+ * counts.
  * head_dim <= 256, max_pages * page_size <= 2^30 (583); q, pages, out and every
  * stride multiples of 16 bytes (591), so head_dim % 8 == 0 (16-bit types) or
  * % 4 (fp32).  n_q_heads a multiple of n_kv_heads (582).  A length out of range

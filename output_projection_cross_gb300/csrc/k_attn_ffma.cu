@@ -1,5 +1,6 @@
 // k_attn_ffma.cu -- the split pass of attention over a paged cache for fp32, on
-// the CUDA cores (the tensor cores' tf32 would drop 13 of 24 bits).
+// the CUDA cores (the tensor cores' tf32 alone would drop 13 of 24 bits; operands
+// split into parts, which would keep them, are not built).
 //
 // As in k_attn_mma.cu every warp walks its own run of units with its own ring
 // of tiles.  A tile's KT tokens lie across the lanes for the scores, 32 / KT
@@ -17,8 +18,8 @@
 // 301 -> 238 us for 4 of 20000 with 128 query heads.  Products and sums go two
 // floats an instruction (219 instead of 237 us at 128 query heads).
 //
-// Measured at 4 sequences of 20000 tokens, 8 KV heads of 128 (655 MB): 111 us =
-// 5.9 TB/s for 8 query heads, 114 for 32, 135 for 64.  Up to 4 rows to a KV head
+// Measured at 4 sequences of 20000 tokens, 8 KV heads of 128 (655 MB): 110 us =
+// 6.0 TB/s for 8 query heads, 112 for 32, 133 for 64, 214 for 128.  Up to 4 rows to a KV head
 // the stream bounds it, beyond that the multiply-adds and their reads of q and
 // of the weights.
 #include "attn_split.cuh"

@@ -3,10 +3,11 @@
 //
 // One new token per sequence makes the pass a stream: every key and value is
 // read once from HBM and meets only the query rows of its KV head (and, for
-// shared pages, of its group), 2 to 32 multiply-adds a byte.  tcgen05 would
-// spend tiles of 128 rows on them, so the products run as mma.sync m16n8k16 with
-// 16 query rows (the tensor pipe is 24 to 29 % active while HBM is read at 86 %
-// of the copy rate), and the kernel is built around the loads:
+// shared pages, of its group).  With 2 to 32 rows to a key tcgen05 would spend
+// tiles of 128 on them, so the products run as mma.sync m16n8k16 with 16 query
+// rows (the tensor pipe is 24 to 29 % active while HBM is read at 86 % of the
+// copy rate), and the kernel is built around the loads.  (From 64 rows on the
+// products bound it: 8 x 8 beams of 64 query heads 76 us, of 128 124.)
 //
 //  - every warp walks its own run of units with its own ring of STAGES tiles
 //    of KT tokens in shared memory, filled by 16-byte asynchronous copies two
@@ -26,7 +27,7 @@
 //
 // Measured, split pass and join: one sequence of 131072 tokens (8 KV heads of
 // 128, bf16, 537 MB) 96 us, the pass alone 92 us = 5.8 TB/s; 33 sequences of 1 to
-// 9000 tokens (160 MB) 37 us; 8 x 8 beams on 4096 shared tokens (170 MB) 50 us.
+// 9000 tokens (160 MB, fp16) 37 us; 8 x 8 beams on 4096 shared tokens (170 MB) 50 us.
 // What bounds it: the stream at 6.2 TB/s at the margin, and about 9 us before
 // the first tile and after the last; with many short items also their products
 // (8 x 8 beams: 37 us without the products, 32 without the loads, 42 with both).

@@ -12,7 +12,7 @@
 // different beams may lie closer together than floats resolve.
 //
 // A row is read once: 65 us for 128 x 8 beams over 151936 tokens (272 MB of
-// live rows, 4.2 TB/s over both kernels), 18 us for 16 x 4, 12 us for one entry
+// live rows, 4.2 TB/s over both kernels), 18 us for 16 x 4, 11 us for one entry
 // of 4 beams over 32000 tokens, which is two launches and their chains of
 // dependent steps (rows 7 us, merge 4).
 #include "../../include/lossk.h"
