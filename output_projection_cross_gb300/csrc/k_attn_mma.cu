@@ -5,8 +5,8 @@
 // read once from HBM and meets only the query rows of its KV head (and, for
 // shared pages, of its group).  With 2 to 32 rows to a key tcgen05 would spend
 // tiles of 128 on them, so the products run as mma.sync m16n8k16 with 16 query
-// rows (the tensor pipe is 24 to 29 % active while HBM is read at 86 % of the
-// copy rate), and the kernel is built around the loads.  (From 64 rows on the
+// rows (the tensor pipe is 23 to 29 % active while HBM is read at 83 to 86 % of
+// the copy rate), and the kernel is built around the loads.  (From 64 rows on the
 // products bound it: 8 x 8 beams of 64 query heads 76 us, of 128 124.)
 //
 //  - every warp walks its own run of units with its own ring of STAGES tiles
