@@ -72,3 +72,34 @@ for b in (0, B // 2, B - 1):
     assert torch.allclose(rank[at], best[:n], rtol=0, atol=1e-5) and len(set(at.tolist())) == n
     assert torch.allclose(got["score"][b].double(), best[:n], rtol=0, atol=1e-5)
 """)
+
+
+def test_a_process_first_calls_recorded_into_a_graph():
+    """Whatever a kernel's first launch needs is done while the stream records."""
+    run("""
+x, s = inputs(2, 4, 20001)
+y, s2 = inputs(3, 5, 77)
+ws, out = L.decode_workspace(L.KIND_BEAM_SELECT, 2, 4, 20001, 8), L.beam_buffers(2, 8)
+ws2, out2 = L.decode_workspace(L.KIND_BEAM_SELECT, 3, 5, 77, 8), L.beam_buffers(3, 8)
+cases = []
+for dt in (torch.bfloat16, torch.float16, torch.float32):
+    k, v = (torch.randn(40, 16, 2, 64, device="cuda", generator=g).to(dt) for _ in range(2))
+    q = torch.randn(4, 8, 64, device="cuda", generator=g).to(dt)
+    t = torch.randperm(40, device="cuda", generator=g).int().view(4, 10)
+    cases.append((q, k, v, t, torch.tensor([160, 1, 77, 33], dtype=torch.int32, device="cuda")))
+wa = [L.decode_workspace(L.KIND_PAGED_ATTN, 4, 8, 2, 64) for _ in cases]
+o = [torch.zeros_like(c[0]) for c in cases]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    L.lossk_beam_select(x, s, 8, out=out, ws=ws)
+    L.lossk_beam_select(y, s2, 8, out=out2, ws=ws2)
+    for c, w, a in zip(cases, wa, o):
+        L.lossk_paged_attn(*c, share=2, out=a, ws=w)
+graph.replay()
+torch.cuda.synchronize()
+for a, b in ((out, L.lossk_beam_select(x, s, 8)), (out2, L.lossk_beam_select(y, s2, 8))):
+    assert all(torch.equal(a[n], b[n]) for n in a)
+for c, a in zip(cases, o):
+    assert torch.equal(a, L.lossk_paged_attn(*c, share=2))
+""")
