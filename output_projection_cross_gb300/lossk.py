@@ -10,6 +10,7 @@ importing this module fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -145,6 +146,18 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on_its_stream(f):
+    """A call given a stream runs with that stream current: what it makes for itself is made and zeroed
+    there, and its memory, once dropped, goes to that stream's later work alone."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return BF16
@@ -206,6 +219,7 @@ def workspace(kind: int, n_tok: int, d_model: int, vocab: int, dtype: int, devic
 
 # ---- device calls -----------------------------------------------------------------
 
+@_on_its_stream
 def lossk_targets_check(targets, vocab, ws=None, stream=None) -> int:
     _contig(targets, "targets")
     ws = ws if ws is not None else torch.zeros(256, dtype=torch.uint8, device=targets.device)
@@ -217,6 +231,7 @@ def _ws(ws, kind, n, d, V, dtype, dev):
     return _contig(ws, "ws") if ws is not None else workspace(kind, n, d, V, dtype, dev)
 
 
+@_on_its_stream
 def lossk_ce_fwd(hidden, weight, targets, loss_mask=None, chunk=None, z_weight=0.0, lse_out=None,
                  ce_out=None, scalars_out=None, ws=None, stream=None):
     for t, nm in ((hidden, "hidden"), (weight, "weight"), (targets, "targets"), (loss_mask, "loss_mask")):
@@ -237,6 +252,7 @@ def lossk_ce_fwd(hidden, weight, targets, loss_mask=None, chunk=None, z_weight=0
     return {"lse": lse_out, "ce": ce_out, "scalars": scalars_out}
 
 
+@_on_its_stream
 def lossk_ce_bwd(hidden, weight, targets, lse, loss_mask=None, z_weight=0.0, grad_scale=1.0,
                  d_hidden=None, d_weight=None, want_d_hidden=True, want_d_weight=True, ws=None,
                  stream=None):
@@ -260,6 +276,7 @@ def lossk_ce_bwd(hidden, weight, targets, lse, loss_mask=None, z_weight=0.0, gra
     return {"d_hidden": d_hidden, "d_weight": d_weight}
 
 
+@_on_its_stream
 def lossk_ce_fwd_bwd(hidden, weight, targets, loss_mask=None, chunk=None, z_weight=0.0,
                      grad_scale=1.0, lse_out=None, ce_out=None, scalars_out=None, d_hidden=None,
                      d_weight=None, want_d_hidden=True, want_d_weight=True, ws=None, stream=None):
@@ -268,6 +285,7 @@ def lossk_ce_fwd_bwd(hidden, weight, targets, loss_mask=None, chunk=None, z_weig
                                want_d_weight, ws, stream)
 
 
+@_on_its_stream
 def lossk_ce_fwd_bwd_ex(hidden, weight, targets, loss_mask=None, chunk=None, z_weight=0.0,
                         grad_scale=1.0, flags=0, lse_out=None, ce_out=None, scalars_out=None,
                         d_hidden=None, d_weight=None, want_d_hidden=True, want_d_weight=True,
@@ -304,6 +322,7 @@ def lossk_ce_fwd_bwd_ex(hidden, weight, targets, loss_mask=None, chunk=None, z_w
             "d_weight": d_weight}
 
 
+@_on_its_stream
 def lossk_ce_from_logits(logits, targets, loss_mask=None, z_weight=0.0, grad_scale=1.0,
                          want_grad=False, lse_out=None, ce_out=None, scalars_out=None,
                          grad_logits=None, ws=None, stream=None):
@@ -326,6 +345,7 @@ def lossk_ce_from_logits(logits, targets, loss_mask=None, z_weight=0.0, grad_sca
     return {"lse": lse_out, "ce": ce_out, "scalars": scalars_out, "grad_logits": grad_logits}
 
 
+@_on_its_stream
 def lossk_ce_from_logits_static(logits, targets, loss_mask=None, z_weight=0.0, grad_scale=1.0,
                                 want_grad=False, lse_out=None, ce_out=None, scalars_out=None,
                                 grad_logits=None, stream=None):
@@ -350,6 +370,7 @@ def lossk_ce_from_logits_static(logits, targets, loss_mask=None, z_weight=0.0, g
     return {"lse": lse_out, "ce": ce_out, "scalars": scalars_out, "grad_logits": grad_logits}
 
 
+@_on_its_stream
 def lossk_distill_fwd_bwd(hidden, weight, teacher_logits, direction="fkl", temperature=1.0,
                           loss_mask=None, chunk=None, z_weight=0.0, grad_scale=1.0,
                           scalars_out=None, per_token_out=None, lse_out=None, d_hidden=None,
@@ -361,6 +382,7 @@ def lossk_distill_fwd_bwd(hidden, weight, teacher_logits, direction="fkl", tempe
                                     want_d_weight, ws, stream)
 
 
+@_on_its_stream
 def lossk_distill_fwd_bwd_ex(hidden, weight, teacher_logits, direction="fkl", temperature=1.0,
                              loss_mask=None, chunk=None, z_weight=0.0, grad_scale=1.0, flags=0,
                              scalars_out=None, per_token_out=None, lse_out=None, d_hidden=None,
@@ -396,6 +418,7 @@ def lossk_distill_fwd_bwd_ex(hidden, weight, teacher_logits, direction="fkl", te
             "d_hidden": d_hidden, "d_weight": d_weight}
 
 
+@_on_its_stream
 def lossk_ce_chunk_invariance(hidden, weight, targets, loss_mask=None, z_weight=0.0, ws=None,
                               stream=None) -> float:
     """Max |difference| between lossk_ce_fwd at chunk 1 and at chunk n_tok (or the largest
@@ -415,6 +438,7 @@ def lossk_ce_chunk_invariance(hidden, weight, targets, loss_mask=None, z_weight=
     return out.value
 
 
+@_on_its_stream
 def lossk_distill_from_logits(logits, teacher_logits, direction="fkl", temperature=1.0,
                               loss_mask=None, z_weight=0.0, grad_scale=1.0, flags=0, want_grad=True,
                               scalars_out=None, per_token_out=None, lse_out=None, grad_logits=None,
@@ -447,6 +471,7 @@ def lossk_device_status(ws, stream=None) -> int:
 
 # ---- vocabulary-parallel cross-entropy ---------------------------------------------
 
+@_on_its_stream
 def lossk_ce_shard_fwd(hidden, weight_shard, targets, v0, vocab_total, partials=None, ws=None, stream=None):
     """Partials float[3][n] of the shard holding vocabulary rows [v0, v0 + rows)."""
     for t, nm in ((hidden, "hidden"), (weight_shard, "weight_shard"), (targets, "targets")):
@@ -464,6 +489,7 @@ def lossk_ce_shard_fwd(hidden, weight_shard, targets, v0, vocab_total, partials=
     return partials
 
 
+@_on_its_stream
 def lossk_ce_shard_combine(partials_all, loss_mask=None, z_weight=0.0, lse_out=None, ce_out=None,
                            scalars_out=None, ws=None, stream=None):
     """lse, ce and the scalars from every shard's partials [P][3][n], in shard order."""
@@ -483,6 +509,7 @@ def lossk_ce_shard_combine(partials_all, loss_mask=None, z_weight=0.0, lse_out=N
     return {"lse": lse_out, "ce": ce_out, "scalars": scalars_out}
 
 
+@_on_its_stream
 def lossk_ce_shard_bwd(hidden, weight_shard, targets, v0, vocab_total, lse, loss_mask=None, z_weight=0.0,
                        grad_scale=1.0, d_hidden=None, d_weight=None, want_d_hidden=True, want_d_weight=True,
                        ws=None, stream=None):

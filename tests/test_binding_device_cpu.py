@@ -57,3 +57,38 @@ def test_inputs_of_another_gpu(name):
         for k in tensors:
             with pytest.raises(ValueError):
                 f(**{i: OnGpu(t, other if i == k else 0) for i, t in tensors.items()}, **out)
+
+
+@pytest.mark.parametrize("name", ["lossk_ce_fwd", "lossk_ce_from_logits", "lossk_distill_from_logits"])
+def test_what_a_call_makes_is_made_on_its_stream(name, monkeypatch):
+    """Made on the current stream, a workspace would be zeroed there while the call runs on its own, and its
+    memory given to the current stream's next allocation while the call still uses it."""
+    current, made = [None], []
+
+    class Stream:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    def maker(make):
+        def f(*args, device=None, **kw):
+            made.append(current[-1])
+            return OnGpu(make(*args, **kw))
+        return f
+    tensors, out = arguments(name)
+    stub = {k: OnGpu(t) for k, t in tensors.items() if k != "ws"}
+    monkeypatch.setattr(lossk, "lossk_workspace_bytes", lambda *_: 1 << 12)
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    for n in ("empty", "zeros"):
+        monkeypatch.setattr(torch, n, maker(getattr(torch, n)))
+    rest = {"want_grad": False} if "want_grad" in out else {}
+    for stream in ("side", None):
+        made.clear()
+        with pytest.raises(Reached):
+            getattr(lossk, name)(**stub, **rest, stream=stream)
+        assert len(made) >= 3 and all(s is stream for s in made)
