@@ -679,6 +679,152 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
                          int64_t lens_len, int64_t max_len, int64_t window, double scale, void *out, int64_t out_len,
                          float *lse_out, void *workspace, int64_t workspace_bytes, lossk_stream_t stream);
 
+/* ---- losses of sampled and compared sequences -------------------------------------
+ * What a user of the head trains it with after the label loss: the clipped
+ * policy loss with a KL term over sampled tokens, and paired log ratios of
+ * chosen and rejected sequences.  The pages have no counterpart to these
+ * calls.  Each loss has two forms, like the label loss: from hidden rows and
+ * the head's weight (the logits are never held), and from given logits.
+ *
+ * With x_t = s_t / temperature (s_t the token's row of logits) and
+ *   logp_t = x_{t,y_t} - log sum_v exp x_{t,v}
+ * a loss is a function of the logp of the tokens that count, and its gradient
+ * grad_logits_t = a_t (softmax(x_t) - onehot_{y_t}), a_t = -grad_scale
+ * (d total / d logp_t) / temperature, folded into d_hidden and d_weight where
+ * the logits are not given.
+ *
+ * Arguments that the calls share:
+ *   first       int32[n_seq + 1] on the device: sequence i is rows first[i] ..
+ *               first[i + 1] - 1; 0 <= first[0], not falling, first[n_seq] <=
+ *               n_tok.  NULL (policy loss only): no sequences, every row may count.
+ *   loss_mask   uint8[n_tok] or NULL.  A row counts when its mask is not 0 and it
+ *               lies in a sequence (where there are sequences).
+ *   targets     int64[n_tok]; those of rows that do not count are not read.
+ *   advantages, old_logp, ref_logp  float per row; where a row does not count, what
+ *               they hold does not matter.
+ *   logp_out    float[n_tok] or NULL: logp_t, 0 where a row does not count.
+ *   hidden, weight, logits, dtype   as above; contiguous
+ *   d_hidden, d_weight  grad_dtype: LOSSK_F32, or the inputs' 16-bit type (each
+ *               element is then rounded once, from its fp32 sum).  NULL to skip.
+ *   grad_logits dtype, or NULL to skip.
+ * Every row of a gradient is written: rows that do not count, and those behind
+ * the last sequence, become 0.  A token on whose logp the loss does not depend
+ * (a clipped one without a KL term) has a zero gradient whatever its logits hold.  A
+ * vocabulary entry at -infinity has probability 0; a row of nothing else has
+ * logp -infinity and a zero gradient.
+ * flags: LOSSK_ACCUMULATE_GRADS adds to the gradients (float d_hidden and d_weight,
+ * or grad_logits; with 16-bit d_hidden or d_weight: 592), LOSSK_REDUCE_SUM sums
+ * where the formulas take means, and the flags below.
+ * Unlike the calls above these do not synchronise: they return once their kernels
+ * are queued and can be recorded into a CUDA graph.  So what is wrong in device
+ * data, a target of a counted row outside [0, vocab) or a wrong `first`, leaves
+ * every output untouched and 586 in the workspace's header, which
+ * lossk_device_status reads and clears.  The workspace's first 256 bytes must be
+ * zero before its first use.  Calls on one workspace must not overlap in time;
+ * nor must replays of graphs that were recorded with it.
+ * Checks: 581, 583, 584, 582, 591, 585, 588, 592 as above; a required pointer that is
+ * NULL or a length too short is 582, d_model % 8 != 0 with 16-bit inputs 591. */
+
+/* LOSSK_SEQ_RATIO: one ratio per sequence, exp of the mean over its counted tokens
+ *   of logp_t - old_t.  LOSSK_SEQ_MEAN: the mean over sequences of the mean over
+ *   their tokens, instead of the mean over all tokens.  LOSSK_SEQ_ADVANTAGES:
+ *   advantages[n_seq], one for all tokens of a sequence.  (All three need `first`: 582.)
+ * LOSSK_LENGTH_MEAN (preference loss): a sequence's log ratio is the mean over its
+ *   tokens instead of the sum. */
+enum lossk_sequence_flags {
+    LOSSK_SEQ_RATIO = 4,
+    LOSSK_SEQ_MEAN = 8,
+    LOSSK_SEQ_ADVANTAGES = 16,
+    LOSSK_LENGTH_MEAN = 32
+};
+
+/* Objectives of the preference loss; any other value: 588. */
+enum lossk_preference_objective { LOSSK_PREF_SIGMOID = 0, LOSSK_PREF_HINGE = 1, LOSSK_PREF_SQUARED = 2 };
+
+/* Workspace kinds of these calls: HEAD for the forms that take hidden and weight,
+ * LOGITS for the others (d_model is then not used).  n_seq: sequences, 2 n_pairs for
+ * the preference loss, 0 for none.  Bytes (a multiple of 256); -1 for sizes that the
+ * calls refuse. */
+enum lossk_sequence_kind { LOSSK_KIND_SEQUENCE_HEAD = 0, LOSSK_KIND_SEQUENCE_LOGITS = 1 };
+int64_t lossk_sequence_workspace_bytes(int32_t kind, int64_t n_tok, int64_t d_model, int64_t vocab, int64_t n_seq,
+                                       int32_t dtype);
+
+/* Clipped policy loss with a KL term.  Per counted token, with A_t its advantage,
+ *   r_t = exp(logp_t - old_t)                       (old_logp NULL: old_t is logp_t
+ *                                                    itself, held constant)
+ *   P_t = -min(r_t A_t, clamp(r_t, 1 - clip_low, 1 + clip_high) A_t)
+ *   K_t = exp(q_t) - q_t - 1,  q_t = ref_t - logp_t (ref_logp NULL: 0)
+ *   L_t = P_t + kl_weight K_t,  total = sum_t w_t L_t
+ * with w_t = 1 / N over the N counted tokens; LOSSK_SEQ_MEAN: 1 / (S n_s) over the S
+ * sequences with a counted token, n_s of the token's own; LOSSK_REDUCE_SUM: without N,
+ * or S.  A ratio on a border of the clamp counts as inside it; an advantage of 0 makes
+ * P_t 0.
+ *   scalars_out    float[4], required: {total, sum w P, sum w K, sum w [clipped]}
+ *   per_token_out  float[n_tok] or NULL: L_t, 0 where a row does not count
+ * clip_low in [0, 1], clip_high >= 0, kl_weight >= 0 (> 0 needs ref_logp: 582),
+ * temperature > 0, all finite (585). */
+int32_t lossk_policy_fwd_bwd(int64_t n_tok, int64_t d_model, int64_t vocab, int64_t n_seq, int32_t dtype,
+                             const void *hidden, int64_t hidden_len, const void *weight, int64_t weight_len,
+                             const int64_t *targets, int64_t targets_len, const uint8_t *loss_mask,
+                             const int32_t *first, int64_t first_len, const float *advantages, int64_t advantages_len,
+                             const float *old_logp, int64_t old_len, const float *ref_logp, int64_t ref_len,
+                             double clip_low, double clip_high, double kl_weight, double temperature,
+                             double grad_scale, uint32_t flags, float *scalars_out, float *per_token_out,
+                             float *logp_out, int32_t grad_dtype, void *d_hidden, void *d_weight, void *workspace,
+                             int64_t workspace_bytes, lossk_stream_t stream);
+
+/* The same from logits[n_tok][vocab]. */
+int32_t lossk_policy_from_logits(int64_t n_tok, int64_t vocab, int64_t n_seq, int32_t dtype, const void *logits,
+                                 int64_t logits_len, const int64_t *targets, int64_t targets_len,
+                                 const uint8_t *loss_mask, const int32_t *first, int64_t first_len,
+                                 const float *advantages, int64_t advantages_len, const float *old_logp,
+                                 int64_t old_len, const float *ref_logp, int64_t ref_len, double clip_low,
+                                 double clip_high, double kl_weight, double temperature, double grad_scale,
+                                 uint32_t flags, float *scalars_out, float *per_token_out, float *logp_out,
+                                 void *grad_logits, int64_t grad_len, void *workspace, int64_t workspace_bytes,
+                                 lossk_stream_t stream);
+
+/* Paired log ratios.  Sequence i < n_pairs is the chosen one of pair i, sequence
+ * n_pairs + i its rejected one (n_seq = 2 n_pairs; temperature 1).  With
+ *   D_s = sum over the counted tokens of s of logp_t - ref_t (ref_logp NULL: ref 0),
+ *         their mean with LOSSK_LENGTH_MEAN
+ *   u = D_chosen - D_rejected,  h = beta u - margin
+ *   LOSSK_PREF_SIGMOID: L = -(1 - label_smoothing) log sigmoid(h)
+ *                           - label_smoothing log sigmoid(-h)
+ *   LOSSK_PREF_HINGE:   L = max(0, 1 - beta u)
+ *   LOSSK_PREF_SQUARED: L = (u - 1 / (2 beta))^2
+ *   total = mean over the pairs of L + nll_weight (mean over the counted tokens of all
+ *           chosen sequences of -logp_t)
+ * A pair of which one sequence has no counted token does not count (L 0, no gradient;
+ * the chosen one's tokens stay in the second mean).  LOSSK_REDUCE_SUM: two sums instead
+ * of two means.
+ *   scalars_out    float[4], required: {total, mean L, mean of -logp of chosen tokens,
+ *                  share of the pairs with u > 0 (LOSSK_REDUCE_SUM: their number)}
+ *   per_pair_out   float[n_pairs] or NULL: L
+ *   log_ratio_out  float[2 n_pairs] or NULL: D_s
+ * beta > 0, margin, label_smoothing in [0, 1], nll_weight >= 0, all finite (585);
+ * margin and label_smoothing belong to LOSSK_PREF_SIGMOID and must be 0 otherwise
+ * (585). */
+int32_t lossk_preference_fwd_bwd(int64_t n_tok, int64_t d_model, int64_t vocab, int64_t n_pairs, int32_t dtype,
+                                 const void *hidden, int64_t hidden_len, const void *weight, int64_t weight_len,
+                                 const int64_t *targets, int64_t targets_len, const uint8_t *loss_mask,
+                                 const int32_t *first, int64_t first_len, const float *ref_logp, int64_t ref_len,
+                                 int32_t objective, double beta, double margin, double label_smoothing,
+                                 double nll_weight, double grad_scale, uint32_t flags, float *scalars_out,
+                                 float *per_pair_out, float *log_ratio_out, float *logp_out, int32_t grad_dtype,
+                                 void *d_hidden, void *d_weight, void *workspace, int64_t workspace_bytes,
+                                 lossk_stream_t stream);
+
+/* The same from logits[n_tok][vocab]. */
+int32_t lossk_preference_from_logits(int64_t n_tok, int64_t vocab, int64_t n_pairs, int32_t dtype, const void *logits,
+                                     int64_t logits_len, const int64_t *targets, int64_t targets_len,
+                                     const uint8_t *loss_mask, const int32_t *first, int64_t first_len,
+                                     const float *ref_logp, int64_t ref_len, int32_t objective, double beta,
+                                     double margin, double label_smoothing, double nll_weight, double grad_scale,
+                                     uint32_t flags, float *scalars_out, float *per_pair_out, float *log_ratio_out,
+                                     float *logp_out, void *grad_logits, int64_t grad_len, void *workspace,
+                                     int64_t workspace_bytes, lossk_stream_t stream);
+
 /* ---- tracing ----------------------------------------------------------------
  * Every kernel the library launches belongs to one of LOSSK_N_KERNELS kinds
  * (lossk_kernel_name gives its name).  lossk_launch_count() is the number of
@@ -688,7 +834,7 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
  * events, adds their durations per kind into total_ms[kind] and
  * launches[kind] (host arrays of `cap` entries), and clears them if `reset`.
  * Returns the number of kinds written, or -1 on a CUDA error. */
-#define LOSSK_N_KERNELS 35
+#define LOSSK_N_KERNELS 43
 const char *lossk_kernel_name(int32_t kind);
 int64_t lossk_launch_count(void);
 int32_t lossk_profile_enable(int32_t on);

@@ -116,15 +116,17 @@ struct BwdUnit {
     int fixed, dg, yt_begin, ny;
 };
 
-__device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs &a, int u)
+// n_fixed, n_loop: the launch's tile counts, or those of the tokens that the
+// device counted (BwdArgs::n_dev).
+__device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs &a, int n_fixed, int n_loop, int u)
 {
     BwdUnit w;
     w.dg = u % a.n_dg;
     u /= a.n_dg;
-    w.fixed = u % a.n_fixed;
-    const int split = u / a.n_fixed;
-    w.yt_begin = static_cast<int>((static_cast<int64_t>(split) * a.n_loop) / a.n_split);
-    const int yt_end = static_cast<int>((static_cast<int64_t>(split + 1) * a.n_loop) / a.n_split);
+    w.fixed = u % n_fixed;
+    const int split = u / n_fixed;
+    w.yt_begin = static_cast<int>((static_cast<int64_t>(split) * n_loop) / a.n_split);
+    const int yt_end = static_cast<int>((static_cast<int64_t>(split + 1) * n_loop) / a.n_split);
     w.ny = yt_end - w.yt_begin;
     return w;
 }
@@ -168,6 +170,17 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
     // Queued behind a validation that found a target out of range: every CTA
     // leaves before it touches anything (a refused call writes no output).
     if (a.refused && *reinterpret_cast<const volatile int *>(a.refused)) return;
+    // a pass that is only the fallback of another one
+    if (a.only_if && !*reinterpret_cast<const volatile int *>(a.only_if)) return;
+    // Tokens and the tiles along them: the launch's, or as many as an earlier
+    // kernel gathered (at most the launch's; with none of them d_weight still
+    // walks one supertile, of zero coefficients, and so becomes zero).
+    int n_tok = a.n_tok, n_fixed = a.n_fixed, n_loop = a.n_loop;
+    if (a.n_dev) {
+        n_tok = min(n_tok, *a.n_dev);
+        if (ROWS) n_fixed = (n_tok + 255) / 256;
+        else n_loop = max((n_tok + BWD_BN - 1) / BWD_BN, 1);
+    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -207,14 +220,14 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
     // per (CTA, slot): tiles published (4 per tile) and loads completed (c per tile)
     unsigned *const gready = a.gsig;
     unsigned *const gfree = a.gsig + G_MAX_CTAS * G_SLOTS;
-    const int n_units = a.n_fixed * a.n_split * a.n_dg;
+    const int n_units = n_fixed * a.n_split * a.n_dg;
     auto cursor_set = [&](BwdCursor &cu, int u, int k) {
         cu.u = u;
         cu.k = k;
         cu.r = 0;
         cu.nr = 0;
         if (u < n_units) {
-            cu.w = bwd_unit(a, u);
+            cu.w = bwd_unit(a, n_fixed, n_loop, u);
             cu.nr = (cu.w.ny + c - 1) / c;
         }
     };
@@ -280,7 +293,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                 // d_weight: the group's next unit has a new fixed tile (128 weight rows
                 // over the whole d_model, read from HBM for the first time); bring it into
                 // L2 now, the CTAs splitting its K steps
-                const int fixn = bwd_unit(a, cur.u + n_groups).fixed * 256 + hh * 128;
+                const int fixn = bwd_unit(a, n_fixed, n_loop, cur.u + n_groups).fixed * 256 + hh * 128;
                 for (int kb = crank; kb < nk; kb += c) tma_prefetch_2d(&a.map_fix, kb * TC_BK, fixn);
             }
             if (cur.u < n_units) {
@@ -423,8 +436,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             prev = cur;
             if (cur.u < n_units) cursor_next(cur);
         }
-        tc_commit_pair_multicast(drain, 1);
-        bw_wait_drain(drain, 0);
+        if (group < n_units) {                 // (a group may have no unit where the device counted the tokens)
+            tc_commit_pair_multicast(drain, 1);
+            bw_wait_drain(drain, 0);
+        }
     } else if (warp == 6 && lane == 0) {
         // ================= grad-tile poller =================
         // The loader's sequence of grad tiles (every round of every unit, the
@@ -436,7 +451,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         int cnt[B_MAXC] = {};
         bool ok = true;
         for (int u = group; u < n_units && ok; u += n_groups) {
-            const BwdUnit w = bwd_unit(a, u);
+            const BwdUnit w = bwd_unit(a, n_fixed, n_loop, u);
             const int nr = (w.ny + c - 1) / c;
             for (int rr = 0; rr < nr && ok; ++rr) {
                 const int y0 = rr * c, y_end = min(y0 + c, w.ny);
@@ -468,10 +483,29 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         // each kind serves both buffers: buffer b's k-th fill is the (2k+b)-th.
         int tiss_all = 0, tuse_all = 0;
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const float L2E = static_cast<float>(LOG2E);
         const float kT = a.inv_t_l2e, kTln2 = kT * static_cast<float>(LN2);
         const float4 P0 = DISTILL ? make_float4(0.f, 0.f, 0.f, 0.f)
                                   : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
+        // fp16 operands: what the grad tiles leave out and the stored accumulators
+        // get back.  coef_max: the largest coefficient of the tokens, found on the
+        // device; the tiles hold G times the power of two that brings it to
+        // [2^13, 2^14), which keeps probabilities down to 2^-38 in fp16's range
+        // and the tiles' largest entry, a coefficient times 1 - p, below its end.
+        float in_scale = 1.f, out_scale = a.out_scale;
+        if (F16 && a.coef_max) {
+            const unsigned m = *a.coef_max;
+            const int e = m > 0 && m < 0x7F800000u ? min(max(14 - static_cast<int>(m >> 23) + 126, -100), 100) : 0;
+            in_scale = __int_as_float((127 + e) << 23);
+            out_scale = __int_as_float((127 - e) << 23);
+        }
+        auto param = [&](int t) {
+            float4 p = t < n_tok ? a.tokp[t] : P0;
+            if (F16 && !DISTILL) {
+                p.y *= in_scale;
+                p.z *= in_scale;
+            }
+            return p;
+        };
         int m_all = 0;                                // own logit tiles consumed so far
         auto n_own_of = [&](const BwdUnit &w) { return crank < w.ny ? (w.ny - crank + c - 1) / c : 0; };
         // d_weight with the token range whole (one split): a CTA's own token
@@ -479,7 +513,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         // are loaded once, into one copy the four warps share (four supertiles
         // at most: 16 KB).  The one barrier among the epilogue warps sits here,
         // before any wait a warp could unwind from.
-        const int n_own_all = crank < a.n_loop ? (a.n_loop - crank + c - 1) / c : 0;
+        const int n_own_all = crank < n_loop ? (n_loop - crank + c - 1) / c : 0;
         const bool pcache = !ROWS && a.n_split == 1 && n_own_all <= 4;
         // Label-CE d_weight keeps a supertile's 256 token parameters (4 KB) as
         // {x_j, c_j, x_j+1, c_j+1} pairs in the first 2 KB (the exponent shift
@@ -501,13 +535,13 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         if (pcache) {
             for (int i = r; i < n_own_all * BWD_BN; i += 128) {
                 const int t = ((i / BWD_BN) * c + crank) * BWD_BN + i % BWD_BN;
-                put_param(sPall + (i / BWD_BN) * BWD_BN, i % BWD_BN, t < a.n_tok ? a.tokp[t] : P0);
+                put_param(sPall + (i / BWD_BN) * BWD_BN, i % BWD_BN, param(t));
             }
             named_bar_sync(1, 128);
         }
         auto params_of = [&](const BwdUnit &w) {      // d_hidden: the fixed token row's parameters
             const int fixrow = w.fixed * 256 + hh * 128 + r;
-            return (ROWS && fixrow < a.n_tok) ? a.tokp[fixrow] : P0;
+            return ROWS ? param(fixrow) : P0;
         };
         // The first row of the teacher block of own supertile m of unit w, for
         // an L2 prefetch one supertile ahead of its use.
@@ -515,7 +549,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             const int fixrow = w.fixed * 256 + hh * 128 + r;
             const int loop0 = (w.yt_begin + m * c + crank) * BWD_BN;
             if (ROWS) {
-                if (fixrow >= a.n_tok) return;
+                if (fixrow >= n_tok) return;
                 const uint16_t *p = a.teacher + static_cast<int64_t>(fixrow) * a.vocab + loop0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -525,7 +559,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int t = loop0 + r + h * 128;
-                    if (t >= a.n_tok) continue;
+                    if (t >= n_tok) continue;
                     const uint16_t *p = a.teacher + static_cast<int64_t>(t) * a.vocab + fix0;
                     prefetch_l2(p);
                     if (fix0 + 64 < a.vocab) prefetch_l2(p + 64);
@@ -552,7 +586,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < BWD_BN / 32; ++i) {
                     const int t = loop0 + lane + i * 32;
-                    put_param(sP, lane + i * 32, t < a.n_tok ? a.tokp[t] : P0);
+                    put_param(sP, lane + i * 32, param(t));
                 }
                 __syncwarp();
             }
@@ -561,10 +595,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             ok = ok && mbar_wait(tfull, m_all & 1, err);
             if (!__all_sync(0xffffffffu, ok)) return false;
             tc_fence_after();
-            const int ncols = min(BWD_BN, (ROWS ? a.vocab : a.n_tok) - loop0);   // valid loop columns
+            const int ncols = min(BWD_BN, (ROWS ? a.vocab : n_tok) - loop0);   // valid loop columns
             const int rel = ROWS && !DISTILL ? __float_as_int(P.w) - loop0 : 0;
             // teacher logits of this thread's row and the supertile's columns
-            const bool t_ok = DISTILL && (ROWS ? fixrow < a.n_tok : fixrow < a.vocab);
+            const bool t_ok = DISTILL && (ROWS ? fixrow < n_tok : fixrow < a.vocab);
             const uint16_t *tbase =
                 DISTILL ? a.teacher + (ROWS ? static_cast<int64_t>(t_ok ? fixrow : 0) * a.vocab + loop0
                                             : static_cast<int64_t>(loop0) * a.vocab + (t_ok ? fixrow : 0))
@@ -650,7 +684,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                     // each column)
                     float gf[32], z0 = 0.f, z1 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) gf[i] = ex2_approx(fmaf(__uint_as_float(v[i]), L2E, -P.x));
+                    for (int i = 0; i < 32; ++i) gf[i] = ex2_approx(fmaf(__uint_as_float(v[i]), kT, -P.x));
                     if (q * 32 + 32 <= ncols) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
@@ -676,7 +710,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                     if (ROWS) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            gf[i] = P.y * ex2_approx(fmaf(__uint_as_float(v[i]), L2E, -P.x));
+                            gf[i] = P.y * ex2_approx(fmaf(__uint_as_float(v[i]), kT, -P.x));
                         const int jr = rel - q * 32;
                         if (static_cast<unsigned>(jr) < 32u) {
 #pragma unroll
@@ -688,8 +722,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             const float4 PP = pp[i >> 1];
-                            gf[i] = PP.y * ex2_approx(fmaf(__uint_as_float(v[i]), L2E, -PP.x));
-                            gf[i + 1] = PP.w * ex2_approx(fmaf(__uint_as_float(v[i + 1]), L2E, -PP.z));
+                            gf[i] = PP.y * ex2_approx(fmaf(__uint_as_float(v[i]), kT, -PP.x));
+                            gf[i + 1] = PP.w * ex2_approx(fmaf(__uint_as_float(v[i + 1]), kT, -PP.z));
                         }
                         const int *tg = reinterpret_cast<const int *>(sPt) + 512 + q * 32;
                         const float *sa = reinterpret_cast<const float *>(sPt) + 768 + q * 32;
@@ -785,7 +819,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         double zsum = 0.0;
         int m0 = 0;                                   // own tiles of unit w already formed
         if (u < n_units) {
-            w = bwd_unit(a, u);
+            w = bwd_unit(a, n_fixed, n_loop, u);
             P = params_of(w);
         }
         bool ok = true;
@@ -799,7 +833,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             double zsum2 = 0.0;
             int m02 = 0;
             if (u2 < n_units) {
-                w2 = bwd_unit(a, u2);
+                w2 = bwd_unit(a, n_fixed, n_loop, u2);
                 P2 = params_of(w2);
                 if (n_own_of(w2) > 0) {
                     ok = tile(w2, 0, P2, zsum2);
@@ -808,8 +842,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                 }
             }
             const int fixrow = w.fixed * 256 + hh * 128 + r;
-            const int split = u / (a.n_fixed * a.n_dg);
-            if (FUSED && w.dg == 0 && fixrow < a.n_tok)
+            const int split = u / (n_fixed * a.n_dg);
+            if (FUSED && w.dg == 0 && fixrow < n_tok)
                 // every d-group recomputes the same logits; the first one reports the sums
                 a.zpart[(static_cast<int64_t>(split) * c + crank) * a.zpart_stride + fixrow] =
                     static_cast<float>(zsum);
@@ -818,7 +852,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
             const int slice0 = (w.dg * c + crank) * TC_SLICE;
-            const int n_rows = ROWS ? a.n_tok : a.vocab;
+            const int n_rows = ROWS ? n_tok : a.vocab;
             float *dst = a.out + static_cast<int64_t>(split) * a.out_split_stride +
                          static_cast<int64_t>(fixrow) * a.d;
             if (STG && a.out_tma) {
@@ -844,7 +878,32 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                     tmem_ld_wait();
                     if (F16) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a.out_scale);
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * out_scale);
+                    }
+                    if (!DISTILL && a.out16) {
+                        // 16-bit d_weight (rounded once, here): a whole chunk is one half block
+                        uint8_t *h = stg + (q & 1) * (B_STG / 2);
+                        if (lane == 0) {
+                            if (q == 0) bulk_wait_read_all();
+                            else if (q >= 2) bulk_wait_read_but1();
+                        }
+                        __syncwarp();
+                        const uint32_t hb = smem_u32(h) + static_cast<uint32_t>(lane) * 64;
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            pk[i] = pack_16x2<F16>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+#pragma unroll
+                        for (int kq = 0; kq < 4; ++kq)
+                            st_shared_v4(hb + ((static_cast<uint32_t>(kq) ^ sw) << 4), pk[4 * kq], pk[4 * kq + 1],
+                                         pk[4 * kq + 2], pk[4 * kq + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&a.map_out, h, col, row0);
+                            bulk_commit_group();
+                        }
+                        continue;
                     }
 #pragma unroll
                     for (int hq = 0; hq < 2; ++hq) {
@@ -886,13 +945,13 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
 #pragma unroll 1
                 for (int q = 0; q < TC_SLICE / 32; ++q) {
                     const int col = slice0 + q * 32;
-                    if (col >= a.d || row0 >= a.n_tok) break;
+                    if (col >= a.d || row0 >= n_tok) break;
                     uint32_t v[32];
                     tmem_ld32(trow + ACC_COL + q * 32, v);
                     tmem_ld_wait();
                     if (F16) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a.out_scale);
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * out_scale);
                     }
                     if (lane == 0) bulk_wait_read_all();            // the block's previous store has read it
                     __syncwarp();
@@ -925,7 +984,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                             if (F16) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    v[h][i] = __float_as_uint(__uint_as_float(v[h][i]) * a.out_scale);
+                                    v[h][i] = __float_as_uint(__uint_as_float(v[h][i]) * out_scale);
                             }
                             if (a.accumulate) {
                                 // gradient accumulation: out += this unit's accumulator

@@ -53,6 +53,12 @@ __device__ __forceinline__ void f2_wait_drain(uint64_t *bar, uint32_t parity)
 template <bool DISTILL, bool F16>
 __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ TcArgs a)
 {
+    if (a.refused && *reinterpret_cast<const volatile int *>(a.refused)) return;
+    if (a.only_if && !*reinterpret_cast<const volatile int *>(a.only_if)) return;
+    // the launch's tokens, or as many as an earlier kernel gathered
+    const int n_tok = a.n_dev ? min(a.n_tok, *a.n_dev) : a.n_tok;
+    const int n_pt = (n_tok + 255) / 256;            // 256-token pair tiles
+    const int n_items = n_pt * a.n_yt;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -70,9 +76,8 @@ __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ Tc
     const uint32_t crank = cluster_ctarank();        // 0: even (MMA issuer), 1: odd
     const bool lead = crank == 0;
     const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-    const int n_pt = (a.n_xt + 1) / 2;               // 256-token pair tiles
-    const int it_begin = static_cast<int>((static_cast<int64_t>(pair) * a.n_items) / n_pairs);
-    const int it_end = static_cast<int>((static_cast<int64_t>(pair + 1) * a.n_items) / n_pairs);
+    const int it_begin = static_cast<int>((static_cast<int64_t>(pair) * n_items) / n_pairs);
+    const int it_end = static_cast<int>((static_cast<int64_t>(pair + 1) * n_items) / n_pairs);
     const int n_it = it_end - it_begin;
     auto coords = [&](int j, int &tok0, int &voc0, int &vt) {
         const int i = it_begin + j;
@@ -154,14 +159,16 @@ __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ Tc
             if (!ok) break;
             tc_commit_pair_multicast(&tfull[b], 3);
         }
-        tc_commit_pair_multicast(drain, 1);
-        f2_wait_drain(drain, 0);
+        if (n_it > 0) {
+            tc_commit_pair_multicast(drain, 1);
+            f2_wait_drain(drain, 0);
+        }
     } else if (warp >= 2) {
         // ================= epilogue (both CTAs, own 128 rows) =================
         const int quad = warp & 3;
         const int r = quad * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const float kS = DISTILL ? a.inv_t_l2e : static_cast<float>(LOG2E);
+        const float kS = a.inv_t_l2e;
         const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), 0);
         bool ok = true;
         for (int j = 0; j < n_it && ok; ++j) {
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ Tc
             coords(j, tok0, voc0, vt);
             const int b = j & 1;
             const int t = tok0 + r;
-            const bool row_ok = t < a.n_tok;
+            const bool row_ok = t < n_tok;
             const int ncols = min(F2_BN, a.vocab - voc0);
             const uint16_t *trow_g = nullptr;
             float lt2 = 0.f;
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ Tc
                     // the next tile's teacher row segment (512 bytes) into L2
                     int tk1, vc1, vt1;
                     coords(j + 1, tk1, vc1, vt1);
-                    if (tk1 + r < a.n_tok) {
+                    if (tk1 + r < n_tok) {
                         const uint16_t *p = a.teacher + static_cast<int64_t>(tk1 + r) * a.vocab + vc1;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)

@@ -1,0 +1,661 @@
+// k_seq.cu -- the losses of sampled and compared sequences, all but their
+// passes over logits: which rows count, log-probabilities from the passes'
+// partial sums, sums over sequences, each row's loss and coefficient, the
+// scalars, d_hidden from its partials.
+//
+// With x = s / T, logp_t = x_{t,y} - lse(x_t), every loss here is a function
+// of the logp of the counted rows, so ds_t = a_t (softmax(x_t) - onehot_y), a_t =
+// -grad_scale (d total / d logp_t) / T: one coefficient per row joins the loss to
+// the passes over the logits.  These kernels handle a few floats per row; what
+// bounds them is latency, one launch after another, so each starts while the
+// one ahead of it ends (decode_launch.h).
+#include "../../include/lossk.h"
+#include "decode_internal.h"
+#include "decode_launch.h"
+#include "ptx.cuh"
+#include "seq_internal.h"
+
+#include <type_traits>
+
+namespace lossk {
+
+namespace {
+
+__device__ __forceinline__ bool refused(const WsHeader *hdr)
+{
+    return *reinterpret_cast<const volatile int *>(&hdr->bad_targets) != 0;
+}
+
+__device__ __forceinline__ int slots_before(int slot) { return slot < 0 ? ~slot : slot; }
+
+// The sequence that holds slot c: the last one whose slots start at or before it.
+__device__ __forceinline__ int seq_of(const int *seq_slot, int n_seq, int c)
+{
+    int lo = 0, hi = n_seq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seq_slot[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+} // namespace
+
+// One block: a prefix sum over the rows, PER at a time per thread, carried from
+// one round of 8192 rows to the next.  In order, so that slots, and with them the
+// order of every sum, are a function of the mask alone.
+constexpr int PREP_T = 1024, PREP_PER = 8;
+__global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const SeqScratch w)
+{
+    wait_for_stream();
+    __shared__ int s_warp[32];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n = l.n_tok;
+    // (an error word of an earlier call stays until lossk_device_status has read it: refused)
+    bool bad = *reinterpret_cast<volatile int *>(&w.hdr->err) != 0;
+    bool range = false;
+    int lo = 0, hi = n;
+    if (l.first) {
+        for (int s = tid; s < l.n_seq; s += PREP_T) {
+            const int a = l.first[s], b = l.first[s + 1];
+            range |= a < 0 || b < a || b > n;
+        }
+        lo = l.first[0];
+        hi = l.first[l.n_seq];
+    }
+    if (tid == 0) s_bad = 0;
+    const bool range_all = __syncthreads_or(range) != 0;
+    if (range_all) lo = hi = 0;
+    int done = 0;                                          // slots of the rounds before
+    int wrong = 0;
+    for (int t0 = 0; t0 < n; t0 += PREP_T * PREP_PER) {
+        const int t = t0 + tid * PREP_PER;
+        unsigned on = 0;
+        int64_t y[PREP_PER];
+#pragma unroll
+        for (int i = 0; i < PREP_PER; ++i) {
+            const int r = t + i;
+            const bool in = r < n && r >= lo && r < hi && (!l.mask || l.mask[r] != 0);
+            y[i] = in ? l.targets[r] : 0;
+            on |= (in ? 1u : 0u) << i;
+        }
+#pragma unroll
+        for (int i = 0; i < PREP_PER; ++i) wrong |= y[i] < 0 || y[i] >= l.vocab;
+        int c = __popc(on), inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        int before = done, all = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const int v = s_warp[k];
+            before += k < warp ? v : 0;
+            all += v;
+        }
+        int at = before + inc - c;
+#pragma unroll
+        for (int i = 0; i < PREP_PER; ++i) {
+            if (t + i >= n) break;
+            const bool in = (on >> i) & 1u;
+            w.slot[t + i] = in ? at : ~at;
+            if (in) {
+                w.row[at] = t + i;
+                w.y[at] = y[i];
+                ++at;
+            }
+        }
+        done += all;
+        __syncthreads();
+    }
+    bad |= range || wrong;
+    int groups = 0, chosen = 0;
+    const int any_bad = __syncthreads_or(bad);
+    if (l.n_seq > 0) {
+        auto slots = [&](int s) {
+            const int t = range_all ? 0 : l.first[s];
+            return t < n ? slots_before(w.slot[t]) : done;
+        };
+        for (int s = tid; s <= l.n_seq; s += PREP_T) {
+            const int a = slots(s);
+            w.seq_slot[s] = a;
+            if (l.pairs > 0) {
+                if (s < l.pairs && slots(s + 1) > a && slots(l.pairs + s + 1) > slots(l.pairs + s)) ++groups;
+            } else if (s < l.n_seq && slots(s + 1) > a) {
+                ++groups;
+            }
+        }
+        if (l.pairs > 0) chosen = slots(l.pairs);          // (tokens before the first sequence do not count)
+        if (groups) atomicAdd(&s_bad, groups);             // s_bad is free by now: the count of groups
+        __syncthreads();
+        groups = s_bad;
+    }
+    if (tid == 0) {
+        w.hdr->bad_targets = any_bad;
+        w.hdr->n_valid = done;
+        w.hdr->redo = 0;
+        w.hdr->pad[HDR_GROUPS] = groups;
+        w.hdr->pad[HDR_CHOSEN] = chosen;
+        w.hdr->pad[HDR_COEF] = 0;
+        if (any_bad && w.hdr->err == 0) raise_fault(&w.hdr->pad[HDR_FAULT], LOSSK_TARGET_OUT_OF_RANGE);
+    }
+}
+
+cudaError_t launch_seq_prep(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
+{
+    Launch k(KK_SEQ_PREP, st);
+    return launch(seq_prep_kernel, dim3(1), dim3(PREP_T), 0, st, l, w);
+}
+
+// One warp per slot: the row's copy and, in the 16-bit types, its product with the
+// target's weight row.  Eight sums per lane, joined pairwise: a chain of d / 256
+// additions (a single sum per lane would be 8 times as long, and its rounding is the
+// log-probability's own).
+template <typename T> // float, uint16_t (bf16 bits) or h16_t (fp16 bits)
+__global__ void __launch_bounds__(256) seq_gather_kernel(const SeqLoss l, const SeqScratch w, const T *__restrict__ H,
+                                                         const T *__restrict__ W, int64_t d, T *__restrict__ out)
+{
+    wait_for_stream();
+    if (refused(w.hdr)) return;
+    const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int n_valid = w.hdr->n_valid;
+    if (c >= max((n_valid + 255) & ~255, 256)) return;
+    T *o = out + c * d;
+    if constexpr (sizeof(T) == 4) {
+        const T *h = c < n_valid ? H + w.row[c] * d : nullptr;
+        for (int64_t k = lane; k < d; k += 32) o[k] = h ? h[k] : 0.f;
+    } else {
+        constexpr bool F16 = std::is_same<T, h16_t>::value;
+        uint4 *ov = reinterpret_cast<uint4 *>(o);
+        if (c >= n_valid) {
+            for (int64_t k = lane; k < d / 8; k += 32) ov[k] = make_uint4(0, 0, 0, 0);
+            return;
+        }
+        const uint4 *h = reinterpret_cast<const uint4 *>(H + w.row[c] * d);
+        const uint4 *v = reinterpret_cast<const uint4 *>(W + w.y[c] * d);
+        float s[8] = {};
+#pragma unroll 4
+        for (int64_t k = lane; k < d / 8; k += 32) {
+            const uint4 a = h[k], b = v[k];
+            ov[k] = a;
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[2 * i] = fmaf(h16_lo<F16>(aw[i]), h16_lo<F16>(bw[i]), s[2 * i]);
+                s[2 * i + 1] = fmaf(h16_hi<F16>(aw[i]), h16_hi<F16>(bw[i]), s[2 * i + 1]);
+            }
+        }
+        float acc = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        for (int q = 16; q > 0; q >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, q);
+        if (lane == 0) {
+            w.tgt[c] = acc;
+            w.tokp[c] = make_float4(fmaf(acc, l.k2, FUSED_SHIFT), 0.f, 0.f, 0.f);
+        }
+    }
+}
+
+cudaError_t launch_seq_gather(int dtype, const SeqLoss &l, const SeqScratch &w, const void *H, const void *W, int64_t d,
+                              void *out, cudaStream_t st)
+{
+    Launch k(KK_SEQ_GATHER, st);
+    const dim3 grid(static_cast<unsigned>((((static_cast<int64_t>(l.n_tok) + 255) & ~int64_t(255)) + 7) / 8));
+    if (dtype == LOSSK_F32)
+        return launch(seq_gather_kernel<float>, grid, dim3(256), 0, st, l, w, static_cast<const float *>(H),
+                      static_cast<const float *>(W), d, static_cast<float *>(out));
+    if (dtype == LOSSK_F16)
+        return launch(seq_gather_kernel<h16_t>, grid, dim3(256), 0, st, l, w, static_cast<const h16_t *>(H),
+                      static_cast<const h16_t *>(W), d, static_cast<h16_t *>(out));
+    return launch(seq_gather_kernel<uint16_t>, grid, dim3(256), 0, st, l, w, static_cast<const uint16_t *>(H),
+                  static_cast<const uint16_t *>(W), d, static_cast<uint16_t *>(out));
+}
+
+// One thread per slot.  With r the row's reference (its target at about 64 in log2
+// units) and Z the sum of 2^(x log2 e - r): lse2 = r + log2 Z, logp = ln 2 (x_y log2 e - r -
+// log2 Z).  The difference is taken in double: r's own rounding, 4e-6 at 64, is in Z
+// as well and must not be in the result.
+__global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, const SeqScratch w,
+                                                             const float *__restrict__ zpart, int64_t nz)
+{
+    wait_for_stream();
+    if (refused(w.hdr)) return;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    if (c >= w.hdr->n_valid) return;
+    float Z = 0.f;
+    int64_t j = 0;
+    for (; j + 16 <= nz; j += 16) {
+        float v[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = zpart[(j + q) * w.n_pad + c];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) Z += v[q];
+    }
+    for (; j < nz; ++j) Z += zpart[j * w.n_pad + c];
+    // outside, the largest shifted term may be near the end of fp32's range (or not a number)
+    if (!(Z >= 0x1p-80f && Z <= 0x1p90f)) w.hdr->redo = 1;
+    const float r = w.tokp[c].x, lz = log2f(Z);
+    const double gap = static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - static_cast<double>(r);
+    w.lse2[c] = r + lz;
+    w.z[c] = Z;
+    w.lp[c] = static_cast<float>((gap - static_cast<double>(lz)) * LN2);
+}
+
+cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const float *zpart, int64_t nz,
+                                   cudaStream_t st)
+{
+    Launch k(KK_SEQ_MERGE, st);
+    return launch(seq_merge_fused_kernel, dim3(static_cast<unsigned>((l.n_tok + 31) / 32)), dim3(32), 0, st, l, w, zpart,
+                  nz);
+}
+
+// 32 slots per block, their tiles dealt to eight warps in runs.
+constexpr int MT_W = 8;
+__global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLoss l, const SeqScratch w,
+                                                                    const float *__restrict__ part, int64_t n_ct,
+                                                                    const int *only_if)
+{
+    wait_for_stream();
+    if (refused(w.hdr) || (only_if && !*reinterpret_cast<const volatile int *>(only_if))) return;
+    __shared__ float s_max[MT_W][32];
+    __shared__ double s_sum[MT_W][32];
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    const bool live = c < w.hdr->n_valid;
+    const float *m2 = part, *zz = part + n_ct * w.n_pad;
+    const int64_t c0 = n_ct * g / MT_W, c1 = n_ct * (g + 1) / MT_W;
+    float M = -INFINITY;
+    if (live)
+        for (int64_t i = c0; i < c1; ++i) M = fmaxf(M, m2[i * w.n_pad + c]);
+    s_max[g][lane] = M;
+    __syncthreads();
+    for (int q = 0; q < MT_W; ++q) M = fmaxf(M, s_max[q][lane]);
+    double Z = 0.0;
+    if (live && M > -INFINITY)
+        for (int64_t i = c0; i < c1; ++i)
+            Z += static_cast<double>(zz[i * w.n_pad + c] * exp2f(m2[i * w.n_pad + c] - M));
+    s_sum[g][lane] = Z;
+    __syncthreads();
+    if (g != 0 || !live) return;
+    Z = 0.0;
+    for (int q = 0; q < MT_W; ++q) Z += s_sum[q][lane];
+    const double lse2 = static_cast<double>(M) + log2(Z);
+    w.lse2[c] = static_cast<float>(lse2);
+    w.z[c] = 1.f;
+    w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2);
+}
+
+cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,
+                                   const int *only_if, cudaStream_t st)
+{
+    Launch k(KK_SEQ_MERGE, st);
+    return launch(seq_merge_tiles_kernel, dim3(static_cast<unsigned>((l.n_tok + 31) / 32)), dim3(32 * MT_W), 0, st, l, w,
+                  part, n_ct, only_if);
+}
+
+namespace {
+
+// A counted row's weight in the mean: n_s its sequence's counted tokens.
+__device__ __forceinline__ double row_weight(const SeqLoss &l, const WsHeader *hdr, int n_s)
+{
+    const bool sum = l.flags & LOSSK_REDUCE_SUM;
+    if (l.flags & LOSSK_SEQ_MEAN) return 1.0 / (static_cast<double>(n_s) * (sum ? 1 : hdr->pad[HDR_GROUPS]));
+    return sum ? 1.0 : 1.0 / hdr->n_valid;
+}
+
+struct PolicyTerm {
+    float loss, slope;      // P and dP / d(log ratio)
+    bool clipped;
+};
+
+// log ratio `delta` (exp in float or, for ratios of sequences a few 1e-4 from 1, in double)
+template <typename F> __device__ __forceinline__ PolicyTerm policy_term(const SeqLoss &l, F delta, float A)
+{
+    if (A == 0.f) return PolicyTerm{0.f, 0.f, false};
+    const F r = exp(delta);
+    const F edge = A > 0.f ? F(1) + static_cast<F>(l.high) : F(1) - static_cast<F>(l.low);
+    const bool out = A > 0.f ? r > edge : r < edge;
+    return PolicyTerm{static_cast<float>(-A * (out ? edge : r)), out ? 0.f : static_cast<float>(-A * r), out};
+}
+
+__device__ __forceinline__ float advantage(const SeqLoss &l, int row, int seq)
+{
+    return l.adv[(l.flags & LOSSK_SEQ_ADVANTAGES) ? seq : row];
+}
+
+__device__ __forceinline__ double block_sum(double v, double *sh)
+{
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+    for (unsigned i = 0; i < blockDim.x / 32; ++i) v += sh[i];
+    return v;
+}
+
+} // namespace
+
+// One block per sequence; the order of the sum is a function of its length.
+constexpr int SUM_T = 256;
+__global__ void __launch_bounds__(SUM_T) seq_sum_kernel(const SeqLoss l, const SeqScratch w)
+{
+    wait_for_stream();
+    if (refused(w.hdr)) return;
+    __shared__ double sh[SUM_T / 32];
+    const int s = blockIdx.x, a = w.seq_slot[s], b = w.seq_slot[s + 1];
+    const float *base = l.pairs > 0 ? l.ref : l.old;
+    double v = 0.0;
+    if (l.pairs > 0 || l.old)
+        for (int c = a + static_cast<int>(threadIdx.x); c < b; c += SUM_T)
+            v += static_cast<double>(w.lp[c]) - (base ? static_cast<double>(base[w.row[c]]) : 0.0);
+    v = block_sum(v, sh);
+    if (threadIdx.x == 0) w.sum[s] = v;
+    if (l.pairs > 0 || a == b) return;
+    // the policy loss by sequence: every token's term moves the one ratio
+    const double delta = v / (b - a), weight = row_weight(l, w.hdr, b - a);
+    double slope = 0.0;
+    for (int c = a + static_cast<int>(threadIdx.x); c < b; c += SUM_T)
+        slope += weight * static_cast<double>(policy_term<double>(l, delta, advantage(l, w.row[c], s)).slope);
+    slope = block_sum(slope, sh);
+    if (threadIdx.x == 0) w.slope[s] = slope;
+}
+
+cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
+{
+    Launch k(KK_SEQ_SUM, st);
+    return launch(seq_sum_kernel, dim3(static_cast<unsigned>(l.n_seq)), dim3(SUM_T), 0, st, l, w);
+}
+
+namespace {
+
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+// Of pair i: its loss and d loss / du.
+__device__ __forceinline__ void pair_term(const SeqLoss &l, double u, float &loss, float &slope)
+{
+    if (l.objective == LOSSK_PREF_SQUARED) {
+        const float g = static_cast<float>(u - 0.5 / static_cast<double>(l.beta));
+        loss = g * g;
+        slope = 2.f * g;
+        return;
+    }
+    const float h = static_cast<float>(static_cast<double>(l.beta) * u - static_cast<double>(l.margin));
+    if (l.objective == LOSSK_PREF_HINGE) {
+        loss = h >= 1.f ? 0.f : 1.f - h;
+        slope = h >= 1.f ? 0.f : -l.beta;
+    } else {
+        loss = (1.f - l.smooth) * softplus(-h);
+        if (l.smooth > 0.f) loss += l.smooth * softplus(h);
+        slope = l.beta * (l.smooth / (1.f + expf(-h)) - (1.f - l.smooth) / (1.f + expf(h)));
+    }
+}
+
+__device__ __forceinline__ double log_ratio(const SeqLoss &l, const SeqScratch &w, int s, int &count)
+{
+    count = w.seq_slot[s + 1] - w.seq_slot[s];
+    const double v = w.sum[s];
+    return (l.flags & LOSSK_LENGTH_MEAN) && count > 0 ? v / count : v;
+}
+
+} // namespace
+
+// One thread per row, and per sequence and pair.
+__global__ void __launch_bounds__(128) seq_coef_kernel(const SeqLoss l, const SeqScratch w)
+{
+    wait_for_stream();
+    if (refused(w.hdr)) return;
+    const int t = blockIdx.x * 128 + threadIdx.x;
+    const bool pref = l.pairs > 0;
+    const bool sum = l.flags & LOSSK_REDUCE_SUM;
+    float coef = 0.f;
+    if (pref && t < l.n_seq && l.log_ratio) {
+        int n_s;
+        l.log_ratio[t] = static_cast<float>(log_ratio(l, w, t, n_s));
+    }
+    if (pref && t < l.pairs) {
+        int nc, nr;
+        const double u = log_ratio(l, w, t, nc) - log_ratio(l, w, l.pairs + t, nr);
+        float loss = 0.f, slope;
+        const bool live = nc > 0 && nr > 0;
+        if (live) pair_term(l, u, loss, slope);
+        if (l.per_token) l.per_token[t] = loss;
+        w.pair[t] = static_cast<double>(loss);
+        w.pair[l.pairs + t] = live && u > 0.0 ? 1.0 : 0.0;
+    }
+    if (t < l.n_tok) {
+        const int c = w.slot[t];
+        if (c < 0) {
+            if (l.logp) l.logp[t] = 0.f;
+            if (!pref && l.per_token) l.per_token[t] = 0.f;
+        } else {
+            const float lp = w.lp[c];
+            const int s = l.n_seq > 0 ? seq_of(w.seq_slot, l.n_seq, c) : 0;
+            const int n_s = l.n_seq > 0 ? w.seq_slot[s + 1] - w.seq_slot[s] : 0;
+            double d_lp;                                   // d total / d logp
+            if (pref) {
+                const bool chosen = s < l.pairs;
+                const int i = chosen ? s : s - l.pairs;
+                int nc, nr;
+                const double u = log_ratio(l, w, i, nc) - log_ratio(l, w, l.pairs + i, nr);
+                d_lp = 0.0;
+                if (nc > 0 && nr > 0) {
+                    float loss, slope;
+                    pair_term(l, u, loss, slope);
+                    double g = chosen ? slope : -slope;
+                    if (l.flags & LOSSK_LENGTH_MEAN) g /= n_s;
+                    d_lp = sum ? g : g / w.hdr->pad[HDR_GROUPS];
+                }
+                if (chosen && l.nll > 0.f) d_lp -= static_cast<double>(l.nll) / (sum ? 1 : w.hdr->pad[HDR_CHOSEN]);
+                w.acc[c] = chosen ? -static_cast<double>(lp) : 0.0;
+            } else {
+                const double weight = row_weight(l, w.hdr, n_s);
+                PolicyTerm p;
+                const float A = advantage(l, t, s);
+                if (l.flags & LOSSK_SEQ_RATIO) {
+                    p = policy_term<double>(l, w.sum[s] / n_s, A);
+                    d_lp = w.slope[s] / n_s;
+                } else {
+                    p = policy_term<float>(l, l.old ? lp - l.old[t] : 0.f, A);
+                    d_lp = weight * static_cast<double>(p.slope);
+                }
+                float kl = 0.f, loss = p.loss;
+                if (l.ref) {
+                    const float q = l.ref[t] - lp, e = expm1f(q);
+                    kl = e - q;
+                    if (l.kl > 0.f) {
+                        loss = fmaf(l.kl, kl, loss);
+                        d_lp -= static_cast<double>(l.kl) * weight * static_cast<double>(e);
+                    }
+                }
+                if (l.per_token) l.per_token[t] = loss;
+                w.acc[c] = weight * static_cast<double>(p.loss);
+                w.acc[w.n_pad + c] = weight * static_cast<double>(kl);
+                w.acc[2 * w.n_pad + c] = p.clipped ? weight : 0.0;
+            }
+            if (l.logp) l.logp[t] = lp;
+            const float lse2 = w.lse2[c];
+            const bool none = lse2 == -INFINITY;           // a row without any probability
+            coef = none ? 0.f : static_cast<float>(d_lp * static_cast<double>(l.per_t));
+            w.tokp[c] = make_float4(none ? 0.f : lse2, coef, coef, __int_as_float(static_cast<int>(w.y[c])));
+        }
+    }
+    // the largest |coefficient| (fp16's passes scale by it): positive floats order as integers
+    unsigned m = __float_as_uint(fabsf(coef));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0 && m) atomicMax(reinterpret_cast<unsigned *>(&w.hdr->pad[HDR_COEF]), m);
+}
+
+cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
+{
+    Launch k(KK_SEQ_COEF, st);
+    const int n = l.n_tok > l.n_seq ? l.n_tok : l.n_seq;
+    return launch(seq_coef_kernel, dim3(static_cast<unsigned>((n + 127) / 128)), dim3(128), 0, st, l, w);
+}
+
+// One block: each thread every 1024th slot in order, then a fixed tree.
+__global__ void __launch_bounds__(1024) seq_scalars_kernel(const SeqLoss l, const SeqScratch w)
+{
+    wait_for_stream();
+    if (refused(w.hdr)) return;
+    __shared__ double sh[32];
+    const bool pref = l.pairs > 0, sum = l.flags & LOSSK_REDUCE_SUM;
+    const int n = w.hdr->n_valid;
+    double v[3] = {0.0, 0.0, 0.0};
+    for (int c = threadIdx.x; c < n; c += 1024) {
+        v[0] += w.acc[c];
+        if (!pref) {
+            v[1] += w.acc[w.n_pad + c];
+            v[2] += w.acc[2 * w.n_pad + c];
+        }
+    }
+    if (pref)
+        for (int i = threadIdx.x; i < l.pairs; i += 1024) {
+            v[1] += w.pair[i];
+            v[2] += w.pair[l.pairs + i];
+        }
+    for (int k = 0; k < 3; ++k) v[k] = block_sum(v[k], sh);
+    if (threadIdx.x != 0) return;
+    float *o = l.scalars;
+    if (pref) {
+        const int pairs = w.hdr->pad[HDR_GROUPS], chosen = w.hdr->pad[HDR_CHOSEN];
+        if (!sum) {
+            v[0] = chosen > 0 ? v[0] / chosen : 0.0;
+            v[1] = pairs > 0 ? v[1] / pairs : 0.0;
+            v[2] = pairs > 0 ? v[2] / pairs : 0.0;
+        }
+        // (without the likelihood term its infinities stay out of the total)
+        o[0] = static_cast<float>(l.nll > 0.f ? v[1] + static_cast<double>(l.nll) * v[0] : v[1]);
+        o[1] = static_cast<float>(v[1]);
+        o[2] = static_cast<float>(v[0]);
+        o[3] = static_cast<float>(v[2]);
+    } else {
+        o[0] = static_cast<float>(l.kl > 0.f ? v[0] + static_cast<double>(l.kl) * v[1] : v[0]);
+        o[1] = static_cast<float>(v[0]);
+        o[2] = static_cast<float>(v[1]);
+        o[3] = static_cast<float>(v[2]);
+    }
+}
+
+cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
+{
+    Launch k(KK_REDUCE, st);
+    return launch(seq_scalars_kernel, dim3(1), dim3(1024), 0, st, l, w);
+}
+
+namespace {
+
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t *p, float v) { *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f)); }
+__device__ __forceinline__ void put(h16_t *p, float v) { p->bits = static_cast<uint16_t>(pack_f16x2(v, 0.f)); }
+__device__ __forceinline__ void put4(float *p, const float (&v)[4])
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void put4(uint16_t *p, const float (&v)[4])
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void put4(h16_t *p, const float (&v)[4])
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
+}
+
+} // namespace
+
+// Four elements per thread where d_model is a multiple of 4, else one.  The
+// splits are added in their order.
+template <typename O, int N>
+__global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqScratch w, const float *__restrict__ part,
+                                                     int64_t nsplit, int64_t d, const uint16_t *__restrict__ W, int fused,
+                                                     const int *only_if, O *out, int add, int by_row)
+{
+    wait_for_stream();
+    if (refused(w.hdr)) return;
+    if (only_if && !*reinterpret_cast<const volatile int *>(only_if)) return;
+    const int64_t dn = d / N, count = l.n_tok * dn, plane = l.n_tok * d;
+    bool bad = false;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < count; i += int64_t(256) * gridDim.x) {
+        const int64_t t = i / dn, k = (i - t * dn) * N;
+        const int c = w.slot[t];
+        float v[N] = {};
+        if (c >= 0) {
+            const float *p = part + (by_row ? t : c) * d + k;
+            auto load = [&](int64_t s, float (&x)[N]) {
+                if constexpr (N == 4) {
+                    const float4 q = __ldcs(reinterpret_cast<const float4 *>(p + s * plane));
+                    x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
+                } else {
+                    x[0] = __ldcs(p + s * plane);
+                }
+            };
+            int64_t s = 0;
+            for (; s + 8 <= nsplit; s += 8) {
+                float x[8][N];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) load(s + q, x[q]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) v[e] += x[q][e];
+            }
+            for (; s < nsplit; ++s) {
+                float x[N];
+                load(s, x);
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] += x[e];
+            }
+            if (fused) {
+                if constexpr (N == 4) {
+                    // (the fused pass runs on bf16 inputs)
+                    const float a = w.tokp[c].y, az = a / w.z[c];
+                    const uint2 b = *reinterpret_cast<const uint2 *>(W + w.y[c] * d + k);
+                    const float wv[4] = {h16_lo<false>(b.x), h16_hi<false>(b.x), h16_lo<false>(b.y), h16_hi<false>(b.y)};
+#pragma unroll
+                    for (int e = 0; e < N; ++e) v[e] = a == 0.f ? 0.f : fmaf(az, v[e], -a * wv[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < N; ++e) bad |= !isfinite(v[e]);
+            }
+        }
+        O *o = out + t * d + k;
+        if constexpr (std::is_same<O, float>::value) {
+            if (add) {
+                if (c < 0) continue;
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] += o[e];
+            }
+        }
+        if constexpr (N == 4) put4(o, v);
+        else put(o, v[0]);
+    }
+    if (bad) w.hdr->redo = 1;
+}
+
+template <typename O>
+static cudaError_t dh_one(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t nsplit, int64_t d,
+                          const void *W, bool fused, const int *only_if, void *out, bool add, bool by_row,
+                          cudaStream_t st)
+{
+    const bool four = d % 4 == 0;
+    int64_t grid = (l.n_tok * (four ? d / 4 : d) + 255) / 256;
+    if (grid > 4096) grid = 4096;
+    return launch(four ? seq_dh_kernel<O, 4> : seq_dh_kernel<O, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st,
+                  l, w, part, nsplit, d, static_cast<const uint16_t *>(W), fused ? 1 : 0, only_if,
+                  static_cast<O *>(out), add ? 1 : 0, by_row ? 1 : 0);
+}
+
+cudaError_t launch_seq_dh(int out_dtype, const SeqLoss &l, const SeqScratch &w, const float *part, int64_t nsplit,
+                          int64_t d, const void *W, bool fused, const int *only_if, void *out, bool add, bool by_row,
+                          cudaStream_t st)
+{
+    Launch k(KK_SEQ_DH, st);
+    if (out_dtype == LOSSK_F32) return dh_one<float>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, st);
+    if (out_dtype == LOSSK_F16) return dh_one<h16_t>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, st);
+    return dh_one<uint16_t>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, st);
+}
+
+} // namespace lossk

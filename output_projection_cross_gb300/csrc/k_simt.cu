@@ -1662,15 +1662,25 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                                                  float *__restrict__ part, float *__restrict__ tgt,
                                                  int64_t part_stride, int64_t part_plane,
                                                  float *__restrict__ out, int64_t out_split_stride,
-                                                 int accumulate)
+                                                 int accumulate, const int *__restrict__ n_dev,
+                                                 const int *__restrict__ refused)
 {
+    if (refused && *reinterpret_cast<const volatile int *>(refused)) return;
     __shared__ float xs[FP_BK][FP_BM + 4];
     __shared__ float ys[FP_BK][FP_BN + 4];
     __shared__ float gs[FP_BM][FP_BN + 1];
     __shared__ float yv[FP_BN][FP_SLICE + 4];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const float L2E = static_cast<float>(LOG2E);
-    const int n_xt = (n_x + FP_BM - 1) / FP_BM, n_yt = (n_y + FP_BN - 1) / FP_BN;
+    // (the label loss; distillation scales by inv_t on its own)
+    const float L2E = DISTILL ? static_cast<float>(LOG2E) : static_cast<float>(LOG2E) * inv_t;
+    const int n_xt = (n_x + FP_BM - 1) / FP_BM;
+    // the launch's tokens, or as many as an earlier kernel gathered
+    if (n_dev) {
+        n_tok = min(n_tok, *n_dev);
+        if (MODE == TC_COLS) n_y = n_tok;
+        else n_x = n_tok;
+    }
+    const int n_yt = (n_y + FP_BN - 1) / FP_BN;
 
     int xt, yt_begin, yt_end, slice = 0, split = 0;
     if (MODE == TC_STATS) {
@@ -1688,6 +1698,7 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
         yt_end = static_cast<int>((static_cast<int64_t>(split + 1) * n_yt) / n_split);
     }
     const int xrow0 = xt * FP_BM;
+    if (xrow0 >= n_x) return;
     float acc[4][4] = {};
     // STATS: the logits are compensated dot products (Dot2 of Ogita, Rump and
     // Oishi, "Accurate sum and dot product", SIAM J. Sci. Comput. 26 (2005)):
@@ -1884,7 +1895,7 @@ cudaError_t launch_fp(int mode, bool distill, const void *X, const void *Y, cons
                       float inv_t, const int64_t *targets, const float4 *tokp, const double2 *tstat,
                       float *part,
                       float *tgt, int64_t part_stride, int64_t part_plane, float *out,
-                      int64_t out_split_stride, cudaStream_t st, bool accumulate)
+                      int64_t out_split_stride, cudaStream_t st, bool accumulate, const int *n_dev, const int *refused)
 {
     const int n_xt = (n_x + FP_BM - 1) / FP_BM, n_yt = (n_y + FP_BN - 1) / FP_BN;
     const int n_sl = (d + FP_SLICE - 1) / FP_SLICE;
@@ -1895,7 +1906,7 @@ cudaError_t launch_fp(int mode, bool distill, const void *X, const void *Y, cons
 #define LOSSK_FP(M, D)                                                                             \
     fp_kernel<M, D><<<grid, 256, 0, st>>>(x, y, teach, n_x, n_y, d, n_tok, vocab, n_split,       \
                                           direction, inv_t, targets, tokp, tstat, part, tgt, part_stride, \
-                                          part_plane, out, out_split_stride, accumulate ? 1 : 0)
+                                          part_plane, out, out_split_stride, accumulate ? 1 : 0, n_dev, refused)
     if (mode == TC_STATS) {
         if (distill) LOSSK_FP(TC_STATS, true); else LOSSK_FP(TC_STATS, false);
     } else if (mode == TC_ROWS) {

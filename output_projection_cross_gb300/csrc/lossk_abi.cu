@@ -3,7 +3,7 @@
 // documented order, workspace layout, tensor-map encoding and the launch
 // sequence of each call.  No device memory is allocated here.
 #include "../../include/lossk.h"
-#include "lossk_internal.h"
+#include "host_internal.h"
 
 #include <atomic>
 #include <cstddef>
@@ -14,18 +14,7 @@
 
 using namespace lossk;
 
-namespace {
-
-// Ceilings: 2^46 work cells and 2^27 logit cells are the pages' constants
-// ("Loss functions and resident-context kernels", lossk function table); the
-// per-dimension ceiling 2^24 is this library's reading of the unprinted one.
-constexpr int64_t MAX_WORK_CELLS = int64_t(1) << 46;
-constexpr int64_t MAX_LOGIT_CELLS = int64_t(1) << 27;
-constexpr int64_t MAX_DIM = int64_t(1) << 24;
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace lossk {
 
 int sm_count()
 {
@@ -40,6 +29,8 @@ int sm_count()
     }
     return cached[dev];
 }
+
+namespace {
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link
 // against libcuda).
@@ -62,6 +53,8 @@ EncodeTiledFn encode_fn()
     });
     return fn;
 }
+
+} // namespace
 
 // A 2-D bf16 tensor [outer][inner] read in boxes of {box_inner, box_outer}
 // without swizzle (row-major in shared memory); out-of-range elements read as zero.
@@ -130,6 +123,21 @@ bool make_map_out_f32(CUtensorMap *m, void *base, int64_t inner, int64_t outer)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A 16-bit [outer][inner] output written by 32 x 32 boxes from 64-byte-
+// swizzled shared memory (inner % 8 == 0, so rows are 16-byte multiples).
+bool make_map_out_16(CUtensorMap *m, void *base, int64_t inner, int64_t outer)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || inner % 8 != 0) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // fp32 [planes][rows][inner] (a d_hidden pass's partial slabs, or d_hidden itself),
 // 32 x 32 boxes of one plane: a box's rows past `rows` are clipped, never
 // written into the next plane.
@@ -161,6 +169,68 @@ bool make_map_blocks(CUtensorMap *m, const void *base, int64_t inner, int64_t ou
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+bool bwd_args(const BwdScratch &w, bool rows, int64_t n, int64_t d, int64_t V, const void *H, const void *W,
+              BwdArgs *a)
+{
+    std::memset(a, 0, sizeof(*a));
+    const void *Fx = rows ? H : W, *Lp = rows ? W : H;
+    const int64_t nf = rows ? n : V, nl = rows ? V : n;
+    const BwdGeom g = bwd_geometry(d, false);
+    // a CTA of a pair loads its 128 fixed rows, half of the loop supertile and
+    // half of the d-slice
+    if (!make_map(&a->map_fix, Fx, d, nf, 64, 128) || !make_map(&a->map_loop, Lp, d, nl, 64, BWD_BN / 2) ||
+        !make_map(&a->map_ys, Lp, d, nl, 64, 64) || !make_map(&a->map_g, w.gring, 128, G_RING_ROWS, 64, 128))
+        return false;
+    a->ys3 = make_map_blocks(&a->map_ys3, Lp, d, nl, 64, 2) ? 1 : 0;
+    a->g_tma = make_map_ring_store(&a->map_gst, w.gring, G_RING_ROWS) ? 1 : 0;
+    a->gscr = w.gring;
+    a->gsig = w.gsig;
+    a->n_tok = static_cast<int>(n);
+    a->vocab = static_cast<int>(V);
+    a->d = static_cast<int>(d);
+    a->n_fixed = static_cast<int>(cdiv(nf, 256));
+    a->n_loop = static_cast<int>(cdiv(nl, BWD_BN));
+    a->n_split = 1;
+    a->n_cl = g.n_cl;
+    a->n_dg = g.n_dg;
+    a->tokp = w.tokp;
+    a->out_split_stride = n * d;
+    a->err = &w.hdr->err;
+    a->refused = &w.hdr->bad_targets;
+    return true;
+}
+
+constexpr int SIDE_PER_DEV = 8;
+
+SideStream *side_stream(cudaStream_t caller)
+{
+    static SideStream sides[64][SIDE_PER_DEV];
+    static std::mutex table_mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    std::lock_guard<std::mutex> g(table_mu);
+    for (int i = 0; i < SIDE_PER_DEV; ++i)
+        if (sides[dev][i].used && sides[dev][i].owner == caller) return &sides[dev][i];
+    for (int i = 0; i < SIDE_PER_DEV; ++i)
+        if (!sides[dev][i].used) {
+            sides[dev][i].used = true;
+            sides[dev][i].owner = caller;
+            return &sides[dev][i];
+        }
+    return nullptr;
+}
+
+} // namespace lossk
+
+namespace {
+
+// Ceilings: 2^46 work cells and 2^27 logit cells are the pages' constants
+// ("Loss functions and resident-context kernels", lossk function table); the
+// per-dimension ceiling 2^24 is this library's reading of the unprinted one.
+constexpr int64_t MAX_WORK_CELLS = int64_t(1) << 46;
+constexpr int64_t MAX_LOGIT_CELLS = int64_t(1) << 27;
+constexpr int64_t MAX_DIM = int64_t(1) << 24;
 
 // ---- tracing: launch counter and optional per-kernel event timing ------------
 std::atomic<int64_t> g_launches{0};
@@ -301,39 +371,7 @@ struct Ws {
     float *dhacc() const { return reinterpret_cast<float *>(base + L.off_dhacc); }
 };
 
-// Tensor maps and shape fields of a cluster pass.  rows: d_hidden / fused
-// (fixed = hidden token tiles, loop = vocabulary); otherwise d_weight (fixed =
-// weight vocabulary tiles, loop = tokens).
-bool bwd_args(const Ws &w, bool rows, int64_t n, int64_t d, int64_t V, const void *H, const void *W,
-              BwdArgs *a)
-{
-    std::memset(a, 0, sizeof(*a));
-    const void *Fx = rows ? H : W, *Lp = rows ? W : H;
-    const int64_t nf = rows ? n : V, nl = rows ? V : n;
-    const BwdGeom g = bwd_geometry(d, false);
-    // a CTA of a pair loads its 128 fixed rows, half of the loop supertile and
-    // half of the d-slice
-    if (!make_map(&a->map_fix, Fx, d, nf, 64, 128) || !make_map(&a->map_loop, Lp, d, nl, 64, BWD_BN / 2) ||
-        !make_map(&a->map_ys, Lp, d, nl, 64, 64) || !make_map(&a->map_g, w.gring(), 128, G_RING_ROWS, 64, 128))
-        return false;
-    a->ys3 = make_map_blocks(&a->map_ys3, Lp, d, nl, 64, 2) ? 1 : 0;
-    a->g_tma = make_map_ring_store(&a->map_gst, w.gring(), G_RING_ROWS) ? 1 : 0;
-    a->gscr = w.gring();
-    a->gsig = w.gsig();
-    a->n_tok = static_cast<int>(n);
-    a->vocab = static_cast<int>(V);
-    a->d = static_cast<int>(d);
-    a->n_fixed = static_cast<int>(cdiv(nf, 256));
-    a->n_loop = static_cast<int>(cdiv(nl, BWD_BN));
-    a->n_split = 1;
-    a->n_cl = g.n_cl;
-    a->n_dg = g.n_dg;
-    a->tokp = w.tokp();
-    a->out_split_stride = n * d;
-    a->err = &w.hdr()->err;
-    a->refused = &w.hdr()->bad_targets;
-    return true;
-}
+BwdScratch bwd_scratch(const Ws &w) { return BwdScratch{w.gring(), w.gsig(), w.tokp(), w.hdr()}; }
 
 // ---- the forward statistics pass + merge + reduction (label CE) ------------
 int32_t run_ce_fwd(const Ws &w, int64_t n, int64_t d, int64_t V, int32_t dtype, const void *H,
@@ -363,6 +401,7 @@ int32_t run_ce_fwd(const Ws &w, int64_t n, int64_t d, int64_t V, int32_t dtype, 
         a.n_xt = static_cast<int>(cdiv(n, TC_BM));
         a.n_yt = static_cast<int>(L.n_ct);
         a.n_items = static_cast<int>(cdiv(a.n_xt, 2)) * a.n_yt;
+        a.inv_t_l2e = static_cast<float>(LOG2E);
         a.targets = targets;
         a.part = w.part();
         a.tgt = w.tgt();
@@ -407,7 +446,7 @@ int32_t run_acc(const Ws &w, int64_t n, int64_t d, int64_t V, int32_t dtype, con
             const bool rows = pass == 0;
             BwdArgs a;
             if (!rows && pre_cols) a = *pre_cols;
-            else if (!bwd_args(w, rows, n, d, V, H, W, &a)) return LOSSK_DEVICE_ERROR;
+            else if (!bwd_args(bwd_scratch(w), rows, n, d, V, H, W, &a)) return LOSSK_DEVICE_ERROR;
             a.teacher = distill ? static_cast<const uint16_t *>(teacher) : nullptr;
             if (distill && !rows && !make_map_plain(&a.map_teach, teacher, V, n, 32, 32))
                 return LOSSK_DEVICE_ERROR;
@@ -471,54 +510,6 @@ int32_t run_acc(const Ws &w, int64_t n, int64_t d, int64_t V, int32_t dtype, con
 // less than the separate forward and d_hidden passes.  A row whose shifted
 // terms left the trusted range raises the workspace's redo word; the caller
 // then recomputes everything on the separate passes.
-// A helper stream per (device, caller stream): the training step's small
-// kernels that nothing after them waits for (the token mean, d_hidden's
-// combine) run on it beside the d_weight pass, on the SMs its groups leave
-// free; the call joins it back into the caller's stream before it returns.
-// Calls on different caller streams get different helper streams, so neither
-// waits for the other's helper work.  Up to SIDE_PER_DEV caller streams per
-// device get one; a call on a further stream runs those kernels on its own
-// stream (the same results, without the overlap).
-struct SideStream {
-    std::mutex mu;
-    cudaStream_t owner = nullptr;      // the caller stream this helper serves
-    bool used = false;
-    cudaStream_t s = nullptr;
-    cudaEvent_t fork = nullptr, join = nullptr;
-    bool ready()
-    {
-        if (s) return true;
-        if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess ||
-            cudaEventCreateWithFlags(&fork, cudaEventDisableTiming) != cudaSuccess ||
-            cudaEventCreateWithFlags(&join, cudaEventDisableTiming) != cudaSuccess) {
-            (void)cudaGetLastError();
-            s = nullptr;
-            return false;
-        }
-        return true;
-    }
-};
-
-constexpr int SIDE_PER_DEV = 8;
-
-SideStream *side_stream(cudaStream_t caller)
-{
-    static SideStream sides[64][SIDE_PER_DEV];
-    static std::mutex table_mu;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    std::lock_guard<std::mutex> g(table_mu);
-    for (int i = 0; i < SIDE_PER_DEV; ++i)
-        if (sides[dev][i].used && sides[dev][i].owner == caller) return &sides[dev][i];
-    for (int i = 0; i < SIDE_PER_DEV; ++i)
-        if (!sides[dev][i].used) {
-            sides[dev][i].used = true;
-            sides[dev][i].owner = caller;
-            return &sides[dev][i];
-        }
-    return nullptr;
-}
-
 int32_t run_fused(const Ws &w, int64_t n, int64_t d, int64_t V, const void *H, const void *W,
                   const int64_t *targets, const uint8_t *mask, double wz, double gs,
                   float *lse_out, float *ce_out, double *scalars, float *d_hidden, cudaStream_t st,
@@ -531,7 +522,7 @@ int32_t run_fused(const Ws &w, int64_t n, int64_t d, int64_t V, const void *H, c
     const BwdGeom g = bwd_geometry(d, false);
     BwdArgs a;
     if (pre) a = *pre;
-    else if (!bwd_args(w, true, n, d, V, H, W, &a)) return LOSSK_DEVICE_ERROR;
+    else if (!bwd_args(bwd_scratch(w), true, n, d, V, H, W, &a)) return LOSSK_DEVICE_ERROR;
     a.n_split = static_cast<int>(L.nsplit);
     a.inv_t_l2e = static_cast<float>(LOG2E);
     float *part = L.nsplit > 1 ? w.dhpart() : d_hidden;
@@ -905,7 +896,7 @@ static int32_t ce_common(bool do_fwd, bool do_bwd, int64_t n, int64_t d, int64_t
                 return LOSSK_DEVICE_ERROR;
         }
         BwdArgs fa, ca;
-        if (!bwd_args(w, true, n, d, V, H, W, &fa) || (dW && !bwd_args(w, false, n, d, V, H, W, &ca)))
+        if (!bwd_args(bwd_scratch(w), true, n, d, V, H, W, &fa) || (dW && !bwd_args(bwd_scratch(w), false, n, d, V, H, W, &ca)))
             return LOSSK_DEVICE_ERROR;
         float *dh_fused = acc ? w.dhacc() : dH;
         SideStream *sd = acc ? nullptr : side_stream(st);
@@ -1285,6 +1276,7 @@ int32_t lossk_ce_shard_fwd(int64_t n, int64_t d, int64_t Vs, int64_t v0, int64_t
         a.n_xt = static_cast<int>(cdiv(n, TC_BM));
         a.n_yt = static_cast<int>(L.n_ct);
         a.n_items = static_cast<int>(cdiv(a.n_xt, 2)) * a.n_yt;
+        a.inv_t_l2e = static_cast<float>(LOG2E);
         a.part = w.part();
         a.part_stride = L.n_pad;
         a.part_plane = L.n_ct * L.n_pad;
@@ -1406,7 +1398,9 @@ const char *lossk_kernel_name(int32_t kind)
                                       "combine_dh",   "teacher_stats", "distill_logits", "readback",
                                       "wait_selftest", "shard_tgt",    "shard_combine", "beam_rows",    "beam_merge",
                                       "beam_gather",  "cache_fork",    "cache_plan",    "cache_copy",   "cache_free",
-                                      "cache_rank",   "cache_write",   "attn_plan",     "attn",         "attn_join"};
+                                      "cache_rank",   "cache_write",   "attn_plan",     "attn",         "attn_join",
+                                      "seq_prep",      "seq_gather",    "seq_stats",    "seq_merge",    "seq_sum",
+                                      "seq_coef",      "seq_grad",      "seq_dh"};
     return (kind >= 0 && kind < KK_N) ? names[kind] : "unknown_kernel";
 }
 

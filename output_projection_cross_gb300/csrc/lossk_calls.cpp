@@ -22,7 +22,8 @@ namespace {
 
 #define LOSSK_CALLS(X)                                                                                                \
     X(lossk_beam_select) X(lossk_beam_gather) X(lossk_cache_fork) X(lossk_cache_reserve) X(lossk_cache_free)          \
-    X(lossk_cache_compact) X(lossk_cache_copy) X(lossk_cache_write) X(lossk_paged_attn)
+    X(lossk_cache_compact) X(lossk_cache_copy) X(lossk_cache_write) X(lossk_paged_attn)          \
+    X(lossk_policy_fwd_bwd) X(lossk_policy_from_logits) X(lossk_preference_fwd_bwd) X(lossk_preference_from_logits)
 
 enum Call {
 #define X(name) CALL_##name,

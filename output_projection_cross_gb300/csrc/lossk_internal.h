@@ -30,6 +30,9 @@ struct WsHeader {
                       // lossk_status), pad[HDR_NEXT] a work counter, 0 between calls
 };
 constexpr int HDR_FAULT = 1, HDR_NEXT = 2;
+// The sequence losses' calls: sequences with a counted token (policy) or pairs that count
+// (preference), counted tokens of chosen sequences, bits of the largest |coefficient|.
+constexpr int HDR_GROUPS = 3, HDR_CHOSEN = 4, HDR_COEF = 5;
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
 // Per-(token, logit tile) partial statistics written by the forward pass
@@ -84,6 +87,9 @@ struct TcArgs {
     int n_split;           // ROWS: vocabulary splits
     int direction;         // distillation objective
     float inv_t_l2e;       // log2(e) / temperature
+    const int *n_dev;      // or NULL: the tokens there are, found by an earlier kernel (at most n_tok)
+    const int *refused;    // or NULL; nonzero: the validation before found a bad target; return at once
+    const int *only_if;    // or NULL; zero: the pass is not needed, return at once
     const int64_t *targets;
     const uint16_t *teacher; // distillation forward: teacher logits [n_tok][vocab] (bf16)
     const double2 *tstat;  // distillation forward: per token (lse_t2, Eb) from teacher_stats
@@ -145,7 +151,12 @@ struct BwdArgs {
     int64_t zpart_stride;
     int accumulate;        // add the accumulator into `out` instead of overwriting it
     float out_scale;       // fp16 operands: the factor the stored accumulator is multiplied by
+    const unsigned *coef_max;  // fp16 operands, or NULL: the bits of the largest |coefficient| among the tokens (label
+                           // loss); the passes then scale by a power of two of their own instead of out_scale
+    int out16;             // d_weight: map_out is a 16-bit tensor, box {32, 32} (label loss, no accumulation)
+    const int *n_dev;      // or NULL: the tokens there are, found by an earlier kernel (at most n_tok)
     const int *refused;    // nonzero: the validation before found a bad target; return at once
+    const int *only_if;    // or NULL; zero: the pass is not needed, return at once
     unsigned *gsig;        // grad-tile ring hand-off counters [2][G_MAX_CTAS][G_SLOTS] (ready, free)
     int *err;
 };
@@ -197,6 +208,14 @@ enum KernelKind : int {
     KK_ATTN_PLAN,
     KK_ATTN,
     KK_ATTN_JOIN,
+    KK_SEQ_PREP,
+    KK_SEQ_GATHER,
+    KK_SEQ_STATS,
+    KK_SEQ_MERGE,
+    KK_SEQ_SUM,
+    KK_SEQ_COEF,
+    KK_SEQ_GRAD,
+    KK_SEQ_DH,
     KK_N
 };
 
@@ -252,7 +271,8 @@ cudaError_t launch_fp(int mode, bool distill, const void *X, const void *Y, cons
                       float inv_t, const int64_t *targets, const float4 *tokp, const double2 *tstat,
                       float *part,
                       float *tgt, int64_t part_stride, int64_t part_plane, float *out,
-                      int64_t out_split_stride, cudaStream_t st, bool accumulate = false);
+                      int64_t out_split_stride, cudaStream_t st, bool accumulate = false,
+                      const int *n_dev = nullptr, const int *refused = nullptr);
 // precise: exact exp2 rescales (the fp32 inputs path); else ex2.approx.
 cudaError_t launch_merge_ce(const float *part, const float *tgt, const int64_t *targets,
                             const uint8_t *mask, int64_t n, int64_t n_ct, int64_t n_pad,

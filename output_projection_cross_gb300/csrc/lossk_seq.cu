@@ -1,0 +1,521 @@
+// lossk_seq.cu -- the extern "C" entry points of the losses of sampled and
+// compared sequences (declared in include/lossk.h): argument checks in the
+// documented order, workspace layout and launch sequence.  No call synchronises
+// and none allocates device memory.
+#include "../../include/lossk.h"
+#include "host_internal.h"
+#include "seq_internal.h"
+
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+using namespace lossk;
+
+namespace {
+
+constexpr int64_t MAX_DIM = int64_t(1) << 24;
+
+bool is16(int32_t dtype) { return dtype == LOSSK_BF16 || dtype == LOSSK_F16; }
+bool dtype_ok(int32_t dtype) { return dtype == LOSSK_F32 || is16(dtype); }
+
+struct Layout {
+    int64_t n_pad, n_ct, nsplit;
+    int splits;
+    size_t off_slot, off_row, off_y, off_seq, off_tgt, off_lp, off_lse2, off_z, off_tokp, off_sum, off_slope, off_acc,
+        off_pair, off_rows, off_hidden, off_part, off_dhpart, off_zpart, off_gring, off_gsig, off_dhacc, total;
+};
+
+// 580, or why there is no layout.
+int32_t layout(int32_t kind, int64_t n, int64_t d, int64_t V, int64_t n_seq, int32_t dtype, Layout *L)
+{
+    const bool head = kind == LOSSK_KIND_SEQUENCE_HEAD;
+    const int32_t s = lossk_dims_check(n, head ? d : 1, V);
+    if (s != LOSSK_OK) return s;
+    if (n_seq < 0) return LOSSK_EMPTY_DIMENSION;
+    if (n_seq > 2 * MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    if (!dtype_ok(dtype)) return LOSSK_LENGTH_MISMATCH;
+    std::memset(L, 0, sizeof(*L));
+    L->n_pad = cdiv(n, 256) * 256;
+    const size_t np = static_cast<size_t>(L->n_pad), ns = static_cast<size_t>(n_seq);
+    size_t off = 256;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    L->off_slot = take(sizeof(int) * np);
+    L->off_row = take(sizeof(int) * np);
+    L->off_y = take(sizeof(int64_t) * np);
+    L->off_seq = take(sizeof(int) * (ns + 1));
+    L->off_tgt = take(sizeof(float) * np);
+    L->off_lp = take(sizeof(float) * np);
+    L->off_lse2 = take(sizeof(float) * np);
+    L->off_z = take(sizeof(float) * np);
+    L->off_tokp = take(sizeof(float4) * np);
+    L->off_sum = take(sizeof(double) * ns);
+    L->off_slope = take(sizeof(double) * ns);
+    L->off_acc = take(sizeof(double) * 3 * np);
+    L->off_pair = take(sizeof(double) * (ns + 1));
+    if (head) {
+        const bool tc = is16(dtype);
+        L->n_ct = cdiv(V, tc ? TC_BN_FWD : FP_BN);
+        L->nsplit = dh_splits(n, d, V, dtype);
+        const size_t nd = static_cast<size_t>(n) * static_cast<size_t>(d);
+        L->off_hidden = take((tc ? 2 : 4) * np * static_cast<size_t>(d));
+        L->off_part = take(sizeof(float) * NSTAT_CE * static_cast<size_t>(L->n_ct) * np);
+        L->off_dhpart = take(sizeof(float) * static_cast<size_t>(L->nsplit) * nd);
+        if (dtype == LOSSK_BF16) {
+            L->off_zpart = take(sizeof(float) * static_cast<size_t>(L->nsplit) * BWD_MAX_CL * np);
+            L->off_dhacc = take(sizeof(float) * nd);
+        }
+        if (tc) {
+            L->off_gring = take(sizeof(uint16_t) * 128 * static_cast<size_t>(G_RING_ROWS));
+            L->off_gsig = take(sizeof(unsigned) * 2 * G_MAX_CTAS * G_SLOTS);
+        }
+    } else {
+        L->splits = seq_stat_splits(n, V, dtype);
+        L->off_rows = take(sizeof(float2) * np * static_cast<size_t>(L->splits));
+    }
+    L->total = off;
+    return LOSSK_OK;
+}
+
+SeqScratch scratch(const Layout &L, void *ws, int64_t n_pairs)
+{
+    uint8_t *b = static_cast<uint8_t *>(ws);
+    SeqScratch w;
+    std::memset(&w, 0, sizeof(w));
+    w.hdr = reinterpret_cast<WsHeader *>(b);
+    w.slot = reinterpret_cast<int *>(b + L.off_slot);
+    w.row = reinterpret_cast<int *>(b + L.off_row);
+    w.y = reinterpret_cast<int64_t *>(b + L.off_y);
+    w.seq_slot = reinterpret_cast<int *>(b + L.off_seq);
+    w.tgt = reinterpret_cast<float *>(b + L.off_tgt);
+    w.lp = reinterpret_cast<float *>(b + L.off_lp);
+    w.lse2 = reinterpret_cast<float *>(b + L.off_lse2);
+    w.z = reinterpret_cast<float *>(b + L.off_z);
+    w.tokp = reinterpret_cast<float4 *>(b + L.off_tokp);
+    w.sum = reinterpret_cast<double *>(b + L.off_sum);
+    w.slope = reinterpret_cast<double *>(b + L.off_slope);
+    w.acc = reinterpret_cast<double *>(b + L.off_acc);
+    w.pair = reinterpret_cast<double *>(b + L.off_pair);
+    w.part = reinterpret_cast<float2 *>(b + L.off_rows);
+    w.n_pad = L.n_pad;
+    (void)n_pairs;
+    return w;
+}
+
+// One call of either loss in either form.
+struct Call {
+    bool head;
+    int64_t n, d, V, n_seq, n_pairs;      // n_pairs 0: the policy loss
+    int32_t dtype;
+    const void *X;                        // hidden or logits
+    int64_t x_len;
+    const void *W;
+    int64_t w_len;
+    const int64_t *targets;
+    int64_t targets_len;
+    const uint8_t *mask;
+    const int32_t *first;
+    int64_t first_len;
+    const float *adv, *old, *ref;
+    int64_t adv_len, old_len, ref_len;
+    double low, high, kl, temperature, beta, margin, smooth, nll, grad_scale;
+    int32_t objective;
+    uint32_t flags;
+    float *scalars, *per_item, *log_ratio, *logp;
+    int32_t grad_dtype;
+    void *g0, *g1;                        // d_hidden and d_weight, or grad_logits
+    int64_t g_len;
+    void *ws;
+    int64_t ws_bytes;
+    cudaStream_t st;
+};
+
+bool finite(std::initializer_list<double> v)
+{
+    for (double x : v)
+        if (!std::isfinite(x)) return false;
+    return true;
+}
+
+int32_t check(const Call &c, Layout *L)
+{
+    const bool pref = c.n_pairs != 0;
+    if (pref && (c.n_pairs < 1 || c.n < 1)) return LOSSK_EMPTY_DIMENSION;
+    if (c.n_pairs > MAX_DIM || c.n_seq > 2 * MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    const int32_t s = layout(c.head ? LOSSK_KIND_SEQUENCE_HEAD : LOSSK_KIND_SEQUENCE_LOGITS, c.n, c.d, c.V, c.n_seq,
+                             c.dtype, L);
+    if (s != LOSSK_OK) return s;
+    const int64_t cells = c.n * (c.head ? c.d : c.V);
+    if (!c.X || c.x_len < cells || (c.head && (!c.W || c.w_len < c.V * c.d)) || !c.targets || c.targets_len < c.n ||
+        !c.scalars || !c.ws || c.ws_bytes < static_cast<int64_t>(L->total))
+        return LOSSK_LENGTH_MISMATCH;
+    if (!c.head && c.g0 && c.g_len < cells) return LOSSK_LENGTH_MISMATCH;
+    if (c.head && c.grad_dtype != LOSSK_F32 && c.grad_dtype != c.dtype) return LOSSK_LENGTH_MISMATCH;
+    if ((c.first != nullptr) != (c.n_seq > 0) || (c.first && c.first_len < c.n_seq + 1)) return LOSSK_LENGTH_MISMATCH;
+    if ((c.old && c.old_len < c.n) || (c.ref && c.ref_len < c.n)) return LOSSK_LENGTH_MISMATCH;
+    if (!pref) {
+        const uint32_t need = LOSSK_SEQ_RATIO | LOSSK_SEQ_MEAN | LOSSK_SEQ_ADVANTAGES;
+        if ((c.flags & need) && !c.first) return LOSSK_LENGTH_MISMATCH;
+        if (!c.adv || c.adv_len < ((c.flags & LOSSK_SEQ_ADVANTAGES) ? c.n_seq : c.n)) return LOSSK_LENGTH_MISMATCH;
+        if (c.kl > 0.0 && !c.ref) return LOSSK_LENGTH_MISMATCH;
+    }
+    if (!aligned16(c.X) || (c.head && !aligned16(c.W)) || (c.g0 && !aligned16(c.g0)) || (c.g1 && !aligned16(c.g1)) ||
+        (reinterpret_cast<uintptr_t>(c.ws) & 255u) || (c.head && is16(c.dtype) && c.d % 8 != 0))
+        return LOSSK_UNALIGNED;
+    if (!finite({c.grad_scale})) return LOSSK_NON_FINITE_SCALAR;
+    if (pref) {
+        if (!finite({c.beta, c.margin, c.smooth, c.nll}) || c.beta <= 0.0 || c.smooth < 0.0 || c.smooth > 1.0 ||
+            c.nll < 0.0)
+            return LOSSK_NON_FINITE_SCALAR;
+        if (c.objective < LOSSK_PREF_SIGMOID || c.objective > LOSSK_PREF_SQUARED) return LOSSK_UNKNOWN_OBJECTIVE;
+        if (c.objective != LOSSK_PREF_SIGMOID && (c.margin != 0.0 || c.smooth != 0.0)) return LOSSK_NON_FINITE_SCALAR;
+    } else if (!finite({c.low, c.high, c.kl, c.temperature}) || c.low < 0.0 || c.low > 1.0 || c.high < 0.0 ||
+               c.kl < 0.0 || c.temperature <= 0.0) {
+        return LOSSK_NON_FINITE_SCALAR;
+    }
+    const uint32_t known = LOSSK_ACCUMULATE_GRADS | LOSSK_REDUCE_SUM |
+                           (pref ? LOSSK_LENGTH_MEAN : LOSSK_SEQ_RATIO | LOSSK_SEQ_MEAN | LOSSK_SEQ_ADVANTAGES);
+    if (c.flags & ~known) return LOSSK_UNKNOWN_FLAGS;
+    if (c.head && (c.flags & LOSSK_ACCUMULATE_GRADS) && (c.g0 || c.g1) && c.grad_dtype != LOSSK_F32)
+        return LOSSK_UNKNOWN_FLAGS;
+    return LOSSK_OK;
+}
+
+#define TRY(x)                                                                                                        \
+    do {                                                                                                              \
+        if ((x) != cudaSuccess) return LOSSK_DEVICE_ERROR;                                                            \
+    } while (0)
+
+// The forward statistics pass over the gathered rows (16-bit inputs).
+int32_t run_forward(const Call &c, const Layout &L, const SeqLoss &l, const SeqScratch &w, const void *hid,
+                    const int *only_if)
+{
+    uint8_t *b = static_cast<uint8_t *>(c.ws);
+    float *part = reinterpret_cast<float *>(b + L.off_part);
+    TcArgs a;
+    std::memset(&a, 0, sizeof(a));
+    if (!make_map(&a.map_x, hid, c.d, L.n_pad, 64, TC_BM) || !make_map(&a.map_y, c.W, c.d, c.V, 64, 128))
+        return LOSSK_DEVICE_ERROR;
+    a.n_x = a.n_tok = static_cast<int>(c.n);
+    a.n_y = a.vocab = static_cast<int>(c.V);
+    a.d = static_cast<int>(c.d);
+    a.n_xt = static_cast<int>(cdiv(c.n, TC_BM));
+    a.n_yt = static_cast<int>(L.n_ct);
+    a.n_items = static_cast<int>(cdiv(a.n_xt, 2)) * a.n_yt;
+    a.inv_t_l2e = l.k2;
+    a.n_dev = &w.hdr->n_valid;
+    a.refused = &w.hdr->bad_targets;
+    a.only_if = only_if;
+    a.part = part;
+    a.part_stride = L.n_pad;
+    a.part_plane = L.n_ct * L.n_pad;
+    a.err = &w.hdr->err;
+    const int pairs = a.n_items < sm_count() / 2 ? a.n_items : sm_count() / 2;
+    {
+        Launch k(KK_TC_STATS, c.st);
+        TRY(launch_fwd2(a, false, c.dtype == LOSSK_F16, 2 * pairs, c.st));
+    }
+    TRY(launch_seq_merge_tiles(l, w, part, L.n_ct, only_if, c.st));
+    return LOSSK_OK;
+}
+
+// What follows the log-probabilities: sums over sequences, coefficients.
+int32_t run_losses(const Call &c, const SeqLoss &l, const SeqScratch &w)
+{
+    if (l.pairs > 0 || (l.flags & LOSSK_SEQ_RATIO)) TRY(launch_seq_sum(l, w, c.st));
+    TRY(launch_seq_coef(l, w, c.st));
+    return LOSSK_OK;
+}
+
+int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScratch &w)
+{
+    uint8_t *b = static_cast<uint8_t *>(c.ws);
+    void *hid = b + L.off_hidden;
+    float *part = reinterpret_cast<float *>(b + L.off_part);
+    float *dhpart = reinterpret_cast<float *>(b + L.off_dhpart);
+    const bool acc = (c.flags & LOSSK_ACCUMULATE_GRADS) != 0, f16 = c.dtype == LOSSK_F16;
+    const int *n_dev = &w.hdr->n_valid, *bad = &w.hdr->bad_targets;
+    const int n = static_cast<int>(c.n), V = static_cast<int>(c.V), d = static_cast<int>(c.d);
+    cudaStream_t st = c.st;
+    TRY(launch_seq_gather(c.dtype, l, w, c.X, c.W, c.d, hid, st));
+    if (!is16(c.dtype)) {
+        const float inv_t = static_cast<float>(1.0 / c.temperature);
+        {
+            Launch k(KK_FP_STATS, st);
+            TRY(launch_fp(TC_STATS, false, hid, c.W, nullptr, n, V, d, n, V, 1, 0, inv_t, w.y, nullptr, nullptr, part,
+                          w.tgt, L.n_pad, L.n_ct * L.n_pad, nullptr, 0, st, false, n_dev, bad));
+        }
+        TRY(launch_seq_merge_tiles(l, w, part, L.n_ct, nullptr, st));
+        int32_t s = run_losses(c, l, w);
+        if (s != LOSSK_OK) return s;
+        TRY(launch_seq_scalars(l, w, st));
+        if (c.g0) {
+            {
+                Launch k(KK_FP_ROWS, st);
+                TRY(launch_fp(TC_ROWS, false, hid, c.W, nullptr, n, V, d, n, V, static_cast<int>(L.nsplit), 0, inv_t,
+                              nullptr, w.tokp, nullptr, nullptr, nullptr, 0, 0, dhpart, c.n * c.d, st, false, n_dev,
+                              bad));
+            }
+            TRY(launch_seq_dh(LOSSK_F32, l, w, dhpart, L.nsplit, c.d, c.W, false, nullptr, c.g0, acc, false, st));
+        }
+        if (c.g1) {
+            Launch k(KK_FP_COLS, st);
+            TRY(launch_fp(TC_COLS, false, c.W, hid, nullptr, V, n, d, n, V, 1, 0, inv_t, nullptr, w.tokp, nullptr,
+                          nullptr, nullptr, 0, 0, static_cast<float *>(c.g1), 0, st, acc, n_dev, bad));
+        }
+        return LOSSK_OK;
+    }
+
+    const BwdScratch bs{reinterpret_cast<uint16_t *>(b + L.off_gring), reinterpret_cast<unsigned *>(b + L.off_gsig),
+                        w.tokp, w.hdr};
+    // The passes' maps span the gathered rows up to a multiple of 256 (zeros past the last).
+    auto rows_args = [&](BwdArgs *a) {
+        if (!bwd_args(bs, true, L.n_pad, c.d, c.V, hid, c.W, a)) return false;
+        a->n_tok = n;
+        a->n_split = static_cast<int>(L.nsplit);
+        a->inv_t_l2e = l.k2;
+        a->n_dev = n_dev;
+        a->out = dhpart;
+        a->out_split_stride = c.n * c.d;
+        a->out3_tma = make_map_out3_f32(&a->map_out3, dhpart, c.d, c.n, L.nsplit) ? 1 : 0;
+        a->out_scale = 1.f;
+        if (f16) a->coef_max = reinterpret_cast<const unsigned *>(&w.hdr->pad[HDR_COEF]);
+        return true;
+    };
+    const bool fused = c.g0 && !f16;
+    int *redo = &w.hdr->redo;
+    BwdArgs a;
+    if (fused) {
+        // forward and d_hidden in one pass; a row that left the range of its
+        // reference asks for the separate forward
+        float *zpart = reinterpret_cast<float *>(b + L.off_zpart);
+        if (!rows_args(&a)) return LOSSK_DEVICE_ERROR;
+        a.zpart = zpart;
+        a.zpart_stride = L.n_pad;
+        {
+            Launch k(KK_TC_FUSED, st);
+            TRY(launch_bwp(BWD_FUSED, false, false, a, a.n_fixed * a.n_split * a.n_dg, st));
+        }
+        TRY(launch_seq_merge_fused(l, w, zpart, L.nsplit * a.n_cl, st));
+    }
+    int32_t s = run_forward(c, L, l, w, hid, fused ? redo : nullptr);
+    if (s == LOSSK_OK) s = run_losses(c, l, w);
+    if (s != LOSSK_OK) return s;
+
+    // The scalars, and d_hidden from the fused pass, beside the d_weight pass.
+    SideStream *sd = c.g1 ? side_stream(st) : nullptr;
+    std::unique_lock<std::mutex> lk;
+    cudaStream_t aux = st;
+    if (sd) {
+        lk = std::unique_lock<std::mutex>(sd->mu);
+        if (sd->ready()) aux = sd->s;
+    }
+    if (aux != st) {
+        TRY(cudaEventRecord(sd->fork, st));
+        TRY(cudaStreamWaitEvent(aux, sd->fork, 0));
+    }
+    s = LOSSK_OK;
+    void *dh_to = fused && acc ? static_cast<void *>(b + L.off_dhacc) : c.g0;
+    if (launch_seq_scalars(l, w, aux) != cudaSuccess) s = LOSSK_DEVICE_ERROR;
+    if (s == LOSSK_OK && fused &&
+        launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, true, nullptr, dh_to, false, false, aux) !=
+            cudaSuccess)
+        s = LOSSK_DEVICE_ERROR;
+    if (s == LOSSK_OK && c.g1) {
+        BwdArgs q;
+        if (!bwd_args(bs, false, L.n_pad, c.d, c.V, hid, c.W, &q)) {
+            s = LOSSK_DEVICE_ERROR;
+        } else {
+            q.n_tok = n;
+            q.inv_t_l2e = l.k2;
+            q.n_dev = n_dev;
+            q.out = static_cast<float *>(c.g1);
+            q.accumulate = acc ? 1 : 0;
+            q.out_scale = 1.f;
+            if (f16) q.coef_max = reinterpret_cast<const unsigned *>(&w.hdr->pad[HDR_COEF]);
+            q.out16 = c.grad_dtype != LOSSK_F32 ? 1 : 0;
+            q.out_tma = (q.out16 ? make_map_out_16(&q.map_out, c.g1, c.d, c.V)
+                                 : make_map_out_f32(&q.map_out, c.g1, c.d, c.V)) ? 1 : 0;
+            Launch k(KK_TC_COLS, st);
+            if (!q.out_tma || launch_bwp(BWD_COLS, false, f16, q, q.n_fixed * q.n_dg, st) != cudaSuccess)
+                s = LOSSK_DEVICE_ERROR;
+        }
+    }
+    if (aux != st) {
+        TRY(cudaEventRecord(sd->join, aux));
+        TRY(cudaStreamWaitEvent(st, sd->join, 0));
+    }
+    if (s != LOSSK_OK || !c.g0) return s;
+    // d_hidden as a pass of its own: fp16, whose tiles need the log-sum-exp, and
+    // bf16 where the fused pass's could not be used
+    const int *only_if = fused ? redo : nullptr;
+    if (!rows_args(&a)) return LOSSK_DEVICE_ERROR;
+    a.only_if = only_if;
+    {
+        Launch k(KK_TC_ROWS, st);
+        TRY(launch_bwp(BWD_ROWS, false, f16, a, a.n_fixed * a.n_split * a.n_dg, st));
+    }
+    TRY(launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, false, only_if, dh_to, !fused && acc, false, st));
+    if (fused && acc)
+        TRY(launch_seq_dh(LOSSK_F32, l, w, static_cast<float *>(dh_to), 1, c.d, c.W, false, nullptr, c.g0, true, true,
+                          st));
+    return LOSSK_OK;
+}
+
+int32_t run_rows(const Call &c, const Layout &L, const SeqLoss &l, const SeqScratch &w)
+{
+    TRY(launch_seq_stats(c.dtype, l, w, c.X, L.splits, c.st));
+    TRY(launch_seq_merge_rows(c.dtype, l, w, c.X, L.splits, c.st));
+    const int32_t s = run_losses(c, l, w);
+    if (s != LOSSK_OK) return s;
+    if (c.g0) TRY(launch_seq_grad(c.dtype, l, w, c.X, c.g0, (c.flags & LOSSK_ACCUMULATE_GRADS) != 0, c.st));
+    TRY(launch_seq_scalars(l, w, c.st));
+    return LOSSK_OK;
+}
+
+int32_t run(const Call &c)
+{
+    Layout L;
+    const int32_t s = check(c, &L);
+    if (s != LOSSK_OK) return s;
+    const SeqScratch w = scratch(L, c.ws, c.n_pairs);
+    SeqLoss l;
+    std::memset(&l, 0, sizeof(l));
+    l.n_tok = static_cast<int>(c.n);
+    l.n_seq = static_cast<int>(c.n_seq);
+    l.pairs = static_cast<int>(c.n_pairs);
+    l.vocab = c.V;
+    l.targets = c.targets;
+    l.mask = c.mask;
+    l.first = c.first;
+    l.adv = c.adv;
+    l.old = c.old;
+    l.ref = c.ref;
+    l.low = static_cast<float>(c.low);
+    l.high = static_cast<float>(c.high);
+    l.kl = static_cast<float>(c.kl);
+    l.k2 = static_cast<float>(LOG2E / c.temperature);
+    l.per_t = static_cast<float>(-c.grad_scale / c.temperature);
+    l.flags = c.flags;
+    l.objective = c.objective;
+    l.beta = static_cast<float>(c.beta);
+    l.margin = static_cast<float>(c.margin);
+    l.smooth = static_cast<float>(c.smooth);
+    l.nll = static_cast<float>(c.nll);
+    l.scalars = c.scalars;
+    l.per_token = c.per_item;
+    l.log_ratio = c.log_ratio;
+    l.logp = c.logp;
+    TRY(launch_seq_prep(l, w, c.st));
+    return c.head ? run_head(c, L, l, w) : run_rows(c, L, l, w);
+}
+
+} // namespace
+
+extern "C" {
+
+int64_t lossk_sequence_workspace_bytes(int32_t kind, int64_t n, int64_t d, int64_t V, int64_t n_seq, int32_t dtype)
+{
+    Layout L;
+    if (kind != LOSSK_KIND_SEQUENCE_HEAD && kind != LOSSK_KIND_SEQUENCE_LOGITS) return -1;
+    return layout(kind, n, d, V, n_seq, dtype, &L) == LOSSK_OK ? static_cast<int64_t>(L.total) : -1;
+}
+
+int32_t lossk_policy_fwd_bwd(int64_t n, int64_t d, int64_t V, int64_t n_seq, int32_t dtype, const void *hidden,
+                             int64_t hidden_len, const void *weight, int64_t weight_len, const int64_t *targets,
+                             int64_t targets_len, const uint8_t *loss_mask, const int32_t *first, int64_t first_len,
+                             const float *advantages, int64_t advantages_len, const float *old_logp, int64_t old_len,
+                             const float *ref_logp, int64_t ref_len, double clip_low, double clip_high,
+                             double kl_weight, double temperature, double grad_scale, uint32_t flags,
+                             float *scalars_out, float *per_token_out, float *logp_out, int32_t grad_dtype,
+                             void *d_hidden, void *d_weight, void *workspace, int64_t workspace_bytes,
+                             lossk_stream_t stream)
+{
+    Call c{};
+    c.head = true;
+    c.n = n, c.d = d, c.V = V, c.n_seq = n_seq, c.dtype = dtype;
+    c.X = hidden, c.x_len = hidden_len, c.W = weight, c.w_len = weight_len;
+    c.targets = targets, c.targets_len = targets_len, c.mask = loss_mask, c.first = first, c.first_len = first_len;
+    c.adv = advantages, c.adv_len = advantages_len, c.old = old_logp, c.old_len = old_len;
+    c.ref = ref_logp, c.ref_len = ref_len;
+    c.low = clip_low, c.high = clip_high, c.kl = kl_weight, c.temperature = temperature, c.grad_scale = grad_scale;
+    c.flags = flags, c.scalars = scalars_out, c.per_item = per_token_out, c.logp = logp_out;
+    c.grad_dtype = grad_dtype, c.g0 = d_hidden, c.g1 = d_weight;
+    c.ws = workspace, c.ws_bytes = workspace_bytes, c.st = reinterpret_cast<cudaStream_t>(stream);
+    return run(c);
+}
+
+int32_t lossk_policy_from_logits(int64_t n, int64_t V, int64_t n_seq, int32_t dtype, const void *logits,
+                                 int64_t logits_len, const int64_t *targets, int64_t targets_len,
+                                 const uint8_t *loss_mask, const int32_t *first, int64_t first_len,
+                                 const float *advantages, int64_t advantages_len, const float *old_logp,
+                                 int64_t old_len, const float *ref_logp, int64_t ref_len, double clip_low,
+                                 double clip_high, double kl_weight, double temperature, double grad_scale,
+                                 uint32_t flags, float *scalars_out, float *per_token_out, float *logp_out,
+                                 void *grad_logits, int64_t grad_len, void *workspace, int64_t workspace_bytes,
+                                 lossk_stream_t stream)
+{
+    Call c{};
+    c.n = n, c.V = V, c.n_seq = n_seq, c.dtype = dtype, c.X = logits, c.x_len = logits_len;
+    c.targets = targets, c.targets_len = targets_len, c.mask = loss_mask, c.first = first, c.first_len = first_len;
+    c.adv = advantages, c.adv_len = advantages_len, c.old = old_logp, c.old_len = old_len;
+    c.ref = ref_logp, c.ref_len = ref_len;
+    c.low = clip_low, c.high = clip_high, c.kl = kl_weight, c.temperature = temperature, c.grad_scale = grad_scale;
+    c.flags = flags, c.scalars = scalars_out, c.per_item = per_token_out, c.logp = logp_out;
+    c.g0 = grad_logits, c.g_len = grad_len;
+    c.ws = workspace, c.ws_bytes = workspace_bytes, c.st = reinterpret_cast<cudaStream_t>(stream);
+    return run(c);
+}
+
+int32_t lossk_preference_fwd_bwd(int64_t n, int64_t d, int64_t V, int64_t n_pairs, int32_t dtype, const void *hidden,
+                                 int64_t hidden_len, const void *weight, int64_t weight_len, const int64_t *targets,
+                                 int64_t targets_len, const uint8_t *loss_mask, const int32_t *first,
+                                 int64_t first_len, const float *ref_logp, int64_t ref_len, int32_t objective,
+                                 double beta, double margin, double label_smoothing, double nll_weight,
+                                 double grad_scale, uint32_t flags, float *scalars_out, float *per_pair_out,
+                                 float *log_ratio_out, float *logp_out, int32_t grad_dtype, void *d_hidden,
+                                 void *d_weight, void *workspace, int64_t workspace_bytes, lossk_stream_t stream)
+{
+    if (n_pairs < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_pairs > MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    Call c{};
+    c.head = true;
+    c.n = n, c.d = d, c.V = V, c.n_seq = 2 * n_pairs, c.n_pairs = n_pairs, c.dtype = dtype;
+    c.X = hidden, c.x_len = hidden_len, c.W = weight, c.w_len = weight_len;
+    c.targets = targets, c.targets_len = targets_len, c.mask = loss_mask, c.first = first, c.first_len = first_len;
+    c.ref = ref_logp, c.ref_len = ref_len, c.temperature = 1.0;
+    c.objective = objective, c.beta = beta, c.margin = margin, c.smooth = label_smoothing, c.nll = nll_weight;
+    c.grad_scale = grad_scale, c.flags = flags, c.scalars = scalars_out, c.per_item = per_pair_out;
+    c.log_ratio = log_ratio_out, c.logp = logp_out, c.grad_dtype = grad_dtype, c.g0 = d_hidden, c.g1 = d_weight;
+    c.ws = workspace, c.ws_bytes = workspace_bytes, c.st = reinterpret_cast<cudaStream_t>(stream);
+    return run(c);
+}
+
+int32_t lossk_preference_from_logits(int64_t n, int64_t V, int64_t n_pairs, int32_t dtype, const void *logits,
+                                     int64_t logits_len, const int64_t *targets, int64_t targets_len,
+                                     const uint8_t *loss_mask, const int32_t *first, int64_t first_len,
+                                     const float *ref_logp, int64_t ref_len, int32_t objective, double beta,
+                                     double margin, double label_smoothing, double nll_weight, double grad_scale,
+                                     uint32_t flags, float *scalars_out, float *per_pair_out, float *log_ratio_out,
+                                     float *logp_out, void *grad_logits, int64_t grad_len, void *workspace,
+                                     int64_t workspace_bytes, lossk_stream_t stream)
+{
+    if (n_pairs < 1) return LOSSK_EMPTY_DIMENSION;
+    if (n_pairs > MAX_DIM) return LOSSK_DIMENSION_TOO_LARGE;
+    Call c{};
+    c.n = n, c.V = V, c.n_seq = 2 * n_pairs, c.n_pairs = n_pairs, c.dtype = dtype;
+    c.X = logits, c.x_len = logits_len;
+    c.targets = targets, c.targets_len = targets_len, c.mask = loss_mask, c.first = first, c.first_len = first_len;
+    c.ref = ref_logp, c.ref_len = ref_len, c.temperature = 1.0;
+    c.objective = objective, c.beta = beta, c.margin = margin, c.smooth = label_smoothing, c.nll = nll_weight;
+    c.grad_scale = grad_scale, c.flags = flags, c.scalars = scalars_out, c.per_item = per_pair_out;
+    c.log_ratio = log_ratio_out, c.logp = logp_out, c.g0 = grad_logits, c.g_len = grad_len;
+    c.ws = workspace, c.ws_bytes = workspace_bytes, c.st = reinterpret_cast<cudaStream_t>(stream);
+    return run(c);
+}
+
+} // extern "C"

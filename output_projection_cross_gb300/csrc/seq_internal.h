@@ -1,0 +1,87 @@
+// seq_internal.h -- the losses of sampled and compared sequences: what their
+// host side (lossk_seq.cu) and kernels (k_seq.cu, k_rows.cu) share.
+#pragma once
+#include "lossk_internal.h"
+
+namespace lossk {
+
+// Rows that count are numbered in order: "slots" 0 .. n_valid - 1.  Every
+// per-row array below but `slot` is indexed by slot, and the fused passes see
+// the rows of a gathered copy of `hidden`, so rows that do not count cost them
+// nothing.
+struct SeqScratch {
+    WsHeader *hdr;
+    int *slot;          // [n_pad] by row: its slot, or ~(slots before it) where it does not count
+    int *row;           // [n_pad] the slot's row
+    int64_t *y;         // [n_pad] its target
+    int *seq_slot;      // [n_seq + 1] slots before each sequence (and all of them)
+    float *tgt;         // [n_pad] its target's logit (the forms from hidden rows)
+    float *lp;          // [n_pad] logp
+    float *lse2;        // [n_pad] log2 sum 2^(x log2 e)
+    float *z;           // [n_pad] fused pass: the sum of its shifted terms
+    float4 *tokp;       // [n_pad] {lse2, a, a, target}: softmax and one-hot coefficients
+    double *sum;        // [n_seq] sum over the sequence of logp minus its base
+    double *slope;      // [n_seq] LOSSK_SEQ_RATIO: sum over the sequence of w dP/d(log ratio)
+    double *acc;        // [3][n_pad] per-slot terms of the scalars
+    double *pair;       // [2][n_pairs] per-pair terms
+    float2 *part;       // forms from logits: [n_pad][splits] (max, sum) of the row's pieces
+    int64_t n_pad;
+};
+
+// The loss: fields of the policy loss, then of the preference loss.
+struct SeqLoss {
+    int n_tok, n_seq, pairs;       // n_seq 0: no sequences; pairs > 0: the preference loss
+    int64_t vocab;
+    const int64_t *targets;
+    const uint8_t *mask;
+    const int32_t *first;
+    const float *adv, *old, *ref;
+    float low, high, kl;
+    float k2;                      // log2(e) / temperature
+    float per_t;                   // -grad_scale / temperature
+    uint32_t flags;
+    int objective;
+    float beta, margin, smooth, nll;
+    float *scalars, *per_token, *logp;      // per_token: per_pair for the preference loss
+    float *log_ratio;
+};
+
+// dtype: lossk_dtype.  All enqueue on `st`.
+// Counts and numbers the rows, checks targets and `first`, clears the header's
+// words of one call; 586 into the header, and every later kernel returns at once.
+cudaError_t launch_seq_prep(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
+// Copies the counted rows of hidden to out (rows up to the next multiple of 256
+// as zeros); 16-bit types: their target logits, and in tokp.x the fused pass's
+// reference target logit * k2 + FUSED_SHIFT.
+cudaError_t launch_seq_gather(int dtype, const SeqLoss &l, const SeqScratch &w, const void *H, const void *W, int64_t d,
+                              void *out, cudaStream_t st);
+// The fused pass's sums -> logp, lse2 (redo where a row left the range).
+cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const float *zpart, int64_t nz,
+                                   cudaStream_t st);
+// The forward pass's (max, sum) partials of n_ct tiles -> logp, lse2.  only_if: or
+// NULL; zero: not needed.
+cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,
+                                   const int *only_if, cudaStream_t st);
+// Given logits: per slot and piece of the row (max, sum); then logp, lse2.
+int seq_stat_splits(int64_t n, int64_t vocab, int dtype);
+cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
+                             cudaStream_t st);
+cudaError_t launch_seq_merge_rows(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
+                                  cudaStream_t st);
+// Per sequence the sum of log ratios (and the slope of LOSSK_SEQ_RATIO).
+cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
+// Per row its loss, outputs and coefficient; per pair its loss.
+cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
+cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
+// grad_logits of every row.
+cudaError_t launch_seq_grad(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,
+                            bool accumulate, cudaStream_t st);
+// d_hidden of every row from the passes' split partials [nsplit][n_tok][d], indexed by
+// slot: fused, a_t / Z_t times their sum minus a_t W[y_t] (a value that is not
+// finite asks for the separate passes, redo), else their sum.  out: out_dtype.
+// add: added to it (float).  by_row: the partials are indexed by row.
+cudaError_t launch_seq_dh(int out_dtype, const SeqLoss &l, const SeqScratch &w, const float *part, int64_t nsplit,
+                          int64_t d, const void *W, bool fused, const int *only_if, void *out, bool add,
+                          bool by_row, cudaStream_t st);
+
+} // namespace lossk

@@ -95,6 +95,15 @@ def _load():
                                                   _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
         "lossk_paged_attn": (_i32, [_i64] * 8 + [_i32, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64,
                                                  _i64, _vp, _i64, _i64, _i64, _dbl, _vp, _i64, _vp, _vp, _i64, _vp]),
+        "lossk_sequence_workspace_bytes": (_i64, [_i32, _i64, _i64, _i64, _i64, _i32]),
+        "lossk_policy_fwd_bwd": (_i32, [_i64] * 4 + [_i32] + [_vp, _i64] * 3 + [_vp] + [_vp, _i64] * 4 + [_dbl] * 5 +
+                                 [_u32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _vp]),
+        "lossk_policy_from_logits": (_i32, [_i64] * 3 + [_i32] + [_vp, _i64] * 2 + [_vp] + [_vp, _i64] * 4 + [_dbl] * 5 +
+                                     [_u32, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
+        "lossk_preference_fwd_bwd": (_i32, [_i64] * 4 + [_i32] + [_vp, _i64] * 3 + [_vp] + [_vp, _i64] * 2 + [_i32] +
+                                     [_dbl] * 5 + [_u32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _vp]),
+        "lossk_preference_from_logits": (_i32, [_i64] * 3 + [_i32] + [_vp, _i64] * 2 + [_vp] + [_vp, _i64] * 2 + [_i32] +
+                                         [_dbl] * 5 + [_u32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
         "lossk_kernel_name": (ctypes.c_char_p, [_i32]),
         "lossk_launch_count": (_i64, []),
         "lossk_profile_enable": (_i32, [_i32]),
@@ -117,8 +126,10 @@ EXPORTED = ("lossk_status_name", "lossk_dims_check", "lossk_chunk_check", "lossk
             "lossk_ce_from_logits_static", "lossk_selftest_wait", "lossk_ce_shard_fwd",
             "lossk_ce_shard_combine", "lossk_ce_shard_bwd", "lossk_decode_workspace_bytes", "lossk_beam_select",
             "lossk_beam_gather", "lossk_cache_fork", "lossk_cache_reserve", "lossk_cache_free",
-            "lossk_cache_compact", "lossk_cache_copy", "lossk_cache_write", "lossk_paged_attn", "lossk_kernel_name", "lossk_launch_count", "lossk_profile_enable", "lossk_profile_read")
-N_KERNELS = 35
+            "lossk_cache_compact", "lossk_cache_copy", "lossk_cache_write", "lossk_paged_attn",
+            "lossk_sequence_workspace_bytes", "lossk_policy_fwd_bwd", "lossk_policy_from_logits",
+            "lossk_preference_fwd_bwd", "lossk_preference_from_logits", "lossk_kernel_name", "lossk_launch_count", "lossk_profile_enable", "lossk_profile_read")
+N_KERNELS = 43
 
 
 class LosskError(RuntimeError):
