@@ -699,6 +699,12 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                         }
                     }
                     zt += z0 + z1;
+                    // the target's logit as this pass has it, its sum's truncations included
+                    if (a.tgt_out && w.dg == 0 && static_cast<unsigned>(rel - q * 32) < 32u && fixrow < n_tok) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i == rel - q * 32) a.tgt_out[fixrow] = __uint_as_float(v[i]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) pk[i >> 1] = pack_16x2<F16>(gf[i], gf[i + 1]);
                 } else if (!DISTILL) {

@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ Tc
             const int t = tok0 + r;
             const bool row_ok = t < n_tok;
             const int ncols = min(F2_BN, a.vocab - voc0);
+            // the target's column in this tile
+            const int rel = !DISTILL && a.tgt_out && row_ok ? static_cast<int>(a.targets[t]) - voc0 : -1;
             const uint16_t *trow_g = nullptr;
             float lt2 = 0.f;
             if (DISTILL) {
@@ -225,6 +227,11 @@ __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ Tc
                 // raw logits scaled once.  Only the vocabulary's last chunk tests its
                 // columns.
                 const bool full = q * 32 + 32 <= ncols;
+                if (!DISTILL && static_cast<unsigned>(rel - q * 32) < 32u) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i == rel - q * 32) a.tgt_out[t] = __uint_as_float(v[i]);
+                }
                 float cr = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)

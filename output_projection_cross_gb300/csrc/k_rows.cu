@@ -80,17 +80,6 @@ template <typename T> struct RowVecs {
     __device__ bool whole(int64_t e) const { return e >= 0 && e + NVEC<T> <= vocab; }
 };
 
-__device__ __forceinline__ void join(float &m, float &z, float mo, float zo)
-{
-    const float M = fmaxf(m, mo);
-    if (M == -INFINITY) {            // no term so far (or NaN: kept)
-        z += zo;
-        return;
-    }
-    z = z * ex2_approx(m - M) + zo * ex2_approx(mo - M);
-    m = M;
-}
-
 } // namespace
 
 // (max, sum) in log2 units of x = k2 s over a piece of a counted row.  Each
@@ -154,19 +143,21 @@ __global__ void __launch_bounds__(ROW_T) row_stats_kernel(const SeqLoss l, const
             vec(f);
         }
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        const float mo = __shfl_xor_sync(0xffffffffu, m, o), zo = __shfl_xor_sync(0xffffffffu, z, o);
-        join(m, z, mo, zo);
-    }
+    // the block's maximum, one rescale of each thread's sum, then plain sums in a fixed order
     __shared__ float sm[ROW_T / 32], sz[ROW_T / 32];
-    if ((threadIdx.x & 31) == 0) {
-        sm[threadIdx.x >> 5] = m;
-        sz[threadIdx.x >> 5] = z;
-    }
+    float M = m;
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROW_T / 32; ++i) M = fmaxf(M, sm[i]);
+    if (M > -INFINITY) z *= ex2_approx(m - M);         // (a NaN of a row of nothing else stays)
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if ((threadIdx.x & 31) == 0) sz[threadIdx.x >> 5] = z;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < ROW_T / 32; ++i) join(m, z, sm[i], sz[i]);
-        w.part[static_cast<int64_t>(c) * splits + piece] = make_float2(m, z);
+        for (int i = 1; i < ROW_T / 32; ++i) z += sz[i];
+        w.part[static_cast<int64_t>(c) * splits + piece] = make_float2(M, z);
     }
 }
 
@@ -203,12 +194,17 @@ __global__ void __launch_bounds__(64) row_merge_kernel(const SeqLoss l, const Se
     const int c = blockIdx.x * 64 + threadIdx.x;
     if (c >= w.hdr->n_valid) return;
     const float2 *p = w.part + static_cast<int64_t>(c) * splits;
-    float m = p[0].x, z = p[0].y;
-    for (int i = 1; i < splits; ++i) join(m, z, p[i].x, p[i].y);
+    float m = p[0].x, z = 0.f;
+    for (int i = 1; i < splits; ++i) m = fmaxf(m, p[i].x);
+    for (int i = 0; i < splits; ++i) z += m > -INFINITY ? p[i].y * ex2_approx(p[i].x - m) : p[i].y;
     const float y = value(logits[w.row[c] * l.vocab + w.y[c]]);
     const double lse2 = static_cast<double>(m) + static_cast<double>(log2f(z));
     w.lse2[c] = static_cast<float>(lse2);
-    w.lp[c] = y == -INFINITY && z == z ? y : static_cast<float>((static_cast<double>(y) * static_cast<double>(l.k2) - lse2) * LN2);
+    // three exponentials for all but a maximum's own terms: the element's, the thread's, the piece's
+    const double low = (splits > 1 ? 3 : 2) * EX2_LOW;
+    w.lp[c] = y == -INFINITY && z == z
+                  ? y
+                  : static_cast<float>((static_cast<double>(y) * static_cast<double>(l.k2) - lse2) * LN2 - low);
 }
 
 cudaError_t launch_seq_merge_rows(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,

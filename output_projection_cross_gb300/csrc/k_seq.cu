@@ -153,9 +153,8 @@ cudaError_t launch_seq_prep(const SeqLoss &l, const SeqScratch &w, cudaStream_t 
 }
 
 // One warp per slot: the row's copy and, in the 16-bit types, its product with the
-// target's weight row.  Eight sums per lane, joined pairwise: a chain of d / 256
-// additions (a single sum per lane would be 8 times as long, and its rounding is the
-// log-probability's own).
+// target's weight row, near which the fused pass takes its exponents (the logit that
+// counts is the pass's own).
 template <typename T> // float, uint16_t (bf16 bits) or h16_t (fp16 bits)
 __global__ void __launch_bounds__(256) seq_gather_kernel(const SeqLoss l, const SeqScratch w, const T *__restrict__ H,
                                                          const T *__restrict__ W, int64_t d, T *__restrict__ out)
@@ -193,8 +192,7 @@ __global__ void __launch_bounds__(256) seq_gather_kernel(const SeqLoss l, const 
         float acc = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
         for (int q = 16; q > 0; q >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, q);
         if (lane == 0) {
-            w.tgt[c] = acc;
-            w.tokp[c] = make_float4(fmaf(acc, l.k2, FUSED_SHIFT), 0.f, 0.f, 0.f);
+            w.tokp[c] = make_float4(fmaf(acc, l.k2, FUSED_SHIFT), 0.f, 0.f, __int_as_float(static_cast<int>(w.y[c])));
         }
     }
 }
@@ -217,7 +215,10 @@ cudaError_t launch_seq_gather(int dtype, const SeqLoss &l, const SeqScratch &w, 
 // One thread per slot.  With r the row's reference (its target at about 64 in log2
 // units) and Z the sum of 2^(x log2 e - r): lse2 = r + log2 Z, logp = ln 2 (x_y log2 e - r -
 // log2 Z).  The difference is taken in double: r's own rounding, 4e-6 at 64, is in Z
-// as well and must not be in the result.
+// as well and must not be in the result.  x_y comes from the pass as the sum does: the
+// tensor cores' sums are truncated, logits come out low by 1e-9 of their size per unit of
+// d_model, and an exact x_y against such a sum was 2.5e-5 off at d_model 4096, the same
+// way for every token of a sequence.
 __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, const SeqScratch w,
                                                              const float *__restrict__ zpart, int64_t nz)
 {
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, co
     const double gap = static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - static_cast<double>(r);
     w.lse2[c] = r + lz;
     w.z[c] = Z;
-    w.lp[c] = static_cast<float>((gap - static_cast<double>(lz)) * LN2);
+    w.lp[c] = static_cast<float>((gap - static_cast<double>(lz)) * LN2 - EX2_LOW);
 }
 
 cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const float *zpart, int64_t nz,
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
     const double lse2 = static_cast<double>(M) + log2(Z);
     w.lse2[c] = static_cast<float>(lse2);
     w.z[c] = 1.f;
-    w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2);
+    w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2 - 2 * EX2_LOW);
 }
 
 cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,

@@ -96,6 +96,7 @@ struct TcArgs {
     const float4 *tokp;    // per-token backward parameters
     float *part;           // STATS output (structure of arrays)
     float *tgt;            // STATS (label CE): target logit per token
+    float *tgt_out;        // forward on CTA pairs, or NULL: each token's target logit as the pass has it (needs targets)
     int64_t part_stride;   // n_pad
     int64_t part_plane;    // n_ct * n_pad
     float *out;            // ROWS/COLS output
@@ -149,6 +150,7 @@ struct BwdArgs {
     int64_t out_split_stride;
     float *zpart;          // BWD_FUSED: sums of G' [n_split * n_cl][zpart_stride]
     int64_t zpart_stride;
+    float *tgt_out;        // BWD_FUSED, or NULL: each token's target logit (the target's column in tokp.w)
     int accumulate;        // add the accumulator into `out` instead of overwriting it
     float out_scale;       // fp16 operands: the factor the stored accumulator is multiplied by
     const unsigned *coef_max;  // fp16 operands, or NULL: the bits of the largest |coefficient| among the tokens (label

@@ -210,6 +210,8 @@ int32_t run_forward(const Call &c, const Layout &L, const SeqLoss &l, const SeqS
     a.n_dev = &w.hdr->n_valid;
     a.refused = &w.hdr->bad_targets;
     a.only_if = only_if;
+    a.targets = w.y;
+    a.tgt_out = w.tgt;
     a.part = part;
     a.part_stride = L.n_pad;
     a.part_plane = L.n_ct * L.n_pad;
@@ -296,6 +298,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
         if (!rows_args(&a)) return LOSSK_DEVICE_ERROR;
         a.zpart = zpart;
         a.zpart_stride = L.n_pad;
+        a.tgt_out = w.tgt;
         {
             Launch k(KK_TC_FUSED, st);
             TRY(launch_bwp(BWD_FUSED, false, false, a, a.n_fixed * a.n_split * a.n_dg, st));
@@ -398,7 +401,8 @@ int32_t run(const Call &c)
     l.low = static_cast<float>(c.low);
     l.high = static_cast<float>(c.high);
     l.kl = static_cast<float>(c.kl);
-    l.k2 = static_cast<float>(LOG2E / c.temperature);
+    l.k2 = static_cast<float>(LOG2E / c.temperature *
+                              (c.head && is16(c.dtype) ? 1.0 + TC_LOW * static_cast<double>(c.d) : 1.0));
     l.per_t = static_cast<float>(-c.grad_scale / c.temperature);
     l.flags = c.flags;
     l.objective = c.objective;

@@ -15,7 +15,7 @@ struct SeqScratch {
     int *row;           // [n_pad] the slot's row
     int64_t *y;         // [n_pad] its target
     int *seq_slot;      // [n_seq + 1] slots before each sequence (and all of them)
-    float *tgt;         // [n_pad] its target's logit (the forms from hidden rows)
+    float *tgt;         // [n_pad] its target's logit (the forms from hidden rows, as the pass has it)
     float *lp;          // [n_pad] logp
     float *lse2;        // [n_pad] log2 sum 2^(x log2 e)
     float *z;           // [n_pad] fused pass: the sum of its shifted terms
@@ -27,6 +27,19 @@ struct SeqScratch {
     float2 *part;       // forms from logits: [n_pad][splits] (max, sum) of the row's pieces
     int64_t n_pad;
 };
+
+// ex2.approx comes out low by 5e-8 of its value on average (measured over [-80, 0]:
+// 4.9e-8 to 5.2e-8), and so does a sum of exponentials, once per exponential that a
+// term has gone through.  That much is given back to the log-probabilities: sequences sum
+// hundreds of them against a reference's, and it would add up.
+constexpr double EX2_LOW = 5e-8;
+
+// The tensor cores drop what lies below an fp32 sum's last bit at each step of 16
+// products: a logit whose sum grows evenly along d_model comes out low by about
+// 1e-9 of itself per unit of d_model (measured, d_model 256 to 4096: 0.86e-9 to 0.96e-9
+// in bf16, 1.07e-9 to 1.24e-9 in fp16), at most 2e-9.  The passes' scale makes up for that mean,
+// so that a softmax over 4096-wide products is not 2.5e-5 flatter than the logits'.
+constexpr double TC_LOW = 1e-9;
 
 // The loss: fields of the policy loss, then of the preference loss.
 struct SeqLoss {
@@ -51,8 +64,8 @@ struct SeqLoss {
 // words of one call; 586 into the header, and every later kernel returns at once.
 cudaError_t launch_seq_prep(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
 // Copies the counted rows of hidden to out (rows up to the next multiple of 256
-// as zeros); 16-bit types: their target logits, and in tokp.x the fused pass's
-// reference target logit * k2 + FUSED_SHIFT.
+// as zeros); 16-bit types: tokp.x, the fused pass's reference target logit * k2 +
+// FUSED_SHIFT, and the target in tokp.w.
 cudaError_t launch_seq_gather(int dtype, const SeqLoss &l, const SeqScratch &w, const void *H, const void *W, int64_t d,
                               void *out, cudaStream_t st);
 // The fused pass's sums -> logp, lse2 (redo where a row left the range).
