@@ -82,7 +82,7 @@ template <typename T> struct RowVecs {
 
 } // namespace
 
-// (max, sum) in log2 units of x = k2 s over a piece of a counted row.  Each
+// (max, sum) in log2 units of x = k2 s over a counted row, or a piece of it.  Each
 // vector's maximum first, one rescale if it rose, then its exponentials,
 // which do not depend on one another.  fp32 sums of at most a few thousand terms per
 // thread.
@@ -155,10 +155,33 @@ __global__ void __launch_bounds__(ROW_T) row_stats_kernel(const SeqLoss l, const
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if ((threadIdx.x & 31) == 0) sz[threadIdx.x >> 5] = z;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < ROW_T / 32; ++i) z += sz[i];
-        w.part[static_cast<int64_t>(c) * splits + piece] = make_float2(M, z);
+    if (threadIdx.x != 0) return;
+    for (int i = 1; i < ROW_T / 32; ++i) z += sz[i];
+    // exponentials that all but a maximum's own terms have gone through: the element's and the
+    // thread's, and where a row has several pieces the piece's
+    double low = 2 * EX2_LOW;
+    if (splits > 1) {
+        float2 *p = w.part + static_cast<int64_t>(c) * splits;
+        p[piece] = make_float2(M, z);
+        __threadfence();
+        if (atomicAdd(&w.tick[c], 1) != splits - 1) return;
+        // the last piece to arrive joins them all, in their order
+        __threadfence();
+        M = -INFINITY;
+        for (int i = 0; i < splits; ++i) M = fmaxf(M, __ldcg(&p[i].x));
+        z = 0.f;
+        for (int i = 0; i < splits; ++i) {
+            const float2 q = __ldcg(p + i);
+            z += M > -INFINITY ? q.y * ex2_approx(q.x - M) : q.y;
+        }
+        low = 3 * EX2_LOW;
     }
+    const float y = value(r.row[w.y[c]]);
+    const double lse2 = static_cast<double>(M) + static_cast<double>(log2f(z));
+    w.lse2[c] = static_cast<float>(lse2);
+    w.lp[c] = y == -INFINITY && z == z
+                  ? y
+                  : static_cast<float>((static_cast<double>(y) * static_cast<double>(l.k2) - lse2) * LN2 - low);
 }
 
 int seq_stat_splits(int64_t n, int64_t vocab, int dtype)
@@ -182,41 +205,6 @@ cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, c
         return launch(row_stats_kernel<h16_t>, grid, dim3(ROW_T), 0, st, l, w, static_cast<const h16_t *>(logits), splits);
     return launch(row_stats_kernel<uint16_t>, grid, dim3(ROW_T), 0, st, l, w, static_cast<const uint16_t *>(logits),
                   splits);
-}
-
-// One thread per slot: the pieces in order, and the target's logit.
-template <typename T>
-__global__ void __launch_bounds__(64) row_merge_kernel(const SeqLoss l, const SeqScratch w, const T *__restrict__ logits,
-                                                       int splits)
-{
-    wait_for_stream();
-    if (refused(w.hdr)) return;
-    const int c = blockIdx.x * 64 + threadIdx.x;
-    if (c >= w.hdr->n_valid) return;
-    const float2 *p = w.part + static_cast<int64_t>(c) * splits;
-    float m = p[0].x, z = 0.f;
-    for (int i = 1; i < splits; ++i) m = fmaxf(m, p[i].x);
-    for (int i = 0; i < splits; ++i) z += m > -INFINITY ? p[i].y * ex2_approx(p[i].x - m) : p[i].y;
-    const float y = value(logits[w.row[c] * l.vocab + w.y[c]]);
-    const double lse2 = static_cast<double>(m) + static_cast<double>(log2f(z));
-    w.lse2[c] = static_cast<float>(lse2);
-    // three exponentials for all but a maximum's own terms: the element's, the thread's, the piece's
-    const double low = (splits > 1 ? 3 : 2) * EX2_LOW;
-    w.lp[c] = y == -INFINITY && z == z
-                  ? y
-                  : static_cast<float>((static_cast<double>(y) * static_cast<double>(l.k2) - lse2) * LN2 - low);
-}
-
-cudaError_t launch_seq_merge_rows(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
-                                  cudaStream_t st)
-{
-    Launch k(KK_SEQ_MERGE, st);
-    const dim3 grid(static_cast<unsigned>((l.n_tok + 63) / 64));
-    if (dtype == LOSSK_F32)
-        return launch(row_merge_kernel<float>, grid, dim3(64), 0, st, l, w, static_cast<const float *>(logits), splits);
-    if (dtype == LOSSK_F16)
-        return launch(row_merge_kernel<h16_t>, grid, dim3(64), 0, st, l, w, static_cast<const h16_t *>(logits), splits);
-    return launch(row_merge_kernel<uint16_t>, grid, dim3(64), 0, st, l, w, static_cast<const uint16_t *>(logits), splits);
 }
 
 // grad_logits of a piece of a row.  A coefficient of 0 (a row that does not

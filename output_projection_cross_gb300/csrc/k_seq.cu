@@ -44,46 +44,57 @@ __device__ __forceinline__ int seq_of(const int *seq_slot, int n_seq, int c)
 
 // One block: a prefix sum over the rows, PER at a time per thread, carried from
 // one round of 8192 rows to the next.  In order, so that slots, and with them the
-// order of every sum, are a function of the mask alone.
+// order of every sum, are a function of the mask alone.  A chain of latencies: masks,
+// targets and the sequences' ends are all asked for at once, before any of them
+// is known to matter (10 -> 5 us at 2048 rows).
 constexpr int PREP_T = 1024, PREP_PER = 8;
 __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
     __shared__ int s_warp[32];
-    __shared__ int s_bad;
+    __shared__ int s_groups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = l.n_tok;
     // (an error word of an earlier call stays until lossk_device_status has read it: refused)
     bool bad = *reinterpret_cast<volatile int *>(&w.hdr->err) != 0;
-    bool range = false;
-    int lo = 0, hi = n;
-    if (l.first) {
-        for (int s = tid; s < l.n_seq; s += PREP_T) {
-            const int a = l.first[s], b = l.first[s + 1];
-            range |= a < 0 || b < a || b > n;
-        }
-        lo = l.first[0];
-        hi = l.first[l.n_seq];
-    }
-    if (tid == 0) s_bad = 0;
-    const bool range_all = __syncthreads_or(range) != 0;
-    if (range_all) lo = hi = 0;
-    int done = 0;                                          // slots of the rounds before
-    int wrong = 0;
-    for (int t0 = 0; t0 < n; t0 += PREP_T * PREP_PER) {
-        const int t = t0 + tid * PREP_PER;
-        unsigned on = 0;
-        int64_t y[PREP_PER];
+    unsigned on;
+    int64_t y[PREP_PER];
+    auto load = [&](int t) {
+        on = 0;
 #pragma unroll
         for (int i = 0; i < PREP_PER; ++i) {
             const int r = t + i;
-            const bool in = r < n && r >= lo && r < hi && (!l.mask || l.mask[r] != 0);
-            y[i] = in ? l.targets[r] : 0;
-            on |= (in ? 1u : 0u) << i;
+            y[i] = r < n ? l.targets[r] : 0;
+            on |= (r < n && (!l.mask || l.mask[r] != 0) ? 1u : 0u) << i;
         }
+    };
+    load(tid * PREP_PER);
+    bool range = false;
+    int lo = 0, hi = n, first0 = 0, first1 = 0;            // of sequence tid
+    if (l.first) {
+        lo = l.first[0];
+        hi = l.first[l.n_seq];
+        for (int s = tid; s < l.n_seq; s += PREP_T) {
+            const int a = l.first[s], b = l.first[s + 1];
+            range |= a < 0 || b < a || b > n;
+            if (s == tid) first0 = a, first1 = b;
+        }
+    }
+    if (tid == 0) s_groups = 0;
+    const bool range_all = __syncthreads_or(range) != 0;
+    if (range_all) lo = hi = first0 = first1 = 0;
+    int done = 0;                                          // slots of the rounds before
+    bool wrong = false;
+    for (int t0 = 0; t0 < n; t0 += PREP_T * PREP_PER) {
+        const int t = t0 + tid * PREP_PER;
+        if (t0 > 0) load(t);
+        // the rows of [lo, hi)
+        const int from = min(max(lo - t, 0), PREP_PER), to = min(max(hi - t, 0), PREP_PER);
+        on &= ((1u << to) - 1u) & ~((1u << from) - 1u);
 #pragma unroll
-        for (int i = 0; i < PREP_PER; ++i) wrong |= y[i] < 0 || y[i] >= l.vocab;
-        int c = __popc(on), inc = c;
+        for (int i = 0; i < PREP_PER; ++i) wrong |= ((on >> i) & 1u) && (y[i] < 0 || y[i] >= l.vocab);
+        const int c = __popc(on);
+        int inc = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -91,14 +102,15 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
         }
         if (lane == 31) s_warp[warp] = inc;
         __syncthreads();
-        int before = done, all = 0;
+        int v = s_warp[lane];                              // the warps' sums, scanned by every warp
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-            const int v = s_warp[k];
-            before += k < warp ? v : 0;
-            all += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
         }
-        int at = before + inc - c;
+        const int all = __shfl_sync(0xffffffffu, v, 31);
+        const int upto = __shfl_sync(0xffffffffu, v, warp > 0 ? warp - 1 : 0);
+        int at = done + (warp > 0 ? upto : 0) + inc - c;
 #pragma unroll
         for (int i = 0; i < PREP_PER; ++i) {
             if (t + i >= n) break;
@@ -107,41 +119,39 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
             if (in) {
                 w.row[at] = t + i;
                 w.y[at] = y[i];
+                w.tick[at] = 0;
                 ++at;
             }
         }
         done += all;
         __syncthreads();
     }
-    bad |= range || wrong;
+    bad |= range_all || wrong;
     int groups = 0, chosen = 0;
-    const int any_bad = __syncthreads_or(bad);
+    const bool any_bad = __syncthreads_or(bad) != 0;
     if (l.n_seq > 0) {
-        auto slots = [&](int s) {
-            const int t = range_all ? 0 : l.first[s];
-            return t < n ? slots_before(w.slot[t]) : done;
-        };
-        for (int s = tid; s <= l.n_seq; s += PREP_T) {
-            const int a = slots(s);
+        auto slots = [&](int t) { return t < n ? slots_before(w.slot[t]) : done; };
+        auto start = [&](int s) { return range_all ? 0 : l.first[s]; };
+        for (int s = tid; s < l.n_seq; s += PREP_T) {
+            const int a = slots(s == tid ? first0 : start(s)), b = slots(s == tid ? first1 : start(s + 1));
             w.seq_slot[s] = a;
-            if (l.pairs > 0) {
-                if (s < l.pairs && slots(s + 1) > a && slots(l.pairs + s + 1) > slots(l.pairs + s)) ++groups;
-            } else if (s < l.n_seq && slots(s + 1) > a) {
-                ++groups;
-            }
+            if (s == l.n_seq - 1) w.seq_slot[l.n_seq] = b;
+            if (b == a) continue;
+            if (l.pairs == 0 || (s < l.pairs && slots(start(l.pairs + s + 1)) > slots(start(l.pairs + s)))) ++groups;
         }
-        if (l.pairs > 0) chosen = slots(l.pairs);          // (tokens before the first sequence do not count)
-        if (groups) atomicAdd(&s_bad, groups);             // s_bad is free by now: the count of groups
+        if (l.pairs > 0 && tid == 0) chosen = slots(start(l.pairs));   // (rows before the first sequence do not count)
+        groups = __reduce_add_sync(0xffffffffu, groups);
+        if (lane == 0 && groups) atomicAdd(&s_groups, groups);
         __syncthreads();
-        groups = s_bad;
     }
     if (tid == 0) {
-        w.hdr->bad_targets = any_bad;
+        w.hdr->bad_targets = any_bad ? 1 : 0;
         w.hdr->n_valid = done;
         w.hdr->redo = 0;
-        w.hdr->pad[HDR_GROUPS] = groups;
+        w.hdr->pad[HDR_GROUPS] = s_groups;
         w.hdr->pad[HDR_CHOSEN] = chosen;
         w.hdr->pad[HDR_COEF] = 0;
+        w.hdr->pad[HDR_TICKET] = 0;
         if (any_bad && w.hdr->err == 0) raise_fault(&w.hdr->pad[HDR_FAULT], LOSSK_TARGET_OUT_OF_RANGE);
     }
 }
@@ -333,8 +343,8 @@ __device__ __forceinline__ double block_sum(double v, double *sh)
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
-    for (unsigned i = 0; i < blockDim.x / 32; ++i) v += sh[i];
+    v = sh[0];
+    for (unsigned i = 1; i < blockDim.x / 32; ++i) v += sh[i];
     return v;
 }
 
@@ -404,15 +414,20 @@ __device__ __forceinline__ double log_ratio(const SeqLoss &l, const SeqScratch &
 
 } // namespace
 
-// One thread per row, and per sequence and pair.
-__global__ void __launch_bounds__(128) seq_coef_kernel(const SeqLoss l, const SeqScratch w)
+// One thread per row, and per sequence and pair.  Each block adds up its threads' terms
+// of the three means; the last one to arrive adds the blocks' sums in their order, so the
+// result does not depend on which that is.  (Doubles run at a sixty-fourth of floats
+// here: one block that summed every row took 34 us, most of it a chain of 32 additions.)
+constexpr int COEF_T = 128;
+__global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
     if (refused(w.hdr)) return;
-    const int t = blockIdx.x * 128 + threadIdx.x;
+    const int t = blockIdx.x * COEF_T + threadIdx.x;
     const bool pref = l.pairs > 0;
     const bool sum = l.flags & LOSSK_REDUCE_SUM;
     float coef = 0.f;
+    double v[3] = {0.0, 0.0, 0.0};
     if (pref && t < l.n_seq && l.log_ratio) {
         int n_s;
         l.log_ratio[t] = static_cast<float>(log_ratio(l, w, t, n_s));
@@ -424,8 +439,8 @@ __global__ void __launch_bounds__(128) seq_coef_kernel(const SeqLoss l, const Se
         const bool live = nc > 0 && nr > 0;
         if (live) pair_term(l, u, loss, slope);
         if (l.per_token) l.per_token[t] = loss;
-        w.pair[t] = static_cast<double>(loss);
-        w.pair[l.pairs + t] = live && u > 0.0 ? 1.0 : 0.0;
+        v[1] = static_cast<double>(loss);
+        v[2] = live && u > 0.0 ? 1.0 : 0.0;
     }
     if (t < l.n_tok) {
         const int c = w.slot[t];
@@ -451,7 +466,7 @@ __global__ void __launch_bounds__(128) seq_coef_kernel(const SeqLoss l, const Se
                     d_lp = sum ? g : g / w.hdr->pad[HDR_GROUPS];
                 }
                 if (chosen && l.nll > 0.f) d_lp -= static_cast<double>(l.nll) / (sum ? 1 : w.hdr->pad[HDR_CHOSEN]);
-                w.acc[c] = chosen ? -static_cast<double>(lp) : 0.0;
+                v[0] = chosen ? -static_cast<double>(lp) : 0.0;
             } else {
                 const double weight = row_weight(l, w.hdr, n_s);
                 PolicyTerm p;
@@ -473,9 +488,9 @@ __global__ void __launch_bounds__(128) seq_coef_kernel(const SeqLoss l, const Se
                     }
                 }
                 if (l.per_token) l.per_token[t] = loss;
-                w.acc[c] = weight * static_cast<double>(p.loss);
-                w.acc[w.n_pad + c] = weight * static_cast<double>(kl);
-                w.acc[2 * w.n_pad + c] = p.clipped ? weight : 0.0;
+                v[0] = weight * static_cast<double>(p.loss);
+                v[1] = weight * static_cast<double>(kl);
+                v[2] = p.clipped ? weight : 0.0;
             }
             if (l.logp) l.logp[t] = lp;
             const float lse2 = w.lse2[c];
@@ -488,38 +503,42 @@ __global__ void __launch_bounds__(128) seq_coef_kernel(const SeqLoss l, const Se
     unsigned m = __float_as_uint(fabsf(coef));
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0 && m) atomicMax(reinterpret_cast<unsigned *>(&w.hdr->pad[HDR_COEF]), m);
-}
 
-cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
-{
-    Launch k(KK_SEQ_COEF, st);
-    const int n = l.n_tok > l.n_seq ? l.n_tok : l.n_seq;
-    return launch(seq_coef_kernel, dim3(static_cast<unsigned>((n + 127) / 128)), dim3(128), 0, st, l, w);
-}
-
-// One block: each thread every 1024th slot in order, then a fixed tree.
-__global__ void __launch_bounds__(1024) seq_scalars_kernel(const SeqLoss l, const SeqScratch w)
-{
-    wait_for_stream();
-    if (refused(w.hdr)) return;
-    __shared__ double sh[32];
-    const bool pref = l.pairs > 0, sum = l.flags & LOSSK_REDUCE_SUM;
-    const int n = w.hdr->n_valid;
-    double v[3] = {0.0, 0.0, 0.0};
-    for (int c = threadIdx.x; c < n; c += 1024) {
-        v[0] += w.acc[c];
-        if (!pref) {
-            v[1] += w.acc[w.n_pad + c];
-            v[2] += w.acc[2 * w.n_pad + c];
+    __shared__ double sh[3][COEF_T / 32];
+    __shared__ bool s_last;
+    auto block_sums = [&]() {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            if ((threadIdx.x & 31) == 0) sh[k][threadIdx.x >> 5] = v[k];
         }
+        __syncthreads();
+    };
+    block_sums();
+    if (threadIdx.x < 3) {
+        double x = sh[threadIdx.x][0];
+        for (int i = 1; i < COEF_T / 32; ++i) x += sh[threadIdx.x][i];
+        w.acc[threadIdx.x * static_cast<int64_t>(gridDim.x) + blockIdx.x] = x;
+        __threadfence();
     }
-    if (pref)
-        for (int i = threadIdx.x; i < l.pairs; i += 1024) {
-            v[1] += w.pair[i];
-            v[2] += w.pair[l.pairs + i];
-        }
-    for (int k = 0; k < 3; ++k) v[k] = block_sum(v[k], sh);
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = atomicAdd(&w.hdr->pad[HDR_TICKET], 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        v[k] = 0.0;
+        for (unsigned b = threadIdx.x; b < gridDim.x; b += COEF_T)
+            v[k] += __ldcg(w.acc + k * static_cast<int64_t>(gridDim.x) + b);
+    }
+    block_sums();
     if (threadIdx.x != 0) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        v[k] = sh[k][0];
+        for (int i = 1; i < COEF_T / 32; ++i) v[k] += sh[k][i];
+    }
     float *o = l.scalars;
     if (pref) {
         const int pairs = w.hdr->pad[HDR_GROUPS], chosen = w.hdr->pad[HDR_CHOSEN];
@@ -541,10 +560,11 @@ __global__ void __launch_bounds__(1024) seq_scalars_kernel(const SeqLoss l, cons
     }
 }
 
-cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
+cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
 {
-    Launch k(KK_REDUCE, st);
-    return launch(seq_scalars_kernel, dim3(1), dim3(1024), 0, st, l, w);
+    Launch k(KK_SEQ_COEF, st);
+    const int n = l.n_tok > l.n_seq ? l.n_tok : l.n_seq;
+    return launch(seq_coef_kernel, dim3(static_cast<unsigned>((n + COEF_T - 1) / COEF_T)), dim3(COEF_T), 0, st, l, w);
 }
 
 namespace {

@@ -23,7 +23,7 @@ struct Layout {
     int64_t n_pad, n_ct, nsplit;
     int splits;
     size_t off_slot, off_row, off_y, off_seq, off_tgt, off_lp, off_lse2, off_z, off_tokp, off_sum, off_slope, off_acc,
-        off_pair, off_rows, off_hidden, off_part, off_dhpart, off_zpart, off_gring, off_gsig, off_dhacc, total;
+        off_tick, off_rows, off_hidden, off_part, off_dhpart, off_zpart, off_gring, off_gsig, off_dhacc, total;
 };
 
 // 580, or why there is no layout.
@@ -55,12 +55,18 @@ int32_t layout(int32_t kind, int64_t n, int64_t d, int64_t V, int64_t n_seq, int
     L->off_tokp = take(sizeof(float4) * np);
     L->off_sum = take(sizeof(double) * ns);
     L->off_slope = take(sizeof(double) * ns);
-    L->off_acc = take(sizeof(double) * 3 * np);
-    L->off_pair = take(sizeof(double) * (ns + 1));
+    L->off_acc = take(sizeof(double) * 3 * static_cast<size_t>(cdiv(n > n_seq ? n : n_seq, 128)));
+    L->off_tick = take(sizeof(int) * np);
     if (head) {
         const bool tc = is16(dtype);
         L->n_ct = cdiv(V, tc ? TC_BN_FWD : FP_BN);
         L->nsplit = dh_splits(n, d, V, dtype);
+        if (!tc) {
+            // two blocks per SM, down to one vocabulary tile each: 64 x 64 x 1000 takes 72 us in the two
+            // splits of the label loss's rule (eight tiles one after another), 13 in sixteen
+            const int64_t base = cdiv(n, FP_BM) * cdiv(d, FP_SLICE), most = cdiv(304, base);
+            L->nsplit = most < L->n_ct ? most : L->n_ct;
+        }
         const size_t nd = static_cast<size_t>(n) * static_cast<size_t>(d);
         L->off_hidden = take((tc ? 2 : 4) * np * static_cast<size_t>(d));
         L->off_part = take(sizeof(float) * NSTAT_CE * static_cast<size_t>(L->n_ct) * np);
@@ -81,7 +87,7 @@ int32_t layout(int32_t kind, int64_t n, int64_t d, int64_t V, int64_t n_seq, int
     return LOSSK_OK;
 }
 
-SeqScratch scratch(const Layout &L, void *ws, int64_t n_pairs)
+SeqScratch scratch(const Layout &L, void *ws)
 {
     uint8_t *b = static_cast<uint8_t *>(ws);
     SeqScratch w;
@@ -99,10 +105,9 @@ SeqScratch scratch(const Layout &L, void *ws, int64_t n_pairs)
     w.sum = reinterpret_cast<double *>(b + L.off_sum);
     w.slope = reinterpret_cast<double *>(b + L.off_slope);
     w.acc = reinterpret_cast<double *>(b + L.off_acc);
-    w.pair = reinterpret_cast<double *>(b + L.off_pair);
+    w.tick = reinterpret_cast<int *>(b + L.off_tick);
     w.part = reinterpret_cast<float2 *>(b + L.off_rows);
     w.n_pad = L.n_pad;
-    (void)n_pairs;
     return w;
 }
 
@@ -254,7 +259,6 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
         TRY(launch_seq_merge_tiles(l, w, part, L.n_ct, nullptr, st));
         int32_t s = run_losses(c, l, w);
         if (s != LOSSK_OK) return s;
-        TRY(launch_seq_scalars(l, w, st));
         if (c.g0) {
             {
                 Launch k(KK_FP_ROWS, st);
@@ -309,8 +313,8 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     if (s == LOSSK_OK) s = run_losses(c, l, w);
     if (s != LOSSK_OK) return s;
 
-    // The scalars, and d_hidden from the fused pass, beside the d_weight pass.
-    SideStream *sd = c.g1 ? side_stream(st) : nullptr;
+    // d_hidden from the fused pass, beside the d_weight pass.
+    SideStream *sd = fused && c.g1 ? side_stream(st) : nullptr;
     std::unique_lock<std::mutex> lk;
     cudaStream_t aux = st;
     if (sd) {
@@ -323,8 +327,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     }
     s = LOSSK_OK;
     void *dh_to = fused && acc ? static_cast<void *>(b + L.off_dhacc) : c.g0;
-    if (launch_seq_scalars(l, w, aux) != cudaSuccess) s = LOSSK_DEVICE_ERROR;
-    if (s == LOSSK_OK && fused &&
+    if (fused &&
         launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, true, nullptr, dh_to, false, false, aux) !=
             cudaSuccess)
         s = LOSSK_DEVICE_ERROR;
@@ -372,11 +375,9 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
 int32_t run_rows(const Call &c, const Layout &L, const SeqLoss &l, const SeqScratch &w)
 {
     TRY(launch_seq_stats(c.dtype, l, w, c.X, L.splits, c.st));
-    TRY(launch_seq_merge_rows(c.dtype, l, w, c.X, L.splits, c.st));
     const int32_t s = run_losses(c, l, w);
     if (s != LOSSK_OK) return s;
     if (c.g0) TRY(launch_seq_grad(c.dtype, l, w, c.X, c.g0, (c.flags & LOSSK_ACCUMULATE_GRADS) != 0, c.st));
-    TRY(launch_seq_scalars(l, w, c.st));
     return LOSSK_OK;
 }
 
@@ -385,7 +386,7 @@ int32_t run(const Call &c)
     Layout L;
     const int32_t s = check(c, &L);
     if (s != LOSSK_OK) return s;
-    const SeqScratch w = scratch(L, c.ws, c.n_pairs);
+    const SeqScratch w = scratch(L, c.ws);
     SeqLoss l;
     std::memset(&l, 0, sizeof(l));
     l.n_tok = static_cast<int>(c.n);

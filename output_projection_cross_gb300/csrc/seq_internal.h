@@ -22,8 +22,8 @@ struct SeqScratch {
     float4 *tokp;       // [n_pad] {lse2, a, a, target}: softmax and one-hot coefficients
     double *sum;        // [n_seq] sum over the sequence of logp minus its base
     double *slope;      // [n_seq] LOSSK_SEQ_RATIO: sum over the sequence of w dP/d(log ratio)
-    double *acc;        // [3][n_pad] per-slot terms of the scalars
-    double *pair;       // [2][n_pairs] per-pair terms
+    double *acc;        // [3][blocks] the coefficient kernel's blocks' terms of the scalars
+    int *tick;          // [n_pad] forms from logits: pieces of the row that are done
     float2 *part;       // forms from logits: [n_pad][splits] (max, sum) of the row's pieces
     int64_t n_pad;
 };
@@ -75,17 +75,14 @@ cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const 
 // NULL; zero: not needed.
 cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,
                                    const int *only_if, cudaStream_t st);
-// Given logits: per slot and piece of the row (max, sum); then logp, lse2.
+// Given logits: logp, lse2, a row in `splits` pieces.
 int seq_stat_splits(int64_t n, int64_t vocab, int dtype);
 cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
                              cudaStream_t st);
-cudaError_t launch_seq_merge_rows(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
-                                  cudaStream_t st);
 // Per sequence the sum of log ratios (and the slope of LOSSK_SEQ_RATIO).
 cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
-// Per row its loss, outputs and coefficient; per pair its loss.
+// Per row its loss, outputs and coefficient; per pair its loss; the scalars.
 cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
-cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
 // grad_logits of every row.
 cudaError_t launch_seq_grad(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,
                             bool accumulate, cudaStream_t st);
