@@ -11,7 +11,7 @@
 #include "../../include/lossk.h"
 #include "decode_launch.h"
 #include "ptx.cuh"
-#include "seq_internal.h"
+#include "seq_scalars.cuh"
 
 #include <type_traits>
 
@@ -187,10 +187,12 @@ __global__ void __launch_bounds__(ROW_T) row_stats_kernel(const SeqLoss l, const
 int seq_stat_splits(int64_t n, int64_t vocab, int dtype)
 {
     const int64_t bytes = vocab * (dtype == LOSSK_F32 ? 4 : 2);
-    // four blocks for each of 152 SMs, pieces of 16 KB (a round of loads) and more
+    // four blocks for each of 152 SMs, pieces of 16 KB (a round of loads) and more; but pieces of
+    // 64 KB also where there are many rows, whose last wave of blocks is short then
     int64_t s = (608 + n - 1) / n;
-    const int64_t most = bytes / (ROW_T * ROW_U * 16);
+    const int64_t most = bytes / (ROW_T * ROW_U * 16), some = bytes / 65536;
     if (s > most) s = most;
+    if (s < some) s = some;
     return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
@@ -198,7 +200,7 @@ cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, c
                              cudaStream_t st)
 {
     Launch k(KK_SEQ_STATS, st);
-    const dim3 grid(static_cast<unsigned>(l.n_tok * splits));
+    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(l.n_tok) * splits));
     if (dtype == LOSSK_F32)
         return launch(row_stats_kernel<float>, grid, dim3(ROW_T), 0, st, l, w, static_cast<const float *>(logits), splits);
     if (dtype == LOSSK_F16)
@@ -216,8 +218,11 @@ __global__ void __launch_bounds__(ROW_T) row_grad_kernel(const SeqLoss l, const 
     constexpr int N = NVEC<T>;
     wait_for_stream();
     if (refused(w.hdr)) return;
-    const int64_t t = blockIdx.x / splits;
-    const int piece = blockIdx.x - static_cast<int>(t) * splits;
+    if (blockIdx.x == 0) seq_scalars<ROW_T>(l, w);
+    // the last rows first: the statistics pass has just read them, and the L2 holds them still
+    const unsigned at = gridDim.x - 1 - blockIdx.x;
+    const int64_t t = at / splits;
+    const int piece = at - static_cast<unsigned>(t) * splits;
     const int c = w.slot[t];
     const float4 P = c >= 0 ? w.tokp[c] : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
     if (ADD && P.y == 0.f) return;

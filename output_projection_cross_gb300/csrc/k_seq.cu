@@ -13,7 +13,7 @@
 #include "decode_internal.h"
 #include "decode_launch.h"
 #include "ptx.cuh"
-#include "seq_internal.h"
+#include "seq_scalars.cuh"
 
 #include <type_traits>
 
@@ -28,30 +28,42 @@ __device__ __forceinline__ bool refused(const WsHeader *hdr)
 
 __device__ __forceinline__ int slots_before(int slot) { return slot < 0 ? ~slot : slot; }
 
-// The sequence that holds slot c: the last one whose slots start at or before it.
-__device__ __forceinline__ int seq_of(const int *seq_slot, int n_seq, int c)
+// The sequence that holds slot c: the last one whose slots start at or before it.  The
+// whole warp calls it, each step reads 32 of the starts (a thread of its own would wait
+// for log2 n_seq loads, one after another); slots rise from lane to lane, c < 0: none.
+__device__ __forceinline__ int seq_of(const int *seq_slot, int n_seq, int c, int lane)
 {
-    int lo = 0, hi = n_seq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (seq_slot[mid] <= c) lo = mid;
-        else hi = mid - 1;
+    const unsigned some = __ballot_sync(0xffffffffu, c >= 0);
+    if (!some) return 0;
+    const int c0 = __shfl_sync(0xffffffffu, c, __ffs(some) - 1);
+    int lo = 0, hi = n_seq;                                // the first slot's is in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int at = lo + lane * step;
+        const bool le = at < hi && seq_slot[at] <= c0;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+        lo += k * step;
+        hi = min(hi, lo + step);
     }
-    return lo;
+    int s = lo;
+    while (s + 1 < n_seq && seq_slot[s + 1] <= c) ++s;
+    return s;
 }
 
 } // namespace
 
-// One block: a prefix sum over the rows, PER at a time per thread, carried from
-// one round of 8192 rows to the next.  In order, so that slots, and with them the
-// order of every sum, are a function of the mask alone.  A chain of latencies: masks,
-// targets and the sequences' ends are all asked for at once, before any of them
-// is known to matter (10 -> 5 us at 2048 rows).
+// One block: a prefix sum over the rows, 8192 in a round, in order, so that slots, and
+// with them the order of every sum, are a function of the mask alone.  A chain of
+// latencies: masks, targets and the sequences' ends are all asked for at once, before
+// any of them is known to matter.  A warp's rows are consecutive, so that what it
+// writes is too (eight rows in a row per thread took 25 us for 8192 rows, most of it
+// stores of 32 sectors each).
 constexpr int PREP_T = 1024, PREP_PER = 8;
 __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
-    __shared__ int s_warp[32];
+    static_assert(PREP_PER * 32 == 256, "a lane of a warp scans eight of the counts");
+    __shared__ int s_count[PREP_PER * 32];
     __shared__ int s_groups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = l.n_tok;
@@ -59,16 +71,16 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
     bool bad = *reinterpret_cast<volatile int *>(&w.hdr->err) != 0;
     unsigned on;
     int64_t y[PREP_PER];
-    auto load = [&](int t) {
+    auto load = [&](int t0) {
         on = 0;
 #pragma unroll
         for (int i = 0; i < PREP_PER; ++i) {
-            const int r = t + i;
+            const int r = t0 + i * PREP_T + tid;
             y[i] = r < n ? l.targets[r] : 0;
             on |= (r < n && (!l.mask || l.mask[r] != 0) ? 1u : 0u) << i;
         }
     };
-    load(tid * PREP_PER);
+    load(0);
     bool range = false;
     int lo = 0, hi = n, first0 = 0, first1 = 0;            // of sequence tid
     if (l.first) {
@@ -86,41 +98,52 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
     int done = 0;                                          // slots of the rounds before
     bool wrong = false;
     for (int t0 = 0; t0 < n; t0 += PREP_T * PREP_PER) {
-        const int t = t0 + tid * PREP_PER;
-        if (t0 > 0) load(t);
-        // the rows of [lo, hi)
-        const int from = min(max(lo - t, 0), PREP_PER), to = min(max(hi - t, 0), PREP_PER);
-        on &= ((1u << to) - 1u) & ~((1u << from) - 1u);
+        if (t0 > 0) load(t0);
+        unsigned vote[PREP_PER];
 #pragma unroll
-        for (int i = 0; i < PREP_PER; ++i) wrong |= ((on >> i) & 1u) && (y[i] < 0 || y[i] >= l.vocab);
-        const int c = __popc(on);
-        int inc = c;
+        for (int i = 0; i < PREP_PER; ++i) {
+            const int r = t0 + i * PREP_T + tid;
+            const bool in = ((on >> i) & 1u) && r >= lo && r < hi;
+            wrong |= in && (y[i] < 0 || y[i] >= l.vocab);
+            vote[i] = __ballot_sync(0xffffffffu, in);
+            if (lane == 0) s_count[i * 32 + warp] = __popc(vote[i]);
+        }
+        __syncthreads();
+        // every warp scans the 256 counts, eight per lane
+        int c[PREP_PER], sum = 0;
+#pragma unroll
+        for (int i = 0; i < PREP_PER; ++i) sum += c[i] = s_count[lane * PREP_PER + i];
+        int inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        if (lane == 31) s_warp[warp] = inc;
-        __syncthreads();
-        int v = s_warp[lane];                              // the warps' sums, scanned by every warp
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
-        }
-        const int all = __shfl_sync(0xffffffffu, v, 31);
-        const int upto = __shfl_sync(0xffffffffu, v, warp > 0 ? warp - 1 : 0);
-        int at = done + (warp > 0 ? upto : 0) + inc - c;
+        const int all = __shfl_sync(0xffffffffu, inc, 31);
+        int before[PREP_PER];                              // counts before each of this lane's eight
+        int run = inc - sum;
 #pragma unroll
         for (int i = 0; i < PREP_PER; ++i) {
-            if (t + i >= n) break;
-            const bool in = (on >> i) & 1u;
-            w.slot[t + i] = in ? at : ~at;
+            before[i] = run;
+            run += c[i];
+        }
+#pragma unroll
+        for (int i = 0; i < PREP_PER; ++i) {
+            // the count before (i, warp): entry i * 32 + warp lies with lane i * 4 + warp / 8
+            int at = 0;
+#pragma unroll
+            for (int q = 0; q < PREP_PER; ++q) {
+                const int v = __shfl_sync(0xffffffffu, before[q], i * 4 + (warp >> 3));
+                if (q == (warp & 7)) at = v;
+            }
+            const int r = t0 + i * PREP_T + tid;
+            const bool in = (vote[i] >> lane) & 1u;
+            at += done + __popc(vote[i] & ((1u << lane) - 1u));
+            if (r < n) w.slot[r] = in ? at : ~at;
             if (in) {
-                w.row[at] = t + i;
+                w.row[at] = r;
                 w.y[at] = y[i];
                 w.tick[at] = 0;
-                ++at;
             }
         }
         done += all;
@@ -151,7 +174,6 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
         w.hdr->pad[HDR_GROUPS] = s_groups;
         w.hdr->pad[HDR_CHOSEN] = chosen;
         w.hdr->pad[HDR_COEF] = 0;
-        w.hdr->pad[HDR_TICKET] = 0;
         if (any_bad && w.hdr->err == 0) raise_fault(&w.hdr->pad[HDR_FAULT], LOSSK_TARGET_OUT_OF_RANGE);
     }
 }
@@ -415,10 +437,9 @@ __device__ __forceinline__ double log_ratio(const SeqLoss &l, const SeqScratch &
 } // namespace
 
 // One thread per row, and per sequence and pair.  Each block adds up its threads' terms
-// of the three means; the last one to arrive adds the blocks' sums in their order, so the
-// result does not depend on which that is.  (Doubles run at a sixty-fourth of floats
-// here: one block that summed every row took 34 us, most of it a chain of 32 additions.)
-constexpr int COEF_T = 128;
+// of the three means; the first block of the kernel after it adds the blocks' sums
+// (seq_scalars).  (Doubles run at a sixty-fourth of floats here: one block that summed
+// every row took 34 us.  The last block to arrive, here, held the next kernel up for 3.)
 __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
@@ -442,14 +463,14 @@ __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const
         v[1] = static_cast<double>(loss);
         v[2] = live && u > 0.0 ? 1.0 : 0.0;
     }
+    const int c = t < l.n_tok ? w.slot[t] : -1;
+    const int s = l.n_seq > 0 ? seq_of(w.seq_slot, l.n_seq, c, threadIdx.x & 31) : 0;
     if (t < l.n_tok) {
-        const int c = w.slot[t];
         if (c < 0) {
             if (l.logp) l.logp[t] = 0.f;
             if (!pref && l.per_token) l.per_token[t] = 0.f;
         } else {
             const float lp = w.lp[c];
-            const int s = l.n_seq > 0 ? seq_of(w.seq_slot, l.n_seq, c) : 0;
             const int n_s = l.n_seq > 0 ? w.seq_slot[s + 1] - w.seq_slot[s] : 0;
             double d_lp;                                   // d total / d logp
             if (pref) {
@@ -505,58 +526,16 @@ __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const
     if ((threadIdx.x & 31) == 0 && m) atomicMax(reinterpret_cast<unsigned *>(&w.hdr->pad[HDR_COEF]), m);
 
     __shared__ double sh[3][COEF_T / 32];
-    __shared__ bool s_last;
-    auto block_sums = [&]() {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-            if ((threadIdx.x & 31) == 0) sh[k][threadIdx.x >> 5] = v[k];
-        }
-        __syncthreads();
-    };
-    block_sums();
+    for (int k = 0; k < 3; ++k) {
+        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if ((threadIdx.x & 31) == 0) sh[k][threadIdx.x >> 5] = v[k];
+    }
+    __syncthreads();
     if (threadIdx.x < 3) {
         double x = sh[threadIdx.x][0];
         for (int i = 1; i < COEF_T / 32; ++i) x += sh[threadIdx.x][i];
         w.acc[threadIdx.x * static_cast<int64_t>(gridDim.x) + blockIdx.x] = x;
-        __threadfence();
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(&w.hdr->pad[HDR_TICKET], 1) == static_cast<int>(gridDim.x) - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        v[k] = 0.0;
-        for (unsigned b = threadIdx.x; b < gridDim.x; b += COEF_T)
-            v[k] += __ldcg(w.acc + k * static_cast<int64_t>(gridDim.x) + b);
-    }
-    block_sums();
-    if (threadIdx.x != 0) return;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        v[k] = sh[k][0];
-        for (int i = 1; i < COEF_T / 32; ++i) v[k] += sh[k][i];
-    }
-    float *o = l.scalars;
-    if (pref) {
-        const int pairs = w.hdr->pad[HDR_GROUPS], chosen = w.hdr->pad[HDR_CHOSEN];
-        if (!sum) {
-            v[0] = chosen > 0 ? v[0] / chosen : 0.0;
-            v[1] = pairs > 0 ? v[1] / pairs : 0.0;
-            v[2] = pairs > 0 ? v[2] / pairs : 0.0;
-        }
-        // (without the likelihood term its infinities stay out of the total)
-        o[0] = static_cast<float>(l.nll > 0.f ? v[1] + static_cast<double>(l.nll) * v[0] : v[1]);
-        o[1] = static_cast<float>(v[1]);
-        o[2] = static_cast<float>(v[0]);
-        o[3] = static_cast<float>(v[2]);
-    } else {
-        o[0] = static_cast<float>(l.kl > 0.f ? v[0] + static_cast<double>(l.kl) * v[1] : v[0]);
-        o[1] = static_cast<float>(v[0]);
-        o[2] = static_cast<float>(v[1]);
-        o[3] = static_cast<float>(v[2]);
     }
 }
 
@@ -565,6 +544,19 @@ cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t 
     Launch k(KK_SEQ_COEF, st);
     const int n = l.n_tok > l.n_seq ? l.n_tok : l.n_seq;
     return launch(seq_coef_kernel, dim3(static_cast<unsigned>((n + COEF_T - 1) / COEF_T)), dim3(COEF_T), 0, st, l, w);
+}
+
+__global__ void __launch_bounds__(256) seq_scalars_kernel(const SeqLoss l, const SeqScratch w)
+{
+    wait_for_stream();
+    if (refused(w.hdr)) return;
+    seq_scalars<256>(l, w);
+}
+
+cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st)
+{
+    Launch k(KK_REDUCE, st);
+    return launch(seq_scalars_kernel, dim3(1), dim3(256), 0, st, l, w);
 }
 
 namespace {
@@ -592,11 +584,13 @@ __device__ __forceinline__ void put4(h16_t *p, const float (&v)[4])
 template <typename O, int N>
 __global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqScratch w, const float *__restrict__ part,
                                                      int64_t nsplit, int64_t d, const uint16_t *__restrict__ W, int fused,
-                                                     const int *only_if, O *out, int add, int by_row)
+                                                     const int *only_if, O *out, int add, int by_row,
+                                                     int scalars)
 {
     wait_for_stream();
     if (refused(w.hdr)) return;
     if (only_if && !*reinterpret_cast<const volatile int *>(only_if)) return;
+    if (scalars && blockIdx.x == 0) seq_scalars<256>(l, w);
     const int64_t dn = d / N, count = l.n_tok * dn, plane = l.n_tok * d;
     bool bad = false;
     for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < count; i += int64_t(256) * gridDim.x) {
@@ -659,24 +653,24 @@ __global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqS
 template <typename O>
 static cudaError_t dh_one(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t nsplit, int64_t d,
                           const void *W, bool fused, const int *only_if, void *out, bool add, bool by_row,
-                          cudaStream_t st)
+                          bool scalars, cudaStream_t st)
 {
     const bool four = d % 4 == 0;
     int64_t grid = (l.n_tok * (four ? d / 4 : d) + 255) / 256;
     if (grid > 4096) grid = 4096;
     return launch(four ? seq_dh_kernel<O, 4> : seq_dh_kernel<O, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st,
                   l, w, part, nsplit, d, static_cast<const uint16_t *>(W), fused ? 1 : 0, only_if,
-                  static_cast<O *>(out), add ? 1 : 0, by_row ? 1 : 0);
+                  static_cast<O *>(out), add ? 1 : 0, by_row ? 1 : 0, scalars ? 1 : 0);
 }
 
 cudaError_t launch_seq_dh(int out_dtype, const SeqLoss &l, const SeqScratch &w, const float *part, int64_t nsplit,
                           int64_t d, const void *W, bool fused, const int *only_if, void *out, bool add, bool by_row,
-                          cudaStream_t st)
+                          bool scalars, cudaStream_t st)
 {
     Launch k(KK_SEQ_DH, st);
-    if (out_dtype == LOSSK_F32) return dh_one<float>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, st);
-    if (out_dtype == LOSSK_F16) return dh_one<h16_t>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, st);
-    return dh_one<uint16_t>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, st);
+    if (out_dtype == LOSSK_F32) return dh_one<float>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, scalars, st);
+    if (out_dtype == LOSSK_F16) return dh_one<h16_t>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, scalars, st);
+    return dh_one<uint16_t>(l, w, part, nsplit, d, W, fused, only_if, out, add, by_row, scalars, st);
 }
 
 } // namespace lossk

@@ -31,9 +31,8 @@ struct WsHeader {
 };
 constexpr int HDR_FAULT = 1, HDR_NEXT = 2;
 // The sequence losses' calls: sequences with a counted token (policy) or pairs that count
-// (preference), counted tokens of chosen sequences, bits of the largest |coefficient|, blocks
-// that have left their sums.
-constexpr int HDR_GROUPS = 3, HDR_CHOSEN = 4, HDR_COEF = 5, HDR_TICKET = 6;
+// (preference), counted tokens of chosen sequences, bits of the largest |coefficient|.
+constexpr int HDR_GROUPS = 3, HDR_CHOSEN = 4, HDR_COEF = 5;
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
 // Per-(token, logit tile) partial statistics written by the forward pass

@@ -259,6 +259,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
         TRY(launch_seq_merge_tiles(l, w, part, L.n_ct, nullptr, st));
         int32_t s = run_losses(c, l, w);
         if (s != LOSSK_OK) return s;
+        if (!c.g0) TRY(launch_seq_scalars(l, w, st));
         if (c.g0) {
             {
                 Launch k(KK_FP_ROWS, st);
@@ -266,7 +267,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
                               nullptr, w.tokp, nullptr, nullptr, nullptr, 0, 0, dhpart, c.n * c.d, st, false, n_dev,
                               bad));
             }
-            TRY(launch_seq_dh(LOSSK_F32, l, w, dhpart, L.nsplit, c.d, c.W, false, nullptr, c.g0, acc, false, st));
+            TRY(launch_seq_dh(LOSSK_F32, l, w, dhpart, L.nsplit, c.d, c.W, false, nullptr, c.g0, acc, false, true, st));
         }
         if (c.g1) {
             Launch k(KK_FP_COLS, st);
@@ -312,6 +313,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     int32_t s = run_forward(c, L, l, w, hid, fused ? redo : nullptr);
     if (s == LOSSK_OK) s = run_losses(c, l, w);
     if (s != LOSSK_OK) return s;
+    if (!c.g0) TRY(launch_seq_scalars(l, w, st));
 
     // d_hidden from the fused pass, beside the d_weight pass.
     SideStream *sd = fused && c.g1 ? side_stream(st) : nullptr;
@@ -328,7 +330,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     s = LOSSK_OK;
     void *dh_to = fused && acc ? static_cast<void *>(b + L.off_dhacc) : c.g0;
     if (fused &&
-        launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, true, nullptr, dh_to, false, false, aux) !=
+        launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, true, nullptr, dh_to, false, false, true, aux) !=
             cudaSuccess)
         s = LOSSK_DEVICE_ERROR;
     if (s == LOSSK_OK && c.g1) {
@@ -365,10 +367,11 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
         Launch k(KK_TC_ROWS, st);
         TRY(launch_bwp(BWD_ROWS, false, f16, a, a.n_fixed * a.n_split * a.n_dg, st));
     }
-    TRY(launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, false, only_if, dh_to, !fused && acc, false, st));
+    TRY(launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, false, only_if, dh_to, !fused && acc, false, !fused,
+                      st));
     if (fused && acc)
         TRY(launch_seq_dh(LOSSK_F32, l, w, static_cast<float *>(dh_to), 1, c.d, c.W, false, nullptr, c.g0, true, true,
-                          st));
+                          false, st));
     return LOSSK_OK;
 }
 
@@ -378,6 +381,7 @@ int32_t run_rows(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     const int32_t s = run_losses(c, l, w);
     if (s != LOSSK_OK) return s;
     if (c.g0) TRY(launch_seq_grad(c.dtype, l, w, c.X, c.g0, (c.flags & LOSSK_ACCUMULATE_GRADS) != 0, c.st));
+    else TRY(launch_seq_scalars(l, w, c.st));
     return LOSSK_OK;
 }
 

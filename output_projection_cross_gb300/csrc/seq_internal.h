@@ -81,17 +81,21 @@ cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, c
                              cudaStream_t st);
 // Per sequence the sum of log ratios (and the slope of LOSSK_SEQ_RATIO).
 cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
-// Per row its loss, outputs and coefficient; per pair its loss; the scalars.
+// Per row its loss, outputs and coefficient; per pair its loss.  The scalars: by a kernel of their
+// own where none follows, else by the one that does.
+constexpr int COEF_T = 128;
 cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
-// grad_logits of every row.
+cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
+// grad_logits of every row, and the scalars.
 cudaError_t launch_seq_grad(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,
                             bool accumulate, cudaStream_t st);
 // d_hidden of every row from the passes' split partials [nsplit][n_tok][d], indexed by
 // slot: fused, a_t / Z_t times their sum minus a_t W[y_t] (a value that is not
 // finite asks for the separate passes, redo), else their sum.  out: out_dtype.
 // add: added to it (float).  by_row: the partials are indexed by row.
+// scalars: writes them too.
 cudaError_t launch_seq_dh(int out_dtype, const SeqLoss &l, const SeqScratch &w, const float *part, int64_t nsplit,
                           int64_t d, const void *W, bool fused, const int *only_if, void *out, bool add,
-                          bool by_row, cudaStream_t st);
+                          bool by_row, bool scalars, cudaStream_t st);
 
 } // namespace lossk
