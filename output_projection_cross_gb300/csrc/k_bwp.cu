@@ -58,16 +58,19 @@
 //
 // The groups are persistent: each walks units u, u + #groups, ... with the
 // TMA ring, the TMEM logit buffer and the ring slots' counts carried across
-// units.  Step s of the schedule issues the pair's own logit tile, one of c
-// consecutive positions of the walk, and the accumulates of step s - 1's
-// positions.  In the row passes a unit takes whole steps (the last of them with
-// positions that hold no tile), so that which pair forms a tile, and with it
-// the order of the sums of G', is a function of the unit alone.  In the
-// d_weight pass the units follow one another without a gap: 9 supertiles over 8
-// pairs take 9/8 of a step, not two (2054 tokens of 2048: see the table of the
-// measurements).  A step may then end one unit and go on with the next.  Where
-// it does, the old unit's accumulates come first, then the own logit tile, under
-// which the accumulator is stored, then the new unit's.
+// units.  Step i of the schedule issues round i's own logit tile and the
+// accumulates of round i-1 (possibly of the previous unit).
+//
+// RUNS (d_weight, where a unit may be no whole number of rounds): the group's
+// tiles are numbered through its units, and step s issues the own one of tiles s c
+// .. s c + c - 1 and the accumulates of step s - 1's.  9 supertiles over 8 pairs then
+// take 9/8 of a step, not two (2050 tokens, d_model 2048, vocabulary 151936: 2270 ->
+// 1780 us).  A step may end one unit and go on with the next; where it does, the old
+// unit's accumulates come first, then the own logit tile, under which the
+// accumulator is stored, then the new unit's.  Every unit's accumulates stay in
+// their order, so d_weight's bits are the same.  The other passes keep rounds: there
+// which pair forms a tile decides the order of the sums of G', and units are long
+// (the run's bookkeeping took 3 to 5 % of a pass over 512 or 1000 tokens).
 //
 // Roles per CTA (224 threads): warp 0 loads this CTA's operand halves with TMA
 // (counted on the even CTA's stage barrier), warp 1 owns the pair's tensor
@@ -139,11 +142,18 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs &a, int n_fixed, int n
     return w;
 }
 
-// Position y of unit u, the k-th of this group, which takes len >= w.ny positions.
+// Position in this group's schedule: unit u (the k-th of the group), round r
+// of its nr rounds of c supertiles.
 struct BwdCursor {
-    int u, k, y, len;
+    int u, k, r, nr;
     BwdUnit w;
-    __device__ bool tile() const { return y < w.ny; }
+};
+
+// Where units follow one another without rounds of their own: position y of unit u, the
+// k-th of this group.
+struct RunCursor {
+    int u, k, y;
+    BwdUnit w;
 };
 
 // Per-writer counters indexed by a run-time CTA rank, kept in registers.
@@ -169,11 +179,12 @@ __device__ __forceinline__ void cnt_inc(int (&cnt)[B_MAXC], int i)
 // grad_scale / N_valid, so it stays inside fp16's range) and the accumulator
 // is multiplied by out_scale when it is stored.
 constexpr int B_THREADS = 224;
-template <int MODE, bool DISTILL, bool F16>
+template <int MODE, bool DISTILL, bool F16, bool RUNS>
 __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant__ BwdArgs a)
 {
     constexpr bool FUSED = MODE == BWD_FUSED;
     constexpr bool ROWS = MODE != BWD_COLS;     // token rows x vocabulary columns
+    static_assert(!RUNS || !ROWS, "the row passes' units have rounds");
     static_assert(!(FUSED && DISTILL), "the fused pass is label cross-entropy only");
     // Queued behind a validation that found a target out of range: every CTA
     // leaves before it touches anything (a refused call writes no output).
@@ -232,33 +243,42 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
     auto cursor_set = [&](BwdCursor &cu, int u, int k) {
         cu.u = u;
         cu.k = k;
-        cu.len = 1;
-        cu.w.ny = 0;
+        cu.r = 0;
+        cu.nr = 0;
         if (u < n_units) {
             cu.w = bwd_unit(a, n_fixed, n_loop, u);
-            cu.len = ROWS ? (cu.w.ny + c - 1) / c * c : cu.w.ny;
+            cu.nr = (cu.w.ny + c - 1) / c;
         }
     };
-    auto cursor_move = [&](BwdCursor &cu, int by) {
+    auto cursor_next = [&](BwdCursor &cu) {
+        if (++cu.r >= cu.nr) cursor_set(cu, cu.u + n_groups, cu.k + 1);
+    };
+    auto run_set = [&](RunCursor &cu, int u, int k) {
+        cu.u = u;
+        cu.k = k;
+        cu.w.ny = 1;
+        if (u < n_units) cu.w = bwd_unit(a, n_fixed, n_loop, u);
+    };
+    auto run_move = [&](RunCursor &cu, int by) {
         cu.y += by;
-        while (cu.u < n_units && cu.y >= cu.len) {
-            cu.y -= cu.len;
-            cursor_set(cu, cu.u + n_groups, cu.k + 1);
+        while (cu.u < n_units && cu.y >= cu.w.ny) {
+            cu.y -= cu.w.ny;
+            run_set(cu, cu.u + n_groups, cu.k + 1);
         }
     };
-    auto cursor_start = [&](BwdCursor &cu, int y) {
+    auto run_start = [&](RunCursor &cu, int y) {
         cu.y = 0;
-        cursor_set(cu, group, 0);
-        cursor_move(cu, y);
+        run_set(cu, group, 0);
+        run_move(cu, y);
     };
-    // A step's accumulates from cursor `acc` on: how many positions come before the own
-    // logit tile (a unit ends among them and another one follows), 0 where all come after.
-    auto before_own = [&](const BwdCursor &acc) {
+    // A step's accumulates from cursor `acc` on: how many come before the own logit tile (a
+    // unit ends among them and another one follows), 0 where all come after.
+    auto before_own = [&](const RunCursor &acc) {
         const int left = acc.w.ny - acc.y;
-        return !ROWS && acc.u + n_groups < n_units && left < c ? left : 0;
+        return acc.u + n_groups < n_units && left < c ? left : 0;
     };
     // 64-token stages of the d_weight pass's supertile that starts at token loop0
-    auto stages_of = [&](int loop0) { return ROWS ? 4 : min(4, max(1, (n_tok - loop0 + 63) >> 6)); };
+    auto stages_of = [&](int loop0) { return min(4, max(1, (n_tok - loop0 + 63) >> 6)); };
     // First row of slot g of grid CTA `cta` in the global grad-tile array
     // (a slot holds two 128 x 128 sub-tiles).
     auto slot_row = [&](int cta, int g) { return (cta * G_SLOTS + g) * 2 * 128; };
@@ -310,58 +330,70 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         auto advance = [&]() {
             if (++st == B_NST) { st = 0; ph ^= 1; }
         };
-        BwdCursor own, acc;
-        cursor_start(own, crank);
-        cursor_start(acc, 0);
-        int ahead = -1;                        // last unit whose successor was fetched ahead
-        // the accumulates' operands of the next n positions, the first of them written by pair wr
-        auto load_acc = [&](int wr, int n) {
-            for (; n > 0 && acc.u < n_units && ok; --n, ++wr, cursor_move(acc, 1)) {
-                if (!acc.tile()) continue;
-                const int slice0 = (acc.w.dg * c + crank) * TC_SLICE + hh * 128;   // own half of the d-slice
-                const int cw = cnt_get(cnt, wr);
-                const int g = cw % G_SLOTS;
-                // the writer's cw-th tile is published (the poller has seen it; its
-                // acquire and this one order the tile's stores before the loads)
-                if (!scnt_wait(smem_u32(&gseen[wr]), static_cast<unsigned>(cw + 1), err)) {
-                    ok = false;
-                    break;
+        if constexpr (RUNS) {
+            RunCursor own, acc;
+            run_start(own, crank);
+            run_start(acc, 0);
+            int ahead = -1;                        // last unit whose successor was fetched ahead
+            // the accumulates' operands of the next n positions, the first of them written by pair wr
+            auto load_acc = [&](int wr, int n) {
+                // in runs of one unit's tiles: work between two tiles' stages holds the ring up
+                while (n > 0 && acc.u < n_units && ok) {
+                  const int run = min(n, acc.w.ny - acc.y);
+                  const int slice0 = (acc.w.dg * c + crank) * TC_SLICE + hh * 128;   // own half of the d-slice
+                  const int tile0 = acc.w.yt_begin + acc.y;
+                  for (int q = 0; q < run; ++q) {
+                    const int cw = cnt_get(cnt, wr + q);
+                    const int g = cw % G_SLOTS;
+                    // the writer's cw-th tile is published (the poller has seen it; its
+                    // acquire and this one order the tile's stores before the loads)
+                    if (!scnt_wait(smem_u32(&gseen[wr + q]), static_cast<unsigned>(cw + 1), err)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_proxy_async_global();
+                    const int loop0 = (tile0 + q) * BWD_BN;
+                    const int grow = slot_row(wcta(wr + q), g);
+                    const int n_st = stages_of(loop0);
+                    for (int i = 0; i < n_st; ++i) {
+                        const int sub = i >> 1, h = i & 1;
+                        uint8_t *sp = acquire();
+                        if (!sp) { ok = false; break; }
+                        const uint32_t fb = fbar();
+                        tma_load_2d_pair(sp, &a.map_g, fb, h * 64, grow + sub * 128);
+                        if (a.ys3 && slice0 + 128 <= a.d)
+                            // the half slice's two 64-column blocks in one box
+                            tma_load_3d_pair(sp + B_APART, &a.map_ys3, fb, 0, loop0 + sub * 128 + h * 64, slice0 / 64);
+                        else
+                            for (int b = 0; b < 2; ++b)
+                                tma_load_2d_pair(sp + B_APART + b * 8192, &a.map_ys, fb, slice0 + b * 64,
+                                                 loop0 + sub * 128 + h * 64);
+                        advance();
+                    }
+                    if (!ok) break;
+                    cnt_inc(cnt, wr + q);
+                  }
+                  run_move(acc, run);
+                  wr += run;
+                  n -= run;
                 }
-                fence_proxy_async_global();
-                const int loop0 = (acc.w.yt_begin + acc.y) * BWD_BN;
-                const int grow = slot_row(wcta(wr), g);
-                const int n_st = stages_of(loop0);
-                for (int i = 0; i < n_st; ++i) {
-                    const int sub = i >> 1, h = i & 1;
-                    uint8_t *sp = acquire();
-                    if (!sp) { ok = false; break; }
-                    const uint32_t fb = fbar();
-                    tma_load_2d_pair(sp, &a.map_g, fb, h * 64, grow + sub * 128);
-                    if (a.ys3 && slice0 + 128 <= a.d)
-                        // the half slice's two 64-column blocks in one box
-                        tma_load_3d_pair(sp + B_APART, &a.map_ys3, fb, 0, loop0 + sub * 128 + h * 64, slice0 / 64);
-                    else
-                        for (int q = 0; q < 2; ++q)
-                            tma_load_2d_pair(sp + B_APART + q * 8192, &a.map_ys, fb, slice0 + q * 64,
-                                             loop0 + sub * 128 + h * 64);
-                    advance();
+            };
+            for (int s = 0; ok && (own.u < n_units || acc.u < n_units); ++s) {
+                if (own.u < n_units && own.k != ahead && own.u + n_groups < n_units) {
+                    // d_weight: the group's next unit has a new fixed tile (128 weight rows
+                    // over the whole d_model, read from HBM for the first time); bring it into
+                    // L2 now, the CTAs splitting its K steps
+                    ahead = own.k;
+                    const int fixn = bwd_unit(a, n_fixed, n_loop, own.u + n_groups).fixed * 256 + hh * 128;
+                    for (int kb = crank; kb < nk; kb += c) tma_prefetch_2d(&a.map_fix, kb * TC_BK, fixn);
                 }
-                cnt_inc(cnt, wr);
-            }
-        };
-        for (int s = 0; ok && (own.u < n_units || acc.u < n_units); ++s) {
-            if (!ROWS && own.u < n_units && own.k != ahead && own.u + n_groups < n_units) {
-                // d_weight: the group's next unit has a new fixed tile (128 weight rows
-                // over the whole d_model, read from HBM for the first time); bring it into
-                // L2 now, the CTAs splitting its K steps
-                ahead = own.k;
-                const int fixn = bwd_unit(a, n_fixed, n_loop, own.u + n_groups).fixed * 256 + hh * 128;
-                for (int kb = crank; kb < nk; kb += c) tma_prefetch_2d(&a.map_fix, kb * TC_BK, fixn);
-            }
-            const int first = s > 0 ? before_own(acc) : 0;
-            if (first) load_acc(0, first);
-            if (ok && own.u < n_units) {
-                if (own.tile()) {
+                const int first = s > 0 ? before_own(acc) : 0;
+                for (int part = first ? 0 : 1; part < 3 && ok; ++part) {
+                    if (part != 1) {
+                        if (s > 0) load_acc(part ? first : 0, part ? c - first : first);
+                        continue;
+                    }
+                    if (own.u >= n_units) continue;
                     // own 128 fixed rows of A, own 128 loop rows of B
                     const int fix0 = own.w.fixed * 256 + hh * 128, loop0 = (own.w.yt_begin + own.y) * BWD_BN + hh * 128;
                     for (int kb = 0; kb < nk; ++kb) {
@@ -372,10 +404,76 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                         tma_load_2d_pair(sp + B_APART, &a.map_loop, fb, kb * TC_BK, loop0);
                         advance();
                     }
+                    run_move(own, c);
                 }
-                cursor_move(own, c);
             }
-            if (ok && s > 0) load_acc(first, c - first);
+        } else {
+            BwdCursor cur, prev;
+            cursor_set(cur, group, 0);
+            bool have_prev = false;
+            while (ok && (cur.u < n_units || have_prev)) {
+                if (!ROWS && cur.u < n_units && cur.r == 0 && cur.u + n_groups < n_units) {
+                    // d_weight: the group's next unit has a new fixed tile (128 weight rows
+                    // over the whole d_model, read from HBM for the first time); bring it into
+                    // L2 now, the CTAs splitting its K steps
+                    const int fixn = bwd_unit(a, n_fixed, n_loop, cur.u + n_groups).fixed * 256 + hh * 128;
+                    for (int kb = crank; kb < nk; kb += c) tma_prefetch_2d(&a.map_fix, kb * TC_BK, fixn);
+                }
+                if (cur.u < n_units) {
+                    const int y = cur.r * c + crank;
+                    if (y < cur.w.ny) {
+                        // own 128 fixed rows of A, own 128 loop rows of B
+                        const int fix0 = cur.w.fixed * 256 + hh * 128, loop0 = (cur.w.yt_begin + y) * BWD_BN + hh * 128;
+                        for (int kb = 0; kb < nk; ++kb) {
+                            uint8_t *sp = acquire();
+                            if (!sp) { ok = false; break; }
+                            const uint32_t fb = fbar();
+                            tma_load_2d_pair(sp, &a.map_fix, fb, kb * TC_BK, fix0);
+                            tma_load_2d_pair(sp + B_APART, &a.map_loop, fb, kb * TC_BK, loop0);
+                            advance();
+                        }
+                        if (!ok) break;
+                    }
+                }
+                if (have_prev) {
+                    const int slice0 = (prev.w.dg * c + crank) * TC_SLICE + hh * 128;   // own half of the d-slice
+                    const int y0 = prev.r * c, y_end = min(y0 + c, prev.w.ny);
+                    for (int yy = y0; yy < y_end && ok; ++yy) {
+                        const int wr = yy - y0;
+                        const int cw = cnt_get(cnt, wr);
+                        const int g = cw % G_SLOTS;
+                        // the writer's cw-th tile is published (the poller has seen it; its
+                        // acquire and this one order the tile's stores before the loads)
+                        if (!scnt_wait(smem_u32(&gseen[wr]), static_cast<unsigned>(cw + 1), err)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_proxy_async_global();
+                        const int loop0 = (prev.w.yt_begin + yy) * BWD_BN;
+                        const int grow = slot_row(wcta(wr), g);
+                        for (int sub = 0; sub < 2 && ok; ++sub)
+                            for (int h = 0; h < 2; ++h) {
+                                uint8_t *sp = acquire();
+                                if (!sp) { ok = false; break; }
+                                const uint32_t fb = fbar();
+                                tma_load_2d_pair(sp, &a.map_g, fb, h * 64, grow + sub * 128);
+                                if (a.ys3 && slice0 + 128 <= a.d)
+                                    // the half slice's two 64-column blocks in one box
+                                    tma_load_3d_pair(sp + B_APART, &a.map_ys3, fb, 0, loop0 + sub * 128 + h * 64,
+                                                     slice0 / 64);
+                                else
+                                    for (int q = 0; q < 2; ++q)
+                                        tma_load_2d_pair(sp + B_APART + q * 8192, &a.map_ys, fb, slice0 + q * 64,
+                                                         loop0 + sub * 128 + h * 64);
+                                advance();
+                            }
+                        cnt_inc(cnt, wr);
+                    }
+                }
+                have_prev = cur.u < n_units;
+                prev = cur;
+                if (cur.u < n_units) cursor_next(cur);
+            }
         }
         for (int s = 0; s < B_NST; ++s)
             if (issued & (1u << s)) bw_wait_drain(&full[s], (last_ph >> s) & 1);
@@ -396,50 +494,61 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         const uint64_t dBs = sdesc_sw128(ring0 + B_APART, 16, 1024);      // logit B: K-major, 128 rows per CTA
         const uint64_t dBa = sdesc_sw128(ring0 + B_APART, 8192, 1024);    // accumulate B: MN-major
         constexpr uint64_t STEP = B_STAGE >> 4;
-        BwdCursor own, acc;
-        cursor_start(own, crank);
-        cursor_start(acc, 0);
-        auto accumulate = [&](int wr, int n) {
-            for (; n > 0 && acc.u < n_units && ok; --n, ++wr, cursor_move(acc, 1)) {
-                if (!acc.tile()) continue;
-                if (acc.y == 0) {
-                    // first accumulate of a unit: the previous unit's accumulator must be stored
-                    if (!mbar_wait(accempty, (acc.k & 1) ^ 1, err)) { ok = false; break; }
-                    tc_fence_after();
-                    first_acc = true;
-                }
-                const int g = cnt_get(cnt, wr) % G_SLOTS;
-                const int n_st = stages_of((acc.w.yt_begin + acc.y) * BWD_BN);
-                for (int i = 0; i < n_st; ++i) {
-                    if (!mbar_wait(&full[st], ph, err)) { ok = false; break; }
-                    tc_fence_after();
-                    // all quarters of both writer CTAs' halves that are read have landed: their
-                    // slots may be refilled (completed reads, nothing to publish: relaxed
-                    // adds, which never hold the issuer)
-                    if (i == n_st - 1) {
-                        gsig_add_relaxed(&gfree[(2 * (pbase + wr)) * G_SLOTS + g], 1u);
-                        gsig_add_relaxed(&gfree[(2 * (pbase + wr) + 1) * G_SLOTS + g], 1u);
+        if constexpr (RUNS) {
+            RunCursor own, acc;
+            run_start(own, crank);
+            run_start(acc, 0);
+            auto accumulate = [&](int wr, int n) {
+                while (n > 0 && acc.u < n_units && ok) {
+                    const int run = min(n, acc.w.ny - acc.y);
+                    if (acc.y == 0) {
+                        // first accumulate of a unit: the previous unit's accumulator must be stored
+                        if (!mbar_wait(accempty, (acc.k & 1) ^ 1, err)) { ok = false; break; }
+                        tc_fence_after();
+                        first_acc = true;
                     }
-                    const uint64_t off = st * STEP;
-                    const uint64_t da = dA + off, db = dBa + off;
-                    tc_mma_bf16_pair(tmem + ACC_COL, da, db, ID_ACC, first_acc ? 0u : 1u);
-                    tc_mma_bf16_pair(tmem + ACC_COL, da + 2, db + 128, ID_ACC, 1u);
-                    tc_mma_bf16_pair(tmem + ACC_COL, da + 4, db + 256, ID_ACC, 1u);
-                    tc_mma_bf16_pair(tmem + ACC_COL, da + 6, db + 384, ID_ACC, 1u);
-                    first_acc = false;
-                    tc_commit_pair_multicast(&empty[st], 3);
-                    if (++st == B_NST) { st = 0; ph ^= 1; }
+                    const int tile0 = acc.w.yt_begin + acc.y;
+                    for (int q = 0; q < run; ++q) {
+                        const int g = cnt_get(cnt, wr + q) % G_SLOTS;
+                        const int n_st = stages_of((tile0 + q) * BWD_BN);
+                        for (int i = 0; i < n_st; ++i) {
+                            if (!mbar_wait(&full[st], ph, err)) { ok = false; break; }
+                            tc_fence_after();
+                            // all quarters of both writer CTAs' halves that are read have landed: their
+                            // slots may be refilled (completed reads, nothing to publish: relaxed
+                            // adds, which never hold the issuer)
+                            if (i == n_st - 1) {
+                                gsig_add_relaxed(&gfree[(2 * (pbase + wr + q)) * G_SLOTS + g], 1u);
+                                gsig_add_relaxed(&gfree[(2 * (pbase + wr + q) + 1) * G_SLOTS + g], 1u);
+                            }
+                            const uint64_t off = st * STEP;
+                            const uint64_t da = dA + off, db = dBa + off;
+                            tc_mma_bf16_pair(tmem + ACC_COL, da, db, ID_ACC, first_acc ? 0u : 1u);
+                            tc_mma_bf16_pair(tmem + ACC_COL, da + 2, db + 128, ID_ACC, 1u);
+                            tc_mma_bf16_pair(tmem + ACC_COL, da + 4, db + 256, ID_ACC, 1u);
+                            tc_mma_bf16_pair(tmem + ACC_COL, da + 6, db + 384, ID_ACC, 1u);
+                            first_acc = false;
+                            tc_commit_pair_multicast(&empty[st], 3);
+                            if (++st == B_NST) { st = 0; ph ^= 1; }
+                        }
+                        if (!ok) break;
+                        cnt_inc(cnt, wr + q);
+                    }
+                    if (!ok) break;
+                    if (acc.y + run == acc.w.ny) tc_commit_pair_multicast(accfull, 3);
+                    run_move(acc, run);
+                    wr += run;
+                    n -= run;
                 }
-                if (!ok) break;
-                cnt_inc(cnt, wr);
-                if (acc.y == acc.w.ny - 1) tc_commit_pair_multicast(accfull, 3);
-            }
-        };
-        for (int s = 0; ok && (own.u < n_units || acc.u < n_units); ++s) {
-            const int first = s > 0 ? before_own(acc) : 0;
-            if (first) accumulate(0, first);
-            if (ok && own.u < n_units) {
-                if (own.tile()) {
+            };
+            for (int s = 0; ok && (own.u < n_units || acc.u < n_units); ++s) {
+                const int first = s > 0 ? before_own(acc) : 0;
+                for (int part = first ? 0 : 1; part < 3 && ok; ++part) {
+                    if (part != 1) {
+                        if (s > 0) accumulate(part ? first : 0, part ? c - first : first);
+                        continue;
+                    }
+                    if (own.u >= n_units) continue;
                     if (!mbar_wait(tempty, (m_all & 1) ^ 1, err)) { ok = false; break; }
                     tc_fence_after();
                     for (int kb = 0; kb < nk; ++kb) {
@@ -457,10 +566,76 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                     if (!ok) break;
                     tc_commit_pair_multicast(tfull, 3);
                     ++m_all;
+                    run_move(own, c);
                 }
-                cursor_move(own, c);
             }
-            if (ok && s > 0) accumulate(first, c - first);
+        } else {
+            BwdCursor cur, prev;
+            cursor_set(cur, group, 0);
+            bool have_prev = false;
+            while (ok && (cur.u < n_units || have_prev)) {
+                if (cur.u < n_units) {
+                    const int y = cur.r * c + crank;
+                    if (y < cur.w.ny) {
+                        if (!mbar_wait(tempty, (m_all & 1) ^ 1, err)) { ok = false; break; }
+                        tc_fence_after();
+                        for (int kb = 0; kb < nk; ++kb) {
+                            if (!mbar_wait(&full[st], ph, err)) { ok = false; break; }
+                            tc_fence_after();
+                            const uint64_t off = st * STEP;
+                            const uint64_t a = dA + off, b = dBs + off;
+                            tc_mma_bf16_pair(tmem, a, b, ID_S, kb != 0);
+                            tc_mma_bf16_pair(tmem, a + 2, b + 2, ID_S, 1u);
+                            tc_mma_bf16_pair(tmem, a + 4, b + 4, ID_S, 1u);
+                            tc_mma_bf16_pair(tmem, a + 6, b + 6, ID_S, 1u);
+                            tc_commit_pair_multicast(&empty[st], 3);
+                            if (++st == B_NST) { st = 0; ph ^= 1; }
+                        }
+                        if (!ok) break;
+                        tc_commit_pair_multicast(tfull, 3);
+                        ++m_all;
+                    }
+                }
+                if (have_prev) {
+                    if (prev.r == 0) {
+                        // first accumulate of a unit: the previous unit's accumulator must be stored
+                        if (!mbar_wait(accempty, (prev.k & 1) ^ 1, err)) { ok = false; break; }
+                        tc_fence_after();
+                        first_acc = true;
+                    }
+                    const int y0 = prev.r * c, y_end = min(y0 + c, prev.w.ny);
+                    for (int yy = y0; yy < y_end && ok; ++yy) {
+                        const int wr = yy - y0;
+                        const int g = cnt_get(cnt, wr) % G_SLOTS;
+                        for (int sidx = 0; sidx < 4; ++sidx) {
+                            if (!mbar_wait(&full[st], ph, err)) { ok = false; break; }
+                            tc_fence_after();
+                            // all four quarters of both writer CTAs' halves have landed: their
+                            // slots may be refilled (completed reads, nothing to publish: relaxed
+                            // adds, which never hold the issuer)
+                            if (sidx == 3) {
+                                gsig_add_relaxed(&gfree[(2 * (pbase + wr)) * G_SLOTS + g], 1u);
+                                gsig_add_relaxed(&gfree[(2 * (pbase + wr) + 1) * G_SLOTS + g], 1u);
+                            }
+                            const uint64_t off = st * STEP;
+                            const uint64_t a = dA + off, b = dBa + off;
+                            tc_mma_bf16_pair(tmem + ACC_COL, a, b, ID_ACC, first_acc ? 0u : 1u);
+                            tc_mma_bf16_pair(tmem + ACC_COL, a + 2, b + 128, ID_ACC, 1u);
+                            tc_mma_bf16_pair(tmem + ACC_COL, a + 4, b + 256, ID_ACC, 1u);
+                            tc_mma_bf16_pair(tmem + ACC_COL, a + 6, b + 384, ID_ACC, 1u);
+                            first_acc = false;
+                            tc_commit_pair_multicast(&empty[st], 3);
+                            if (++st == B_NST) { st = 0; ph ^= 1; }
+                        }
+                        cnt_inc(cnt, wr);
+                    }
+                    if (!ok) break;
+                    if (prev.r == prev.nr - 1) tc_commit_pair_multicast(accfull, 3);
+                }
+                have_prev = cur.u < n_units;
+                prev = cur;
+                if (cur.u < n_units) cursor_next(cur);
+            }
         }
         if (group < n_units) {                 // (a group may have no unit where the device counted the tokens)
             tc_commit_pair_multicast(drain, 1);
@@ -476,18 +651,38 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         // loaded it, so the counts stay in step with what the loader reads.
         int cnt[B_MAXC] = {};
         bool ok = true;
-        BwdCursor acc;
-        cursor_start(acc, 0);
-        for (int wr = 0; acc.u < n_units && ok; cursor_move(acc, 1), wr = wr + 1 == c ? 0 : wr + 1) {
-            if (!acc.tile()) continue;
-            const int cw = cnt_get(cnt, wr);
-            if (!gsig_wait(&gready[wcta(wr) * G_SLOTS + cw % G_SLOTS], 4u * static_cast<unsigned>(cw / G_SLOTS + 1),
-                           err)) {
-                ok = false;
-                break;
+        if constexpr (RUNS) {
+            RunCursor acc;
+            run_start(acc, 0);
+            for (int wr = 0; acc.u < n_units && ok; run_move(acc, 1), wr = wr + 1 == c ? 0 : wr + 1) {
+                const int cw = cnt_get(cnt, wr);
+                if (!gsig_wait(&gready[wcta(wr) * G_SLOTS + cw % G_SLOTS], 4u * static_cast<unsigned>(cw / G_SLOTS + 1),
+                               err)) {
+                    ok = false;
+                    break;
+                }
+                st_release_cta_shared(smem_u32(&gseen[wr]), static_cast<unsigned>(cw + 1));
+                cnt_inc(cnt, wr);
             }
-            st_release_cta_shared(smem_u32(&gseen[wr]), static_cast<unsigned>(cw + 1));
-            cnt_inc(cnt, wr);
+        } else {
+            for (int u = group; u < n_units && ok; u += n_groups) {
+                const BwdUnit w = bwd_unit(a, n_fixed, n_loop, u);
+                const int nr = (w.ny + c - 1) / c;
+                for (int rr = 0; rr < nr && ok; ++rr) {
+                    const int y0 = rr * c, y_end = min(y0 + c, w.ny);
+                    for (int yy = y0; yy < y_end; ++yy) {
+                        const int wr = yy - y0;
+                        const int cw = cnt_get(cnt, wr);
+                        if (!gsig_wait(&gready[wcta(wr) * G_SLOTS + cw % G_SLOTS],
+                                       4u * static_cast<unsigned>(cw / G_SLOTS + 1), err)) {
+                            ok = false;
+                            break;
+                        }
+                        st_release_cta_shared(smem_u32(&gseen[wr]), static_cast<unsigned>(cw + 1));
+                        cnt_inc(cnt, wr);
+                    }
+                }
+            }
         }
     } else if (warp >= 2 && warp < 6) {
         // ================= epilogue =================
@@ -528,14 +723,15 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             return p;
         };
         int m_all = 0;                                // own logit tiles consumed so far
-        // d_weight with the token range whole (one split): a CTA's own token supertiles
-        // are the same in every unit where a unit takes whole steps, and no more than four
-        // where there are four; their per-token parameters are then loaded once, into
-        // one copy the four warps share (four supertiles at most: 16 KB).  The one
-        // barrier among the epilogue warps sits here, before any wait a warp could
-        // unwind from.
-        const bool whole = n_loop % c == 0;
-        const int n_cached = whole ? n_loop / c : n_loop;      // block i: supertile i c + crank, or i
+        auto n_own_of = [&](const BwdUnit &w) { return crank < w.ny ? (w.ny - crank + c - 1) / c : 0; };
+        // d_weight with the token range whole (one split): where a unit takes whole rounds
+        // a CTA's own token supertiles are the same in every unit, and in a run of units they
+        // are no more than the supertiles there are; their per-token parameters are then
+        // loaded once, into one copy the four warps share (four supertiles at most: 16
+        // KB).  The one barrier among the epilogue warps sits here, before any wait a warp
+        // could unwind from.
+        const bool by_own = !RUNS || n_loop % c == 0;          // block i: supertile i c + crank, or i
+        const int n_cached = !by_own ? n_loop : crank < n_loop ? (n_loop - crank + c - 1) / c : 0;
         const bool pcache = !ROWS && a.n_split == 1 && n_cached <= 4;
         // Label-CE d_weight keeps a supertile's 256 token parameters (4 KB) as
         // {x_j, c_j, x_j+1, c_j+1} pairs in the first 2 KB (the exponent shift
@@ -556,7 +752,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         };
         if (pcache) {
             for (int i = r; i < n_cached * BWD_BN; i += 128) {
-                const int t = (whole ? (i / BWD_BN) * c + crank : i / BWD_BN) * BWD_BN + i % BWD_BN;
+                const int t = (by_own ? (i / BWD_BN) * c + crank : i / BWD_BN) * BWD_BN + i % BWD_BN;
                 put_param(sPall + (i / BWD_BN) * BWD_BN, i % BWD_BN, param(t));
             }
             named_bar_sync(1, 128);
@@ -611,7 +807,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                 }
                 __syncwarp();
             }
-            const float4 *sPt = pcache ? sPall + (whole ? y / c : y) * BWD_BN : sP;   // d_weight: the tile's token parameters
+            const float4 *sPt = pcache ? sPall + (by_own ? y / c : y) * BWD_BN : sP;   // d_weight: the tile's token parameters
             if (DISTILL && y + c < w.ny) teacher_prefetch(w, y + c);
             ok = ok && mbar_wait(tfull, m_all & 1, err);
             if (!__all_sync(0xffffffffu, ok)) return false;
@@ -1008,50 +1204,84 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             }
             return true;
         };
-        // The steps in order: a step's own tile, then the accumulators of the units that end
-        // in its accumulates (its tile's logits are ready earlier, and the MMA can start the
-        // next logit tile while the store runs), but for one that ends before the own
-        // logit tile is computed, which is stored first.
-        BwdCursor own, acc;
-        cursor_start(own, crank);
-        cursor_start(acc, 0);
-        int mine = -1;                                // the unit (k) that P and zsum belong to
-        float4 P = P0;
-        double zsum = 0.0, zlast = 0.0;               // of the unit of `mine`, of the one before it
-        bool ok = true;
-        for (int s = 0; ok && (own.u < n_units || acc.u < n_units); ++s) {
-            int left = s > 0 ? c : 0;                 // positions whose accumulates this step issues
-            // on to the end of the unit, whose accumulator is stored, or of the positions
-            auto ends = [&]() -> bool {
-                const int n = acc.w.ny - acc.y;
-                const bool end = n > 0 && n <= left;
-                const int by = end ? n : left;
-                if (end) {
-                    const int u = acc.u, k = acc.k;
+        if constexpr (RUNS) {
+            // The steps in order: a step's own tile, then the accumulators of the units that end
+            // in its accumulates (its tile's logits are ready earlier, and the MMA can start the
+            // next logit tile while the store runs), but for one that ends before the own
+            // logit tile is computed, which is stored first.
+            RunCursor own, acc;
+            run_start(own, crank);
+            run_start(acc, 0);
+            double zsum = 0.0;                            // (of the fused pass, whose units have rounds)
+            bool ok = true;
+            for (int s = 0; ok && (own.u < n_units || acc.u < n_units); ++s) {
+                int left = s > 0 ? c : 0;                 // positions whose accumulates this step issues
+                bool store_first = left > 0 && before_own(acc) > 0, formed = false;
+                while (ok) {
+                    if (!formed && !store_first) {
+                        formed = true;
+                        if (own.u < n_units) {
+                            ok = tile(own.w, own.y, P0, zsum);
+                            run_move(own, c);
+                            if (!ok) break;
+                        }
+                    }
+                    store_first = false;
+                    if (left <= 0 || acc.u >= n_units) {
+                        if (formed) break;
+                        continue;
+                    }
+                    // on to the end of the unit, whose accumulator is stored, or of the positions
+                    const int n = acc.w.ny - acc.y;
+                    const bool end = n <= left;
+                    const int by = end ? n : left, u = acc.u, k = acc.k;
                     const BwdUnit w = acc.w;
-                    cursor_move(acc, by);
+                    run_move(acc, by);
                     left -= by;
-                    return store(u, k, w, k == mine ? zsum : zlast);
+                    if (end) ok = store(u, k, w, zsum);
                 }
-                cursor_move(acc, by);
-                left -= by;
-                return true;
-            };
-            if (left > 0 && before_own(acc)) ok = ends();
-            if (ok && own.u < n_units) {
-                if (own.k != mine) {
-                    mine = own.k;
-                    P = params_of(own.w);
-                    zlast = zsum;
-                    zsum = 0.0;
-                }
-                if (own.tile()) ok = tile(own.w, own.y, P, zsum);
-                cursor_move(own, c);
-            } else if (own.k != mine) {               // no unit left of its own
-                mine = own.k;
-                zlast = zsum;
             }
-            while (ok && left > 0 && acc.u < n_units) ok = ends();
+        } else {
+            // Units in order.  The next unit's first own tile is formed before this
+            // unit's accumulator is stored: its logits are ready earlier (the MMA
+            // issues them before this unit's last accumulates), and the MMA can
+            // then start the next logit tile while the store runs.
+            int u = group;
+            BwdUnit w;
+            float4 P = P0;
+            double zsum = 0.0;
+            int m0 = 0;                                   // own tiles of unit w already formed
+            if (u < n_units) {
+                w = bwd_unit(a, n_fixed, n_loop, u);
+                P = params_of(w);
+            }
+            bool ok = true;
+            for (int k = 0; u < n_units && ok; ++k) {
+                const int n_own = n_own_of(w);
+                for (int m = m0; m < n_own && ok; ++m) ok = tile(w, m * c + crank, P, zsum);
+                if (!ok) break;
+                const int u2 = u + n_groups;
+                BwdUnit w2;
+                float4 P2 = P0;
+                double zsum2 = 0.0;
+                int m02 = 0;
+                if (u2 < n_units) {
+                    w2 = bwd_unit(a, n_fixed, n_loop, u2);
+                    P2 = params_of(w2);
+                    if (n_own_of(w2) > 0) {
+                        ok = tile(w2, crank, P2, zsum2);
+                        if (!ok) break;
+                        m02 = 1;
+                    }
+                }
+                ok = store(u, k, w, zsum);
+                if (!ok) break;
+                u = u2;
+                w = w2;
+                P = P2;
+                zsum = zsum2;
+                m0 = m02;
+            }
         }
         if (TTMA)
             for (int k = tuse_all; k < tiss_all; ++k) bw_wait_drain(&tw_b[k & 1], (k >> 1) & 1);
@@ -1069,10 +1299,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
     }
 }
 
-template <int MODE, bool DISTILL, bool F16>
+template <int MODE, bool DISTILL, bool F16, bool RUNS = false>
 static cudaError_t launch_bwp_one(const BwdArgs &a, int n_units, cudaStream_t st)
 {
-    auto k = bwp_kernel<MODE, DISTILL, F16>;
+    auto k = bwp_kernel<MODE, DISTILL, F16, RUNS>;
     constexpr int SMEM = bwd_smem<MODE, DISTILL>();
     // The function attribute and the resident-pair count are set up once per
     // device: the launch of the training step's first pass waits on the host
@@ -1129,6 +1359,10 @@ static cudaError_t launch_bwp_one(const BwdArgs &a, int n_units, cudaStream_t st
 cudaError_t launch_bwp(int mode, bool distill, bool f16, const BwdArgs &a, int n_units, cudaStream_t st)
 {
     if (a.n_cl < 1 || a.n_cl > B_MAXC) return cudaErrorInvalidValue;
+    // d_weight: a run of units where a unit may be no whole number of rounds
+    const bool runs = mode == BWD_COLS && !distill && (a.n_dev || a.n_loop % a.n_cl != 0);
+    if (runs) return f16 ? launch_bwp_one<BWD_COLS, false, true, true>(a, n_units, st)
+                         : launch_bwp_one<BWD_COLS, false, false, true>(a, n_units, st);
     if (mode == BWD_FUSED) return f16 ? cudaErrorInvalidValue : launch_bwp_one<BWD_FUSED, false, false>(a, n_units, st);
     if (f16) {
         if (mode == BWD_ROWS)
