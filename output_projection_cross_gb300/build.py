@@ -25,7 +25,7 @@ LIB = os.path.join(BUILD, "liblossk.so")
 CALLS = os.path.join(BUILD, "_lossk_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["lossk_abi.cu", "k_fwd2.cu", "k_bwp.cu", "k_simt.cu", "lossk_static.cu", "lossk_decode.cu", "k_beam.cu", "k_pages.cu",
            "k_attn.cu", "k_attn_mma.cu", "k_attn_ffma.cu", "lossk_seq.cu", "k_seq.cu", "k_rows.cu"]
-HEADERS = ["ptx.cuh", "lossk_internal.h", "host_internal.h", "seq_internal.h", "seq_scalars.cuh", "decode_internal.h", "decode_launch.h", "attn_split.cuh", "float2.cuh"]
+HEADERS = ["ptx.cuh", "lossk_internal.h", "host_internal.h", "seq_internal.h", "seq_terms.cuh", "decode_internal.h", "decode_launch.h", "attn_split.cuh", "float2.cuh"]
 CALLS_SOURCE = "lossk_calls.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -81,6 +81,7 @@
 // path (it otherwise held the MMAs up at the first stage of every grad tile
 // but a round's first).  TMEM per CTA: one 256-column
 // logit buffer and the 256-column accumulator.  Every wait is bounded.
+#include "decode_launch.h"
 #include "lossk_internal.h"
 #include "ptx.cuh"
 
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
     constexpr bool ROWS = MODE != BWD_COLS;     // token rows x vocabulary columns
     static_assert(!RUNS || !ROWS, "the row passes' units have rounds");
     static_assert(!(FUSED && DISTILL), "the fused pass is label cross-entropy only");
+    wait_for_stream();
     // Queued behind a validation that found a target out of range: every CTA
     // leaves before it touches anything (a refused call writes no output).
     if (a.refused && *reinterpret_cast<const volatile int *>(a.refused)) return;
@@ -1317,7 +1319,9 @@ static cudaError_t launch_bwp_one(const BwdArgs &a, int n_units, cudaStream_t st
     cfg.blockDim = dim3(B_THREADS, 1, 1);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
@@ -1349,10 +1353,12 @@ static cudaError_t launch_bwp_one(const BwdArgs &a, int n_units, cudaStream_t st
     if (groups * 2 * a.n_cl > G_MAX_CTAS) groups = G_MAX_CTAS / (2 * a.n_cl);
     if (groups < 1) return cudaErrorInvalidConfiguration;
     // the ring's hand-off counters start from zero
-    e = cudaMemsetAsync(a.gsig, 0, sizeof(unsigned) * 2 * G_MAX_CTAS * G_SLOTS, st);
-    if (e != cudaSuccess) return e;
+    if (!a.chained) {
+        e = cudaMemsetAsync(a.gsig, 0, sizeof(unsigned) * 2 * G_MAX_CTAS * G_SLOTS, st);
+        if (e != cudaSuccess) return e;
+    }
     cfg.gridDim = dim3(groups * 2 * a.n_cl, 1, 1);
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.chained ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 

@@ -22,6 +22,7 @@
 // TMA, counting the bytes on the even CTA's stage barrier; warp 1 of both
 // CTAs owns the pair's tensor memory, and the even CTA's issues the MMAs;
 // warps 2-5 of each CTA reduce that CTA's 128 rows.  Every wait is bounded.
+#include "decode_launch.h"
 #include "lossk_internal.h"
 #include "ptx.cuh"
 
@@ -53,6 +54,7 @@ __device__ __forceinline__ void f2_wait_drain(uint64_t *bar, uint32_t parity)
 template <bool DISTILL, bool F16>
 __global__ void __launch_bounds__(192, 1) fwd2_kernel(const __grid_constant__ TcArgs a)
 {
+    wait_for_stream();
     if (a.refused && *reinterpret_cast<const volatile int *>(a.refused)) return;
     if (a.only_if && !*reinterpret_cast<const volatile int *>(a.only_if)) return;
     // the launch's tokens, or as many as an earlier kernel gathered
@@ -300,13 +302,15 @@ template <bool DISTILL, bool F16> static cudaError_t launch_fwd2_one(const TcArg
     cfg.blockDim = dim3(192, 1, 1);
     cfg.dynamicSmemBytes = F2_SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.chained ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 

@@ -13,20 +13,13 @@
 #include "decode_internal.h"
 #include "decode_launch.h"
 #include "ptx.cuh"
-#include "seq_scalars.cuh"
+#include "seq_terms.cuh"
 
 #include <type_traits>
 
 namespace lossk {
 
 namespace {
-
-__device__ __forceinline__ bool refused(const WsHeader *hdr)
-{
-    return *reinterpret_cast<const volatile int *>(&hdr->bad_targets) != 0;
-}
-
-__device__ __forceinline__ int slots_before(int slot) { return slot < 0 ? ~slot : slot; }
 
 // The sequence that holds slot c: the last one whose slots start at or before it.  The
 // whole warp calls it, each step reads 32 of the starts (a thread of its own would wait
@@ -149,6 +142,7 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
         done += all;
         __syncthreads();
     }
+    for (int i = tid; i < w.n_words; i += PREP_T) w.words[i] = 0;
     bad |= range_all || wrong;
     int groups = 0, chosen = 0;
     const bool any_bad = __syncthreads_or(bad) != 0;
@@ -192,7 +186,7 @@ __global__ void __launch_bounds__(256) seq_gather_kernel(const SeqLoss l, const 
                                                          const T *__restrict__ W, int64_t d, T *__restrict__ out)
 {
     wait_for_stream();
-    if (refused(w.hdr)) return;
+    if (seq_refused(w.hdr)) return;
     const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int n_valid = w.hdr->n_valid;
     if (c >= max((n_valid + 255) & ~255, 256)) return;
@@ -255,7 +249,7 @@ __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, co
                                                              const float *__restrict__ zpart, int64_t nz)
 {
     wait_for_stream();
-    if (refused(w.hdr)) return;
+    if (seq_refused(w.hdr)) return;
     const int c = blockIdx.x * 32 + threadIdx.x;
     if (c >= w.hdr->n_valid) return;
     float Z = 0.f;
@@ -292,7 +286,7 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
                                                                     const int *only_if)
 {
     wait_for_stream();
-    if (refused(w.hdr) || (only_if && !*reinterpret_cast<const volatile int *>(only_if))) return;
+    if (seq_refused(w.hdr) || (only_if && !*reinterpret_cast<const volatile int *>(only_if))) return;
     __shared__ float s_max[MT_W][32];
     __shared__ double s_sum[MT_W][32];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
@@ -329,55 +323,12 @@ cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const 
                   part, n_ct, only_if);
 }
 
-namespace {
-
-// A counted row's weight in the mean: n_s its sequence's counted tokens.
-__device__ __forceinline__ double row_weight(const SeqLoss &l, const WsHeader *hdr, int n_s)
-{
-    const bool sum = l.flags & LOSSK_REDUCE_SUM;
-    if (l.flags & LOSSK_SEQ_MEAN) return 1.0 / (static_cast<double>(n_s) * (sum ? 1 : hdr->pad[HDR_GROUPS]));
-    return sum ? 1.0 : 1.0 / hdr->n_valid;
-}
-
-struct PolicyTerm {
-    float loss, slope;      // P and dP / d(log ratio)
-    bool clipped;
-};
-
-// log ratio `delta` (exp in float or, for ratios of sequences a few 1e-4 from 1, in double)
-template <typename F> __device__ __forceinline__ PolicyTerm policy_term(const SeqLoss &l, F delta, float A)
-{
-    if (A == 0.f) return PolicyTerm{0.f, 0.f, false};
-    const F r = exp(delta);
-    const F edge = A > 0.f ? F(1) + static_cast<F>(l.high) : F(1) - static_cast<F>(l.low);
-    const bool out = A > 0.f ? r > edge : r < edge;
-    return PolicyTerm{static_cast<float>(-A * (out ? edge : r)), out ? 0.f : static_cast<float>(-A * r), out};
-}
-
-__device__ __forceinline__ float advantage(const SeqLoss &l, int row, int seq)
-{
-    return l.adv[(l.flags & LOSSK_SEQ_ADVANTAGES) ? seq : row];
-}
-
-__device__ __forceinline__ double block_sum(double v, double *sh)
-{
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sh[0];
-    for (unsigned i = 1; i < blockDim.x / 32; ++i) v += sh[i];
-    return v;
-}
-
-} // namespace
-
 // One block per sequence; the order of the sum is a function of its length.
 constexpr int SUM_T = 256;
 __global__ void __launch_bounds__(SUM_T) seq_sum_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
-    if (refused(w.hdr)) return;
+    if (seq_refused(w.hdr)) return;
     __shared__ double sh[SUM_T / 32];
     const int s = blockIdx.x, a = w.seq_slot[s], b = w.seq_slot[s + 1];
     const float *base = l.pairs > 0 ? l.ref : l.old;
@@ -405,28 +356,6 @@ cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t s
 
 namespace {
 
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-
-// Of pair i: its loss and d loss / du.
-__device__ __forceinline__ void pair_term(const SeqLoss &l, double u, float &loss, float &slope)
-{
-    if (l.objective == LOSSK_PREF_SQUARED) {
-        const float g = static_cast<float>(u - 0.5 / static_cast<double>(l.beta));
-        loss = g * g;
-        slope = 2.f * g;
-        return;
-    }
-    const float h = static_cast<float>(static_cast<double>(l.beta) * u - static_cast<double>(l.margin));
-    if (l.objective == LOSSK_PREF_HINGE) {
-        loss = h >= 1.f ? 0.f : 1.f - h;
-        slope = h >= 1.f ? 0.f : -l.beta;
-    } else {
-        loss = (1.f - l.smooth) * softplus(-h);
-        if (l.smooth > 0.f) loss += l.smooth * softplus(h);
-        slope = l.beta * (l.smooth / (1.f + expf(-h)) - (1.f - l.smooth) / (1.f + expf(h)));
-    }
-}
-
 __device__ __forceinline__ double log_ratio(const SeqLoss &l, const SeqScratch &w, int s, int &count)
 {
     count = w.seq_slot[s + 1] - w.seq_slot[s];
@@ -443,10 +372,9 @@ __device__ __forceinline__ double log_ratio(const SeqLoss &l, const SeqScratch &
 __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
-    if (refused(w.hdr)) return;
+    if (seq_refused(w.hdr)) return;
     const int t = blockIdx.x * COEF_T + threadIdx.x;
     const bool pref = l.pairs > 0;
-    const bool sum = l.flags & LOSSK_REDUCE_SUM;
     float coef = 0.f;
     double v[3] = {0.0, 0.0, 0.0};
     if (pref && t < l.n_seq && l.log_ratio) {
@@ -472,52 +400,27 @@ __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const
         } else {
             const float lp = w.lp[c];
             const int n_s = l.n_seq > 0 ? w.seq_slot[s + 1] - w.seq_slot[s] : 0;
-            double d_lp;                                   // d total / d logp
+            RowTerms r;
             if (pref) {
                 const bool chosen = s < l.pairs;
                 const int i = chosen ? s : s - l.pairs;
                 int nc, nr;
                 const double u = log_ratio(l, w, i, nc) - log_ratio(l, w, l.pairs + i, nr);
-                d_lp = 0.0;
-                if (nc > 0 && nr > 0) {
-                    float loss, slope;
-                    pair_term(l, u, loss, slope);
-                    double g = chosen ? slope : -slope;
-                    if (l.flags & LOSSK_LENGTH_MEAN) g /= n_s;
-                    d_lp = sum ? g : g / w.hdr->pad[HDR_GROUPS];
-                }
-                if (chosen && l.nll > 0.f) d_lp -= static_cast<double>(l.nll) / (sum ? 1 : w.hdr->pad[HDR_CHOSEN]);
-                v[0] = chosen ? -static_cast<double>(lp) : 0.0;
+                float loss, slope = 0.f;
+                if (nc > 0 && nr > 0) pair_term(l, u, loss, slope);
+                r = pair_row(l, w.hdr, chosen, n_s, slope, lp);
+                v[0] = r.v[0];
             } else {
-                const double weight = row_weight(l, w.hdr, n_s);
-                PolicyTerm p;
-                const float A = advantage(l, t, s);
-                if (l.flags & LOSSK_SEQ_RATIO) {
-                    p = policy_term<double>(l, w.sum[s] / n_s, A);
-                    d_lp = w.slope[s] / n_s;
-                } else {
-                    p = policy_term<float>(l, l.old ? lp - l.old[t] : 0.f, A);
-                    d_lp = weight * static_cast<double>(p.slope);
-                }
-                float kl = 0.f, loss = p.loss;
-                if (l.ref) {
-                    const float q = l.ref[t] - lp, e = expm1f(q);
-                    kl = e - q;
-                    if (l.kl > 0.f) {
-                        loss = fmaf(l.kl, kl, loss);
-                        d_lp -= static_cast<double>(l.kl) * weight * static_cast<double>(e);
-                    }
-                }
-                if (l.per_token) l.per_token[t] = loss;
-                v[0] = weight * static_cast<double>(p.loss);
-                v[1] = weight * static_cast<double>(kl);
-                v[2] = p.clipped ? weight : 0.0;
+                const bool by_seq = l.flags & LOSSK_SEQ_RATIO;
+                r = policy_row(l, policy_inputs(l, w.hdr, t, s, n_s), t, lp, by_seq ? w.sum[s] / n_s : 0.0,
+                               by_seq ? static_cast<float>(w.slope[s] / n_s) : 0.f);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) v[k] = r.v[k];
             }
             if (l.logp) l.logp[t] = lp;
-            const float lse2 = w.lse2[c];
-            const bool none = lse2 == -INFINITY;           // a row without any probability
-            coef = none ? 0.f : static_cast<float>(d_lp * static_cast<double>(l.per_t));
-            w.tokp[c] = make_float4(none ? 0.f : lse2, coef, coef, __int_as_float(static_cast<int>(w.y[c])));
+            const float4 P = row_params(w.lse2[c], r.coef, w.y[c]);
+            w.tokp[c] = P;
+            coef = P.y;
         }
     }
     // the largest |coefficient| (fp16's passes scale by it): positive floats order as integers
@@ -549,7 +452,7 @@ cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t 
 __global__ void __launch_bounds__(256) seq_scalars_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
-    if (refused(w.hdr)) return;
+    if (seq_refused(w.hdr)) return;
     seq_scalars<256>(l, w);
 }
 
@@ -588,7 +491,7 @@ __global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqS
                                                      int scalars)
 {
     wait_for_stream();
-    if (refused(w.hdr)) return;
+    if (seq_refused(w.hdr)) return;
     if (only_if && !*reinterpret_cast<const volatile int *>(only_if)) return;
     if (scalars && blockIdx.x == 0) seq_scalars<256>(l, w);
     const int64_t dn = d / N, count = l.n_tok * dn, plane = l.n_tok * d;

@@ -1399,8 +1399,8 @@ const char *lossk_kernel_name(int32_t kind)
                                       "wait_selftest", "shard_tgt",    "shard_combine", "beam_rows",    "beam_merge",
                                       "beam_gather",  "cache_fork",    "cache_plan",    "cache_copy",   "cache_free",
                                       "cache_rank",   "cache_write",   "attn_plan",     "attn",         "attn_join",
-                                      "seq_prep",      "seq_gather",    "seq_stats",    "seq_merge",    "seq_sum",
-                                      "seq_coef",      "seq_grad",      "seq_dh"};
+                                      "seq_prep",      "seq_gather",    "seq_merge",    "seq_sum",      "seq_coef",
+                                      "seq_stats",     "seq_grad",      "policy_rows",  "seq_dh"};
     return (kind >= 0 && kind < KK_N) ? names[kind] : "unknown_kernel";
 }
 

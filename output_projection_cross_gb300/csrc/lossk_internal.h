@@ -90,6 +90,7 @@ struct TcArgs {
     const int *n_dev;      // or NULL: the tokens there are, found by an earlier kernel (at most n_tok)
     const int *refused;    // or NULL; nonzero: the validation before found a bad target; return at once
     const int *only_if;    // or NULL; zero: the pass is not needed, return at once
+    int chained;           // the pass may be set up while the kernel ahead of it ends
     const int64_t *targets;
     const uint16_t *teacher; // distillation forward: teacher logits [n_tok][vocab] (bf16)
     const double2 *tstat;  // distillation forward: per token (lse_t2, Eb) from teacher_stats
@@ -159,6 +160,7 @@ struct BwdArgs {
     const int *n_dev;      // or NULL: the tokens there are, found by an earlier kernel (at most n_tok)
     const int *refused;    // nonzero: the validation before found a bad target; return at once
     const int *only_if;    // or NULL; zero: the pass is not needed, return at once
+    int chained;           // gsig is zero already, and the pass may be set up while the kernel ahead of it ends
     unsigned *gsig;        // grad-tile ring hand-off counters [2][G_MAX_CTAS][G_SLOTS] (ready, free)
     int *err;
 };
@@ -212,11 +214,12 @@ enum KernelKind : int {
     KK_ATTN_JOIN,
     KK_SEQ_PREP,
     KK_SEQ_GATHER,
-    KK_SEQ_STATS,
     KK_SEQ_MERGE,
     KK_SEQ_SUM,
     KK_SEQ_COEF,
+    KK_SEQ_STATS,
     KK_SEQ_GRAD,
+    KK_POLICY_ROWS,
     KK_SEQ_DH,
     KK_N
 };

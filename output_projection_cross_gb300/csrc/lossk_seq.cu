@@ -19,11 +19,14 @@ constexpr int64_t MAX_DIM = int64_t(1) << 24;
 bool is16(int32_t dtype) { return dtype == LOSSK_BF16 || dtype == LOSSK_F16; }
 bool dtype_ok(int32_t dtype) { return dtype == LOSSK_F32 || is16(dtype); }
 
+// hand-off counters of a group pass
+constexpr int GSIG_WORDS = 2 * G_MAX_CTAS * G_SLOTS;
+
 struct Layout {
     int64_t n_pad, n_ct, nsplit;
-    int splits;
+    int splits, cluster;
     size_t off_slot, off_row, off_y, off_seq, off_tgt, off_lp, off_lse2, off_z, off_tokp, off_sum, off_slope, off_acc,
-        off_tick, off_rows, off_hidden, off_part, off_dhpart, off_zpart, off_gring, off_gsig, off_dhacc, total;
+        off_terms, off_tick, off_rows, off_hidden, off_part, off_dhpart, off_zpart, off_gring, off_gsig, off_dhacc, total;
 };
 
 // 580, or why there is no layout.
@@ -77,11 +80,13 @@ int32_t layout(int32_t kind, int64_t n, int64_t d, int64_t V, int64_t n_seq, int
         }
         if (tc) {
             L->off_gring = take(sizeof(uint16_t) * 128 * static_cast<size_t>(G_RING_ROWS));
-            L->off_gsig = take(sizeof(unsigned) * 2 * G_MAX_CTAS * G_SLOTS);
+            L->off_gsig = take(sizeof(unsigned) * 3 * GSIG_WORDS);      // one set for each pass of a call
         }
     } else {
         L->splits = seq_stat_splits(n, V, dtype);
+        L->cluster = policy_rows_cluster(n, V, dtype);
         L->off_rows = take(sizeof(float2) * np * static_cast<size_t>(L->splits));
+        L->off_terms = take(sizeof(float4) * np);
     }
     L->total = off;
     return LOSSK_OK;
@@ -106,7 +111,10 @@ SeqScratch scratch(const Layout &L, void *ws)
     w.slope = reinterpret_cast<double *>(b + L.off_slope);
     w.acc = reinterpret_cast<double *>(b + L.off_acc);
     w.tick = reinterpret_cast<int *>(b + L.off_tick);
+    w.terms = reinterpret_cast<float4 *>(b + L.off_terms);
     w.part = reinterpret_cast<float2 *>(b + L.off_rows);
+    w.words = reinterpret_cast<unsigned *>(b + L.off_gsig);
+    w.n_words = L.off_gsig ? 3 * GSIG_WORDS : 0;
     w.n_pad = L.n_pad;
     return w;
 }
@@ -215,6 +223,7 @@ int32_t run_forward(const Call &c, const Layout &L, const SeqLoss &l, const SeqS
     a.n_dev = &w.hdr->n_valid;
     a.refused = &w.hdr->bad_targets;
     a.only_if = only_if;
+    a.chained = 1;
     a.targets = w.y;
     a.tgt_out = w.tgt;
     a.part = part;
@@ -280,8 +289,10 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     const BwdScratch bs{reinterpret_cast<uint16_t *>(b + L.off_gring), reinterpret_cast<unsigned *>(b + L.off_gsig),
                         w.tokp, w.hdr};
     // The passes' maps span the gathered rows up to a multiple of 256 (zeros past the last).
-    auto rows_args = [&](BwdArgs *a) {
+    auto rows_args = [&](BwdArgs *a, int pass) {
         if (!bwd_args(bs, true, L.n_pad, c.d, c.V, hid, c.W, a)) return false;
+        a->gsig = w.words + pass * GSIG_WORDS;
+        a->chained = 1;
         a->n_tok = n;
         a->n_split = static_cast<int>(L.nsplit);
         a->inv_t_l2e = l.k2;
@@ -300,7 +311,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
         // forward and d_hidden in one pass; a row that left the range of its
         // reference asks for the separate forward
         float *zpart = reinterpret_cast<float *>(b + L.off_zpart);
-        if (!rows_args(&a)) return LOSSK_DEVICE_ERROR;
+        if (!rows_args(&a, 0)) return LOSSK_DEVICE_ERROR;
         a.zpart = zpart;
         a.zpart_stride = L.n_pad;
         a.tgt_out = w.tgt;
@@ -339,6 +350,8 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
             s = LOSSK_DEVICE_ERROR;
         } else {
             q.n_tok = n;
+            q.gsig = w.words + GSIG_WORDS;
+            q.chained = 1;
             q.inv_t_l2e = l.k2;
             q.n_dev = n_dev;
             q.out = static_cast<float *>(c.g1);
@@ -361,7 +374,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     // d_hidden as a pass of its own: fp16, whose tiles need the log-sum-exp, and
     // bf16 where the fused pass's could not be used
     const int *only_if = fused ? redo : nullptr;
-    if (!rows_args(&a)) return LOSSK_DEVICE_ERROR;
+    if (!rows_args(&a, 2)) return LOSSK_DEVICE_ERROR;
     a.only_if = only_if;
     {
         Launch k(KK_TC_ROWS, st);
@@ -377,10 +390,15 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
 
 int32_t run_rows(const Call &c, const Layout &L, const SeqLoss &l, const SeqScratch &w)
 {
+    const bool acc = (c.flags & LOSSK_ACCUMULATE_GRADS) != 0;
+    if (l.pairs == 0 && !(l.flags & LOSSK_SEQ_RATIO) && L.cluster > 0) {
+        TRY(launch_policy_rows(c.dtype, l, w, c.X, c.g0, acc, L.cluster, c.st));
+        return LOSSK_OK;
+    }
     TRY(launch_seq_stats(c.dtype, l, w, c.X, L.splits, c.st));
     const int32_t s = run_losses(c, l, w);
     if (s != LOSSK_OK) return s;
-    if (c.g0) TRY(launch_seq_grad(c.dtype, l, w, c.X, c.g0, (c.flags & LOSSK_ACCUMULATE_GRADS) != 0, c.st));
+    if (c.g0) TRY(launch_seq_grad(c.dtype, l, w, c.X, c.g0, acc, c.st));
     else TRY(launch_seq_scalars(l, w, c.st));
     return LOSSK_OK;
 }

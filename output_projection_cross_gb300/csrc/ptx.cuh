@@ -477,6 +477,22 @@ __device__ __forceinline__ void tc_commit_multicast(uint64_t *bar, uint16_t mask
         : "memory");
 }
 
+// Untiled bulk copy global -> this CTA's shared memory, completion counted in bytes on `bar`: both
+// addresses and the size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_copy_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Eight bytes into the shared memory of a CTA of this cluster.
+__device__ __forceinline__ void st_cluster_f2(uint32_t cluster_addr, float2 v)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr), "f"(v.x), "f"(v.y) : "memory");
+}
+
 // Full cluster barrier (every thread of every CTA of the cluster).
 __device__ __forceinline__ void cluster_sync()
 {

@@ -23,8 +23,11 @@ struct SeqScratch {
     double *sum;        // [n_seq] sum over the sequence of logp minus its base
     double *slope;      // [n_seq] LOSSK_SEQ_RATIO: sum over the sequence of w dP/d(log ratio)
     double *acc;        // [3][blocks] the coefficient kernel's blocks' terms of the scalars
+    float4 *terms;      // forms from logits, policy loss by token: [n_tok] each row's terms of the scalars
     int *tick;          // [n_pad] forms from logits: pieces of the row that are done
-    float2 *part;       // forms from logits: [n_pad][splits] (max, sum) of the row's pieces
+    unsigned *words;    // [n_words] forms from hidden rows: zeroed by seq_prep, the group passes' hand-off counters
+    int n_words;
+    float2 *part;       // forms from logits: [n_pad][seq_stat_splits] (max, sum) of the row's pieces
     int64_t n_pad;
 };
 
@@ -75,10 +78,6 @@ cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const 
 // NULL; zero: not needed.
 cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,
                                    const int *only_if, cudaStream_t st);
-// Given logits: logp, lse2, a row in `splits` pieces.
-int seq_stat_splits(int64_t n, int64_t vocab, int dtype);
-cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
-                             cudaStream_t st);
 // Per sequence the sum of log ratios (and the slope of LOSSK_SEQ_RATIO).
 cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
 // Per row its loss, outputs and coefficient; per pair its loss.  The scalars: by a kernel of their
@@ -86,9 +85,17 @@ cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t s
 constexpr int COEF_T = 128;
 cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
 cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
-// grad_logits of every row, and the scalars.
+// Given logits: logp, lse2, a row in `splits` pieces; grad_logits of every row, and the scalars.
+int seq_stat_splits(int64_t n, int64_t vocab, int dtype);
+cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
+                             cudaStream_t st);
 cudaError_t launch_seq_grad(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,
                             bool accumulate, cudaStream_t st);
+// The policy loss by token in one launch, a row's logits on the chip from its statistics to
+// its gradient (grad NULL: none); blocks of a cluster that take a row, 0 where a row does not fit.
+int policy_rows_cluster(int64_t n, int64_t vocab, int dtype);
+cudaError_t launch_policy_rows(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,
+                               bool accumulate, int cluster, cudaStream_t st);
 // d_hidden of every row from the passes' split partials [nsplit][n_tok][d], indexed by
 // slot: fused, a_t / Z_t times their sum minus a_t W[y_t] (a value that is not
 // finite asks for the separate passes, redo), else their sum.  out: out_dtype.

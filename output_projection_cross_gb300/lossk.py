@@ -129,7 +129,7 @@ EXPORTED = ("lossk_status_name", "lossk_dims_check", "lossk_chunk_check", "lossk
             "lossk_cache_compact", "lossk_cache_copy", "lossk_cache_write", "lossk_paged_attn",
             "lossk_sequence_workspace_bytes", "lossk_policy_fwd_bwd", "lossk_policy_from_logits",
             "lossk_preference_fwd_bwd", "lossk_preference_from_logits", "lossk_kernel_name", "lossk_launch_count", "lossk_profile_enable", "lossk_profile_read")
-N_KERNELS = 43
+N_KERNELS = 44
 
 
 class LosskError(RuntimeError):
