@@ -882,8 +882,10 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             uint16_t *gdst = a.gscr + static_cast<int64_t>(((blockIdx.x * G_SLOTS + g) * 2) * 128 + r) * 128;
             const int grow0 = ((blockIdx.x * G_SLOTS + g) * 2) * 128 + quad * 32;   // this warp's first ring row
             float zt = 0.f;
+            // RUNS: no chunk that no accumulate reads (53 tokens: two of eight)
+            const int n_chunk = RUNS ? 2 * stages_of(loop0) : BWD_BN / 32;
 #pragma unroll 1
-            for (int q = 0; q < BWD_BN / 32; ++q) {
+            for (int q = 0; q < n_chunk; ++q) {
                 uint32_t v[32];
                 tmem_ld32(trow + q * 32, v);
                 uint32_t tcur[16];

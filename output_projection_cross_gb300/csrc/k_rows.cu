@@ -33,6 +33,10 @@ constexpr int GRAD_T = 128, GRAD_U = 4;
 // SM, 249; blocks of 768 247 and of 1024 262.
 constexpr int POLICY_T = 512, POLICY_BLOCKS = 2;
 constexpr int POLICY_CHUNKS = 4;               // copies that a block's share of a row arrives in
+// Rows of up to so many bytes are a warp's each, four or eight to a block (3967 rows of 1086 in bf16, two
+// pairs: 47 -> SMALL_US us; a block of 256 threads has half a vector for each of its threads there).
+constexpr int64_t SMALL_ROW = 8192;
+constexpr int SMALL_U = 4;
 
 template <typename T> constexpr int NVEC = 16 / sizeof(T);
 
@@ -184,6 +188,44 @@ __device__ __forceinline__ void row_logp(const SeqLoss &l, float M, float z, flo
              : static_cast<float>((static_cast<double>(y) * static_cast<double>(l.k2) - s) * LN2 - exps * EX2_LOW);
 }
 
+// A warp's (max, sum) from its lanes', as block_stats; valid in every lane.
+__device__ __forceinline__ void warp_stats(float &m, float &z)
+{
+    float M = m;
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M > -INFINITY) z *= ex2_approx(m - M);
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    m = M;
+}
+
+// Thread tid of a team's (max, sum) over vectors [v0, v1) of a row, U loads in flight.
+template <typename T, int TEAM, int U>
+__device__ __forceinline__ void scan_row(const RowVecs<T> &r, int v0, int v1, int tid, float k2, float &m, float &z)
+{
+    constexpr int N = NVEC<T>;
+    for (int j0 = v0; j0 < v1; j0 += TEAM * U) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * TEAM + tid, e = r.at(j);
+            if (j < v1 && r.whole(e)) v[u] = __ldg(reinterpret_cast<const uint4 *>(r.row + e));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * TEAM + tid, e = r.at(j);
+            if (j >= v1) continue;
+            float f[N];
+            if (r.whole(e)) {
+                unpack<T>(v[u], f);
+                add_vec<N>(m, z, f, vec_max<T>(v[u]), k2);
+            } else {
+                r.load_part(e, f);
+                add_part<N>(m, z, f, k2);
+            }
+        }
+    }
+}
+
 // A vector of the gradient from its logits f: a (softmax - onehot), the row's parameters P.
 template <int N> __device__ __forceinline__ void grad_vec(float (&f)[N], const float4 &P, float k2, int e)
 {
@@ -210,43 +252,73 @@ template <typename T, bool ADD> __device__ __forceinline__ void put_part(const R
         if (e + i >= 0 && e + i < r.vocab) put(g + e + i, ADD ? f[i] + value(g[e + i]) : f[i]);
 }
 
+// Vectors [v0, v1) of a row's gradient by thread tid of a team.
+template <typename T, bool ADD, int TEAM, int U>
+__device__ __forceinline__ void write_row(const RowVecs<T> &r, T *g, int v0, int v1, int tid, const float4 &P, float k2)
+{
+    constexpr int N = NVEC<T>;
+    for (int j0 = v0; j0 < v1; j0 += TEAM * U) {
+        uint4 v[U], old[ADD ? U : 1];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * TEAM + tid, e = r.at(j);
+            if (j < v1 && P.y != 0.f && r.whole(e)) {
+                v[u] = __ldcs(reinterpret_cast<const uint4 *>(r.row + e));
+                if (ADD) old[ADD ? u : 0] = __ldcs(reinterpret_cast<const uint4 *>(g + e));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * TEAM + tid, e = r.at(j);
+            if (j >= v1) continue;
+            float f[N] = {};
+            const bool whole = r.whole(e);
+            if (P.y != 0.f) {
+                if (whole) unpack<T>(v[u], f);
+                else r.load_part(e, f);
+                grad_vec<N>(f, P, k2, e);
+            }
+            if (!whole) {
+                put_part<T, ADD>(r, g, e, f);
+                continue;
+            }
+            if (ADD) {
+                float o[N];
+                unpack<T>(old[ADD ? u : 0], o);
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] += o[i];
+            }
+            __stcs(reinterpret_cast<uint4 *>(g + e), pack<T>(f));
+        }
+    }}
+
 } // namespace
 
 // logp and lse2 of a counted row, which comes in pieces of one block each; the last piece to
-// arrive joins them all, in their order.
-template <typename T>
+// arrive joins them all, in their order.  SMALL: a warp per row.
+template <typename T, bool SMALL>
 __global__ void __launch_bounds__(ROW_T) row_stats_kernel(const SeqLoss l, const SeqScratch w,
                                                           const T *__restrict__ logits, int splits)
 {
-    constexpr int N = NVEC<T>;
     wait_for_stream();
     if (seq_refused(w.hdr)) return;
+    if constexpr (SMALL) {
+        const int c = blockIdx.x * (ROW_T / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+        if (c >= w.hdr->n_valid) return;
+        const RowVecs<T> r(logits + w.row[c] * l.vocab, l.vocab);
+        const float y = lane == 0 ? value(r.row[w.y[c]]) : 0.f;
+        float m = -INFINITY, z = 0.f;
+        scan_row<T, 32, SMALL_U>(r, 0, r.n, lane, l.k2, m, z);
+        warp_stats(m, z);
+        if (lane == 0) row_logp(l, m, z, y, 2, w.lp[c], w.lse2[c]);
+        return;
+    }
     const int c = blockIdx.x / splits, piece = blockIdx.x - c * splits;
     if (c >= w.hdr->n_valid) return;
     const RowVecs<T> r(logits + w.row[c] * l.vocab, l.vocab);
     const int v0 = r.piece(piece, splits), v1 = r.piece(piece + 1, splits);
     float m = -INFINITY, z = 0.f;
-    for (int j0 = v0; j0 < v1; j0 += ROW_T * ROW_U) {
-        uint4 v[ROW_U];
-#pragma unroll
-        for (int u = 0; u < ROW_U; ++u) {
-            const int j = j0 + u * ROW_T + threadIdx.x, e = r.at(j);
-            if (j < v1 && r.whole(e)) v[u] = __ldg(reinterpret_cast<const uint4 *>(r.row + e));
-        }
-#pragma unroll
-        for (int u = 0; u < ROW_U; ++u) {
-            const int j = j0 + u * ROW_T + threadIdx.x, e = r.at(j);
-            if (j >= v1) continue;
-            float f[N];
-            if (r.whole(e)) {
-                unpack<T>(v[u], f);
-                add_vec<N>(m, z, f, vec_max<T>(v[u]), l.k2);
-            } else {
-                r.load_part(e, f);
-                add_part<N>(m, z, f, l.k2);
-            }
-        }
-    }
+    scan_row<T, ROW_T, ROW_U>(r, v0, v1, threadIdx.x, l.k2, m, z);
     __shared__ float sm[ROW_T / 32], sz[ROW_T / 32];
     block_stats<ROW_T>(m, z, sm, sz);
     if (threadIdx.x != 0) return;
@@ -278,29 +350,43 @@ int seq_stat_splits(int64_t n, int64_t vocab, int dtype)
     return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
+template <typename T>
+static cudaError_t stats_one(const SeqLoss &l, const SeqScratch &w, const void *logits, int splits, cudaStream_t st)
+{
+    const bool small = l.vocab * static_cast<int64_t>(sizeof(T)) <= SMALL_ROW;
+    const int64_t grid = small ? (l.n_tok + ROW_T / 32 - 1) / (ROW_T / 32) : static_cast<int64_t>(l.n_tok) * splits;
+    return launch(small ? row_stats_kernel<T, true> : row_stats_kernel<T, false>, dim3(static_cast<unsigned>(grid)),
+                  dim3(ROW_T), 0, st, l, w, static_cast<const T *>(logits), splits);
+}
+
 cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
                              cudaStream_t st)
 {
     Launch k(KK_SEQ_STATS, st);
-    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(l.n_tok) * splits));
-    if (dtype == LOSSK_F32)
-        return launch(row_stats_kernel<float>, grid, dim3(ROW_T), 0, st, l, w, static_cast<const float *>(logits), splits);
-    if (dtype == LOSSK_F16)
-        return launch(row_stats_kernel<h16_t>, grid, dim3(ROW_T), 0, st, l, w, static_cast<const h16_t *>(logits), splits);
-    return launch(row_stats_kernel<uint16_t>, grid, dim3(ROW_T), 0, st, l, w, static_cast<const uint16_t *>(logits),
-                  splits);
+    if (dtype == LOSSK_F32) return stats_one<float>(l, w, logits, splits, st);
+    if (dtype == LOSSK_F16) return stats_one<h16_t>(l, w, logits, splits, st);
+    return stats_one<uint16_t>(l, w, logits, splits, st);
 }
 
 // grad_logits of a piece of a row.  A coefficient of 0 (a row that does not
 // count, a clipped token) writes zeros and reads nothing.
-template <typename T, bool ADD>
+template <typename T, bool ADD, bool SMALL>
 __global__ void __launch_bounds__(GRAD_T) row_grad_kernel(const SeqLoss l, const SeqScratch w,
                                                          const T *logits, T *grad, int splits)
 {
-    constexpr int N = NVEC<T>;
     wait_for_stream();
     if (seq_refused(w.hdr)) return;
     if (blockIdx.x == 0) seq_scalars<GRAD_T>(l, w);
+    if constexpr (SMALL) {
+        const int t = blockIdx.x * (GRAD_T / 32) + (threadIdx.x >> 5);
+        if (t >= l.n_tok) return;
+        const int c = w.slot[t];
+        const float4 P = c >= 0 ? w.tokp[c] : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
+        if (ADD && P.y == 0.f) return;
+        const RowVecs<T> r(logits + t * l.vocab, l.vocab);
+        write_row<T, ADD, 32, SMALL_U>(r, grad + t * l.vocab, 0, r.n, threadIdx.x & 31, P, l.k2);
+        return;
+    }
     // the last rows first: the statistics pass has just read them, and the L2 holds them still
     const unsigned at = gridDim.x - 1 - blockIdx.x;
     const int64_t t = at / splits;
@@ -311,40 +397,7 @@ __global__ void __launch_bounds__(GRAD_T) row_grad_kernel(const SeqLoss l, const
     const RowVecs<T> r(logits + t * l.vocab, l.vocab);
     T *g = grad + t * l.vocab;
     const int v0 = r.piece(piece, splits), v1 = r.piece(piece + 1, splits);
-    for (int j0 = v0; j0 < v1; j0 += GRAD_T * GRAD_U) {
-        uint4 v[GRAD_U], old[ADD ? GRAD_U : 1];
-#pragma unroll
-        for (int u = 0; u < GRAD_U; ++u) {
-            const int j = j0 + u * GRAD_T + threadIdx.x, e = r.at(j);
-            if (j < v1 && P.y != 0.f && r.whole(e)) {
-                v[u] = __ldcs(reinterpret_cast<const uint4 *>(r.row + e));
-                if (ADD) old[ADD ? u : 0] = __ldcs(reinterpret_cast<const uint4 *>(g + e));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < GRAD_U; ++u) {
-            const int j = j0 + u * GRAD_T + threadIdx.x, e = r.at(j);
-            if (j >= v1) continue;
-            float f[N] = {};
-            const bool whole = r.whole(e);
-            if (P.y != 0.f) {
-                if (whole) unpack<T>(v[u], f);
-                else r.load_part(e, f);
-                grad_vec<N>(f, P, l.k2, e);
-            }
-            if (!whole) {
-                put_part<T, ADD>(r, g, e, f);
-                continue;
-            }
-            if (ADD) {
-                float o[N];
-                unpack<T>(old[ADD ? u : 0], o);
-#pragma unroll
-                for (int i = 0; i < N; ++i) f[i] += o[i];
-            }
-            __stcs(reinterpret_cast<uint4 *>(g + e), pack<T>(f));
-        }
-    }
+    write_row<T, ADD, GRAD_T, GRAD_U>(r, g, v0, v1, threadIdx.x, P, l.k2);
 }
 
 template <typename T>
@@ -354,9 +407,12 @@ static cudaError_t grad_one(const SeqLoss &l, const SeqScratch &w, const void *l
     // pieces of 16 KB: two rounds of loads
     int64_t s = l.vocab * static_cast<int64_t>(sizeof(T)) / (2 * GRAD_T * GRAD_U * 16);
     const int splits = static_cast<int>(s < 1 ? 1 : (s > 1024 ? 1024 : s));
-    const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(l.n_tok) * splits));
-    return launch(add ? row_grad_kernel<T, true> : row_grad_kernel<T, false>, grid, dim3(GRAD_T), 0, st, l, w,
-                  static_cast<const T *>(logits), static_cast<T *>(grad), splits);
+    const bool small = l.vocab * static_cast<int64_t>(sizeof(T)) <= SMALL_ROW;
+    const int64_t grid = small ? (l.n_tok + GRAD_T / 32 - 1) / (GRAD_T / 32) : static_cast<int64_t>(l.n_tok) * splits;
+    auto kern = small ? (add ? row_grad_kernel<T, true, true> : row_grad_kernel<T, false, true>)
+                      : (add ? row_grad_kernel<T, true, false> : row_grad_kernel<T, false, false>);
+    return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(GRAD_T), 0, st, l, w, static_cast<const T *>(logits),
+                  static_cast<T *>(grad), splits);
 }
 
 cudaError_t launch_seq_grad(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,
@@ -384,6 +440,70 @@ int policy_rows_cluster(int64_t n, int64_t vocab, int dtype)
     // few rows: more blocks for each, down to 8 KB
     while (c < 8 && n * c < 304 && bytes > 2 * c * 8192) c *= 2;
     return bytes > c * POLICY_MOST ? 0 : c;
+}
+
+namespace {
+
+// What the policy loss reads for the row t of slot c.
+__device__ __forceinline__ RowInputs slot_inputs(const SeqLoss &l, const SeqScratch &w, int t, int c)
+{
+    int s = 0, n_s = 0;
+    if (l.n_seq > 0 && (l.flags & (LOSSK_SEQ_MEAN | LOSSK_SEQ_ADVANTAGES))) {
+        int hi = l.n_seq;                      // the last sequence that starts at or before slot c
+        while (hi - s > 1) {
+            const int mid = (s + hi) >> 1;
+            if (w.seq_slot[mid] <= c) s = mid;
+            else hi = mid;
+        }
+        n_s = w.seq_slot[s + 1] - w.seq_slot[s];
+    }
+    return policy_inputs(l, w.hdr, t, s, n_s);
+}
+
+} // namespace
+
+// Small rows, a warp each: the second read finds them in the L1 or L2.  GRAD: 0 none, 1
+// written, 2 added to what is there.
+template <typename T, int GRAD>
+__global__ void __launch_bounds__(GRAD_T) policy_small_kernel(const SeqLoss l, const SeqScratch w, const T *logits, T *grad)
+{
+    wait_for_stream();
+    const int t = blockIdx.x * (GRAD_T / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int c = t < l.n_tok ? w.slot[t] : -1;
+    if (t >= l.n_tok || seq_refused(w.hdr)) return;
+    const RowVecs<T> r(logits + t * l.vocab, l.vocab);
+    float4 P = make_float4(0.f, 0.f, 0.f, __int_as_float(-1)), terms = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c >= 0) {
+        RowInputs in{};
+        int64_t target = 0;
+        float y = 0.f;
+        if (lane == 0) {
+            target = w.y[c];
+            y = value(r.row[target]);
+            in = slot_inputs(l, w, t, c);
+        }
+        float m = -INFINITY, z = 0.f;
+        scan_row<T, 32, SMALL_U>(r, 0, r.n, lane, l.k2, m, z);
+        warp_stats(m, z);
+        if (lane == 0) {
+            float lp, lse2;
+            row_logp(l, m, z, y, 2, lp, lse2);
+            const RowTerms x = policy_row(l, in, t, lp, 0.0, 0.f);
+            if (l.logp) l.logp[t] = lp;
+            P = row_params(lse2, x.coef, target);
+            terms = make_float4(x.v[0], x.v[1], x.v[2], 0.f);
+        }
+        P.x = __shfl_sync(0xffffffffu, P.x, 0);
+        P.y = __shfl_sync(0xffffffffu, P.y, 0);
+        P.z = __shfl_sync(0xffffffffu, P.z, 0);
+        P.w = __shfl_sync(0xffffffffu, P.w, 0);
+    } else if (lane == 0) {
+        if (l.logp) l.logp[t] = 0.f;
+        if (l.per_token) l.per_token[t] = 0.f;
+    }
+    if (lane == 0) w.terms[t] = terms;
+    if (GRAD == 1 || (GRAD == 2 && P.y != 0.f))
+        write_row<T, GRAD == 2, 32, SMALL_U>(r, grad + t * l.vocab, 0, r.n, lane, P, l.k2);
 }
 
 // GRAD: 0 none, 1 written, 2 added to what is there.
@@ -428,19 +548,9 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
         int64_t target = 0;
         RowInputs in{};
         if (tid == 0) {
-            int s = 0, n_s = 0;
-            if (l.n_seq > 0 && (l.flags & (LOSSK_SEQ_MEAN | LOSSK_SEQ_ADVANTAGES))) {
-                int hi = l.n_seq;              // the last sequence that starts at or before slot c
-                while (hi - s > 1) {
-                    const int mid = (s + hi) >> 1;
-                    if (w.seq_slot[mid] <= c) s = mid;
-                    else hi = mid;
-                }
-                n_s = w.seq_slot[s + 1] - w.seq_slot[s];
-            }
             target = w.y[c];
             y = value(r.row[target]);
-            in = policy_inputs(l, w.hdr, t, s, n_s);
+            in = slot_inputs(l, w, t, c);
         }
         float m = -INFINITY, z = 0.f;
         // the first and the last vector where they are partly outside the row
@@ -560,6 +670,9 @@ template <typename T, int GRAD>
 static cudaError_t policy_one(const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad, int cluster,
                               cudaStream_t st)
 {
+    if (l.vocab * static_cast<int64_t>(sizeof(T)) <= SMALL_ROW)
+        return launch(policy_small_kernel<T, GRAD>, dim3(static_cast<unsigned>((l.n_tok + GRAD_T / 32 - 1) / (GRAD_T / 32))),
+                      dim3(GRAD_T), 0, st, l, w, static_cast<const T *>(logits), static_cast<T *>(grad));
     constexpr auto K = policy_rows_kernel<T, GRAD>;
     // a share of the row's vectors, rounded up, and the one that a row may begin in
     const size_t smem = static_cast<size_t>((l.vocab / NVEC<T> + 2) / cluster + 2) * 16;
