@@ -706,7 +706,7 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
  *   hidden, weight, logits, dtype   as above; contiguous
  *   d_hidden, d_weight  grad_dtype: LOSSK_F32, or the inputs' 16-bit type (each
  *               element is then rounded once, from its fp32 sum).  NULL to skip.
- *   grad_logits dtype, or NULL to skip.
+ *   grad_logits dtype, or NULL to skip; it may be logits itself.
  * Every row of a gradient is written: rows that do not count, and those behind
  * the last sequence, become 0.  A token on whose logp the loss does not depend
  * (a clipped one without a KL term) has a zero gradient whatever its logits hold.  A
@@ -762,7 +762,7 @@ int64_t lossk_sequence_workspace_bytes(int32_t kind, int64_t n_tok, int64_t d_mo
  *   scalars_out    float[4], required: {total, sum w P, sum w K, sum w [clipped]}
  *   per_token_out  float[n_tok] or NULL: L_t, 0 where a row does not count
  * clip_low in [0, 1], clip_high >= 0, kl_weight >= 0 (> 0 needs ref_logp: 582),
- * temperature > 0, all finite (585). */
+ * temperature in [1e-30, 1e30], all finite (585). */
 int32_t lossk_policy_fwd_bwd(int64_t n_tok, int64_t d_model, int64_t vocab, int64_t n_seq, int32_t dtype,
                              const void *hidden, int64_t hidden_len, const void *weight, int64_t weight_len,
                              const int64_t *targets, int64_t targets_len, const uint8_t *loss_mask,

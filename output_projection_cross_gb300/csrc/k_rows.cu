@@ -34,7 +34,7 @@ constexpr int GRAD_T = 128, GRAD_U = 4;
 constexpr int POLICY_T = 512, POLICY_BLOCKS = 2;
 constexpr int POLICY_CHUNKS = 4;               // copies that a block's share of a row arrives in
 // Rows of up to so many bytes are a warp's each, four or eight to a block (3967 rows of 1086 in bf16, two
-// pairs: 47 -> SMALL_US us; a block of 256 threads has half a vector for each of its threads there).
+// pairs: 47 -> 33 us; a block of 256 threads has half a vector for each of its threads there).
 constexpr int64_t SMALL_ROW = 8192;
 constexpr int SMALL_U = 4;
 

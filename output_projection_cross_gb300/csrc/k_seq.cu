@@ -482,23 +482,26 @@ __device__ __forceinline__ void put4(h16_t *p, const float (&v)[4])
 
 } // namespace
 
-// Four elements per thread where d_model is a multiple of 4, else one.  The
-// splits are added in their order.
-template <typename O, int N>
+// Four elements per thread where d_model is a multiple of 4, else one, and with few elements
+// LANES threads for each, which share the splits.  The splits are added in their order, or each
+// thread's every LANES-th in order and then the threads' sums: a function of the sizes.
+template <typename O, int N, int LANES>
 __global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqScratch w, const float *__restrict__ part,
                                                      int64_t nsplit, int64_t d, const uint16_t *__restrict__ W, int fused,
-                                                     const int *only_if, O *out, int add, int by_row,
-                                                     int scalars)
+                                                     const int *only_if, O *out, int add, int by_row, int scalars)
 {
     wait_for_stream();
     if (seq_refused(w.hdr)) return;
     if (only_if && !*reinterpret_cast<const volatile int *>(only_if)) return;
     if (scalars && blockIdx.x == 0) seq_scalars<256>(l, w);
     const int64_t dn = d / N, count = l.n_tok * dn, plane = l.n_tok * d;
+    const int sub = threadIdx.x % LANES;
     bool bad = false;
-    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < count; i += int64_t(256) * gridDim.x) {
-        const int64_t t = i / dn, k = (i - t * dn) * N;
-        const int c = w.slot[t];
+    for (int64_t i0 = blockIdx.x * int64_t(256 / LANES); i0 < count; i0 += int64_t(256 / LANES) * gridDim.x) {
+        const int64_t i = i0 + threadIdx.x / LANES;
+        const bool in = i < count;
+        const int64_t t = in ? i / dn : 0, k = in ? (i - t * dn) * N : 0;
+        const int c = in ? w.slot[t] : -1;
         float v[N] = {};
         if (c >= 0) {
             const float *p = part + (by_row ? t : c) * d + k;
@@ -510,34 +513,39 @@ __global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqS
                     x[0] = __ldcs(p + s * plane);
                 }
             };
-            int64_t s = 0;
-            for (; s + 8 <= nsplit; s += 8) {
+            int64_t s = sub;
+            for (; s + 7 * LANES < nsplit; s += 8 * LANES) {
                 float x[8][N];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) load(s + q, x[q]);
+                for (int q = 0; q < 8; ++q) load(s + q * LANES, x[q]);
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
 #pragma unroll
                     for (int e = 0; e < N; ++e) v[e] += x[q][e];
             }
-            for (; s < nsplit; ++s) {
+            for (; s < nsplit; s += LANES) {
                 float x[N];
                 load(s, x);
 #pragma unroll
                 for (int e = 0; e < N; ++e) v[e] += x[e];
             }
-            if (fused) {
-                if constexpr (N == 4) {
-                    // (the fused pass runs on bf16 inputs)
-                    const float a = w.tokp[c].y, az = a / w.z[c];
-                    const uint2 b = *reinterpret_cast<const uint2 *>(W + w.y[c] * d + k);
-                    const float wv[4] = {h16_lo<false>(b.x), h16_hi<false>(b.x), h16_lo<false>(b.y), h16_hi<false>(b.y)};
+        }
 #pragma unroll
-                    for (int e = 0; e < N; ++e) v[e] = a == 0.f ? 0.f : fmaf(az, v[e], -a * wv[e]);
-                }
+        for (int o = LANES / 2; o > 0; o >>= 1)
 #pragma unroll
-                for (int e = 0; e < N; ++e) bad |= !isfinite(v[e]);
+            for (int e = 0; e < N; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+        if (!in || sub != 0) continue;
+        if (fused && c >= 0) {
+            if constexpr (N == 4) {
+                // (the fused pass runs on bf16 inputs)
+                const float a = w.tokp[c].y, az = a / w.z[c];
+                const uint2 b = *reinterpret_cast<const uint2 *>(W + w.y[c] * d + k);
+                const float wv[4] = {h16_lo<false>(b.x), h16_hi<false>(b.x), h16_lo<false>(b.y), h16_hi<false>(b.y)};
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] = a == 0.f ? 0.f : fmaf(az, v[e], -a * wv[e]);
             }
+#pragma unroll
+            for (int e = 0; e < N; ++e) bad |= !isfinite(v[e]);
         }
         O *o = out + t * d + k;
         if constexpr (std::is_same<O, float>::value) {
@@ -559,11 +567,16 @@ static cudaError_t dh_one(const SeqLoss &l, const SeqScratch &w, const float *pa
                           bool scalars, cudaStream_t st)
 {
     const bool four = d % 4 == 0;
-    int64_t grid = (l.n_tok * (four ? d / 4 : d) + 255) / 256;
+    const int64_t items = l.n_tok * (four ? d / 4 : d);
+    // fewer elements than eight threads for each would fill the GPU with
+    const bool few = items < 152 * 256 && nsplit >= 16;
+    int64_t grid = (items * (few ? 8 : 1) + 255) / 256;
     if (grid > 4096) grid = 4096;
-    return launch(four ? seq_dh_kernel<O, 4> : seq_dh_kernel<O, 1>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st,
-                  l, w, part, nsplit, d, static_cast<const uint16_t *>(W), fused ? 1 : 0, only_if,
-                  static_cast<O *>(out), add ? 1 : 0, by_row ? 1 : 0, scalars ? 1 : 0);
+    auto kern = four ? (few ? seq_dh_kernel<O, 4, 8> : seq_dh_kernel<O, 4, 1>)
+                     : (few ? seq_dh_kernel<O, 1, 8> : seq_dh_kernel<O, 1, 1>);
+    return launch(kern, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, l, w, part, nsplit, d,
+                  static_cast<const uint16_t *>(W), fused ? 1 : 0, only_if, static_cast<O *>(out), add ? 1 : 0,
+                  by_row ? 1 : 0, scalars ? 1 : 0);
 }
 
 cudaError_t launch_seq_dh(int out_dtype, const SeqLoss &l, const SeqScratch &w, const float *part, int64_t nsplit,

@@ -1650,7 +1650,13 @@ cudaError_t launch_distill_logits(int dtype, const void *student, const void *te
 // kernel: STATS writes per-tile partial statistics, ROWS/COLS rebuild the
 // gradient tile in shared memory (fp32, never rounded) and accumulate
 // G . Y[:, slice] over the loop of Y tiles.
-template <int MODE, bool DISTILL>
+//
+// B: the tiles' edge, SL: columns of a slice.  64 and 64, or, for the sequence losses where
+// that leaves most SMs idle, 32 and 256: four times the blocks, and for d_model up to 256 each
+// logit computed once (a policy step over 94 tokens of 256 and a vocabulary of 4000: 207 ->
+// 132 us, 64 x 64 x 1000 71 -> 52).  The contraction's next step is loaded while this one is
+// worked on.
+template <int MODE, bool DISTILL, int B, int SL>
 __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                                                  const float *__restrict__ Y,
                                                  const float *__restrict__ teach, int n_x, int n_y,
@@ -1666,21 +1672,25 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                                                  const int *__restrict__ refused)
 {
     if (refused && *reinterpret_cast<const volatile int *>(refused)) return;
-    __shared__ float xs[FP_BK][FP_BM + 4];
-    __shared__ float ys[FP_BK][FP_BN + 4];
-    __shared__ float gs[FP_BM][FP_BN + 1];
-    __shared__ float yv[FP_BN][FP_SLICE + 4];
+    constexpr int T = B / 16, S = SL / 16;     // a thread's rows and columns of a tile, its columns of a slice
+    constexpr int LD = B * FP_BK / 256;        // elements of each operand a thread loads per step
+    __shared__ float xs[FP_BK][B + 4];
+    __shared__ float ys[FP_BK][B + 4];
+    __shared__ float gs[B][B + 1];
+    __shared__ float yv[MODE == TC_STATS ? 1 : B][SL + 4];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    // a thread's slice columns: four in a row, 64 apart
+    auto column = [&](int i) { return (i >> 2) * 64 + tx * 4 + (i & 3); };
     // (the label loss; distillation scales by inv_t on its own)
     const float L2E = DISTILL ? static_cast<float>(LOG2E) : static_cast<float>(LOG2E) * inv_t;
-    const int n_xt = (n_x + FP_BM - 1) / FP_BM;
+    const int n_xt = (n_x + B - 1) / B;
     // the launch's tokens, or as many as an earlier kernel gathered
     if (n_dev) {
         n_tok = min(n_tok, *n_dev);
         if (MODE == TC_COLS) n_y = n_tok;
         else n_x = n_tok;
     }
-    const int n_yt = (n_y + FP_BN - 1) / FP_BN;
+    const int n_yt = (n_y + B - 1) / B;
 
     int xt, yt_begin, yt_end, slice = 0, split = 0;
     if (MODE == TC_STATS) {
@@ -1688,7 +1698,7 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
         yt_begin = blockIdx.x / n_xt;
         yt_end = yt_begin + 1;
     } else {
-        const int n_sl = (d + FP_SLICE - 1) / FP_SLICE;
+        const int n_sl = (d + SL - 1) / SL;
         int b = blockIdx.x;
         slice = b % n_sl;
         b /= n_sl;
@@ -1697,9 +1707,9 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
         yt_begin = static_cast<int>((static_cast<int64_t>(split) * n_yt) / n_split);
         yt_end = static_cast<int>((static_cast<int64_t>(split + 1) * n_yt) / n_split);
     }
-    const int xrow0 = xt * FP_BM;
+    const int xrow0 = xt * B;
     if (xrow0 >= n_x) return;
-    float acc[4][4] = {};
+    float acc[T][S] = {};
     // STATS: the logits are compensated dot products (Dot2 of Ogita, Rump and
     // Oishi, "Accurate sum and dot product", SIAM J. Sci. Comput. 26 (2005)):
     // each product is split exactly into its rounded value and the FMA
@@ -1710,28 +1720,40 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
     constexpr bool DOT2 = MODE == TC_STATS;
 
     for (int yt = yt_begin; yt < yt_end; ++yt) {
-        const int ycol0 = yt * FP_BN;
-        float s[4][4] = {}, sc[4][4] = {};
+        const int ycol0 = yt * B;
+        float s[T][T] = {}, sc[T][T] = {};
+        float xn[LD], yn[LD];
+        auto fetch = [&](int k0) {
+#pragma unroll
+            for (int i = 0; i < LD; ++i) {
+                const int e = threadIdx.x + i * 256, rr = e / FP_BK, gk = k0 + e % FP_BK;
+                const int gx = xrow0 + rr, gy = ycol0 + rr;
+                xn[i] = (gx < n_x && gk < d) ? X[static_cast<int64_t>(gx) * d + gk] : 0.f;
+                yn[i] = (gy < n_y && gk < d) ? Y[static_cast<int64_t>(gy) * d + gk] : 0.f;
+            }
+        };
+        fetch(0);
         for (int k0 = 0; k0 < d; k0 += FP_BK) {
-            for (int e = threadIdx.x; e < FP_BM * FP_BK; e += 256) {
-                const int rr = e / FP_BK, kk = e % FP_BK;
-                const int gx = xrow0 + rr, gy = ycol0 + rr, gk = k0 + kk;
-                xs[kk][rr] = (gx < n_x && gk < d) ? X[static_cast<int64_t>(gx) * d + gk] : 0.f;
-                ys[kk][rr] = (gy < n_y && gk < d) ? Y[static_cast<int64_t>(gy) * d + gk] : 0.f;
+#pragma unroll
+            for (int i = 0; i < LD; ++i) {
+                const int e = threadIdx.x + i * 256;
+                xs[e % FP_BK][e / FP_BK] = xn[i];
+                ys[e % FP_BK][e / FP_BK] = yn[i];
             }
             __syncthreads();
+            if (k0 + FP_BK < d) fetch(k0 + FP_BK);
 #pragma unroll
             for (int kk = 0; kk < FP_BK; ++kk) {
-                float xa[4], yb[4];
+                float xa[T], yb[T];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    xa[i] = xs[kk][ty * 4 + i];
-                    yb[i] = ys[kk][tx * 4 + i];
+                for (int i = 0; i < T; ++i) {
+                    xa[i] = xs[kk][ty * T + i];
+                    yb[i] = ys[kk][tx * T + i];
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < T; ++i)
 #pragma unroll
-                    for (int jx = 0; jx < 4; ++jx) {
+                    for (int jx = 0; jx < T; ++jx) {
                         if (DOT2) {
                             const float p = __fmul_rn(xa[i], yb[jx]);
                             const float pe = __fmaf_rn(xa[i], yb[jx], -p);       // a b = p + pe exactly
@@ -1749,20 +1771,20 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
         }
         if (DOT2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < T; ++i)
 #pragma unroll
-                for (int jx = 0; jx < 4; ++jx) s[i][jx] = __fadd_rn(s[i][jx], sc[i][jx]);
+                for (int jx = 0; jx < T; ++jx) s[i][jx] = __fadd_rn(s[i][jx], sc[i][jx]);
         }
         if (MODE == TC_STATS) {
-            // rows ty*4+i, columns tx*4+jx; a row's 64 columns live in 16
+            // rows ty*T+i, columns tx*T+jx; a row's B columns live in 16
             // lanes of one half-warp
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = xrow0 + ty * 4 + i;
-                float vs[4], vt[4];
+            for (int i = 0; i < T; ++i) {
+                const int t = xrow0 + ty * T + i;
+                float vs[T], vt[T];
 #pragma unroll
-                for (int jx = 0; jx < 4; ++jx) {
-                    const int v = ycol0 + tx * 4 + jx;
+                for (int jx = 0; jx < T; ++jx) {
+                    const int v = ycol0 + tx * T + jx;
                     const bool in = v < vocab && t < n_tok;
                     vs[jx] = in ? s[i][jx] : -INFINITY;
                     vt[jx] = (DISTILL && in) ? teach[static_cast<int64_t>(t) * vocab + v] : -INFINITY;
@@ -1770,10 +1792,10 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                 if (!DISTILL) {
                     float m = -INFINITY, z = 0.f;
 #pragma unroll
-                    for (int jx = 0; jx < 4; ++jx) m = fmaxf(m, vs[jx] * L2E);
+                    for (int jx = 0; jx < T; ++jx) m = fmaxf(m, vs[jx] * L2E);
                     for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
-                    for (int jx = 0; jx < 4; ++jx) z += exp2f(vs[jx] * L2E - m);
+                    for (int jx = 0; jx < T; ++jx) z += exp2f(vs[jx] * L2E - m);
                     for (int o = 1; o < 16; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
                     if (t < n_tok) {
                         if (tx == 0) {
@@ -1782,9 +1804,9 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                             part[part_plane + o] = z;
                         }
                         // no targets (a vocabulary shard): the target logit comes from elsewhere
-                        const int64_t rel = targets ? targets[t] - ycol0 - tx * 4 : -1;
+                        const int64_t rel = targets ? targets[t] - ycol0 - tx * T : -1;
 #pragma unroll
-                        for (int jx = 0; jx < 4; ++jx)
+                        for (int jx = 0; jx < T; ++jx)
                             if (rel == jx) tgt[t] = s[i][jx];
                     }
                 } else {
@@ -1792,9 +1814,9 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                     // CE / forward KL: sum p a with the teacher's p exact (its lse from
                     // teacher_stats); reverse KL: sum 2^(a - max) (a - b)
                     const float lt2 = t < n_tok ? static_cast<float>(tstat[t].x) : 0.f;
-                    float a2[4], b2[4], ms = -INFINITY;
+                    float a2[T], b2[T], ms = -INFINITY;
 #pragma unroll
-                    for (int jx = 0; jx < 4; ++jx) {
+                    for (int jx = 0; jx < T; ++jx) {
                         a2[jx] = vs[jx] * inv_t * L2E;
                         b2[jx] = vt[jx] * inv_t * L2E;
                         ms = fmaxf(ms, a2[jx]);
@@ -1802,7 +1824,7 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                     for (int o = 1; o < 16; o <<= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o));
                     float zs = 0.f, xx = 0.f;
 #pragma unroll
-                    for (int jx = 0; jx < 4; ++jx) {
+                    for (int jx = 0; jx < T; ++jx) {
                         if (vs[jx] == -INFINITY) continue;
                         const float es = exp2f(a2[jx] - ms);
                         zs += es;
@@ -1824,10 +1846,10 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
         } else {
             // gradient tile (rows of X by columns of Y) into shared memory
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < T; ++i) {
 #pragma unroll
-                for (int jx = 0; jx < 4; ++jx) {
-                    const int xr = xrow0 + ty * 4 + i, yc = ycol0 + tx * 4 + jx;
+                for (int jx = 0; jx < T; ++jx) {
+                    const int xr = xrow0 + ty * T + i, yc = ycol0 + tx * T + jx;
                     const int tok = (MODE == TC_ROWS) ? xr : yc;
                     const int voc = (MODE == TC_ROWS) ? yc : xr;
                     float g = 0.f;
@@ -1847,27 +1869,26 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                                 g = P.z * qv - P.w * exp2f(b2v - P.y);
                         }
                     }
-                    gs[ty * 4 + i][tx * 4 + jx] = g;
+                    gs[ty * T + i][tx * T + jx] = g;
                 }
             }
-            // Y[ycol0 .. +64][slice cols]
-            for (int e = threadIdx.x; e < FP_BN * FP_SLICE; e += 256) {
-                const int rr = e / FP_SLICE, cc = e % FP_SLICE;
-                const int gy = ycol0 + rr, gc = slice * FP_SLICE + cc;
+            // Y[ycol0 .. +B][slice cols]
+            for (int e = threadIdx.x; e < B * SL; e += 256) {
+                const int rr = e / SL, cc = e % SL;
+                const int gy = ycol0 + rr, gc = slice * SL + cc;
                 yv[rr][cc] = (gy < n_y && gc < d) ? Y[static_cast<int64_t>(gy) * d + gc] : 0.f;
             }
             __syncthreads();
-            for (int kk = 0; kk < FP_BN; ++kk) {
-                float ga[4], yb[4];
+            for (int kk = 0; kk < B; ++kk) {
+                float ga[T], yb[S];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ga[i] = gs[ty * 4 + i][kk];
-                    yb[i] = yv[kk][tx * 4 + i];
-                }
+                for (int i = 0; i < T; ++i) ga[i] = gs[ty * T + i][kk];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < S; ++i) yb[i] = yv[kk][column(i)];
 #pragma unroll
-                    for (int jx = 0; jx < 4; ++jx) acc[i][jx] = fmaf(ga[i], yb[jx], acc[i][jx]);
+                for (int i = 0; i < T; ++i)
+#pragma unroll
+                    for (int jx = 0; jx < S; ++jx) acc[i][jx] = fmaf(ga[i], yb[jx], acc[i][jx]);
             }
             __syncthreads();
         }
@@ -1875,12 +1896,12 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
     if (MODE != TC_STATS) {
         float *o = out + static_cast<int64_t>(split) * out_split_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int xr = xrow0 + ty * 4 + i;
+        for (int i = 0; i < T; ++i) {
+            const int xr = xrow0 + ty * T + i;
             if (xr >= n_x) continue;
 #pragma unroll
-            for (int jx = 0; jx < 4; ++jx) {
-                const int c = slice * FP_SLICE + tx * 4 + jx;
+            for (int jx = 0; jx < S; ++jx) {
+                const int c = slice * SL + column(jx);
                 if (c < d) {
                     float *p = o + static_cast<int64_t>(xr) * d + c;
                     *p = accumulate ? *p + acc[i][jx] : acc[i][jx];
@@ -1895,19 +1916,26 @@ cudaError_t launch_fp(int mode, bool distill, const void *X, const void *Y, cons
                       float inv_t, const int64_t *targets, const float4 *tokp, const double2 *tstat,
                       float *part,
                       float *tgt, int64_t part_stride, int64_t part_plane, float *out,
-                      int64_t out_split_stride, cudaStream_t st, bool accumulate, const int *n_dev, const int *refused)
+                      int64_t out_split_stride, cudaStream_t st, bool accumulate, const int *n_dev, const int *refused, bool small)
 {
-    const int n_xt = (n_x + FP_BM - 1) / FP_BM, n_yt = (n_y + FP_BN - 1) / FP_BN;
-    const int n_sl = (d + FP_SLICE - 1) / FP_SLICE;
+    const int b = small ? FP_SMALL : FP_BM, sl = small ? FP_SMALL_SLICE : FP_SLICE;
+    const int n_xt = (n_x + b - 1) / b, n_yt = (n_y + b - 1) / b;
+    const int n_sl = (d + sl - 1) / sl;
     const int64_t grid64 = mode == TC_STATS ? static_cast<int64_t>(n_xt) * n_yt
                                             : static_cast<int64_t>(n_xt) * n_sl * n_split;
     const unsigned grid = static_cast<unsigned>(grid64);
     const float *x = static_cast<const float *>(X), *y = static_cast<const float *>(Y);
-#define LOSSK_FP(M, D)                                                                             \
-    fp_kernel<M, D><<<grid, 256, 0, st>>>(x, y, teach, n_x, n_y, d, n_tok, vocab, n_split,       \
+#define LOSSK_FP_T(M, D, B, SL)                                                                    \
+    fp_kernel<M, D, B, SL><<<grid, 256, 0, st>>>(x, y, teach, n_x, n_y, d, n_tok, vocab, n_split,       \
                                           direction, inv_t, targets, tokp, tstat, part, tgt, part_stride, \
                                           part_plane, out, out_split_stride, accumulate ? 1 : 0, n_dev, refused)
-    if (mode == TC_STATS) {
+#define LOSSK_FP(M, D) LOSSK_FP_T(M, D, FP_BM, FP_SLICE)
+    if (small) {
+        // (label losses only)
+        if (mode == TC_STATS) LOSSK_FP_T(TC_STATS, false, FP_SMALL, FP_SMALL_SLICE);
+        else if (mode == TC_ROWS) LOSSK_FP_T(TC_ROWS, false, FP_SMALL, FP_SMALL_SLICE);
+        else LOSSK_FP_T(TC_COLS, false, FP_SMALL, FP_SMALL_SLICE);
+    } else if (mode == TC_STATS) {
         if (distill) LOSSK_FP(TC_STATS, true); else LOSSK_FP(TC_STATS, false);
     } else if (mode == TC_ROWS) {
         if (distill) LOSSK_FP(TC_ROWS, true); else LOSSK_FP(TC_ROWS, false);
@@ -1915,6 +1943,7 @@ cudaError_t launch_fp(int mode, bool distill, const void *X, const void *Y, cons
         if (distill) LOSSK_FP(TC_COLS, true); else LOSSK_FP(TC_COLS, false);
     }
 #undef LOSSK_FP
+#undef LOSSK_FP_T
     return cudaGetLastError();
 }
 

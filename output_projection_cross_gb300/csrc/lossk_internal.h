@@ -19,6 +19,7 @@ constexpr int TC_BK = 64;          // K per pipeline stage (one 128-byte swizzle
 constexpr int TC_SLICE = 256;      // d_model columns one backward CTA accumulates
 // Tile geometry of the fp32 FFMA path.
 constexpr int FP_BM = 64, FP_BN = 64, FP_BK = 16, FP_SLICE = 64;
+constexpr int FP_SMALL = 32, FP_SMALL_SLICE = 256;     // and of its small form
 
 // Workspace header (first 256 bytes of every workspace).
 struct WsHeader {
@@ -277,7 +278,7 @@ cudaError_t launch_fp(int mode, bool distill, const void *X, const void *Y, cons
                       float *part,
                       float *tgt, int64_t part_stride, int64_t part_plane, float *out,
                       int64_t out_split_stride, cudaStream_t st, bool accumulate = false,
-                      const int *n_dev = nullptr, const int *refused = nullptr);
+                      const int *n_dev = nullptr, const int *refused = nullptr, bool small = false);
 // precise: exact exp2 rescales (the fp32 inputs path); else ex2.approx.
 cudaError_t launch_merge_ce(const float *part, const float *tgt, const int64_t *targets,
                             const uint8_t *mask, int64_t n, int64_t n_ct, int64_t n_pad,

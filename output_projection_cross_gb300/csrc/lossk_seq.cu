@@ -24,6 +24,7 @@ constexpr int GSIG_WORDS = 2 * G_MAX_CTAS * G_SLOTS;
 
 struct Layout {
     int64_t n_pad, n_ct, nsplit;
+    bool small;
     int splits, cluster;
     size_t off_slot, off_row, off_y, off_seq, off_tgt, off_lp, off_lse2, off_z, off_tokp, off_sum, off_slope, off_acc,
         off_terms, off_tick, off_rows, off_hidden, off_part, off_dhpart, off_zpart, off_gring, off_gsig, off_dhacc, total;
@@ -62,12 +63,16 @@ int32_t layout(int32_t kind, int64_t n, int64_t d, int64_t V, int64_t n_seq, int
     L->off_tick = take(sizeof(int) * np);
     if (head) {
         const bool tc = is16(dtype);
-        L->n_ct = cdiv(V, tc ? TC_BN_FWD : FP_BN);
+        // fp32: small tiles where those of 64 x 64 would be fewer than two for each SM
+        L->small = !tc && cdiv(n, FP_BM) * cdiv(V, FP_BN) < 304;
+        const int64_t edge = L->small ? FP_SMALL : FP_BM, slice = L->small ? FP_SMALL_SLICE : FP_SLICE;
+        L->n_ct = cdiv(V, tc ? TC_BN_FWD : edge);
         L->nsplit = dh_splits(n, d, V, dtype);
         if (!tc) {
-            // two blocks per SM, down to one vocabulary tile each: 64 x 64 x 1000 takes 72 us in the two
-            // splits of the label loss's rule (eight tiles one after another), 13 in sixteen
-            const int64_t base = cdiv(n, FP_BM) * cdiv(d, FP_SLICE), most = cdiv(304, base);
+            // d_hidden in as many splits of the vocabulary as make two blocks per SM, down to one tile
+            // each: 64 x 64 x 1000 takes 72 us in the two splits of the label loss's rule (eight tiles one
+            // after another)
+            const int64_t base = cdiv(n, edge) * cdiv(d, slice), most = cdiv(304, base);
             L->nsplit = most < L->n_ct ? most : L->n_ct;
         }
         const size_t nd = static_cast<size_t>(n) * static_cast<size_t>(d);
@@ -187,7 +192,7 @@ int32_t check(const Call &c, Layout *L)
         if (c.objective < LOSSK_PREF_SIGMOID || c.objective > LOSSK_PREF_SQUARED) return LOSSK_UNKNOWN_OBJECTIVE;
         if (c.objective != LOSSK_PREF_SIGMOID && (c.margin != 0.0 || c.smooth != 0.0)) return LOSSK_NON_FINITE_SCALAR;
     } else if (!finite({c.low, c.high, c.kl, c.temperature}) || c.low < 0.0 || c.low > 1.0 || c.high < 0.0 ||
-               c.kl < 0.0 || c.temperature <= 0.0) {
+               c.kl < 0.0 || c.temperature < 1e-30 || c.temperature > 1e30) {
         return LOSSK_NON_FINITE_SCALAR;
     }
     const uint32_t known = LOSSK_ACCUMULATE_GRADS | LOSSK_REDUCE_SUM |
@@ -263,7 +268,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
         {
             Launch k(KK_FP_STATS, st);
             TRY(launch_fp(TC_STATS, false, hid, c.W, nullptr, n, V, d, n, V, 1, 0, inv_t, w.y, nullptr, nullptr, part,
-                          w.tgt, L.n_pad, L.n_ct * L.n_pad, nullptr, 0, st, false, n_dev, bad));
+                          w.tgt, L.n_pad, L.n_ct * L.n_pad, nullptr, 0, st, false, n_dev, bad, L.small));
         }
         TRY(launch_seq_merge_tiles(l, w, part, L.n_ct, nullptr, st));
         int32_t s = run_losses(c, l, w);
@@ -274,14 +279,14 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
                 Launch k(KK_FP_ROWS, st);
                 TRY(launch_fp(TC_ROWS, false, hid, c.W, nullptr, n, V, d, n, V, static_cast<int>(L.nsplit), 0, inv_t,
                               nullptr, w.tokp, nullptr, nullptr, nullptr, 0, 0, dhpart, c.n * c.d, st, false, n_dev,
-                              bad));
+                              bad, L.small));
             }
             TRY(launch_seq_dh(LOSSK_F32, l, w, dhpart, L.nsplit, c.d, c.W, false, nullptr, c.g0, acc, false, true, st));
         }
         if (c.g1) {
             Launch k(KK_FP_COLS, st);
             TRY(launch_fp(TC_COLS, false, c.W, hid, nullptr, V, n, d, n, V, 1, 0, inv_t, nullptr, w.tokp, nullptr,
-                          nullptr, nullptr, 0, 0, static_cast<float *>(c.g1), 0, st, acc, n_dev, bad));
+                          nullptr, nullptr, 0, 0, static_cast<float *>(c.g1), 0, st, acc, n_dev, bad, L.small));
         }
         return LOSSK_OK;
     }

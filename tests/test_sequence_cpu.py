@@ -79,7 +79,7 @@ def test_refusals_of_the_policy_loss(f):
                 dict(flags=4), dict(flags=8), dict(flags=16), dict(n_seq=3, first=P, fl=4, flags=16, al=2)):
         assert f(**bad) == 582, bad
     for bad in (dict(low=-0.1), dict(low=1.1), dict(high=-0.1), dict(kl=-1.0), dict(T=0.0), dict(T=-1.0), dict(T=NAN),
-                dict(low=NAN), dict(high=INF), dict(kl=INF), dict(T=INF)):
+                dict(low=NAN), dict(high=INF), dict(kl=INF), dict(T=INF), dict(T=1e-31), dict(T=1e31)):
         assert f(**bad) == 585, bad
     assert f(flags=32) == 592
 
