@@ -107,9 +107,11 @@ def check_grads(c, out, ref, scale=1.0, base=None, grad="same", moves=0.0):
     own[rows, c.targets[rows]] += a.abs()[rows]
     rel = 8.0 * c.lp_tol() + moves + 2.0 ** -20
     half = HALF[c.dtype]
+    # fp32 and bf16 end at 2^-126: a probability, its product with the coefficient and a result below it may be zero
+    under = 2.0 ** -126 * (2.0 + float(a.abs().max()))
     if not c.d:
         want = g if base is None else g + base.double()
-        close(out["grad_logits"], want, rel * size + half * want.abs() + TINY[c.dtype], "grad_logits")
+        close(out["grad_logits"], want, rel * size + half * want.abs() + TINY[c.dtype] + under, "grad_logits")
         return
     h, w = torch.where(c.on[:, None], c.hidden.double(), 0.0), c.weight.double()
     # fp16 tiles hold the coefficients scaled to 2^14: their smallest step is 2^-39 of the largest
@@ -117,8 +119,8 @@ def check_grads(c, out, ref, scale=1.0, base=None, grad="same", moves=0.0):
     sums = rel + (c.d + max(c.n, c.V) / 16) * 2.0 ** -23
     fine = 2.0 ** -38 * float(a.abs().max()) if c.dtype == "f16" else 0.0
     out_half = half if grad == "same" and c.dtype != "f32" else 2.0 ** -24
-    tiny = TINY[c.dtype] if grad == "same" else 0.0
-    err = tile * own + sums * size + fine
+    tiny = (TINY[c.dtype] if grad == "same" else 0.0) + 2.0 ** -126
+    err = tile * own + sums * size + fine + under
     for name, m, ab in (("d_hidden", g @ w, err @ w.abs()), ("d_weight", g.t() @ h, err.t() @ h.abs())):
         if out[name] is None:
             continue
