@@ -10,6 +10,11 @@ namespace lossk {
 // launch() starts.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The kernel after this one, if launch() starts it, may be set up from here on, once every
+// block has come this far.  Called after wait_for_stream(), so that never more than two
+// kernels are on the way: what was ahead of this one has ended before the next one begins.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A launch whose blocks may be set up while the kernel ahead of them in the
 // stream, of whatever call, ends.  Between two calls of a few microseconds that
 // saves 2 us of each (4 beams over 32000 tokens: 14.1 -> 11.6 us a call).

@@ -47,7 +47,7 @@ template <int T> __global__ void __launch_bounds__(T) attn_share_kernel(AttnArgs
     __shared__ int s_first, s_min, s_max;
     const int g = blockIdx.x, t = threadIdx.x;
     wait_for_stream();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
     if (t == 0) {
         int mn = 1 << 30, mx = 0;
         for (int i = 0; i < a.share; ++i) {
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(PLAN_T) attn_plan_kernel(AttnArgs a)
 {
     __shared__ long long s_warp[PLAN_T / 32];
     wait_for_stream();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
     check_lens(a);
     sum_units(a, a.base, s_warp);
 }

@@ -442,13 +442,22 @@ int policy_rows_cluster(int64_t n, int64_t vocab, int dtype)
     return bytes > c * POLICY_MOST ? 0 : c;
 }
 
+// Every block has its place at once: the rows' copies and statistics run beside the kernel that
+// numbers the rows (48 rows of 32000 in bf16 17.9 -> 15.0 us a call).  With more rows than that what
+// comes after the wait would be in every row's chain (2048 of 151936: 226 -> 234).
+bool policy_rows_early(int64_t n, int64_t vocab, int dtype, int cluster)
+{
+    return vocab * (dtype == LOSSK_F32 ? 4 : 2) > SMALL_ROW && n * cluster <= 152 * POLICY_BLOCKS;
+}
+
 namespace {
 
-// What the policy loss reads for the row t of slot c.
-__device__ __forceinline__ RowInputs slot_inputs(const SeqLoss &l, const SeqScratch &w, int t, int c)
+// What the policy loss reads for row t, counted.
+__device__ __forceinline__ RowInputs slot_inputs(const SeqLoss &l, const SeqScratch &w, int t)
 {
     int s = 0, n_s = 0;
     if (l.n_seq > 0 && (l.flags & (LOSSK_SEQ_MEAN | LOSSK_SEQ_ADVANTAGES))) {
+        const int c = w.slot[t];
         int hi = l.n_seq;                      // the last sequence that starts at or before slot c
         while (hi - s > 1) {
             const int mid = (s + hi) >> 1;
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(GRAD_T) policy_small_kernel(const SeqLoss l, c
         if (lane == 0) {
             target = w.y[c];
             y = value(r.row[target]);
-            in = slot_inputs(l, w, t, c);
+            in = slot_inputs(l, w, t);
         }
         float m = -INFINITY, z = 0.f;
         scan_row<T, 32, SMALL_U>(r, 0, r.n, lane, l.k2, m, z);
@@ -506,8 +515,8 @@ __global__ void __launch_bounds__(GRAD_T) policy_small_kernel(const SeqLoss l, c
         write_row<T, GRAD == 2, 32, SMALL_U>(r, grad + t * l.vocab, 0, r.n, lane, P, l.k2);
 }
 
-// GRAD: 0 none, 1 written, 2 added to what is there.
-template <typename T, int GRAD>
+// GRAD: 0 none, 1 written, 2 added to what is there.  EARLY: policy_rows_early().
+template <typename T, int GRAD, bool EARLY>
 __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(const SeqLoss l, const SeqScratch w, const T *logits, T *grad,
                                                             int cluster)
 {
@@ -524,15 +533,25 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
     }
     __syncthreads();
     const int t = blockIdx.x / cluster, rank = blockIdx.x - t * cluster, tid = threadIdx.x;
-    wait_for_stream();
-    const int c = w.slot[t];                   // (asked for beside the refusal)
-    if (seq_refused(w.hdr)) return;
+    // Early: all that the copies and the statistics read is the call's inputs, which were there before
+    // the kernel ahead began (let_next_start), and which row counts follows from them.
+    bool on;
+    if constexpr (!EARLY) {
+        wait_for_stream();
+        on = w.slot[t] >= 0;                   // (asked for beside the refusal)
+        if (seq_refused(w.hdr)) return;
+    } else {
+        on = (!l.mask || l.mask[t] != 0) && (!l.first || (t >= l.first[0] && t < l.first[l.n_seq]));
+    }
     const RowVecs<T> r(logits + t * l.vocab, l.vocab);
     const int v0 = r.piece(rank, cluster), v1 = r.piece(rank + 1, cluster);
     T *g = GRAD ? grad + t * l.vocab : nullptr;
     float4 P = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
     float4 terms = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c >= 0) {
+    float m = -INFINITY, z = 0.f, y = 0.f;
+    int64_t target = 0;
+    RowInputs in{};
+    if (on) {
         // the share's whole vectors arrive in chunks
         const int va = v0 < v1 && !r.whole(r.at(v0)) ? v0 + 1 : v0;
         const int vb = v1 > va && !r.whole(r.at(v1 - 1)) ? v1 - 1 : v1, nv = max(vb - va, 0);
@@ -544,15 +563,11 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
                 if (bytes) bulk_copy_g2s(s_row + chunk(k) - v0, r.row + r.at(chunk(k)), bytes, &s_bar[k]);
             }
         // what does not come from the row's statistics, asked for before they are taken
-        float y = 0.f;
-        int64_t target = 0;
-        RowInputs in{};
         if (tid == 0) {
-            target = w.y[c];
-            y = value(r.row[target]);
-            in = slot_inputs(l, w, t, c);
+            target = l.targets[t];
+            y = !EARLY || (target >= 0 && target < l.vocab) ? value(r.row[target]) : 0.f;
+            if (!EARLY) in = slot_inputs(l, w, t);
         }
-        float m = -INFINITY, z = 0.f;
         // the first and the last vector where they are partly outside the row
         if ((tid == 0 && va > v0) || (tid == 1 && vb < v1)) {
             float f[N];
@@ -584,6 +599,14 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
                     z += m > -INFINITY ? s_part[q].y * ex2_approx(s_part[q].x - m) : s_part[q].y;
             }
         }
+    }
+    if constexpr (EARLY) {
+        wait_for_stream();
+        let_next_start();
+        if (seq_refused(w.hdr)) return;
+        if (on && tid == 0) in = slot_inputs(l, w, t);
+    }
+    if (on) {
         if (tid == 0) {
             float lp, lse2;
             row_logp(l, m, z, y, cluster > 1 ? 3 : 2, lp, lse2);
@@ -666,14 +689,15 @@ __global__ void __launch_bounds__(1024) policy_scalars_kernel(const SeqLoss l, c
     if (threadIdx.x == 0) write_scalars(l, w.hdr, v[0], v[1], v[2]);
 }
 
-template <typename T, int GRAD>
+template <typename T, int GRAD, bool EARLY>
 static cudaError_t policy_one(const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad, int cluster,
                               cudaStream_t st)
 {
-    if (l.vocab * static_cast<int64_t>(sizeof(T)) <= SMALL_ROW)
-        return launch(policy_small_kernel<T, GRAD>, dim3(static_cast<unsigned>((l.n_tok + GRAD_T / 32 - 1) / (GRAD_T / 32))),
-                      dim3(GRAD_T), 0, st, l, w, static_cast<const T *>(logits), static_cast<T *>(grad));
-    constexpr auto K = policy_rows_kernel<T, GRAD>;
+    if constexpr (!EARLY)
+        if (l.vocab * static_cast<int64_t>(sizeof(T)) <= SMALL_ROW)
+            return launch(policy_small_kernel<T, GRAD>, dim3(static_cast<unsigned>((l.n_tok + GRAD_T / 32 - 1) / (GRAD_T / 32))),
+                          dim3(GRAD_T), 0, st, l, w, static_cast<const T *>(logits), static_cast<T *>(grad));
+    constexpr auto K = policy_rows_kernel<T, GRAD, EARLY>;
     // a share of the row's vectors, rounded up, and the one that a row may begin in
     const size_t smem = static_cast<size_t>((l.vocab / NVEC<T> + 2) / cluster + 2) * 16;
     cudaError_t e = raise_smem<K>(smem);
@@ -699,8 +723,13 @@ template <typename T>
 static cudaError_t policy_type(const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad, bool add,
                                int cluster, cudaStream_t st)
 {
-    if (!grad) return policy_one<T, 0>(l, w, logits, grad, cluster, st);
-    return add ? policy_one<T, 2>(l, w, logits, grad, cluster, st) : policy_one<T, 1>(l, w, logits, grad, cluster, st);
+    auto one = [&](auto early) {
+        constexpr bool E = decltype(early)::value;
+        if (!grad) return policy_one<T, 0, E>(l, w, logits, grad, cluster, st);
+        return add ? policy_one<T, 2, E>(l, w, logits, grad, cluster, st)
+                   : policy_one<T, 1, E>(l, w, logits, grad, cluster, st);
+    };
+    return l.early ? one(std::true_type{}) : one(std::false_type{});
 }
 
 cudaError_t launch_policy_rows(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,

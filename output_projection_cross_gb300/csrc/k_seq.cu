@@ -55,6 +55,7 @@ constexpr int PREP_T = 1024, PREP_PER = 8;
 __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
+    if (l.early) let_next_start();
     static_assert(PREP_PER * 32 == 256, "a lane of a warp scans eight of the counts");
     __shared__ int s_count[PREP_PER * 32];
     __shared__ int s_groups;
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(256) seq_gather_kernel(const SeqLoss l, const 
                                                          const T *__restrict__ W, int64_t d, T *__restrict__ out)
 {
     wait_for_stream();
+    if (l.early_pass) let_next_start();
     if (seq_refused(w.hdr)) return;
     const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int n_valid = w.hdr->n_valid;
@@ -249,6 +251,7 @@ __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, co
                                                              const float *__restrict__ zpart, int64_t nz)
 {
     wait_for_stream();
+    if (l.early) let_next_start();
     if (seq_refused(w.hdr)) return;
     const int c = blockIdx.x * 32 + threadIdx.x;
     if (c >= w.hdr->n_valid) return;
@@ -286,6 +289,7 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
                                                                     const int *only_if)
 {
     wait_for_stream();
+    if (l.early) let_next_start();
     if (seq_refused(w.hdr) || (only_if && !*reinterpret_cast<const volatile int *>(only_if))) return;
     __shared__ float s_max[MT_W][32];
     __shared__ double s_sum[MT_W][32];
@@ -328,6 +332,7 @@ constexpr int SUM_T = 256;
 __global__ void __launch_bounds__(SUM_T) seq_sum_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
+    if (l.early) let_next_start();
     if (seq_refused(w.hdr)) return;
     __shared__ double sh[SUM_T / 32];
     const int s = blockIdx.x, a = w.seq_slot[s], b = w.seq_slot[s + 1];
@@ -372,6 +377,7 @@ __device__ __forceinline__ double log_ratio(const SeqLoss &l, const SeqScratch &
 __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
+    if (l.early_pass) let_next_start();
     if (seq_refused(w.hdr)) return;
     const int t = blockIdx.x * COEF_T + threadIdx.x;
     const bool pref = l.pairs > 0;
@@ -452,6 +458,7 @@ cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t 
 __global__ void __launch_bounds__(256) seq_scalars_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
+    if (l.early) let_next_start();
     if (seq_refused(w.hdr)) return;
     seq_scalars<256>(l, w);
 }
@@ -491,6 +498,7 @@ __global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqS
                                                      const int *only_if, O *out, int add, int by_row, int scalars)
 {
     wait_for_stream();
+    if (l.early) let_next_start();
     if (seq_refused(w.hdr)) return;
     if (only_if && !*reinterpret_cast<const volatile int *>(only_if)) return;
     if (scalars && blockIdx.x == 0) seq_scalars<256>(l, w);

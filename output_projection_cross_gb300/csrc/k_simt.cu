@@ -26,6 +26,7 @@
 //                  grad_logits write
 //   fp_kernel      the fp32 inputs path: the same three passes as the tensor
 //                  core kernel (statistics, d_hidden, d_weight) on FFMA tiles.
+#include "decode_launch.h"
 #include "lossk_internal.h"
 #include "ptx.cuh"
 
@@ -1671,6 +1672,8 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                                                  int accumulate, const int *__restrict__ n_dev,
                                                  const int *__restrict__ refused)
 {
+    wait_for_stream();
+    let_next_start();
     if (refused && *reinterpret_cast<const volatile int *>(refused)) return;
     constexpr int T = B / 16, S = SL / 16;     // a thread's rows and columns of a tile, its columns of a slice
     constexpr int LD = B * FP_BK / 256;        // elements of each operand a thread loads per step
@@ -1926,25 +1929,21 @@ cudaError_t launch_fp(int mode, bool distill, const void *X, const void *Y, cons
     const unsigned grid = static_cast<unsigned>(grid64);
     const float *x = static_cast<const float *>(X), *y = static_cast<const float *>(Y);
 #define LOSSK_FP_T(M, D, B, SL)                                                                    \
-    fp_kernel<M, D, B, SL><<<grid, 256, 0, st>>>(x, y, teach, n_x, n_y, d, n_tok, vocab, n_split,       \
-                                          direction, inv_t, targets, tokp, tstat, part, tgt, part_stride, \
-                                          part_plane, out, out_split_stride, accumulate ? 1 : 0, n_dev, refused)
+    launch(fp_kernel<M, D, B, SL>, dim3(grid), dim3(256), 0, st, x, y, teach, n_x, n_y, d, n_tok, vocab, \
+           n_split, direction, inv_t, targets, tokp, tstat, part, tgt, part_stride, part_plane, out,     \
+           out_split_stride, accumulate ? 1 : 0, n_dev, refused)
 #define LOSSK_FP(M, D) LOSSK_FP_T(M, D, FP_BM, FP_SLICE)
     if (small) {
         // (label losses only)
-        if (mode == TC_STATS) LOSSK_FP_T(TC_STATS, false, FP_SMALL, FP_SMALL_SLICE);
-        else if (mode == TC_ROWS) LOSSK_FP_T(TC_ROWS, false, FP_SMALL, FP_SMALL_SLICE);
-        else LOSSK_FP_T(TC_COLS, false, FP_SMALL, FP_SMALL_SLICE);
-    } else if (mode == TC_STATS) {
-        if (distill) LOSSK_FP(TC_STATS, true); else LOSSK_FP(TC_STATS, false);
-    } else if (mode == TC_ROWS) {
-        if (distill) LOSSK_FP(TC_ROWS, true); else LOSSK_FP(TC_ROWS, false);
-    } else {
-        if (distill) LOSSK_FP(TC_COLS, true); else LOSSK_FP(TC_COLS, false);
+        if (mode == TC_STATS) return LOSSK_FP_T(TC_STATS, false, FP_SMALL, FP_SMALL_SLICE);
+        if (mode == TC_ROWS) return LOSSK_FP_T(TC_ROWS, false, FP_SMALL, FP_SMALL_SLICE);
+        return LOSSK_FP_T(TC_COLS, false, FP_SMALL, FP_SMALL_SLICE);
     }
+    if (mode == TC_STATS) return distill ? LOSSK_FP(TC_STATS, true) : LOSSK_FP(TC_STATS, false);
+    if (mode == TC_ROWS) return distill ? LOSSK_FP(TC_ROWS, true) : LOSSK_FP(TC_ROWS, false);
+    return distill ? LOSSK_FP(TC_COLS, true) : LOSSK_FP(TC_COLS, false);
 #undef LOSSK_FP
 #undef LOSSK_FP_T
-    return cudaGetLastError();
 }
 
 } // namespace lossk

@@ -244,6 +244,29 @@ int32_t run_forward(const Call &c, const Layout &L, const SeqLoss &l, const SeqS
     return LOSSK_OK;
 }
 
+// The caller's stream's helper, forked from it where `want`: aux, until join().  (Without
+// a helper aux is the caller's stream.)
+struct Fork {
+    cudaStream_t st, aux;
+    SideStream *sd;
+    std::unique_lock<std::mutex> lk;
+    bool ok = true;
+
+    Fork(bool want, cudaStream_t s) : st(s), aux(s), sd(want ? side_stream(s) : nullptr)
+    {
+        if (!sd) return;
+        lk = std::unique_lock<std::mutex>(sd->mu);
+        if (!sd->ready()) return;
+        ok = cudaEventRecord(sd->fork, st) == cudaSuccess && cudaStreamWaitEvent(sd->s, sd->fork, 0) == cudaSuccess;
+        if (ok) aux = sd->s;
+    }
+    bool join()
+    {
+        if (aux == st) return true;
+        return cudaEventRecord(sd->join, aux) == cudaSuccess && cudaStreamWaitEvent(st, sd->join, 0) == cudaSuccess;
+    }
+};
+
 // What follows the log-probabilities: sums over sequences, coefficients.
 int32_t run_losses(const Call &c, const SeqLoss &l, const SeqScratch &w)
 {
@@ -274,21 +297,27 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
         int32_t s = run_losses(c, l, w);
         if (s != LOSSK_OK) return s;
         if (!c.g0) TRY(launch_seq_scalars(l, w, st));
+        // d_hidden beside d_weight
+        Fork f(c.g0 && c.g1, st);
+        if (!f.ok) return LOSSK_DEVICE_ERROR;
+        cudaError_t e = cudaSuccess;
         if (c.g0) {
             {
-                Launch k(KK_FP_ROWS, st);
-                TRY(launch_fp(TC_ROWS, false, hid, c.W, nullptr, n, V, d, n, V, static_cast<int>(L.nsplit), 0, inv_t,
-                              nullptr, w.tokp, nullptr, nullptr, nullptr, 0, 0, dhpart, c.n * c.d, st, false, n_dev,
-                              bad, L.small));
+                Launch k(KK_FP_ROWS, f.aux);
+                e = launch_fp(TC_ROWS, false, hid, c.W, nullptr, n, V, d, n, V, static_cast<int>(L.nsplit), 0, inv_t,
+                              nullptr, w.tokp, nullptr, nullptr, nullptr, 0, 0, dhpart, c.n * c.d, f.aux, false, n_dev,
+                              bad, L.small);
             }
-            TRY(launch_seq_dh(LOSSK_F32, l, w, dhpart, L.nsplit, c.d, c.W, false, nullptr, c.g0, acc, false, true, st));
+            if (e == cudaSuccess)
+                e = launch_seq_dh(LOSSK_F32, l, w, dhpart, L.nsplit, c.d, c.W, false, nullptr, c.g0, acc, false, true,
+                                  f.aux);
         }
-        if (c.g1) {
+        if (c.g1 && e == cudaSuccess) {
             Launch k(KK_FP_COLS, st);
-            TRY(launch_fp(TC_COLS, false, c.W, hid, nullptr, V, n, d, n, V, 1, 0, inv_t, nullptr, w.tokp, nullptr,
-                          nullptr, nullptr, 0, 0, static_cast<float *>(c.g1), 0, st, acc, n_dev, bad, L.small));
+            e = launch_fp(TC_COLS, false, c.W, hid, nullptr, V, n, d, n, V, 1, 0, inv_t, nullptr, w.tokp, nullptr,
+                          nullptr, nullptr, 0, 0, static_cast<float *>(c.g1), 0, st, acc, n_dev, bad, L.small);
         }
-        return LOSSK_OK;
+        return f.join() && e == cudaSuccess ? LOSSK_OK : LOSSK_DEVICE_ERROR;
     }
 
     const BwdScratch bs{reinterpret_cast<uint16_t *>(b + L.off_gring), reinterpret_cast<unsigned *>(b + L.off_gsig),
@@ -332,21 +361,11 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     if (!c.g0) TRY(launch_seq_scalars(l, w, st));
 
     // d_hidden from the fused pass, beside the d_weight pass.
-    SideStream *sd = fused && c.g1 ? side_stream(st) : nullptr;
-    std::unique_lock<std::mutex> lk;
-    cudaStream_t aux = st;
-    if (sd) {
-        lk = std::unique_lock<std::mutex>(sd->mu);
-        if (sd->ready()) aux = sd->s;
-    }
-    if (aux != st) {
-        TRY(cudaEventRecord(sd->fork, st));
-        TRY(cudaStreamWaitEvent(aux, sd->fork, 0));
-    }
-    s = LOSSK_OK;
+    Fork f(fused && c.g1, st);
+    if (!f.ok) return LOSSK_DEVICE_ERROR;
     void *dh_to = fused && acc ? static_cast<void *>(b + L.off_dhacc) : c.g0;
     if (fused &&
-        launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, true, nullptr, dh_to, false, false, true, aux) !=
+        launch_seq_dh(c.grad_dtype, l, w, dhpart, L.nsplit, c.d, c.W, true, nullptr, dh_to, false, false, true, f.aux) !=
             cudaSuccess)
         s = LOSSK_DEVICE_ERROR;
     if (s == LOSSK_OK && c.g1) {
@@ -371,10 +390,7 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
                 s = LOSSK_DEVICE_ERROR;
         }
     }
-    if (aux != st) {
-        TRY(cudaEventRecord(sd->join, aux));
-        TRY(cudaStreamWaitEvent(st, sd->join, 0));
-    }
+    if (!f.join()) return LOSSK_DEVICE_ERROR;
     if (s != LOSSK_OK || !c.g0) return s;
     // d_hidden as a pass of its own: fp16, whose tiles need the log-sum-exp, and
     // bf16 where the fused pass's could not be used
@@ -393,10 +409,15 @@ int32_t run_head(const Call &c, const Layout &L, const SeqLoss &l, const SeqScra
     return LOSSK_OK;
 }
 
+bool one_launch(const Call &c, const Layout &L)
+{
+    return c.n_pairs == 0 && !(c.flags & LOSSK_SEQ_RATIO) && L.cluster > 0;
+}
+
 int32_t run_rows(const Call &c, const Layout &L, const SeqLoss &l, const SeqScratch &w)
 {
     const bool acc = (c.flags & LOSSK_ACCUMULATE_GRADS) != 0;
-    if (l.pairs == 0 && !(l.flags & LOSSK_SEQ_RATIO) && L.cluster > 0) {
+    if (one_launch(c, L)) {
         TRY(launch_policy_rows(c.dtype, l, w, c.X, c.g0, acc, L.cluster, c.st));
         return LOSSK_OK;
     }
@@ -442,6 +463,11 @@ int32_t run(const Call &c)
     l.per_token = c.per_item;
     l.log_ratio = c.log_ratio;
     l.logp = c.logp;
+    // The passes over given logits are 0 to 2 us slower with it, but for few rows in one launch.  Group
+    // passes: 203 x 264 x 5000 in fp16 86 -> 80 us a call, 512 x 1024 x 32000 in bf16 164.5 -> 163.7,
+    // 8192 x 4096 x 128256 17190 -> 17260 (pairs whose blocks came as others left).
+    l.early = c.head || (one_launch(c, L) && policy_rows_early(c.n, c.V, c.dtype, L.cluster));
+    l.early_pass = c.head && (!is16(c.dtype) || c.n * c.V <= (int64_t(1) << 25));
     TRY(launch_seq_prep(l, w, c.st));
     return c.head ? run_head(c, L, l, w) : run_rows(c, L, l, w);
 }

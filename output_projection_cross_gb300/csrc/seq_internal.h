@@ -60,6 +60,9 @@ struct SeqLoss {
     float beta, margin, smooth, nll;
     float *scalars, *per_token, *logp;      // per_token: per_pair for the preference loss
     float *log_ratio;
+    // Each kernel's blocks are set up while the kernel ahead runs, not while it ends; those of the passes
+    // over the logits.
+    bool early, early_pass;
 };
 
 // dtype: lossk_dtype.  All enqueue on `st`.
@@ -94,6 +97,7 @@ cudaError_t launch_seq_grad(int dtype, const SeqLoss &l, const SeqScratch &w, co
 // The policy loss by token in one launch, a row's logits on the chip from its statistics to
 // its gradient (grad NULL: none); blocks of a cluster that take a row, 0 where a row does not fit.
 int policy_rows_cluster(int64_t n, int64_t vocab, int dtype);
+bool policy_rows_early(int64_t n, int64_t vocab, int dtype, int cluster);
 cudaError_t launch_policy_rows(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, void *grad,
                                bool accumulate, int cluster, cudaStream_t st);
 // d_hidden of every row from the passes' split partials [nsplit][n_tok][d], indexed by
