@@ -55,7 +55,7 @@ constexpr int PREP_T = 1024, PREP_PER = 8;
 __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const SeqScratch w)
 {
     wait_for_stream();
-    if (l.early) let_next_start();
+    let_next_start();
     static_assert(PREP_PER * 32 == 256, "a lane of a warp scans eight of the counts");
     __shared__ int s_count[PREP_PER * 32];
     __shared__ int s_groups;
