@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         float in_scale = 1.f, out_scale = a.out_scale;
         if (F16 && a.coef_max) {
             const unsigned m = *a.coef_max;
-            const int e = m > 0 && m < 0x7F800000u ? min(max(14 - static_cast<int>(m >> 23) + 126, -100), 100) : 0;
+            const int e = m > 0 && m < 0x7F800000u ? min(max(14 - static_cast<int>(m >> 23) + 126, -126), 126) : 0;
             in_scale = __int_as_float((127 + e) << 23);
             out_scale = __int_as_float((127 - e) << 23);
         }
@@ -985,6 +985,14 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                     }
                     pk[i >> 1] = pack_16x2<F16>(gg[0], gg[1]);
                 }
+                }
+                // Columns past the vocabulary's end have logit 0 and weight row 0, but e^(0 - lse)
+                // is infinity where every logit of a row is low (fp16: a few units below 0), and
+                // infinity times 0 no number.
+                if (ROWS && q * 32 + 32 > ncols) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        pk[i >> 1] &= (q * 32 + i < ncols ? 0xFFFFu : 0u) | (q * 32 + i + 1 < ncols ? 0xFFFF0000u : 0u);
                 }
                 // columns q*32 .. q*32+31: sub-tile q/4, 64 bytes at column (q%4)*32
                 if (GSTG && a.g_tma) {
