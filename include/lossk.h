@@ -338,7 +338,7 @@ int32_t lossk_distill_from_logits(int64_t n_tok, int64_t vocab, int32_t dtype, c
 
 /* Synchronises `stream`, then reports and clears the workspace's device
  * error words: 580 (none), 590 (a bounded device wait timed out), 589, or what
- * a decoding call found on the device (586, 585 or 584, see there). */
+ * a decoding call or a loss of sequences found on the device (586, 585 or 584, see there). */
 int32_t lossk_device_status(void *workspace, int64_t workspace_bytes, lossk_stream_t stream);
 
 /* ---- vocabulary-parallel cross-entropy ---------------------------------------
@@ -709,9 +709,10 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
  *   grad_logits dtype, or NULL to skip; it may be logits itself.
  * Every row of a gradient is written: rows that do not count, and those behind
  * the last sequence, become 0.  A token on whose logp the loss does not depend
- * (a clipped one without a KL term) has a zero gradient whatever its logits hold.  A
- * vocabulary entry at -infinity has probability 0; a row of nothing else has
- * logp -infinity and a zero gradient.
+ * (a clipped one without a KL term) has a zero gradient.  A vocabulary entry at
+ * -infinity has probability 0; a row of nothing else has logp -infinity and a zero
+ * gradient.  NaN or +infinity among the logits of a row that counts makes its logp NaN,
+ * and what depends on it.
  * flags: LOSSK_ACCUMULATE_GRADS adds to the gradients (float d_hidden and d_weight,
  * or grad_logits; with 16-bit d_hidden or d_weight: 592), LOSSK_REDUCE_SUM sums
  * where the formulas take means, and the flags below.
@@ -719,7 +720,8 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
  * are queued and can be recorded into a CUDA graph.  So what is wrong in device
  * data, a target of a counted row outside [0, vocab) or a wrong `first`, leaves
  * every output untouched and 586 in the workspace's header, which
- * lossk_device_status reads and clears.  The workspace's first 256 bytes must be
+ * lossk_device_status reads and clears; until it has, calls on that workspace do
+ * nothing.  The workspace's first 256 bytes must be
  * zero before its first use.  Calls on one workspace must not overlap in time;
  * nor must replays of graphs that were recorded with it.
  * Checks: 581, 583, 584, 582, 591, 585, 588, 592 as above; a required pointer that is
@@ -762,7 +764,7 @@ int64_t lossk_sequence_workspace_bytes(int32_t kind, int64_t n_tok, int64_t d_mo
  *   scalars_out    float[4], required: {total, sum w P, sum w K, sum w [clipped]}
  *   per_token_out  float[n_tok] or NULL: L_t, 0 where a row does not count
  * clip_low in [0, 1], clip_high >= 0, kl_weight >= 0 (> 0 needs ref_logp: 582),
- * temperature in [1e-30, 1e30], all finite (585). */
+ * temperature in [1e-30, 1e30], all finite as floats (585). */
 int32_t lossk_policy_fwd_bwd(int64_t n_tok, int64_t d_model, int64_t vocab, int64_t n_seq, int32_t dtype,
                              const void *hidden, int64_t hidden_len, const void *weight, int64_t weight_len,
                              const int64_t *targets, int64_t targets_len, const uint8_t *loss_mask,
@@ -802,7 +804,7 @@ int32_t lossk_policy_from_logits(int64_t n_tok, int64_t vocab, int64_t n_seq, in
  *                  share of the pairs with u > 0 (LOSSK_REDUCE_SUM: their number)}
  *   per_pair_out   float[n_pairs] or NULL: L
  *   log_ratio_out  float[2 n_pairs] or NULL: D_s
- * beta > 0, margin, label_smoothing in [0, 1], nll_weight >= 0, all finite (585);
+ * beta >= 1e-30, margin, label_smoothing in [0, 1], nll_weight >= 0, all finite as floats (585);
  * margin and label_smoothing belong to LOSSK_PREF_SIGMOID and must be 0 otherwise
  * (585). */
 int32_t lossk_preference_fwd_bwd(int64_t n_tok, int64_t d_model, int64_t vocab, int64_t n_pairs, int32_t dtype,

@@ -8,6 +8,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <limits>
 #include <mutex>
 
 using namespace lossk;
@@ -152,10 +153,11 @@ struct Call {
     cudaStream_t st;
 };
 
+// Finite, as the floats that the kernels take too.
 bool finite(std::initializer_list<double> v)
 {
     for (double x : v)
-        if (!std::isfinite(x)) return false;
+        if (!(std::fabs(x) <= std::numeric_limits<float>::max())) return false;
     return true;
 }
 
@@ -186,7 +188,7 @@ int32_t check(const Call &c, Layout *L)
         return LOSSK_UNALIGNED;
     if (!finite({c.grad_scale})) return LOSSK_NON_FINITE_SCALAR;
     if (pref) {
-        if (!finite({c.beta, c.margin, c.smooth, c.nll}) || c.beta <= 0.0 || c.smooth < 0.0 || c.smooth > 1.0 ||
+        if (!finite({c.beta, c.margin, c.smooth, c.nll}) || c.beta < 1e-30 || c.smooth < 0.0 || c.smooth > 1.0 ||
             c.nll < 0.0)
             return LOSSK_NON_FINITE_SCALAR;
         if (c.objective < LOSSK_PREF_SIGMOID || c.objective > LOSSK_PREF_SQUARED) return LOSSK_UNKNOWN_OBJECTIVE;

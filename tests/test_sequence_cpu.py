@@ -79,7 +79,7 @@ def test_refusals_of_the_policy_loss(f):
                 dict(flags=4), dict(flags=8), dict(flags=16), dict(n_seq=3, first=P, fl=4, flags=16, al=2)):
         assert f(**bad) == 582, bad
     for bad in (dict(low=-0.1), dict(low=1.1), dict(high=-0.1), dict(kl=-1.0), dict(T=0.0), dict(T=-1.0), dict(T=NAN),
-                dict(low=NAN), dict(high=INF), dict(kl=INF), dict(T=INF), dict(T=1e-31), dict(T=1e31)):
+                dict(low=NAN), dict(high=INF), dict(kl=INF), dict(T=INF), dict(T=1e-31), dict(T=1e31), dict(high=1e39), dict(kl=1e39), dict(gs=1e39)):
         assert f(**bad) == 585, bad
     assert f(flags=32) == 592
 
@@ -89,7 +89,7 @@ def test_refusals_of_the_preference_loss(f):
     assert f(pairs=0) == f(pairs=-3) == 581 and f(pairs=(1 << 24) + 1) == 583
     assert f(first=None) == f(fl=4) == 582
     for bad in (dict(beta=0.0), dict(beta=-1.0), dict(beta=NAN), dict(margin=INF), dict(smooth=-0.1), dict(smooth=1.1),
-                dict(nll=-1.0), dict(nll=NAN), dict(obj=1, margin=0.1), dict(obj=2, smooth=0.1)):
+                dict(nll=-1.0), dict(nll=NAN), dict(beta=1e-31), dict(beta=1e39), dict(margin=1e39), dict(nll=1e39), dict(obj=1, margin=0.1), dict(obj=2, smooth=0.1)):
         assert f(**bad) == 585, bad
     assert f(obj=3) == f(obj=-1) == 588
     for flag in (4, 8, 16):
