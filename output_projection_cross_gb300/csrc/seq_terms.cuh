@@ -1,5 +1,5 @@
 // seq_terms.cuh -- the sequence losses' arithmetic per row, sequence and pair, and
-// their scalars: device code that the coefficient kernel (k_seq.cu) and the walk over
+// their scalars: device code that the coefficient kernel (k_seq.cu) and the passes over
 // given logits (k_rows.cu) share.
 #pragma once
 #include "../../include/lossk.h"
