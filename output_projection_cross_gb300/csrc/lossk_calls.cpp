@@ -1,4 +1,4 @@
-// lossk_calls.cpp -- the decoding calls as a CPython module: arguments by
+// lossk_calls.cpp -- the decoding calls and the losses of sequences as a CPython module: arguments by
 // position, in the order of lossk.h, None for NULL, the status returned.  And
 // spans() and device(), the checks and addresses of the tensors that such a call
 // takes.
@@ -22,7 +22,7 @@ namespace {
 
 #define LOSSK_CALLS(X)                                                                                                \
     X(lossk_beam_select) X(lossk_beam_gather) X(lossk_cache_fork) X(lossk_cache_reserve) X(lossk_cache_free)          \
-    X(lossk_cache_compact) X(lossk_cache_copy) X(lossk_cache_write) X(lossk_paged_attn)          \
+    X(lossk_cache_compact) X(lossk_cache_copy) X(lossk_cache_write) X(lossk_paged_attn)                          \
     X(lossk_policy_fwd_bwd) X(lossk_policy_from_logits) X(lossk_preference_fwd_bwd) X(lossk_preference_from_logits)
 
 enum Call {

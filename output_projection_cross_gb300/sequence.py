@@ -16,8 +16,8 @@ from __future__ import annotations
 import torch
 
 from .decode import _calls, _NotBuilt, _on_gpu, _raw_stream, _stream_of
-from .lossk import (ACCUMULATE_GRADS, F32, LosskError, _check, _contig, _dtype_code, _len, _on_its_stream, _ptr, _stream,
-                    lib, lossk_dims_check)
+from .lossk import (ACCUMULATE_GRADS, F32, LosskError, _check, _contig, _dtype_code, _on_its_stream, _stream, lib,
+                    lossk_dims_check)
 
 KIND_SEQUENCE_HEAD, KIND_SEQUENCE_LOGITS = 0, 1
 SEQ_RATIO, SEQ_MEAN, SEQ_ADVANTAGES, LENGTH_MEAN = 4, 8, 16, 32
@@ -29,6 +29,11 @@ __all__ = ["KIND_SEQUENCE_HEAD", "KIND_SEQUENCE_LOGITS", "SEQ_RATIO", "SEQ_MEAN"
 
 # through the CPython module where there is one (ctypes takes 3 us for the arguments of one such call)
 _lib = lib if isinstance(_calls, _NotBuilt) else _calls
+
+# the tensors of one type that a call looks at together
+_HEAD, _HEAD_GRADS, _LOGITS, _LOGITS_GRADS = ("hidden", "weight"), ("d_hidden", "d_weight"), ("logits",), ("grad_logits",)
+_POLICY = ("advantages", "old_logp", "ref_logp", "scalars_out", "per_token_out", "logp_out")
+_PREFERENCE = ("ref_logp", "scalars_out", "per_pair_out", "log_ratio_out", "logp_out")
 
 
 def lossk_sequence_workspace_bytes(kind: int, n_tok: int, d_model: int, vocab: int, n_seq: int, dtype: int) -> int:
@@ -44,21 +49,31 @@ def sequence_workspace(kind: int, n_tok: int, d_model: int, vocab: int, n_seq: i
     return torch.zeros(nb, dtype=torch.uint8, device=device or "cuda")
 
 
-def _given(stream, tensors):
-    """The stream's handle, once every tensor is contiguous, of its type and on the current device.
-
-    tensors: (name, tensor, type or None, elements it must hold or None)."""
-    for name, t, dtype, n in tensors:
-        if t is None:
-            continue
-        if isinstance(_calls, _NotBuilt):
+def _spans(dtype, names, *tensors):
+    """(address, elements) of each contiguous tensor of that type (None: any), flat; a tensor left out is 0, 0."""
+    if dtype is not None and not isinstance(_calls, _NotBuilt):
+        r = _calls.spans(dtype, *tensors)
+        if r is not None:
+            return r
+    out = []
+    for name, t in zip(names, tensors):
+        if isinstance(_calls, _NotBuilt) and t is not None:
             _contig(t, name)
-        _on_gpu(t, name, dtype)
-        if n is not None and t.numel() < n:
+        _on_gpu(t, name, dtype)                   # (whether it is on the GPU is _handle's to say)
+        out += (0, 0) if t is None else (t.data_ptr(), t.numel())
+    return out
+
+
+def _handle(stream, *tensors):
+    """The stream's handle, once all tensors are on the current device."""
+    return _stream(stream) if isinstance(_calls, _NotBuilt) else _stream_of(stream, *tensors)
+
+
+def _holds(spans, *wanted):
+    """wanted: (position among the spans, name, elements that it must hold unless it is left out)."""
+    for i, name, n in wanted:
+        if spans[2 * i] and spans[2 * i + 1] < n:
             raise ValueError(f"{name} must hold {n} elements")
-    if isinstance(_calls, _NotBuilt):
-        return _stream(stream)
-    return _stream_of(stream, *(t for _, t, _, _ in tensors))
 
 
 def _new(t, n, device):
@@ -91,7 +106,7 @@ def _head_grads(hidden, weight, flags, grad_dtype, d_hidden, d_weight, want_d_hi
         if want and t.shape != like.shape:
             raise ValueError(f"{name} must be of shape {tuple(like.shape)}")
         out.append(t if want else None)
-    return out[0], out[1], _dtype_code_of(dtype)
+    return out[0], out[1], dtype
 
 
 def _dtype_code_of(dtype):
@@ -122,25 +137,29 @@ def _no_stream(f):
 
 # ---- the policy loss ------------------------------------------------------------------
 
-def _policy(fn, name, given, n, d, V, n_grad, targets, advantages, old_logp, ref_logp, first, loss_mask, scalars, flags,
-            scalars_out, per_token_out, logp_out, grads, grad_tail, kind, dt, ws, stream):
+def _policy(fn, name, given, names, sizes, kind, targets, advantages, old_logp, ref_logp, first, loss_mask, scalars, flags,
+            scalars_out, per_token_out, logp_out, grads, grad_names, grad_dtype, ws, stream):
+    """sizes: n_tok, d_model, vocab, type; given: what the logits come from; grads: what takes their gradient."""
+    n, d, V, dt = sizes
     dev = targets.device
     scalars_out, per_token_out, logp_out = _new(scalars_out, 4, dev), _new(per_token_out, n, dev), _new(logp_out, n, dev)
     n_seq = first.numel() - 1 if first is not None else 0
     if ws is None:
         ws = sequence_workspace(kind, n, d, V, max(n_seq, 0), dt, dev)
-    f32 = torch.float32
-    handle = _given(stream, (*given, ("targets", targets, torch.int64, n), ("advantages", advantages, f32, None),
-                             ("old_logp", old_logp, f32, None), ("ref_logp", ref_logp, f32, None),
-                             ("first", first, torch.int32, None), ("loss_mask", loss_mask, torch.uint8, n),
-                             ("scalars_out", scalars_out, f32, 4), ("per_token_out", per_token_out, f32, n),
-                             ("logp_out", logp_out, f32, n), *grads, ("ws", ws, torch.uint8, None)))
-    sizes = (n, d, V, n_seq, dt) if kind == KIND_SEQUENCE_HEAD else (n, V, n_seq, dt)
-    tensors = [x for _, t, _, _ in given for x in (_ptr(t), _len(t))]
-    _check(fn(*sizes, *tensors, _ptr(targets), _len(targets), _ptr(loss_mask), _ptr(first), _len(first),
-              _ptr(advantages), _len(advantages), _ptr(old_logp), _len(old_logp), _ptr(ref_logp), _len(ref_logp),
-              *scalars, flags, _ptr(scalars_out), _ptr(per_token_out), _ptr(logp_out), *grad_tail, _ptr(ws), ws.numel(),
-              handle), name)
+    x = _spans(given[0].dtype, names, *given)
+    y = _spans(torch.int64, ("targets",), targets)
+    f = _spans(torch.float32, _POLICY, advantages, old_logp, ref_logp, scalars_out, per_token_out, logp_out)
+    s = _spans(torch.int32, ("first",), first)
+    b = _spans(torch.uint8, ("loss_mask", "ws"), loss_mask, ws)
+    g = _spans(grad_dtype, grad_names, *grads)
+    _holds(y, (0, "targets", n))
+    _holds(b, (0, "loss_mask", n))
+    _holds(f, (3, "scalars_out", 4), (4, "per_token_out", n), (5, "logp_out", n))
+    handle = _handle(stream, *given, targets, advantages, old_logp, ref_logp, scalars_out, per_token_out, logp_out, first,
+                     loss_mask, ws, *grads)
+    head = kind == KIND_SEQUENCE_HEAD
+    _check(fn(*((n, d, V, n_seq, dt) if head else (n, V, n_seq, dt)), *x, *y, b[0], *s, *f[:6], *scalars, flags, f[6], f[8],
+              f[10], *((_dtype_code_of(grad_dtype), g[0], g[2]) if head else g), b[2], b[3], handle), name)
     return {"scalars": scalars_out, "per_token": per_token_out, "logp": logp_out}
 
 
@@ -157,14 +176,12 @@ def lossk_policy_fwd_bwd(hidden, weight, targets, advantages, old_logp=None, ref
     False it is the forward pass alone (the log-probabilities of a sampling policy or a reference model).
     Returns scalars (total, policy, KL, clipped share), per_token, logp, d_hidden, d_weight."""
     n, d, V, dt = _head(hidden, weight)
-    d_hidden, d_weight, code = _head_grads(hidden, weight, flags, grad_dtype, d_hidden, d_weight, want_d_hidden,
-                                           want_d_weight)
-    out = _policy(_lib.lossk_policy_fwd_bwd, "lossk_policy_fwd_bwd",
-                  (("hidden", hidden, None, None), ("weight", weight, None, None)), n, d, V, None, targets, advantages,
-                  old_logp, ref_logp, first, loss_mask, (clip_low, clip_high, kl_weight, temperature, grad_scale), flags,
-                  scalars_out, per_token_out, logp_out,
-                  (("d_hidden", d_hidden, None, None), ("d_weight", d_weight, None, None)),
-                  (code, _ptr(d_hidden), _ptr(d_weight)), KIND_SEQUENCE_HEAD, dt, ws, stream)
+    d_hidden, d_weight, grad_dtype = _head_grads(hidden, weight, flags, grad_dtype, d_hidden, d_weight, want_d_hidden,
+                                                 want_d_weight)
+    out = _policy(_lib.lossk_policy_fwd_bwd, "lossk_policy_fwd_bwd", (hidden, weight), _HEAD, (n, d, V, dt),
+                  KIND_SEQUENCE_HEAD, targets, advantages, old_logp, ref_logp, first, loss_mask,
+                  (clip_low, clip_high, kl_weight, temperature, grad_scale), flags, scalars_out, per_token_out, logp_out,
+                  (d_hidden, d_weight), _HEAD_GRADS, grad_dtype, ws, stream)
     out["d_hidden"], out["d_weight"] = d_hidden, d_weight
     return out
 
@@ -178,19 +195,19 @@ def lossk_policy_from_logits(logits, targets, advantages, old_logp=None, ref_log
     n, V = logits.shape
     dt = _dtype_code(logits)
     grad_logits = _logits_grad(logits, flags, grad_logits, want_grad)
-    out = _policy(_lib.lossk_policy_from_logits, "lossk_policy_from_logits", (("logits", logits, None, None),), n, 1, V,
-                  None, targets, advantages, old_logp, ref_logp, first, loss_mask,
+    out = _policy(_lib.lossk_policy_from_logits, "lossk_policy_from_logits", (logits,), _LOGITS, (n, 1, V, dt),
+                  KIND_SEQUENCE_LOGITS, targets, advantages, old_logp, ref_logp, first, loss_mask,
                   (clip_low, clip_high, kl_weight, temperature, grad_scale), flags, scalars_out, per_token_out, logp_out,
-                  (("grad_logits", grad_logits, logits.dtype, None),), (_ptr(grad_logits), _len(grad_logits)),
-                  KIND_SEQUENCE_LOGITS, dt, ws, stream)
+                  (grad_logits,), _LOGITS_GRADS, logits.dtype, ws, stream)
     out["grad_logits"] = grad_logits
     return out
 
 
 # ---- the preference loss ----------------------------------------------------------------
 
-def _preference(fn, name, given, n, d, V, targets, first, ref_logp, loss_mask, objective, scalars, flags, scalars_out,
-                per_pair_out, log_ratio_out, logp_out, grads, grad_tail, kind, dt, ws, stream):
+def _preference(fn, name, given, names, sizes, kind, targets, first, ref_logp, loss_mask, objective, scalars, flags,
+                scalars_out, per_pair_out, log_ratio_out, logp_out, grads, grad_names, grad_dtype, ws, stream):
+    n, d, V, dt = sizes
     dev = targets.device
     if first.numel() % 2 != 1:
         raise ValueError("first must hold 2 * n_pairs + 1 elements")
@@ -199,18 +216,21 @@ def _preference(fn, name, given, n, d, V, targets, first, ref_logp, loss_mask, o
     log_ratio_out, logp_out = _new(log_ratio_out, 2 * pairs, dev), _new(logp_out, n, dev)
     if ws is None:
         ws = sequence_workspace(kind, n, d, V, 2 * pairs, dt, dev)
-    f32 = torch.float32
-    handle = _given(stream, (*given, ("targets", targets, torch.int64, n), ("first", first, torch.int32, None),
-                             ("ref_logp", ref_logp, f32, None), ("loss_mask", loss_mask, torch.uint8, n),
-                             ("scalars_out", scalars_out, f32, 4), ("per_pair_out", per_pair_out, f32, pairs),
-                             ("log_ratio_out", log_ratio_out, f32, 2 * pairs), ("logp_out", logp_out, f32, n), *grads,
-                             ("ws", ws, torch.uint8, None)))
-    sizes = (n, d, V, pairs, dt) if kind == KIND_SEQUENCE_HEAD else (n, V, pairs, dt)
-    tensors = [x for _, t, _, _ in given for x in (_ptr(t), _len(t))]
-    _check(fn(*sizes, *tensors, _ptr(targets), _len(targets), _ptr(loss_mask), _ptr(first), _len(first),
-              _ptr(ref_logp), _len(ref_logp), OBJECTIVES[objective] if isinstance(objective, str) else int(objective),
-              *scalars, flags, _ptr(scalars_out), _ptr(per_pair_out), _ptr(log_ratio_out), _ptr(logp_out), *grad_tail,
-              _ptr(ws), ws.numel(), handle), name)
+    x = _spans(given[0].dtype, names, *given)
+    y = _spans(torch.int64, ("targets",), targets)
+    f = _spans(torch.float32, _PREFERENCE, ref_logp, scalars_out, per_pair_out, log_ratio_out, logp_out)
+    s = _spans(torch.int32, ("first",), first)
+    b = _spans(torch.uint8, ("loss_mask", "ws"), loss_mask, ws)
+    g = _spans(grad_dtype, grad_names, *grads)
+    _holds(y, (0, "targets", n))
+    _holds(b, (0, "loss_mask", n))
+    _holds(f, (1, "scalars_out", 4), (2, "per_pair_out", pairs), (3, "log_ratio_out", 2 * pairs), (4, "logp_out", n))
+    handle = _handle(stream, *given, targets, first, ref_logp, scalars_out, per_pair_out, log_ratio_out, logp_out, loss_mask,
+                     ws, *grads)
+    head = kind == KIND_SEQUENCE_HEAD
+    _check(fn(*((n, d, V, pairs, dt) if head else (n, V, pairs, dt)), *x, *y, b[0], *s, f[0], f[1],
+              OBJECTIVES[objective] if isinstance(objective, str) else int(objective), *scalars, flags, f[2], f[4], f[6],
+              f[8], *((_dtype_code_of(grad_dtype), g[0], g[2]) if head else g), b[2], b[3], handle), name)
     return {"scalars": scalars_out, "per_pair": per_pair_out, "log_ratio": log_ratio_out, "logp": logp_out}
 
 
@@ -226,14 +246,12 @@ def lossk_preference_fwd_bwd(hidden, weight, targets, first, ref_logp=None, loss
     ACCUMULATE_GRADS, REDUCE_SUM, LENGTH_MEAN.  Returns scalars (total, preference, -logp of the chosen tokens,
     share of pairs in order), per_pair, log_ratio (per sequence), logp, d_hidden, d_weight."""
     n, d, V, dt = _head(hidden, weight)
-    d_hidden, d_weight, code = _head_grads(hidden, weight, flags, grad_dtype, d_hidden, d_weight, want_d_hidden,
-                                           want_d_weight)
-    out = _preference(_lib.lossk_preference_fwd_bwd, "lossk_preference_fwd_bwd",
-                      (("hidden", hidden, None, None), ("weight", weight, None, None)), n, d, V, targets, first, ref_logp,
-                      loss_mask, objective, (beta, margin, label_smoothing, nll_weight, grad_scale), flags, scalars_out,
-                      per_pair_out, log_ratio_out, logp_out,
-                      (("d_hidden", d_hidden, None, None), ("d_weight", d_weight, None, None)),
-                      (code, _ptr(d_hidden), _ptr(d_weight)), KIND_SEQUENCE_HEAD, dt, ws, stream)
+    d_hidden, d_weight, grad_dtype = _head_grads(hidden, weight, flags, grad_dtype, d_hidden, d_weight, want_d_hidden,
+                                                 want_d_weight)
+    out = _preference(_lib.lossk_preference_fwd_bwd, "lossk_preference_fwd_bwd", (hidden, weight), _HEAD, (n, d, V, dt),
+                      KIND_SEQUENCE_HEAD, targets, first, ref_logp, loss_mask, objective,
+                      (beta, margin, label_smoothing, nll_weight, grad_scale), flags, scalars_out, per_pair_out,
+                      log_ratio_out, logp_out, (d_hidden, d_weight), _HEAD_GRADS, grad_dtype, ws, stream)
     out["d_hidden"], out["d_weight"] = d_hidden, d_weight
     return out
 
@@ -247,10 +265,9 @@ def lossk_preference_from_logits(logits, targets, first, ref_logp=None, loss_mas
     n, V = logits.shape
     dt = _dtype_code(logits)
     grad_logits = _logits_grad(logits, flags, grad_logits, want_grad)
-    out = _preference(_lib.lossk_preference_from_logits, "lossk_preference_from_logits", (("logits", logits, None, None),),
-                      n, 1, V, targets, first, ref_logp, loss_mask, objective,
+    out = _preference(_lib.lossk_preference_from_logits, "lossk_preference_from_logits", (logits,), _LOGITS, (n, 1, V, dt),
+                      KIND_SEQUENCE_LOGITS, targets, first, ref_logp, loss_mask, objective,
                       (beta, margin, label_smoothing, nll_weight, grad_scale), flags, scalars_out, per_pair_out,
-                      log_ratio_out, logp_out, (("grad_logits", grad_logits, logits.dtype, None),),
-                      (_ptr(grad_logits), _len(grad_logits)), KIND_SEQUENCE_LOGITS, dt, ws, stream)
+                      log_ratio_out, logp_out, (grad_logits,), _LOGITS_GRADS, logits.dtype, ws, stream)
     out["grad_logits"] = grad_logits
     return out
