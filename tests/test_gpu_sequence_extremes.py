@@ -146,3 +146,62 @@ def test_a_run_of_them(dtype):
     out = run_preference(c, ws=ws, **of(c))
     check_preference(c, out)
     assert L.lossk_device_status(ws) == 580
+
+
+@pytest.mark.parametrize("kw", [dict(n=37, V=901, d=72, dtype="bf16"), dict(n=37, V=901, d=72, dtype="f16"),
+                                dict(n=37, V=901, d=19, dtype="f32"), dict(n=300, V=2000, d=264, dtype="bf16"),
+                                dict(n=37, V=1001, dtype="bf16"), dict(n=37, V=9001, dtype="f16"), dict(n=5, V=40003, dtype="f32"),
+                                dict(n=2, V=120001, dtype="bf16"), dict(n=2, V=500003, dtype="bf16")], ids=str)
+@pytest.mark.parametrize("grad", ["same", "float"])
+def test_nothing_is_written_beside_the_outputs(kw, grad):
+    """Each output and the workspace in the middle of a larger buffer; the workspace but its header begins as 0xFF."""
+    c = Case(seqs=4 if kw["n"] > 4 else 2, masked=0.2 if kw["n"] > 4 else 0.0, **kw)
+    if not c.d and grad == "float":
+        pytest.skip("grad_logits is of the logits' type")
+    n, V, d, seqs = c.n, c.V, c.d, len(c.first) - 1
+    kind = 0 if c.d else 1
+    gt = torch.float32 if grad == "float" else DT[c.dtype]
+    kept = []
+
+    def inside(shape, dtype):
+        size = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+        whole = torch.full((4096 + size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        kept.append((whole, size))
+        return whole[4096:4096 + size].view(dtype).view(shape)
+
+    f32 = torch.float32
+    ws = inside((L.lossk_sequence_workspace_bytes(kind, n, max(d, 1), V, seqs, CODE[c.dtype]),), torch.uint8)
+    ws[256:] = 0xFF
+    ws[:256] = 0
+    outs = dict(scalars_out=inside((4,), f32), logp_out=inside((n,), f32), ws=ws)
+    if c.d:
+        outs.update(d_hidden=inside((n, d), gt), d_weight=inside((V, d), gt))
+    else:
+        outs.update(grad_logits=inside((n, V), gt))
+    kwargs = dict(grad="float") if c.d and grad == "float" else {}
+    check_policy(c, run_policy(c, kl=0.1, per_token_out=inside((n,), f32), **outs), kl=0.1, **kwargs)
+    ws[256:] = 0xFF
+    check_policy(c, run_policy(c, L.SEQ_RATIO, low=0.013, high=0.017, **outs), L.SEQ_RATIO, low=0.013, high=0.017, **kwargs)
+    ws[256:] = 0xFF
+    check_preference(c, run_preference(c, per_pair_out=inside((seqs // 2,), f32), log_ratio_out=inside((seqs,), f32), **outs),
+                     **kwargs)
+    for whole, size in kept:
+        assert (whole[:4096] == 0xA5).all() and (whole[4096 + size:] == 0xA5).all()
+
+
+def test_graphs_that_share_a_workspace():
+    """Two graphs recorded with one workspace, replayed in turn on one stream."""
+    a, b = Case(n=70, V=900, d=136, dtype="bf16", seqs=4, seed=1), Case(n=60, V=900, d=136, dtype="bf16", seqs=4, seed=2)
+    want = run_policy(a, **of(a)), run_preference(b, **of(b))
+    ws = L.sequence_workspace(0, 70, 136, 900, 4, CODE["bf16"])
+    graphs, got, stream = [], [], torch.cuda.Stream()
+    for run, c in ((run_policy, a), (run_preference, b)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            got.append(run(c, ws=ws, **of(c)))
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    same(want[0], got[0])
+    same(want[1], got[1])
