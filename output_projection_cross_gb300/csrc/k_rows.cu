@@ -546,6 +546,8 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
         fence_mbarrier_init();
     }
     __syncthreads();
+    // (waited for beside the row's copies, ahead of the first store into another block's memory)
+    if (cluster > 1) cluster_arrive_started();
     const int t = blockIdx.x / cluster, rank = blockIdx.x - t * cluster, tid = threadIdx.x;
     // Early: all that the copies and the statistics read is the call's inputs, which were there before
     // the kernel ahead began (let_next_start), and which row counts follows from them.
@@ -553,7 +555,10 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
     if constexpr (!EARLY) {
         wait_for_stream();
         on = w.slot[t] >= 0;                   // (asked for beside the refusal)
-        if (seq_refused(w.hdr)) return;
+        if (seq_refused(w.hdr)) {
+            if (cluster > 1) cluster_wait_started();
+            return;
+        }
     } else {
         on = row_counts(l, t);
     }
@@ -600,6 +605,8 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
         }
         block_stats<POLICY_T>(m, z, sm, sz);
         if (cluster > 1) {
+            __syncwarp();
+            cluster_wait_started();
             if (tid == 0)
                 for (int q = 0; q < cluster; ++q)
                     st_cluster_f2(mapa_shared(smem_u32(&s_part[rank]), q), make_float2(m, z));
@@ -613,6 +620,8 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
                     z += m > -INFINITY ? s_part[q].y * ex2_approx(s_part[q].x - m) : s_part[q].y;
             }
         }
+    } else if (cluster > 1) {
+        cluster_wait_started();                // (a row counts in all blocks of its cluster, or in none)
     }
     if constexpr (EARLY) {
         wait_for_stream();

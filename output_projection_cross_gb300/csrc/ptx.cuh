@@ -500,6 +500,18 @@ __device__ __forceinline__ void cluster_sync()
                      : "memory");
 }
 
+// The same barrier in two steps, where all that it has to say is that every CTA of the cluster has
+// started and its shared memory may be written (it orders no data): arrive first thing, wait just
+// before the first access to another CTA's shared memory.  Every thread that arrives waits.
+__device__ __forceinline__ void cluster_arrive_started()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // ---- tcgen05 on CTA pairs (cta_group::2) -------------------------------------------
 // With cta_group::2 the two CTAs of an even/odd pair in a cluster act as one
 // MMA unit: A's M rows are split 128/128 between them, B's N columns half and
