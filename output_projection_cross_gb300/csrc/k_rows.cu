@@ -118,9 +118,11 @@ template <typename T> __device__ __forceinline__ float vec_max(const uint4 &v)
     }
 }
 
-// One vector's terms (f its values, lm the largest) into a running (max m, sum z) of x = k2 s in
-// log2 units: one rescale if the maximum rose, then exponentials that do not depend on one
-// another, their arguments and sums two an instruction.
+// One vector's terms (f its values, lm the largest) into a running (max m, sum z of 2^(k2 (f - m))):
+// one rescale if the maximum rose, then exponentials that do not depend on one another, their
+// arguments and sums two an instruction.  m is one of the logits itself, and what is scaled is the
+// distance to it: k2 f - k2 m would end where k2 f does (a mask of bf16's or fp32's lowest value, a
+// temperature far below 1), and there be no number.
 template <int N> __device__ __forceinline__ void add_vec(float &m, float &z, const float (&f)[N], float lm, float k2)
 {
     if (lm == -INFINITY) {
@@ -130,9 +132,8 @@ template <int N> __device__ __forceinline__ void add_vec(float &m, float &z, con
             if (f[i] != f[i]) z = f[i];
         return;
     }
-    lm *= k2;
     if (lm > m) {
-        z *= ex2_approx(m - lm);
+        z *= ex2_approx((m - lm) * k2);
         m = lm;
     }
     const uint64_t kk = pack2(k2, k2), mm = pack2(-m, -m);
@@ -140,7 +141,7 @@ template <int N> __device__ __forceinline__ void add_vec(float &m, float &z, con
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
         float a, b;
-        unpack2(fma2(pack2(f[i], f[i + 1]), kk, mm), a, b);
+        unpack2(mul2(add2(pack2(f[i], f[i + 1]), mm), kk), a, b);
         const uint64_t e = pack2(ex2_approx(a), ex2_approx(b));
         s = i ? add2(s, e) : e;
     }
@@ -160,7 +161,8 @@ template <int N> __device__ __forceinline__ void add_part(float &m, float &z, co
 
 // The block's (max, sum) from its threads': its maximum, one rescale of each thread's sum, then
 // plain sums in a fixed order.  Valid in thread 0.
-template <int T> __device__ __forceinline__ void block_stats(float &m, float &z, float (&sm)[T / 32], float (&sz)[T / 32])
+template <int T>
+__device__ __forceinline__ void block_stats(float &m, float &z, float k2, float (&sm)[T / 32], float (&sz)[T / 32])
 {
     float M = m;
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -168,7 +170,7 @@ template <int T> __device__ __forceinline__ void block_stats(float &m, float &z,
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < T / 32; ++i) M = fmaxf(M, sm[i]);
-    if (M > -INFINITY) z *= ex2_approx(m - M);         // (a NaN of a row of nothing else stays)
+    if (M > -INFINITY) z *= ex2_approx((m - M) * k2);  // (a NaN of a row of nothing else stays)
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if ((threadIdx.x & 31) == 0) sz[threadIdx.x >> 5] = z;
     __syncthreads();
@@ -177,23 +179,22 @@ template <int T> __device__ __forceinline__ void block_stats(float &m, float &z,
         for (int i = 1; i < T / 32; ++i) z += sz[i];
 }
 
-// logp and lse2 from a row's (max, sum) and its target's logit y.  exps: exponentials that all
+// logp from a row's (max, sum) and its target's logit y.  exps: exponentials that all
 // but a maximum's own terms have gone through.
-__device__ __forceinline__ void row_logp(const SeqLoss &l, float M, float z, float y, int exps, float &lp, float &lse2)
+__device__ __forceinline__ float row_logp(const SeqLoss &l, float M, float z, float y, int exps)
 {
-    const double s = static_cast<double>(M) + static_cast<double>(log2f(z));
-    lse2 = static_cast<float>(s);
-    lp = y == -INFINITY && z == z
-             ? y
-             : static_cast<float>((static_cast<double>(y) * static_cast<double>(l.k2) - s) * LN2 - exps * EX2_LOW);
+    const double gap = (static_cast<double>(y) - static_cast<double>(M)) * static_cast<double>(l.k2);
+    return y == -INFINITY && z == z
+               ? y
+               : static_cast<float>((gap - static_cast<double>(log2f(z))) * LN2 - exps * EX2_LOW);
 }
 
 // A warp's (max, sum) from its lanes', as block_stats; valid in every lane.
-__device__ __forceinline__ void warp_stats(float &m, float &z)
+__device__ __forceinline__ void warp_stats(float &m, float &z, float k2)
 {
     float M = m;
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (M > -INFINITY) z *= ex2_approx(m - M);
+    if (M > -INFINITY) z *= ex2_approx((m - M) * k2);
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     m = M;
 }
@@ -226,14 +227,15 @@ __device__ __forceinline__ void scan_row(const RowVecs<T> &r, int v0, int v1, in
     }
 }
 
-// A vector of the gradient from its logits f: a (softmax - onehot), the row's parameters P.
+// A vector of the gradient from its logits f: a (softmax - onehot), the row's parameters P (its largest
+// logit as the reference, so that a common offset of the logits costs no bits).
 template <int N> __device__ __forceinline__ void grad_vec(float (&f)[N], const float4 &P, float k2, int e)
 {
     const uint64_t kk = pack2(k2, k2), mm = pack2(-P.x, -P.x), pp = pack2(P.y, P.y);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
         float a, b;
-        unpack2(fma2(pack2(f[i], f[i + 1]), kk, mm), a, b);
+        unpack2(mul2(add2(pack2(f[i], f[i + 1]), mm), kk), a, b);
         unpack2(mul2(pp, pack2(ex2_approx(a), ex2_approx(b))), f[i], f[i + 1]);
     }
     const int dy = __float_as_int(P.w) - e;                // the one-hot term, in one vector of the row
@@ -262,7 +264,7 @@ __device__ __forceinline__ void write_row(const RowVecs<T> &r, T *g, int v0, int
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = j0 + u * TEAM + tid, e = r.at(j);
-            if (j < v1 && P.y != 0.f && r.whole(e)) {
+            if (j < v1 && P.z != 0.f && r.whole(e)) {
                 v[u] = __ldcs(reinterpret_cast<const uint4 *>(r.row + e));
                 if (ADD) old[ADD ? u : 0] = __ldcs(reinterpret_cast<const uint4 *>(g + e));
             }
@@ -273,7 +275,7 @@ __device__ __forceinline__ void write_row(const RowVecs<T> &r, T *g, int v0, int
             if (j >= v1) continue;
             float f[N] = {};
             const bool whole = r.whole(e);
-            if (P.y != 0.f) {
+            if (P.z != 0.f) {
                 if (whole) unpack<T>(v[u], f);
                 else r.load_part(e, f);
                 grad_vec<N>(f, P, k2, e);
@@ -290,7 +292,8 @@ __device__ __forceinline__ void write_row(const RowVecs<T> &r, T *g, int v0, int
             }
             __stcs(reinterpret_cast<uint4 *>(g + e), pack<T>(f));
         }
-    }}
+    }
+}
 
 } // namespace
 
@@ -300,7 +303,7 @@ __device__ __forceinline__ bool row_counts(const SeqLoss &l, int64_t t)
     return (!l.mask || l.mask[t] != 0) && (!l.first || (t >= l.first[0] && t < l.first[l.n_seq]));
 }
 
-// logp and lse2 of a counted row, which comes in pieces of one block each; the last piece to
+// logp, largest logit and sum of a counted row, which comes in pieces of one block each; the last piece to
 // arrive joins them all, in their order.  SMALL: a warp per row.  The rows' numbering runs beside
 // the first rows: all that their statistics read is the call's inputs, which were there before it
 // began (let_next_start), and results wait for it: 1531 rows of 32003 in fp32, by sequence, 108.9 -> 103.8
@@ -326,11 +329,11 @@ __global__ void __launch_bounds__(ROW_T) row_stats_kernel(const SeqLoss l, const
     float m = -INFINITY, z = 0.f;
     if constexpr (SMALL) {
         scan_row<T, 32, SMALL_U>(r, 0, r.n, tid, l.k2, m, z);
-        warp_stats(m, z);
+        warp_stats(m, z, l.k2);
     } else {
         scan_row<T, ROW_T, ROW_U>(r, r.piece(piece, splits), r.piece(piece + 1, splits), tid, l.k2, m, z);
         __shared__ float sm[ROW_T / 32], sz[ROW_T / 32];
-        block_stats<ROW_T>(m, z, sm, sz);
+        block_stats<ROW_T>(m, z, l.k2, sm, sz);
     }
     if (tid != 0) return;
     wait_for_stream();
@@ -347,10 +350,12 @@ __global__ void __launch_bounds__(ROW_T) row_stats_kernel(const SeqLoss l, const
         z = 0.f;
         for (int i = 0; i < splits; ++i) {
             const float2 q = __ldcg(p + i);
-            z += m > -INFINITY ? q.y * ex2_approx(q.x - m) : q.y;
+            z += m > -INFINITY ? q.y * ex2_approx((q.x - m) * l.k2) : q.y;
         }
     }
-    row_logp(l, m, z, y, splits > 1 ? 3 : 2, w.lp[c], w.lse2[c]);
+    w.lp[c] = row_logp(l, m, z, y, splits > 1 ? 3 : 2);
+    w.ref[c] = m;
+    w.share[c] = 1.f / z;
 }
 
 int seq_stat_splits(int64_t n, int64_t vocab, int dtype)
@@ -396,7 +401,7 @@ __global__ void __launch_bounds__(GRAD_T) row_grad_kernel(const SeqLoss l, const
         if (t >= l.n_tok) return;
         const int c = w.slot[t];
         const float4 P = c >= 0 ? w.tokp[c] : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
-        if (ADD && P.y == 0.f) return;
+        if (ADD && P.z == 0.f) return;
         const RowVecs<T> r(logits + t * l.vocab, l.vocab);
         write_row<T, ADD, 32, SMALL_U>(r, grad + t * l.vocab, 0, r.n, threadIdx.x & 31, P, l.k2);
         return;
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(GRAD_T) row_grad_kernel(const SeqLoss l, const
     const int piece = at - static_cast<unsigned>(t) * splits;
     const int c = w.slot[t];
     const float4 P = c >= 0 ? w.tokp[c] : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
-    if (ADD && P.y == 0.f) return;
+    if (ADD && P.z == 0.f) return;
     const RowVecs<T> r(logits + t * l.vocab, l.vocab);
     T *g = grad + t * l.vocab;
     const int v0 = r.piece(piece, splits), v1 = r.piece(piece + 1, splits);
@@ -507,13 +512,12 @@ __global__ void __launch_bounds__(GRAD_T) policy_small_kernel(const SeqLoss l, c
         }
         float m = -INFINITY, z = 0.f;
         scan_row<T, 32, SMALL_U>(r, 0, r.n, lane, l.k2, m, z);
-        warp_stats(m, z);
+        warp_stats(m, z, l.k2);
         if (lane == 0) {
-            float lp, lse2;
-            row_logp(l, m, z, y, 2, lp, lse2);
+            const float lp = row_logp(l, m, z, y, 2);
             const RowTerms x = policy_row(l, in, t, lp, 0.0, 0.f);
             if (l.logp) l.logp[t] = lp;
-            P = row_params(lse2, x.coef, target);
+            P = row_params(m, 1.f / z, x.coef, target);
             terms = make_float4(x.v[0], x.v[1], x.v[2], 0.f);
         }
         P.x = __shfl_sync(0xffffffffu, P.x, 0);
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(GRAD_T) policy_small_kernel(const SeqLoss l, c
         if (l.per_token) l.per_token[t] = 0.f;
     }
     if (lane == 0) w.terms[t] = terms;
-    if (GRAD == 1 || (GRAD == 2 && P.y != 0.f))
+    if (GRAD == 1 || (GRAD == 2 && P.z != 0.f))
         write_row<T, GRAD == 2, 32, SMALL_U>(r, grad + t * l.vocab, 0, r.n, lane, P, l.k2);
 }
 
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
                 add_vec<N>(m, z, f, vec_max<T>(v), l.k2);
             }
         }
-        block_stats<POLICY_T>(m, z, sm, sz);
+        block_stats<POLICY_T>(m, z, l.k2, sm, sz);
         if (cluster > 1) {
             __syncwarp();
             cluster_wait_started();
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
                 for (int q = 0; q < cluster; ++q) m = fmaxf(m, s_part[q].x);
                 z = 0.f;
                 for (int q = 0; q < cluster; ++q)
-                    z += m > -INFINITY ? s_part[q].y * ex2_approx(s_part[q].x - m) : s_part[q].y;
+                    z += m > -INFINITY ? s_part[q].y * ex2_approx((s_part[q].x - m) * l.k2) : s_part[q].y;
             }
         }
     } else if (cluster > 1) {
@@ -631,11 +635,10 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
     }
     if (on) {
         if (tid == 0) {
-            float lp, lse2;
-            row_logp(l, m, z, y, cluster > 1 ? 3 : 2, lp, lse2);
+            const float lp = row_logp(l, m, z, y, cluster > 1 ? 3 : 2);
             const RowTerms x = policy_row(l, in, t, lp, 0.0, 0.f, rank == 0);
             if (rank == 0 && l.logp) l.logp[t] = lp;
-            s_param = row_params(lse2, x.coef, target);
+            s_param = row_params(m, 1.f / z, x.coef, target);
             terms = make_float4(x.v[0], x.v[1], x.v[2], 0.f);
         }
         __syncthreads();
@@ -644,12 +647,12 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
         if (l.logp) l.logp[t] = 0.f;
         if (l.per_token) l.per_token[t] = 0.f;
     }
-    if (GRAD == 1 || (GRAD == 2 && P.y != 0.f)) {
+    if (GRAD == 1 || (GRAD == 2 && P.z != 0.f)) {
         for (int j = v0 + tid; j < v1; j += POLICY_T) {
             const int e = r.at(j);
             const bool whole = r.whole(e);
             float f[N] = {};
-            if (P.y != 0.f) {
+            if (P.z != 0.f) {
                 if (whole) unpack<T>(s_row[j - v0], f);
                 else r.load_part(e, f);
                 grad_vec<N>(f, P, l.k2, e);

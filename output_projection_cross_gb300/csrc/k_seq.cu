@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, co
     if (!(Z >= 0x1p-80f && Z <= 0x1p90f)) w.hdr->redo = 1;
     const float r = w.tokp[c].x, lz = log2f(Z);
     const double gap = static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - static_cast<double>(r);
-    w.lse2[c] = r + lz;
+    w.ref[c] = r + lz;
+    w.share[c] = 1.f;
     w.z[c] = Z;
     w.lp[c] = static_cast<float>((gap - static_cast<double>(lz)) * LN2 - EX2_LOW);
 }
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
     Z = 0.0;
     for (int q = 0; q < MT_W; ++q) Z += s_sum[q][lane];
     const double lse2 = static_cast<double>(M) + log2(Z);
-    w.lse2[c] = static_cast<float>(lse2);
+    w.ref[c] = static_cast<float>(lse2);
+    w.share[c] = 1.f;
     w.z[c] = 1.f;
     w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2 - 2 * EX2_LOW);
 }
@@ -424,9 +426,9 @@ __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const
                 for (int k = 0; k < 3; ++k) v[k] = r.v[k];
             }
             if (l.logp) l.logp[t] = lp;
-            const float4 P = row_params(w.lse2[c], r.coef, w.y[c]);
+            const float4 P = row_params(w.ref[c], w.share[c], r.coef, w.y[c]);
             w.tokp[c] = P;
-            coef = P.y;
+            coef = P.z;
         }
     }
     // the largest |coefficient| (fp16's passes scale by it): positive floats order as integers
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(256) seq_dh_kernel(const SeqLoss l, const SeqS
         if (fused && c >= 0) {
             if constexpr (N == 4) {
                 // (the fused pass runs on bf16 inputs)
-                const float a = w.tokp[c].y, az = a / w.z[c];
+                const float a = w.tokp[c].z, az = a / w.z[c];
                 const uint2 b = *reinterpret_cast<const uint2 *>(W + w.y[c] * d + k);
                 const float wv[4] = {h16_lo<false>(b.x), h16_hi<false>(b.x), h16_lo<false>(b.y), h16_hi<false>(b.y)};
 #pragma unroll

@@ -27,7 +27,7 @@ struct Layout {
     int64_t n_pad, n_ct, nsplit;
     bool small;
     int splits, cluster;
-    size_t off_slot, off_row, off_y, off_seq, off_tgt, off_lp, off_lse2, off_z, off_tokp, off_sum, off_slope, off_acc,
+    size_t off_slot, off_row, off_y, off_seq, off_tgt, off_lp, off_ref, off_share, off_z, off_tokp, off_sum, off_slope, off_acc,
         off_terms, off_tick, off_rows, off_hidden, off_part, off_dhpart, off_zpart, off_gring, off_gsig, off_dhacc, total;
 };
 
@@ -55,7 +55,8 @@ int32_t layout(int32_t kind, int64_t n, int64_t d, int64_t V, int64_t n_seq, int
     L->off_seq = take(sizeof(int) * (ns + 1));
     L->off_tgt = take(sizeof(float) * np);
     L->off_lp = take(sizeof(float) * np);
-    L->off_lse2 = take(sizeof(float) * np);
+    L->off_ref = take(sizeof(float) * np);
+    L->off_share = take(sizeof(float) * np);
     L->off_z = take(sizeof(float) * np);
     L->off_tokp = take(sizeof(float4) * np);
     L->off_sum = take(sizeof(double) * ns);
@@ -110,7 +111,8 @@ SeqScratch scratch(const Layout &L, void *ws)
     w.seq_slot = reinterpret_cast<int *>(b + L.off_seq);
     w.tgt = reinterpret_cast<float *>(b + L.off_tgt);
     w.lp = reinterpret_cast<float *>(b + L.off_lp);
-    w.lse2 = reinterpret_cast<float *>(b + L.off_lse2);
+    w.ref = reinterpret_cast<float *>(b + L.off_ref);
+    w.share = reinterpret_cast<float *>(b + L.off_share);
     w.z = reinterpret_cast<float *>(b + L.off_z);
     w.tokp = reinterpret_cast<float4 *>(b + L.off_tokp);
     w.sum = reinterpret_cast<double *>(b + L.off_sum);

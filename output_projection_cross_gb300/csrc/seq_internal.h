@@ -17,9 +17,10 @@ struct SeqScratch {
     int *seq_slot;      // [n_seq + 1] slots before each sequence (and all of them)
     float *tgt;         // [n_pad] its target's logit (the forms from hidden rows, as the pass has it)
     float *lp;          // [n_pad] logp
-    float *lse2;        // [n_pad] log2 sum 2^(x log2 e)
+    float *ref;         // [n_pad] from hidden rows log2 sum 2^(x log2 e), given logits the largest of them
+    float *share;       // [n_pad] a term relative to the reference times this is a probability
     float *z;           // [n_pad] fused pass: the sum of its shifted terms
-    float4 *tokp;       // [n_pad] {lse2, a, a, target}: softmax and one-hot coefficients
+    float4 *tokp;       // [n_pad] {ref, a share, a, target}: softmax and one-hot coefficients
     double *sum;        // [n_seq] sum over the sequence of logp minus its base
     double *slope;      // [n_seq] LOSSK_SEQ_RATIO: sum over the sequence of w dP/d(log ratio)
     double *acc;        // [3][blocks] the coefficient kernel's blocks' terms of the scalars
@@ -74,10 +75,10 @@ cudaError_t launch_seq_prep(const SeqLoss &l, const SeqScratch &w, cudaStream_t 
 // FUSED_SHIFT, and the target in tokp.w.
 cudaError_t launch_seq_gather(int dtype, const SeqLoss &l, const SeqScratch &w, const void *H, const void *W, int64_t d,
                               void *out, cudaStream_t st);
-// The fused pass's sums -> logp, lse2 (redo where a row left the range).
+// The fused pass's sums -> logp, ref, share (redo where a row left the range).
 cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const float *zpart, int64_t nz,
                                    cudaStream_t st);
-// The forward pass's (max, sum) partials of n_ct tiles -> logp, lse2.  only_if: or
+// The forward pass's (max, sum) partials of n_ct tiles -> logp, ref, share.  only_if: or
 // NULL; zero: not needed.
 cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,
                                    const int *only_if, cudaStream_t st);
@@ -88,7 +89,7 @@ cudaError_t launch_seq_sum(const SeqLoss &l, const SeqScratch &w, cudaStream_t s
 constexpr int COEF_T = 128;
 cudaError_t launch_seq_coef(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
 cudaError_t launch_seq_scalars(const SeqLoss &l, const SeqScratch &w, cudaStream_t st);
-// Given logits: logp, lse2, a row in `splits` pieces; grad_logits of every row, and the scalars.
+// Given logits: logp, ref, share, a row in `splits` pieces; grad_logits of every row, and the scalars.
 int seq_stat_splits(int64_t n, int64_t vocab, int dtype);
 cudaError_t launch_seq_stats(int dtype, const SeqLoss &l, const SeqScratch &w, const void *logits, int splits,
                              cudaStream_t st);

@@ -123,13 +123,14 @@ __device__ __forceinline__ RowTerms pair_row(const SeqLoss &l, const WsHeader *h
     return RowTerms{d_lp * l.per_t, {chosen ? -lp : 0.f, 0.f, 0.f}};
 }
 
-// The record that the passes over the logits read: {lse2, a, a, target}; a row without any
-// probability gets a zero gradient.
-__device__ __forceinline__ float4 row_params(float lse2, float coef, int64_t y)
+// The record that the passes over the logits read: {reference, a share, a, target}, where share
+// 2^(x log2 e - reference) is a probability (given logits: share 2^(k2 (s - reference)), the reference
+// being the largest of them); a row without any probability gets a zero gradient.
+__device__ __forceinline__ float4 row_params(float ref, float share, float coef, int64_t y)
 {
-    const bool none = lse2 == -INFINITY;
+    const bool none = ref == -INFINITY && share == share;
     const float a = none ? 0.f : coef;
-    return make_float4(none ? 0.f : lse2, a, a, __int_as_float(static_cast<int>(y)));
+    return make_float4(none ? 0.f : ref, none ? 0.f : a * share, a, __int_as_float(static_cast<int>(y)));
 }
 
 // The scalars from their three sums.

@@ -1,0 +1,108 @@
+"""The policy and preference losses from given logits whose values lie far out: masks of the type's lowest value, a common
+offset, temperatures far below 1.
+
+Tolerances of a gradient element, where the coefficient is exact: the distance to the row's largest logit and its product
+with the scale are rounded once each (2^-23 of an argument of at most 64 where the probability is above 2^-64: 64 ln 2
+2^-23), the row's sum as in test_gpu_sequence (4e-6 of additions, 2^-21 of ex2.approx), the result to its type."""
+import math
+
+import pytest
+import torch
+
+import output_projection_cross_gb300 as L
+import seq_ref as R
+from test_gpu_sequence import DT, HALF, TINY, Case, check_policy, check_preference, close, gen, run_policy, run_preference
+
+pytestmark = pytest.mark.gpu
+REL = 64.0 * 2.0 ** -23 + 4e-6 + 2.0 ** -21
+
+# a warp's rows, a cluster's, and rows too long for it
+ROWS = [dict(n=40, V=900, dtype="bf16"), dict(n=40, V=901, dtype="f32"), dict(n=40, V=9001, dtype="bf16"),
+        dict(n=24, V=9001, dtype="f32"), dict(n=16, V=9001, dtype="f16"), dict(n=24, V=100003, dtype="bf16"),
+        dict(n=400, V=40003, dtype="f32"), dict(n=6, V=500003, dtype="bf16")]
+
+
+def shifted(c):
+    """The case's scaled logits, each row's largest at 0 (in double their sums lose nothing then)."""
+    x = c.logits.double()
+    return (x - x.max(1, keepdim=True).values) / c.T
+
+
+@pytest.mark.parametrize("kw", ROWS, ids=str)
+@pytest.mark.parametrize("by", ["token", "sequence", "pair"])
+def test_masks_of_the_lowest_value(kw, by):
+    c = Case(seqs=4, **kw)
+    g, low = gen(5), torch.finfo(DT[c.dtype]).min
+    hide = torch.rand(c.n, c.V, device="cuda", generator=g) < 0.3
+    hide[: c.n // 2, : c.V // 2] = True                     # whole threads' and pieces' shares
+    hide[:, -3:] = True
+    hide[torch.arange(c.n), c.targets.clamp_(max=c.V - 4)] = False
+    c.logits[hide] = low
+    c.logits[3] = low                                       # a uniform row
+    c.logits[4] = low
+    c.logits[4, 5] = -math.inf
+    c.targets[4] = 6
+    c.x = shifted(c)
+    c.fill(g)
+    if by == "pair":
+        check_preference(c, run_preference(c))
+        return
+    flags = L.SEQ_RATIO if by == "sequence" else 0
+    band = dict(low=0.013, high=0.017) if flags else {}
+    out = run_policy(c, flags, kl=0.1, **band)
+    check_policy(c, out, flags, kl=0.1, **band)
+    rest = torch.ones(c.n, dtype=torch.bool, device="cuda")
+    rest[3:5] = False
+    assert not out["grad_logits"][hide & rest[:, None]].any()
+
+
+def exact_rows(c, out):
+    """grad_logits of a policy gradient with advantages as coefficients."""
+    p = torch.softmax(c.x, -1)
+    g, a = R.grad_logits(c.x, c.targets, c.on, -c.adv.double(), c.T)
+    own = a.abs()[:, None] * p
+    hit = torch.zeros_like(own)
+    hit[torch.arange(c.n), c.targets] = a.abs()
+    under = 2.0 ** -126 * (2.0 + float(a.abs().max()))
+    close(out["grad_logits"], g, REL * own + 2.0 ** -22 * (own + hit) + HALF[c.dtype] * g.abs() + TINY[c.dtype] + under, "grad_logits")
+
+
+@pytest.mark.parametrize("kw", [r for r in ROWS if r["dtype"] == "f32"], ids=str)
+@pytest.mark.parametrize("offset", [0.0, 30.0, -3000.0, 1e5])
+def test_a_common_offset(kw, offset):
+    """Every probability relative to its own size, whatever all logits have in common."""
+    c = Case(**kw)
+    c.logits += offset
+    c.x = shifted(c)
+    c.lp = R.logprobs(c.x, c.targets, c.on)
+    # -A (total = -sum A logp): a_t = A_t
+    out = L.lossk_policy_from_logits(c.logits, c.targets, c.adv, flags=L.REDUCE_SUM)
+    close(out["logp"], c.lp, c.lp_tol() + 2.0 ** -24 * c.lp.abs(), "logp")
+    exact_rows(c, out)
+    first = torch.tensor([0, c.n // 2, c.n], dtype=torch.int32, device="cuda")
+    c.first, c.ref = first, c.lp.float()
+    out = run_preference(c)
+    # The reference's log-probabilities are the rounded exact ones, so u is the difference of two sums of roundings, each
+    # below its tolerance: whether it is above 0 is open, and the share of such pairs 0 or 1.
+    assert float(out["scalars"][3]) in (0.0, 1.0)
+    out["scalars"][3] = R.preference(c.lp, c.on, c.first, c.ref)["scalars"][3]
+    check_preference(c, out)
+
+
+@pytest.mark.parametrize("kw", ROWS, ids=str)
+@pytest.mark.parametrize("T", [1e-6, 1e-9, 1e-20, 1e-30, 1e30])
+def test_temperatures_far_from_one(kw, T):
+    """Where logits over the temperature differ by less than fp32's range in log2 units or by far more."""
+    c = Case(**kw)
+    c.T = T
+    rows = torch.arange(c.n, device="cuda")
+    near = rows < c.n // 2
+    c.targets = torch.where(near, c.logits.float().argmax(1), c.targets)
+    c.x = shifted(c)
+    c.lp = R.logprobs(c.x, c.targets, c.on)
+    out = L.lossk_policy_from_logits(c.logits, c.targets, c.adv, temperature=T, flags=L.REDUCE_SUM, grad_scale=min(T, 1.0))
+    assert not torch.isnan(out["logp"]).any() and not torch.isnan(out["grad_logits"]).any()
+    far = c.lp.float().double()                             # -infinity beyond fp32
+    close(out["logp"], torch.where(torch.isinf(far), far, c.lp), 8e-6 + 2.0 ** -22 * c.lp.abs(), "logp")
+    c.adv *= min(T, 1.0)
+    exact_rows(c, out)
