@@ -61,8 +61,10 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
     __shared__ int s_groups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = l.n_tok;
-    // (an error word of an earlier call stays until lossk_device_status has read it: refused)
-    bool bad = *reinterpret_cast<volatile int *>(&w.hdr->err) != 0;
+    // (what an earlier call left in the error or the fault word stays until lossk_device_status has
+    // read it: refused)
+    bool bad = *reinterpret_cast<volatile int *>(&w.hdr->err) != 0 ||
+               is_fault(*reinterpret_cast<volatile int *>(&w.hdr->pad[HDR_FAULT]));
     unsigned on;
     int64_t y[PREP_PER];
     auto load = [&](int t0) {
@@ -169,7 +171,8 @@ __global__ void __launch_bounds__(PREP_T) seq_prep_kernel(const SeqLoss l, const
         w.hdr->pad[HDR_GROUPS] = s_groups;
         w.hdr->pad[HDR_CHOSEN] = chosen;
         w.hdr->pad[HDR_COEF] = 0;
-        if (any_bad && w.hdr->err == 0) raise_fault(&w.hdr->pad[HDR_FAULT], LOSSK_TARGET_OUT_OF_RANGE);
+        int *fault = &w.hdr->pad[HDR_FAULT];
+        if (any_bad && w.hdr->err == 0 && !is_fault(*fault)) *fault = LOSSK_TARGET_OUT_OF_RANGE;
     }
 }
 

@@ -1212,9 +1212,8 @@ int32_t lossk_device_status(void *workspace, int64_t workspace_bytes, lossk_stre
     int words[4 + HDR_FAULT + 1];
     static_assert(offsetof(WsHeader, pad) == 4 * sizeof(int), "the words up to the fault word");
     if (cudaMemcpy(words, hdr, sizeof(words), cudaMemcpyDeviceToHost) != cudaSuccess) return LOSSK_DEVICE_ERROR;
-    // the losses' calls neither use nor clear the fault word: what is no code of the decoding calls is not theirs
     const int err = words[0], left = words[4 + HDR_FAULT];
-    const bool fault = left == LOSSK_TARGET_OUT_OF_RANGE || left == LOSSK_NON_FINITE_SCALAR || left == LOSSK_WORK_BUDGET_EXCEEDED;
+    const bool fault = is_fault(left);
     const int zero = 0;
     if ((err && cudaMemcpy(&hdr->err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) ||
         (fault && cudaMemcpy(&hdr->pad[HDR_FAULT], &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess))

@@ -2,6 +2,8 @@
 // the workspace layout, the per-token parameter records and the launcher
 // declarations.  Not part of the public ABI.
 #pragma once
+#include "../../include/lossk.h"
+
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -31,6 +33,12 @@ struct WsHeader {
                       // lossk_status), pad[HDR_NEXT] a work counter, 0 between calls
 };
 constexpr int HDR_FAULT = 1, HDR_NEXT = 2;
+// Whether the fault word holds one of the statuses that are left there (the label losses' calls
+// neither use nor clear it: what else it holds is no fault).
+__host__ __device__ inline bool is_fault(int word)
+{
+    return word == LOSSK_TARGET_OUT_OF_RANGE || word == LOSSK_NON_FINITE_SCALAR || word == LOSSK_WORK_BUDGET_EXCEEDED;
+}
 // The sequence losses' calls: sequences with a counted token (policy) or pairs that count
 // (preference), counted tokens of chosen sequences, bits of the largest |coefficient|.
 constexpr int HDR_GROUPS = 3, HDR_CHOSEN = 4, HDR_COEF = 5;
