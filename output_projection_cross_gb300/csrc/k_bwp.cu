@@ -705,22 +705,30 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
         const float4 P0 = DISTILL ? make_float4(0.f, 0.f, 0.f, 0.f)
                                   : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
         // fp16 operands: what the grad tiles leave out and the stored accumulators
-        // get back.  coef_max: the largest coefficient of the tokens, found on the
-        // device; the tiles hold G times the power of two that brings it to
-        // [2^13, 2^14), which keeps probabilities down to 2^-38 in fp16's range
-        // and the tiles' largest entry, a coefficient times 1 - p, below its end.
+        // get back.  With coef_max the tiles hold G times the power of two that brings a
+        // coefficient to [2^13, 2^14), which keeps probabilities down to 2^-38 in
+        // fp16's range and the tiles' largest entry, a coefficient times 1 - p, below
+        // its end.  d_weight, where a sum runs over the tokens: the largest coefficient
+        // of them, found on the device.  d_hidden: each row its own, so that a row far
+        // above the others, or one whose coefficient is no number, costs them nothing.
+        const bool own_scale = F16 && ROWS && a.coef_max;
+        auto exponent = [](unsigned m) {
+            return m > 0 && m < 0x7F800000u ? min(max(14 - static_cast<int>(m >> 23) + 126, -126), 126) : 0;
+        };
+        auto row_exponent = [&](float coef) { return exponent(__float_as_uint(fabsf(coef))); };
+        auto pow2 = [](int e) { return __int_as_float((127 + e) << 23); };
         float in_scale = 1.f, out_scale = a.out_scale;
-        if (F16 && a.coef_max) {
-            const unsigned m = *a.coef_max;
-            const int e = m > 0 && m < 0x7F800000u ? min(max(14 - static_cast<int>(m >> 23) + 126, -126), 126) : 0;
-            in_scale = __int_as_float((127 + e) << 23);
-            out_scale = __int_as_float((127 - e) << 23);
+        if (F16 && !ROWS && a.coef_max) {
+            const int e = exponent(*a.coef_max);
+            in_scale = pow2(e);
+            out_scale = pow2(-e);
         }
         auto param = [&](int t) {
             float4 p = t < n_tok ? a.tokp[t] : P0;
             if (F16 && !DISTILL) {
-                p.y *= in_scale;
-                p.z *= in_scale;
+                const float s = own_scale ? pow2(row_exponent(p.z)) : in_scale;
+                p.y *= s;
+                p.z *= s;
             }
             return p;
         };
@@ -1058,6 +1066,8 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
             tc_fence_after();
             const int slice0 = (w.dg * c + crank) * TC_SLICE;
             const int n_rows = ROWS ? n_tok : a.vocab;
+            const float row_scale =
+                own_scale ? pow2(-row_exponent(fixrow < n_tok ? a.tokp[fixrow].z : 0.f)) : out_scale;
             float *dst = a.out + static_cast<int64_t>(split) * a.out_split_stride +
                          static_cast<int64_t>(fixrow) * a.d;
             if (STG && a.out_tma) {
@@ -1083,7 +1093,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                     tmem_ld_wait();
                     if (F16) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * out_scale);
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * row_scale);
                     }
                     if (!DISTILL && a.out16) {
                         // 16-bit d_weight (rounded once, here): a whole chunk is one half block
@@ -1156,7 +1166,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                     tmem_ld_wait();
                     if (F16) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * out_scale);
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * row_scale);
                     }
                     if (lane == 0) bulk_wait_read_all();            // the block's previous store has read it
                     __syncwarp();
@@ -1189,7 +1199,7 @@ __global__ void __launch_bounds__(B_THREADS, 1) bwp_kernel(const __grid_constant
                             if (F16) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    v[h][i] = __float_as_uint(__uint_as_float(v[h][i]) * out_scale);
+                                    v[h][i] = __float_as_uint(__uint_as_float(v[h][i]) * row_scale);
                             }
                             if (a.accumulate) {
                                 // gradient accumulation: out += this unit's accumulator

@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(COEF_T) seq_coef_kernel(const SeqLoss l, const
             coef = P.z;
         }
     }
-    // the largest |coefficient| (fp16's passes scale by it): positive floats order as integers
-    unsigned m = __float_as_uint(fabsf(coef));
+    // the largest finite |coefficient| (fp16's d_weight pass scales by it): positive floats order as integers
+    unsigned m = isfinite(coef) ? __float_as_uint(fabsf(coef)) : 0;
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0 && m) atomicMax(reinterpret_cast<unsigned *>(&w.hdr->pad[HDR_COEF]), m);
 

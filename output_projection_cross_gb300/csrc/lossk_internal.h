@@ -163,8 +163,9 @@ struct BwdArgs {
     float *tgt_out;        // BWD_FUSED, or NULL: each token's target logit (the target's column in tokp.w)
     int accumulate;        // add the accumulator into `out` instead of overwriting it
     float out_scale;       // fp16 operands: the factor the stored accumulator is multiplied by
-    const unsigned *coef_max;  // fp16 operands, or NULL: the bits of the largest |coefficient| among the tokens (label
-                           // loss); the passes then scale by a power of two of their own instead of out_scale
+    const unsigned *coef_max;  // fp16 operands, or NULL: the bits of the largest finite |coefficient| among the tokens;
+                           // d_weight then scales by a power of two from it, d_hidden each row by one from its own,
+                           // instead of out_scale (label loss)
     int out16;             // d_weight: map_out is a 16-bit tensor, box {32, 32} (label loss, no accumulation)
     const int *n_dev;      // or NULL: the tokens there are, found by an earlier kernel (at most n_tok)
     const int *refused;    // nonzero: the validation before found a bad target; return at once

@@ -1,0 +1,69 @@
+"""Heads of the policy and preference losses whose rows' coefficients are of very different sizes, or of which one is no
+number: what the others get does not depend on it."""
+import math
+
+import pytest
+import torch
+
+import output_projection_cross_gb300 as L
+import seq_ref as R
+from test_gpu_sequence import DT, HALF, TINY, Case, close, run_policy
+
+pytestmark = pytest.mark.gpu
+HEADS = [dict(n=70, V=900, d=136, dtype="f16"), dict(n=300, V=2001, d=264, dtype="f16"), dict(n=70, V=900, d=136, dtype="bf16"),
+         dict(n=70, V=900, d=72, dtype="f32")]
+
+
+def check_rows(c, out, rows, scale, grad, adv):
+    """d_hidden of `rows` against the 64-bit definition; each row's error is relative to its own coefficient."""
+    r = R.policy(c.lp, c.on, c.first, adv, c.old, c.ref)
+    g, a = R.grad_logits(c.x, c.targets, c.on, r["slope"] * scale, c.T)
+    p = torch.softmax(c.x, -1)
+    mass = r["mass"] * scale / c.T
+    size, own = mass[:, None] * p, a.abs()[:, None] * p
+    at = torch.arange(c.n)
+    size[at, c.targets] += mass
+    own[at, c.targets] += a.abs()
+    half = HALF[c.dtype]
+    # as in test_gpu_sequence.check_grads, but that a row's tile ends 2^-38 below its own coefficient
+    err = (0.0 if c.dtype == "f32" else half) * own + (8 * c.lp_tol() + 2.0 ** -20 + (c.d + c.V / 16) * 2.0 ** -23) * size
+    err = err + (2.0 ** -38 * a.abs()[:, None] if c.dtype == "f16" else 0.0) + 2.0 ** -126 * (2.0 + a.abs()[:, None])
+    w = c.weight.double()
+    want = g @ w
+    out_half = half if grad == "same" and c.dtype != "f32" else 2.0 ** -24
+    tol = err @ w.abs() + out_half * want.abs() + (TINY[c.dtype] if grad == "same" else 0.0) + 2.0 ** -126
+    close(out["d_hidden"][rows], want[rows], tol[rows], "d_hidden")
+
+
+@pytest.mark.parametrize("kw", HEADS, ids=str)
+@pytest.mark.parametrize("grad", ["same", "float"])
+@pytest.mark.parametrize("what", ["hidden NaN", "hidden infinite", "ratio infinite", "ratio far above", "advantages"])
+def test_one_row_costs_the_others_nothing(kw, grad, what):
+    c = Case(**kw)
+    rows = torch.ones(c.n, dtype=torch.bool, device="cuda")
+    rows[5] = False
+    # mean-reduced coefficients of a long batch
+    scale = 1e-3
+    if what == "hidden NaN":
+        c.hidden[5] = math.nan
+    elif what == "hidden infinite":
+        c.hidden[5, 0] = math.inf
+    elif what == "ratio infinite":
+        c.old[5], c.adv[5] = float(c.lp[5]) - 200.0, -1.0
+    elif what == "ratio far above":
+        c.old[5], c.adv[5] = float(c.lp[5]) - 40.0, -1.0
+    else:
+        # sizes over 20 powers of ten, among them one that takes no part
+        c.adv *= 10.0 ** torch.linspace(-12.0, 8.0, c.n, device="cuda")
+        c.adv[5] = 0.0
+    out = run_policy(c, grad_scale=scale, grad_dtype=DT[c.dtype] if grad == "same" else torch.float32)
+    adv = c.adv.clone()
+    if what.startswith("hidden"):
+        c.x[5] = 0.0                                       # (the definition's row, left out of the comparison)
+        c.lp = torch.where(rows, c.lp, 0.0)
+    elif what.startswith("ratio"):
+        adv[5] = 0.0
+        assert not torch.isfinite(out["d_hidden"][5]).all() or what.endswith("above")
+    check_rows(c, out, rows, scale, grad, adv)
+    if what.startswith("hidden"):
+        assert torch.isnan(out["logp"][5]) and torch.isfinite(out["logp"][rows]).all()
