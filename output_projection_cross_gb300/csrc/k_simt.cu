@@ -1798,7 +1798,10 @@ __global__ void __launch_bounds__(256) fp_kernel(const float *__restrict__ X,
                     for (int jx = 0; jx < T; ++jx) m = fmaxf(m, vs[jx] * L2E);
                     for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
-                    for (int jx = 0; jx < T; ++jx) z += exp2f(vs[jx] * L2E - m);
+                    for (int jx = 0; jx < T; ++jx)
+                        // relative to m as it is, rounded once (n_dev: the sequence losses; the label loss
+                        // rounds the scaled logit first, 2^-25 of it, as its results have it)
+                        z += exp2f(n_dev ? fmaf(vs[jx], L2E, -m) : vs[jx] * L2E - m);
                     for (int o = 1; o < 16; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
                     if (t < n_tok) {
                         if (tx == 0) {

@@ -106,3 +106,23 @@ def test_temperatures_far_from_one(kw, T):
     close(out["logp"], torch.where(torch.isinf(far), far, c.lp), 8e-6 + 2.0 ** -22 * c.lp.abs(), "logp")
     c.adv *= min(T, 1.0)
     exact_rows(c, out)
+
+
+def exact_head(offset, T=1.0, V=1001):
+    """One token in fp32 and a head whose logits are exact sums: hidden, weight, target, scaled logits (the largest 0)."""
+    hidden = torch.tensor([[1.0, 1.0]], device="cuda")
+    weight = torch.stack([torch.randint(-2048, 2049, (V,), device="cuda", generator=gen(3)) / 256.0,
+                          torch.full((V,), offset, device="cuda")], 1).contiguous()
+    x = hidden.double() @ weight.double().t()
+    assert torch.equal(x, x.float().double())
+    return hidden, weight, torch.tensor([7], device="cuda"), (x - x.max()) / T
+
+
+@pytest.mark.parametrize("offset", [0.0, 48.0, 300.0, 3000.0, -20000.0])
+@pytest.mark.parametrize("T", [1.0, 0.7, 1.3])
+def test_logp_of_a_head_with_a_common_offset(offset, T):
+    hidden, weight, y, x = exact_head(offset, T)
+    out = L.lossk_policy_fwd_bwd(hidden, weight, y, torch.ones(1, device="cuda"), temperature=T)
+    want = torch.log_softmax(x, -1)[:, 7]
+    # as from given logits, and the scale's two roundings (2^-23 of a distance to the target's logit)
+    close(out["logp"], want, 8e-6 + 2.0 ** -22 * want.abs(), "logp")
