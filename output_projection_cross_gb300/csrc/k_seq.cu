@@ -15,6 +15,7 @@
 #include "ptx.cuh"
 #include "seq_terms.cuh"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace lossk {
@@ -41,6 +42,13 @@ __device__ __forceinline__ int seq_of(const int *seq_slot, int n_seq, int c, int
     int s = lo;
     while (s + 1 < n_seq && seq_slot[s + 1] <= c) ++s;
     return s;
+}
+
+__device__ __forceinline__ void put_lse2(const SeqScratch &w, int c, double lse2)
+{
+    const float ref = static_cast<float>(lse2);
+    w.ref[c] = ref;
+    w.share[c] = fabsf(ref) <= FLT_MAX ? exp2f(static_cast<float>(static_cast<double>(ref) - lse2)) : 1.f;
 }
 
 } // namespace
@@ -246,7 +254,9 @@ cudaError_t launch_seq_gather(int dtype, const SeqLoss &l, const SeqScratch &w, 
 // One thread per slot.  With r the row's reference (its target at about 64 in log2
 // units) and Z the sum of 2^(x log2 e - r): lse2 = r + log2 Z, logp = ln 2 (x_y log2 e - r -
 // log2 Z).  The difference is taken in double: r's own rounding, 4e-6 at 64, is in Z
-// as well and must not be in the result.  x_y comes from the pass as the sum does: the
+// as well and must not be in the result.  The passes take 2^(x log2 e - lse2) with lse2 a
+// float: what its rounding moves every probability of the row by (2e-6 at 64, 7e-5 at 3000)
+// is given back in `share`.  x_y comes from the pass as the sum does: the
 // tensor cores' sums are truncated, logits come out low by 1e-9 of their size per unit of
 // d_model, and an exact x_y against such a sum was 2.5e-5 off at d_model 4096, the same
 // way for every token of a sequence.
@@ -270,12 +280,12 @@ __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, co
     for (; j < nz; ++j) Z += zpart[j * w.n_pad + c];
     // outside, the largest shifted term may be near the end of fp32's range (or not a number)
     if (!(Z >= 0x1p-80f && Z <= 0x1p90f)) w.hdr->redo = 1;
-    const float r = w.tokp[c].x, lz = log2f(Z);
+    const float r = w.tokp[c].x;
+    const double lz = log2_of(Z), lse2 = static_cast<double>(r) + lz;
     const double gap = static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - static_cast<double>(r);
-    w.ref[c] = r + lz;
-    w.share[c] = 1.f;
+    put_lse2(w, c, lse2);
     w.z[c] = Z;
-    w.lp[c] = static_cast<float>((gap - static_cast<double>(lz)) * LN2 - EX2_LOW);
+    w.lp[c] = static_cast<float>((gap - lz) * LN2 - EX2_LOW);
 }
 
 cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const float *zpart, int64_t nz,
@@ -309,17 +319,16 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
     __syncthreads();
     for (int q = 0; q < MT_W; ++q) M = fmaxf(M, s_max[q][lane]);
     double Z = 0.0;
-    if (live && M > -INFINITY)
+    if (live)                                  // (a row without any probability: 0, or the NaNs that maxima pass over)
         for (int64_t i = c0; i < c1; ++i)
-            Z += static_cast<double>(zz[i * w.n_pad + c] * exp2f(m2[i * w.n_pad + c] - M));
+            Z += static_cast<double>(zz[i * w.n_pad + c] * (M > -INFINITY ? exp2f(m2[i * w.n_pad + c] - M) : 1.f));
     s_sum[g][lane] = Z;
     __syncthreads();
     if (g != 0 || !live) return;
     Z = 0.0;
     for (int q = 0; q < MT_W; ++q) Z += s_sum[q][lane];
     const double lse2 = static_cast<double>(M) + log2(Z);
-    w.ref[c] = static_cast<float>(lse2);
-    w.share[c] = 1.f;
+    put_lse2(w, c, lse2);
     w.z[c] = 1.f;
     w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2 - 2 * EX2_LOW);
 }

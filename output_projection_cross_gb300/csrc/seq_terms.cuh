@@ -12,6 +12,14 @@ __device__ __forceinline__ bool seq_refused(const WsHeader *hdr)
     return *reinterpret_cast<const volatile int *>(&hdr->bad_targets) != 0;
 }
 
+// log2 z to 2^-24 or so, of whatever size it is (log2f keeps that many of its own bits, 2^-18 at 64).
+__device__ __forceinline__ double log2_of(float z)
+{
+    int e;
+    const float f = frexpf(z, &e);
+    return static_cast<double>(e) + static_cast<double>(log2f(f));
+}
+
 __device__ __forceinline__ int slots_before(int slot) { return slot < 0 ? ~slot : slot; }
 
 // A counted row's weight in the mean: n_s its sequence's counted tokens.

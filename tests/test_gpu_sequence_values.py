@@ -126,3 +126,16 @@ def test_logp_of_a_head_with_a_common_offset(offset, T):
     want = torch.log_softmax(x, -1)[:, 7]
     # as from given logits, and the scale's two roundings (2^-23 of a distance to the target's logit)
     close(out["logp"], want, 8e-6 + 2.0 ** -22 * want.abs(), "logp")
+
+
+@pytest.mark.parametrize("offset", [0.0, 48.0, 3000.0, -20000.0])
+def test_gradient_of_a_head_with_a_common_offset(offset):
+    """d_weight's first column is a p_v (a - a p_y the target's)."""
+    hidden, weight, y, x = exact_head(offset)
+    out = L.lossk_policy_fwd_bwd(hidden, weight, y, torch.ones(1, device="cuda"))
+    p = torch.softmax(x, -1)[0]
+    hit = torch.arange(len(p), device="cuda") == 7
+    want = p - hit.double()
+    # one rounding of an argument below 32 (32 ln 2 2^-24), exp2f's two units, the row's sum (test_gpu_sequence)
+    tol = (32 * 2.0 ** -24 + 2.0 ** -22 + 4e-6) * (p + hit * p[7]) + 2.0 ** -24 * want.abs()
+    close(out["d_weight"][:, 0], want, tol, "d_weight")
