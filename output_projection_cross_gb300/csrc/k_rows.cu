@@ -186,7 +186,7 @@ __device__ __forceinline__ float row_logp(const SeqLoss &l, float M, float z, fl
     const double gap = (static_cast<double>(y) - static_cast<double>(M)) * static_cast<double>(l.k2);
     return y == -INFINITY && z == z
                ? y
-               : static_cast<float>((gap - log2_of(z)) * LN2 - exps * EX2_LOW);
+               : static_cast<float>((gap - log2_of(z)) * LN2 - ex2_low(z, exps));
 }
 
 // A warp's (max, sum) from its lanes', as block_stats; valid in every lane.

@@ -285,7 +285,9 @@ __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, co
     const double gap = static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - static_cast<double>(r);
     put_lse2(w, c, lse2);
     w.z[c] = Z;
-    w.lp[c] = static_cast<float>((gap - lz) * LN2 - EX2_LOW);
+    // (the exponentials are of -64 for the target, as exact as of 0, and anything for the others)
+    const float lp = static_cast<float>((gap - lz) * LN2);
+    w.lp[c] = static_cast<float>((gap - lz) * LN2 - EX2_LOW * static_cast<double>(1.f - expf(fminf(lp, 0.f))));
 }
 
 cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const float *zpart, int64_t nz,
@@ -330,7 +332,8 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
     const double lse2 = static_cast<double>(M) + log2(Z);
     put_lse2(w, c, lse2);
     w.z[c] = 1.f;
-    w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2 - 2 * EX2_LOW);
+    w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2 -
+                                 ex2_low(static_cast<float>(Z), 2));
 }
 
 cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,

@@ -35,7 +35,9 @@ struct SeqScratch {
 // ex2.approx comes out low by 5e-8 of its value on average (measured over [-80, 0]:
 // 4.9e-8 to 5.2e-8), and so does a sum of exponentials, once per exponential that a
 // term has gone through.  That much is given back to the log-probabilities: sequences sum
-// hundreds of them against a reference's, and it would add up.
+// hundreds of them against a reference's, and it would add up.  A largest term's own exponentials are of 0,
+// and exact: what is given back is of the other terms' share of the sum (a token that is all but
+// certain has logp 0, not 1e-7).
 constexpr double EX2_LOW = 5e-8;
 
 // The tensor cores drop what lies below an fp32 sum's last bit at each step of 16

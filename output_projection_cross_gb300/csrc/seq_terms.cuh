@@ -20,6 +20,13 @@ __device__ __forceinline__ double log2_of(float z)
     return static_cast<double>(e) + static_cast<double>(log2f(f));
 }
 
+// What a log-probability is given back where the sum z of terms relative to the largest went through
+// `exps` exponentials, that one's own terms aside.
+__device__ __forceinline__ double ex2_low(float z, int exps)
+{
+    return static_cast<double>(exps * static_cast<float>(EX2_LOW) * (1.f - 1.f / z));
+}
+
 __device__ __forceinline__ int slots_before(int slot) { return slot < 0 ? ~slot : slot; }
 
 // A counted row's weight in the mean: n_s its sequence's counted tokens.

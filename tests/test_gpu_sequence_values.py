@@ -139,3 +139,32 @@ def test_gradient_of_a_head_with_a_common_offset(offset):
     # one rounding of an argument below 32 (32 ln 2 2^-24), exp2f's two units, the row's sum (test_gpu_sequence)
     tol = (32 * 2.0 ** -24 + 2.0 ** -22 + 4e-6) * (p + hit * p[7]) + 2.0 ** -24 * want.abs()
     close(out["d_weight"][:, 0], want, tol, "d_weight")
+
+
+@pytest.mark.parametrize("kw", ROWS + [dict(n=40, V=1, dtype=t) for t in ("bf16", "f16", "f32")], ids=str)
+@pytest.mark.parametrize("loss", ["policy", "pairs"])
+def test_a_certain_token_has_logp_0(kw, loss):
+    """All but the target 40 below it and more: its sum is 1 to the last bit, and so is its probability."""
+    c = Case(**kw)
+    c.logits.clamp_(-20.0, 20.0)
+    c.logits[torch.arange(c.n), c.targets] = 60.0
+    if loss == "policy":
+        out = L.lossk_policy_from_logits(c.logits, c.targets, c.adv)
+    else:
+        out = L.lossk_preference_from_logits(c.logits, c.targets, torch.tensor([0, c.n // 2, c.n], dtype=torch.int32, device="cuda"))
+    assert not out["logp"].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [1, 300])
+def test_certain_tokens_of_a_head(dtype, V):
+    """logp without a bias: a sum about 1 is rounded by 2^-24 at most, up in some rows and down in others."""
+    n, d = 1000, 64
+    c = Case(n=n, V=V, d=d, dtype=dtype, std=0.2)
+    c.hidden[:, :2] = 0.0
+    c.hidden[:, 0] = 8.0
+    c.weight[:, 0] = 0.0
+    c.weight[0, 0] = 6.0
+    c.targets.zero_()
+    out = L.lossk_policy_fwd_bwd(c.hidden, c.weight, c.targets, c.adv, want_d_hidden=False, want_d_weight=False)
+    assert abs(float(out["logp"].double().mean())) <= 2.0 ** -24 and float(out["logp"].abs().max()) <= 2.0 ** -21
