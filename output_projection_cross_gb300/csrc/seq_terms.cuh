@@ -93,7 +93,7 @@ __device__ __forceinline__ RowTerms policy_row(const SeqLoss &l, const RowInputs
     float kl = 0.f, loss = p.loss;
     if (l.ref) {
         const float q = in.ref - lp, e = expm1f(q);
-        kl = e - q;
+        kl = e == INFINITY ? e : e - q;                    // (of a token of probability 0: infinity, not infinity less itself)
         if (l.kl > 0.f) {
             loss = fmaf(l.kl, kl, loss);
             d_lp = fmaf(-l.kl * weight, e, d_lp);

@@ -168,3 +168,24 @@ def test_certain_tokens_of_a_head(dtype, V):
     c.targets.zero_()
     out = L.lossk_policy_fwd_bwd(c.hidden, c.weight, c.targets, c.adv, want_d_hidden=False, want_d_weight=False)
     assert abs(float(out["logp"].double().mean())) <= 2.0 ** -24 and float(out["logp"].abs().max()) <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("kw", [dict(n=9, V=900, dtype="bf16"), dict(n=9, V=9001, dtype="f32"), dict(n=3, V=500003, dtype="bf16")], ids=str)
+@pytest.mark.parametrize("flags", [0, L.SEQ_MEAN, L.SEQ_RATIO])
+@pytest.mark.parametrize("kl", [0.0, 0.1])
+def test_kl_of_a_token_of_probability_0(kw, flags, kl):
+    """exp(q) - q - 1 of an infinite q is infinite, and so is what it is part of; without a weight it stays out of the total."""
+    c = Case(seqs=2, **kw)
+    c.logits[1, c.targets[1]] = -math.inf
+    c.adv.abs_()
+    c.x = c.logits.double()
+    c.lp = R.logprobs(c.x, c.targets, c.on)
+    c.old[1], c.ref[1] = -8.0, -9.0
+    out = run_policy(c, flags, kl=kl)
+    total, policy, far = (float(v) for v in out["scalars"][:3])
+    assert math.isinf(float(out["logp"][1])) and far == math.inf and math.isfinite(policy)
+    assert total == (math.inf if kl else policy)
+    rest = torch.arange(c.n, device="cuda") != 1
+    assert torch.isfinite(out["per_token"][rest]).all()
+    if not flags & L.SEQ_RATIO:
+        assert float(out["per_token"][1]) == (math.inf if kl else 0.0)
