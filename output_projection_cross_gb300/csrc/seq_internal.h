@@ -57,7 +57,7 @@ struct SeqLoss {
     const float *adv, *old, *ref;
     float low, high, kl;
     float k2;                      // log2(e) / temperature
-    float per_t;                   // -grad_scale / temperature
+    double per_t;                  // -grad_scale / temperature (beyond floats where both are at their ends)
     uint32_t flags;
     int objective;
     float beta, margin, smooth, nll;

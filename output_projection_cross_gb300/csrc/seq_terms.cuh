@@ -65,6 +65,12 @@ struct RowTerms {
     float coef, v[3];
 };
 
+// a_t from d total / d logp.
+__device__ __forceinline__ float coefficient(const SeqLoss &l, float d_lp)
+{
+    return static_cast<float>(static_cast<double>(d_lp) * l.per_t);
+}
+
 // What the policy loss reads for row t of sequence s (of n_s counted tokens).
 struct RowInputs {
     float weight, adv, old, ref;
@@ -100,7 +106,7 @@ __device__ __forceinline__ RowTerms policy_row(const SeqLoss &l, const RowInputs
         }
     }
     if (write && l.per_token) l.per_token[t] = loss;
-    return RowTerms{d_lp * l.per_t, {weight * p.loss, weight * kl, p.clipped ? weight : 0.f}};
+    return RowTerms{coefficient(l, d_lp), {weight * p.loss, weight * kl, p.clipped ? weight : 0.f}};
 }
 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
@@ -135,7 +141,7 @@ __device__ __forceinline__ RowTerms pair_row(const SeqLoss &l, const WsHeader *h
     if (l.flags & LOSSK_LENGTH_MEAN) d_lp /= static_cast<float>(n_s);
     if (!sum && slope != 0.f) d_lp /= static_cast<float>(hdr->pad[HDR_GROUPS]);
     if (chosen && l.nll > 0.f) d_lp -= l.nll / (sum ? 1.f : static_cast<float>(hdr->pad[HDR_CHOSEN]));
-    return RowTerms{d_lp * l.per_t, {chosen ? -lp : 0.f, 0.f, 0.f}};
+    return RowTerms{coefficient(l, d_lp), {chosen ? -lp : 0.f, 0.f, 0.f}};
 }
 
 // The record that the passes over the logits read: {reference, a share, a, target}, where share

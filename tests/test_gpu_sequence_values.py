@@ -189,3 +189,19 @@ def test_kl_of_a_token_of_probability_0(kw, flags, kl):
     assert torch.isfinite(out["per_token"][rest]).all()
     if not flags & L.SEQ_RATIO:
         assert float(out["per_token"][1]) == (math.inf if kl else 0.0)
+
+
+@pytest.mark.parametrize("kw", [dict(n=40, V=900, dtype="f32"), dict(n=24, V=9001, dtype="f32")], ids=str)
+@pytest.mark.parametrize("T,scale", [(1e-20, 1e25), (1e-30, 1e9), (1e30, 1e-30)])
+def test_a_scale_over_the_temperature_beyond_floats(kw, T, scale):
+    """1e39 and more, or nothing: a token without an advantage has a zero gradient, one with a small one a finite one."""
+    c = Case(**kw)
+    c.T = T
+    c.adv *= 1e-35 if scale > 1.0 else 1e35
+    c.adv[::2] = 0.0
+    c.x = shifted(c)
+    out = L.lossk_policy_from_logits(c.logits, c.targets, c.adv, temperature=T, grad_scale=scale, flags=L.REDUCE_SUM)
+    assert not out["grad_logits"][::2].any()
+    assert T > 1.0 or out["grad_logits"][1::2].any()
+    c.adv = c.adv.double() * scale
+    exact_rows(c, out)
