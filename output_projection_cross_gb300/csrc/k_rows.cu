@@ -597,9 +597,9 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
             r.load_part(r.at(tid == 0 ? v0 : v1 - 1), f);
             add_part<N>(m, z, f, l.k2);
         }
+        bool in_time = true;                   // (where not, the error word says so, and the call's status)
         for (int k = 0; k < POLICY_CHUNKS; ++k) {
-            // (where the wait runs out the error word says so, and the call's status)
-            mbar_wait(&s_bar[k], 0, &w.hdr->err);
+            in_time &= mbar_wait(&s_bar[k], 0, &w.hdr->err);
             for (int j = chunk(k) + tid; j < chunk(k + 1); j += POLICY_T) {
                 const uint4 v = s_row[j - v0];
                 float f[N];
@@ -607,6 +607,8 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
                 add_vec<N>(m, z, f, vec_max<T>(v), l.k2);
             }
         }
+        if (!in_time)
+            for (int k = 0; k < POLICY_CHUNKS; ++k) mbar_drain(&s_bar[k], 0);
         block_stats<POLICY_T>(m, z, l.k2, sm, sz);
         if (cluster > 1) {
             __syncwarp();

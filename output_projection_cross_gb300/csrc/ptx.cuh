@@ -98,6 +98,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *e
     }
 }
 
+// After a wait that ran out: gives copies in flight 0.2 s to land, so that the block does not leave its
+// shared memory to another one while they still write to it.
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > 200000000ull) return;
+}
+
 // As mbar_wait, with cluster-scope acquire.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, int *err,
                                                   uint64_t limit_ns = 2000000000ull)
