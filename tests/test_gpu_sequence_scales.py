@@ -1,5 +1,5 @@
-"""Heads of the policy and preference losses whose rows' coefficients are of very different sizes, or of which one is no
-number: what the others get does not depend on it."""
+"""The policy and preference losses where coefficients are of very different sizes, one of them is no number, or all are far
+from 1: what a row gets depends on its own coefficient alone."""
 import math
 
 import pytest
@@ -7,7 +7,8 @@ import torch
 
 import output_projection_cross_gb300 as L
 import seq_ref as R
-from test_gpu_sequence import DT, HALF, TINY, Case, close, run_policy
+from test_gpu_sequence import (DT, HALF, TINY, Case, check_grads, check_policy, check_preference, close, run_policy,
+                               run_preference)
 
 pytestmark = pytest.mark.gpu
 HEADS = [dict(n=70, V=900, d=136, dtype="f16"), dict(n=300, V=2001, d=264, dtype="f16"), dict(n=70, V=900, d=136, dtype="bf16"),
@@ -67,3 +68,32 @@ def test_one_row_costs_the_others_nothing(kw, grad, what):
     check_rows(c, out, rows, scale, grad, adv)
     if what.startswith("hidden"):
         assert torch.isnan(out["logp"][5]) and torch.isfinite(out["logp"][rows]).all()
+
+
+@pytest.mark.parametrize("kw", [dict(n=70, V=9000, dtype="f16"), dict(n=70, V=900, dtype="f16"), dict(n=70, V=9000, dtype="bf16"),
+                                dict(n=70, V=9001, dtype="f32"), dict(n=9, V=500003, dtype="bf16")], ids=str)
+@pytest.mark.parametrize("loss", ["policy", "pairs"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 1e3, 1e20])
+def test_scales_of_given_logits_gradient(kw, loss, scale):
+    """The gradient has the scale, and what its type does not hold of it is 0 or infinite; nothing else moves."""
+    c = Case(seqs=2, masked=0.2, **kw)
+    run, kwargs = (run_policy, dict(kl=0.1)) if loss == "policy" else (run_preference, {})
+    one, out = run(c, **kwargs), run(c, grad_scale=scale, **kwargs)
+    for k in one:
+        if k != "grad_logits":
+            assert torch.equal(one[k], out[k]), k
+    (check_policy if loss == "policy" else check_preference)(c, one, **kwargs)
+    g = out["grad_logits"]
+    assert not torch.isnan(g).any() and not g[~c.on].any()
+    if c.dtype == "f16" and scale == 1e-30:
+        assert not g.any()                                 # below fp16's smallest, 6e-8
+        return
+    if c.dtype == "f16" and scale == 1e20:
+        assert torch.isinf(g).any()                        # above its largest, 65504
+        return
+    r = (R.policy(c.lp, c.on, c.first, c.adv, c.old, c.ref, kl=0.1) if loss == "policy"
+         else R.preference(c.lp, c.on, c.first, c.ref))
+    moves = 0.0 if loss == "policy" else 4.0 * 0.1 * max(len(s) for s in R.groups(c.n, c.first, c.on)) * (
+        c.lp_tol() + 2.0 ** -24 * (float(r["logp"].abs().max()) + 1.0))
+    check_grads(c, out, r, scale=scale, moves=moves)
+    assert g[c.on].any()
