@@ -712,7 +712,8 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
  * (a clipped one without a KL term) has a zero gradient.  A vocabulary entry at
  * -infinity has probability 0; a row of nothing else has logp -infinity and a zero
  * gradient.  NaN or +infinity among the logits of a row that counts makes its logp NaN,
- * and what depends on it.
+ * and what depends on it.  From hidden rows, where logits are fp32 sums, so does a
+ * log-sum-exp of x beyond 7e8 in magnitude (a temperature that far below the logits).
  * flags: LOSSK_ACCUMULATE_GRADS adds to the gradients (float d_hidden and d_weight,
  * or grad_logits; with 16-bit d_hidden or d_weight: 592), LOSSK_REDUCE_SUM sums
  * where the formulas take means, and the flags below.

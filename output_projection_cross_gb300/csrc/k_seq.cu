@@ -51,6 +51,10 @@ __device__ __forceinline__ int seq_of(const int *seq_slot, int n_seq, int c, int
     return s;
 }
 
+// The passes from hidden rows scale fp32 logits: the scaled ones' last bit is 2^6 at 2^30, and above that
+// 2^(x log2 e - lse2) leaves fp32's range whatever x.  No number then, rather than one that means nothing.
+__device__ __forceinline__ double lse2_or_nan(double lse2) { return fabs(lse2) <= 0x1p30 || lse2 == -INFINITY ? lse2 : NAN; }
+
 __device__ __forceinline__ void put_lse2(const SeqScratch &w, int c, double lse2)
 {
     const float ref = static_cast<float>(lse2);
@@ -288,13 +292,13 @@ __global__ void __launch_bounds__(32) seq_merge_fused_kernel(const SeqLoss l, co
     // outside, the largest shifted term may be near the end of fp32's range (or not a number)
     if (!(Z >= 0x1p-80f && Z <= 0x1p90f)) w.hdr->redo = 1;
     const float r = w.tokp[c].x;
-    const double lz = log2_of(Z), lse2 = static_cast<double>(r) + lz;
+    const double lz = log2_of(Z), lse2 = lse2_or_nan(static_cast<double>(r) + lz);
     const double gap = static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - static_cast<double>(r);
     put_lse2(w, c, lse2);
     w.z[c] = Z;
     // (the exponentials are of -64 for the target, as exact as of 0, and anything for the others)
-    const float lp = static_cast<float>((gap - lz) * LN2);
-    w.lp[c] = static_cast<float>((gap - lz) * LN2 - EX2_LOW * static_cast<double>(1.f - expf(fminf(lp, 0.f))));
+    const double lp = lse2 == lse2 ? (gap - lz) * LN2 : NAN;
+    w.lp[c] = static_cast<float>(lp - EX2_LOW * static_cast<double>(1.f - expf(fminf(static_cast<float>(lp), 0.f))));
 }
 
 cudaError_t launch_seq_merge_fused(const SeqLoss &l, const SeqScratch &w, const float *zpart, int64_t nz,
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
     if (g != 0 || !live) return;
     Z = 0.0;
     for (int q = 0; q < MT_W; ++q) Z += s_sum[q][lane];
-    const double lse2 = static_cast<double>(M) + log2(Z);
+    const double lse2 = lse2_or_nan(static_cast<double>(M) + (M > -INFINITY && Z == 0.0 ? NAN : log2(Z)));
     put_lse2(w, c, lse2);
     w.z[c] = 1.f;
     w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2 -

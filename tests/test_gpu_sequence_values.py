@@ -205,3 +205,28 @@ def test_a_scale_over_the_temperature_beyond_floats(kw, T, scale):
     assert T > 1.0 or out["grad_logits"][1::2].any()
     c.adv = c.adv.double() * scale
     exact_rows(c, out)
+
+
+@pytest.mark.parametrize("kw", [dict(n=40, V=900, d=136, dtype="bf16"), dict(n=40, V=900, d=136, dtype="f16"), dict(n=40, V=900, d=72, dtype="f32")],
+                         ids=str)
+@pytest.mark.parametrize("T", [1e-3, 1e-5, 1e-7, 1e-9, 1e-20, 1e-30])
+@pytest.mark.parametrize("forward", [False, True])
+def test_a_head_at_temperatures_far_below_one(kw, T, forward):
+    """logp as far off as the logits over the temperature are, and no number where its log-sum-exp passes 7e8."""
+    c = Case(**kw)
+    s = c.x
+    c.T, c.x = T, (s - s.max(1, keepdim=True).values) / T
+    want = R.logprobs(c.x, c.targets, c.on)
+    lse = s.max(1).values / T
+    assert float(lse.min()) > 7.5e8 or float(lse.max()) < 7.3e8
+    kwargs = dict(want_d_hidden=False, want_d_weight=False) if forward else {}
+    out = L.lossk_policy_fwd_bwd(c.hidden, c.weight, c.targets, c.adv, temperature=T, grad_scale=T, **kwargs)
+    if float(lse.min()) > 7.5e8:
+        assert torch.isnan(out["logp"]).all()
+        return
+    # a logit's error in test_gpu_sequence's lp_tol, and the scale's rounding
+    top = float(s.abs().max())
+    sums = 2.0 ** -22 if c.dtype == "f32" else (c.d / 16 + 8) * 2.0 ** -22
+    close(out["logp"], want, 8e-6 + (sums + 2.0 ** -22) * top / T, "logp")
+    if not forward:
+        assert torch.isfinite(out["d_hidden"]).all() and torch.isfinite(out["d_weight"]).all()
