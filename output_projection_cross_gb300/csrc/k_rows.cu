@@ -183,10 +183,7 @@ __device__ __forceinline__ void block_stats(float &m, float &z, float k2, float 
 // but a maximum's own terms have gone through.
 __device__ __forceinline__ float row_logp(const SeqLoss &l, float M, float z, float y, int exps)
 {
-    const double gap = (static_cast<double>(y) - static_cast<double>(M)) * static_cast<double>(l.k2);
-    return y == -INFINITY && z == z
-               ? y
-               : static_cast<float>((gap - log2_of(z)) * LN2 - ex2_low(z, exps));
+    return y == -INFINITY && z == z ? y : logp_of(y, M, l.k2, z, ex2_low(z, exps));
 }
 
 // A warp's (max, sum) from its lanes', as block_stats; valid in every lane.
@@ -597,9 +594,9 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
             r.load_part(r.at(tid == 0 ? v0 : v1 - 1), f);
             add_part<N>(m, z, f, l.k2);
         }
-        bool in_time = true;                   // (where not, the error word says so, and the call's status)
         for (int k = 0; k < POLICY_CHUNKS; ++k) {
-            in_time &= mbar_wait(&s_bar[k], 0, &w.hdr->err);
+            // (a wait that ran out: the error word says so, and the call's status)
+            if (!mbar_wait(&s_bar[k], 0, &w.hdr->err)) mbar_drain(&s_bar[k], 0);
             for (int j = chunk(k) + tid; j < chunk(k + 1); j += POLICY_T) {
                 const uint4 v = s_row[j - v0];
                 float f[N];
@@ -607,8 +604,6 @@ __global__ void __launch_bounds__(POLICY_T, POLICY_BLOCKS) policy_rows_kernel(co
                 add_vec<N>(m, z, f, vec_max<T>(v), l.k2);
             }
         }
-        if (!in_time)
-            for (int k = 0; k < POLICY_CHUNKS; ++k) mbar_drain(&s_bar[k], 0);
         block_stats<POLICY_T>(m, z, l.k2, sm, sz);
         if (cluster > 1) {
             __syncwarp();

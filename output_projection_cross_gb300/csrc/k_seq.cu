@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(32 * MT_W) seq_merge_tiles_kernel(const SeqLos
     put_lse2(w, c, lse2);
     w.z[c] = 1.f;
     w.lp[c] = static_cast<float>((static_cast<double>(w.tgt[c]) * static_cast<double>(l.k2) - lse2) * LN2 -
-                                 ex2_low(static_cast<float>(Z), 2));
+                                 static_cast<double>(ex2_low(static_cast<float>(Z), 2)));
 }
 
 cudaError_t launch_seq_merge_tiles(const SeqLoss &l, const SeqScratch &w, const float *part, int64_t n_ct,

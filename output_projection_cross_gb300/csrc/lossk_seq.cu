@@ -458,7 +458,10 @@ int32_t run(const Call &c)
                               (c.head && is16(c.dtype) ? 1.0 + TC_LOW * static_cast<double>(c.d) : 1.0));
     // (as the fp32 passes have it: the target's logit is scaled by what the sum's are)
     if (c.head && !is16(c.dtype)) l.k2 = static_cast<float>(LOG2E) * static_cast<float>(1.0 / c.temperature);
-    l.per_t = -c.grad_scale / c.temperature;
+    int up = 0;
+    l.per_t = static_cast<float>(std::frexp(-c.grad_scale / c.temperature, &up));
+    if (up & 1) l.per_t *= 2.f, --up;
+    l.per_t_up = static_cast<float>(std::ldexp(1.0, up / 2));
     l.flags = c.flags;
     l.objective = c.objective;
     l.beta = static_cast<float>(c.beta);

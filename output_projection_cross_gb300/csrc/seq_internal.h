@@ -57,7 +57,8 @@ struct SeqLoss {
     const float *adv, *old, *ref;
     float low, high, kl;
     float k2;                      // log2(e) / temperature
-    double per_t;                  // -grad_scale / temperature (beyond floats where both are at their ends)
+    float per_t, per_t_up;         // -grad_scale / temperature as per_t per_t_up^2, per_t_up a power of two (the
+                                   // quotient is beyond floats where both are at their ends)
     uint32_t flags;
     int objective;
     float beta, margin, smooth, nll;
