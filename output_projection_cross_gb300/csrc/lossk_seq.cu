@@ -472,9 +472,10 @@ int32_t run(const Call &c)
     l.per_token = c.per_item;
     l.log_ratio = c.log_ratio;
     l.logp = c.logp;
-    // (Beside the numbering of the rows, which always lets the next kernel start.)  The gradients of given
-    // logits by sequence and pair are 0 to 2 us slower with it.  Group passes: 203 x 264 x 5000 in fp16 86 -> 80 us a call, 512 x 1024 x 32000 in bf16 164.5 -> 163.7,
-    // 8192 x 4096 x 128256 17190 -> 17260 (pairs whose blocks came as others left).
+    // (Which kernels are set up while the one ahead runs; the rows' numbering always lets its next one be.)
+    // Not the gradients of given logits by sequence and pair: 0 to 2 us slower with it.  The group passes'
+    // own hand-overs up to 2^25 logits: 203 x 264 x 5000 in fp16 86 -> 80 us a call, 512 x 1024 x 32000 in bf16 164.5
+    // -> 163.7, 8192 x 4096 x 128256 17190 -> 17260 (pairs whose blocks came as others left).
     l.early = c.head || (one_launch(c, L) && policy_rows_early(c.n, c.V, c.dtype, L.cluster));
     l.early_pass = c.head && (!is16(c.dtype) || c.n * c.V <= (int64_t(1) << 25));
     TRY(launch_seq_prep(l, w, c.st));
