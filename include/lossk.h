@@ -706,7 +706,8 @@ int32_t lossk_paged_attn(int64_t n_seq, int64_t n_q_heads, int64_t n_kv_heads, i
  *   hidden, weight, logits, dtype   as above; contiguous
  *   d_hidden, d_weight  grad_dtype: LOSSK_F32, or the inputs' 16-bit type (each
  *               element is then rounded once, from its fp32 sum).  NULL to skip.
- *   grad_logits dtype, or NULL to skip; it may be logits itself.
+ *   grad_logits dtype, or NULL to skip; it may be logits itself.  No other output may
+ *               overlap an input.
  * Every row of a gradient is written: rows that do not count, and those behind
  * the last sequence, become 0.  A token on whose logp the loss does not depend
  * (a clipped one without a KL term) has a zero gradient.  A vocabulary entry at
