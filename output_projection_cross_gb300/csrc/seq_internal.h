@@ -43,7 +43,7 @@ constexpr double EX2_LOW = 5e-8;
 // The tensor cores drop what lies below an fp32 sum's last bit at each step of 16
 // products: a logit comes out low by so much of itself per unit of d_model (measured, d_model
 // 256 to 4096): 0.9e-9 to 1.2e-9 where its sum grows evenly along d_model or is carried by a few
-// channels anywhere, 0.1e-9 to 0.3e-9 where the last channel carries it, 1.5e-9 to 2.2e-9 where
+// channels anywhere, 0.1e-9 to 0.3e-9 where the last channel carries it, 1.5e-9 to 2.3e-9 where
 // the first one does or they fall in size.  The passes' scale makes up for the middle of that
 // range, 1e-9: a softmax over 4096-wide products is then not 2.5e-5 flatter than the logits', and
 // at the ends of the range, either way, half as far off as the lowest was (logp of 4096-wide rows, root mean

@@ -230,3 +230,35 @@ def test_a_head_at_temperatures_far_below_one(kw, T, forward):
     close(out["logp"], want, 8e-6 + (sums + 2.0 ** -22) * top / T, "logp")
     if not forward:
         assert torch.isfinite(out["d_hidden"]).all() and torch.isfinite(out["d_weight"]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [1024, 4096])
+@pytest.mark.parametrize("how", ["even", "few large", "first", "last", "falling"])
+def test_what_the_tensor_cores_drop(dtype, d, how):
+    """How far logits are off in proportion to their size, by how their sums grow along d_model.
+
+    A step of 16 products drops half of a sum's last bit on average, 2^-24 of it or less (0.72 of that over a binade), so a
+    logit comes out low by 0 to 0.72 * 2^-24 / 16 = 2.7e-9 of itself per unit of d_model.  The passes scale 1e-9 of that
+    back for every row, whatever its sums are like: between 1.7e-9 low and 1e-9 high is left (and 1e-10 of noise)."""
+    g, n, V = gen(11), 512, 8000
+    h = torch.randn(n, d, device="cuda", generator=g)
+    if how == "few large":
+        h[:, torch.randperm(d, device="cuda", generator=g)[:8]] *= 40.0
+    elif how in ("first", "last"):
+        h[:, 0 if how == "first" else -1] *= 200.0
+    elif how == "falling":
+        h *= torch.logspace(1.0, -1.0, d, device="cuda")
+    hidden = (h / h.pow(2).mean(1, keepdim=True).sqrt()).to(DT[dtype])
+    weight = (torch.randn(V, d, device="cuda", generator=g) * (2.5 / math.sqrt(d))).to(DT[dtype])
+    x = hidden.double() @ weight.double().t()
+    p = torch.softmax(x, -1)
+    y = torch.multinomial(p, 1, generator=g)[:, 0]
+    rows = torch.arange(n, device="cuda")
+    out = L.lossk_policy_fwd_bwd(hidden, weight, y, torch.ones(n, device="cuda"), want_d_hidden=False, want_d_weight=False)
+    off = out["logp"].double() - torch.log_softmax(x, -1)[rows, y]
+    # logits of 1 + e times their size move logp by e (x_y - E x)
+    lever = x[rows, y] - (p * x).sum(1)
+    e = float((off * lever).sum() / lever.pow(2).sum()) / d
+    print(how, e)
+    assert -1.8e-9 < e < 1.1e-9
